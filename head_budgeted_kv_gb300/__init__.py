@@ -16,7 +16,7 @@ from typing import Optional
 import torch
 
 from . import binding
-from .binding import (HWKV_BF16, HWKV_F32, HWKV_KERNEL_AUTO, HWKV_KERNEL_SIMT, HWKV_KERNEL_TENSOR, DecodeLaunch, HwkvError,
+from .binding import (HWKV_BF16, HWKV_E4M3, HWKV_F32, HWKV_KERNEL_AUTO, HWKV_KERNEL_SIMT, HWKV_KERNEL_TENSOR, DecodeLaunch, HwkvError,
                       hwkv_abi_version, hwkv_advance_positions, hwkv_append, hwkv_append_decode_attn, hwkv_block_table,
                       hwkv_check_device_errors, hwkv_kernel_launches,
                       hwkv_decode_attn, hwkv_decode_workspace_bytes, hwkv_materialize, hwkv_pool_bytes,
@@ -25,7 +25,7 @@ from .binding import (HWKV_BF16, HWKV_F32, HWKV_KERNEL_AUTO, HWKV_KERNEL_SIMT, H
                       hwkv_set_prefill_config, hwkv_wait_selftest)
 
 __all__ = [
-    "Pool", "DecodeLaunch", "HwkvError", "binding", "HWKV_F32", "HWKV_BF16", "HWKV_KERNEL_AUTO", "HWKV_KERNEL_TENSOR",
+    "Pool", "DecodeLaunch", "HwkvError", "binding", "HWKV_F32", "HWKV_BF16", "HWKV_E4M3", "HWKV_KERNEL_AUTO", "HWKV_KERNEL_TENSOR",
     "HWKV_KERNEL_SIMT", "hwkv_abi_version", "hwkv_advance_positions", "hwkv_append", "hwkv_append_decode_attn", "hwkv_block_table",
     "hwkv_check_device_errors", "hwkv_kernel_launches",
     "hwkv_decode_attn", "hwkv_decode_workspace_bytes", "hwkv_materialize", "hwkv_pool_bytes", "hwkv_pool_create",
@@ -38,13 +38,16 @@ class Pool:
     """A per-head paged KV pool on the current CUDA device.
 
     The pool buffer is one torch uint8 allocation of exactly ``hwkv_pool_bytes`` bytes
-    (the pre-serving prediction), bound with ``hwkv_pool_create``.
+    (the pre-serving prediction), bound with ``hwkv_pool_create``.  With dtype
+    ``torch.float8_e4m3fn`` it holds 8-bit codes and a scale per 16 slots (``scales``); queries,
+    new rows and outputs are then bf16 (``io_dtype``).
     """
 
     def __init__(self, layers: int, kv_heads: int, head_dim: int, block_size: int, windows, num_seqs: int,
                  dtype: torch.dtype, q_heads: Optional[int] = None, device=None, stream=None):
         self.layers, self.kv_heads, self.head_dim = layers, kv_heads, head_dim
         self.block_size, self.num_seqs, self.dtype = block_size, num_seqs, dtype
+        self.io_dtype = torch.bfloat16 if dtype == torch.float8_e4m3fn else dtype
         self.q_heads = q_heads or kv_heads
         self.nbytes = hwkv_pool_bytes(layers, kv_heads, head_dim, block_size, windows, num_seqs, dtype)
         device = torch.device(device or "cuda")
@@ -68,9 +71,28 @@ class Pool:
         return hwkv_pool_geometry(self.handle)
 
     def blocks(self) -> torch.Tensor:
-        """View of the pool as [total_blocks][2][block_size][head_dim] elements."""
-        _, total, _ = self.geometry()
-        return self.buffer.view(self.dtype).view(total, 2, self.block_size, self.head_dim)
+        """View of the pool as [total_blocks][2][block_size][head_dim] elements (the codes of an
+        8-bit pool)."""
+        _, total, block_bytes = self.geometry()
+        rows = self.buffer[:total * block_bytes].view(self.dtype)
+        return rows.view(total, 2, self.block_size, self.head_dim)
+
+    def scales(self) -> torch.Tensor:
+        """View of an 8-bit pool's scales, fp32 [total_blocks][block_size / 16][2 (K, V)]: a value
+        of ``blocks()`` stands for its code times the scale of its 16 slots."""
+        if self.dtype != torch.float8_e4m3fn:
+            raise ValueError("only an 8-bit pool has scales")
+        _, total, block_bytes = self.geometry()
+        groups = self.block_size // 16
+        area = self.buffer[total * block_bytes:total * block_bytes + total * groups * 8]
+        return area.view(torch.float32).view(total, groups, 2)
+
+    def _check_io(self, *tensors):
+        # an 8-bit pool does not share its element type with the tensors passed to it
+        if self.dtype == torch.float8_e4m3fn:
+            for t in tensors:
+                if t is not None and t.dtype != torch.bfloat16:
+                    raise ValueError(f"an 8-bit pool takes bf16 tensors (got {t.dtype})")
 
     def block_table(self, seq: int, layer: int, kv_head: int):
         return hwkv_block_table(self.handle, seq, layer, kv_head)
@@ -79,14 +101,17 @@ class Pool:
         hwkv_set_block_table(self.handle, table, stream)
 
     def materialize(self, layer: int, k_full, v_full, lens, stream=None):
+        self._check_io(k_full, v_full)
         hwkv_materialize(self.handle, layer, k_full, v_full, lens, stream)
 
     def append(self, layer: int, k_new, v_new, pos, stream=None):
+        self._check_io(k_new, v_new)
         hwkv_append(self.handle, layer, k_new, v_new, pos, stream)
 
     def decode(self, layer: int, q, scale: float, lens, out=None, stream=None, early_reads: bool = False):
         if out is None:
             out = torch.empty_like(q)
+        self._check_io(q, out)
         if q.shape[1] != self.q_heads:
             self.q_heads = q.shape[1]
             self._size_workspace()
@@ -100,6 +125,7 @@ class Pool:
         and this layer's pool not written by the kernel just before in the stream)."""
         if out is None:
             out = torch.empty_like(q)
+        self._check_io(q, k_new, v_new, out)
         if q.shape[1] != self.q_heads:
             self.q_heads = q.shape[1]
             self._size_workspace()
@@ -111,6 +137,7 @@ class Pool:
                       early_reads: bool = False) -> DecodeLaunch:
         """A prepared launch of decode (k_new None, ``lens`` = lengths after the append) or of the
         fused append + decode (``lens`` = positions) on fixed buffers: calling it launches."""
+        self._check_io(q, out, k_new, v_new)
         if q.shape[1] != self.q_heads:
             self.q_heads = q.shape[1]
             self._size_workspace()

@@ -30,6 +30,7 @@ DISTORTION_FN = ctypes.CFUNCTYPE(ctypes.c_double, ctypes.c_void_p, ctypes.c_int,
 
 HWKV_F32 = 0
 HWKV_BF16 = 1
+HWKV_E4M3 = 2
 HWKV_KERNEL_AUTO, HWKV_KERNEL_TENSOR, HWKV_KERNEL_SIMT = 0, 1, 2
 HWKV_DEVERR_NEG_LENGTH, HWKV_DEVERR_BAD_BLOCK, HWKV_DEVERR_SRC_RANGE, HWKV_DEVERR_WAIT_TIMEOUT = 1, 2, 4, 8
 HWKV_DECODE_EARLY_READS = 1
@@ -136,12 +137,14 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _dtype_code(dtype) -> int:
-    if dtype in (HWKV_F32, HWKV_BF16):
+    if dtype in (HWKV_F32, HWKV_BF16, HWKV_E4M3):
         return int(dtype)
     if dtype in (torch.float32, "f32", "float32"):
         return HWKV_F32
     if dtype in (torch.bfloat16, "bf16", "bfloat16"):
         return HWKV_BF16
+    if dtype in (torch.float8_e4m3fn, "e4m3", "float8_e4m3fn"):
+        return HWKV_E4M3
     raise ValueError(f"unsupported dtype {dtype}")
 
 

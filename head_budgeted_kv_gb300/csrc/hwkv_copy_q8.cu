@@ -1,0 +1,142 @@
+// Append and materialise for 8-bit pools (HWKV_E4M3): the rows are stored as e4m3 codes, 16
+// consecutive ring slots of a head sharing a scale for K and one for V (hwkv_fp8.cuh).
+//
+// "HeadWiseKV: Budgeted Per-Head Cache Residency for Hybrid Long-Context Language Models",
+// abstract and section "Grouped-Cache Runtime": each KV head keeps its newest w tokens in a ring
+// of ceil(w / bs) blocks; position p lives in slot p mod C.
+//
+// Both kernels write whole groups: slots of a group that hold no position of the window become
+// zero.  Bad lengths and table entries are recorded in the device error word and skipped.
+#include "hwkv_fp8.cuh"
+
+namespace hwkv {
+namespace {
+
+// Block of ring slot t of (seq s, kv head h), or -1 (recorded) when the table entry is bad.
+__device__ __forceinline__ int32_t slot_block(const PoolView& pv, const LayerGeom& g, int s, int h, int t, int lane) {
+  const int32_t blk = pv.tbl[g.tbl_base + (int64_t)s * g.tbl_seq_stride + g.nblk_prefix[h] + t / pv.block_size];
+  if (blk >= 0 && (int64_t)blk < pv.total_blocks) return blk;
+  if (lane == 0) atomicOr(pv.err, HWKV_DEVERR_BAD_BLOCK);
+  return -1;
+}
+
+// One warp per (seq, kv head, K or V): the new token's group is stored anew (recode_group).
+template <int D>
+__global__ void __launch_bounds__(128) append_q8_kernel(const __grid_constant__ CopyArgs a) {
+  const int warp = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
+  const int lane = threadIdx.x & 31;
+  const int H = a.pv.kv_heads;
+  if (warp >= 2 * a.pv.num_seqs * H) return;
+  const int kv = warp & 1, sh = warp >> 1;
+  const int s = sh / H, h = sh - s * H;
+  const int32_t p = a.lens[s];
+  if (p < 0) {
+    if (lane == 0) atomicOr(a.pv.err, HWKV_DEVERR_NEG_LENGTH);
+    return;
+  }
+  const int bs = a.pv.block_size;
+  const int C = (a.g.nblk_prefix[h + 1] - a.g.nblk_prefix[h]) * bs;
+  const int slot = p % C, t0 = slot & ~(kScaleGroup - 1);
+  const int32_t blk = slot_block(a.pv, a.g, s, h, t0, lane);
+  if (blk < 0) return;
+  const int r0 = t0 % bs;
+  uint8_t* rows = static_cast<uint8_t*>(a.pv.pool) + (((int64_t)blk * 2 + kv) * bs + r0) * D;
+  float* scale = a.pv.scales + ((int64_t)blk * (bs / kScaleGroup) + r0 / kScaleGroup) * 2 + kv;
+  const float now = recode_group<D>(
+      static_cast<const __nv_bfloat16*>(kv ? a.v : a.k) + (int64_t)sh * D, t0, slot, p, a.g.window[h], C, *scale,
+      [&](int r, int c) { return *reinterpret_cast<const uint4*>(rows + r * D + 16 * c); },
+      [&](int r, int c, uint4 v) { *reinterpret_cast<uint4*>(rows + r * D + 16 * c) = v; }, lane);
+  if (lane == 0) *scale = now;
+}
+
+constexpr int kMatWarps = 8;
+
+// grid.x: per sequence, kMatWarps / 2 of its groups of 16 ring slots (all heads in a row, so no
+// CTA is empty whatever the windows); one warp per group and K or V.  A lane takes 16 dims of a
+// row, all its rows loaded before any is used.
+template <int D>
+__global__ void __launch_bounds__(kMatWarps * 32) materialize_q8_kernel(const __grid_constant__ CopyArgs a) {
+  constexpr int kChunks = D / 16;                    // lanes per row
+  constexpr int kPer = kScaleGroup * kChunks / 32;   // rows per lane
+  const int H = a.pv.kv_heads;
+  const int per_group = a.pv.block_size / kScaleGroup;  // groups per block
+  const int ngroups = a.g.nblk_prefix[H] * per_group;
+  const int nchunks = (ngroups + kMatWarps / 2 - 1) / (kMatWarps / 2);
+  const int s = (int)blockIdx.x / nchunks;
+  const int32_t L = a.lens[s];
+  if (L < 0 || (int64_t)L > a.max_len) {
+    if (threadIdx.x == 0 && (int)blockIdx.x == s * nchunks)
+      atomicOr(a.pv.err, L < 0 ? HWKV_DEVERR_NEG_LENGTH : HWKV_DEVERR_SRC_RANGE);
+    return;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int kv = warp & 1;
+  const int bs = a.pv.block_size;
+  const int gi = ((int)blockIdx.x - s * nchunks) * (kMatWarps / 2) + (warp >> 1);
+  if (gi >= ngroups) return;
+  int h = 0;
+  while (a.g.nblk_prefix[h + 1] * per_group <= gi) ++h;
+  const int C = (a.g.nblk_prefix[h + 1] - a.g.nblk_prefix[h]) * bs;
+  const int t0 = (gi - a.g.nblk_prefix[h] * per_group) * kScaleGroup;
+  const Resident rs = resident(L, a.g.window[h], C);
+  const int c = lane % kChunks;
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(kv ? a.v : a.k) + a.seq_stride * s + a.head_stride * h;
+  uint4 lo[kPer], hi[kPer];
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int t = t0 + (lane + 32 * i) / kChunks;
+    int d = t - rs.first_slot;  // positions above the oldest resident one
+    if (d < 0) d += C;
+    lo[i] = hi[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (d < rs.n) {
+      any = true;
+      const uint4* row = reinterpret_cast<const uint4*>(src + (int64_t)(L - rs.n + d) * D + 16 * c);
+      lo[i] = __ldcs(row);
+      hi[i] = __ldcs(row + 1);
+    }
+  }
+  if (!__any_sync(0xffffffffu, any)) return;
+  const int32_t blk = slot_block(a.pv, a.g, s, h, t0, lane);
+  if (blk < 0) return;
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const Row16 x = widen16(lo[i], hi[i]);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(x.v[e]));
+  }
+  const float scale = pow2i(scale_exponent(warp_max(amax))), inv = pow2_inverse(scale);
+  const int r0 = t0 % bs;
+  uint8_t* rows = static_cast<uint8_t*>(a.pv.pool) + (((int64_t)blk * 2 + kv) * bs + r0) * D;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    *reinterpret_cast<uint4*>(rows + ((lane + 32 * i) / kChunks) * D + 16 * c) = encode16(widen16(lo[i], hi[i]), inv);
+  if (lane == 0) a.pv.scales[((int64_t)blk * (bs / kScaleGroup) + r0 / kScaleGroup) * 2 + kv] = scale;
+}
+
+}  // namespace
+
+cudaError_t launch_append_q8(const CopyArgs& a, cudaStream_t st) {
+  const int warps = 2 * a.pv.num_seqs * a.pv.kv_heads;
+  const int blocks = (warps + 3) / 4;
+  if (a.pv.head_dim == 128) append_q8_kernel<128><<<blocks, 128, 0, st>>>(a);
+  else if (a.pv.head_dim == 64) append_q8_kernel<64><<<blocks, 128, 0, st>>>(a);
+  else return cudaErrorInvalidValue;
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_materialize_q8(const CopyArgs& a, cudaStream_t st) {
+  constexpr int kPerCta = kMatWarps / 2;
+  const int64_t groups = (int64_t)a.g.nblk_prefix[a.pv.kv_heads] * (a.pv.block_size / kScaleGroup);
+  // at most the pool's rows / 64, which is below 2^31
+  const unsigned grid = (unsigned)((groups + kPerCta - 1) / kPerCta * a.pv.num_seqs);
+  if (a.pv.head_dim == 128) materialize_q8_kernel<128><<<grid, kMatWarps * 32, 0, st>>>(a);
+  else if (a.pv.head_dim == 64) materialize_q8_kernel<64><<<grid, kMatWarps * 32, 0, st>>>(a);
+  else return cudaErrorInvalidValue;
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace hwkv

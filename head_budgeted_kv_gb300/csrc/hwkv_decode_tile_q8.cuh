@@ -1,0 +1,302 @@
+// Tile-level pieces of the stream-K decode kernel (hwkv_decode_sk.cuh) for 8-bit pools
+// (HWKV_E4M3, hwkv_fp8.cuh): the loads of one 16-token tile with its two scales, the fused
+// append, and one warp's work on a tile.
+//
+// With K = k_scale * Kc and V = v_scale * Vc for the codes Kc, Vc of a tile (one group of 16
+// slots, so one pair of scales):
+//   S = (Kc . Qn^T) * (k_scale * qs)       Qn = Q / qs, qs a power of two per query head
+//   O = sum over tiles of (P * v_scale) . Vc
+// Codes become fp16 exactly, one conversion instruction per two values, and feed
+// mma.sync.m16n8k16 fp16 -> fp32.  fp16's range is kept in three exact ways: each query head is
+// scaled by a power of two so its largest element lies in [2^14, 2^15) (the elements then lose
+// nothing above 2^-39 of that largest one); P carries a factor 2^15 that cancels in O / l, so a
+// weight keeps its 11 bits down to 2^-29 of the largest; and v_scale enters P relative to the
+// largest v_scale the warp has met, by which its accumulators are finally multiplied.
+// A dim or token index may be permuted freely inside a contraction: K's bytes are fed in the
+// order ldmatrix delivers them, against queries loaded in the same order, and V's columns come
+// out as dim pairs (2i, 2i + 1) in the accumulator's row halves, which publish() undoes.
+#pragma once
+
+#include "hwkv_decode_tile.cuh"
+#include "hwkv_fp8.cuh"
+
+namespace hwkv {
+namespace {
+
+// Byte offset of byte b of row r of a 16-row tile of codes, as TMA stores it: rows of D bytes,
+// 128-byte swizzle for D = 128 (chunk ^ row % 8), 64-byte swizzle for D = 64 (chunk ^ row / 2 % 4).
+template <int D>
+__device__ __forceinline__ uint32_t swz_q8(int row, int b) {
+  const int c = b >> 4;
+  if constexpr (D == 128) return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4) + (b & 15));
+  else return (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4) + (b & 15));
+}
+
+// Shared memory of one stage's scales: the 16-byte copy that holds them and which half they are.
+struct __align__(16) ScaleSlot {
+  float pair[2][2];  // scales of two neighbouring groups: [group % 2][K, V]
+  int half;          // written by the issuing lane before it arrives on the stage's barrier
+  int pad[3];
+};
+
+// Issues the loads of one tile of an 8-bit pool: K and V rows in one box of the 3-D map
+// (head_dim, block_size rows, 2 * block + K/V), and the 16 bytes that hold the group's scales.
+template <int D>
+__device__ __forceinline__ void issue_tile_q8(const CUtensorMap* tmap, const DecodeArgs& a, const Group& gr, int t0,
+                                              uint32_t dst, ScaleSlot* slot, uint64_t* bar, uint64_t policy,
+                                              bool through_l2) {
+  const int bs = a.pv.block_size;
+  const int jb = t0 / bs;
+  const int r0 = t0 - jb * bs;
+  int32_t blk = through_l2 ? __ldcg(gr.tbl + jb) : gr.tbl[jb];
+  if (blk < 0 || (int64_t)blk >= a.pv.total_blocks) {
+    atomicOr(a.pv.err, HWKV_DEVERR_BAD_BLOCK);
+    blk = 0;
+  }
+  const int64_t group = (int64_t)blk * (bs / kScaleGroup) + r0 / kScaleGroup;
+  slot->half = (int)(group & 1);
+  mbar_arrive_expect_tx(bar, 2 * kTile * D + 16);
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(r0), "r"(2 * blk), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+  bulk_load(smem_addr(slot->pair), a.pv.scales + (group & ~(int64_t)1) * 2, 16, bar);
+}
+
+// Fused append: when the tile starting at slot t0 is the new token's group, the group is stored
+// anew with the new row (recode_group), in shared memory and in the pool, and `scale` (K, V) is
+// replaced.  No other CTA reads this tile, or its scales, in the launch.
+template <int D>
+__device__ __forceinline__ bool patch_new_row_q8(const DecodeArgs& a, const Group& gr, int t0, int new_slot,
+                                                 uint32_t sK, float (&scale)[2], int lane) {
+  if (new_slot < t0 || new_slot >= t0 + kTile) return false;
+  const int bs = a.pv.block_size;
+  const int jb = t0 / bs, r0 = t0 - jb * bs;
+  const int32_t blk = gr.tbl[jb];
+  const bool blk_ok = blk >= 0 && (int64_t)blk < a.pv.total_blocks;
+  const int64_t src = ((int64_t)gr.s * a.pv.kv_heads + gr.h) * D;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    const uint32_t base = sK + kv * (kTile * D);
+    uint8_t* dst = static_cast<uint8_t*>(a.pv.pool) + (((int64_t)(blk_ok ? blk : 0) * 2 + kv) * bs + r0) * D;
+    scale[kv] = recode_group<D>(
+        static_cast<const __nv_bfloat16*>(kv ? a.v_new : a.k_new) + src, t0, new_slot, gr.len - 1, a.g.window[gr.h],
+        gr.rs.C, scale[kv],
+        [&](int r, int c) {
+          uint4 v;
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(base + swz_q8<D>(r, 16 * c)));
+          return v;
+        },
+        [&](int r, int c, uint4 v) {
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(base + swz_q8<D>(r, 16 * c)), "r"(v.x), "r"(v.y),
+                       "r"(v.z), "r"(v.w)
+                       : "memory");
+          if (blk_ok) *reinterpret_cast<uint4*>(dst + r * D + 16 * c) = v;
+        },
+        lane);
+  }
+  if (lane == 0 && blk_ok) {
+    const int64_t group = (int64_t)blk * (bs / kScaleGroup) + r0 / kScaleGroup;
+    *reinterpret_cast<float2*>(a.pv.scales + group * 2) = make_float2(scale[0], scale[1]);
+  }
+  __syncwarp();
+  return true;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 8-bit pools: the GQA group on the N side of mma.sync as for bf16, fp32 accumulators in units
+// of the warp's largest V scale `vs`.
+template <int D, int GP>
+struct WarpState<E4m3, D, GP> {
+  static constexpr int NT = (GP + 7) / 8;
+  static constexpr float kShift = 15.f;  // log2 of the factor P carries
+  uint32_t qf[NT][D / 16][2];
+  float acc[D / 16][NT][4];
+  float mx[NT][2], ls[NT][2];
+  float qs[NT][2];  // scale * log2(e) * the power of two taken out of each of the lane's heads
+  float vs;         // largest V scale met (0 at first)
+
+  // Q of the group, normalised: the lane holds q[g][16i + 4*q4 .. + 3], g = 8*nt + lane / 4
+  __device__ __forceinline__ void begin(const DecodeArgs& a, const Group& gr, int G, int lane) {
+    const int gq = lane >> 2, q4 = lane & 3;
+    const int Hq = a.pv.kv_heads * G;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int g = 8 * nt + gq;
+      const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(a.q) + ((int64_t)gr.s * Hq + gr.h * G + g) * D;
+      uint2 raw[D / 16];
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        raw[i] = g < G ? *reinterpret_cast<const uint2*>(qrow + 16 * i + 4 * q4) : make_uint2(0u, 0u);
+        const float x0 = __uint_as_float(raw[i].x << 16), x1 = __uint_as_float(raw[i].x & 0xFFFF0000u);
+        const float x2 = __uint_as_float(raw[i].y << 16), x3 = __uint_as_float(raw[i].y & 0xFFFF0000u);
+        top = fmaxf(top, fmaxf(fmaxf(finite_abs(x0), finite_abs(x1)), fmaxf(finite_abs(x2), finite_abs(x3))));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // top = f * 2^x, f in [1, 2): elements times 2^(14 - x); x is clamped so the factor is normal
+      const int x = max((int)(__float_as_uint(top) >> 23) - 127, -112);
+      const float f = pow2i(14 - x);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        qf[nt][i][0] = pack_f16(__uint_as_float(raw[i].x << 16) * f, __uint_as_float(raw[i].x & 0xFFFF0000u) * f);
+        qf[nt][i][1] = pack_f16(__uint_as_float(raw[i].y << 16) * f, __uint_as_float(raw[i].y & 0xFFFF0000u) * f);
+      }
+      // the accumulator's columns are heads 2 q4 and 2 q4 + 1
+      const float inv = pow2i(x - 14);
+      qs[nt][0] = __shfl_sync(0xffffffffu, inv, (2 * q4) * 4) * a.scale_log2;
+      qs[nt][1] = __shfl_sync(0xffffffffu, inv, (2 * q4 + 1) * 4) * a.scale_log2;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) acc[j][nt][0] = acc[j][nt][1] = acc[j][nt][2] = acc[j][nt][3] = 0.f;
+      mx[nt][0] = mx[nt][1] = kNegInf;
+      ls[nt][0] = ls[nt][1] = 0.f;
+    }
+    vs = 0.f;
+  }
+
+  __device__ __forceinline__ bool consume(const DecodeArgs& a, const Group& gr, int t0, int new_slot, uint32_t sK,
+                                          uint32_t sV, const ScaleSlot* slot, int lane) {
+    const int mi = lane >> 3, rr = lane & 7;
+    const int row = rr + ((mi & 1) << 3);  // ldmatrix: matrices 0, 1 are rows 0-7, 8-15 of one chunk,
+    const int col = (mi >> 1) << 4;        // matrices 2, 3 those of the next chunk
+    const int gq = lane >> 2;
+    const int half = slot->half;
+    float scale[2] = {slot->pair[half][0], slot->pair[half][1]};
+    bool dirty = patch_new_row_q8<D>(a, gr, t0, new_slot, sK, scale, lane);
+
+    float sa[NT][4], sb[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sa[nt][e] = sb[nt][e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; i += 2) {
+      uint32_t w[4], a0[4], a1[4];
+      ldsm_x4(w, sK + swz_q8<D>(row, 16 * i + col));
+      e4m3x4_to_f16(w[0], a0[0], a0[2]);
+      e4m3x4_to_f16(w[1], a0[1], a0[3]);
+      e4m3x4_to_f16(w[2], a1[0], a1[2]);
+      e4m3x4_to_f16(w[3], a1[1], a1[3]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_f16(sa[nt], a0, qf[nt][i][0], qf[nt][i][1]);
+        mma_f16(sb[nt], a1, qf[nt][i + 1][0], qf[nt][i + 1][1]);
+      }
+    }
+
+    // V scale: accumulators and P are in units of the largest one so far
+    const float vs_new = fmaxf(vs, scale[1]);
+    const float vs_inv = vs_new > 0.f ? pow2_inverse(vs_new) : 0.f;
+    const float keep = vs * vs_inv, part = scale[1] * vs_inv;
+    vs = vs_new;
+
+    const bool v0 = slot_valid(gr.rs, t0 + gq), v1 = slot_valid(gr.rs, t0 + gq + 8);
+    float al[NT][2];
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float f0 = qs[nt][0] * scale[0], f1 = qs[nt][1] * scale[0];
+      const float s0 = v0 ? (sa[nt][0] + sb[nt][0]) * f0 : kNegInf;
+      const float s1 = v0 ? (sa[nt][1] + sb[nt][1]) * f1 : kNegInf;
+      const float s2 = v1 ? (sa[nt][2] + sb[nt][2]) * f0 : kNegInf;
+      const float s3 = v1 ? (sa[nt][3] + sb[nt][3]) * f1 : kNegInf;
+      float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+      }
+      const float n0 = fmaxf(mx[nt][0], mx0), n1 = fmaxf(mx[nt][1], mx1);
+      const float b0 = n0 == kNegInf ? 0.f : n0, b1 = n1 == kNegInf ? 0.f : n1;
+      al[nt][0] = ex2(mx[nt][0] - b0);
+      al[nt][1] = ex2(mx[nt][1] - b1);
+      const float p0 = ex2(s0 - b0 + kShift), p1 = ex2(s1 - b1 + kShift);
+      const float p2 = ex2(s2 - b0 + kShift), p3 = ex2(s3 - b1 + kShift);
+      ls[nt][0] = fmaf(ls[nt][0], al[nt][0], p0 + p2);
+      ls[nt][1] = fmaf(ls[nt][1], al[nt][1], p1 + p3);
+      mx[nt][0] = n0;
+      mx[nt][1] = n1;
+      pb[nt][0] = movmatrix_trans(pack_f16(p0 * part, p1 * part));
+      pb[nt][1] = movmatrix_trans(pack_f16(p2 * part, p3 * part));
+      al[nt][0] *= keep;
+      al[nt][1] *= keep;
+    }
+
+    // V rows of slots outside the window are zeroed: their P is 0, but 0 times a NaN is not
+    if (!__all_sync(0xffffffffu, v0 && v1)) {
+      const int r = lane >> 1;
+      if (!slot_valid(gr.rs, t0 + r)) {
+#pragma unroll
+        for (int c = lane & 1; c < D / 16; c += 2)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sV + swz_q8<D>(r, 16 * c)), "r"(0u) : "memory");
+      }
+      __syncwarp();
+      dirty = true;
+    }
+#pragma unroll
+    for (int j = 0; j < D / 16; j += 2) {
+      uint32_t w[4], a0[4], a1[4];
+      ldsm_x4_trans(w, sV + swz_q8<D>(row, 16 * j + col));
+      // bytes of a register: (token 2 q4, dims 2 gq, 2 gq + 1), (token 2 q4 + 1, the same dims)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = __byte_perm(w[e], 0u, 0x3120);
+      e4m3x4_to_f16(w[0], a0[0], a0[1]);
+      e4m3x4_to_f16(w[1], a0[2], a0[3]);
+      e4m3x4_to_f16(w[2], a1[0], a1[1]);
+      e4m3x4_to_f16(w[3], a1[2], a1[3]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[j][nt][e] *= al[nt][e & 1];
+          acc[j + 1][nt][e] *= al[nt][e & 1];
+        }
+        mma_f16(acc[j][nt], a0, pb[nt][0], pb[nt][1]);
+        mma_f16(acc[j + 1][nt], a1, pb[nt][0], pb[nt][1]);
+      }
+    }
+    return dirty;
+  }
+
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        ls[nt][0] += __shfl_xor_sync(0xffffffffu, ls[nt][0], off);
+        ls[nt][1] += __shfl_xor_sync(0xffffffffu, ls[nt][1], off);
+      }
+  }
+
+  template <int SG>
+  __device__ __forceinline__ void publish(int nt, int hh, int warp, int lane, float* sc_m, float* sc_l,
+                                          float* sc_acc) const {
+    const int gq = lane >> 2, q4 = lane & 3;
+    const int c0 = 2 * q4 - hh * SG;  // this lane's first column within the pass
+    if (c0 < 0 || c0 >= SG) return;
+    if (gq == 0) {
+      sc_m[warp * SG + c0] = mx[nt][0];
+      sc_m[warp * SG + c0 + 1] = mx[nt][1];
+      sc_l[warp * SG + c0] = ls[nt][0];
+      sc_l[warp * SG + c0 + 1] = ls[nt][1];
+    }
+    float* wacc = sc_acc + warp * SG * D;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      const int d = 16 * j + 2 * gq;
+      *reinterpret_cast<float2*>(wacc + c0 * D + d) = make_float2(acc[j][nt][0] * vs, acc[j][nt][2] * vs);
+      *reinterpret_cast<float2*>(wacc + (c0 + 1) * D + d) = make_float2(acc[j][nt][1] * vs, acc[j][nt][3] * vs);
+    }
+  }
+};
+
+}  // namespace
+}  // namespace hwkv

@@ -148,6 +148,15 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// C[16x8] += A[16x16] * B[16x8], fp16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
@@ -173,6 +182,21 @@ __device__ __forceinline__ bool slot_valid(const Resident& r, int t) {
   if (d < 0) d += r.C;
   return d < r.n;
 }
+
+// Marks a pool of 8-bit codes (HWKV_E4M3) where the kernels are instances of an element type.
+struct E4m3 {
+  uint8_t code;
+};
+
+// the element type of the tensors passed with a pool of T: queries, new rows, outputs
+template <typename T_>
+struct IoType {
+  using T = T_;
+};
+template <>
+struct IoType<E4m3> {
+  using T = __nv_bfloat16;
+};
 
 template <typename T>
 __device__ __forceinline__ void store_out(T* p, float x);

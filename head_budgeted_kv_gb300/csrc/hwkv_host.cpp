@@ -80,10 +80,12 @@ struct NvtxRange {
 
 struct Geometry {
   int layers = 0, kv_heads = 0, head_dim = 0, block_size = 0, num_seqs = 0, dtype = 0, eb = 0;
+  int io_eb = 0;               // element bytes of the tensors passed with the pool
   std::vector<int32_t> windows, nblk;   // [layers * kv_heads]
   std::vector<int64_t> tbl_base;        // [layers] table offset of (layer, seq 0, head 0)
   std::vector<int32_t> seq_stride;      // [layers] sum_h nblk
   int64_t total_blocks = 0;
+  uint64_t block_area = 0;     // bytes of the blocks; the scales of an 8-bit pool follow them
   uint64_t pool_bytes = 0;
 };
 
@@ -98,7 +100,10 @@ int plan_geometry(int layers, int kv_heads, int head_dim, int block_size, const 
     return fail(HWKV_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", head_dim);
   if (block_size < 1) return fail(HWKV_ERR_INVALID_ARG, "block_size must be >= 1 (got %d)", block_size);
   if (num_seqs < 1) return fail(HWKV_ERR_INVALID_ARG, "num_seqs must be >= 1 (got %d)", num_seqs);
-  if (dtype != HWKV_F32 && dtype != HWKV_BF16) return fail(HWKV_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (dtype != HWKV_F32 && dtype != HWKV_BF16 && dtype != HWKV_E4M3)
+    return fail(HWKV_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (dtype == HWKV_E4M3 && block_size % 16 != 0)
+    return fail(HWKV_ERR_UNSUPPORTED, "an 8-bit pool needs block_size %% 16 == 0 (got %d)", block_size);
   if (!windows) return fail(HWKV_ERR_INVALID_ARG, "windows is NULL");
   g->layers = layers;
   g->kv_heads = kv_heads;
@@ -106,7 +111,8 @@ int plan_geometry(int layers, int kv_heads, int head_dim, int block_size, const 
   g->block_size = block_size;
   g->num_seqs = num_seqs;
   g->dtype = dtype;
-  g->eb = dtype == HWKV_F32 ? 4 : 2;
+  g->eb = dtype == HWKV_F32 ? 4 : dtype == HWKV_BF16 ? 2 : 1;
+  g->io_eb = dtype == HWKV_F32 ? 4 : 2;
   g->windows.assign(windows, windows + (size_t)layers * kv_heads);
   g->nblk.resize(g->windows.size());
   g->tbl_base.resize(layers);
@@ -131,7 +137,10 @@ int plan_geometry(int layers, int kv_heads, int head_dim, int block_size, const 
       return fail(HWKV_ERR_UNSUPPORTED, "pool exceeds 2^31 rows (blocks x 2 x block_size)");
   }
   g->total_blocks = blocks;
-  g->pool_bytes = (uint64_t)blocks * 2u * (uint64_t)block_size * (uint64_t)head_dim * (uint64_t)g->eb;
+  g->block_area = (uint64_t)blocks * 2u * (uint64_t)block_size * (uint64_t)head_dim * (uint64_t)g->eb;
+  g->pool_bytes = g->block_area;
+  if (dtype == HWKV_E4M3)  // two fp32 scales per 16 slots after the blocks, read in 16-byte pairs
+    g->pool_bytes += ((uint64_t)blocks * (uint64_t)(block_size / 16) * 8u + 15u) & ~uint64_t(15);
   return HWKV_OK;
 }
 
@@ -204,13 +213,11 @@ struct hwkv_pool {
 
 namespace {
 
-// The stream-K decode kernel takes bf16 pools (tensor cores) and fp32 pools (CUDA cores, up to
-// 4 query heads per KV head) whose block size is a multiple of 16 (one TMA box of 16 rows).
-bool tc_eligible(const hwkv_pool* p) {
-  return (p->g.dtype == HWKV_BF16 || p->g.dtype == HWKV_F32) && p->g.block_size % 16 == 0 && p->has_tmap;
-}
+// The stream-K decode kernel takes bf16 and 8-bit pools (tensor cores) and fp32 pools (CUDA cores,
+// up to 4 query heads per KV head) whose block size is a multiple of 16 (one TMA box of 16 rows).
+bool tc_eligible(const hwkv_pool* p) { return p->g.block_size % 16 == 0 && p->has_tmap; }
 
-bool tc_group_ok(const hwkv_pool* p, int group) { return p->g.dtype == HWKV_BF16 || group <= 4; }
+bool tc_group_ok(const hwkv_pool* p, int group) { return p->g.dtype != HWKV_F32 || group <= 4; }
 
 bool use_tc(const hwkv_pool* p, int group) {
   if (p->kernel_choice == HWKV_KERNEL_SIMT) return false;
@@ -489,6 +496,7 @@ PoolView pool_view(const hwkv_pool* p) {
   v.kv_heads = p->g.kv_heads;
   v.num_seqs = p->g.num_seqs;
   v.elem_bytes = p->g.eb;
+  v.scales = p->g.dtype == HWKV_E4M3 ? reinterpret_cast<float*>(p->dev_pool + p->g.block_area) : nullptr;
   return v;
 }
 
@@ -634,6 +642,27 @@ int hwkv_pool_create(int layers, int kv_heads, int head_dim, int block_size, con
       p->has_stage_map = p->has_tmap;
     }
   }
+  if (p->g.dtype == HWKV_E4M3) {
+    // 8-bit: (head_dim, block_size rows, 2 * block + K/V), one box holds the K and V rows of a tile
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    CUresult cr = CUDA_ERROR_NOT_SUPPORTED;
+    if (encode) {
+      const cuuint64_t d = (cuuint64_t)p->g.head_dim, bs = (cuuint64_t)p->g.block_size;
+      const cuuint64_t dims[3] = {d, bs, (cuuint64_t)p->g.total_blocks * 2};
+      const cuuint64_t strides[2] = {d, bs * d};
+      const cuuint32_t box[3] = {(cuuint32_t)d, 16, 2};
+      const cuuint32_t estr[3] = {1, 1, 1};
+      cr = encode(&p->tmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p->dev_pool, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    }
+    p->has_tmap = cr == CUDA_SUCCESS;
+    if (!p->has_tmap) {  // an 8-bit pool has no other decode kernel
+      cudaFree(p->d_meta);
+      delete p;
+      return fail(HWKV_ERR_CUDA, "tensor map of the 8-bit pool could not be encoded (%d)", (int)cr);
+    }
+  }
   if (p->has_tmap) {
     e = configure_decode_tc(p->g.head_dim, p->g.dtype, p->ctas_per_sm);
     if (e != cudaSuccess) return cleanup_fail("cudaFuncSetAttribute", e);
@@ -716,7 +745,7 @@ int hwkv_materialize(hwkv_pool_t p, int layer, const void* k_full, const void* v
   if (!k_full || !v_full || !lens_dev) return fail(HWKV_ERR_INVALID_ARG, "NULL tensor argument");
   if (!aligned(k_full, 16) || !aligned(v_full, 16) || !aligned(lens_dev, 4))
     return fail(HWKV_ERR_ALIGNMENT, "k_full / v_full must be 16-byte aligned, lens 4-byte aligned");
-  if ((seq_stride * g.eb) % 16 != 0 || (head_stride * g.eb) % 16 != 0)
+  if ((seq_stride * g.io_eb) % 16 != 0 || (head_stride * g.io_eb) % 16 != 0)
     return fail(HWKV_ERR_ALIGNMENT, "seq_stride and head_stride must be multiples of 16 bytes");
   if (max_len > kInt32Max) return fail(HWKV_ERR_INVALID_ARG, "max_len must be below 2^31");
   int rc = check_device(p);
@@ -736,6 +765,10 @@ int hwkv_materialize(hwkv_pool_t p, int layer, const void* k_full, const void* v
   for (int h = 0; h < g.kv_heads; ++h) max_rows = std::max<int64_t>(max_rows, a.g.window[h]);
   max_rows = std::min<int64_t>(max_rows, max_len);
   if (max_rows == 0) return ok();
+  if (g.dtype == HWKV_E4M3) {
+    HWKV_CUDA_TRY(launch_materialize_q8(a, static_cast<cudaStream_t>(stream)), "materialize launch");
+    return ok();
+  }
   HWKV_CUDA_TRY(launch_materialize(a, g.dtype, (int)max_rows, static_cast<cudaStream_t>(stream)), "materialize launch");
   return ok();
 }
@@ -757,7 +790,9 @@ int hwkv_append(hwkv_pool_t p, int layer, const void* k_new, const void* v_new, 
   a.k = k_new;
   a.v = v_new;
   a.lens = pos_dev;
-  HWKV_CUDA_TRY(launch_append(a, g.dtype, static_cast<cudaStream_t>(stream)), "append launch");
+  HWKV_CUDA_TRY(g.dtype == HWKV_E4M3 ? launch_append_q8(a, static_cast<cudaStream_t>(stream))
+                                     : launch_append(a, g.dtype, static_cast<cudaStream_t>(stream)),
+                "append launch");
   return ok();
 }
 
@@ -1044,6 +1079,8 @@ int hwkv_set_decode_config(hwkv_pool_t p, int split_tokens, int workers, int ker
     return fail(HWKV_ERR_INVALID_ARG, "unknown kernel %d", kernel);
   if (kernel == HWKV_KERNEL_TENSOR && !tc_eligible(p))
     return fail(HWKV_ERR_UNSUPPORTED, "the stream-K decode needs block_size % 16 == 0");
+  if (kernel == HWKV_KERNEL_SIMT && p->g.dtype == HWKV_E4M3)
+    return fail(HWKV_ERR_UNSUPPORTED, "the split CUDA-core decode does not take 8-bit pools");
   p->split_override = split_tokens;
   p->workers_override = workers;
   p->kernel_choice = kernel;

@@ -34,7 +34,8 @@ struct PoolView {
   int32_t head_dim;
   int32_t kv_heads;
   int32_t num_seqs;
-  int32_t elem_bytes;      // 4 (f32) or 2 (bf16)
+  int32_t elem_bytes;      // 4 (f32), 2 (bf16) or 1 (e4m3)
+  float* scales;           // e4m3: [total_blocks][bs / 16][2] scales of K and V, after the blocks; else null
 };
 
 struct CopyArgs {
@@ -106,7 +107,7 @@ int set_error(int code, const char* fmt, ...);
 // HWKV_OK when the pool's device is the current one, else an error (message recorded).
 int check_pool_device(const struct ::hwkv_pool* p);
 
-// Launchers (hwkv_copy.cu, hwkv_decode.cu).  dtype: 0 = f32, 1 = bf16.
+// Launchers.  dtype: 0 = f32, 1 = bf16 (e4m3 pools have launchers of their own).
 cudaError_t launch_append(const CopyArgs& a, int dtype, cudaStream_t st);
 // out[i] = in[i] + delta for i < n (in == out allowed)
 cudaError_t launch_advance_positions(const int32_t* in, int32_t* out, int n, int32_t delta, cudaStream_t st);
@@ -114,12 +115,18 @@ cudaError_t launch_advance_positions(const int32_t* in, int32_t* out, int n, int
 cudaError_t launch_wait_selftest(int32_t* out, uint32_t limit_us, cudaStream_t st);
 // max_rows: the most positions any (seq, head) of the layer copies, min(max window, max_len)
 cudaError_t launch_materialize(const CopyArgs& a, int dtype, int max_rows, cudaStream_t st);
+// append and materialise of e4m3 pools (hwkv_copy_q8.cu): groups of 16 slots stored at a scale each
+cudaError_t launch_append_q8(const CopyArgs& a, cudaStream_t st);
+cudaError_t launch_materialize_q8(const CopyArgs& a, cudaStream_t st);
 // once per device before the first launch; returns resident CTAs per SM of the instances
 // for 4, 8 and 16 query-head columns (fp32 pools: 4 only, the others 0)
 cudaError_t configure_decode_tc(int head_dim, int dtype, int ctas_per_sm[kGroupPads]);
 // stream-K kernel (tensor cores for bf16, CUDA cores for fp32 with group <= 4): `ctas`
 // persistent CTAs split the resident tiles of the layer evenly
 cudaError_t launch_decode_tc(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, cudaStream_t st);
+// the same for e4m3 pools (hwkv_decode_q8.cu)
+cudaError_t configure_decode_q8(int head_dim, int ctas_per_sm[kGroupPads]);
+cudaError_t launch_decode_q8(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, cudaStream_t st);
 int decode_tc_group_pad(int group);  // query-head columns the kernel instance holds (4, 8 or 16)
 int decode_tc_pad_index(int group);  // 0, 1, 2 for 4, 8, 16 columns
 cudaError_t launch_decode_simt(const DecodeArgs& a, int dtype, int items, cudaStream_t st);

@@ -27,7 +27,7 @@ class DecodeStepGraph:
     def __init__(self, pool, scale: float, q_heads: int, pos0, fused: bool = True):
         dev = pool.buffer.device
         L, B, H, D = pool.layers, pool.num_seqs, pool.kv_heads, pool.head_dim
-        dt = pool.dtype
+        dt = pool.io_dtype
         self.pool = pool
         self.q = torch.zeros((L, B, q_heads, D), dtype=dt, device=dev)
         self.k_new = torch.zeros((L, B, H, D), dtype=dt, device=dev)

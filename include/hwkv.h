@@ -21,6 +21,18 @@
  *   Decode attention at length len covers positions [max(0, len - w), len): the last
  *   min(w, len) tokens, including the one appended in the same step.
  *
+ * 8-bit pools (HWKV_E4M3)
+ *   Blocks hold e4m3 codes (eb = 1), and bs % 16 == 0.  The pool buffer continues after the
+ *   blocks with fp32 scales [total_blocks][bs / 16][2]: one for the K rows and one for the V rows
+ *   of each group of 16 consecutive slots; a stored value is code * scale.  The scale is 2^e with
+ *   the smallest e >= -120 such that the group's largest finite magnitude is at most 448 * 2^e;
+ *   codes are rounded to nearest even; what is not finite is stored as NaN.
+ *   Storing a token stores its whole group anew: the slots of the group whose positions are in
+ *   the window of the new length keep their values at the new scale (rounded again where a code
+ *   becomes subnormal), every other slot becomes zero.  Materialise does so with every group
+ *   that holds a resident position.  Slots outside the window never reach a result, whatever
+ *   they hold.
+ *
  * Conventions
  *   - Every function returns an int status (HWKV_OK or a negative HWKV_ERR_*); on error
  *     hwkv_last_error() (thread-local) describes it.  Argument errors are reported before
@@ -32,7 +44,7 @@
  *     across decode steps; kernels check them and record problems in a device error word
  *     that hwkv_check_device_errors() reads.  Kernels never trap or spin without bound.
  *   - Inputs must be finite: a masked pool row that holds Inf/NaN bits can still poison
- *     a result (0 * Inf), as in any attention kernel.
+ *     a result (0 * Inf), as in any attention kernel (not so in 8-bit pools).
  */
 #ifndef HWKV_H
 #define HWKV_H
@@ -56,15 +68,17 @@ extern "C" {
 #define HWKV_ERR_WORKSPACE_TOO_SMALL (-7)
 #define HWKV_ERR_BUDGET (-8)
 
-/* element types of the pool and of every tensor passed with it */
+/* element types of the pool and of every tensor passed with it; HWKV_E4M3 pools hold 8-bit codes
+ * and take and return BF16 tensors */
 #define HWKV_F32 0
 #define HWKV_BF16 1
+#define HWKV_E4M3 2
 
 /* decode kernel selection for hwkv_set_decode_config */
 #define HWKV_KERNEL_AUTO 0   /* stream-K kernel where supported, else the split kernel       */
-#define HWKV_KERNEL_TENSOR 1 /* stream-K kernel: tensor cores for bf16, CUDA cores for fp32
+#define HWKV_KERNEL_TENSOR 1 /* stream-K kernel: tensor cores for bf16 and 8 bit, CUDA cores for fp32
                                 (fp32: up to 4 query heads per KV head); bs % 16 == 0 only  */
-#define HWKV_KERNEL_SIMT 2   /* split-K CUDA-core kernel, any supported shape                  */
+#define HWKV_KERNEL_SIMT 2   /* split-K CUDA-core kernel, any supported shape but 8-bit pools  */
 
 /* bits of the device error word */
 #define HWKV_DEVERR_NEG_LENGTH 1     /* a length / position below 0                    */
@@ -87,9 +101,11 @@ const char* hwkv_status_string(int status);
 /* Pre-serving footprint prediction ("Grouped-Cache Runtime": ceil(w / bs) blocks per head;
  * abstract: demand known exactly before serving).  Pure host, needs no GPU.
  *   windows: host int32 [layers][kv_heads], each >= 1.
- *   out_bytes = num_seqs * sum_{l,h} ceil(w[l][h]/bs) * bs * head_dim * 2 * eb.
- * Supported: 1 <= kv_heads <= 32, head_dim in {64, 128}, block_size >= 1, dtype F32/BF16,
- * every ring capacity below 2^31 tokens and at most 2^31 - 1 blocks in total.
+ *   out_bytes = num_seqs * sum_{l,h} ceil(w[l][h]/bs) * bs * head_dim * 2 * eb,
+ *   for HWKV_E4M3 plus the scales: 8 bytes per 16 slots, their sum rounded up to 16 bytes.
+ * Supported: 1 <= kv_heads <= 32, head_dim in {64, 128}, block_size >= 1 (E4M3: a multiple of
+ * 16), dtype F32/BF16/E4M3, every ring capacity below 2^31 tokens and at most 2^31 - 1 blocks in
+ * total.
  * Errors: HWKV_ERR_INVALID_ARG, HWKV_ERR_UNSUPPORTED. */
 int hwkv_pool_bytes(int layers, int kv_heads, int head_dim, int block_size, const int32_t* windows,
                     int num_seqs, int dtype, uint64_t* out_bytes);
@@ -111,7 +127,8 @@ int hwkv_pool_create(int layers, int kv_heads, int head_dim, int block_size, con
  * still in flight.  NULL is accepted. */
 int hwkv_pool_destroy(hwkv_pool_t pool);
 
-/* Geometry of a created pool: bytes, physical block count, bytes per block. */
+/* Geometry of a created pool: bytes, physical block count, bytes per block (an 8-bit pool's
+ * scales, total_blocks * block_bytes into the pool, are not part of a block). */
 int hwkv_pool_geometry(hwkv_pool_t pool, uint64_t* pool_bytes, int64_t* total_blocks, int64_t* block_bytes);
 
 /* Copies the physical block ids of (seq, layer, kv_head) -- nblk of them, logical block
@@ -134,7 +151,8 @@ int hwkv_set_block_table(hwkv_pool_t pool, const int32_t* host_table, int64_t n,
  *            (checked on the device: HWKV_DEVERR_NEG_LENGTH / HWKV_DEVERR_SRC_RANGE, the
  *            sequence is skipped).
  *   lens_dev: device int32 [num_seqs] prefill lengths L_s.
- * max_len == 0 is an empty prefill: nothing is read or written and the pointers may be NULL. */
+ * max_len == 0 is an empty prefill: nothing is read or written and the pointers may be NULL.
+ * 8-bit pools take a bf16 source and store whole groups (see above). */
 int hwkv_materialize(hwkv_pool_t pool, int layer, const void* k_full, const void* v_full,
                      int64_t seq_stride, int64_t head_stride, int64_t max_len, const int32_t* lens_dev,
                      void* stream);
@@ -188,7 +206,8 @@ int hwkv_decode_workspace_bytes(hwkv_pool_t pool, int q_heads, uint64_t* out);
  * merges partial results through per-(seq, head) arrival counters that the library keeps in
  * its own device memory (one set per layer); concurrent launches of the SAME layer race.
  * Other shapes (block_size not a multiple of 16, fp32 groups above 4) take the split-K
- * CUDA-core kernel and a merge kernel.
+ * CUDA-core kernel and a merge kernel.  8-bit pools always take the stream-K kernel, on the
+ * tensor cores; q, k_new, v_new and out are bf16.
  * Errors: HWKV_ERR_INVALID_ARG, HWKV_ERR_ALIGNMENT, HWKV_ERR_WORKSPACE_TOO_SMALL,
  *         HWKV_ERR_UNSUPPORTED, HWKV_ERR_CUDA (launch failure). */
 int hwkv_decode_attn(hwkv_pool_t pool, int layer, const void* q, int q_heads, float scale,

@@ -1,0 +1,77 @@
+"""Host side of the operators around the cache, without a GPU: footprints, refusals, and the
+64-bit reference the GPU tests compare with."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from head_budgeted_kv_gb300 import _build, binding
+from reference_ops import Ring8, encode_group, nearest_e4m3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return binding.load()
+
+
+def _pool_bytes(*args):
+    return binding.hwkv_pool_bytes(*args)
+
+
+@pytest.mark.parametrize("D,bs,B", [(64, 16, 1), (128, 16, 3), (128, 64, 2), (64, 48, 5)])
+def test_8_bit_footprint(lib, D, bs, B):
+    windows = [[33, 128, 1], [700, 16, 17]]
+    blocks = B * sum(-(-w // bs) for row in windows for w in row)
+    want = blocks * 2 * bs * D + (blocks * (bs // 16) * 8 + 15) // 16 * 16
+    for dtype in (torch.float8_e4m3fn, "e4m3", binding.HWKV_E4M3):
+        assert _pool_bytes(2, 3, D, bs, windows, B, dtype) == want
+
+
+@pytest.mark.parametrize("bs", [1, 5, 8, 24])
+def test_8_bit_pools_need_whole_groups(lib, bs):
+    with pytest.raises(binding.HwkvError) as e:
+        _pool_bytes(1, 1, 64, bs, [[64]], 1, torch.float8_e4m3fn)
+    assert e.value.status == binding.HWKV_ERR_UNSUPPORTED
+
+
+def test_seqcalib_budgets_8_bit_pools(lib):
+    cand = np.array([[[64], [1024]]], dtype=np.int32)
+    budget = _pool_bytes(1, 1, 128, 16, [[1024]], 1, "e4m3")
+    w, choice, nbytes = binding.hwkv_seqcalib(cand, np.array([[2.0, 1.0]]), budget, 128, 16, 1, "e4m3")
+    assert choice.tolist() == [1] and nbytes == budget
+    w, choice, nbytes = binding.hwkv_seqcalib(cand, np.array([[2.0, 1.0]]), budget - 1, 128, 16, 1, "e4m3")
+    assert choice.tolist() == [0]
+
+
+def test_reference_codes_are_torchs_codes():
+    """The reference's rounding to e4m3 is the nearest one with ties to even, as torch's cast has it."""
+    gen = torch.Generator().manual_seed(0)
+    x = torch.randn(20000, generator=gen) * torch.exp2(torch.randint(-14, 9, (20000,), generator=gen))
+    every = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    every = every[torch.isfinite(every)].sort().values
+    x = torch.cat((x.clamp(-448, 448), every, (every[1:] + every[:-1]) / 2))
+    want = x.to(torch.float8_e4m3fn).double().numpy()
+    np.testing.assert_array_equal(nearest_e4m3(x.double().numpy()), want)
+
+
+def test_reference_group_scale():
+    for top, e in ((448.0, 0), (448.0001, 1), (449.0, 1), (896.0, 1), (224.0, -1), (224.5, 0), (1.0, -8), (0.0, -120),
+                   (2.0 ** -133, -120), (3.3895e38, 120)):
+        rows = np.zeros((16, 64))
+        rows[3, 5] = -top
+        assert encode_group(rows)[1] == 2.0 ** e, top
+
+
+def test_reference_ring_keeps_the_window():
+    """A ring filled by appends holds what a stored prompt holds, up to a second rounding of subnormal codes."""
+    rng = np.random.default_rng(0)
+    k, v = rng.standard_normal((2, 90, 64))
+    a, b = Ring8(40, 16, 64), Ring8(40, 16, 64)
+    a.materialize(k, v, 90)
+    for p in range(90):
+        b.append(k[p], v[p], p)
+    for x, y, src in zip(a.resident(90)[1:], b.resident(90)[1:], (k, v)):
+        assert np.abs(x - y).max() <= 2.0 ** -9 * a.scales.max()
+        assert (np.abs(x - src[50:]) <= 2.0 ** -4 * np.abs(src[50:]) + 2.0 ** -10 * a.scales.max()).all()

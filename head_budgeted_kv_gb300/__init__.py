@@ -16,22 +16,43 @@ from typing import Optional
 import torch
 
 from . import binding
-from .binding import (HWKV_BF16, HWKV_E4M3, HWKV_F32, HWKV_KERNEL_AUTO, HWKV_KERNEL_SIMT, HWKV_KERNEL_TENSOR, DecodeLaunch, HwkvError,
+from .binding import (HWKV_BF16, HWKV_E4M3, HWKV_F32, HWKV_KERNEL_AUTO, HWKV_KERNEL_SIMT, HWKV_KERNEL_TENSOR, DecodeLaunch, HwkvError, RopeTable,
                       hwkv_abi_version, hwkv_advance_positions, hwkv_append, hwkv_append_decode_attn, hwkv_block_table,
                       hwkv_check_device_errors, hwkv_kernel_launches,
                       hwkv_decode_attn, hwkv_decode_workspace_bytes, hwkv_materialize, hwkv_pool_bytes,
                       hwkv_pool_create, hwkv_pool_destroy, hwkv_pool_geometry, hwkv_prefill_attn,
-                      hwkv_prefill_plan, hwkv_prefill_workspace_bytes, hwkv_set_block_table, hwkv_set_decode_config,
+                      hwkv_prefill_plan, hwkv_prefill_workspace_bytes, hwkv_rope, hwkv_rope_table, hwkv_set_block_table, hwkv_set_decode_config,
                       hwkv_set_prefill_config, hwkv_wait_selftest)
 
 __all__ = [
-    "Pool", "DecodeLaunch", "HwkvError", "binding", "HWKV_F32", "HWKV_BF16", "HWKV_E4M3", "HWKV_KERNEL_AUTO", "HWKV_KERNEL_TENSOR",
+    "Pool", "DecodeLaunch", "HwkvError", "RopeTable", "binding", "rope_table", "HWKV_F32", "HWKV_BF16", "HWKV_E4M3", "HWKV_KERNEL_AUTO", "HWKV_KERNEL_TENSOR",
     "HWKV_KERNEL_SIMT", "hwkv_abi_version", "hwkv_advance_positions", "hwkv_append", "hwkv_append_decode_attn", "hwkv_block_table",
     "hwkv_check_device_errors", "hwkv_kernel_launches",
     "hwkv_decode_attn", "hwkv_decode_workspace_bytes", "hwkv_materialize", "hwkv_pool_bytes", "hwkv_pool_create",
-    "hwkv_pool_destroy", "hwkv_pool_geometry", "hwkv_prefill_attn", "hwkv_prefill_plan", "hwkv_prefill_workspace_bytes",
+    "hwkv_pool_destroy", "hwkv_pool_geometry", "hwkv_prefill_attn", "hwkv_prefill_plan", "hwkv_prefill_workspace_bytes", "hwkv_rope", "hwkv_rope_table",
     "hwkv_set_block_table", "hwkv_set_decode_config", "hwkv_set_prefill_config", "hwkv_wait_selftest",
 ]
+
+
+_ROPE_LAYOUTS = {"half": binding.HWKV_ROPE_HALF, "interleaved": binding.HWKV_ROPE_INTERLEAVED}
+_ROPE_SCALINGS = {"none": binding.HWKV_ROPE_SCALE_NONE, "linear": binding.HWKV_ROPE_SCALE_LINEAR,
+                  "ntk": binding.HWKV_ROPE_SCALE_NTK, "by_parts": binding.HWKV_ROPE_SCALE_BY_PARTS}
+
+
+def rope_table(head_dim: int, rot_dim: Optional[int] = None, base: float = 10000.0, layout: str = "half",
+               scaling: str = "none", factor: float = 1.0, original_len: float = 0.0, beta_fast: float = 32.0,
+               beta_slow: float = 1.0) -> RopeTable:
+    """The table ``Pool.rope`` turns heads of ``head_dim`` with: pairs of the first ``rot_dim`` dims
+    (all by default), ``layout`` "half" (i, i + rot_dim / 2) or "interleaved" (2i, 2i + 1),
+    frequencies base^(-2i / rot_dim) scaled for longer contexts by ``scaling`` "none", "linear",
+    "ntk" or "by_parts" (see hwkv_rope_table in the header)."""
+    rot_dim = head_dim if rot_dim is None else rot_dim
+    if rot_dim > head_dim:
+        raise ValueError(f"rot_dim {rot_dim} exceeds head_dim {head_dim}")
+    if layout not in _ROPE_LAYOUTS or scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"unknown rope layout {layout!r} or scaling {scaling!r}")
+    return hwkv_rope_table(rot_dim, _ROPE_LAYOUTS[layout], base, _ROPE_SCALINGS[scaling], factor, original_len, beta_fast,
+                           beta_slow)
 
 
 class Pool:
@@ -163,6 +184,27 @@ class Pool:
         out = pos if out is None else out
         hwkv_advance_positions(self.handle, pos, out, delta, stream)
         return out
+
+    def rope(self, table: RopeTable, q, k, pos, n=None, q_out=None, k_out=None, stream=None):
+        """Rotary positions: turns q [B][n_max][Hq][D] and k [B][n_max][Hkv][D] (or single rows
+        [B][heads][D]; either may be None) at positions pos[s] + row, rows below n[s] (all when n is
+        None).  Inputs may be slices of a fused projection.  Outputs default to new tensors (zeros past
+        n); pass q_out=q, k_out=k to work in place.  Returns (q_out, k_out)."""
+        new = torch.empty if n is None else torch.zeros
+        for t, name in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out")):
+            if t is None:
+                continue
+            if t.dtype != self.io_dtype or t.shape[0] != self.num_seqs or t.shape[-1] != self.head_dim:
+                raise ValueError(f"{name} must hold {self.io_dtype} rows of head_dim {self.head_dim} for "
+                                 f"{self.num_seqs} sequences")
+        if k is not None and k.shape[-2] != self.kv_heads:
+            raise ValueError(f"k must hold {self.kv_heads} heads")
+        if q is not None and q_out is None:
+            q_out = new(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = new(k.shape, dtype=k.dtype, device=k.device)
+        hwkv_rope(self.handle, table, q, k, pos, n, q_out, k_out, stream)
+        return q_out, k_out
 
     def check_device_errors(self, stream=None) -> int:
         return hwkv_check_device_errors(self.handle, stream)

@@ -34,7 +34,23 @@ HWKV_E4M3 = 2
 HWKV_KERNEL_AUTO, HWKV_KERNEL_TENSOR, HWKV_KERNEL_SIMT = 0, 1, 2
 HWKV_DEVERR_NEG_LENGTH, HWKV_DEVERR_BAD_BLOCK, HWKV_DEVERR_SRC_RANGE, HWKV_DEVERR_WAIT_TIMEOUT = 1, 2, 4, 8
 HWKV_DECODE_EARLY_READS = 1
+HWKV_ROPE_HALF, HWKV_ROPE_INTERLEAVED = 0, 1
+HWKV_ROPE_SCALE_NONE, HWKV_ROPE_SCALE_LINEAR, HWKV_ROPE_SCALE_NTK, HWKV_ROPE_SCALE_BY_PARTS = 0, 1, 2, 3
 
+
+class RopeTable(ctypes.Structure):
+    """hwkv_rope_t: what turns a head's pairs (see ``hwkv_rope_table``)."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("magnitude", ctypes.c_double),
+                ("freq", ctypes.c_double * 64)]
+
+
+class Rows(ctypes.Structure):
+    """hwkv_rows_t: the rows of a chunk, by sequence and row strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("seq_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
+
+
+_rowsp = ctypes.POINTER(Rows)
+_ropep = ctypes.POINTER(RopeTable)
 _c_i32p = ctypes.POINTER(ctypes.c_int32)
 _c_u64p = ctypes.POINTER(ctypes.c_uint64)
 _c_i64p = ctypes.POINTER(ctypes.c_int64)
@@ -57,6 +73,9 @@ SIGNATURES = [
     ("hwkv_materialize", _i, [_vp, _i, _vp, _vp, _i64, _i64, _i64, _vp, _vp]),
     ("hwkv_append", _i, [_vp, _i, _vp, _vp, _vp, _vp]),
     ("hwkv_advance_positions", _i, [_vp, _vp, _vp, ctypes.c_int32, _vp]),
+    ("hwkv_rope_table", _i, [_i, _i, ctypes.c_double, _i, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                             ctypes.c_double, _ropep]),
+    ("hwkv_rope", _i, [_vp, _ropep, _rowsp, _i, _rowsp, _i, _vp, _vp, _rowsp, _rowsp, _vp]),
     ("hwkv_wait_selftest", _i, [ctypes.c_uint32, _vp, _vp]),
     ("hwkv_decode_workspace_bytes", _i, [_vp, _i, _c_u64p]),
     ("hwkv_decode_attn", _i, [_vp, _i, _vp, _i, ctypes.c_float, _vp, _vp, _vp, _u64, _vp]),
@@ -230,6 +249,44 @@ def hwkv_advance_positions(pool: int, pos: torch.Tensor, out: torch.Tensor, delt
     if pos.dtype != torch.int32 or out.dtype != torch.int32:
         raise ValueError("positions must be int32")
     _check(load().hwkv_advance_positions(pool, _ptr(pos), _ptr(out), int(delta), _stream_ptr(stream)))
+
+
+def hwkv_rope_table(rot_dim: int, layout: int = HWKV_ROPE_HALF, base: float = 10000.0,
+                    scaling: int = HWKV_ROPE_SCALE_NONE, factor: float = 1.0, original_len: float = 0.0,
+                    beta_fast: float = 32.0, beta_slow: float = 1.0) -> RopeTable:
+    """The frequencies of rotary positions, scaled for longer contexts (host only)."""
+    t = RopeTable()
+    _check(load().hwkv_rope_table(int(rot_dim), int(layout), float(base), int(scaling), float(factor),
+                                  float(original_len), float(beta_fast), float(beta_slow), ctypes.byref(t)))
+    return t
+
+
+def _rows(t: Optional[torch.Tensor], name: str):
+    """(hwkv_rows_t, rows, heads) of [B][n][heads][D], or of [B][heads][D] as one row."""
+    if t is None:
+        return None, 0, 0
+    if t.dim() not in (3, 4) or t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]):
+        raise ValueError(f"{name} must be [B][n][heads][D] or [B][heads][D] with the heads of a row contiguous")
+    n, row = (t.shape[1], t.stride(1)) if t.dim() == 4 else (1, 0)
+    return Rows(t.data_ptr(), t.stride(0), row), n, t.shape[-2]
+
+
+def hwkv_rope(pool: int, table: RopeTable, q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: torch.Tensor,
+              n: Optional[torch.Tensor], q_out: Optional[torch.Tensor], k_out: Optional[torch.Tensor], stream=None):
+    """Turns q [B][n_max][Hq][D] and k [B][n_max][Hkv][D] (or one row each, [B][heads][D]; either may be
+    None) at positions pos + row; outputs may be the inputs; n: int32 [B] rows per sequence or None."""
+    if pos.dtype != torch.int32 or (n is not None and n.dtype != torch.int32):
+        raise ValueError("positions and row counts must be int32")
+    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if (x is None) != (y is None) or (x is not None and (x.shape != y.shape or x.dtype != y.dtype)):
+            raise ValueError(f"{name}_out must match {name}")
+    if q is not None and k is not None and (q.dim() != k.dim() or q.shape[:-2] != k.shape[:-2]):
+        raise ValueError("q and k must have the same sequences and rows")
+    rq, nq, hq = _rows(q, "q")
+    rk, nk, _ = _rows(k, "k")
+    ro, _, _ = _rows(q_out, "q_out")
+    rp, _, _ = _rows(k_out, "k_out")
+    _check(load().hwkv_rope(pool, table, rq, hq, rk, nq or nk, _ptr(pos), _ptr(n), ro, rp, _stream_ptr(stream)))
 
 
 def hwkv_decode_workspace_bytes(pool: int, q_heads: int) -> int:

@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -89,6 +90,7 @@ struct Geometry {
   uint64_t pool_bytes = 0;
 };
 
+constexpr double kInvTwoPi = 0.15915494309189533577;
 constexpr int64_t kInt32Max = std::numeric_limits<int32_t>::max();
 
 int plan_geometry(int layers, int kv_heads, int head_dim, int block_size, const int32_t* windows, int num_seqs,
@@ -804,6 +806,120 @@ int hwkv_advance_positions(hwkv_pool_t p, const int32_t* pos_dev, int32_t* out_d
   if (rc != HWKV_OK) return rc;
   HWKV_CUDA_TRY(launch_advance_positions(pos_dev, out_dev, p->g.num_seqs, delta, static_cast<cudaStream_t>(stream)),
                 "advance-positions launch");
+  return ok();
+}
+
+int hwkv_rope_table(int rot_dim, int layout, double base, int scaling, double factor, double original_len,
+                    double beta_fast, double beta_slow, hwkv_rope_t* out) {
+  if (!out) return fail(HWKV_ERR_INVALID_ARG, "out is NULL");
+  if (rot_dim < 2 || rot_dim > 128 || rot_dim % 2 != 0)
+    return fail(HWKV_ERR_INVALID_ARG, "rot_dim must be even and in [2, 128] (got %d)", rot_dim);
+  if (layout != HWKV_ROPE_HALF && layout != HWKV_ROPE_INTERLEAVED)
+    return fail(HWKV_ERR_INVALID_ARG, "unknown rope layout %d", layout);
+  if (!(base > 0) || !std::isfinite(base)) return fail(HWKV_ERR_INVALID_ARG, "base must be positive and finite");
+  if (scaling < HWKV_ROPE_SCALE_NONE || scaling > HWKV_ROPE_SCALE_BY_PARTS)
+    return fail(HWKV_ERR_INVALID_ARG, "unknown rope scaling %d", scaling);
+  if (scaling != HWKV_ROPE_SCALE_NONE && (!(factor >= 1) || !std::isfinite(factor)))
+    return fail(HWKV_ERR_INVALID_ARG, "factor must be finite and at least 1");
+  if (scaling == HWKV_ROPE_SCALE_BY_PARTS &&
+      (!(original_len > 0) || !std::isfinite(original_len) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast) ||
+       !std::isfinite(beta_slow)))
+    return fail(HWKV_ERR_INVALID_ARG, "scaling by parts needs original_len > 0 and beta_fast > beta_slow");
+  hwkv_rope_t t;
+  std::memset(&t, 0, sizeof t);
+  t.rot_dim = rot_dim;
+  t.layout = layout;
+  t.magnitude = 1.0;
+  if (scaling == HWKV_ROPE_SCALE_NTK && rot_dim > 2) base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot_dim);
+    if (scaling == HWKV_ROPE_SCALE_LINEAR) f /= factor;
+    if (scaling == HWKV_ROPE_SCALE_BY_PARTS) {
+      const double r = original_len * f * kInvTwoPi;
+      const double c = std::min(1.0, std::max(0.0, (r - beta_slow) / (beta_fast - beta_slow)));
+      f = c * f + (1.0 - c) * f / factor;
+    }
+    t.freq[i] = f;
+  }
+  if (scaling == HWKV_ROPE_SCALE_BY_PARTS) t.magnitude = 0.1 * std::log(factor) + 1.0;
+  *out = t;
+  return ok();
+}
+
+int hwkv_rope(hwkv_pool_t p, const hwkv_rope_t* rope, const hwkv_rows_t* q, int q_heads, const hwkv_rows_t* k,
+              int n_max, const int32_t* pos_dev, const int32_t* n_dev, const hwkv_rows_t* q_out,
+              const hwkv_rows_t* k_out, void* stream) {
+  if (!p) return fail(HWKV_ERR_INVALID_ARG, "pool is NULL");
+  const Geometry& g = p->g;
+  if (!rope || !pos_dev) return fail(HWKV_ERR_INVALID_ARG, "NULL argument");
+  if (rope->rot_dim < 2 || rope->rot_dim > g.head_dim || rope->rot_dim % 2 != 0)
+    return fail(HWKV_ERR_INVALID_ARG, "rot_dim must be even and in [2, head_dim = %d] (got %d)", g.head_dim, rope->rot_dim);
+  if (rope->layout != HWKV_ROPE_HALF && rope->layout != HWKV_ROPE_INTERLEAVED)
+    return fail(HWKV_ERR_INVALID_ARG, "unknown rope layout %d", rope->layout);
+  if (!std::isfinite(rope->magnitude) || !std::isfinite((float)rope->magnitude))
+    return fail(HWKV_ERR_INVALID_ARG, "magnitude must be finite");
+  for (int i = 0; i < rope->rot_dim / 2; ++i)
+    if (!std::isfinite(rope->freq[i])) return fail(HWKV_ERR_INVALID_ARG, "freq[%d] must be finite", i);
+  if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr) || (!q && !k))
+    return fail(HWKV_ERR_INVALID_ARG, "q goes with q_out and k with k_out, and one of them must be given");
+  if (q && (q_heads < 1 || q_heads > 65535)) return fail(HWKV_ERR_UNSUPPORTED, "q_heads must be in [1, 65535] (got %d)", q_heads);
+  if (n_max < 1) return fail(HWKV_ERR_INVALID_ARG, "n_max must be >= 1");
+  if ((int64_t)g.num_seqs * n_max > kInt32Max) return fail(HWKV_ERR_UNSUPPORTED, "num_seqs * n_max must be below 2^31");
+  if (!aligned(pos_dev, 4) || !aligned(n_dev, 4)) return fail(HWKV_ERR_ALIGNMENT, "positions must be 4-byte aligned");
+  const hwkv_rows_t* in[2] = {q, k};
+  const hwkv_rows_t* to[2] = {q_out, k_out};
+  const int heads[2] = {q ? q_heads : 0, k ? g.kv_heads : 0};
+  bool copy = false;
+  for (int i = 0; i < 2; ++i) {
+    if (!in[i]) continue;
+    for (const hwkv_rows_t* r : {in[i], to[i]}) {
+      if (!r->data) return fail(HWKV_ERR_INVALID_ARG, "NULL tensor argument");
+      if (r->seq_stride < 0 || r->row_stride < 0) return fail(HWKV_ERR_INVALID_ARG, "negative stride");
+      if (!aligned(r->data, 16) || (r->seq_stride * g.io_eb) % 16 != 0 || (r->row_stride * g.io_eb) % 16 != 0)
+        return fail(HWKV_ERR_ALIGNMENT, "rows must be 16-byte aligned, strides multiples of 16 bytes");
+    }
+    // no two rows of an output may share an element: sequences apart by whole chunks, or rows
+    // apart by whole batches
+    const int64_t row = (int64_t)heads[i] * g.head_dim;
+    const int64_t ss = g.num_seqs > 1 ? to[i]->seq_stride : 0, rs = n_max > 1 ? to[i]->row_stride : 0;
+    const bool by_seq = (n_max == 1 || rs >= row) && (g.num_seqs == 1 || ss >= (n_max - 1) * rs + row);
+    const bool by_row = (g.num_seqs == 1 || ss >= row) && (n_max == 1 || rs >= (g.num_seqs - 1) * ss + row);
+    if (!by_seq && !by_row) return fail(HWKV_ERR_INVALID_ARG, "rows of an output overlap");
+    if (in[i]->data != to[i]->data) copy = true;
+    else if ((g.num_seqs > 1 && in[i]->seq_stride != to[i]->seq_stride) || (n_max > 1 && in[i]->row_stride != to[i]->row_stride))
+      return fail(HWKV_ERR_INVALID_ARG, "an output in place of its input needs the input's strides");
+  }
+  if (q && k && q_out->data == k_out->data) return fail(HWKV_ERR_INVALID_ARG, "q_out and k_out overlap");
+  int rc = check_device(p);
+  if (rc != HWKV_OK) return rc;
+  NvtxRange range_("hwkv_rope", n_max);
+  RopeArgs a;
+  std::memset(&a, 0, sizeof a);
+  RopeTensor* t[4] = {&a.q, &a.k, &a.q_out, &a.k_out};
+  const hwkv_rows_t* r[4] = {q, k, q_out, k_out};
+  for (int i = 0; i < 4; ++i)
+    if (r[i]) *t[i] = RopeTensor{r[i]->data, r[i]->seq_stride, r[i]->row_stride};
+  a.pos = pos_dev;
+  a.n = n_dev;
+  a.err = p->d_err;
+  a.num_seqs = g.num_seqs;
+  a.n_max = n_max;
+  a.q_heads = heads[0];
+  a.k_heads = heads[1];
+  a.head_dim = g.head_dim;
+  a.rot = rope->rot_dim;
+  a.copy = copy ? 1 : 0;
+  a.rows = rope_rows((int64_t)g.num_seqs * n_max);
+  a.magnitude = (float)rope->magnitude;
+  for (int i = 0; i < rope->rot_dim / 2; ++i) {
+    // the fraction of a turn per position, in [0, 1), as a 64-bit fraction
+    const double turns = rope->freq[i] * kInvTwoPi;
+    const double frac = turns - std::floor(turns);
+    // 2^32 steps at a time: both parts convert exactly
+    const double hi = std::floor(frac * 0x1p32), lo = (frac * 0x1p32 - hi) * 0x1p32;
+    a.turns[i] = ((uint64_t)hi << 32) + (uint64_t)lo;
+  }
+  HWKV_CUDA_TRY(launch_rope(a, rope->layout, g.dtype == HWKV_F32, static_cast<cudaStream_t>(stream)), "rope launch");
   return ok();
 }
 

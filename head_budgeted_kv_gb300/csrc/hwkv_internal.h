@@ -98,6 +98,26 @@ struct PrefillArgs {
   float* part_ml;          // [CTA][256 rows][2] (reference maximum in log2 units, sum)
 };
 
+struct RopeTensor {
+  void* data;              // element (s, i, head, d) at s * seq_stride + i * row_stride + head * D + d
+  int64_t seq_stride;      // elements
+  int64_t row_stride;
+};
+
+struct RopeArgs {
+  RopeTensor q, k, q_out, k_out;
+  const int32_t* pos;      // [B] position of row 0
+  const int32_t* n;        // [B] rows, null: n_max
+  int32_t* err;            // device error word
+  int32_t num_seqs, n_max;
+  int32_t q_heads, k_heads;  // 0: that tensor is not given
+  int32_t head_dim, rot;   // the first rot dims of a row turn
+  int32_t copy;            // 1: the other dims are written too (not in place)
+  int32_t rows;            // rows of one CTA
+  float magnitude;
+  uint64_t turns[64];      // turns per position of each pair, times 2^64
+};
+
 // Counts every kernel launch the library makes (read by hwkv_kernel_launches).
 void count_launches(uint64_t n);
 
@@ -131,6 +151,9 @@ int decode_tc_group_pad(int group);  // query-head columns the kernel instance h
 int decode_tc_pad_index(int group);  // 0, 1, 2 for 4, 8, 16 columns
 cudaError_t launch_decode_simt(const DecodeArgs& a, int dtype, int items, cudaStream_t st);
 cudaError_t launch_combine(const DecodeArgs& a, int dtype, cudaStream_t st);
+// rotary positions (hwkv_rope.cu)
+int rope_rows(int64_t tokens);  // rows of one CTA when `tokens` rows are turned in all
+cudaError_t launch_rope(const RopeArgs& a, int layout, bool f32, cudaStream_t st);
 // chunked prefill (hwkv_prefill.cu): attention, then the chunk appended to the rings
 int prefill_tokens_per_cta(int group);  // chunk tokens one CTA answers (two query tiles)
 int prefill_tile_tokens(int group);     // chunk tokens of one 128-row query tile

@@ -6,8 +6,9 @@ kernel launches as a programmatic dependent so consecutive layers keep their ove
 the graph.  ``DecodeStepGraph`` records, for every layer, the append of the new token and the
 windowed attention (``hwkv_append_decode_attn``, or ``hwkv_append`` + ``hwkv_decode_attn``),
 followed by the advance of the positions (``hwkv_advance_positions``), and replays that whole
-step with one launch from the host: every kernel of a replayed step is the library's.
-Inputs are read from, and outputs written to, the static buffers it owns.
+step with one launch from the host: every kernel of a replayed step is the library's.  With a
+rotary table each layer's queries and new keys are first turned at the step's positions
+(``hwkv_rope``).  Inputs are read from, and outputs written to, the static buffers it owns.
 """
 from __future__ import annotations
 
@@ -22,9 +23,10 @@ class DecodeStepGraph:
       k_new [layers][B][kv_heads][D]  new keys, v_new likewise
       pos   [B] int32                 lengths before the append; the step adds 1 to them
     Output: out [layers][B][q_heads][D].
+    rope: a ``rope_table`` when q and k_new come without their rotary positions.
     """
 
-    def __init__(self, pool, scale: float, q_heads: int, pos0, fused: bool = True):
+    def __init__(self, pool, scale: float, q_heads: int, pos0, fused: bool = True, rope=None):
         dev = pool.buffer.device
         L, B, H, D = pool.layers, pool.num_seqs, pool.kv_heads, pool.head_dim
         dt = pool.io_dtype
@@ -38,6 +40,10 @@ class DecodeStepGraph:
         if q_heads != pool.q_heads:
             pool.q_heads = q_heads
             pool._size_workspace()
+        self.rope = rope
+        self._q, self._k = self.q, self.k_new  # what the attention reads
+        if rope is not None:
+            self._q, self._k = torch.empty_like(self.q), torch.empty_like(self.k_new)
         self.scale = float(scale)
         self.fused = fused
         self.graph = torch.cuda.CUDAGraph()
@@ -53,14 +59,16 @@ class DecodeStepGraph:
         if not self.fused:
             p.advance_positions(self.pos, out=self.lens)  # lengths after the append
         for l in range(p.layers):
+            if self.rope is not None:
+                p.rope(self.rope, self.q[l], self.k_new[l], self.pos, q_out=self._q[l], k_out=self._k[l])
             if self.fused:
-                # after layer 0 the kernel just before is the previous layer's attention, which
-                # writes neither the positions nor this layer's pool
-                p.append_decode(l, self.q[l], self.scale, self.k_new[l], self.v_new[l], self.pos, out=self.out[l],
-                                early_reads=l > 0)
+                # the kernel just before is the rotary one, or after layer 0 the previous layer's
+                # attention: neither writes the positions or this layer's pool
+                p.append_decode(l, self._q[l], self.scale, self._k[l], self.v_new[l], self.pos, out=self.out[l],
+                                early_reads=l > 0 or self.rope is not None)
             else:
-                p.append(l, self.k_new[l], self.v_new[l], self.pos)
-                p.decode(l, self.q[l], self.scale, self.lens, out=self.out[l])
+                p.append(l, self._k[l], self.v_new[l], self.pos)
+                p.decode(l, self._q[l], self.scale, self.lens, out=self.out[l])
         p.advance_positions(self.pos)  # the next step's positions
 
     def replay(self):

@@ -319,6 +319,61 @@ int hwkv_set_prefill_config(hwkv_pool_t pool, int max_stages);
  * Changes the workspace size.  Results differ between configurations only by rounding. */
 int hwkv_set_decode_config(hwkv_pool_t pool, int split_tokens, int workers, int kernel);
 
+/* Rotary positions: before a key is appended and a query attends, the pairs of their rows turn
+ * with the position.  (The pages store keys after this step and leave it to the caller.)  Pair i
+ * of a row at position p, (a, b), becomes
+ *     magnitude * (a cos t - b sin t, b cos t + a sin t),   t = p * freq[i],
+ * in fp32, with the angle exact to 2^-23 rad at every position below 2^24, rounded once. */
+#define HWKV_ROPE_HALF 0         /* pairs (i, i + rot_dim / 2)                                   */
+#define HWKV_ROPE_INTERLEAVED 1  /* pairs (2 i, 2 i + 1)                                         */
+typedef struct hwkv_rope {
+  int32_t rot_dim;   /* the first rot_dim dims of a head turn (even, 2 .. head_dim), others pass  */
+  int32_t layout;    /* HWKV_ROPE_*                                                              */
+  double magnitude;  /* factor on the turned dims                                                */
+  double freq[64];   /* radians per position of pair i < rot_dim / 2                             */
+} hwkv_rope_t;
+
+/* Fills a table: freq[i] = base^(-2 i / rot_dim), magnitude 1, then for longer contexts
+ *   HWKV_ROPE_SCALE_NONE
+ *   HWKV_ROPE_SCALE_LINEAR    every freq divided by factor;
+ *   HWKV_ROPE_SCALE_NTK       base * factor^(rot_dim / (rot_dim - 2)) in place of base (no change
+ *                             for rot_dim 2, whose one freq is 1);
+ *   HWKV_ROPE_SCALE_BY_PARTS  a pair that makes r turns over original_len positions keeps the
+ *                             share c = clamp((r - beta_slow) / (beta_fast - beta_slow), 0, 1):
+ *                             freq = c freq + (1 - c) freq / factor; magnitude 0.1 ln(factor) + 1.
+ * factor >= 1 and finite; original_len > 0 and beta_fast > beta_slow for BY_PARTS (ignored
+ * otherwise); base > 0 and finite.  Host only.  Errors: HWKV_ERR_INVALID_ARG.  A caller may also
+ * fill the struct itself. */
+#define HWKV_ROPE_SCALE_NONE 0
+#define HWKV_ROPE_SCALE_LINEAR 1
+#define HWKV_ROPE_SCALE_NTK 2
+#define HWKV_ROPE_SCALE_BY_PARTS 3
+int hwkv_rope_table(int rot_dim, int layout, double base, int scaling, double factor, double original_len,
+                    double beta_fast, double beta_slow, hwkv_rope_t* out);
+
+/* Rows of a chunk: element (seq s, row i, head, d) at s * seq_stride + i * row_stride + head * D + d
+ * (strides in elements, 0 allowed where that index takes one value), so the query and key heads of
+ * a fused projection's output need no copy.  16-byte aligned, strides multiples of 16 bytes. */
+typedef struct hwkv_rows {
+  void* data;
+  int64_t seq_stride;
+  int64_t row_stride;
+} hwkv_rows_t;
+
+/* Turns the queries and keys of a chunk: row i of sequence s, at position pos_dev[s] + i, for
+ * 0 <= i < n_dev[s] (n_dev NULL: all n_max rows).  Rows at or past n_s are not touched.  Tensors
+ * are of the pool's type (bf16 for 8-bit pools), with q_heads query and the pool's kv_heads key
+ * heads; q with q_out, or k with k_out, may be NULL.  An output may be its input (same pointer and
+ * strides); outputs must not overlap anything else.
+ *   pos_dev, n_dev: device int32 [num_seqs]; a negative position or n_s outside [0, n_max] flags
+ *   HWKV_DEVERR_NEG_LENGTH and skips the sequence.
+ * One kernel on `stream`.  A decode call with HWKV_DECODE_EARLY_READS may follow it: it writes
+ * neither lengths nor pool.
+ * Errors: HWKV_ERR_INVALID_ARG, HWKV_ERR_ALIGNMENT, HWKV_ERR_UNSUPPORTED, HWKV_ERR_CUDA. */
+int hwkv_rope(hwkv_pool_t pool, const hwkv_rope_t* rope, const hwkv_rows_t* q, int q_heads, const hwkv_rows_t* k,
+              int n_max, const int32_t* pos_dev, const int32_t* n_dev, const hwkv_rows_t* q_out,
+              const hwkv_rows_t* k_out, void* stream);
+
 /* Number of kernels this library has launched in this process (all pools, all devices).
  * Lets a caller count the launches inside a timed region. */
 int hwkv_kernel_launches(uint64_t* out);

@@ -75,3 +75,37 @@ def test_reference_ring_keeps_the_window():
     for x, y, src in zip(a.resident(90)[1:], b.resident(90)[1:], (k, v)):
         assert np.abs(x - y).max() <= 2.0 ** -9 * a.scales.max()
         assert (np.abs(x - src[50:]) <= 2.0 ** -4 * np.abs(src[50:]) + 2.0 ** -10 * a.scales.max()).all()
+
+
+# ---- rotary tables and refusals --------------------------------------------------------------------
+from reference_ops import rope_frequencies  # noqa: E402
+
+SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+
+
+@pytest.mark.parametrize("scaling", sorted(SCALINGS))
+@pytest.mark.parametrize("rot", [2, 24, 64, 128])
+def test_rope_table_follows_its_formulas(lib, scaling, rot):
+    import head_budgeted_kv_gb300 as hw
+    t = hw.rope_table(128, rot_dim=rot, base=500000.0, scaling=scaling, factor=8.0, original_len=8192)
+    f, m = rope_frequencies(rot, 500000.0, scaling, 8.0, 8192)
+    assert t.rot_dim == rot and t.layout == 0
+    np.testing.assert_allclose(list(t.freq)[:rot // 2], f, rtol=1e-13)
+    assert abs(t.magnitude - m) < 1e-14
+
+
+@pytest.mark.parametrize("args", [
+    (0, 0, 1e4, 0, 1.0, 0.0, 32.0, 1.0), (3, 0, 1e4, 0, 1.0, 0.0, 32.0, 1.0), (130, 0, 1e4, 0, 1.0, 0.0, 32.0, 1.0),
+    (64, 2, 1e4, 0, 1.0, 0.0, 32.0, 1.0), (64, 0, 0.0, 0, 1.0, 0.0, 32.0, 1.0), (64, 0, float("inf"), 0, 1.0, 0.0, 32.0, 1.0),
+    (64, 0, 1e4, 4, 1.0, 0.0, 32.0, 1.0), (64, 0, 1e4, 1, 0.5, 0.0, 32.0, 1.0), (64, 0, 1e4, 2, float("nan"), 0.0, 32.0, 1.0),
+    (64, 0, 1e4, 3, 8.0, 0.0, 32.0, 1.0), (64, 0, 1e4, 3, 8.0, 8192.0, 1.0, 1.0),
+])
+def test_bad_rope_tables_are_refused(lib, args):
+    out = binding.RopeTable()
+    assert lib.hwkv_rope_table(*args, ctypes.byref(out)) == binding.HWKV_ERR_INVALID_ARG
+    assert lib.hwkv_rope_table(64, 0, 1e4, 0, 1.0, 0.0, 32.0, 1.0, None) == binding.HWKV_ERR_INVALID_ARG
+
+
+def test_rope_needs_a_pool(lib):
+    t = binding.hwkv_rope_table(64)
+    assert lib.hwkv_rope(None, t, None, 4, None, 1, None, None, None, None, None) == binding.HWKV_ERR_INVALID_ARG

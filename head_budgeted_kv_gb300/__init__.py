@@ -16,20 +16,20 @@ from typing import Optional
 import torch
 
 from . import binding
-from .binding import (HWKV_BF16, HWKV_E4M3, HWKV_F32, HWKV_KERNEL_AUTO, HWKV_KERNEL_SIMT, HWKV_KERNEL_TENSOR, DecodeLaunch, HwkvError, RopeTable,
+from .binding import (HWKV_BF16, HWKV_E4M3, HWKV_F32, HWKV_KERNEL_AUTO, HWKV_KERNEL_SIMT, HWKV_KERNEL_TENSOR, DecodeLaunch, HwkvError, RopeTable, Score,
                       hwkv_abi_version, hwkv_advance_positions, hwkv_append, hwkv_append_decode_attn, hwkv_block_table,
                       hwkv_check_device_errors, hwkv_kernel_launches,
-                      hwkv_decode_attn, hwkv_decode_workspace_bytes, hwkv_materialize, hwkv_pool_bytes,
+                      hwkv_decode_attn, hwkv_decode_attn_score, hwkv_decode_workspace_bytes, hwkv_materialize, hwkv_pool_bytes,
                       hwkv_pool_create, hwkv_pool_destroy, hwkv_pool_geometry, hwkv_prefill_attn,
-                      hwkv_prefill_plan, hwkv_prefill_workspace_bytes, hwkv_rope, hwkv_rope_table, hwkv_set_block_table, hwkv_set_decode_config,
+                      hwkv_prefill_attn_score, hwkv_prefill_plan, hwkv_prefill_workspace_bytes, hwkv_rope, hwkv_rope_table, hwkv_set_block_table, hwkv_set_decode_config,
                       hwkv_set_prefill_config, hwkv_wait_selftest)
 
 __all__ = [
-    "Pool", "DecodeLaunch", "HwkvError", "RopeTable", "binding", "rope_table", "HWKV_F32", "HWKV_BF16", "HWKV_E4M3", "HWKV_KERNEL_AUTO", "HWKV_KERNEL_TENSOR",
+    "Pool", "DecodeLaunch", "HwkvError", "RopeTable", "Score", "binding", "rope_table", "HWKV_F32", "HWKV_BF16", "HWKV_E4M3", "HWKV_KERNEL_AUTO", "HWKV_KERNEL_TENSOR",
     "HWKV_KERNEL_SIMT", "hwkv_abi_version", "hwkv_advance_positions", "hwkv_append", "hwkv_append_decode_attn", "hwkv_block_table",
     "hwkv_check_device_errors", "hwkv_kernel_launches",
-    "hwkv_decode_attn", "hwkv_decode_workspace_bytes", "hwkv_materialize", "hwkv_pool_bytes", "hwkv_pool_create",
-    "hwkv_pool_destroy", "hwkv_pool_geometry", "hwkv_prefill_attn", "hwkv_prefill_plan", "hwkv_prefill_workspace_bytes", "hwkv_rope", "hwkv_rope_table",
+    "hwkv_decode_attn", "hwkv_decode_attn_score", "hwkv_decode_workspace_bytes", "hwkv_materialize", "hwkv_pool_bytes", "hwkv_pool_create",
+    "hwkv_pool_destroy", "hwkv_pool_geometry", "hwkv_prefill_attn", "hwkv_prefill_attn_score", "hwkv_prefill_plan", "hwkv_prefill_workspace_bytes", "hwkv_rope", "hwkv_rope_table",
     "hwkv_set_block_table", "hwkv_set_decode_config", "hwkv_set_prefill_config", "hwkv_wait_selftest",
 ]
 
@@ -129,19 +129,27 @@ class Pool:
         self._check_io(k_new, v_new)
         hwkv_append(self.handle, layer, k_new, v_new, pos, stream)
 
-    def decode(self, layer: int, q, scale: float, lens, out=None, stream=None, early_reads: bool = False):
+    def decode(self, layer: int, q, scale: float, lens, out=None, stream=None, early_reads: bool = False,
+               softcap: float = 0.0, slopes=None):
+        """Attention of q [B][Hq][D] at lengths ``lens`` (after the append).  softcap > 0 caps the scores
+        at softcap * tanh(score / softcap); slopes (float32 [Hq]) lowers them by slope * distance."""
         if out is None:
             out = torch.empty_like(q)
         self._check_io(q, out)
         if q.shape[1] != self.q_heads:
             self.q_heads = q.shape[1]
             self._size_workspace()
-        hwkv_decode_attn(self.handle, layer, q, scale, lens, out, self.workspace, stream, early_reads)
+        if softcap == 0 and slopes is None:
+            hwkv_decode_attn(self.handle, layer, q, scale, lens, out, self.workspace, stream, early_reads)
+        else:
+            hwkv_decode_attn_score(self.handle, layer, q, binding.score(scale, softcap, slopes, q.shape[1]), lens, out,
+                                   self.workspace, None, None, stream, early_reads)
         return out
 
     def append_decode(self, layer: int, q, scale: float, k_new, v_new, pos, out=None, stream=None,
-                      early_reads: bool = False):
+                      early_reads: bool = False, softcap: float = 0.0, slopes=None):
         """Append the new token (positions ``pos``) and decode at ``pos + 1`` in one call.
+        softcap, slopes: as ``decode``.
         early_reads: the caller's guarantee of HWKV_DECODE_EARLY_READS (lengths, block table
         and this layer's pool not written by the kernel just before in the stream)."""
         if out is None:
@@ -150,30 +158,41 @@ class Pool:
         if q.shape[1] != self.q_heads:
             self.q_heads = q.shape[1]
             self._size_workspace()
-        hwkv_append_decode_attn(self.handle, layer, q, scale, k_new, v_new, pos, out, self.workspace, stream,
-                                early_reads)
+        if softcap == 0 and slopes is None:
+            hwkv_append_decode_attn(self.handle, layer, q, scale, k_new, v_new, pos, out, self.workspace, stream,
+                                    early_reads)
+        else:
+            hwkv_decode_attn_score(self.handle, layer, q, binding.score(scale, softcap, slopes, q.shape[1]), pos, out,
+                                   self.workspace, k_new, v_new, stream, early_reads)
         return out
 
     def decode_launch(self, layer: int, q, scale: float, lens, out, k_new=None, v_new=None, stream=None,
-                      early_reads: bool = False) -> DecodeLaunch:
+                      early_reads: bool = False, softcap: float = 0.0, slopes=None) -> DecodeLaunch:
         """A prepared launch of decode (k_new None, ``lens`` = lengths after the append) or of the
         fused append + decode (``lens`` = positions) on fixed buffers: calling it launches."""
         self._check_io(q, out, k_new, v_new)
         if q.shape[1] != self.q_heads:
             self.q_heads = q.shape[1]
             self._size_workspace()
-        return DecodeLaunch(self.handle, layer, q, scale, lens, out, self.workspace, k_new, v_new, stream, early_reads)
+        return DecodeLaunch(self.handle, layer, q, scale, lens, out, self.workspace, k_new, v_new, stream, early_reads,
+                            softcap, slopes)
 
-    def prefill(self, layer: int, q, scale: float, k_new, v_new, pos, n, out=None, stream=None):
-        """Chunked prefill: q [B][n_max][Hq][D], k_new/v_new [B][n_max][Hkv][D]; pos, n int32 [B].
+    def prefill(self, layer: int, q, scale: float, k_new, v_new, pos, n, out=None, stream=None, softcap: float = 0.0,
+                slopes=None):
+        """Chunked prefill: q [B][n_max][Hq][D], k_new/v_new [B][n_max][Hkv][D]; pos, n int32 [B];
+        softcap, slopes: as ``decode``.
         Keeps a workspace for the split of long key streams, grown on demand."""
         if out is None:
             out = torch.zeros_like(q)
         need = hwkv_prefill_workspace_bytes(self.handle, layer, q.shape[2], q.shape[1])
         if need and (self.prefill_workspace is None or self.prefill_workspace.numel() < need):
             self.prefill_workspace = torch.empty(need, dtype=torch.uint8, device=self.buffer.device)
-        hwkv_prefill_attn(self.handle, layer, q, scale, k_new, v_new, pos, n, out,
-                          self.prefill_workspace if need else None, stream)
+        workspace = self.prefill_workspace if need else None
+        if softcap == 0 and slopes is None:
+            hwkv_prefill_attn(self.handle, layer, q, scale, k_new, v_new, pos, n, out, workspace, stream)
+        else:
+            hwkv_prefill_attn_score(self.handle, layer, q, binding.score(scale, softcap, slopes, q.shape[2]), k_new, v_new,
+                                    pos, n, out, workspace, stream)
         return out
 
     def set_prefill_config(self, max_stages: int = 0):

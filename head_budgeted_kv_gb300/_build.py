@@ -18,7 +18,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libhwkv.so")
 
 SOURCES = ("hwkv_host.cpp", "hwkv_copy.cu", "hwkv_copy_q8.cu", "hwkv_decode_simt.cu", "hwkv_decode_tc.cu",
-           "hwkv_decode_q8.cu", "hwkv_rope.cu", "hwkv_noalloc.cu", "hwkv_prefill.cu")
+           "hwkv_decode_q8.cu", "hwkv_decode_score.cu", "hwkv_rope.cu", "hwkv_noalloc.cu", "hwkv_prefill.cu")
 HEADERS = (os.path.join(CSRC, "hwkv_internal.h"), os.path.join(CSRC, "hwkv_device.cuh"),
            os.path.join(CSRC, "hwkv_tcgen05.cuh"), os.path.join(CSRC, "hwkv_decode_tile.cuh"),
            os.path.join(CSRC, "hwkv_fp8.cuh"), os.path.join(CSRC, "hwkv_decode_tile_q8.cuh"),

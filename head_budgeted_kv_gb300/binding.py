@@ -44,11 +44,17 @@ class RopeTable(ctypes.Structure):
                 ("freq", ctypes.c_double * 64)]
 
 
+class Score(ctypes.Structure):
+    """hwkv_score_t: a scale, a cap (0: none) and a device pointer to slopes per query head (or None)."""
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes_dev", ctypes.c_void_p)]
+
+
 class Rows(ctypes.Structure):
     """hwkv_rows_t: the rows of a chunk, by sequence and row strides in elements."""
     _fields_ = [("data", ctypes.c_void_p), ("seq_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
 
 
+_scorep = ctypes.POINTER(Score)
 _rowsp = ctypes.POINTER(Rows)
 _ropep = ctypes.POINTER(RopeTable)
 _c_i32p = ctypes.POINTER(ctypes.c_int32)
@@ -81,8 +87,10 @@ SIGNATURES = [
     ("hwkv_decode_attn", _i, [_vp, _i, _vp, _i, ctypes.c_float, _vp, _vp, _vp, _u64, _vp]),
     ("hwkv_append_decode_attn", _i, [_vp, _i, _vp, _i, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _u64, _vp]),
     ("hwkv_decode_attn_ex", _i, [_vp, _i, _vp, _i, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _u64, _i, _vp]),
+    ("hwkv_decode_attn_score", _i, [_vp, _i, _vp, _i, _scorep, _vp, _vp, _vp, _vp, _vp, _u64, _i, _vp]),
     ("hwkv_decode_attn_noalloc", _i, [_vp, _i, _vp, _i, ctypes.c_float, _vp, _vp, _vp]),
     ("hwkv_prefill_attn", _i, [_vp, _i, _vp, _i, ctypes.c_float, _vp, _vp, _i, _vp, _vp, _vp, _vp, _u64, _vp]),
+    ("hwkv_prefill_attn_score", _i, [_vp, _i, _vp, _i, _scorep, _vp, _vp, _i, _vp, _vp, _vp, _vp, _u64, _vp]),
     ("hwkv_prefill_workspace_bytes", _i, [_vp, _i, _i, _i, ctypes.POINTER(_u64)]),
     ("hwkv_prefill_plan", _i, [_i, _i, _i, _i, _c_i32p, _i, _i, _i, _i, _i, _i, _c_i32p, _c_i32p, _c_i32p, _c_u64p]),
     ("hwkv_set_prefill_config", _i, [_vp, _i]),
@@ -328,8 +336,30 @@ def hwkv_append_decode_attn(pool: int, layer: int, q: torch.Tensor, scale: float
                                           _ptr(pos), _ptr(out), _ptr(workspace), ws_bytes, _stream_ptr(stream)))
 
 
+def score(scale: float, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+          q_heads: Optional[int] = None) -> Score:
+    """A hwkv_score_t; slopes: float32 [q_heads] on the device (the caller keeps it alive)."""
+    if slopes is not None and (slopes.dtype != torch.float32 or not slopes.is_contiguous()
+                               or (q_heads is not None and slopes.numel() != q_heads)):
+        raise ValueError("slopes must be contiguous float32, one per query head")
+    return Score(float(scale), float(softcap), _ptr(slopes))
+
+
+def hwkv_decode_attn_score(pool: int, layer: int, q: torch.Tensor, score: Score, lens: torch.Tensor, out: torch.Tensor,
+                           workspace: Optional[torch.Tensor], k_new: Optional[torch.Tensor] = None,
+                           v_new: Optional[torch.Tensor] = None, stream=None, early_reads: bool = False):
+    """Decode with a capped or distance-biased score: at lengths `lens` (after the append), or with
+    k_new, v_new at positions `lens`, appended first."""
+    if not all(t.is_contiguous() for t in (q, out, k_new, v_new) if t is not None):
+        raise ValueError("q, out, k_new and v_new must be contiguous")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().hwkv_decode_attn_score(pool, layer, _ptr(q), q.shape[1], score, _ptr(k_new), _ptr(v_new), _ptr(lens),
+                                         _ptr(out), _ptr(workspace), ws_bytes,
+                                         HWKV_DECODE_EARLY_READS if early_reads else 0, _stream_ptr(stream)))
+
+
 class DecodeLaunch:
-    """One hwkv_decode_attn_ex launch whose arguments are checked and marshalled once; each call
+    """One hwkv_decode_attn_ex (or, with a cap or slopes, hwkv_decode_attn_score) launch whose arguments are checked and marshalled once; each call
     issues the launch again with the same buffers (a serving loop's static q / k_new / v_new /
     positions / output, or inputs prepared ahead of a timed loop).  k_new and v_new None: decode
     at lengths `lens` (after the append); given: append at positions `lens`, then decode.  The
@@ -338,16 +368,19 @@ class DecodeLaunch:
 
     def __init__(self, pool: int, layer: int, q: torch.Tensor, scale: float, lens: torch.Tensor, out: torch.Tensor,
                  workspace: Optional[torch.Tensor], k_new: Optional[torch.Tensor] = None,
-                 v_new: Optional[torch.Tensor] = None, stream=None, early_reads: bool = False):
+                 v_new: Optional[torch.Tensor] = None, stream=None, early_reads: bool = False, softcap: float = 0.0,
+                 slopes: Optional[torch.Tensor] = None):
         tensors = [t for t in (q, out, k_new, v_new) if t is not None]
         if not all(t.is_contiguous() for t in tensors):
             raise ValueError("q, out, k_new and v_new must be contiguous")
         if (k_new is None) != (v_new is None):
             raise ValueError("k_new and v_new go together")
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        self._keep = (q, lens, out, workspace, k_new, v_new)
-        self._fn = load().hwkv_decode_attn_ex
-        self._args = (pool, layer, _ptr(q), q.shape[1], float(scale), _ptr(k_new), _ptr(v_new), _ptr(lens), _ptr(out),
+        self._keep = (q, lens, out, workspace, k_new, v_new, slopes)
+        plain = softcap == 0 and slopes is None
+        self._fn = load().hwkv_decode_attn_ex if plain else load().hwkv_decode_attn_score
+        how = float(scale) if plain else score(scale, softcap, slopes, q.shape[1])
+        self._args = (pool, layer, _ptr(q), q.shape[1], how, _ptr(k_new), _ptr(v_new), _ptr(lens), _ptr(out),
                       _ptr(workspace), ws_bytes, HWKV_DECODE_EARLY_READS if early_reads else 0, _stream_ptr(stream))
 
     def __call__(self):
@@ -375,6 +408,18 @@ def hwkv_prefill_attn(pool: int, layer: int, q: torch.Tensor, scale: float, k_ne
     ws, ws_bytes = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
     _check(load().hwkv_prefill_attn(pool, layer, _ptr(q), q.shape[2], float(scale), _ptr(k_new), _ptr(v_new),
                                     q.shape[1], _ptr(pos), _ptr(n), _ptr(out), ws, ws_bytes, _stream_ptr(stream)))
+
+
+def hwkv_prefill_attn_score(pool: int, layer: int, q: torch.Tensor, score: Score, k_new: torch.Tensor,
+                            v_new: torch.Tensor, pos: torch.Tensor, n: torch.Tensor, out: torch.Tensor, workspace=None,
+                            stream=None):
+    """hwkv_prefill_attn with a capped or distance-biased score."""
+    for t in (q, k_new, v_new, out):
+        if not t.is_contiguous():
+            raise ValueError("prefill tensors must be contiguous")
+    ws, ws_bytes = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
+    _check(load().hwkv_prefill_attn_score(pool, layer, _ptr(q), q.shape[2], score, _ptr(k_new), _ptr(v_new), q.shape[1],
+                                          _ptr(pos), _ptr(n), _ptr(out), ws, ws_bytes, _stream_ptr(stream)))
 
 
 def hwkv_prefill_workspace_bytes(pool: int, layer: int, q_heads: int, n_max: int) -> int:

@@ -12,12 +12,12 @@ cudaError_t configure_dim(int ctas_per_sm[kGroupPads]) {
   return configure_one<E4m3, D, 16>(&ctas_per_sm[2]);
 }
 
-template <int D>
+template <int D, bool SC>
 cudaError_t launch_dim(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, cudaStream_t st) {
   switch (decode_tc_group_pad(a.group)) {
-    case 4: return launch_one<E4m3, D, 4>(a, tmap, ctas, st);
-    case 8: return launch_one<E4m3, D, 8>(a, tmap, ctas, st);
-    default: return launch_one<E4m3, D, 16>(a, tmap, ctas, st);
+    case 4: return launch_one<E4m3, D, 4, SC>(a, tmap, ctas, st);
+    case 8: return launch_one<E4m3, D, 8, SC>(a, tmap, ctas, st);
+    default: return launch_one<E4m3, D, 16, SC>(a, tmap, ctas, st);
   }
 }
 
@@ -30,8 +30,10 @@ cudaError_t configure_decode_q8(int head_dim, int ctas_per_sm[kGroupPads]) {
 }
 
 cudaError_t launch_decode_q8(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, cudaStream_t st) {
-  if (a.pv.head_dim == 128) return launch_dim<128>(a, tmap, ctas, st);
-  if (a.pv.head_dim == 64) return launch_dim<64>(a, tmap, ctas, st);
+  if (a.pv.head_dim == 128)
+    return a.score.on ? launch_dim<128, true>(a, tmap, ctas, st) : launch_dim<128, false>(a, tmap, ctas, st);
+  if (a.pv.head_dim == 64)
+    return a.score.on ? launch_dim<64, true>(a, tmap, ctas, st) : launch_dim<64, false>(a, tmap, ctas, st);
   return cudaErrorInvalidValue;
 }
 

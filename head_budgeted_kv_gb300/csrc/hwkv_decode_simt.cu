@@ -41,7 +41,8 @@ __device__ __forceinline__ Item decode_item(const DecodeArgs& a, int item) {
 constexpr int kSimtWarps = 4;
 constexpr int kSimtHeads = 8;  // query heads per CTA
 
-template <typename T, int D>
+// SC: scores are capped or biased by distance
+template <typename T, int D, bool SC>
 __global__ void __launch_bounds__(kSimtWarps * 32) decode_simt_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int W = kSimtWarps;
   constexpr int PER = D / 32;
@@ -71,11 +72,13 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_simt_kernel(const __gr
 
   float qv[GH][PER];
   float m[GH], l[GH], acc[GH][PER];
+  float slope[GH];
   const T* qbase = static_cast<const T*>(a.q) + ((int64_t)it.s * Hq + it.h * G + g0) * D;
 #pragma unroll
   for (int g = 0; g < GH; ++g) {
     m[g] = kNegInf;
     l[g] = 0.f;
+    slope[g] = SC && g < ng ? slope_log2(a.score, it.h * G + g0 + g) : 0.f;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       qv[g][k] = g < ng ? load_in<T>(qbase + g * D + lane + 32 * k) : 0.f;
@@ -107,7 +110,8 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_simt_kernel(const __gr
         for (int k = 0; k < PER; ++k) dot = fmaf(qv[g][k], kv[k], dot);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-        const float sc = dot * sl2;
+        const float sc = SC ? scored_log2<sizeof(T) == 4>(a.score, sl2, dot, slope[g], (float)slot_distance(rs, t))
+                            : dot * sl2;
         const float mn = fmaxf(m[g], sc);
         const float al = ex2(m[g] - mn);
         const float p = ex2(sc - mn);
@@ -188,14 +192,25 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ De
 
 }  // namespace
 
-cudaError_t launch_decode_simt(const DecodeArgs& a, int dtype, int items, cudaStream_t st) {
+namespace {
+
+template <bool SC>
+cudaError_t launch_simt(const DecodeArgs& a, int dtype, int items, cudaStream_t st) {
   const int D = a.pv.head_dim;
   const dim3 grid((unsigned)items, (unsigned)((a.group + kSimtHeads - 1) / kSimtHeads));
-  if (dtype == HWKV_F32 && D == 64) decode_simt_kernel<float, 64><<<grid, kSimtWarps * 32, 0, st>>>(a);
-  else if (dtype == HWKV_F32 && D == 128) decode_simt_kernel<float, 128><<<grid, kSimtWarps * 32, 0, st>>>(a);
-  else if (dtype == HWKV_BF16 && D == 64) decode_simt_kernel<__nv_bfloat16, 64><<<grid, kSimtWarps * 32, 0, st>>>(a);
-  else if (dtype == HWKV_BF16 && D == 128) decode_simt_kernel<__nv_bfloat16, 128><<<grid, kSimtWarps * 32, 0, st>>>(a);
+  if (dtype == HWKV_F32 && D == 64) decode_simt_kernel<float, 64, SC><<<grid, kSimtWarps * 32, 0, st>>>(a);
+  else if (dtype == HWKV_F32 && D == 128) decode_simt_kernel<float, 128, SC><<<grid, kSimtWarps * 32, 0, st>>>(a);
+  else if (dtype == HWKV_BF16 && D == 64) decode_simt_kernel<__nv_bfloat16, 64, SC><<<grid, kSimtWarps * 32, 0, st>>>(a);
+  else if (dtype == HWKV_BF16 && D == 128) decode_simt_kernel<__nv_bfloat16, 128, SC><<<grid, kSimtWarps * 32, 0, st>>>(a);
   else return cudaErrorInvalidValue;
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_decode_simt(const DecodeArgs& a, int dtype, int items, cudaStream_t st) {
+  const cudaError_t e = a.score.on ? launch_simt<true>(a, dtype, items, st) : launch_simt<false>(a, dtype, items, st);
+  if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
 }

@@ -36,6 +36,8 @@
 // Waits are bounded (~2 s); a timeout records HWKV_DEVERR_WAIT_TIMEOUT and the warp stops.
 #pragma once
 
+#include <atomic>
+
 #include "hwkv_decode_tile.cuh"
 #include "hwkv_decode_tile_q8.cuh"
 
@@ -396,10 +398,10 @@ __host__ __device__ constexpr int sk_min_ctas() {
   return sizeof(T) == 1 ? 3 : sizeof(T) == 2 ? (D == 64 ? 3 : 2) : (D == 64 ? 2 : 1);
 }
 
-template <typename Elem, int D, int GP, int NS>
+template <typename Elem, int D, int GP, int NS, bool SC>
 __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
     decode_sk_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ DecodeArgs a) {
-  using State = WarpState<Elem, D, GP>;
+  using State = WarpState<Elem, D, GP, SC>;
   using Out = typename IoType<Elem>::T;  // element type of q, the new rows and the output
   constexpr int W = kWarps;
   constexpr int kEB = (int)sizeof(Elem);
@@ -736,16 +738,31 @@ constexpr int stages() {
 template <typename T, int D, int GP>
 cudaError_t configure_one(int* ctas_per_sm) {
   constexpr int NS = stages<T, D>();
-  cudaError_t e = cudaFuncSetAttribute(decode_sk_kernel<T, D, GP, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       sk_smem_bytes<T, D, GP, NS>());
+  cudaError_t e = cudaFuncSetAttribute(decode_sk_kernel<T, D, GP, NS, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, sk_smem_bytes<T, D, GP, NS>());
   if (e != cudaSuccess) return e;
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_sk_kernel<T, D, GP, NS>, kWarps * 32,
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_sk_kernel<T, D, GP, NS, false>, kWarps * 32,
                                                        sk_smem_bytes<T, D, GP, NS>());
 }
 
-template <typename T, int D, int GP>
+// Scored instances (SC) are prepared at their first launch on a device, not with every pool, and
+// run on the grid of the plain ones.
+template <typename T, int D, int GP, bool SC = false>
 cudaError_t launch_one(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, cudaStream_t st) {
   constexpr int NS = stages<T, D>();
+  if constexpr (SC) {
+    static std::atomic<uint64_t> prepared{0};  // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (!(prepared.load(std::memory_order_relaxed) & bit)) {
+      e = cudaFuncSetAttribute(decode_sk_kernel<T, D, GP, NS, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               sk_smem_bytes<T, D, GP, NS>());
+      if (e != cudaSuccess) return e;
+      prepared.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
   // programmatic dependent launch: the CTAs may become resident while the previous kernel in
   // the stream finishes; they wait for it (griddepcontrol.wait) before reading anything
   cudaLaunchConfig_t cfg = {};
@@ -758,7 +775,7 @@ cudaError_t launch_one(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, decode_sk_kernel<T, D, GP, NS>, *tmap, a);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, decode_sk_kernel<T, D, GP, NS, SC>, *tmap, a);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -46,6 +46,7 @@ cudaError_t configure_decode_tc(int head_dim, int dtype, int ctas_per_sm[kGroupP
 
 cudaError_t launch_decode_tc(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, cudaStream_t st) {
   if (a.pv.elem_bytes == 1) return launch_decode_q8(a, tmap, ctas, st);
+  if (a.score.on) return launch_decode_score(a, tmap, ctas, st);
   const bool f32 = a.pv.elem_bytes == 4;
   if (a.pv.head_dim == 128) return f32 ? launch_dim<float, 128>(a, tmap, ctas, st) : launch_dim<__nv_bfloat16, 128>(a, tmap, ctas, st);
   if (a.pv.head_dim == 64) return f32 ? launch_dim<float, 64>(a, tmap, ctas, st) : launch_dim<__nv_bfloat16, 64>(a, tmap, ctas, st);

@@ -121,6 +121,18 @@ __device__ __forceinline__ void load_q_frags(const DecodeArgs& a, const Group& g
   }
 }
 
+// Slopes (log2 units) of the accumulator columns a lane holds: heads 8*nt + 2*(lane % 4) + {0, 1}.
+template <int NT>
+__device__ __forceinline__ void load_slopes(const DecodeArgs& a, const Group& gr, int G, int lane, float (&slope)[NT][2]) {
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int g = 8 * nt + 2 * (lane & 3) + e;
+      slope[nt][e] = g < G ? slope_log2(a.score, gr.h * G + g) : 0.f;
+    }
+}
+
 // Fused append: when the 16-token tile starting at ring slot t0 holds the new token's slot,
 // that row's copy in shared memory (sK / sV, EB-byte elements, 128-byte swizzle) is replaced
 // by k_new / v_new and the row is written to the pool; no other CTA reads this tile in the
@@ -159,11 +171,12 @@ __device__ __forceinline__ bool patch_new_row(const DecodeArgs& a, const Group& 
 //   * S[16 tok][8 q] = K_tile . Q^T per n-tile (two accumulation chains), masked to resident
 //     slots, online softmax in fp32 in the log2 domain;
 //   * O^T[D][8 q] = alpha * O^T + V_tile^T . P per n-tile.
-template <int D, int NT>
+// SC: scores are capped or biased first (slope[nt]: the lane's two heads), then in log2 units.
+template <int D, int NT, bool SC>
 __device__ __forceinline__ bool consume_tile(const DecodeArgs& a, const Group& gr, int t0, int new_slot,
                                              uint32_t sK, uint32_t sV, const uint32_t (&qf)[NT][D / 16][2],
                                              float (&acc)[D / 16][NT][4], float (&mx)[NT][2], float (&ls)[NT][2],
-                                             int lane) {
+                                             const float (&slope)[NT][2], int lane) {
   constexpr int kSteps = D / 16;
   // ldmatrix lane roles: matrix mi = lane/8, row rr = lane%8
   const int mi = lane >> 3, rr = lane & 7;
@@ -172,7 +185,7 @@ __device__ __forceinline__ bool consume_tile(const DecodeArgs& a, const Group& g
   const int v_row = rr + ((mi >> 1) << 3);  // V tile (transposed A operand): token row
   const int v_dof = (mi & 1) << 3;          //                                +8 dims
   const int gq = lane >> 2;                 // accumulator roles: token/dim row
-  const float sl2 = a.scale_log2;
+  const float sl2 = SC ? 1.f : a.scale_log2;
 
   const bool patched = patch_new_row<2, D>(a, gr, t0, new_slot, sK, sV, lane);
 
@@ -192,6 +205,16 @@ __device__ __forceinline__ bool consume_tile(const DecodeArgs& a, const Group& g
     }
   }
   const bool v0 = slot_valid(gr.rs, t0 + gq), v1 = slot_valid(gr.rs, t0 + gq + 8);
+  if constexpr (SC) {
+    const float d0 = (float)slot_distance(gr.rs, t0 + gq), d1 = (float)slot_distance(gr.rs, t0 + gq + 8);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sa[nt][e] = scored_log2<false>(a.score, a.scale_log2, sa[nt][e] + sb[nt][e], slope[nt][e & 1], e < 2 ? d0 : d1);
+        sb[nt][e] = 0.f;
+      }
+  }
   float al[NT][2];
   uint32_t pb[NT][2];
 #pragma unroll
@@ -275,11 +298,12 @@ __device__ __forceinline__ void issue_tile(const CUtensorMap* tmap, const Decode
 //   * per head: tile maximum and, after exponentiation, tile sum over the 16 lanes of that
 //     parity, the online-softmax update (alpha = 2^(m_old - m_new));
 //   * P (16 x 4 fp32) goes through the warp's 64 floats of `p_s`, and O += P^T . V as FMAs.
-template <int D>
+// SC: scores are capped or biased (slope: the lane's heads 2 (l % 2) and 2 (l % 2) + 1).
+template <int D, bool SC>
 __device__ __forceinline__ bool consume_tile_f32(const DecodeArgs& a, const Group& gr, int t0, int new_slot,
                                                  uint32_t sK, uint32_t sV, const float (&q)[4][D / 32],
                                                  float (&acc)[4][D / 32], float (&m)[4], float (&l)[4],
-                                                 float* p_s, int lane) {
+                                                 const float (&slope)[2], float* p_s, int lane) {
   constexpr int DPL = D / 32;
   const bool patched = patch_new_row<4, D>(a, gr, t0, new_slot, sK, sV, lane);
   float v[64];  // partial <q_g, k_t> over this lane's dims, index t * 4 + g
@@ -316,7 +340,13 @@ __device__ __forceinline__ bool consume_tile_f32(const DecodeArgs& a, const Grou
   const int par = lane & 1;  // this lane's heads: 2 par, 2 par + 1
   const bool valid = slot_valid(gr.rs, t0 + (lane >> 1));
   const float sl2 = a.scale_log2;
-  const float s0 = valid ? v[0] * sl2 : kNegInf, s1 = valid ? v[1] * sl2 : kNegInf;
+  float t_0 = v[0] * sl2, t_1 = v[1] * sl2;
+  if constexpr (SC) {
+    const float d = (float)slot_distance(gr.rs, t0 + (lane >> 1));
+    t_0 = scored_log2<true>(a.score, sl2, v[0], slope[0], d);
+    t_1 = scored_log2<true>(a.score, sl2, v[1], slope[1], d);
+  }
+  const float s0 = valid ? t_0 : kNegInf, s1 = valid ? t_1 : kNegInf;
   float x0 = s0, x1 = s1;
 #pragma unroll
   for (int off = 2; off < 32; off <<= 1) {
@@ -373,22 +403,24 @@ __device__ __forceinline__ bool consume_tile_f32(const DecodeArgs& a, const Grou
   return patched;
 }
 
-// The state one warp carries through a segment, by element type.
-template <typename T, int D, int GP>
+// The state one warp carries through a segment, by element type; SC: capped or biased scores.
+template <typename T, int D, int GP, bool SC>
 struct WarpState;
 
 // bf16: the GQA group on the N side of mma.sync (GP columns in 8-column n-tiles), fp32
 // accumulators in the mma layout; ls holds this lane's partial row sums until finish().
-template <int D, int GP>
-struct WarpState<__nv_bfloat16, D, GP> {
+template <int D, int GP, bool SC>
+struct WarpState<__nv_bfloat16, D, GP, SC> {
   static constexpr int NT = (GP + 7) / 8;
   static constexpr int kEB = 2;
   uint32_t qf[NT][D / 16][2];
   float acc[D / 16][NT][4];
   float mx[NT][2], ls[NT][2];
+  float slope[NT][2];  // SC: of the accumulator's columns, heads 2 (lane % 4) and the next
 
   __device__ __forceinline__ void begin(const DecodeArgs& a, const Group& gr, int G, int lane) {
     load_q_frags<D, NT>(a, gr, G, lane, qf);
+    if constexpr (SC) load_slopes<NT>(a, gr, G, lane, slope);
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -398,7 +430,7 @@ struct WarpState<__nv_bfloat16, D, GP> {
   }
   __device__ __forceinline__ bool consume(const DecodeArgs& a, const Group& gr, int t0, int new_slot, uint32_t sK,
                                           uint32_t sV, float*, int lane) {
-    return consume_tile<D, NT>(a, gr, t0, new_slot, sK, sV, qf, acc, mx, ls, lane);
+    return consume_tile<D, NT, SC>(a, gr, t0, new_slot, sK, sV, qf, acc, mx, ls, slope, lane);
   }
   __device__ __forceinline__ void finish() {
 #pragma unroll
@@ -435,13 +467,14 @@ struct WarpState<__nv_bfloat16, D, GP> {
 };
 
 // fp32: CUDA-core tile work (consume_tile_f32), up to 4 query heads.
-template <int D, int GP>
-struct WarpState<float, D, GP> {
+template <int D, int GP, bool SC>
+struct WarpState<float, D, GP, SC> {
   static_assert(GP == 4, "fp32 tile decode holds 4 query-head columns");
   static constexpr int NT = 1;
   static constexpr int kEB = 4;
   static constexpr int DPL = D / 32;
   float q[4][DPL], acc[4][DPL], m[4], l[4];
+  float slope[2];  // SC: of heads 2 (lane % 2) and the next
 
   __device__ __forceinline__ void begin(const DecodeArgs& a, const Group& gr, int G, int lane) {
     const int Hq = a.pv.kv_heads * G;
@@ -456,10 +489,15 @@ struct WarpState<float, D, GP> {
       m[g] = kNegInf;
       l[g] = 0.f;
     }
+    if constexpr (SC) {
+      const int g = 2 * (lane & 1);
+      slope[0] = g < G ? slope_log2(a.score, gr.h * G + g) : 0.f;
+      slope[1] = g + 1 < G ? slope_log2(a.score, gr.h * G + g + 1) : 0.f;
+    }
   }
   __device__ __forceinline__ bool consume(const DecodeArgs& a, const Group& gr, int t0, int new_slot, uint32_t sK,
                                           uint32_t sV, float* p_s, int lane) {
-    return consume_tile_f32<D>(a, gr, t0, new_slot, sK, sV, q, acc, m, l, p_s, lane);
+    return consume_tile_f32<D, SC>(a, gr, t0, new_slot, sK, sV, q, acc, m, l, slope, p_s, lane);
   }
   __device__ __forceinline__ void finish() {}
   template <int SG>

@@ -113,14 +113,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 
 // 8-bit pools: the GQA group on the N side of mma.sync as for bf16, fp32 accumulators in units
 // of the warp's largest V scale `vs`.
-template <int D, int GP>
-struct WarpState<E4m3, D, GP> {
+template <int D, int GP, bool SC>
+struct WarpState<E4m3, D, GP, SC> {
   static constexpr int NT = (GP + 7) / 8;
   static constexpr float kShift = 15.f;  // log2 of the factor P carries
   uint32_t qf[NT][D / 16][2];
   float acc[D / 16][NT][4];
   float mx[NT][2], ls[NT][2];
-  float qs[NT][2];  // scale * log2(e) * the power of two taken out of each of the lane's heads
+  float qs[NT][2];  // the power of two taken out of each of the lane's heads (times scale * log2(e) unless SC)
+  float slope[NT][2];  // SC: of the lane's heads, log2 units
   float vs;         // largest V scale met (0 at first)
 
   // Q of the group, normalised: the lane holds q[g][16i + 4*q4 .. + 3], g = 8*nt + lane / 4
@@ -152,14 +153,15 @@ struct WarpState<E4m3, D, GP> {
       }
       // the accumulator's columns are heads 2 q4 and 2 q4 + 1
       const float inv = pow2i(x - 14);
-      qs[nt][0] = __shfl_sync(0xffffffffu, inv, (2 * q4) * 4) * a.scale_log2;
-      qs[nt][1] = __shfl_sync(0xffffffffu, inv, (2 * q4 + 1) * 4) * a.scale_log2;
+      qs[nt][0] = __shfl_sync(0xffffffffu, inv, (2 * q4) * 4) * (SC ? 1.f : a.scale_log2);
+      qs[nt][1] = __shfl_sync(0xffffffffu, inv, (2 * q4 + 1) * 4) * (SC ? 1.f : a.scale_log2);
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) acc[j][nt][0] = acc[j][nt][1] = acc[j][nt][2] = acc[j][nt][3] = 0.f;
       mx[nt][0] = mx[nt][1] = kNegInf;
       ls[nt][0] = ls[nt][1] = 0.f;
     }
     vs = 0.f;
+    if constexpr (SC) load_slopes<NT>(a, gr, G, lane, slope);
   }
 
   __device__ __forceinline__ bool consume(const DecodeArgs& a, const Group& gr, int t0, int new_slot, uint32_t sK,
@@ -204,10 +206,16 @@ struct WarpState<E4m3, D, GP> {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float f0 = qs[nt][0] * scale[0], f1 = qs[nt][1] * scale[0];
-      const float s0 = v0 ? (sa[nt][0] + sb[nt][0]) * f0 : kNegInf;
-      const float s1 = v0 ? (sa[nt][1] + sb[nt][1]) * f1 : kNegInf;
-      const float s2 = v1 ? (sa[nt][2] + sb[nt][2]) * f0 : kNegInf;
-      const float s3 = v1 ? (sa[nt][3] + sb[nt][3]) * f1 : kNegInf;
+      float t[4] = {(sa[nt][0] + sb[nt][0]) * f0, (sa[nt][1] + sb[nt][1]) * f1, (sa[nt][2] + sb[nt][2]) * f0,
+                    (sa[nt][3] + sb[nt][3]) * f1};
+      if constexpr (SC) {
+        const float d0 = (float)slot_distance(gr.rs, t0 + gq), d1 = (float)slot_distance(gr.rs, t0 + gq + 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          t[e] = scored_log2<false>(a.score, a.scale_log2, t[e], slope[nt][e & 1], e < 2 ? d0 : d1);
+      }
+      const float s0 = v0 ? t[0] : kNegInf, s1 = v0 ? t[1] : kNegInf;
+      const float s2 = v1 ? t[2] : kNegInf, s3 = v1 ? t[3] : kNegInf;
       float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {

@@ -23,6 +23,33 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// tanh(u): 1 - 2 / (1 + e^2u) with the hardware's approximate exponential and reciprocal, which
+// loses relative accuracy near 0 (the difference's absolute error stays 2^-22), so below 1/4 the
+// odd Taylor polynomial to u^9 (next term 1382/155925 u^11: 2^-26 of u there).  Relative error
+// below 2^-20.  `exact`: CUDA's tanhf, 2 units of fp32.
+template <bool exact>
+__device__ __forceinline__ float tanh_f32(float u) {
+  if constexpr (exact) return tanhf(u);
+  const float t = u * u;
+  const float p = u * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
+  const float r = 1.f - __fdividef(2.f, 1.f + ex2(u * 2.8853900817779268f));
+  return fabsf(u) < 0.25f ? p : r;
+}
+
+// The score of a raw dot product in log2 units: capped, then lowered by slope_log2 per position of
+// distance (exact: fp32 pools).
+template <bool exact>
+__device__ __forceinline__ float scored_log2(const ScoreArgs& sc, float scale_log2, float raw, float slope_log2,
+                                             float distance) {
+  const float t = sc.capped ? sc.cap_out * tanh_f32<exact>(raw * sc.cap_in) : raw * scale_log2;
+  return fmaf(-slope_log2, distance, t);
+}
+
+// slope of query head `head` in log2 units (0 without slopes)
+__device__ __forceinline__ float slope_log2(const ScoreArgs& sc, int head) {
+  return sc.slopes != nullptr ? __ldg(sc.slopes + head) * 1.4426950408889634f : 0.f;
+}
+
 __device__ __forceinline__ uint64_t global_timer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -204,6 +231,13 @@ template <>
 __device__ __forceinline__ void store_out<float>(float* p, float x) { *p = x; }
 template <>
 __device__ __forceinline__ void store_out<__nv_bfloat16>(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// distance of ring slot t's token from the newest one, meaningful for a valid slot
+__device__ __forceinline__ int slot_distance(const Resident& r, int t) {
+  int d = t - r.first_slot;
+  if (d < 0) d += r.C;
+  return r.n - 1 - d;
+}
 
 template <typename T>
 __device__ __forceinline__ float load_in(const T* p);

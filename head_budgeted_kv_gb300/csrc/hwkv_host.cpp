@@ -943,9 +943,28 @@ int hwkv_decode_workspace_bytes(hwkv_pool_t p, int q_heads, uint64_t* out) {
 
 namespace {
 
+// Checks a score and turns it into the kernels' form (plain: only a scale).
+int score_args(const hwkv_score_t& sc, ScoreArgs* out) {
+  if (!std::isfinite(sc.scale)) return fail(HWKV_ERR_INVALID_ARG, "scale must be finite");
+  if (!(sc.softcap >= 0.f) || !std::isfinite(sc.softcap))
+    return fail(HWKV_ERR_INVALID_ARG, "softcap must be finite and not negative");
+  if (!aligned(sc.slopes_dev, 4)) return fail(HWKV_ERR_ALIGNMENT, "slopes must be 4-byte aligned");
+  std::memset(out, 0, sizeof *out);
+  out->capped = sc.softcap > 0.f;
+  out->slopes = sc.slopes_dev;
+  out->on = out->capped || out->slopes != nullptr;
+  if (out->capped) {
+    out->cap_in = sc.scale / sc.softcap;
+    out->cap_out = sc.softcap * 1.4426950408889634f;
+    if (!std::isfinite(out->cap_in) || !std::isfinite(out->cap_out))
+      return fail(HWKV_ERR_INVALID_ARG, "scale / softcap and softcap * log2(e) must be finite in fp32");
+  }
+  return HWKV_OK;
+}
+
 // Shared body of hwkv_decode_attn (len_add 0, no new rows) and hwkv_append_decode_attn
 // (len_add 1: lens are the positions before the append, k_new / v_new are appended).
-int decode_common(hwkv_pool_t p, int layer, const void* q, int q_heads, float scale, const int32_t* lens_dev,
+int decode_common(hwkv_pool_t p, int layer, const void* q, int q_heads, hwkv_score_t score, const int32_t* lens_dev,
                   int len_add, const void* k_new, const void* v_new, void* out, void* workspace, uint64_t ws_bytes,
                   int flags, void* stream) {
   if (!p) return fail(HWKV_ERR_INVALID_ARG, "pool is NULL");
@@ -954,9 +973,9 @@ int decode_common(hwkv_pool_t p, int layer, const void* q, int q_heads, float sc
   if (layer < 0 || layer >= g.layers) return fail(HWKV_ERR_INVALID_ARG, "layer %d out of range", layer);
   if (q_heads < g.kv_heads || q_heads % g.kv_heads != 0 || q_heads / g.kv_heads > kMaxGroup)
     return fail(HWKV_ERR_UNSUPPORTED, "q_heads must be G * kv_heads with 1 <= G <= %d (got %d)", kMaxGroup, q_heads);
-  if (!(scale == scale) || scale == std::numeric_limits<float>::infinity() ||
-      scale == -std::numeric_limits<float>::infinity())
-    return fail(HWKV_ERR_INVALID_ARG, "scale must be finite");
+  ScoreArgs sa;
+  const int src = score_args(score, &sa);
+  if (src != HWKV_OK) return src;
   if (!q || !out || !lens_dev) return fail(HWKV_ERR_INVALID_ARG, "NULL tensor argument");
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lens_dev, 4))
     return fail(HWKV_ERR_ALIGNMENT, "q / out must be 16-byte aligned, lens 4-byte aligned");
@@ -1002,7 +1021,8 @@ int decode_common(hwkv_pool_t p, int layer, const void* q, int q_heads, float sc
     a.counters = p->d_counters + (int64_t)layer * groups;
     a.counters1 = p->d_counters + (int64_t)g.layers * groups + (int64_t)layer * groups * p->counter_merge_blocks;
   }
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = score.scale * 1.4426950408889634f;
+  a.score = sa;
   a.group = G;
   a.split_tokens = lp.split;
   std::memcpy(a.chunk_prefix, lp.chunk_prefix, sizeof a.chunk_prefix);
@@ -1034,22 +1054,32 @@ extern "C" {
 
 int hwkv_decode_attn(hwkv_pool_t p, int layer, const void* q, int q_heads, float scale, const int32_t* lens_dev,
                      void* out, void* workspace, uint64_t ws_bytes, void* stream) {
-  return decode_common(p, layer, q, q_heads, scale, lens_dev, 0, nullptr, nullptr, out, workspace, ws_bytes, 0,
-                       stream);
+  return decode_common(p, layer, q, q_heads, {scale, 0.f, nullptr}, lens_dev, 0, nullptr, nullptr, out, workspace,
+                       ws_bytes, 0, stream);
 }
 
 int hwkv_decode_attn_ex(hwkv_pool_t p, int layer, const void* q, int q_heads, float scale, const void* k_new,
                         const void* v_new, const int32_t* lens_dev, void* out, void* workspace, uint64_t ws_bytes,
                         int flags, void* stream) {
   const bool fused = k_new != nullptr || v_new != nullptr;
-  return decode_common(p, layer, q, q_heads, scale, lens_dev, fused ? 1 : 0, k_new, v_new, out, workspace, ws_bytes,
+  return decode_common(p, layer, q, q_heads, {scale, 0.f, nullptr}, lens_dev, fused ? 1 : 0, k_new, v_new, out,
+                       workspace, ws_bytes, flags, stream);
+}
+
+int hwkv_decode_attn_score(hwkv_pool_t p, int layer, const void* q, int q_heads, const hwkv_score_t* score,
+                           const void* k_new, const void* v_new, const int32_t* lens_dev, void* out, void* workspace,
+                           uint64_t ws_bytes, int flags, void* stream) {
+  if (!score) return fail(HWKV_ERR_INVALID_ARG, "score is NULL");
+  const bool fused = k_new != nullptr || v_new != nullptr;
+  return decode_common(p, layer, q, q_heads, *score, lens_dev, fused ? 1 : 0, k_new, v_new, out, workspace, ws_bytes,
                        flags, stream);
 }
 
 int hwkv_append_decode_attn(hwkv_pool_t p, int layer, const void* q, int q_heads, float scale, const void* k_new,
                             const void* v_new, const int32_t* pos_dev, void* out, void* workspace, uint64_t ws_bytes,
                             void* stream) {
-  return decode_common(p, layer, q, q_heads, scale, pos_dev, 1, k_new, v_new, out, workspace, ws_bytes, 0, stream);
+  return decode_common(p, layer, q, q_heads, {scale, 0.f, nullptr}, pos_dev, 1, k_new, v_new, out, workspace,
+                       ws_bytes, 0, stream);
 }
 
 int hwkv_prefill_workspace_bytes(hwkv_pool_t p, int layer, int q_heads, int n_max, uint64_t* out) {
@@ -1102,6 +1132,14 @@ int hwkv_set_prefill_config(hwkv_pool_t p, int max_stages) {
 int hwkv_prefill_attn(hwkv_pool_t p, int layer, const void* q, int q_heads, float scale, const void* k_new,
                       const void* v_new, int n_max, const int32_t* pos_dev, const int32_t* n_dev, void* out,
                       void* workspace, uint64_t workspace_bytes, void* stream) {
+  const hwkv_score_t score = {scale, 0.f, nullptr};
+  return hwkv_prefill_attn_score(p, layer, q, q_heads, &score, k_new, v_new, n_max, pos_dev, n_dev, out, workspace,
+                                 workspace_bytes, stream);
+}
+
+int hwkv_prefill_attn_score(hwkv_pool_t p, int layer, const void* q, int q_heads, const hwkv_score_t* score,
+                            const void* k_new, const void* v_new, int n_max, const int32_t* pos_dev,
+                            const int32_t* n_dev, void* out, void* workspace, uint64_t workspace_bytes, void* stream) {
   if (!p) return fail(HWKV_ERR_INVALID_ARG, "pool is NULL");
   const Geometry& g = p->g;
   if (layer < 0 || layer >= g.layers) return fail(HWKV_ERR_INVALID_ARG, "layer %d out of range", layer);
@@ -1110,9 +1148,10 @@ int hwkv_prefill_attn(hwkv_pool_t p, int layer, const void* q, int q_heads, floa
     return fail(HWKV_ERR_UNSUPPORTED, "q_heads must be a multiple of kv_heads");
   const int G = q_heads / g.kv_heads;
   if (G > kMaxGroup) return fail(HWKV_ERR_UNSUPPORTED, "q_heads must be G * kv_heads with 1 <= G <= %d", kMaxGroup);
-  if (!(scale == scale) || scale == std::numeric_limits<float>::infinity() ||
-      scale == -std::numeric_limits<float>::infinity())
-    return fail(HWKV_ERR_INVALID_ARG, "scale must be finite");
+  if (!score) return fail(HWKV_ERR_INVALID_ARG, "score is NULL");
+  ScoreArgs sa;
+  const int src = score_args(*score, &sa);
+  if (src != HWKV_OK) return src;
   if (n_max < 1) return fail(HWKV_ERR_INVALID_ARG, "n_max must be >= 1");
   if ((int64_t)g.num_seqs * n_max > kInt32Max) return fail(HWKV_ERR_UNSUPPORTED, "num_seqs * n_max must be below 2^31");
   if (!q || !k_new || !v_new || !out || !pos_dev || !n_dev) return fail(HWKV_ERR_INVALID_ARG, "NULL tensor argument");
@@ -1169,7 +1208,8 @@ int hwkv_prefill_attn(hwkv_pool_t p, int layer, const void* q, int q_heads, floa
     a.part_o = static_cast<float*>(workspace);
     a.part_ml = a.part_o + (size_t)a.head_ctas[g.kv_heads] * 2 * 128 * g.head_dim;
   }
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = score->scale * 1.4426950408889634f;
+  a.score = sa;
   a.bs_log2 = -1;
   for (int b = 0; b < 31; ++b)
     if ((1 << b) == g.block_size) a.bs_log2 = b;

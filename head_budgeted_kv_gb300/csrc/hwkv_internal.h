@@ -50,6 +50,16 @@ struct CopyArgs {
   int32_t rows_per_cta;    // materialise only
 };
 
+// What happens to a score s = scale <q, k> before the softmax: cap * tanh(s / cap) when capped,
+// then less slope * (distance of the key from the query).
+struct ScoreArgs {
+  int32_t on;              // the scored kernel instances run
+  int32_t capped;
+  float cap_in;            // scale / cap
+  float cap_out;           // cap * log2(e)
+  const float* slopes;     // [Hq] slopes, or null
+};
+
 struct DecodeArgs {
   PoolView pv;
   LayerGeom g;
@@ -68,6 +78,7 @@ struct DecodeArgs {
   float* part2_ml;         // [B*H*merge_blocks][G][2]
   int32_t merge_blocks;    // first-level merge blocks per head: ceil(CTAs / kMergeBlock) + 1
   float scale_log2;        // scale * log2(e)
+  ScoreArgs score;         // capped or distance-biased scores (scored instances only)
   int32_t group;           // G = Hq / H
   int32_t split_tokens;    // CUDA-core kernel: tokens per split-K chunk (power of two)
   int32_t chunk_prefix[kMaxKvHeads + 1];  // CUDA-core kernel: prefix over heads of ceil(C_h / split)
@@ -86,6 +97,7 @@ struct PrefillArgs {
   int32_t group;           // G = Hq / H
   int32_t q_tiles;         // query-tile pairs per (seq, head): ceil(n_max / chunk tokens per pair)
   float scale_log2;
+  ScoreArgs score;         // capped or distance-biased scores (the scored instance only)
   int32_t bs_log2;         // log2(block_size), or -1 when it is not a power of two
   int32_t stage_tb;        // rows of one block in a 64-key pool copy (16, 32, 64), 0: per-tile copies only
   int32_t head_order[kMaxKvHeads];  // heads in work order (longest CTAs first)
@@ -147,6 +159,8 @@ cudaError_t launch_decode_tc(const DecodeArgs& a, const CUtensorMap* tmap, int c
 // the same for e4m3 pools (hwkv_decode_q8.cu)
 cudaError_t configure_decode_q8(int head_dim, int ctas_per_sm[kGroupPads]);
 cudaError_t launch_decode_q8(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, cudaStream_t st);
+// the same for capped or distance-biased scores, bf16 and fp32 pools (hwkv_decode_score.cu)
+cudaError_t launch_decode_score(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, cudaStream_t st);
 int decode_tc_group_pad(int group);  // query-head columns the kernel instance holds (4, 8 or 16)
 int decode_tc_pad_index(int group);  // 0, 1, 2 for 4, 8, 16 columns
 cudaError_t launch_decode_simt(const DecodeArgs& a, int dtype, int items, cudaStream_t st);

@@ -175,7 +175,8 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
   return lo > hi ? 0u : ((0xFFFFu >> (15 - hi)) & (0xFFFFu << lo));
 }
 
-template <int D>
+// SC: scores are capped or biased by distance, in registers between the two products.
+template <int D, bool SC>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap pool_map,
                                                                const __grid_constant__ CUtensorMap stage_map,
                                                                const __grid_constant__ CUtensorMap knew_map,
@@ -521,7 +522,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
     const int pq = p0 + tok;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t colO = Cfg::kColO + x * D;
-    const float sl2 = a.scale_log2;
+    const float sl2 = SC ? 1.f : a.scale_log2;  // capped and biased scores are in log2 units already
+    const float slope = SC ? slope_log2(a.score, h * G + r % G) : 0.f;
     // with a positive scale the row maximum is taken on raw scores and scale-and-subtract is
     // one packed FMA; masked scores become -inf before scaling (+inf for a negative scale)
     const bool pos_scale = sl2 > 0.f;
@@ -546,6 +548,19 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       if ((jj & 31) == 0)
         clean_word = jj < 32 * kCleanWords ? reinterpret_cast<volatile uint32_t*>(s_clean[x])[jj >> 5] : 0u;
       const bool clean = (clean_word >> (jj & 31)) & 1u;
+      if constexpr (SC) {
+#pragma unroll
+        for (int u = 0; u < kPfSub; ++u) {
+          // distance of the row from the tile's first key; a ring tile may wrap to keys C older
+          const PfKeyTile kt = key_tile(tl, j * kPfSub + u, C);
+          const int d0 = pq - (kt.kind == 0 ? tl.p_oldest : p0) - kt.a;
+          const int wrap = kt.kind == 0 ? C - kt.a : kTile;
+#pragma unroll
+          for (int i = 0; i < kTile; ++i)
+            sv[u * kTile + i] = scored_log2<false>(a.score, a.scale_log2, sv[u * kTile + i], slope,
+                                                   (float)(d0 - i + (i >= wrap ? C : 0)));
+        }
+      }
       if (!clean) {
         PfKeyTile kt[kPfSub];
 #pragma unroll
@@ -838,13 +853,13 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const __grid_const
   }
 }
 
-template <int D>
+template <int D, bool SC>
 cudaError_t launch_pf(const PrefillArgs& a, const CUtensorMap* pm, const CUtensorMap* sm, const CUtensorMap* km,
                       const CUtensorMap* vm, const CUtensorMap* km64, const CUtensorMap* vm64, const CUtensorMap* qm,
                       int items, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  prefill_kernel<D><<<items, kPfThreads, PfCfg<D>::kSmem, st>>>(*pm, *sm, *km, *vm, *km64, *vm64, *qm, a);
+  prefill_kernel<D, SC><<<items, kPfThreads, PfCfg<D>::kSmem, st>>>(*pm, *sm, *km, *vm, *km64, *vm64, *qm, a);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -887,10 +902,10 @@ cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap* pool_map, co
                            const CUtensorMap* vnew64_map, const CUtensorMap* q_map, cudaStream_t st) {
   const int items = a.head_ctas[a.pv.kv_heads];
   if (a.group < 1 || a.group > kMaxGroup) return cudaErrorInvalidValue;
-  if (a.pv.head_dim == 128)
-    return launch_pf<128>(a, pool_map, stage_map, knew_map, vnew_map, knew64_map, vnew64_map, q_map, items, st);
-  if (a.pv.head_dim == 64)
-    return launch_pf<64>(a, pool_map, stage_map, knew_map, vnew_map, knew64_map, vnew64_map, q_map, items, st);
+  auto* launch = a.pv.head_dim == 128 ? (a.score.on ? launch_pf<128, true> : launch_pf<128, false>)
+                                      : (a.score.on ? launch_pf<64, true> : launch_pf<64, false>);
+  if (a.pv.head_dim == 128 || a.pv.head_dim == 64)
+    return launch(a, pool_map, stage_map, knew_map, vnew_map, knew64_map, vnew64_map, q_map, items, st);
   return cudaErrorInvalidValue;
 }
 

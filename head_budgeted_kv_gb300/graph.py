@@ -24,9 +24,11 @@ class DecodeStepGraph:
       pos   [B] int32                 lengths before the append; the step adds 1 to them
     Output: out [layers][B][q_heads][D].
     rope: a ``rope_table`` when q and k_new come without their rotary positions.
+    softcap, slopes: capped or distance-biased scores, as in ``Pool.decode``.
     """
 
-    def __init__(self, pool, scale: float, q_heads: int, pos0, fused: bool = True, rope=None):
+    def __init__(self, pool, scale: float, q_heads: int, pos0, fused: bool = True, rope=None, softcap: float = 0.0,
+                 slopes=None):
         dev = pool.buffer.device
         L, B, H, D = pool.layers, pool.num_seqs, pool.kv_heads, pool.head_dim
         dt = pool.io_dtype
@@ -41,6 +43,7 @@ class DecodeStepGraph:
             pool.q_heads = q_heads
             pool._size_workspace()
         self.rope = rope
+        self._score = {"softcap": softcap, "slopes": slopes}
         self._q, self._k = self.q, self.k_new  # what the attention reads
         if rope is not None:
             self._q, self._k = torch.empty_like(self.q), torch.empty_like(self.k_new)
@@ -65,10 +68,10 @@ class DecodeStepGraph:
                 # the kernel just before is the rotary one, or after layer 0 the previous layer's
                 # attention: neither writes the positions or this layer's pool
                 p.append_decode(l, self._q[l], self.scale, self._k[l], self.v_new[l], self.pos, out=self.out[l],
-                                early_reads=l > 0 or self.rope is not None)
+                                early_reads=l > 0 or self.rope is not None, **self._score)
             else:
                 p.append(l, self._k[l], self.v_new[l], self.pos)
-                p.decode(l, self._q[l], self.scale, self.lens, out=self.out[l])
+                p.decode(l, self._q[l], self.scale, self.lens, out=self.out[l], **self._score)
         p.advance_positions(self.pos)  # the next step's positions
 
     def replay(self):

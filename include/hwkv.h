@@ -241,6 +241,26 @@ int hwkv_decode_attn_ex(hwkv_pool_t pool, int layer, const void* q, int q_heads,
                         const void* v_new, const int32_t* lens_dev, void* out, void* workspace,
                         uint64_t workspace_bytes, int flags, void* stream);
 
+/* A score that is more than scale * <q, k>: capped, then lowered with the distance of the key,
+ *     s = scale * <q, k>;  if softcap > 0: s = softcap * tanh(s / softcap);
+ *     s = s - slope[query head] * (position of the query - position of the key).
+ * In a decode step the query's position is len - 1, so the newest token's distance is 0.
+ *   softcap: finite, 0 (none) or positive, with scale / softcap and softcap * log2(e) finite in
+ *            fp32;  slopes_dev: device float [q_heads], finite, or NULL (none). */
+typedef struct hwkv_score {
+  float scale;
+  float softcap;
+  const float* slopes_dev;
+} hwkv_score_t;
+
+/* hwkv_decode_attn_ex with such a score, for every pool type and shape; the same workspace, flags
+ * and errors.  The capped or biased scores differ from the formula by at most 2^-20 of their size
+ * before the softmax (fp32 pools: a few fp32 roundings).  A score with neither cap nor slopes runs
+ * the plain kernels. */
+int hwkv_decode_attn_score(hwkv_pool_t pool, int layer, const void* q, int q_heads, const hwkv_score_t* score,
+                           const void* k_new, const void* v_new, const int32_t* lens_dev, void* out, void* workspace,
+                           uint64_t workspace_bytes, int flags, void* stream);
+
 /* Bytes of the static scratch array behind hwkv_decode_attn_noalloc. */
 #define HWKV_NOALLOC_SCRATCH_BYTES (4u << 20)
 
@@ -284,6 +304,12 @@ int hwkv_decode_attn_noalloc(hwkv_pool_t pool, int layer, const void* q, int q_h
 int hwkv_prefill_attn(hwkv_pool_t pool, int layer, const void* q, int q_heads, float scale, const void* k_new,
                       const void* v_new, int n_max, const int32_t* pos_dev, const int32_t* n_dev, void* out,
                       void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* hwkv_prefill_attn with a capped or distance-biased score (see hwkv_score_t; a query's position
+ * is that of its token). */
+int hwkv_prefill_attn_score(hwkv_pool_t pool, int layer, const void* q, int q_heads, const hwkv_score_t* score,
+                            const void* k_new, const void* v_new, int n_max, const int32_t* pos_dev,
+                            const int32_t* n_dev, void* out, void* workspace, uint64_t workspace_bytes, void* stream);
 
 /* Bytes of workspace hwkv_prefill_attn uses to split the key streams of `layer` for chunks of up
  * to n_max tokens and q_heads query heads (0 when nothing would be split).  Host only; depends on

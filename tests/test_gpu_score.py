@@ -1,0 +1,237 @@
+"""Capped and distance-biased scores on the GPU, decode and chunked prefill, against 64 bits.
+
+Tolerance, per element, with A = sum_p softmax_p |v_p| and T the largest |score| of the row:
+* the score's own error: 2^-20 T from the cap (header) and 2^-22 T from the fp32 products, the log2
+  units and the bias, against a dot product whose 128 terms each round by 2^-24 of |q||k| (2^-17 of
+  sum |q_d k_d| scale, bounded by S below); the exponential 2^-22: each weight is off by
+  e = 2^-19 T + 2^-17 S + 2^-22 relatively, and the sum it is normalised by as well: 2 e A;
+* tensor-core paths round the weights to bf16 (2^-8 A more, 8-bit pools to fp16, 2^-11 A; the sum is
+  taken of the unrounded weights); bf16 outputs round by 2^-8 of the value;
+* fp32 pools take tanhf (2 units) instead: e = 2^-21 T + 2^-17 S + 2^-22, outputs 2^-23."""
+import numpy as np
+import pytest
+import torch
+
+import head_budgeted_kv_gb300 as hw
+from reference_ops import Ring8, attention
+
+pytestmark = pytest.mark.gpu
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32, "e4m3": torch.float8_e4m3fn}
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    hw.binding.load()
+    yield
+    torch.cuda.synchronize()
+
+
+def np64(t):
+    return t.float().cpu().double().numpy()
+
+
+def tolerance(kind, q, k, v, scale, distance, cap, slope):
+    ref, mass, top = attention(q, k, v, scale, distance, cap, slope)
+    size = float((np.abs(k) @ np.abs(q)).max(initial=0.0)) * abs(scale)
+    e = 2.0 ** (-21 if kind == "f32" else -19) * top + 2.0 ** -17 * size + 2.0 ** -22
+    tol = 2 * e * mass + {"f32": 0.0, "bf16": 2.0 ** -8, "e4m3": 2.0 ** -10}[kind] * mass
+    return ref, tol + (2.0 ** -23 if kind == "f32" else 2.0 ** -8) * np.abs(ref) + 1e-30
+
+
+def histories(gen, B, H, L, D, dtype):
+    return (torch.randn((B, H, L, D), generator=gen, device="cuda").to(dtype) for _ in range(2))
+
+
+SCORES = {"cap": (15.0, False), "bias": (0.0, True), "both": (8.0, True), "tiny cap": (1e-3, False), "large cap": (1e5, False)}
+
+
+@pytest.mark.parametrize("score", sorted(SCORES))
+@pytest.mark.parametrize("kind,D,G,bs,windows,lens", [
+    ("bf16", 128, 4, 16, [64, 200, 1], [300, 20]),
+    ("bf16", 64, 16, 32, [100, 40], [333, 0]),
+    ("bf16", 128, 9, 16, [700], [1000]),
+    ("bf16", 128, 3, 5, [23, 60], [100, 9]),        # CUDA-core kernel
+    ("f32", 128, 4, 16, [64, 200], [300, 20]),
+    ("f32", 64, 3, 16, [33], [100, 7]),
+    ("f32", 64, 10, 16, [130, 20], [400, 3]),       # CUDA-core kernel, two slices of heads
+    ("e4m3", 128, 4, 16, [64, 200, 33], [300, 20]),
+    ("e4m3", 64, 16, 48, [100, 40], [333, 0]),
+    ("e4m3", 128, 1, 16, [2000], [2500]),
+])
+def test_decode(kind, D, G, bs, windows, lens, score):
+    cap, biased = SCORES[score]
+    B, H = len(lens), len(windows)
+    gen = torch.Generator(device="cuda").manual_seed(len(windows) * 100 + G)
+    pool = hw.Pool(1, H, D, bs, [windows], B, TYPES[kind], q_heads=G * H)
+    io = pool.io_dtype
+    k, v = histories(gen, B, H, max(lens) + 1, D, io)
+    pos = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    pool.materialize(0, k, v, pos)
+    q = (torch.randn((B, G * H, D), generator=gen, device="cuda") * 3).to(io)
+    slopes = torch.tensor([0.0 if g == 1 else 2.0 ** (-8.0 * (g + 1) / (G * H)) for g in range(G * H)], device="cuda")
+    kw = dict(softcap=cap, slopes=slopes if biased else None)
+    at = torch.arange(B, device="cuda")
+    kn, vn = k[at, :, pos.long()].contiguous(), v[at, :, pos.long()].contiguous()
+    scale = D ** -0.5
+    before = pool.decode(0, q, scale, pos, **kw)
+    after = pool.append_decode(0, q, scale, kn, vn, pos, **kw)
+    qq, kk, vv = np64(q), np64(k), np64(v)
+    for s in range(B):
+        for h in range(H):
+            ring = Ring8(windows[h], bs, D) if kind == "e4m3" else None
+            if ring:
+                ring.materialize(kk[s, h], vv[s, h], lens[s])
+            for out, n in ((before, lens[s]), (after, lens[s] + 1)):
+                if ring and n > lens[s]:
+                    ring.append(kk[s, h, n - 1], vv[s, h, n - 1], n - 1)
+                p, rk, rv = ring.resident(n) if ring else (np.arange(max(0, n - windows[h]), n), None, None)
+                rk, rv = (rk, rv) if ring else (kk[s, h, p], vv[s, h, p])
+                got = np64(out)[s]
+                for g in range(h * G, (h + 1) * G):
+                    slope = float(slopes[g]) if biased else 0.0
+                    ref, tol = tolerance(kind, qq[s, g], rk, rv, scale, n - 1 - p, cap, slope)
+                    assert (np.abs(got[g] - ref) <= tol).all(), (s, g, n, float((np.abs(got[g] - ref) / tol).max()))
+    # a prepared launch with early reads gives the same bits
+    out = torch.empty_like(q)
+    launch = pool.decode_launch(0, q, scale, pos + 1, out, early_reads=True, **kw)
+    launch()
+    again = pool.decode(0, q, scale, pos + 1, **kw)
+    assert torch.equal(out, again)
+    assert pool.check_device_errors() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
+def test_neither_cap_nor_slopes_is_the_plain_call(kind):
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    pool = hw.Pool(1, 2, 64, 16, [[64, 200]], 2, TYPES[kind], q_heads=8)
+    k, v = histories(gen, 2, 2, 300, 64, pool.io_dtype)
+    lens = torch.tensor([300, 41], dtype=torch.int32, device="cuda")
+    pool.materialize(0, k, v, lens)
+    q = torch.randn((2, 8, 64), generator=gen, device="cuda").to(pool.io_dtype)
+    out = torch.empty_like(q)
+    hw.hwkv_decode_attn_score(pool.handle, 0, q, hw.binding.score(0.125), lens, out, pool.workspace)
+    assert torch.equal(out, pool.decode(0, q, 0.125, lens))
+    # zero slopes take the scored kernels: the same scores up to their rounding
+    zero = pool.decode(0, q, 0.125, lens, slopes=torch.zeros(8, device="cuda"))
+    assert (zero.float() - out.float()).abs().max() <= 2.0 ** -7 * out.float().abs().max()
+
+
+def test_long_groups_merge_alike():
+    """A biased group split over many CTAs, and few, against the same formula."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    pool = hw.Pool(1, 1, 128, 16, [[8000]], 1, torch.bfloat16, q_heads=4)
+    k, v = histories(gen, 1, 1, 9000, 128, torch.bfloat16)
+    lens = torch.tensor([9000], dtype=torch.int32, device="cuda")
+    pool.materialize(0, k, v, lens)
+    q = torch.randn((1, 4, 128), generator=gen, device="cuda").bfloat16()
+    slopes = torch.tensor([1e-4, 1e-3, 0.0, 1.0], device="cuda")
+    p = np.arange(1000, 9000)
+    for workers in (0, 1, 40, 280):
+        pool.set_decode_config(workers=workers)
+        got = np64(pool.decode(0, q, 0.09, lens, softcap=20.0, slopes=slopes))
+        for g in range(4):
+            ref, tol = tolerance("bf16", np64(q)[0, g], np64(k)[0, 0, p], np64(v)[0, 0, p], 0.09, 8999 - p, 20.0,
+                                 float(slopes[g]))
+            assert (np.abs(got[0, g] - ref) <= tol).all(), (workers, g)
+
+
+@pytest.mark.parametrize("score", ["cap", "bias", "both"])
+@pytest.mark.parametrize("D,G,bs,windows,pos,n,max_stages", [
+    (128, 4, 16, [64, 200], [0, 150], [130, 7], 0),
+    (64, 2, 16, [40, 500, 16], [333, 20], [50, 100], 0),
+    (128, 16, 32, [100], [300], [33], 0),
+    (64, 1, 64, [129, 700], [1000, 64], [300, 1], 0),
+    (128, 3, 48, [333], [90], [200], 0),
+    (128, 4, 16, [3000], [4000], [40], 8),          # a split key stream
+    (64, 8, 16, [24], [24], [0], 0),                # an empty chunk
+])
+def test_prefill(D, G, bs, windows, pos, n, max_stages, score):
+    cap, biased = SCORES[score]
+    B, H, n_max = len(pos), len(windows), max(max(n), 1)
+    gen = torch.Generator(device="cuda").manual_seed(sum(pos) + G)
+    pool = hw.Pool(1, H, D, bs, [windows], B, torch.bfloat16, q_heads=G * H)
+    pool.set_prefill_config(max_stages)
+    L = max(p + c for p, c in zip(pos, n)) + n_max
+    k, v = histories(gen, B, H, L, D, torch.bfloat16)
+    tpos = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    tn = torch.tensor(n, dtype=torch.int32, device="cuda")
+    pool.materialize(0, k, v, tpos)
+    q = (torch.randn((B, n_max, G * H, D), generator=gen, device="cuda") * 3).bfloat16()
+    kn, vn = (torch.stack([t[s, :, pos[s]:pos[s] + n_max].transpose(0, 1) for s in range(B)]).contiguous() for t in (k, v))
+    slopes = torch.tensor([2.0 ** (-8.0 * (g + 1) / (G * H)) for g in range(G * H)], device="cuda")
+    out = torch.full_like(q, 7.0)
+    scale = D ** -0.5
+    pool.prefill(0, q, scale, kn, vn, tpos, tn, out=out, softcap=cap, slopes=slopes if biased else None)
+    assert pool.check_device_errors() == 0
+    qq, kk, vv, got = np64(q), np64(k), np64(v), np64(out)
+    for s in range(B):
+        assert (got[s, n[s]:] == 7.0).all()
+        for i in {0, 1, n[s] // 3, n[s] // 2, n[s] - 2, n[s] - 1} & set(range(n[s])):
+            for h, w in enumerate(windows):
+                at = pos[s] + i
+                p = np.arange(max(0, at + 1 - w), at + 1)
+                for g in range(h * G, (h + 1) * G):
+                    ref, tol = tolerance("bf16", qq[s, i, g], kk[s, h, p], vv[s, h, p], scale, at - p, cap,
+                                         float(slopes[g]) if biased else 0.0)
+                    assert (np.abs(got[s, i, g] - ref) <= tol).all(), (s, i, g, float((np.abs(got[s, i, g] - ref) / tol).max()))
+    # the chunk is appended: decoding the last token of each sequence gives the chunk's last row
+    if min(n) > 0:
+        last = torch.stack([q[s, n[s] - 1] for s in range(B)])
+        dec = np64(pool.decode(0, last, scale, tpos + tn, softcap=cap, slopes=slopes if biased else None))
+        for s in range(B):
+            np.testing.assert_allclose(dec[s], got[s, n[s] - 1], atol=2.0 ** -5, rtol=2.0 ** -6)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_captured_step(kind):
+    from head_budgeted_kv_gb300.graph import DecodeStepGraph
+    slopes = torch.tensor([2.0 ** -(i + 1) for i in range(8)], device="cuda")
+    results = []
+    for graph in (False, True):
+        gen = torch.Generator(device="cuda").manual_seed(8)
+
+        def randn(*shape):
+            return torch.randn(shape, generator=gen, device="cuda").bfloat16()
+
+        pool = hw.Pool(2, 2, 64, 16, [[64, 30], [200, 16]], 1, TYPES[kind], q_heads=8)
+        pos = torch.tensor([70], dtype=torch.int32, device="cuda")
+        for l in range(2):
+            pool.materialize(l, randn(1, 2, 70, 64), randn(1, 2, 70, 64), pos)
+        # the scored kernels load on their first call: make it before a capture
+        pool.decode(0, randn(1, 8, 64), 0.2, pos, softcap=10.0, slopes=slopes)
+        step = DecodeStepGraph(pool, 0.2, 8, pos, softcap=10.0, slopes=slopes, rope=hw.rope_table(64)) if graph else None
+        outs = []
+        for _ in range(4):
+            q, k, v = randn(2, 1, 8, 64), randn(2, 1, 2, 64), randn(2, 1, 2, 64)
+            if graph:
+                step.q.copy_(q), step.k_new.copy_(k), step.v_new.copy_(v)
+                step.replay()
+                outs.append(step.out.clone())
+            else:
+                one = []
+                for l in range(2):
+                    qr, kr = pool.rope(hw.rope_table(64), q[l], k[l], pos)
+                    one.append(pool.append_decode(l, qr, 0.2, kr, v[l], pos, softcap=10.0, slopes=slopes))
+                outs.append(torch.stack(one))
+                pos = pos + 1
+        results.append(torch.stack(outs))
+    assert torch.equal(results[0], results[1])
+
+
+def test_refusals():
+    pool = hw.Pool(1, 2, 64, 16, [[64, 200]], 1, torch.bfloat16, q_heads=4)
+    q = torch.zeros((1, 4, 64), device="cuda").bfloat16()
+    lens = torch.tensor([5], dtype=torch.int32, device="cuda")
+    ok = torch.zeros(4, device="cuda")
+    for bad in (ok[:3], ok.double(), torch.zeros(8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            pool.decode(0, q, 0.1, lens, slopes=bad)
+    for scale, cap in ((0.1, -1.0), (0.1, float("nan")), (0.1, float("inf")), (float("nan"), 5.0), (1e30, 1e-30), (1.0, 3e38)):
+        with pytest.raises(hw.HwkvError) as e:
+            pool.decode(0, q, scale, lens, softcap=cap)
+        assert e.value.status == hw.binding.HWKV_ERR_INVALID_ARG
+    chunk = torch.zeros((1, 1, 4, 64), device="cuda").bfloat16()
+    with pytest.raises(hw.HwkvError):
+        pool.prefill(0, chunk, 0.1, chunk[:, :, :2].contiguous(), chunk[:, :, :2].contiguous(), lens, lens, softcap=-1.0)

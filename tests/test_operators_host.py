@@ -109,3 +109,25 @@ def test_bad_rope_tables_are_refused(lib, args):
 def test_rope_needs_a_pool(lib):
     t = binding.hwkv_rope_table(64)
     assert lib.hwkv_rope(None, t, None, 4, None, 1, None, None, None, None, None) == binding.HWKV_ERR_INVALID_ARG
+
+
+def test_scored_calls_check_their_arguments(lib):
+    s = binding.Score(1.0, 0.0, None)
+    assert lib.hwkv_decode_attn_score(None, 0, None, 4, s, None, None, None, None, None, 0, 0, None) == binding.HWKV_ERR_INVALID_ARG
+    assert lib.hwkv_prefill_attn_score(None, 0, None, 4, s, None, None, 1, None, None, None, None, 0, None) == binding.HWKV_ERR_INVALID_ARG
+    with pytest.raises(ValueError):
+        binding.score(1.0, 0.0, torch.zeros(4), 5)
+
+
+def test_capped_exponential_form():
+    """The form the kernels use for tanh, in fp32 steps: below 2^-20 relative error over the range."""
+    u = np.concatenate([np.linspace(-12, 12, 40001), np.geomspace(1e-20, 0.25, 2000)]).astype(np.float32)
+    t = (u * u).astype(np.float32)
+    p = np.float32(62 / 2835) * t + np.float32(-17 / 315)
+    p = (p * t + np.float32(2 / 15)) * t + np.float32(-1 / 3)
+    p = (u * (p * t + np.float32(1))).astype(np.float32)
+    r = (np.float32(1) - np.float32(2) / (np.float32(1) + np.exp2(u * np.float32(2.8853900817779268)).astype(np.float32)))
+    got = np.where(np.abs(u) < 0.25, p, r).astype(np.float64)
+    want = np.tanh(u.astype(np.float64))
+    fine = want != 0
+    assert (np.abs(got - want)[fine] <= 2.0 ** -20 * np.abs(want)[fine]).all()

@@ -68,13 +68,21 @@ class Pool:
                  dtype: torch.dtype, q_heads: Optional[int] = None, device=None, stream=None):
         self.layers, self.kv_heads, self.head_dim = layers, kv_heads, head_dim
         self.block_size, self.num_seqs, self.dtype = block_size, num_seqs, dtype
-        self.io_dtype = torch.bfloat16 if dtype == torch.float8_e4m3fn else dtype
+        elem = (torch.float32, torch.bfloat16, torch.float8_e4m3fn)[binding._dtype_code(dtype)]
+        self.io_dtype = torch.bfloat16 if elem == torch.float8_e4m3fn else elem
         self.q_heads = q_heads or kv_heads
         self.nbytes = hwkv_pool_bytes(layers, kv_heads, head_dim, block_size, windows, num_seqs, dtype)
         device = torch.device(device or "cuda")
         self.buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
         self.handle = hwkv_pool_create(layers, kv_heads, head_dim, block_size, windows, num_seqs, dtype,
                                        self.buffer, stream)
+        _, total, block_bytes = hwkv_pool_geometry(self.handle)
+        self._blocks = self.buffer[:total * block_bytes].view(elem).view(total, 2, block_size, head_dim)
+        self._scales = None
+        if elem == torch.float8_e4m3fn:
+            groups = block_size // 16
+            area = self.buffer[total * block_bytes:total * block_bytes + total * groups * 8]
+            self._scales = area.view(torch.float32).view(total, groups, 2)
         self.workspace = None
         self.prefill_workspace = None
         self._size_workspace()
@@ -94,23 +102,18 @@ class Pool:
     def blocks(self) -> torch.Tensor:
         """View of the pool as [total_blocks][2][block_size][head_dim] elements (the codes of an
         8-bit pool)."""
-        _, total, block_bytes = self.geometry()
-        rows = self.buffer[:total * block_bytes].view(self.dtype)
-        return rows.view(total, 2, self.block_size, self.head_dim)
+        return self._blocks
 
     def scales(self) -> torch.Tensor:
         """View of an 8-bit pool's scales, fp32 [total_blocks][block_size / 16][2 (K, V)]: a value
         of ``blocks()`` stands for its code times the scale of its 16 slots."""
-        if self.dtype != torch.float8_e4m3fn:
+        if self._scales is None:
             raise ValueError("only an 8-bit pool has scales")
-        _, total, block_bytes = self.geometry()
-        groups = self.block_size // 16
-        area = self.buffer[total * block_bytes:total * block_bytes + total * groups * 8]
-        return area.view(torch.float32).view(total, groups, 2)
+        return self._scales
 
     def _check_io(self, *tensors):
         # an 8-bit pool does not share its element type with the tensors passed to it
-        if self.dtype == torch.float8_e4m3fn:
+        if self._scales is not None:
             for t in tensors:
                 if t is not None and t.dtype != torch.bfloat16:
                     raise ValueError(f"an 8-bit pool takes bf16 tensors (got {t.dtype})")
@@ -210,20 +213,24 @@ class Pool:
         None).  Inputs may be slices of a fused projection.  Outputs default to new tensors (zeros past
         n); pass q_out=q, k_out=k to work in place.  Returns (q_out, k_out)."""
         new = torch.empty if n is None else torch.zeros
-        for t, name in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out")):
-            if t is None:
-                continue
-            if t.dtype != self.io_dtype or t.shape[0] != self.num_seqs or t.shape[-1] != self.head_dim:
-                raise ValueError(f"{name} must hold {self.io_dtype} rows of head_dim {self.head_dim} for "
-                                 f"{self.num_seqs} sequences")
-        if k is not None and k.shape[-2] != self.kv_heads:
-            raise ValueError(f"k must hold {self.kv_heads} heads")
-        if q is not None and q_out is None:
-            q_out = new(q.shape, dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = new(k.shape, dtype=k.dtype, device=k.device)
+        if q is not None:
+            self._check_rows(q, "q")
+            if q_out is None:
+                q_out = new(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None:
+            if self._check_rows(k, "k") != self.kv_heads:
+                raise ValueError(f"k must hold {self.kv_heads} heads")
+            if k_out is None:
+                k_out = new(k.shape, dtype=k.dtype, device=k.device)
         hwkv_rope(self.handle, table, q, k, pos, n, q_out, k_out, stream)
         return q_out, k_out
+
+    def _check_rows(self, t, name) -> int:
+        shape = t.shape
+        if t.dtype != self.io_dtype or len(shape) < 3 or shape[0] != self.num_seqs or shape[-1] != self.head_dim:
+            raise ValueError(f"{name} must hold {self.io_dtype} rows of head_dim {self.head_dim} for "
+                             f"{self.num_seqs} sequences")
+        return shape[-2]
 
     def check_device_errors(self, stream=None) -> int:
         return hwkv_check_device_errors(self.handle, stream)

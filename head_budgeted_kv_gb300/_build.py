@@ -22,7 +22,7 @@ SOURCES = ("hwkv_host.cpp", "hwkv_copy.cu", "hwkv_copy_q8.cu", "hwkv_decode_simt
 HEADERS = (os.path.join(CSRC, "hwkv_internal.h"), os.path.join(CSRC, "hwkv_device.cuh"),
            os.path.join(CSRC, "hwkv_tcgen05.cuh"), os.path.join(CSRC, "hwkv_decode_tile.cuh"),
            os.path.join(CSRC, "hwkv_fp8.cuh"), os.path.join(CSRC, "hwkv_decode_tile_q8.cuh"),
-           os.path.join(CSRC, "hwkv_decode_sk.cuh"),
+           os.path.join(CSRC, "hwkv_decode_sk.cuh"), os.path.join(CSRC, "hwkv_decode_merge.cuh"),
            os.path.join(INCLUDE, "hwkv.h"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

@@ -1,23 +1,359 @@
-// The stream-K decode kernel (hwkv_decode_sk.cuh) for 8-bit pools (HWKV_E4M3).
-#include "hwkv_decode_sk.cuh"
+// Stream-K decode attention for 8-bit pools (HWKV_E4M3), optionally fused with the append of the
+// step's new token.
+//
+// "HeadWiseKV: Budgeted Per-Head Cache Residency for Hybrid Long-Context Language Models",
+// abstract and section "Grouped-Cache Runtime": attention reads only the materialised window
+// of each KV head (the last min(w, len) tokens), through the head's block table.
+//
+// The line of tiles, its split over the CTAs and the merges are those of hwkv_decode_sk.cuh; the
+// tile's mathematics is in hwkv_decode_tile_q8.cuh.  What differs is how tiles reach the warps: an
+// 8-bit tile holds half the bytes and costs as many instructions, so the per-tile work of finding
+// and issuing a tile (about a third of what a warp ran) goes to a producer warp:
+//   warp W      producer: 32 tiles of a segment per round, one per lane -- ring slot, table entry
+//               (the next round's read ahead), then the TMA copies of a stage's tiles by as many
+//               lanes, once the stage is free;
+//   warps 0-3   consumers: a stage holds M consecutive tiles of a segment (32 tokens at head_dim
+//               128, 64 at 64: 8 KB), stage n of the CTA goes to warp n % W.
+// Stages are handed over by mbarriers: full[] (bytes landed), empty[] (its consumer has read it).
+//
+// Bound: HBM.  Waits are bounded (~2 s); a timeout records HWKV_DEVERR_WAIT_TIMEOUT, all roles stop
+// and the copies in flight land before the shared memory is released.
+#include <atomic>
+
+#include "hwkv_decode_merge.cuh"
+#include "hwkv_decode_tile_q8.cuh"
 
 namespace hwkv {
 namespace {
 
 template <int D>
+struct Q8Cfg {
+  static constexpr int W = kWarps;                    // consumer warps
+  static constexpr int kThreads = (W + 1) * 32;
+  static constexpr int M = D == 128 ? 2 : 4;          // tiles of a stage
+  static constexpr int kTileBytes = 2 * kTile * D;    // K and V codes
+  static constexpr int kStageBytes = M * kTileBytes;  // 8 KB
+  static constexpr int NS = 12;                       // stages of a CTA
+  static constexpr int kCtas = 2;                     // CTAs per SM
+  using Sync = PartSync<W * 32>;
+};
+
+template <int D, int GP>
+constexpr int q8_smem_bytes() {
+  using Cfg = Q8Cfg<D>;
+  return Cfg::NS * Cfg::kStageBytes + Cfg::W * merge_heads<D, GP>() * D * 4 + 1024;
+}
+
+__device__ __forceinline__ void mbar_arrive_one(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// Waits for a phase; gives up when another role has (`abort`) or after ~2 s, which it records and
+// announces.
+__device__ __forceinline__ bool q8_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*abort) return false;
+      if (global_timer_ns() - t0 > 2000000000ull) {
+        *abort = 1;
+        atomicOr(err, HWKV_DEVERR_WAIT_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+template <int D, int GP, bool SC>
+__global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
+    decode_q8_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ DecodeArgs a) {
+  using Cfg = Q8Cfg<D>;
+  using Sync = typename Cfg::Sync;
+  using State = WarpState<E4m3, D, GP, SC>;
+  constexpr int W = Cfg::W, M = Cfg::M, NS = Cfg::NS;
+  constexpr int SG = merge_heads<D, GP>();
+  constexpr int kThreads = Cfg::kThreads;
+
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  float* sc_acc = reinterpret_cast<float*>(smem + NS * Cfg::kStageBytes);  // [W][SG][D]
+  __shared__ __align__(8) uint64_t full[NS], empty[NS];
+  __shared__ __align__(8) uint64_t merge_bar[2];  // bulk copies of partial blocks
+  __shared__ ScaleSlot s_scale[NS * M];
+  __shared__ float sc_m[W * SG], sc_l[W * SG];
+  __shared__ long long s_scan[W + 1];
+  __shared__ long long s_start[2];
+  __shared__ int s_last, s_abort;
+  __shared__ int s_lens_buf[kLensCache];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int H = a.pv.kv_heads;
+  const int B = a.pv.num_seqs;
+  const int ngroups = B * H;
+  const int nctas = gridDim.x, cta = blockIdx.x;
+  const int G = a.group;
+
+  // the next grid in the stream may start at once (see hwkv_decode_sk.cuh); with a.early the
+  // schedule and the loads run before the dependent-launch wait, all else after it
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) prefetch_tensormap(&tmap);
+  if (!a.early) griddep_wait();
+
+  if (cta == 0) {
+    for (int s = threadIdx.x; s < B; s += kThreads)
+      if (__ldcg(a.lens + s) + a.len_add < 0) atomicOr(a.pv.err, HWKV_DEVERR_NEG_LENGTH);
+  }
+  const int* s_lens = B <= kLensCache ? s_lens_buf : nullptr;
+  if (s_lens != nullptr) {
+    for (int s = threadIdx.x; s < B; s += kThreads) s_lens_buf[s] = seq_len(a, s);
+    __syncthreads();
+  }
+
+  // ---- schedule: needed tiles per group, their prefix sums, this CTA's range ----------
+  if (threadIdx.x == 0) {
+    s_start[0] = -1;
+    s_abort = 0;
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&merge_bar[0], 1);
+    mbar_init(&merge_bar[1], 1);
+    fence_mbar_init();
+  }
+  const int per = (ngroups + kThreads - 1) / kThreads;
+  const int g_lo = min(ngroups, (int)threadIdx.x * per), g_hi = min(ngroups, g_lo + per);
+  long long mine = 0;
+  for (int g = g_lo; g < g_hi; ++g) mine += group_span(load_group(a, s_lens, g));
+  long long T;
+  const long long excl = block_exclusive_scan<W + 1>(mine, s_scan, T);
+  const long long t_lo = range_start(T, cta, nctas), t_hi = range_start(T, cta + 1, nctas);
+  if (t_lo < t_hi && excl <= t_lo && t_lo < excl + mine) {
+    long long pre = excl;
+    for (int g = g_lo; g < g_hi; ++g) {
+      const int c = group_span(load_group(a, s_lens, g));
+      if (t_lo < pre + c) {
+        s_start[0] = g;
+        s_start[1] = pre;
+        break;
+      }
+      pre += c;
+    }
+  }
+  __syncthreads();
+  // the range holds a tile unless it lies within one group's gap
+  const bool has_range =
+      t_lo < t_hi && s_start[0] >= 0 && t_hi > (t_lo > s_start[1] + kGapTiles ? t_lo : s_start[1] + kGapTiles);
+  volatile int* abort = &s_abort;
+  // segment cursor: group, its boundary on the line
+  int sg = has_range ? (int)s_start[0] : 0;
+  long long spre = has_range ? s_start[1] : 0;
+  Group sgr = load_group(a, s_lens, sg);
+  // the segment's tiles of the group, [first, first + count); true when another segment follows
+  auto segment = [&](int& first, int& count) {
+    const long long lo = t_lo > spre + kGapTiles ? t_lo : spre + kGapTiles;
+    const long long hi = t_hi < spre + group_span(sgr) ? t_hi : spre + group_span(sgr);
+    first = (int)(lo - spre) - kGapTiles;
+    count = (int)(hi - lo);
+    return spre + group_span(sgr) + kGapTiles < t_hi;
+  };
+  auto next_segment = [&]() {
+    do {
+      spre += group_span(sgr);
+      sgr = load_group(a, s_lens, ++sg);
+    } while (sgr.tiles == 0);
+  };
+
+  if (warp == W) {
+    // ---- producer ----------------------------------------------------------------------
+    if (!has_range) return;
+    const uint64_t policy = evict_first_policy();
+    const uint32_t sbase = smem_addr(smem);
+    int stage = 0;  // stages issued
+    bool ok = true;
+    for (;;) {
+      int first, count;
+      const bool more = segment(first, count);
+      // a round's tiles: lane i's table entry and row in the block, read one round ahead
+      auto look = [&](int i, int& blk, int& r0) {
+        blk = 0;
+        r0 = 0;
+        if (i >= count) return;
+        const int t0 = tile_slot(sgr, first + i);
+        const int jb = a.bs_log2 >= 0 ? t0 >> a.bs_log2 : t0 / a.pv.block_size;
+        blk = __ldcg(sgr.tbl + jb);
+        r0 = t0 - jb * a.pv.block_size;
+      };
+      int blk, r0;
+      look(lane, blk, r0);
+      for (int i0 = 0; ok && i0 < count; i0 += 32) {
+        int blk_next, r0_next;
+        look(i0 + 32 + lane, blk_next, r0_next);
+        if (blk < 0 || (int64_t)blk >= a.pv.total_blocks) {
+          // flagged, and block 0 read, so the barrier accounting stays intact
+          atomicOr(a.pv.err, HWKV_DEVERR_BAD_BLOCK);
+          blk = 0;
+        }
+        const int n = min(32, count - i0);
+        for (int i = 0; i < n; i += M) {
+          const int st = stage % NS;
+          if (stage >= NS) ok = __all_sync(0xffffffffu, q8_wait(&empty[st], (uint32_t)(stage / NS - 1) & 1u, abort, a.pv.err));
+          if (!ok) break;
+          const int m = lane - i;  // this lane's tile of the stage
+          const bool mine_ = m >= 0 && m < M && lane < n;
+          if (mine_) s_scale[st * M + m].half = (int)(((int64_t)blk * (a.pv.block_size / kScaleGroup) + (r0 >> 4)) & 1);
+          __syncwarp();
+          if (m == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)min(M, n - i) * tile_load_bytes<D>());
+          __syncwarp();
+          if (mine_)
+            issue_tile_q8<D>(&tmap, a, blk, r0, sbase + st * Cfg::kStageBytes + m * Cfg::kTileBytes, &s_scale[st * M + m],
+                             &full[st], policy);
+          __syncwarp();
+          ++stage;
+        }
+        blk = blk_next;
+        r0 = r0_next;
+      }
+      if (!ok || !more) break;
+      next_segment();
+    }
+    if (!ok) {  // let the copies in flight land before the shared memory is released
+      for (int j = max(0, stage - NS); j < stage; ++j)
+        if (!mbar_wait_bounded(&full[j % NS], (uint32_t)(j / NS) & 1u)) break;
+    }
+    return;
+  }
+
+  // ---- consumers -------------------------------------------------------------------------
+  if (a.early) griddep_wait();
+  // groups with nothing resident (length 0) get a zero output, each from one CTA
+  for (int g = cta; g < ngroups; g += nctas) {
+    const Group gr = load_group(a, s_lens, g);
+    if (gr.tiles == 0) {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)gr.s * H + gr.h) * G * D;
+      for (int e = threadIdx.x; e < G * D; e += W * 32) store_out<__nv_bfloat16>(o + e, 0.f);
+    }
+  }
+  if (!has_range) return;
+
+  int stage0 = 0;  // the segment's first stage
+  bool ok = true;
+  MergeStage ms{nullptr, (uint32_t)(NS * Cfg::kStageBytes), &merge_bar[0], &merge_bar[1], 0u, 0u, -1, -1};
+  for (;;) {
+    int first, count;
+    const bool more = segment(first, count);
+    State ws;
+    ws.begin(a, sgr, G, lane);
+    const int new_slot = a.k_new != nullptr ? (sgr.len - 1) % sgr.rs.C : -1;
+    const int nstages = (count + M - 1) / M;
+    int k = warp - stage0 % W;
+    if (k < 0) k += W;
+    for (; ok && k < nstages; k += W) {
+      const int n = stage0 + k, st = n % NS;
+      ok = __all_sync(0xffffffffu, q8_wait(&full[st], (uint32_t)(n / NS) & 1u, abort, a.pv.err));
+      if (!ok) break;
+      const int have = min(M, count - k * M);
+      int t[M];
+      uint32_t sk[M];
+      const ScaleSlot* sl[M];
+      bool dirty = false;
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        t[m] = tile_slot(sgr, first + k * M + m);
+        sk[m] = smem_addr(smem) + st * Cfg::kStageBytes + m * Cfg::kTileBytes;
+        sl[m] = &s_scale[st * M + m];
+        if (m < have && new_slot >= t[m] && new_slot < t[m] + kTile) {
+          patch_new_row_q8<D>(a, sgr.tbl, sgr.s, sgr.h, sgr.len - 1, sgr.rs.C, t[m], new_slot, sk[m], &s_scale[st * M + m],
+                              lane);
+          dirty = true;
+        }
+      }
+      if (have == M) {
+        if (ws.template consume<M>(a, sgr, t, sk, sl, lane)) dirty = true;
+      } else {
+        for (int m = 0; m < have; ++m) {
+          const int t1[1] = {tile_slot(sgr, first + k * M + m)};
+          const uint32_t sk1[1] = {smem_addr(smem) + st * Cfg::kStageBytes + m * Cfg::kTileBytes};
+          const ScaleSlot* sl1[1] = {&s_scale[st * M + m]};
+          if (ws.template consume<1>(a, sgr, t1, sk1, sl1, lane)) dirty = true;
+        }
+      }
+      if (dirty) fence_proxy_async_smem();  // this lane's shared-memory writes before the next TMA
+      __syncwarp();
+      if (lane == 0) mbar_arrive_one(&empty[st]);
+    }
+    const long long seg_begin = spre + kGapTiles + first;
+    end_segment<__nv_bfloat16, D, GP, Sync>(a, ws, sgr, sg, spre, seg_begin, seg_begin + count, T, nctas, cta, more, !ok,
+                                            smem, sc_m, sc_l, sc_acc, &s_last, ms);
+    Sync::sync();  // the merge scratch is rewritten by the next segment
+    if (!more) break;
+    stage0 += nstages;
+    next_segment();
+  }
+  if (ms.stuck0 >= 0) mbar_wait_bounded(&merge_bar[0], (uint32_t)ms.stuck0);
+  if (ms.stuck1 >= 0) mbar_wait_bounded(&merge_bar[1], (uint32_t)ms.stuck1);
+}
+
+template <int D, int GP, bool SC>
+cudaError_t prepare_one() {
+  return cudaFuncSetAttribute(decode_q8_kernel<D, GP, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              q8_smem_bytes<D, GP>());
+}
+
+template <int D, int GP>
+cudaError_t configure_one(int* ctas_per_sm) {
+  const cudaError_t e = prepare_one<D, GP, false>();
+  if (e != cudaSuccess) return e;
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_q8_kernel<D, GP, false>, Q8Cfg<D>::kThreads,
+                                                       q8_smem_bytes<D, GP>());
+}
+
+// Scored instances (SC) are prepared at their first launch on a device, not with every pool, and
+// run on the grid of the plain ones.
+template <int D, int GP, bool SC>
+cudaError_t launch_one(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, cudaStream_t st) {
+  if constexpr (SC) {
+    static std::atomic<uint64_t> prepared{0};  // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (!(prepared.load(std::memory_order_relaxed) & bit)) {
+      if ((e = prepare_one<D, GP, SC>()) != cudaSuccess) return e;
+      prepared.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(Q8Cfg<D>::kThreads);
+  cfg.dynamicSmemBytes = q8_smem_bytes<D, GP>();
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_q8_kernel<D, GP, SC>, *tmap, a);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D>
 cudaError_t configure_dim(int ctas_per_sm[kGroupPads]) {
   cudaError_t e;
-  if ((e = configure_one<E4m3, D, 4>(&ctas_per_sm[0])) != cudaSuccess) return e;
-  if ((e = configure_one<E4m3, D, 8>(&ctas_per_sm[1])) != cudaSuccess) return e;
-  return configure_one<E4m3, D, 16>(&ctas_per_sm[2]);
+  if ((e = configure_one<D, 4>(&ctas_per_sm[0])) != cudaSuccess) return e;
+  if ((e = configure_one<D, 8>(&ctas_per_sm[1])) != cudaSuccess) return e;
+  return configure_one<D, 16>(&ctas_per_sm[2]);
 }
 
 template <int D, bool SC>
 cudaError_t launch_dim(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, cudaStream_t st) {
   switch (decode_tc_group_pad(a.group)) {
-    case 4: return launch_one<E4m3, D, 4, SC>(a, tmap, ctas, st);
-    case 8: return launch_one<E4m3, D, 8, SC>(a, tmap, ctas, st);
-    default: return launch_one<E4m3, D, 16, SC>(a, tmap, ctas, st);
+    case 4: return launch_one<D, 4, SC>(a, tmap, ctas, st);
+    case 8: return launch_one<D, 8, SC>(a, tmap, ctas, st);
+    default: return launch_one<D, 16, SC>(a, tmap, ctas, st);
   }
 }
 

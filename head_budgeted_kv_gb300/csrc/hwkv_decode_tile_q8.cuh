@@ -1,5 +1,5 @@
-// Tile-level pieces of the stream-K decode kernel (hwkv_decode_sk.cuh) for 8-bit pools
-// (HWKV_E4M3, hwkv_fp8.cuh): the loads of one 16-token tile with its two scales, the fused
+// Tile-level pieces of the stream-K decode kernel for 8-bit pools (hwkv_decode_q8.cu; HWKV_E4M3,
+// hwkv_fp8.cuh): the loads of one 16-token tile with its two scales, the fused
 // append, and one warp's work on a tile.
 //
 // With K = k_scale * Kc and V = v_scale * Vc for the codes Kc, Vc of a tile (one group of 16
@@ -9,8 +9,9 @@
 // Codes become fp16 exactly, one conversion instruction per two values, and feed
 // mma.sync.m16n8k16 fp16 -> fp32.  fp16's range is kept in three exact ways: each query head is
 // scaled by a power of two so its largest element lies in [2^14, 2^15) (the elements then lose
-// nothing above 2^-39 of that largest one); P carries a factor 2^15 that cancels in O / l, so a
-// weight keeps its 11 bits down to 2^-29 of the largest; and v_scale enters P relative to the
+// nothing above 2^-39 of that largest one); P carries a factor 2^11 that cancels in O / l (2^15
+// at most, as a maximum may lag by 2^4), so a weight keeps its 11 bits down to 2^-25 of the largest
+// and is off by at most 2^-36 of the largest below; and v_scale enters P relative to the
 // largest v_scale the warp has met, by which its accumulators are finally multiplied.
 // A dim or token index may be permuted freely inside a contraction: K's bytes are fed in the
 // order ldmatrix delivers them, against queries loaded in the same order, and V's columns come
@@ -35,27 +36,22 @@ __device__ __forceinline__ uint32_t swz_q8(int row, int b) {
 // Shared memory of one stage's scales: the 16-byte copy that holds them and which half they are.
 struct __align__(16) ScaleSlot {
   float pair[2][2];  // scales of two neighbouring groups: [group % 2][K, V]
-  int half;          // written by the issuing lane before it arrives on the stage's barrier
+  int half;          // written by the issuing warp before it arrives on the stage's barrier
   int pad[3];
 };
 
-// Issues the loads of one tile of an 8-bit pool: K and V rows in one box of the 3-D map
-// (head_dim, block_size rows, 2 * block + K/V), and the 16 bytes that hold the group's scales.
+// The loads of one tile whose table entry `blk` is in range, first row r0 of the block: K and V rows
+// in one box of the 3-D map (head_dim, block_size rows, 2 * block + K/V), and the 16 bytes that
+// hold the group's scales.  tile_load_bytes() arrive on the barrier.
 template <int D>
-__device__ __forceinline__ void issue_tile_q8(const CUtensorMap* tmap, const DecodeArgs& a, const Group& gr, int t0,
-                                              uint32_t dst, ScaleSlot* slot, uint64_t* bar, uint64_t policy,
-                                              bool through_l2) {
-  const int bs = a.pv.block_size;
-  const int jb = t0 / bs;
-  const int r0 = t0 - jb * bs;
-  int32_t blk = through_l2 ? __ldcg(gr.tbl + jb) : gr.tbl[jb];
-  if (blk < 0 || (int64_t)blk >= a.pv.total_blocks) {
-    atomicOr(a.pv.err, HWKV_DEVERR_BAD_BLOCK);
-    blk = 0;
-  }
-  const int64_t group = (int64_t)blk * (bs / kScaleGroup) + r0 / kScaleGroup;
-  slot->half = (int)(group & 1);
-  mbar_arrive_expect_tx(bar, 2 * kTile * D + 16);
+__host__ __device__ constexpr uint32_t tile_load_bytes() {
+  return 2 * kTile * D + 16;
+}
+
+template <int D>
+__device__ __forceinline__ void issue_tile_q8(const CUtensorMap* tmap, const DecodeArgs& a, int blk, int r0, uint32_t dst,
+                                              ScaleSlot* slot, uint64_t* bar, uint64_t policy) {
+  const int64_t group = (int64_t)blk * (a.pv.block_size / kScaleGroup) + (r0 >> 4);
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
@@ -65,24 +61,27 @@ __device__ __forceinline__ void issue_tile_q8(const CUtensorMap* tmap, const Dec
 }
 
 // Fused append: when the tile starting at slot t0 is the new token's group, the group is stored
-// anew with the new row (recode_group), in shared memory and in the pool, and `scale` (K, V) is
-// replaced.  No other CTA reads this tile, or its scales, in the launch.
+// anew with the new row (recode_group), in shared memory and in the pool, with its scales.  No
+// other CTA reads this tile, or its scales, in the launch.  A call of its own: it happens once per
+// group and would only fill the tile loop's registers and instruction cache.
 template <int D>
-__device__ __forceinline__ bool patch_new_row_q8(const DecodeArgs& a, const Group& gr, int t0, int new_slot,
-                                                 uint32_t sK, float (&scale)[2], int lane) {
-  if (new_slot < t0 || new_slot >= t0 + kTile) return false;
+__device__ __noinline__ void patch_new_row_q8(const DecodeArgs& a, const int32_t* tbl, int s, int h, int pos, int C,
+                                              int t0, int new_slot, uint32_t sK, ScaleSlot* slot, int lane) {
+  const int half = slot->half;
+  float scale[2] = {slot->pair[half][0], slot->pair[half][1]};
+  __syncwarp();
   const int bs = a.pv.block_size;
   const int jb = t0 / bs, r0 = t0 - jb * bs;
-  const int32_t blk = gr.tbl[jb];
+  const int32_t blk = tbl[jb];
   const bool blk_ok = blk >= 0 && (int64_t)blk < a.pv.total_blocks;
-  const int64_t src = ((int64_t)gr.s * a.pv.kv_heads + gr.h) * D;
-#pragma unroll
+  const int64_t src = ((int64_t)s * a.pv.kv_heads + h) * D;
+#pragma unroll 1
   for (int kv = 0; kv < 2; ++kv) {
     const uint32_t base = sK + kv * (kTile * D);
     uint8_t* dst = static_cast<uint8_t*>(a.pv.pool) + (((int64_t)(blk_ok ? blk : 0) * 2 + kv) * bs + r0) * D;
     scale[kv] = recode_group<D>(
-        static_cast<const __nv_bfloat16*>(kv ? a.v_new : a.k_new) + src, t0, new_slot, gr.len - 1, a.g.window[gr.h],
-        gr.rs.C, scale[kv],
+        static_cast<const __nv_bfloat16*>(kv ? a.v_new : a.k_new) + src, t0, new_slot, pos, a.g.window[h], C,
+        scale[kv],
         [&](int r, int c) {
           uint4 v;
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -98,12 +97,13 @@ __device__ __forceinline__ bool patch_new_row_q8(const DecodeArgs& a, const Grou
         },
         lane);
   }
-  if (lane == 0 && blk_ok) {
+  if (lane == 0) {
+    slot->pair[half][0] = scale[0];
+    slot->pair[half][1] = scale[1];
     const int64_t group = (int64_t)blk * (bs / kScaleGroup) + r0 / kScaleGroup;
-    *reinterpret_cast<float2*>(a.pv.scales + group * 2) = make_float2(scale[0], scale[1]);
+    if (blk_ok) *reinterpret_cast<float2*>(a.pv.scales + group * 2) = make_float2(scale[0], scale[1]);
   }
   __syncwarp();
-  return true;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -116,13 +116,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 template <int D, int GP, bool SC>
 struct WarpState<E4m3, D, GP, SC> {
   static constexpr int NT = (GP + 7) / 8;
-  static constexpr float kShift = 15.f;  // log2 of the factor P carries
+  static constexpr float kShift = 11.f;  // log2 of the factor P carries over the reference maximum
+  static constexpr float kSlack = 4.f;   // log2 of how far a score may pass it (P stays below 2^15)
   uint32_t qf[NT][D / 16][2];
   float acc[D / 16][NT][4];
-  float mx[NT][2], ls[NT][2];
+  float mx[NT][2], ls[NT][2];  // reference maximum (log2 units) and this lane's partial sums
+  float base[NT][2];           // what is subtracted from a score: mx - kShift
   float qs[NT][2];  // the power of two taken out of each of the lane's heads (times scale * log2(e) unless SC)
   float slope[NT][2];  // SC: of the lane's heads, log2 units
-  float vs;         // largest V scale met (0 at first)
+  float vs, vs_inv;  // largest V scale met (0 at first) and its inverse
 
   // Q of the group, normalised: the lane holds q[g][16i + 4*q4 .. + 3], g = 8*nt + lane / 4
   __device__ __forceinline__ void begin(const DecodeArgs& a, const Group& gr, int G, int lane) {
@@ -159,116 +161,160 @@ struct WarpState<E4m3, D, GP, SC> {
       for (int j = 0; j < D / 16; ++j) acc[j][nt][0] = acc[j][nt][1] = acc[j][nt][2] = acc[j][nt][3] = 0.f;
       mx[nt][0] = mx[nt][1] = kNegInf;
       ls[nt][0] = ls[nt][1] = 0.f;
+      base[nt][0] = base[nt][1] = -kShift;
     }
-    vs = 0.f;
+    vs = vs_inv = 0.f;
     if constexpr (SC) load_slopes<NT>(a, gr, G, lane, slope);
   }
 
-  __device__ __forceinline__ bool consume(const DecodeArgs& a, const Group& gr, int t0, int new_slot, uint32_t sK,
-                                          uint32_t sV, const ScaleSlot* slot, int lane) {
+  // M tiles at once: more work between the waits, one check of the maximum for all of them.
+  // `slot[m]` and `sK[m]` are tile m's scales and codes (V kTile * D bytes after K).  Returns true
+  // when shared memory was written (the caller fences before TMA refills the stages).
+  template <int M>
+  __device__ __forceinline__ bool consume(const DecodeArgs& a, const Group& gr, const int (&t0)[M],
+                                          const uint32_t (&sK)[M], const ScaleSlot* (&slot)[M], int lane) {
     const int mi = lane >> 3, rr = lane & 7;
     const int row = rr + ((mi & 1) << 3);  // ldmatrix: matrices 0, 1 are rows 0-7, 8-15 of one chunk,
     const int col = (mi >> 1) << 4;        // matrices 2, 3 those of the next chunk
     const int gq = lane >> 2;
-    const int half = slot->half;
-    float scale[2] = {slot->pair[half][0], slot->pair[half][1]};
-    bool dirty = patch_new_row_q8<D>(a, gr, t0, new_slot, sK, scale, lane);
+    bool dirty = false;
 
-    float sa[NT][4], sb[NT][4];
+    float s[M][NT][4];
+    float ks[M], vscale[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int half = slot[m]->half;
+      ks[m] = slot[m]->pair[half][0];
+      vscale[m] = slot[m]->pair[half][1];
+      float sb[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[m][nt][e] = sb[nt][e] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; i += 2) {
+        uint32_t w[4], a0[4], a1[4];
+        ldsm_x4(w, sK[m] + swz_q8<D>(row, 16 * i + col));
+        e4m3x4_to_f16(w[0], a0[0], a0[2]);
+        e4m3x4_to_f16(w[1], a0[1], a0[3]);
+        e4m3x4_to_f16(w[2], a1[0], a1[2]);
+        e4m3x4_to_f16(w[3], a1[1], a1[3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(s[m][nt], a0, qf[nt][i][0], qf[nt][i][1]);
+          mma_f16(sb[nt], a1, qf[nt][i + 1][0], qf[nt][i + 1][1]);
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[m][nt][e] = (s[m][nt][e] + sb[nt][e]) * (qs[nt][e & 1] * ks[m]);
+      if constexpr (SC) {
+        const float d0 = (float)slot_distance(gr.rs, t0[m] + gq), d1 = (float)slot_distance(gr.rs, t0[m] + gq + 8);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[m][nt][e] = scored_log2<false>(a.score, a.scale_log2, s[m][nt][e], slope[nt][e & 1], e < 2 ? d0 : d1);
+      }
+      // a tile with slots outside the window: their scores are masked, and their V rows zeroed, as
+      // 0 times a NaN is not 0
+      int first = t0[m] - gr.rs.first_slot;
+      if (first < 0) first += gr.rs.C;
+      if (first + kTile > gr.rs.n) {
+        const bool v0 = slot_valid(gr.rs, t0[m] + gq), v1 = slot_valid(gr.rs, t0[m] + gq + 8);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[m][nt][e] = (e < 2 ? v0 : v1) ? s[m][nt][e] : kNegInf;
+        const int r = lane >> 1;
+        if (!slot_valid(gr.rs, t0[m] + r)) {
+          for (int c = lane & 1; c < D / 16; c += 2)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sK[m] + kTile * D + swz_q8<D>(r, 16 * c)), "r"(0u)
+                         : "memory");
+        }
+        __syncwarp();
+        dirty = true;
+      }
+    }
+
+    // The reference maximum moves only when a score passes it by more than 2^kSlack (or a V scale
+    // the largest so far): seldom after a group's first tiles, so the common case reduces nothing
+    // over the warp and rescales nothing.
+    float vmax = vscale[0];
+#pragma unroll
+    for (int m = 1; m < M; ++m) vmax = fmaxf(vmax, vscale[m]);
+    float top[NT][2];
+    bool grow = vmax > vs;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sa[nt][e] = sb[nt][e] = 0.f;
+      for (int c = 0; c < 2; ++c) {
+        float x = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
 #pragma unroll
-    for (int i = 0; i < D / 16; i += 2) {
-      uint32_t w[4], a0[4], a1[4];
-      ldsm_x4(w, sK + swz_q8<D>(row, 16 * i + col));
-      e4m3x4_to_f16(w[0], a0[0], a0[2]);
-      e4m3x4_to_f16(w[1], a0[1], a0[3]);
-      e4m3x4_to_f16(w[2], a1[0], a1[2]);
-      e4m3x4_to_f16(w[3], a1[1], a1[3]);
+        for (int m = 1; m < M; ++m) x = fmaxf(x, fmaxf(s[m][nt][c], s[m][nt][c + 2]));
+        top[nt][c] = x;
+        grow = grow || x > mx[nt][c] + kSlack;
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+      const float vs_new = fmaxf(vs, vmax);
+      vs_inv = vs_new > 0.f ? pow2_inverse(vs_new) : 0.f;
+      const float keep = vs * vs_inv;
+      vs = vs_new;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float x = top[nt][c];
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+          const float n = fmaxf(mx[nt][c], x);
+          const float b = n == kNegInf ? 0.f : n;
+          const float al = ex2(mx[nt][c] - b);
+          mx[nt][c] = n;
+          base[nt][c] = b - kShift;
+          ls[nt][c] *= al;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            acc[j][nt][c] *= al * keep;
+            acc[j][nt][c + 2] *= al * keep;
+          }
+        }
+    }
+
+    uint32_t pb[M][NT][2];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const float part = vscale[m] * vs_inv;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        mma_f16(sa[nt], a0, qf[nt][i][0], qf[nt][i][1]);
-        mma_f16(sb[nt], a1, qf[nt][i + 1][0], qf[nt][i + 1][1]);
+        const float p0 = ex2(s[m][nt][0] - base[nt][0]), p1 = ex2(s[m][nt][1] - base[nt][1]);
+        const float p2 = ex2(s[m][nt][2] - base[nt][0]), p3 = ex2(s[m][nt][3] - base[nt][1]);
+        ls[nt][0] += p0 + p2;
+        ls[nt][1] += p1 + p3;
+        pb[m][nt][0] = movmatrix_trans(pack_f16(p0 * part, p1 * part));
+        pb[m][nt][1] = movmatrix_trans(pack_f16(p2 * part, p3 * part));
       }
     }
 
-    // V scale: accumulators and P are in units of the largest one so far
-    const float vs_new = fmaxf(vs, scale[1]);
-    const float vs_inv = vs_new > 0.f ? pow2_inverse(vs_new) : 0.f;
-    const float keep = vs * vs_inv, part = scale[1] * vs_inv;
-    vs = vs_new;
-
-    const bool v0 = slot_valid(gr.rs, t0 + gq), v1 = slot_valid(gr.rs, t0 + gq + 8);
-    float al[NT][2];
-    uint32_t pb[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float f0 = qs[nt][0] * scale[0], f1 = qs[nt][1] * scale[0];
-      float t[4] = {(sa[nt][0] + sb[nt][0]) * f0, (sa[nt][1] + sb[nt][1]) * f1, (sa[nt][2] + sb[nt][2]) * f0,
-                    (sa[nt][3] + sb[nt][3]) * f1};
-      if constexpr (SC) {
-        const float d0 = (float)slot_distance(gr.rs, t0 + gq), d1 = (float)slot_distance(gr.rs, t0 + gq + 8);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          t[e] = scored_log2<false>(a.score, a.scale_log2, t[e], slope[nt][e & 1], e < 2 ? d0 : d1);
-      }
-      const float s0 = v0 ? t[0] : kNegInf, s1 = v0 ? t[1] : kNegInf;
-      const float s2 = v1 ? t[2] : kNegInf, s3 = v1 ? t[3] : kNegInf;
-      float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
-      }
-      const float n0 = fmaxf(mx[nt][0], mx0), n1 = fmaxf(mx[nt][1], mx1);
-      const float b0 = n0 == kNegInf ? 0.f : n0, b1 = n1 == kNegInf ? 0.f : n1;
-      al[nt][0] = ex2(mx[nt][0] - b0);
-      al[nt][1] = ex2(mx[nt][1] - b1);
-      const float p0 = ex2(s0 - b0 + kShift), p1 = ex2(s1 - b1 + kShift);
-      const float p2 = ex2(s2 - b0 + kShift), p3 = ex2(s3 - b1 + kShift);
-      ls[nt][0] = fmaf(ls[nt][0], al[nt][0], p0 + p2);
-      ls[nt][1] = fmaf(ls[nt][1], al[nt][1], p1 + p3);
-      mx[nt][0] = n0;
-      mx[nt][1] = n1;
-      pb[nt][0] = movmatrix_trans(pack_f16(p0 * part, p1 * part));
-      pb[nt][1] = movmatrix_trans(pack_f16(p2 * part, p3 * part));
-      al[nt][0] *= keep;
-      al[nt][1] *= keep;
-    }
-
-    // V rows of slots outside the window are zeroed: their P is 0, but 0 times a NaN is not
-    if (!__all_sync(0xffffffffu, v0 && v1)) {
-      const int r = lane >> 1;
-      if (!slot_valid(gr.rs, t0 + r)) {
-#pragma unroll
-        for (int c = lane & 1; c < D / 16; c += 2)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sV + swz_q8<D>(r, 16 * c)), "r"(0u) : "memory");
-      }
-      __syncwarp();
-      dirty = true;
-    }
 #pragma unroll
     for (int j = 0; j < D / 16; j += 2) {
-      uint32_t w[4], a0[4], a1[4];
-      ldsm_x4_trans(w, sV + swz_q8<D>(row, 16 * j + col));
-      // bytes of a register: (token 2 q4, dims 2 gq, 2 gq + 1), (token 2 q4 + 1, the same dims)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = __byte_perm(w[e], 0u, 0x3120);
-      e4m3x4_to_f16(w[0], a0[0], a0[1]);
-      e4m3x4_to_f16(w[1], a0[2], a0[3]);
-      e4m3x4_to_f16(w[2], a1[0], a1[1]);
-      e4m3x4_to_f16(w[3], a1[2], a1[3]);
+      for (int m = 0; m < M; ++m) {
+        uint32_t w[4], a0[4], a1[4];
+        ldsm_x4_trans(w, sK[m] + kTile * D + swz_q8<D>(row, 16 * j + col));
+        // bytes of a register: (token 2 q4, dims 2 gq, 2 gq + 1), (token 2 q4 + 1, the same dims)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+        for (int e = 0; e < 4; ++e) w[e] = __byte_perm(w[e], 0u, 0x3120);
+        e4m3x4_to_f16(w[0], a0[0], a0[1]);
+        e4m3x4_to_f16(w[1], a0[2], a0[3]);
+        e4m3x4_to_f16(w[2], a1[0], a1[1]);
+        e4m3x4_to_f16(w[3], a1[2], a1[3]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          acc[j][nt][e] *= al[nt][e & 1];
-          acc[j + 1][nt][e] *= al[nt][e & 1];
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(acc[j][nt], a0, pb[m][nt][0], pb[m][nt][1]);
+          mma_f16(acc[j + 1][nt], a1, pb[m][nt][0], pb[m][nt][1]);
         }
-        mma_f16(acc[j][nt], a0, pb[nt][0], pb[nt][1]);
-        mma_f16(acc[j + 1][nt], a1, pb[nt][0], pb[nt][1]);
       }
     }
     return dirty;

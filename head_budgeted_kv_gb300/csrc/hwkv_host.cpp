@@ -165,6 +165,13 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
+// log2(x), or -1 when x is not a power of two
+int log2_of(int x) {
+  for (int b = 0; b < 31; ++b)
+    if ((1 << b) == x) return b;
+  return -1;
+}
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
@@ -1023,6 +1030,7 @@ int decode_common(hwkv_pool_t p, int layer, const void* q, int q_heads, hwkv_sco
   }
   a.scale_log2 = score.scale * 1.4426950408889634f;
   a.score = sa;
+  a.bs_log2 = log2_of(g.block_size);
   a.group = G;
   a.split_tokens = lp.split;
   std::memcpy(a.chunk_prefix, lp.chunk_prefix, sizeof a.chunk_prefix);
@@ -1210,9 +1218,7 @@ int hwkv_prefill_attn_score(hwkv_pool_t p, int layer, const void* q, int q_heads
   }
   a.scale_log2 = score->scale * 1.4426950408889634f;
   a.score = sa;
-  a.bs_log2 = -1;
-  for (int b = 0; b < 31; ++b)
-    if ((1 << b) == g.block_size) a.bs_log2 = b;
+  a.bs_log2 = log2_of(g.block_size);
   a.stage_tb = p->stage_tb;
   int max_c = 0;
   for (int h = 0; h < g.kv_heads; ++h) max_c = std::max(max_c, a.g.nblk_prefix[h + 1] - a.g.nblk_prefix[h]);

@@ -80,6 +80,7 @@ struct DecodeArgs {
   float scale_log2;        // scale * log2(e)
   ScoreArgs score;         // capped or distance-biased scores (scored instances only)
   int32_t group;           // G = Hq / H
+  int32_t bs_log2;         // log2(block_size), or -1 when it is not a power of two
   int32_t split_tokens;    // CUDA-core kernel: tokens per split-K chunk (power of two)
   int32_t chunk_prefix[kMaxKvHeads + 1];  // CUDA-core kernel: prefix over heads of ceil(C_h / split)
 };

@@ -41,7 +41,11 @@ struct PartSync {
   static __device__ __forceinline__ bool sync_or(bool p) { return !sync_and(!p); }
 };
 
-__device__ __forceinline__ int group_span(const Group& gr) { return gr.tiles > 0 ? gr.tiles + kGapTiles : 0; }
+// line positions of a group whose boundary is charged Gap of them
+template <int Gap = kGapTiles>
+__device__ __forceinline__ int group_span(const Group& gr) {
+  return gr.tiles > 0 ? gr.tiles + Gap : 0;
+}
 
 // Writes a merged (M, L, acc) of query head q, columns 4*d4 .. 4*d4 + 3: normalised to the
 // output `out_grp` (bf16 or fp32) when it is non-null, else unnormalised to partial slot `dst_slot`.
@@ -372,7 +376,7 @@ __host__ __device__ constexpr int merge_heads() {
 // sc_acc) into the group's output, or into this CTA's partial, which the group's last arriver
 // merges with the others.  `more`: the CTA has another segment; `failed`: this thread's warp gave
 // up a wait.  smem: the stage buffers, free after the last segment.
-template <typename Out, int D, int GP, typename Sync, typename State>
+template <typename Out, int D, int GP, typename Sync, int Gap, typename State>
 __device__ __forceinline__ void end_segment(const DecodeArgs& a, State& ws, const Group& sgr, int sg, long long spre,
                                             long long seg_begin, long long seg_end, long long T, int nctas, int cta,
                                             bool more, bool failed, uint8_t* smem, float* sc_m, float* sc_l,
@@ -388,7 +392,7 @@ __device__ __forceinline__ void end_segment(const DecodeArgs& a, State& ws, cons
   const int Hq = a.pv.kv_heads * G;
   Out* const out = static_cast<Out*>(a.out);
   ws.finish();
-  const bool whole = seg_begin == spre + kGapTiles && seg_end == spre + group_span(sgr);
+  const bool whole = seg_begin == spre + Gap && seg_end == spre + group_span<Gap>(sgr);
   const long long slot = (long long)sg + cta;  // unique per (group, CTA) along the line
   // pass (nt, hh): the warps' states of query heads [8*nt + hh*SG, 8*nt + (hh+1)*SG) meet in
   // shared memory and are folded into the output or this CTA's partial
@@ -437,7 +441,7 @@ __device__ __forceinline__ void end_segment(const DecodeArgs& a, State& ws, cons
     // After the last segment no copy is in flight (unless a wait timed out): merges may
     // stage partial blocks in the stage buffers.
     if (!more) ms.buf = Sync::sync_or(failed) ? nullptr : reinterpret_cast<float*>(smem);
-    const int c_lo = cta_of(spre + kGapTiles, T, nctas), c_hi = cta_of(spre + group_span(sgr) - 1, T, nctas);
+    const int c_lo = cta_of(spre + Gap, T, nctas), c_hi = cta_of(spre + group_span<Gap>(sgr) - 1, T, nctas);
     const bool all_live = T >= nctas;  // then no CTA range is empty
     const int k = c_hi - c_lo + 1;
     Out* const out_grp = out + ((int64_t)sgr.s * Hq + sgr.h * G) * D;

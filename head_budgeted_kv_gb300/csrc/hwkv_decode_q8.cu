@@ -7,11 +7,11 @@
 //
 // The line of tiles, its split over the CTAs and the merges are those of hwkv_decode_sk.cuh; the
 // tile's mathematics is in hwkv_decode_tile_q8.cuh.  What differs is how tiles reach the warps: an
-// 8-bit tile holds half the bytes and costs as many instructions, so the per-tile work of finding
-// and issuing a tile (about a third of what a warp ran) goes to a producer warp:
+// 8-bit tile holds half the bytes, so what it costs to find and issue one weighs twice as much, and
+// goes to a producer warp (a policy layer of four sequences at 112K: 83 -> 62 us):
 //   warp W      producer: 32 tiles of a segment per round, one per lane -- ring slot, table entry
-//               (the next round's read ahead), then the TMA copies of a stage's tiles by as many
-//               lanes, once the stage is free;
+//               (read two rounds ahead), scales (one round ahead) -- then, stage by stage once it is
+//               free, the scales stored by their lanes and the TMA copies issued by one;
 //   warps 0-3   consumers: a stage holds M consecutive tiles of a segment (32 tokens at head_dim
 //               128, 64 at 64: 8 KB), stage n of the CTA goes to warp n % W.
 // Stages are handed over by mbarriers: full[] (bytes landed), empty[] (its consumer has read it).
@@ -26,9 +26,16 @@
 namespace hwkv {
 namespace {
 
+// Line positions charged for a group's boundary (see kGapTiles): twice those of bf16, as a position
+// stands for half the bytes (policy layer / 64 ragged sequences at head_dim 64, 24 -> 48: 57.4 -> 56.7
+// / 60.5 -> 55.4 us; 64: 56.9 / 58.0).
+constexpr int kGap = 2 * kGapTiles;
+
 template <int D>
 struct Q8Cfg {
-  static constexpr int W = kWarps;                    // consumer warps
+  // 3 consumers and the producer: with two CTAs per SM a warp may then hold 255 registers and none
+  // spills (4 or 5 consumers: 168, with spills, and slower: policy layer 58.6 -> 62.1 and 59.7 us)
+  static constexpr int W = 3;
   static constexpr int kThreads = (W + 1) * 32;
   static constexpr int M = D == 128 ? 2 : 4;          // tiles of a stage
   static constexpr int kTileBytes = 2 * kTile * D;    // K and V codes
@@ -36,6 +43,10 @@ struct Q8Cfg {
   static constexpr int NS = 12;                       // stages of a CTA
   static constexpr int kCtas = 2;                     // CTAs per SM
   using Sync = PartSync<W * 32>;
+  // A buffer's stages must all go to one warp: it has then seen a buffer's use k before it waits for
+  // use k + 1.  Another warp could wait while use k is still landing, and a wait for a phase parity
+  // cannot tell use k - 1 from use k + 1.
+  static_assert(NS % W == 0, "a stage buffer belongs to one consumer warp");
 };
 
 template <int D, int GP>
@@ -81,7 +92,11 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
   float* sc_acc = reinterpret_cast<float*>(smem + NS * Cfg::kStageBytes);  // [W][SG][D]
   __shared__ __align__(8) uint64_t full[NS], empty[NS];
   __shared__ __align__(8) uint64_t merge_bar[2];  // bulk copies of partial blocks
-  __shared__ ScaleSlot s_scale[NS * M];
+  // scales (K, V) of each stage's tiles.  A round of 32 tiles stores its scales before its stages are
+  // free: at most 32 / M stages ahead of one whose buffer, NS stages back, has been read.
+  constexpr int kRing = 32;
+  static_assert(kRing >= 32 / M + NS, "scales of stages still being read stay");
+  __shared__ float2 s_scale[kRing][M];
   __shared__ float sc_m[W * SG], sc_l[W * SG];
   __shared__ long long s_scan[W + 1];
   __shared__ long long s_start[2];
@@ -126,14 +141,14 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
   const int per = (ngroups + kThreads - 1) / kThreads;
   const int g_lo = min(ngroups, (int)threadIdx.x * per), g_hi = min(ngroups, g_lo + per);
   long long mine = 0;
-  for (int g = g_lo; g < g_hi; ++g) mine += group_span(load_group(a, s_lens, g));
+  for (int g = g_lo; g < g_hi; ++g) mine += group_span<kGap>(load_group(a, s_lens, g));
   long long T;
   const long long excl = block_exclusive_scan<W + 1>(mine, s_scan, T);
   const long long t_lo = range_start(T, cta, nctas), t_hi = range_start(T, cta + 1, nctas);
   if (t_lo < t_hi && excl <= t_lo && t_lo < excl + mine) {
     long long pre = excl;
     for (int g = g_lo; g < g_hi; ++g) {
-      const int c = group_span(load_group(a, s_lens, g));
+      const int c = group_span<kGap>(load_group(a, s_lens, g));
       if (t_lo < pre + c) {
         s_start[0] = g;
         s_start[1] = pre;
@@ -145,7 +160,7 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
   __syncthreads();
   // the range holds a tile unless it lies within one group's gap
   const bool has_range =
-      t_lo < t_hi && s_start[0] >= 0 && t_hi > (t_lo > s_start[1] + kGapTiles ? t_lo : s_start[1] + kGapTiles);
+      t_lo < t_hi && s_start[0] >= 0 && t_hi > (t_lo > s_start[1] + kGap ? t_lo : s_start[1] + kGap);
   volatile int* abort = &s_abort;
   // segment cursor: group, its boundary on the line
   int sg = has_range ? (int)s_start[0] : 0;
@@ -153,15 +168,15 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
   Group sgr = load_group(a, s_lens, sg);
   // the segment's tiles of the group, [first, first + count); true when another segment follows
   auto segment = [&](int& first, int& count) {
-    const long long lo = t_lo > spre + kGapTiles ? t_lo : spre + kGapTiles;
-    const long long hi = t_hi < spre + group_span(sgr) ? t_hi : spre + group_span(sgr);
-    first = (int)(lo - spre) - kGapTiles;
+    const long long lo = t_lo > spre + kGap ? t_lo : spre + kGap;
+    const long long hi = t_hi < spre + group_span<kGap>(sgr) ? t_hi : spre + group_span<kGap>(sgr);
+    first = (int)(lo - spre) - kGap;
     count = (int)(hi - lo);
-    return spre + group_span(sgr) + kGapTiles < t_hi;
+    return spre + group_span<kGap>(sgr) + kGap < t_hi;
   };
   auto next_segment = [&]() {
     do {
-      spre += group_span(sgr);
+      spre += group_span<kGap>(sgr);
       sgr = load_group(a, s_lens, ++sg);
     } while (sgr.tiles == 0);
   };
@@ -173,48 +188,66 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
     const uint32_t sbase = smem_addr(smem);
     int stage = 0;  // stages issued
     bool ok = true;
+    struct Look {  // one lane's tile of a round
+      int blk, r0;
+    };
     for (;;) {
       int first, count;
       const bool more = segment(first, count);
-      // a round's tiles: lane i's table entry and row in the block, read one round ahead
-      auto look = [&](int i, int& blk, int& r0) {
-        blk = 0;
-        r0 = 0;
-        if (i >= count) return;
-        const int t0 = tile_slot(sgr, first + i);
-        const int jb = a.bs_log2 >= 0 ? t0 >> a.bs_log2 : t0 / a.pv.block_size;
-        blk = __ldcg(sgr.tbl + jb);
-        r0 = t0 - jb * a.pv.block_size;
+      auto look = [&](int i) {
+        Look l{0, 0};
+        if (i < count) {
+          const int t0 = tile_slot(sgr, first + i);
+          const int jb = a.bs_log2 >= 0 ? t0 >> a.bs_log2 : t0 / a.pv.block_size;
+          l.blk = __ldcg(sgr.tbl + jb);
+          l.r0 = t0 - jb * a.pv.block_size;
+        }
+        return l;
       };
-      int blk, r0;
-      look(lane, blk, r0);
-      for (int i0 = 0; ok && i0 < count; i0 += 32) {
-        int blk_next, r0_next;
-        look(i0 + 32 + lane, blk_next, r0_next);
-        if (blk < 0 || (int64_t)blk >= a.pv.total_blocks) {
-          // flagged, and block 0 read, so the barrier accounting stays intact
+      auto checked = [&](Look l) {  // a bad entry is flagged and block 0 read, so the barriers stay in step
+        if (l.blk < 0 || (int64_t)l.blk >= a.pv.total_blocks) {
           atomicOr(a.pv.err, HWKV_DEVERR_BAD_BLOCK);
-          blk = 0;
+          l.blk = 0;
         }
+        return l;
+      };
+      auto scales = [&](Look l) {
+        const int64_t group = (int64_t)l.blk * (a.pv.block_size / kScaleGroup) + (l.r0 >> 4);
+        return __ldcg(reinterpret_cast<const float2*>(a.pv.scales) + group);
+      };
+      // One round: the tiles [i0, i0 + 32) in `now`, their scales in `sc`, whose loads were issued a
+      // round ago; `next` (two rounds ago) gives the next round's scales, and `after` is looked up.
+      // Rounds rotate three register sets by name: a copy between sets would wait for the loads.
+      auto round = [&](int i0, const Look& now, const float2& sc, Look& next, float2& sc_next, Look& after) {
+        after = look(i0 + 64 + lane);
+        next = checked(next);
+        sc_next = scales(next);
         const int n = min(32, count - i0);
-        for (int i = 0; i < n; i += M) {
+        if (lane < n) s_scale[(stage + lane / M) % kRing][lane % M] = sc;
+        __syncwarp();
+        for (int i = 0; i < n; i += M, ++stage) {
           const int st = stage % NS;
-          if (stage >= NS) ok = __all_sync(0xffffffffu, q8_wait(&empty[st], (uint32_t)(stage / NS - 1) & 1u, abort, a.pv.err));
-          if (!ok) break;
-          const int m = lane - i;  // this lane's tile of the stage
-          const bool mine_ = m >= 0 && m < M && lane < n;
-          if (mine_) s_scale[st * M + m].half = (int)(((int64_t)blk * (a.pv.block_size / kScaleGroup) + (r0 >> 4)) & 1);
-          __syncwarp();
-          if (m == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)min(M, n - i) * tile_load_bytes<D>());
-          __syncwarp();
-          if (mine_)
-            issue_tile_q8<D>(&tmap, a, blk, r0, sbase + st * Cfg::kStageBytes + m * Cfg::kTileBytes, &s_scale[st * M + m],
-                             &full[st], policy);
-          __syncwarp();
-          ++stage;
+          if (stage >= NS) {
+            ok = __all_sync(0xffffffffu, q8_wait(&empty[st], (uint32_t)(stage / NS - 1) & 1u, abort, a.pv.err));
+            if (!ok) return;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)min(M, n - i) * Cfg::kTileBytes);
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            const int blk = __shfl_sync(0xffffffffu, now.blk, i + m), r0 = __shfl_sync(0xffffffffu, now.r0, i + m);
+            if (lane == 0 && i + m < n)
+              issue_tile_q8<D>(&tmap, blk, r0, sbase + st * Cfg::kStageBytes + m * Cfg::kTileBytes, &full[st], policy);
+          }
         }
-        blk = blk_next;
-        r0 = r0_next;
+      };
+      Look la = checked(look(lane)), lb = look(32 + lane), lc{0, 0};
+      float2 sa = scales(la), sb, sc;
+      for (int i0 = 0; ok && i0 < count; i0 += 96) {
+        round(i0, la, sa, lb, sb, lc);
+        if (!ok || i0 + 32 >= count) break;
+        round(i0 + 32, lb, sb, lc, sc, la);
+        if (!ok || i0 + 64 >= count) break;
+        round(i0 + 64, lc, sc, la, sa, lb);
       }
       if (!ok || !more) break;
       next_segment();
@@ -257,15 +290,15 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
       const int have = min(M, count - k * M);
       int t[M];
       uint32_t sk[M];
-      const ScaleSlot* sl[M];
+      const float2* sl[M];
       bool dirty = false;
 #pragma unroll
       for (int m = 0; m < M; ++m) {
         t[m] = tile_slot(sgr, first + k * M + m);
         sk[m] = smem_addr(smem) + st * Cfg::kStageBytes + m * Cfg::kTileBytes;
-        sl[m] = &s_scale[st * M + m];
+        sl[m] = &s_scale[n % kRing][m];
         if (m < have && new_slot >= t[m] && new_slot < t[m] + kTile) {
-          patch_new_row_q8<D>(a, sgr.tbl, sgr.s, sgr.h, sgr.len - 1, sgr.rs.C, t[m], new_slot, sk[m], &s_scale[st * M + m],
+          patch_new_row_q8<D>(a, sgr.tbl, sgr.s, sgr.h, sgr.len - 1, sgr.rs.C, t[m], new_slot, sk[m], &s_scale[n % kRing][m],
                               lane);
           dirty = true;
         }
@@ -276,7 +309,7 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
         for (int m = 0; m < have; ++m) {
           const int t1[1] = {tile_slot(sgr, first + k * M + m)};
           const uint32_t sk1[1] = {smem_addr(smem) + st * Cfg::kStageBytes + m * Cfg::kTileBytes};
-          const ScaleSlot* sl1[1] = {&s_scale[st * M + m]};
+          const float2* sl1[1] = {&s_scale[n % kRing][m]};
           if (ws.template consume<1>(a, sgr, t1, sk1, sl1, lane)) dirty = true;
         }
       }
@@ -284,8 +317,8 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
       __syncwarp();
       if (lane == 0) mbar_arrive_one(&empty[st]);
     }
-    const long long seg_begin = spre + kGapTiles + first;
-    end_segment<__nv_bfloat16, D, GP, Sync>(a, ws, sgr, sg, spre, seg_begin, seg_begin + count, T, nctas, cta, more, !ok,
+    const long long seg_begin = spre + kGap + first;
+    end_segment<__nv_bfloat16, D, GP, Sync, kGap>(a, ws, sgr, sg, spre, seg_begin, seg_begin + count, T, nctas, cta, more, !ok,
                                             smem, sc_m, sc_l, sc_acc, &s_last, ms);
     Sync::sync();  // the merge scratch is rewritten by the next segment
     if (!more) break;

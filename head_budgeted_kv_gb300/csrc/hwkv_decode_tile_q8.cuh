@@ -33,31 +33,16 @@ __device__ __forceinline__ uint32_t swz_q8(int row, int b) {
   else return (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4) + (b & 15));
 }
 
-// Shared memory of one stage's scales: the 16-byte copy that holds them and which half they are.
-struct __align__(16) ScaleSlot {
-  float pair[2][2];  // scales of two neighbouring groups: [group % 2][K, V]
-  int half;          // written by the issuing warp before it arrives on the stage's barrier
-  int pad[3];
-};
-
-// The loads of one tile whose table entry `blk` is in range, first row r0 of the block: K and V rows
-// in one box of the 3-D map (head_dim, block_size rows, 2 * block + K/V), and the 16 bytes that
-// hold the group's scales.  tile_load_bytes() arrive on the barrier.
+// The copy of one tile whose table entry `blk` is in range, first row r0 of the block: K and V rows
+// in one box of the 3-D map (head_dim, block_size rows, 2 * block + K/V).
 template <int D>
-__host__ __device__ constexpr uint32_t tile_load_bytes() {
-  return 2 * kTile * D + 16;
-}
-
-template <int D>
-__device__ __forceinline__ void issue_tile_q8(const CUtensorMap* tmap, const DecodeArgs& a, int blk, int r0, uint32_t dst,
-                                              ScaleSlot* slot, uint64_t* bar, uint64_t policy) {
-  const int64_t group = (int64_t)blk * (a.pv.block_size / kScaleGroup) + (r0 >> 4);
+__device__ __forceinline__ void issue_tile_q8(const CUtensorMap* tmap, int blk, int r0, uint32_t dst, uint64_t* bar,
+                                              uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(r0), "r"(2 * blk), "r"(smem_addr(bar)), "l"(policy)
       : "memory");
-  bulk_load(smem_addr(slot->pair), a.pv.scales + (group & ~(int64_t)1) * 2, 16, bar);
 }
 
 // Fused append: when the tile starting at slot t0 is the new token's group, the group is stored
@@ -66,9 +51,8 @@ __device__ __forceinline__ void issue_tile_q8(const CUtensorMap* tmap, const Dec
 // group and would only fill the tile loop's registers and instruction cache.
 template <int D>
 __device__ __noinline__ void patch_new_row_q8(const DecodeArgs& a, const int32_t* tbl, int s, int h, int pos, int C,
-                                              int t0, int new_slot, uint32_t sK, ScaleSlot* slot, int lane) {
-  const int half = slot->half;
-  float scale[2] = {slot->pair[half][0], slot->pair[half][1]};
+                                              int t0, int new_slot, uint32_t sK, float2* slot, int lane) {
+  float scale[2] = {slot->x, slot->y};
   __syncwarp();
   const int bs = a.pv.block_size;
   const int jb = t0 / bs, r0 = t0 - jb * bs;
@@ -98,8 +82,7 @@ __device__ __noinline__ void patch_new_row_q8(const DecodeArgs& a, const int32_t
         lane);
   }
   if (lane == 0) {
-    slot->pair[half][0] = scale[0];
-    slot->pair[half][1] = scale[1];
+    *slot = make_float2(scale[0], scale[1]);
     const int64_t group = (int64_t)blk * (bs / kScaleGroup) + r0 / kScaleGroup;
     if (blk_ok) *reinterpret_cast<float2*>(a.pv.scales + group * 2) = make_float2(scale[0], scale[1]);
   }
@@ -120,9 +103,10 @@ struct WarpState<E4m3, D, GP, SC> {
   static constexpr float kSlack = 4.f;   // log2 of how far a score may pass it (P stays below 2^15)
   uint32_t qf[NT][D / 16][2];
   float acc[D / 16][NT][4];
-  float mx[NT][2], ls[NT][2];  // reference maximum (log2 units) and this lane's partial sums
+  float mx[NT][2];   // reference maximum (log2 units)
+  float2 ls[NT];     // this lane's partial sums
   float base[NT][2];           // what is subtracted from a score: mx - kShift
-  float qs[NT][2];  // the power of two taken out of each of the lane's heads (times scale * log2(e) unless SC)
+  float qs[NT][2];  // the power of two taken out of each of the lane's heads (times |scale| log2(e) unless SC)
   float slope[NT][2];  // SC: of the lane's heads, log2 units
   float vs, vs_inv;  // largest V scale met (0 at first) and its inverse
 
@@ -147,7 +131,8 @@ struct WarpState<E4m3, D, GP, SC> {
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // top = f * 2^x, f in [1, 2): elements times 2^(14 - x); x is clamped so the factor is normal
       const int x = max((int)(__float_as_uint(top) >> 23) - 127, -112);
-      const float f = pow2i(14 - x);
+      // (a negative scale's sign goes into the elements: scores' factors stay positive)
+      const float f = !SC && a.scale_log2 < 0.f ? -pow2i(14 - x) : pow2i(14 - x);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         qf[nt][i][0] = pack_f16(__uint_as_float(raw[i].x << 16) * f, __uint_as_float(raw[i].x & 0xFFFF0000u) * f);
@@ -155,12 +140,12 @@ struct WarpState<E4m3, D, GP, SC> {
       }
       // the accumulator's columns are heads 2 q4 and 2 q4 + 1
       const float inv = pow2i(x - 14);
-      qs[nt][0] = __shfl_sync(0xffffffffu, inv, (2 * q4) * 4) * (SC ? 1.f : a.scale_log2);
-      qs[nt][1] = __shfl_sync(0xffffffffu, inv, (2 * q4 + 1) * 4) * (SC ? 1.f : a.scale_log2);
+      qs[nt][0] = __shfl_sync(0xffffffffu, inv, (2 * q4) * 4) * (SC ? 1.f : fabsf(a.scale_log2));
+      qs[nt][1] = __shfl_sync(0xffffffffu, inv, (2 * q4 + 1) * 4) * (SC ? 1.f : fabsf(a.scale_log2));
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) acc[j][nt][0] = acc[j][nt][1] = acc[j][nt][2] = acc[j][nt][3] = 0.f;
       mx[nt][0] = mx[nt][1] = kNegInf;
-      ls[nt][0] = ls[nt][1] = 0.f;
+      ls[nt] = make_float2(0.f, 0.f);
       base[nt][0] = base[nt][1] = -kShift;
     }
     vs = vs_inv = 0.f;
@@ -168,24 +153,25 @@ struct WarpState<E4m3, D, GP, SC> {
   }
 
   // M tiles at once: more work between the waits, one check of the maximum for all of them.
-  // `slot[m]` and `sK[m]` are tile m's scales and codes (V kTile * D bytes after K).  Returns true
+  // `slot[m]` and `sK[m]` are tile m's scales (K, V) and codes (V kTile * D bytes after K).  Returns true
   // when shared memory was written (the caller fences before TMA refills the stages).
   template <int M>
   __device__ __forceinline__ bool consume(const DecodeArgs& a, const Group& gr, const int (&t0)[M],
-                                          const uint32_t (&sK)[M], const ScaleSlot* (&slot)[M], int lane) {
-    const int mi = lane >> 3, rr = lane & 7;
-    const int row = rr + ((mi & 1) << 3);  // ldmatrix: matrices 0, 1 are rows 0-7, 8-15 of one chunk,
-    const int col = (mi >> 1) << 4;        // matrices 2, 3 those of the next chunk
+                                          const uint32_t (&sK)[M], const float2* (&slot)[M], int lane) {
     const int gq = lane >> 2;
+    // ldmatrix lane roles: matrices 0, 1 are rows 0-7, 8-15 of a 16-byte chunk, matrices 2, 3 those of
+    // the next; the swizzle xors the chunk index, so chunk i + {0, 1} of a tile is one xor away
+    const uint32_t lane_off = swz_q8<D>((lane & 7) + ((lane >> 3) & 1) * 8, (lane >> 4) * 16);
     bool dirty = false;
 
-    float s[M][NT][4];
-    float ks[M], vscale[M];
+    float s[M][NT][4];  // raw scores; times f in log2 units
+    float2 f[M][NT];
+    float vscale[M];
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      const int half = slot[m]->half;
-      ks[m] = slot[m]->pair[half][0];
-      vscale[m] = slot[m]->pair[half][1];
+      const float2 sc = *slot[m];
+      vscale[m] = sc.y;
+      constexpr bool kTwoChains = M * NT < 4;  // few scores at once: shorter accumulation chains
       float sb[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -194,7 +180,7 @@ struct WarpState<E4m3, D, GP, SC> {
 #pragma unroll
       for (int i = 0; i < D / 16; i += 2) {
         uint32_t w[4], a0[4], a1[4];
-        ldsm_x4(w, sK[m] + swz_q8<D>(row, 16 * i + col));
+        ldsm_x4(w, (sK[m] + lane_off) ^ (uint32_t)(16 * i));
         e4m3x4_to_f16(w[0], a0[0], a0[2]);
         e4m3x4_to_f16(w[1], a0[1], a0[3]);
         e4m3x4_to_f16(w[2], a1[0], a1[2]);
@@ -202,20 +188,29 @@ struct WarpState<E4m3, D, GP, SC> {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma_f16(s[m][nt], a0, qf[nt][i][0], qf[nt][i][1]);
-          mma_f16(sb[nt], a1, qf[nt][i + 1][0], qf[nt][i + 1][1]);
+          if constexpr (kTwoChains) mma_f16(sb[nt], a1, qf[nt][i + 1][0], qf[nt][i + 1][1]);
+          else mma_f16(s[m][nt], a1, qf[nt][i + 1][0], qf[nt][i + 1][1]);
         }
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (kTwoChains) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[m][nt][e] = (s[m][nt][e] + sb[nt][e]) * (qs[nt][e & 1] * ks[m]);
+          for (int e = 0; e < 4; ++e) s[m][nt][e] += sb[nt][e];
+        }
+        // positive (begin() moved a negative scale into Q), and normal so that -inf stays -inf
+        f[m][nt] = make_float2(fmaxf(qs[nt][0] * sc.x, 0x1p-126f), fmaxf(qs[nt][1] * sc.x, 0x1p-126f));
+      }
       if constexpr (SC) {
         const float d0 = (float)slot_distance(gr.rs, t0[m] + gq), d1 = (float)slot_distance(gr.rs, t0[m] + gq + 8);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            s[m][nt][e] = scored_log2<false>(a.score, a.scale_log2, s[m][nt][e], slope[nt][e & 1], e < 2 ? d0 : d1);
+            s[m][nt][e] = scored_log2<false>(a.score, a.scale_log2, s[m][nt][e] * ((e & 1) ? f[m][nt].y : f[m][nt].x),
+                                             slope[nt][e & 1], e < 2 ? d0 : d1);
+          f[m][nt] = make_float2(1.f, 1.f);
+        }
       }
       // a tile with slots outside the window: their scores are masked, and their V rows zeroed, as
       // 0 times a NaN is not 0
@@ -250,9 +245,9 @@ struct WarpState<E4m3, D, GP, SC> {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float x = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
+        float x = kNegInf;
 #pragma unroll
-        for (int m = 1; m < M; ++m) x = fmaxf(x, fmaxf(s[m][nt][c], s[m][nt][c + 2]));
+        for (int m = 0; m < M; ++m) x = fmaxf(x, fmaxf(s[m][nt][c], s[m][nt][c + 2]) * (c ? f[m][nt].y : f[m][nt].x));
         top[nt][c] = x;
         grow = grow || x > mx[nt][c] + kSlack;
       }
@@ -273,7 +268,7 @@ struct WarpState<E4m3, D, GP, SC> {
           const float al = ex2(mx[nt][c] - b);
           mx[nt][c] = n;
           base[nt][c] = b - kShift;
-          ls[nt][c] *= al;
+          (c ? ls[nt].y : ls[nt].x) *= al;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             acc[j][nt][c] *= al * keep;
@@ -285,15 +280,17 @@ struct WarpState<E4m3, D, GP, SC> {
     uint32_t pb[M][NT][2];
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      const float part = vscale[m] * vs_inv;
+      const float2 part = make_float2(vscale[m] * vs_inv, vscale[m] * vs_inv);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float p0 = ex2(s[m][nt][0] - base[nt][0]), p1 = ex2(s[m][nt][1] - base[nt][1]);
-        const float p2 = ex2(s[m][nt][2] - base[nt][0]), p3 = ex2(s[m][nt][3] - base[nt][1]);
-        ls[nt][0] += p0 + p2;
-        ls[nt][1] += p1 + p3;
-        pb[m][nt][0] = movmatrix_trans(pack_f16(p0 * part, p1 * part));
-        pb[m][nt][1] = movmatrix_trans(pack_f16(p2 * part, p3 * part));
+        const float2 nb = make_float2(-base[nt][0], -base[nt][1]);
+        const float2 x = ffma2(make_float2(s[m][nt][0], s[m][nt][1]), f[m][nt], nb);
+        const float2 y = ffma2(make_float2(s[m][nt][2], s[m][nt][3]), f[m][nt], nb);
+        const float2 p = make_float2(ex2(x.x), ex2(x.y)), r = make_float2(ex2(y.x), ex2(y.y));
+        ls[nt] = fadd2(ls[nt], fadd2(p, r));
+        const float2 pv = fmul2(p, part), rv = fmul2(r, part);
+        pb[m][nt][0] = movmatrix_trans(pack_f16(pv.x, pv.y));
+        pb[m][nt][1] = movmatrix_trans(pack_f16(rv.x, rv.y));
       }
     }
 
@@ -302,7 +299,7 @@ struct WarpState<E4m3, D, GP, SC> {
 #pragma unroll
       for (int m = 0; m < M; ++m) {
         uint32_t w[4], a0[4], a1[4];
-        ldsm_x4_trans(w, sK[m] + kTile * D + swz_q8<D>(row, 16 * j + col));
+        ldsm_x4_trans(w, (sK[m] + kTile * D + lane_off) ^ (uint32_t)(16 * j));
         // bytes of a register: (token 2 q4, dims 2 gq, 2 gq + 1), (token 2 q4 + 1, the same dims)
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = __byte_perm(w[e], 0u, 0x3120);
@@ -325,8 +322,8 @@ struct WarpState<E4m3, D, GP, SC> {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
-        ls[nt][0] += __shfl_xor_sync(0xffffffffu, ls[nt][0], off);
-        ls[nt][1] += __shfl_xor_sync(0xffffffffu, ls[nt][1], off);
+        ls[nt].x += __shfl_xor_sync(0xffffffffu, ls[nt].x, off);
+        ls[nt].y += __shfl_xor_sync(0xffffffffu, ls[nt].y, off);
       }
   }
 
@@ -339,8 +336,8 @@ struct WarpState<E4m3, D, GP, SC> {
     if (gq == 0) {
       sc_m[warp * SG + c0] = mx[nt][0];
       sc_m[warp * SG + c0 + 1] = mx[nt][1];
-      sc_l[warp * SG + c0] = ls[nt][0];
-      sc_l[warp * SG + c0 + 1] = ls[nt][1];
+      sc_l[warp * SG + c0] = ls[nt].x;
+      sc_l[warp * SG + c0 + 1] = ls[nt].y;
     }
     float* wacc = sc_acc + warp * SG * D;
 #pragma unroll

@@ -115,6 +115,28 @@ __device__ __forceinline__ uint4 encode16(const Row16& r, float inv) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 8 finite bf16 values (a 16-byte vector) times a power of two, as codes
+__device__ __forceinline__ uint2 encode8_finite(uint4 a, float inv) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  uint16_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = fmul2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), make_float2(inv, inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c[i]) : "f"(x.y), "f"(x.x));
+  }
+  return make_uint2((uint32_t)c[0] | ((uint32_t)c[1] << 16), (uint32_t)c[2] | ((uint32_t)c[3] << 16));
+}
+
+// the same for any 8 values: what is not finite becomes NaN
+__device__ __forceinline__ uint2 encode8(uint4 a, float inv) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i] = e4m3x2(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xFFFF0000u) * inv);
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));

@@ -22,7 +22,7 @@ namespace hwkv {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeAhead = 4;
+constexpr int kRopeAhead = 2;
 constexpr int kRopeRows = 4;  // most rows of a CTA
 
 template <typename T>

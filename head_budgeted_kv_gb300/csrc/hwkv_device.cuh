@@ -23,17 +23,69 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// tanh(u): 1 - 2 / (1 + e^2u) with the hardware's approximate exponential and reciprocal, which
-// loses relative accuracy near 0 (the difference's absolute error stays 2^-22), so below 1/4 the
-// odd Taylor polynomial to u^9 (next term 1382/155925 u^11: 2^-26 of u there).  Relative error
-// below 2^-20.  `exact`: CUDA's tanhf, 2 units of fp32.
+// Packed fp32 pair arithmetic (sm_100 family), elementwise: d = a * b + c, d = a + b, d = a * b.
+__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// tanh(u) for |u| <= 1 is u * tanh_poly(u^2): the polynomial of degree 5 in u^2 whose largest
+// relative error on [0, 1] is smallest (found by linear programming on 4001 Chebyshev points: 2^-20.7;
+// 2^-20.4 with the fp32 steps).
+constexpr float kTanh0 = 0.9999994039535522f, kTanh1 = -0.3332904279232025f, kTanh2 = 0.13281433284282684f;
+constexpr float kTanh3 = -0.05160565674304962f, kTanh4 = 0.016743095591664314f, kTanh5 = -0.0030670526903122663f;
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// the polynomial of two values of u^2
+__device__ __forceinline__ float2 tanh_poly2(float2 t) {
+  float2 p = ffma2(t, make_float2(kTanh5, kTanh5), make_float2(kTanh4, kTanh4));
+  p = ffma2(t, p, make_float2(kTanh3, kTanh3));
+  p = ffma2(t, p, make_float2(kTanh2, kTanh2));
+  p = ffma2(t, p, make_float2(kTanh1, kTanh1));
+  return ffma2(t, p, make_float2(kTanh0, kTanh0));
+}
+
+// tanh(u) beyond: 1 - 2 / (1 + e^2u) with the hardware's approximate exponential and reciprocal, whose
+// absolute error of 2^-22 is below 2^-21 of |tanh u| > 3/4.
+__device__ __forceinline__ float tanh_exp(float u) { return fmaf(-2.f, rcp(1.f + ex2(u * 2.8853900817779268f)), 1.f); }
+
+// tanh(u) with a relative error below 2^-20; `exact`: CUDA's tanhf, 2 units of fp32.
 template <bool exact>
 __device__ __forceinline__ float tanh_f32(float u) {
   if constexpr (exact) return tanhf(u);
   const float t = u * u;
-  const float p = u * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
-  const float r = 1.f - __fdividef(2.f, 1.f + ex2(u * 2.8853900817779268f));
-  return fabsf(u) < 0.25f ? p : r;
+  const float p = fmaf(t, fmaf(t, fmaf(t, fmaf(t, fmaf(t, kTanh5, kTanh4), kTanh3), kTanh2), kTanh1), kTanh0);
+  return fabsf(u) <= 1.f ? u * p : tanh_exp(u);
 }
 
 // The score of a raw dot product in log2 units: capped, then lowered by slope_log2 per position of
@@ -187,37 +239,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// Packed fp32 pair arithmetic (sm_100 family), elementwise: d = a * b + c, d = a + b, d = a * b.
-__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
-      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
-__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
 }
 
 // The resident window of a head at length len: the n = min(w, len) newest positions, which

@@ -548,41 +548,112 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       if ((jj & 31) == 0)
         clean_word = jj < 32 * kCleanWords ? reinterpret_cast<volatile uint32_t*>(s_clean[x])[jj >> 5] : 0u;
       const bool clean = (clean_word >> (jj & 31)) & 1u;
-      if constexpr (SC) {
-#pragma unroll
-        for (int u = 0; u < kPfSub; ++u) {
-          // distance of the row from the tile's first key; a ring tile may wrap to keys C older
-          const PfKeyTile kt = key_tile(tl, j * kPfSub + u, C);
-          const int d0 = pq - (kt.kind == 0 ? tl.p_oldest : p0) - kt.a;
-          const int wrap = kt.kind == 0 ? C - kt.a : kTile;
-#pragma unroll
-          for (int i = 0; i < kTile; ++i)
-            sv[u * kTile + i] = scored_log2<false>(a.score, a.scale_log2, sv[u * kTile + i], slope,
-                                                   (float)(d0 - i + (i >= wrap ? C : 0)));
-        }
-      }
-      if (!clean) {
-        PfKeyTile kt[kPfSub];
+      // visible keys of this row per 16-key tile, all of a clean stage: position in (pq - w, pq],
+      // resident or in the chunk, as intervals of the tile's key index
+      PfKeyTile kt[kPfSub];
+      uint32_t vis[kPfSub];
+      auto visible = [&]() {
 #pragma unroll
         for (int u = 0; u < kPfSub; ++u) kt[u] = key_tile(tl, j * kPfSub + u, C);
-        // visible keys of this row per 16-key tile: position in (pq - w, pq], resident or in
-        // the chunk, as intervals of the tile's key index
 #pragma unroll
         for (int u = 0; u < kPfSub; ++u) {
-          uint32_t vis = 0;
+          vis[u] = 0;
           const int ka = kt[u].a;
           if (kt[u].kind == 0) {
             // ring distance d = ka + i (wrapping at C) holds position p_oldest + d
             const int dlo = max(0, pq - w + 1 - tl.p_oldest), dhi = min(tl.rs.n - 1, pq - tl.p_oldest);
-            vis = range_bits(dlo - ka, min(dhi - ka, C - 1 - ka));
-            if (ka + kTile > C) vis |= range_bits(max(dlo - ka + C, C - ka), dhi - ka + C);
+            vis[u] = range_bits(dlo - ka, min(dhi - ka, C - 1 - ka));
+            if (ka + kTile > C) vis[u] |= range_bits(max(dlo - ka + C, C - ka), dhi - ka + C);
           } else if (kt[u].kind == 1) {
-            vis = range_bits(pq - w + 1 - p0 - ka, min(n - 1 - ka, pq - p0 - ka));
+            vis[u] = range_bits(pq - w + 1 - p0 - ka, min(n - 1 - ka, pq - p0 - ka));
           }
-          if (!live) vis = 0;
-#pragma unroll
-          for (int i = 0; i < kTile; ++i) sv[u * kTile + i] = (vis >> i) & 1u ? sv[u * kTile + i] : masked;
+          if (!live) vis[u] = 0;
         }
+      };
+      float row_off = 0.f;  // SC: what is still to be added to every score of the row
+      if constexpr (SC) {
+        if (!clean) {  // what is masked does not decide how the others are computed
+          visible();
+#pragma unroll
+          for (int u = 0; u < kPfSub; ++u)
+#pragma unroll
+            for (int i = 0; i < kTile; ++i) sv[u * kTile + i] = (vis[u] >> i) & 1u ? sv[u * kTile + i] : 0.f;
+        }
+        const float2 sl = make_float2(a.scale_log2, a.scale_log2);
+        if (a.score.capped) {
+          float big[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < kPfKeys; ++c) big[c & 3] = fmaxf(big[c & 3], fabsf(sv[c]));
+          const float u_max = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * fabsf(a.score.cap_in);
+          if (__all_sync(0xffffffffu, u_max <= 1.f || !live)) {
+            // no score of the warp reaches the cap: the polynomial alone, on packed pairs (a chunk of up
+            // to 1024 tokens at a 40000-token context, cap 50: 349 us; where scores pass the cap, with
+            // both forms, 489 us; uncapped 226 us)
+            const float2 ci = make_float2(a.score.cap_in, a.score.cap_in);
+#pragma unroll
+            for (int c = 0; c < kPfKeys; c += 2) {
+              const float2 x = make_float2(sv[c], sv[c + 1]);
+              const float2 u = fmul2(x, ci), t = fmul2(u, u);
+              const float2 y = fmul2(fmul2(x, sl), tanh_poly2(t));  // cap * u = scale * x
+              sv[c] = y.x;
+              sv[c + 1] = y.y;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kPfKeys; c += 2) {  // both forms of tanh_f32, packed, and a choice per score
+              const float2 x = make_float2(sv[c], sv[c + 1]);
+              const float2 u = fmul2(x, make_float2(a.score.cap_in, a.score.cap_in)), t = fmul2(u, u);
+              const float2 y = fmul2(fmul2(x, sl), tanh_poly2(t));
+              const float2 g = fmul2(u, make_float2(2.8853900817779268f, 2.8853900817779268f));
+              const float2 d = fadd2(make_float2(ex2(g.x), ex2(g.y)), make_float2(1.f, 1.f));
+              const float2 z = ffma2(make_float2(rcp(d.x), rcp(d.y)), make_float2(-2.f * a.score.cap_out, -2.f * a.score.cap_out),
+                                     make_float2(a.score.cap_out, a.score.cap_out));
+              sv[c] = fabsf(u.x) <= 1.f ? y.x : z.x;
+              sv[c + 1] = fabsf(u.y) <= 1.f ? y.y : z.y;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kPfKeys; c += 2) {
+            const float2 y = fmul2(make_float2(sv[c], sv[c + 1]), sl);
+            sv[c] = y.x;
+            sv[c + 1] = y.y;
+          }
+        }
+        if (a.score.slopes != nullptr) {
+          // less slope * distance.  Tile u's first key is d0[u] away, key i that much less i, and a ring
+          // tile's keys past the ring's end C more.  In a stage of 64 consecutive positions key c gets
+          // slope * c alone, an immediate operand, and the row's maximum and exponents the rest.
+          int d0[kPfSub];
+          bool run = true;
+#pragma unroll
+          for (int u = 0; u < kPfSub; ++u) {
+            const PfKeyTile k = key_tile(tl, j * kPfSub + u, C);
+            d0[u] = pq - (k.kind == 0 ? tl.p_oldest : p0) - k.a;
+            run = run && d0[u] == d0[0] - u * kTile && (k.kind != 0 || k.a + kTile <= C);
+          }
+          if (run) {
+            row_off = -slope * (float)d0[0];
+#pragma unroll
+            for (int c = 0; c < kPfKeys; ++c) sv[c] = fmaf(slope, (float)c, sv[c]);
+          } else {
+#pragma unroll
+            for (int u = 0; u < kPfSub; ++u) {
+              const PfKeyTile k = key_tile(tl, j * kPfSub + u, C);
+              const float far = -slope * (float)d0[u], wrapped = -slope * (float)(d0[u] + C);
+              const int wrap = k.kind == 0 ? C - k.a : kTile;
+#pragma unroll
+              for (int i = 0; i < kTile; ++i) sv[u * kTile + i] += fmaf(slope, (float)i, i < wrap ? far : wrapped);
+            }
+          }
+        }
+      }
+      if (!clean) {
+        if constexpr (!SC) visible();
+#pragma unroll
+        for (int u = 0; u < kPfSub; ++u)
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) sv[u * kTile + i] = (vis[u] >> i) & 1u ? sv[u * kTile + i] : masked;
       }
       // row maximum in log2 units
       float mx;
@@ -599,7 +670,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         t3[1] = fmax3(t2[3], t2[4], t2[5]);
         t3[2] = fmaxf(t2[6], t2[7]);
         const float m3 = fmax3(t3[0], t3[1], t3[2]);
-        mx = m3 == kNegInf ? kNegInf : m3 * sl2;
+        mx = m3 == kNegInf ? kNegInf : SC ? m3 + row_off : m3 * sl2;
       } else {
         mx = kNegInf;
 #pragma unroll
@@ -662,7 +733,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
 
       // P row (bf16 pairs) over the S columns it came from: p = 2^(s * scale_log2 - m_ref)
       const float2 sl2v = make_float2(pos_scale ? sl2 : 1.f, pos_scale ? sl2 : 1.f);
-      const float2 nb = make_float2(-bm, -bm);
+      const float2 nb = make_float2(row_off - bm, row_off - bm);
       float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       float pk[kPfKeys / 2];
 #pragma unroll

@@ -45,10 +45,18 @@ struct RopeVec {  // a 16-byte vector as fp32
   }
 };
 
-__device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   const float x = a, y = b;
-  a = fmaf(x, cs.x, -(y * cs.y));
-  b = fmaf(y, cs.x, x * cs.y);
+  a = fmaf(x, c, -(y * s));
+  b = fmaf(y, c, x * s);
+}
+
+// Cosines and sines of a row, two pairs to a 16-byte vector: (cos 2v, cos 2v + 1, sin 2v, sin 2v + 1).
+// A unit takes K consecutive vectors; vector v is stored at (v % K) * (32 / K) + v / K, so that the
+// units of neighbouring threads read neighbouring vectors (unit after unit they would share banks).
+template <int K>
+__device__ __forceinline__ int cs_slot(int v) {
+  return v % K * (32 / K) + v / K;
 }
 
 // Layouts of the pairs across 16-byte vectors
@@ -62,7 +70,8 @@ template <typename T, int kLayout>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   using Vec = RopeVec<T>;
   constexpr int V = Vec::V;
-  __shared__ __align__(16) float2 s_cs[kRopeRows][64];
+  constexpr int K = kLayout == kRopeHalf ? V / 2 : kLayout == kRopeInterleaved ? (V >= 4 ? V / 4 : 1) : 1;
+  __shared__ float4 s_cs[kRopeRows][32];
   griddep_launch_dependents();  // a decode launched with early reads may start its schedule and loads
 
   const int tiles = (a.n_max + a.rows - 1) / a.rows;
@@ -88,36 +97,46 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const int pairs = D / 2;
     for (int e = threadIdx.x; e < rows * pairs; e += kRopeThreads) {
       const int r = e / pairs, i = e - r * pairs;
-      float2 cs = make_float2(1.f, 0.f);
+      float sn = 0.f, cn = 1.f;
       if (i < half) {
         const uint64_t t = a.turns[i] * (uint64_t)((uint32_t)pos + (uint32_t)(i0 + r));
         const float x = (float)(int32_t)(t >> 32) * 0x1p-31f;  // half turns
-        sincospif(x, &cs.y, &cs.x);
-        cs.x *= a.magnitude;
-        cs.y *= a.magnitude;
+        sincospif(x, &sn, &cn);
+        cn *= a.magnitude;
+        sn *= a.magnitude;
       }
-      s_cs[r][i] = cs;
+      float* at = reinterpret_cast<float*>(&s_cs[r][cs_slot<K>(i >> 1)]) + (i & 1);
+      at[0] = cn;
+      at[2] = sn;
     }
   };
 
+  // the thread's units are kRopeThreads apart: (row, head, place in the head) steps on without divisions
   struct Unit {
-    const T* src;
-    T* dst;
-    int r, j;
+    int r, h, j;
   };
-  auto unit_at = [&](int u) {
-    Unit x;
-    const int rh = u / per_head;
-    x.j = u - rh * per_head;
-    x.r = rh / nh;
-    const int h = rh - x.r * nh;
-    const bool key = h >= a.q_heads;
-    const RopeTensor& in = key ? a.k : a.q;
-    const RopeTensor& out = key ? a.k_out : a.q_out;
-    const int64_t col = (int64_t)(key ? h - a.q_heads : h) * D;
-    x.src = static_cast<const T*>(in.data) + s * in.seq_stride + (i0 + x.r) * in.row_stride + col;
-    x.dst = static_cast<T*>(out.data) + s * out.seq_stride + (i0 + x.r) * out.row_stride + col;
-    return x;
+  const int dj = kRopeThreads % per_head, dh = kRopeThreads / per_head;
+  Unit at;
+  at.h = (int)threadIdx.x / per_head;
+  at.j = (int)threadIdx.x - at.h * per_head;
+  at.r = at.h / nh;
+  at.h -= at.r * nh;
+  auto step = [&]() {
+    at.j += dj;
+    at.h += dh;
+    if (at.j >= per_head) {
+      at.j -= per_head;
+      ++at.h;
+    }
+    while (at.h >= nh) {
+      at.h -= nh;
+      ++at.r;
+    }
+  };
+  auto row_of = [&](const Unit& x, const RopeTensor& q, const RopeTensor& k) {
+    const bool key = x.h >= a.q_heads;
+    const RopeTensor& t = key ? k : q;
+    return static_cast<T*>(t.data) + s * t.seq_stride + (i0 + x.r) * t.row_stride + (int64_t)(key ? x.h - a.q_heads : x.h) * D;
   };
 
   for (int u0 = 0; u0 < units; u0 += kRopeThreads * kRopeAhead) {
@@ -127,20 +146,22 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 #pragma unroll
     for (int k = 0; k < kRopeAhead; ++k) {
       const int u = u0 + k * kRopeThreads + (int)threadIdx.x;
+      un[k] = at;
+      step();
       if (u >= units) continue;
-      un[k] = unit_at(u);
       const int j = un[k].j;
+      const T* src = row_of(un[k], a.q, a.k);
       if constexpr (kLayout == kRopeHalf) {
         const int at = j < turned ? j * V : a.rot + (j - turned) * V;
-        lo[k] = *reinterpret_cast<const uint4*>(un[k].src + at);
-        if (j < turned) hi[k] = *reinterpret_cast<const uint4*>(un[k].src + half + at);
+        lo[k] = *reinterpret_cast<const uint4*>(src + at);
+        if (j < turned) hi[k] = *reinterpret_cast<const uint4*>(src + half + at);
       } else {
-        lo[k] = *reinterpret_cast<const uint4*>(un[k].src + j * V);
+        lo[k] = *reinterpret_cast<const uint4*>(src + j * V);
         if constexpr (kLayout == kRopeHalfAny) {
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             const int d = j * V + e;
-            if (d < a.rot) mate[k][e] = un[k].src[d < half ? d + half : d - half];
+            if (d < a.rot) mate[k][e] = src[d < half ? d + half : d - half];
           }
         }
       }
@@ -156,33 +177,46 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
       const int u = u0 + k * kRopeThreads + (int)threadIdx.x;
       if (u >= units) continue;
       const int j = un[k].j;
-      const float2* cs = s_cs[un[k].r];
+      const float4* cs = s_cs[un[k].r];
+      T* dst = row_of(un[k], a.q_out, a.k_out);
       if constexpr (kLayout == kRopeHalf) {
         if (j < turned) {
           Vec x, y;
           x.load(lo[k]);
           y.load(hi[k]);
 #pragma unroll
-          for (int e = 0; e < V; ++e) turn(x.v[e], y.v[e], cs[j * V + e]);
-          *reinterpret_cast<uint4*>(un[k].dst + j * V) = x.store();
-          *reinterpret_cast<uint4*>(un[k].dst + half + j * V) = y.store();
+          for (int e = 0; e < V; e += 2) {
+            const float4 t = cs[e / 2 * (32 / K) + j];  // cs_slot<K>((j * V + e) / 2)
+            const float2 c = make_float2(t.x, t.y), sn = make_float2(t.z, t.w);
+            const float2 xe = make_float2(x.v[e], x.v[e + 1]), ye = make_float2(y.v[e], y.v[e + 1]);
+            const float2 p = ffma2(xe, c, fmul2(ye, make_float2(-sn.x, -sn.y))), q = ffma2(ye, c, fmul2(xe, sn));
+            x.v[e] = p.x;
+            x.v[e + 1] = p.y;
+            y.v[e] = q.x;
+            y.v[e + 1] = q.y;
+          }
+          *reinterpret_cast<uint4*>(dst + j * V) = x.store();
+          *reinterpret_cast<uint4*>(dst + half + j * V) = y.store();
         } else {
-          *reinterpret_cast<uint4*>(un[k].dst + a.rot + (j - turned) * V) = lo[k];
+          *reinterpret_cast<uint4*>(dst + a.rot + (j - turned) * V) = lo[k];
         }
       } else if constexpr (kLayout == kRopeInterleaved) {
         if (j * V >= a.rot) {  // past the pairs: unchanged, whatever its bits
-          if (a.copy) *reinterpret_cast<uint4*>(un[k].dst + j * V) = lo[k];
+          if (a.copy) *reinterpret_cast<uint4*>(dst + j * V) = lo[k];
           continue;
         }
         Vec x;
         x.load(lo[k]);
 #pragma unroll
-        for (int e = 0; e < V; e += 2)
-          if (j * V + e < a.rot) turn(x.v[e], x.v[e + 1], cs[(j * V + e) / 2]);
-        *reinterpret_cast<uint4*>(un[k].dst + j * V) = x.store();
+        for (int e = 0; e < V; e += 4) {  // two pairs; those past rot do not turn
+          const float4 t = cs[e / 4 * (32 / K) + j];  // cs_slot<K>((j * V + e) / 4)
+          if (j * V + e < a.rot) turn(x.v[e], x.v[e + 1], t.x, t.z);
+          if (j * V + e + 2 < a.rot) turn(x.v[e + 2], x.v[e + 3], t.y, t.w);
+        }
+        *reinterpret_cast<uint4*>(dst + j * V) = x.store();
       } else {
         if (j * V >= a.rot) {
-          if (a.copy) *reinterpret_cast<uint4*>(un[k].dst + j * V) = lo[k];
+          if (a.copy) *reinterpret_cast<uint4*>(dst + j * V) = lo[k];
           continue;
         }
         Vec x;
@@ -192,10 +226,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
           const int d = j * V + e;
           if (d >= a.rot) continue;
           const float m = load_in<T>(&mate[k][e]);
-          const float2 c = cs[d < half ? d : d - half];
-          x.v[e] = d < half ? fmaf(x.v[e], c.x, -(m * c.y)) : fmaf(x.v[e], c.x, m * c.y);
+          const int i = d < half ? d : d - half;
+          const float* t = reinterpret_cast<const float*>(&cs[i >> 1]) + (i & 1);
+          x.v[e] = d < half ? fmaf(x.v[e], t[0], -(m * t[2])) : fmaf(x.v[e], t[0], m * t[2]);
         }
-        *reinterpret_cast<uint4*>(un[k].dst + j * V) = x.store();
+        *reinterpret_cast<uint4*>(dst + j * V) = x.store();
       }
     }
   }

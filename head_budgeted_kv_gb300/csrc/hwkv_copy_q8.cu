@@ -20,7 +20,7 @@ __device__ __forceinline__ int32_t slot_block(const PoolView& pv, const LayerGeo
   return -1;
 }
 
-// One warp per (seq, kv head, K or V): the new token's group is stored anew (recode_group).
+// One warp per (seq, kv head, K or V): the new token's group is stored anew (GroupRecode).
 template <int D>
 __global__ void __launch_bounds__(128) append_q8_kernel(const __grid_constant__ CopyArgs a) {
   const int warp = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
@@ -42,10 +42,12 @@ __global__ void __launch_bounds__(128) append_q8_kernel(const __grid_constant__ 
   const int r0 = t0 % bs;
   uint8_t* rows = static_cast<uint8_t*>(a.pv.pool) + (((int64_t)blk * 2 + kv) * bs + r0) * D;
   float* scale = a.pv.scales + ((int64_t)blk * (bs / kScaleGroup) + r0 / kScaleGroup) * 2 + kv;
-  const float now = recode_group<D>(
-      static_cast<const __nv_bfloat16*>(kv ? a.v : a.k) + (int64_t)sh * D, t0, slot, p, a.g.window[h], C, *scale,
-      [&](int r, int c) { return *reinterpret_cast<const uint4*>(rows + r * D + 16 * c); },
-      [&](int r, int c, uint4 v) { *reinterpret_cast<uint4*>(rows + r * D + 16 * c) = v; }, lane);
+  const float old = *scale;
+  GroupRecode<D> g;
+  g.load(static_cast<const __nv_bfloat16*>(kv ? a.v : a.k) + (int64_t)sh * D, t0, slot, p, a.g.window[h], C,
+         [&](int r, int c) { return *reinterpret_cast<const uint4*>(rows + r * D + 16 * c); }, lane);
+  const float now = g.store(warp_max(g.amax(old)), old,
+                            [&](int r, int c, uint4 v) { *reinterpret_cast<uint4*>(rows + r * D + 16 * c) = v; }, lane);
   if (lane == 0) *scale = now;
 }
 

@@ -46,45 +46,52 @@ __device__ __forceinline__ void issue_tile_q8(const CUtensorMap* tmap, int blk, 
 }
 
 // Fused append: when the tile starting at slot t0 is the new token's group, the group is stored
-// anew with the new row (recode_group), in shared memory and in the pool, with its scales.  No
+// anew with the new row (GroupRecode), in shared memory and in the pool, with its scales.  No
 // other CTA reads this tile, or its scales, in the launch.  A call of its own: it happens once per
 // group and would only fill the tile loop's registers and instruction cache.
 template <int D>
 __device__ __noinline__ void patch_new_row_q8(const DecodeArgs& a, const int32_t* tbl, int s, int h, int pos, int C,
                                               int t0, int new_slot, uint32_t sK, float2* slot, int lane) {
-  float scale[2] = {slot->x, slot->y};
+  const float2 old = *slot;
   __syncwarp();
   const int bs = a.pv.block_size;
   const int jb = t0 / bs, r0 = t0 - jb * bs;
   const int32_t blk = tbl[jb];
   const bool blk_ok = blk >= 0 && (int64_t)blk < a.pv.total_blocks;
   const int64_t src = ((int64_t)s * a.pv.kv_heads + h) * D;
-#pragma unroll 1
-  for (int kv = 0; kv < 2; ++kv) {
-    const uint32_t base = sK + kv * (kTile * D);
-    uint8_t* dst = static_cast<uint8_t*>(a.pv.pool) + (((int64_t)(blk_ok ? blk : 0) * 2 + kv) * bs + r0) * D;
-    scale[kv] = recode_group<D>(
-        static_cast<const __nv_bfloat16*>(kv ? a.v_new : a.k_new) + src, t0, new_slot, pos, a.g.window[h], C,
-        scale[kv],
-        [&](int r, int c) {
-          uint4 v;
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                       : "r"(base + swz_q8<D>(r, 16 * c)));
-          return v;
-        },
-        [&](int r, int c, uint4 v) {
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(base + swz_q8<D>(r, 16 * c)), "r"(v.x), "r"(v.y),
-                       "r"(v.z), "r"(v.w)
-                       : "memory");
-          if (blk_ok) *reinterpret_cast<uint4*>(dst + r * D + 16 * c) = v;
-        },
-        lane);
+  auto ld = [&](uint32_t base) {
+    return [base](int r, int c) {
+      uint4 v;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "r"(base + swz_q8<D>(r, 16 * c)));
+      return v;
+    };
+  };
+  auto st = [&](uint32_t base, uint8_t* dst) {
+    return [base, dst, blk_ok](int r, int c, uint4 v) {
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(base + swz_q8<D>(r, 16 * c)), "r"(v.x), "r"(v.y),
+                   "r"(v.z), "r"(v.w)
+                   : "memory");
+      if (blk_ok) *reinterpret_cast<uint4*>(dst + r * D + 16 * c) = v;
+    };
+  };
+  GroupRecode<D> k, v;
+  k.load(static_cast<const __nv_bfloat16*>(a.k_new) + src, t0, new_slot, pos, a.g.window[h], C, ld(sK), lane);
+  v.load(static_cast<const __nv_bfloat16*>(a.v_new) + src, t0, new_slot, pos, a.g.window[h], C, ld(sK + kTile * D), lane);
+  float mk = k.amax(old.x), mv = v.amax(old.y);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, off));
+    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, off));
   }
+  uint8_t* rows = static_cast<uint8_t*>(a.pv.pool) + ((int64_t)(blk_ok ? blk : 0) * 2 * bs + r0) * D;
+  const float2 now = make_float2(k.store(mk, old.x, st(sK, rows), lane),
+                                 v.store(mv, old.y, st(sK + kTile * D, rows + (int64_t)bs * D), lane));
   if (lane == 0) {
-    *slot = make_float2(scale[0], scale[1]);
+    *slot = now;
     const int64_t group = (int64_t)blk * (bs / kScaleGroup) + r0 / kScaleGroup;
-    if (blk_ok) *reinterpret_cast<float2*>(a.pv.scales + group * 2) = make_float2(scale[0], scale[1]);
+    if (blk_ok) *reinterpret_cast<float2*>(a.pv.scales + group * 2) = now;
   }
   __syncwarp();
 }

@@ -6,7 +6,7 @@
 // largest magnitude lies in (224, 448] * 2^e unless e is clamped.  A power of two costs e4m3
 // nothing against an exact amax / 448 (a floating-point code's relative step does not depend on
 // the scale) and makes both directions exact but for the one rounding to a code: scaling by 2^-e
-// rounds nothing, and when a later token makes the group's scale anew (recode_group), the codes
+// rounds nothing, and when a later token makes the group's scale anew (GroupRecode), the codes
 // move by a power of two, which rounds only those that become subnormal.
 // What is not finite is stored as NaN and does not count for the scale.
 #pragma once
@@ -143,57 +143,73 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
-// Stores a new token's row into one group (K or V) with the whole warp, scaling the group anew:
-// the row at slot `new_slot` (position `pos`) is replaced by `row` (bf16 [D]); the stored values
-// of the other slots of the group whose positions are in the window [pos + 1 - w, pos) are kept
-// at the new scale, and every other slot becomes zero.  `t0`: first slot of the group, C: ring
-// capacity; ld(r, c) / st(r, c, v) access 16-byte chunk c of row r.  Returns the new scale.
-template <int D, typename Ld, typename St>
-__device__ __forceinline__ float recode_group(const __nv_bfloat16* row, int t0, int new_slot, int pos, int w, int C,
-                                              float old_scale, Ld ld, St st, int lane) {
-  constexpr int kChunks = D / 16;             // 16-byte chunks of a row of codes
-  constexpr int kPer = kScaleGroup * kChunks / 32;  // chunks a lane owns
+// Storing a new token's row into one group (K or V) with the whole warp, scaling the group anew:
+// the row at slot `new_slot` (position `pos`) is replaced; the stored values of the other slots of
+// the group whose positions are in the window [pos + 1 - w, pos) are kept at the new scale, and every
+// other slot becomes zero.  Three steps, so that K and V can take them side by side:
+//   load     the chunks a lane owns (16 bytes of codes each), and its chunk of the new row;
+//   amax     the largest finite magnitude this lane sees (to be maximised over the warp);
+//   store    the chunks at the new scale.
+template <int D>
+struct GroupRecode {
+  static constexpr int kChunks = D / 16;                   // 16-byte chunks of a row of codes
+  static constexpr int kPer = kScaleGroup * kChunks / 32;  // chunks a lane owns: rows 32 / kChunks apart,
+                                                           // so at most one is of the new row
   uint4 code[kPer];
   int kind[kPer];  // 0 zero, 1 kept, 2 the new row
-  Row16 fresh;     // a lane owns at most one chunk of the new row: its rows step by 32 / kChunks >= 4
-  float amax = 0.f;
-  uint32_t best = 0u;
+  uint4 fresh[2];  // chunk lane % kChunks of the new row, bf16
+
+  // t0: first slot of the group, C: ring capacity; ld(r, c): 16-byte chunk c of row r
+  template <typename Ld>
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int t0, int new_slot, int pos, int w, int C, Ld ld,
+                                       int lane) {
+    const uint4* src = reinterpret_cast<const uint4*>(row + 16 * (lane % kChunks));
+    fresh[0] = src[0];
+    fresh[1] = src[1];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int id = lane + 32 * i, r = id / kChunks, c = id % kChunks;
-    int age = new_slot - (t0 + r);
-    if (age < 0) age += C;
-    kind[i] = age == 0 ? 2 : (age < w && age <= pos ? 1 : 0);
-    code[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (kind[i] == 1) code[i] = ld(r, c);
-    if (kind[i] == 2) {
-      const uint4* src = reinterpret_cast<const uint4*>(row + 16 * c);
-      fresh = widen16(src[0], src[1]);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(fresh.v[e]));
+    for (int i = 0; i < kPer; ++i) {
+      const int r = (lane + 32 * i) / kChunks;
+      int age = new_slot - (t0 + r);
+      if (age < 0) age += C;
+      kind[i] = age == 0 ? 2 : (age < w && age <= pos ? 1 : 0);
+      code[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (kind[i] == 1) code[i] = ld(r, lane % kChunks);
     }
   }
+
+  __device__ __forceinline__ float amax(float old_scale) const {
+    float m = 0.f;
+    uint32_t best = 0u;
+    bool owner = false;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    best = code_max4(best, code[i].x);
-    best = code_max4(best, code[i].y);
-    best = code_max4(best, code[i].z);
-    best = code_max4(best, code[i].w);
-  }
-  amax = warp_max(fmaxf(amax, code_max_value(best) * old_scale));
-  const float scale = pow2i(scale_exponent(amax)), inv = pow2_inverse(scale);
-  // a kept code that is not 0 bounds this by 2^18; with none the product may overflow, and 0
-  // times infinity must stay 0
-  const float factor = fminf(old_scale * inv, 0x1p100f);
+    for (int i = 0; i < kPer; ++i) {
+      owner = owner || kind[i] == 2;
+      best = code_max4(code_max4(code_max4(code_max4(best, code[i].x), code[i].y), code[i].z), code[i].w);
+    }
+    if (owner) {
+      const Row16 x = widen16(fresh[0], fresh[1]);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int id = lane + 32 * i, r = id / kChunks, c = id % kChunks;
-    uint4 v = code[i];
-    if (kind[i] == 2) v = encode16(fresh, inv);
-    else if (factor != 1.f) v = rescale_codes(v, factor);
-    st(r, c, v);
+      for (int e = 0; e < 16; ++e) m = fmaxf(m, finite_abs(x.v[e]));
+    }
+    return fmaxf(m, code_max_value(best) * old_scale);
   }
-  return scale;
-}
+
+  // amax: over the warp; st(r, c, v) writes a chunk.  Returns the new scale.
+  template <typename St>
+  __device__ __forceinline__ float store(float amax, float old_scale, St st, int lane) {
+    const float scale = pow2i(scale_exponent(amax)), inv = pow2_inverse(scale);
+    // a kept code that is not 0 bounds this by 2^18; with none the product may overflow, and 0
+    // times infinity must stay 0
+    const float factor = fminf(old_scale * inv, 0x1p100f);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      uint4 v = code[i];
+      if (kind[i] == 2) v = encode16(widen16(fresh[0], fresh[1]), inv);
+      else if (factor != 1.f) v = rescale_codes(v, factor);
+      st((lane + 32 * i) / kChunks, lane % kChunks, v);
+    }
+    return scale;
+  }
+};
 
 }  // namespace hwkv

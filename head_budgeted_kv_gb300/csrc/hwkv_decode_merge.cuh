@@ -19,6 +19,8 @@ constexpr int kGapTiles = 24;
 // while a producer warp runs on.  Thread indices count from 0 in both.
 struct CtaSync {
   static constexpr int kThreads = kWarps * 32;
+  static constexpr int kMergeCols = kThreads;  // most 4-float columns a head pass of a merge sums
+  static constexpr int kFold = 1;              // columns a thread folds together at a segment's end
   static __device__ __forceinline__ void sync() { __syncthreads(); }
   static __device__ __forceinline__ bool sync_and(bool p) { return __syncthreads_and(p) != 0; }
   static __device__ __forceinline__ bool sync_or(bool p) { return __syncthreads_or(p) != 0; }
@@ -27,6 +29,10 @@ struct CtaSync {
 template <int N>
 struct PartSync {
   static constexpr int kThreads = N;
+  // a pass may hold more columns than threads: half the heads a pass would double the passes' round
+  // trips (96 threads, 16 query heads of 128: 85 -> 80 us for a policy layer of 8-bit pools)
+  static constexpr int kMergeCols = (N + 127) / 128 * 128;
+  static constexpr int kFold = 4;  // fewer threads: a head's weights serve four columns
   static __device__ __forceinline__ void sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(N) : "memory"); }
   static __device__ __forceinline__ bool sync_and(bool p) {
     uint32_t r;
@@ -228,11 +234,11 @@ __device__ __forceinline__ void merge_slots_passes(const float* src_acc, const f
   const uint32_t bytes = (uint32_t)count * (uint32_t)G * D * 4u;
   const bool one = bytes <= ms.bytes;
   // heads per pass when the accumulators exceed the buffers: the largest power of two dividing
-  // G whose pass fits half the buffers and gives every column its own thread
+  // G whose pass fits half the buffers and whose columns Sync allows
   int hp = one ? G : 0;
   if (!one)
     for (int h = G; h >= 1; h >>= 1)
-      if (G % h == 0 && (uint32_t)count * (uint32_t)h * D * 4u <= ms.bytes / 2u && h * kV <= Sync::kThreads) {
+      if (G % h == 0 && (uint32_t)count * (uint32_t)h * D * 4u <= ms.bytes / 2u && h * kV <= Sync::kMergeCols) {
         hp = h;
         break;
       }
@@ -375,15 +381,14 @@ __host__ __device__ constexpr int merge_heads() {
 // line of T positions): the consuming warps' states are merged in shared memory (sc_m, sc_l,
 // sc_acc) into the group's output, or into this CTA's partial, which the group's last arriver
 // merges with the others.  `more`: the CTA has another segment; `failed`: this thread's warp gave
-// up a wait.  smem: the stage buffers, free after the last segment.
-template <typename Out, int D, int GP, typename Sync, int Gap, typename State>
+// up a wait.  SG: query heads merged per pass.  smem: the stage buffers, free after the last segment.
+template <typename Out, int D, int GP, int SG, typename Sync, int Gap, typename State>
 __device__ __forceinline__ void end_segment(const DecodeArgs& a, State& ws, const Group& sgr, int sg, long long spre,
                                             long long seg_begin, long long seg_end, long long T, int nctas, int cta,
                                             bool more, bool failed, uint8_t* smem, float* sc_m, float* sc_l,
                                             float* sc_acc, int* s_last, MergeStage& ms) {
   constexpr int W = Sync::kThreads / 32;
   constexpr int NT = State::NT;                 // 8-column groups of query heads
-  constexpr int SG = merge_heads<D, GP>();      // query heads merged per pass in shared memory
   constexpr int kPasses = GP < 8 ? 1 : 8 / SG;  // passes per 8-column group
   // the partial merge's (m, l) scratch reuses the warps' merge area: 2 * slots * G floats
   constexpr int kMlCap = W * SG * D;
@@ -405,25 +410,40 @@ __device__ __forceinline__ void end_segment(const DecodeArgs& a, State& ws, cons
     Sync::sync();
     const int g0 = 8 * nt + hh * SG;
     const int ng = min(SG, G - g0);  // real query heads of this pass
-    for (int e = threadIdx.x; e < ng * D; e += Sync::kThreads) {
+    constexpr int F = Sync::kFold;
+    for (int e = threadIdx.x * F; e < ng * D; e += Sync::kThreads * F) {
       const int gl = e / D, d = e - (e / D) * D;
       const int g = g0 + gl;
       float M = kNegInf;
 #pragma unroll
       for (int w = 0; w < W; ++w) M = fmaxf(M, sc_m[w * SG + gl]);
-      float Ls = 0.f, A = 0.f;
+      float Ls = 0.f, A[F] = {};
       if (M != kNegInf) {
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const float f = ex2(sc_m[w * SG + gl] - M);
           Ls += sc_l[w * SG + gl] * f;
-          A += sc_acc[(w * SG + gl) * D + d] * f;
+          const float* acc = sc_acc + (w * SG + gl) * D + d;
+          if constexpr (F == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(acc);
+            A[0] += v.x * f;
+            A[1] += v.y * f;
+            A[2] += v.z * f;
+            A[3] += v.w * f;
+          } else {
+            A[0] += acc[0] * f;
+          }
         }
       }
       if (whole) {
-        store_out<Out>(out + ((int64_t)sgr.s * Hq + sgr.h * G + g) * D + d, Ls > 0.f ? A / Ls : 0.f);
+        if constexpr (F == 4)
+          store_merged<Out, D>(M, Ls, make_float4(A[0], A[1], A[2], A[3]), g, d / 4, G,
+                               out + ((int64_t)sgr.s * Hq + sgr.h * G) * D, nullptr, nullptr, 0);
+        else
+          store_out<Out>(out + ((int64_t)sgr.s * Hq + sgr.h * G + g) * D + d, Ls > 0.f ? A[0] / Ls : 0.f);
       } else {
-        a.part_acc[(slot * G + g) * D + d] = A;
+        if constexpr (F == 4) *reinterpret_cast<float4*>(a.part_acc + (slot * G + g) * D + d) = make_float4(A[0], A[1], A[2], A[3]);
+        else a.part_acc[(slot * G + g) * D + d] = A[0];
         if (d == 0) {
           a.part_ml[(slot * G + g) * 2 + 0] = M;
           a.part_ml[(slot * G + g) * 2 + 1] = Ls;

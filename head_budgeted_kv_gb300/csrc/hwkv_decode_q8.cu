@@ -49,10 +49,17 @@ struct Q8Cfg {
   static_assert(NS % W == 0, "a stage buffer belongs to one consumer warp");
 };
 
+// query heads whose warp states meet in shared memory per merge pass: a whole 8-column n-tile
+// (three warps leave the room that four take at head_dim 128)
+template <int GP>
+__host__ __device__ constexpr int q8_merge_heads() {
+  return GP < 8 ? GP : 8;
+}
+
 template <int D, int GP>
 constexpr int q8_smem_bytes() {
   using Cfg = Q8Cfg<D>;
-  return Cfg::NS * Cfg::kStageBytes + Cfg::W * merge_heads<D, GP>() * D * 4 + 1024;
+  return Cfg::NS * Cfg::kStageBytes + Cfg::W * q8_merge_heads<GP>() * D * 4 + 1024;
 }
 
 __device__ __forceinline__ void mbar_arrive_one(uint64_t* bar) {
@@ -84,7 +91,7 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
   using Sync = typename Cfg::Sync;
   using State = WarpState<E4m3, D, GP, SC>;
   constexpr int W = Cfg::W, M = Cfg::M, NS = Cfg::NS;
-  constexpr int SG = merge_heads<D, GP>();
+  constexpr int SG = q8_merge_heads<GP>();
   constexpr int kThreads = Cfg::kThreads;
 
   extern __shared__ uint8_t smem_dyn[];
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
       if (lane == 0) mbar_arrive_one(&empty[st]);
     }
     const long long seg_begin = spre + kGap + first;
-    end_segment<__nv_bfloat16, D, GP, Sync, kGap>(a, ws, sgr, sg, spre, seg_begin, seg_begin + count, T, nctas, cta, more, !ok,
+    end_segment<__nv_bfloat16, D, GP, SG, Sync, kGap>(a, ws, sgr, sg, spre, seg_begin, seg_begin + count, T, nctas, cta, more, !ok,
                                             smem, sc_m, sc_l, sc_acc, &s_last, ms);
     Sync::sync();  // the merge scratch is rewritten by the next segment
     if (!more) break;

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
       j_cons += W;
     }
 
-    end_segment<Elem, D, GP, CtaSync, kGapTiles>(a, ws, sgr, sg, spre, seg_begin, seg_end, T, nctas, cta, more, drain_from >= 0, smem,
+    end_segment<Elem, D, GP, SG, CtaSync, kGapTiles>(a, ws, sgr, sg, spre, seg_begin, seg_end, T, nctas, cta, more, drain_from >= 0, smem,
                                       sc_m, sc_l, sc_acc, &s_last, ms);
     __syncthreads();  // the merge scratch is rewritten by the next segment
     if (!more) break;

@@ -26,10 +26,17 @@
 namespace hwkv {
 namespace {
 
-// Line positions charged for a group's boundary (see kGapTiles): twice those of bf16, as a position
-// stands for half the bytes (policy layer / 64 ragged sequences at head_dim 64, 24 -> 48: 57.4 -> 56.7
-// / 60.5 -> 55.4 us; 64: 56.9 / 58.0).
-constexpr int kGap = 2 * kGapTiles;
+// Line positions charged for a group's boundary (see kGapTiles): more than bf16's, as a position
+// stands for half the bytes.  Policy layer / 64 ragged sequences at head_dim 64 / batch 1 at 161K:
+// 24 55.6 / 54.7 / 21.0 us, 32 54.3 / 53.5 / 22.5, 40 54.1 / 54.4 / 20.8, 48 55.4 / 54.7 / 21.2, 64 55.8 /
+// 56.8 / 20.7.
+constexpr int kGap = 40;
+
+// Fewest line positions of a CTA: a short line is split over fewer CTAs, as each one more costs the
+// groups a partial to publish, count and merge; but a CTA takes ~0.35 us per position.  One sequence
+// with windows of 4096 and 1024: 1 16.2 us, 16 13.0, 20 14.0, 32 14.5, 64 17.5; five short sequences:
+// 16 15.5 us, 24 17.3, 32 18.1, 64 25.
+constexpr int kMinPositions = 16;
 
 template <int D>
 struct Q8Cfg {
@@ -40,7 +47,7 @@ struct Q8Cfg {
   static constexpr int M = D == 128 ? 2 : 4;          // tiles of a stage
   static constexpr int kTileBytes = 2 * kTile * D;    // K and V codes
   static constexpr int kStageBytes = M * kTileBytes;  // 8 KB
-  static constexpr int NS = 12;                       // stages of a CTA
+  static constexpr int NS = 9;                        // stages of a CTA (12: batch 1 0.5 us slower)
   static constexpr int kCtas = 2;                     // CTAs per SM
   using Sync = PartSync<W * 32>;
   // A buffer's stages must all go to one warp: it has then seen a buffer's use k before it waits for
@@ -114,7 +121,7 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
   const int H = a.pv.kv_heads;
   const int B = a.pv.num_seqs;
   const int ngroups = B * H;
-  const int nctas = gridDim.x, cta = blockIdx.x;
+  const int cta = blockIdx.x;
   const int G = a.group;
 
   // the next grid in the stream may start at once (see hwkv_decode_sk.cuh); with a.early the
@@ -151,7 +158,9 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
   for (int g = g_lo; g < g_hi; ++g) mine += group_span<kGap>(load_group(a, s_lens, g));
   long long T;
   const long long excl = block_exclusive_scan<W + 1>(mine, s_scan, T);
-  const long long t_lo = range_start(T, cta, nctas), t_hi = range_start(T, cta + 1, nctas);
+  const int nctas = (int)min((long long)gridDim.x, max(1LL, T / kMinPositions));  // CTAs with a range
+  const long long t_lo = cta < nctas ? range_start(T, cta, nctas) : T;
+  const long long t_hi = cta < nctas ? range_start(T, cta + 1, nctas) : T;
   if (t_lo < t_hi && excl <= t_lo && t_lo < excl + mine) {
     long long pre = excl;
     for (int g = g_lo; g < g_hi; ++g) {
@@ -269,7 +278,7 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
   // ---- consumers -------------------------------------------------------------------------
   if (a.early) griddep_wait();
   // groups with nothing resident (length 0) get a zero output, each from one CTA
-  for (int g = cta; g < ngroups; g += nctas) {
+  for (int g = cta; g < ngroups; g += (int)gridDim.x) {
     const Group gr = load_group(a, s_lens, g);
     if (gr.tiles == 0) {
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)gr.s * H + gr.h) * G * D;

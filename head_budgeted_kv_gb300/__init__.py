@@ -145,7 +145,7 @@ class Pool:
         if softcap == 0 and slopes is None:
             hwkv_decode_attn(self.handle, layer, q, scale, lens, out, self.workspace, stream, early_reads)
         else:
-            hwkv_decode_attn_score(self.handle, layer, q, binding.score(scale, softcap, slopes, q.shape[1]), lens, out,
+            hwkv_decode_attn_score(self.handle, layer, q, binding.score(scale, softcap, slopes, q), lens, out,
                                    self.workspace, None, None, stream, early_reads)
         return out
 
@@ -165,7 +165,7 @@ class Pool:
             hwkv_append_decode_attn(self.handle, layer, q, scale, k_new, v_new, pos, out, self.workspace, stream,
                                     early_reads)
         else:
-            hwkv_decode_attn_score(self.handle, layer, q, binding.score(scale, softcap, slopes, q.shape[1]), pos, out,
+            hwkv_decode_attn_score(self.handle, layer, q, binding.score(scale, softcap, slopes, q), pos, out,
                                    self.workspace, k_new, v_new, stream, early_reads)
         return out
 
@@ -194,7 +194,7 @@ class Pool:
         if softcap == 0 and slopes is None:
             hwkv_prefill_attn(self.handle, layer, q, scale, k_new, v_new, pos, n, out, workspace, stream)
         else:
-            hwkv_prefill_attn_score(self.handle, layer, q, binding.score(scale, softcap, slopes, q.shape[2]), k_new, v_new,
+            hwkv_prefill_attn_score(self.handle, layer, q, binding.score(scale, softcap, slopes, q), k_new, v_new,
                                     pos, n, out, workspace, stream)
         return out
 
@@ -227,9 +227,10 @@ class Pool:
 
     def _check_rows(self, t, name) -> int:
         shape = t.shape
-        if t.dtype != self.io_dtype or len(shape) < 3 or shape[0] != self.num_seqs or shape[-1] != self.head_dim:
+        if (t.dtype != self.io_dtype or len(shape) < 3 or shape[0] != self.num_seqs or shape[-1] != self.head_dim
+                or t.device != self.buffer.device):
             raise ValueError(f"{name} must hold {self.io_dtype} rows of head_dim {self.head_dim} for "
-                             f"{self.num_seqs} sequences")
+                             f"{self.num_seqs} sequences on {self.buffer.device}")
         return shape[-2]
 
     def check_device_errors(self, stream=None) -> int:

@@ -350,11 +350,14 @@ def hwkv_append_decode_attn(pool: int, layer: int, q: torch.Tensor, scale: float
 
 
 def score(scale: float, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
-          q_heads: Optional[int] = None) -> Score:
-    """A hwkv_score_t; slopes: float32 [q_heads] on the device (the caller keeps it alive)."""
-    if slopes is not None and (slopes.dtype != torch.float32 or not slopes.is_contiguous()
-                               or (q_heads is not None and slopes.numel() != q_heads)):
-        raise ValueError("slopes must be contiguous float32, one per query head")
+          q: Optional[torch.Tensor] = None) -> Score:
+    """A hwkv_score_t; slopes: float32 [q_heads] on the device (the caller keeps it alive).  With the
+    queries given, slopes must have one entry per query head and lie on their device."""
+    if slopes is not None:
+        if slopes.dtype != torch.float32 or not slopes.is_contiguous():
+            raise ValueError("slopes must be contiguous float32")
+        if q is not None and (slopes.numel() != q.shape[-2] or slopes.device != q.device):
+            raise ValueError("slopes must hold one value per query head, on the queries' device")
     return Score(float(scale), float(softcap), _ptr(slopes))
 
 
@@ -392,7 +395,7 @@ class DecodeLaunch:
         self._keep = (q, lens, out, workspace, k_new, v_new, slopes)
         plain = softcap == 0 and slopes is None
         self._fn = load().hwkv_decode_attn_ex if plain else load().hwkv_decode_attn_score
-        how = float(scale) if plain else score(scale, softcap, slopes, q.shape[1])
+        how = float(scale) if plain else score(scale, softcap, slopes, q)
         self._args = (pool, layer, _ptr(q), q.shape[1], how, _ptr(k_new), _ptr(v_new), _ptr(lens), _ptr(out),
                       _ptr(workspace), ws_bytes, HWKV_DECODE_EARLY_READS if early_reads else 0, _stream_ptr(stream))
 

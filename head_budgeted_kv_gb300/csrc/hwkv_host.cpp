@@ -896,7 +896,8 @@ int hwkv_rope(hwkv_pool_t p, const hwkv_rope_t* rope, const hwkv_rows_t* q, int 
     else if ((g.num_seqs > 1 && in[i]->seq_stride != to[i]->seq_stride) || (n_max > 1 && in[i]->row_stride != to[i]->row_stride))
       return fail(HWKV_ERR_INVALID_ARG, "an output in place of its input needs the input's strides");
   }
-  if (q && k && q_out->data == k_out->data) return fail(HWKV_ERR_INVALID_ARG, "q_out and k_out overlap");
+  if (q && k && (q_out->data == k_out->data || q_out->data == k->data || k_out->data == q->data))
+    return fail(HWKV_ERR_INVALID_ARG, "an output overlaps the other output or the other input");
   int rc = check_device(p);
   if (rc != HWKV_OK) return rc;
   NvtxRange range_("hwkv_rope", n_max);

@@ -374,3 +374,99 @@ def test_footprint_and_views():
     q, lens = c.randn(3, 8, 64), c.i32([200, 5, 64])
     assert torch.equal(c.pool.decode(0, q, c.scale, lens), d.pool.decode(0, q, c.scale, lens))
     c.close(), d.close()
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+def test_negative_and_zero_scale(scale):
+    """A negative scale attends to the least alike keys; a zero one gives the mean of the values."""
+    c = Case([64, 30], 1, 4, 64, 16, 41)
+    c.scale = scale
+    c.materialize([80])
+    q = c.randn(1, 8, 64)
+    c.check_out(q, c.pool.decode(0, q, scale, c.i32([80])), [80])
+    c.close()
+
+
+def test_more_sequences_than_lengths_staged():
+    """Past 256 sequences the lengths are read from global memory; some prompts are empty."""
+    lens = [(i * 37) % 90 for i in range(300)]
+    c = Case([20, 48], 300, 2, 64, 16, 43)
+    c.materialize(lens)
+    c.check_pool()
+    c.step(lens, True, check=False)
+    c.check_pool("appended")
+    q = c.randn(300, 4, 64)
+    now = [x + 1 for x in lens]
+    c.check_out(q, c.pool.decode(0, q, c.scale, c.i32(now)), now)
+    c.close()
+
+
+def test_source_by_strides():
+    """The prompt's K and V may be slices of larger tensors."""
+    a, b = Case([40, 20], 2, 4, 64, 16, 47), Case([40, 20], 2, 4, 64, 16, 47)
+    big = a.randn(2, 5, 90, 64)
+    k, v = big[:, 0:2], big[:, 2:4]
+    a.pool.materialize(0, k, v, a.i32([90, 33]))
+    b.pool.materialize(0, k.contiguous(), v.contiguous(), b.i32([90, 33]))
+    assert torch.equal(a.pool.buffer, b.pool.buffer) and a.pool.buffer.any()
+    a.close(), b.close()
+
+
+def test_refusals():
+    c = Case([64, 30], 1, 4, 64, 16, 53)
+    q, k, lens = c.randn(1, 8, 64), c.randn(1, 2, 64), c.i32([5])
+    for call in (lambda: c.pool.decode(0, q.float(), 0.1, lens), lambda: c.pool.append(0, k.float(), k, lens),
+                 lambda: c.pool.append_decode(0, q, 0.1, k, k.half(), lens),
+                 lambda: c.pool.materialize(0, k[:, :, None].float(), k[:, :, None].float(), lens),
+                 lambda: c.pool.decode(0, q, 0.1, lens, out=torch.empty_like(q, dtype=torch.float32))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: c.pool.set_decode_config(kernel=hw.HWKV_KERNEL_SIMT),
+                 lambda: c.pool.prefill(0, q[:, None].contiguous(), 0.1, k[:, None].contiguous(), k[:, None].contiguous(),
+                                        lens, lens)):
+        with pytest.raises(hw.HwkvError) as e:
+            call()
+        assert e.value.status == hw.binding.HWKV_ERR_UNSUPPORTED
+    plain = hw.Pool(1, 1, 64, 16, [[16]], 1, torch.bfloat16)
+    with pytest.raises(ValueError):
+        plain.scales()
+    assert plain.io_dtype == torch.bfloat16 and c.pool.io_dtype == torch.bfloat16
+    c.close()
+
+
+def test_serving_run_with_every_operator():
+    """A prompt stored in 8 bits, then steps of rotary positions, the append and capped, biased
+    attention, against the reference of all three."""
+    from reference_ops import rope, rope_frequencies
+    c = Case([48, 200], 2, 4, 64, 16, 59, table_seed=3)
+    table = hw.rope_table(64, base=500000.0, scaling="by_parts", factor=4.0, original_len=128)
+    freqs, magnitude = rope_frequencies(64, 500000.0, "by_parts", 4.0, 128)
+    slopes = torch.tensor([2.0 ** -(g + 1) for g in range(8)], device=c.dev)
+    lens = [150, 7]
+    k = c.randn(2, 150, 2, 64)
+    _, kr = c.pool.rope(table, None, k, c.i32([0, 0]), c.i32(lens))
+    v = c.randn(2, 2, 150, 64)
+    c.materialize(lens, kr.transpose(1, 2).contiguous(), v)
+    c.check_pool("prompt")
+    for _ in range(5):
+        q, k, v = c.randn(2, 8, 64), c.randn(2, 2, 64), c.randn(2, 2, 64)
+        pos = c.i32(lens)
+        qr, kr = c.pool.rope(table, q, k, pos)
+        for x, y in ((q, qr), (k, kr)):
+            for s in range(2):
+                ref = rope(np64(x)[s], lens[s], freqs, "half", magnitude)
+                size = np.abs(np64(x)[s]).max() * 2 ** 0.5 * magnitude
+                assert (np.abs(np64(y)[s] - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * size).all()
+        out = c.pool.append_decode(0, qr, c.scale, kr, v, pos, softcap=20.0, slopes=slopes)
+        c.ref_append(kr, v, lens)
+        lens = [n + 1 for n in lens]
+        c.check_pool("step")
+        for s in range(2):
+            for h in range(2):
+                p, rk, rv = c.rings[s][h].resident(lens[s])
+                for g in range(4 * h, 4 * h + 4):
+                    ref, mass, top = attention(np64(qr)[s, g], rk, rv, c.scale, lens[s] - 1 - p, 20.0, float(slopes[g]))
+                    # the capped score is off by 2^-20 of itself (header): 2^-19 top more on each weight
+                    tol = 2.0 ** -8 * np.abs(ref) + 2 * (2.0 ** -11 + 2.0 ** -12 + 2.0 ** -19 * top) * mass
+                    assert (np.abs(np64(out)[s, g] - ref) <= tol + 2.0 ** -36 * np.abs(rv).sum(0)).all()
+    c.close()

@@ -167,6 +167,10 @@ def test_refusals_and_flags():
     one = torch.zeros((1, 1, 4, D), device="cuda").bfloat16().expand(B, 3, 4, D)
     assert status(lambda: pool.rope(table, q, None, pos, q_out=one)) == hw.binding.HWKV_ERR_INVALID_ARG
     assert status(lambda: pool.rope(table, q, q[:, :, :H], pos, q_out=q, k_out=q[:, :, :H])) == hw.binding.HWKV_ERR_INVALID_ARG
+    kk = torch.zeros((B, 3, H, D), device="cuda").bfloat16()
+    assert status(lambda: pool.rope(table, kk, k, pos, q_out=k, k_out=kk)) == hw.binding.HWKV_ERR_INVALID_ARG
+    with pytest.raises(ValueError):
+        pool.rope(table, q.cpu(), None, pos)
     odd = torch.empty(B * 3 * 4 * D + 1, device="cuda").bfloat16()[1:].view(B, 3, 4, D)
     assert status(lambda: pool.rope(table, odd, None, pos)) == hw.binding.HWKV_ERR_ALIGNMENT
     broken = hw.rope_table(D)

@@ -225,7 +225,7 @@ def test_refusals():
     q = torch.zeros((1, 4, 64), device="cuda").bfloat16()
     lens = torch.tensor([5], dtype=torch.int32, device="cuda")
     ok = torch.zeros(4, device="cuda")
-    for bad in (ok[:3], ok.double(), torch.zeros(8, device="cuda")[::2]):
+    for bad in (ok[:3], ok.double(), torch.zeros(8, device="cuda")[::2], ok.cpu()):
         with pytest.raises(ValueError):
             pool.decode(0, q, 0.1, lens, slopes=bad)
     for scale, cap in ((0.1, -1.0), (0.1, float("nan")), (0.1, float("inf")), (float("nan"), 5.0), (1e30, 1e-30), (1.0, 3e38)):

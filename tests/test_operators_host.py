@@ -116,7 +116,9 @@ def test_scored_calls_check_their_arguments(lib):
     assert lib.hwkv_decode_attn_score(None, 0, None, 4, s, None, None, None, None, None, 0, 0, None) == binding.HWKV_ERR_INVALID_ARG
     assert lib.hwkv_prefill_attn_score(None, 0, None, 4, s, None, None, 1, None, None, None, None, 0, None) == binding.HWKV_ERR_INVALID_ARG
     with pytest.raises(ValueError):
-        binding.score(1.0, 0.0, torch.zeros(4), 5)
+        binding.score(1.0, 0.0, torch.zeros(4), torch.zeros(1, 5, 64))
+    with pytest.raises(ValueError):
+        binding.score(1.0, 0.0, torch.zeros(4).double())
 
 
 def test_tanh_form():

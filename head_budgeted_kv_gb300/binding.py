@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Optional
 
 import numpy as np
@@ -275,20 +276,31 @@ def hwkv_rope_table(rot_dim: int, layout: int = HWKV_ROPE_HALF, base: float = 10
     return t
 
 
-def _rows(t: torch.Tensor, shape, name: str) -> Rows:
-    """The hwkv_rows_t of [B][n][heads][D], or of [B][heads][D] as one row."""
+class _RowSlots(threading.local):
+    """The four hwkv_rows_t of a rope call, kept per thread with the references ctypes passes: making
+    them anew costs a small call as much as its launch."""
+
+    def __init__(self):
+        self.rows = [Rows() for _ in range(4)]
+        self.refs = [ctypes.byref(r) for r in self.rows]
+
+
+_row_slots = _RowSlots()
+
+
+def _fill_rows(r: Rows, t: torch.Tensor, head_dim: int, name: str):
+    """r describes [B][n][heads][D], or [B][heads][D] as one row."""
     st = t.stride()
-    if len(st) not in (3, 4) or st[-1] != 1 or (shape[-2] > 1 and st[-2] != shape[-1]):
+    if len(st) == 4:
+        r.seq_stride, r.row_stride, head, elem = st
+    elif len(st) == 3:
+        r.seq_stride, head, elem = st
+        r.row_stride = 0
+    else:
+        head = elem = 0
+    if elem != 1 or (head != head_dim and t.shape[-2] > 1):
         raise ValueError(f"{name} must be [B][n][heads][D] or [B][heads][D] with the heads of a row contiguous")
-    return Rows(t.data_ptr(), st[0], st[1] if len(st) == 4 else 0)
-
-
-def _row_pair(x: torch.Tensor, out: Optional[torch.Tensor], name: str):
-    """(shape, rows of the input, rows of the output), checked against one another."""
-    shape = x.shape
-    if out is None or out.shape != shape or out.dtype != x.dtype:
-        raise ValueError(f"{name}_out must match {name}")
-    return shape, _rows(x, shape, name), _rows(out, shape, name + "_out")
+    r.data = t.data_ptr()
 
 
 def hwkv_rope(pool: int, table: RopeTable, q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: torch.Tensor,
@@ -297,17 +309,35 @@ def hwkv_rope(pool: int, table: RopeTable, q: Optional[torch.Tensor], k: Optiona
     None) at positions pos + row; outputs may be the inputs; n: int32 [B] rows per sequence or None."""
     if pos.dtype != torch.int32 or (n is not None and n.dtype != torch.int32):
         raise ValueError("positions and row counts must be int32")
+    slots = _row_slots
+    rows, refs = slots.rows, slots.refs
     rq = rk = ro = rp = None
-    rows, heads = 0, 0
+    n_max, heads, dims = 0, 0, 0
     if q is not None:
-        sq, rq, ro = _row_pair(q, q_out, "q")
-        rows, heads = (sq[1] if len(sq) == 4 else 1), sq[-2]
+        shape = q.shape
+        if q_out is None or (q_out is not q and (q_out.shape != shape or q_out.dtype != q.dtype)):
+            raise ValueError("q_out must match q")
+        dims = len(shape)
+        n_max, heads = (shape[1] if dims == 4 else 1), shape[-2]
+        _fill_rows(rows[0], q, shape[-1], "q")
+        rq = ro = refs[0]
+        if q_out is not q:
+            _fill_rows(rows[1], q_out, shape[-1], "q_out")
+            ro = refs[1]
+        seqs = shape[0]
     if k is not None:
-        sk, rk, rp = _row_pair(k, k_out, "k")
-        rows = sk[1] if len(sk) == 4 else 1
-        if q is not None and sk[:-2] != sq[:-2]:
+        shape = k.shape
+        if k_out is None or (k_out is not k and (k_out.shape != shape or k_out.dtype != k.dtype)):
+            raise ValueError("k_out must match k")
+        if dims and (len(shape) != dims or shape[0] != seqs or (dims == 4 and shape[1] != n_max)):
             raise ValueError("q and k must have the same sequences and rows")
-    _check(load().hwkv_rope(pool, table, rq, heads, rk, rows, _ptr(pos), _ptr(n), ro, rp, _stream_ptr(stream)))
+        n_max = shape[1] if len(shape) == 4 else 1
+        _fill_rows(rows[2], k, shape[-1], "k")
+        rk = rp = refs[2]
+        if k_out is not k:
+            _fill_rows(rows[3], k_out, shape[-1], "k_out")
+            rp = refs[3]
+    _check(load().hwkv_rope(pool, table, rq, heads, rk, n_max, pos.data_ptr(), _ptr(n), ro, rp, _stream_ptr(stream)))
 
 
 def hwkv_decode_workspace_bytes(pool: int, q_heads: int) -> int:

@@ -54,12 +54,6 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
   return d;
 }
 
-// tanh(u) for |u| <= 1 is u * tanh_poly(u^2): the polynomial of degree 5 in u^2 whose largest
-// relative error on [0, 1] is smallest (found by linear programming on 4001 Chebyshev points: 2^-20.7;
-// 2^-20.4 with the fp32 steps).
-constexpr float kTanh0 = 0.9999994039535522f, kTanh1 = -0.3332904279232025f, kTanh2 = 0.13281433284282684f;
-constexpr float kTanh3 = -0.05160565674304962f, kTanh4 = 0.016743095591664314f, kTanh5 = -0.0030670526903122663f;
-
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -966,6 +966,20 @@ int score_args(const hwkv_score_t& sc, ScoreArgs* out) {
     out->cap_out = sc.softcap * 1.4426950408889634f;
     if (!std::isfinite(out->cap_in) || !std::isfinite(out->cap_out))
       return fail(HWKV_ERR_INVALID_ARG, "scale / softcap and softcap * log2(e) must be finite in fp32");
+    out->poly_on = 1;
+    const double u = out->cap_in;
+    double f = sc.scale * 1.4426950408889634;
+    const float tanh_poly[6] = {kTanh0, kTanh1, kTanh2, kTanh3, kTanh4, kTanh5};
+    for (int k = 0; k < 6; ++k, f *= u * u) {
+      out->poly[k] = (float)(tanh_poly[k] * f);
+      if (!std::isnormal(out->poly[k])) out->poly_on = 0;
+    }
+    const float half_poly[4] = {kTanhHalf0, kTanhHalf1, kTanhHalf2, kTanhHalf3};
+    f = sc.scale * 1.4426950408889634;
+    for (int k = 0; k < 4; ++k, f *= u * u) {  // no smaller than poly[]'s last ones
+      out->half[k] = (float)(half_poly[k] * f);
+      if (!std::isnormal(out->half[k])) out->poly_on = 0;
+    }
   }
   return HWKV_OK;
 }

@@ -50,6 +50,16 @@ struct CopyArgs {
   int32_t rows_per_cta;    // materialise only
 };
 
+// tanh(u) = u * (kTanh0 + kTanh1 u^2 + ... + kTanh5 u^10) for |u| <= 1: the polynomial of degree 5 in
+// u^2 whose largest relative error on [0, 1] is smallest (found by linear programming on 4001
+// Chebyshev points: 2^-20.7; 2^-20.4 with fp32 steps).
+constexpr float kTanh0 = 0.9999994039535522f, kTanh1 = -0.3332904279232025f, kTanh2 = 0.13281433284282684f;
+constexpr float kTanh3 = -0.05160565674304962f, kTanh4 = 0.016743095591664314f, kTanh5 = -0.0030670526903122663f;
+
+// The same for |u| <= 1/2 with degree 3 in u^2 (2^-20.8; 2^-20.6 with fp32 steps).
+constexpr float kTanhHalf0 = 0.999999463558197f, kTanhHalf1 = -0.33326318860054016f;
+constexpr float kTanhHalf2 = 0.13190296292304993f, kTanhHalf3 = -0.04440220072865486f;
+
 // What happens to a score s = scale <q, k> before the softmax: cap * tanh(s / cap) when capped,
 // then less slope * (distance of the key from the query).
 struct ScoreArgs {
@@ -57,6 +67,12 @@ struct ScoreArgs {
   int32_t capped;
   float cap_in;            // scale / cap
   float cap_out;           // cap * log2(e)
+  // below the cap, the score in log2 units of a raw dot product x is x * (poly[0] + poly[1] x^2 + ..):
+  // tanh's polynomials with the scale and 1 / cap worked in, half[] below half of the cap; poly_on:
+  // their coefficients are normal fp32
+  int32_t poly_on;
+  float poly[6];
+  float half[4];
   const float* slopes;     // [Hq] slopes, or null
 };
 

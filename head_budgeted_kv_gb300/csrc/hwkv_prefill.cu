@@ -33,6 +33,7 @@
 //   O is rarely touched between stages.  Every wait is bounded (~2 s); a timeout records
 //   HWKV_DEVERR_WAIT_TIMEOUT and all roles stop.
 #include <algorithm>
+#include <type_traits>
 
 #include "hwkv_tcgen05.cuh"
 
@@ -173,6 +174,19 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
   lo = max(lo, 0);
   hi = min(hi, 15);
   return lo > hi ? 0u : ((0xFFFFu >> (15 - hi)) & (0xFFFFu << lo));
+}
+
+// 64 values folded by a tree of three-input operations (64 -> 22 -> 8 -> 3 -> 1), not a dependent chain
+template <typename Op>
+__device__ __forceinline__ float tree64(const float (&v)[kPfKeys], Op op) {
+  float t1[22], t2[8];
+#pragma unroll
+  for (int i = 0; i < 21; ++i) t1[i] = op(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
+  t1[21] = v[63];
+#pragma unroll
+  for (int i = 0; i < 7; ++i) t2[i] = op(t1[3 * i], t1[3 * i + 1], t1[3 * i + 2]);
+  t2[7] = t1[21];
+  return op(op(t2[0], t2[1], t2[2]), op(t2[3], t2[4], t2[5]), op(t2[6], t2[7], t2[7]));
 }
 
 // SC: scores are capped or biased by distance, in registers between the two products.
@@ -522,8 +536,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
     const int pq = p0 + tok;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t colO = Cfg::kColO + x * D;
-    const float sl2 = SC ? 1.f : a.scale_log2;  // capped and biased scores are in log2 units already
-    const float slope = SC ? slope_log2(a.score, h * G + r % G) : 0.f;
+    // capped scores are in log2 units when they meet the softmax; biased ones alone stay raw, the slope
+    // divided by the scale, unless that is too small or negative
+    const bool raw_bias = SC && !a.score.capped && a.scale_log2 > 0x1p-40f;
+    const float sl2 = SC && !raw_bias ? 1.f : a.scale_log2;
+    const float slope = SC ? slope_log2(a.score, h * G + r % G) / sl2 : 0.f;  // in units of sl2
+    uint32_t run_word = 0u;  // SC: bit i: stage i of the next 32 holds 64 consecutive positions ...
+    int run_first = 0;       // ... and, in lane i, its first key's position
     // with a positive scale the row maximum is taken on raw scores and scale-and-subtract is
     // one packed FMA; masked scores become -inf before scaling (+inf for a negative scale)
     const bool pos_scale = sl2 > 0.f;
@@ -571,6 +590,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         }
       };
       float row_off = 0.f;  // SC: what is still to be added to every score of the row
+      float row_max = 0.f;  // SC: the row's maximum, when have_max
+      bool have_max = false;
       if constexpr (SC) {
         if (!clean) {  // what is masked does not decide how the others are computed
           visible();
@@ -581,23 +602,39 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         }
         const float2 sl = make_float2(a.scale_log2, a.scale_log2);
         if (a.score.capped) {
-          float big[4] = {0.f, 0.f, 0.f, 0.f};
+          const float hi = tree64(sv, [](float p, float q, float r) { return fmax3(p, q, r); });
+          const float lo = tree64(sv, [](float p, float q, float r) { return fmin3(p, q, r); });
+          const float u_max = fmaxf(hi, -lo) * fabsf(a.score.cap_in);
+          // No score of the warp reaches the cap (or half of it): a polynomial in x^2 alone, on packed
+          // pairs.  Its terms are what a capped stage costs, 20 us each for a chunk of up to 1024 tokens at
+          // a 40000-token context (cap 50, scores to half the cap: 325 us; cap 25, to the cap:
+          // 335 us; past it, both forms: 515 us; uncapped: 226 us).
+          auto polynomial = [&](auto degree, const float* coef) {
+            constexpr int n = decltype(degree)::value;
+            auto capped = [&](float2 v) {
+              const float2 t = fmul2(v, v);
+              float2 p = make_float2(coef[n], coef[n]);
 #pragma unroll
-          for (int c = 0; c < kPfKeys; ++c) big[c & 3] = fmaxf(big[c & 3], fabsf(sv[c]));
-          const float u_max = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * fabsf(a.score.cap_in);
-          if (__all_sync(0xffffffffu, u_max <= 1.f || !live)) {
-            // no score of the warp reaches the cap: the polynomial alone, on packed pairs (a chunk of up
-            // to 1024 tokens at a 40000-token context, cap 50: 349 us; where scores pass the cap, with
-            // both forms, 489 us; uncapped 226 us)
-            const float2 ci = make_float2(a.score.cap_in, a.score.cap_in);
+              for (int k = n - 1; k >= 0; --k) p = ffma2(t, p, make_float2(coef[k], coef[k]));
+              return fmul2(v, p);
+            };
 #pragma unroll
             for (int c = 0; c < kPfKeys; c += 2) {
-              const float2 x = make_float2(sv[c], sv[c + 1]);
-              const float2 u = fmul2(x, ci), t = fmul2(u, u);
-              const float2 y = fmul2(fmul2(x, sl), tanh_poly2(t));  // cap * u = scale * x
+              const float2 y = capped(make_float2(sv[c], sv[c + 1]));
               sv[c] = y.x;
               sv[c + 1] = y.y;
             }
+            // the cap keeps the order, so a clean stage's maximum is that of its largest raw score
+            if (clean && a.score.slopes == nullptr) {
+              const float top = a.scale_log2 > 0.f ? hi : lo;
+              row_max = capped(make_float2(top, top)).x;
+              have_max = true;
+            }
+          };
+          if (a.score.poly_on && __all_sync(0xffffffffu, u_max <= 0.5f || !live)) {
+            polynomial(std::integral_constant<int, 3>(), a.score.half);
+          } else if (a.score.poly_on && __all_sync(0xffffffffu, u_max <= 1.f || !live)) {
+            polynomial(std::integral_constant<int, 5>(), a.score.poly);
           } else {
 #pragma unroll
             for (int c = 0; c < kPfKeys; c += 2) {  // both forms of tanh_f32, packed, and a choice per score
@@ -612,7 +649,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
               sv[c + 1] = fabsf(u.y) <= 1.f ? y.y : z.y;
             }
           }
-        } else {
+        } else if (!raw_bias) {
 #pragma unroll
           for (int c = 0; c < kPfKeys; c += 2) {
             const float2 y = fmul2(make_float2(sv[c], sv[c + 1]), sl);
@@ -621,26 +658,32 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
           }
         }
         if (a.score.slopes != nullptr) {
-          // less slope * distance.  Tile u's first key is d0[u] away, key i that much less i, and a ring
-          // tile's keys past the ring's end C more.  In a stage of 64 consecutive positions key c gets
-          // slope * c alone, an immediate operand, and the row's maximum and exponents the rest.
-          int d0[kPfSub];
-          bool run = true;
+          // less slope * distance.  In a stage of 64 consecutive positions key c gets slope * c alone, an
+          // immediate operand, and the row's maximum and exponents the rest.
+          auto first_key = [&](const PfKeyTile& k) { return (k.kind == 0 ? tl.p_oldest : p0) + k.a; };
+          if ((jj & 31) == 0) {  // 32 stages at a time, one per lane
+            const PfKeyTile k0 = key_tile(tl, (j + lane) * kPfSub, C);
+            run_first = first_key(k0);
+            bool run = true;
 #pragma unroll
-          for (int u = 0; u < kPfSub; ++u) {
-            const PfKeyTile k = key_tile(tl, j * kPfSub + u, C);
-            d0[u] = pq - (k.kind == 0 ? tl.p_oldest : p0) - k.a;
-            run = run && d0[u] == d0[0] - u * kTile && (k.kind != 0 || k.a + kTile <= C);
+            for (int u = 0; u < kPfSub; ++u) {
+              const PfKeyTile k = key_tile(tl, (j + lane) * kPfSub + u, C);
+              run = run && first_key(k) == run_first + u * kTile && (k.kind != 0 || k.a + kTile <= C);
+            }
+            run_word = __ballot_sync(0xffffffffu, run);
           }
-          if (run) {
-            row_off = -slope * (float)d0[0];
+          const int first = __shfl_sync(0xffffffffu, run_first, jj & 31);
+          if ((run_word >> (jj & 31)) & 1u) {
+            row_off = -slope * sl2 * (float)(pq - first);
 #pragma unroll
             for (int c = 0; c < kPfKeys; ++c) sv[c] = fmaf(slope, (float)c, sv[c]);
           } else {
+            // tile by tile; a ring tile's keys past the ring's end are C positions older
 #pragma unroll
             for (int u = 0; u < kPfSub; ++u) {
               const PfKeyTile k = key_tile(tl, j * kPfSub + u, C);
-              const float far = -slope * (float)d0[u], wrapped = -slope * (float)(d0[u] + C);
+              const int d0 = pq - first_key(k);
+              const float far = -slope * (float)d0, wrapped = -slope * (float)(d0 + C);
               const int wrap = k.kind == 0 ? C - k.a : kTile;
 #pragma unroll
               for (int i = 0; i < kTile; ++i) sv[u * kTile + i] += fmaf(slope, (float)i, i < wrap ? far : wrapped);
@@ -658,19 +701,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       // row maximum in log2 units
       float mx;
       if (pos_scale) {
-        // a tree of three-input maxima (64 -> 22 -> 8 -> 3 -> 1), not a dependent chain
-        float t1[22], t2[8], t3[3];
-#pragma unroll
-        for (int i = 0; i < 21; ++i) t1[i] = fmax3(sv[3 * i], sv[3 * i + 1], sv[3 * i + 2]);
-        t1[21] = sv[63];
-#pragma unroll
-        for (int i = 0; i < 7; ++i) t2[i] = fmax3(t1[3 * i], t1[3 * i + 1], t1[3 * i + 2]);
-        t2[7] = t1[21];
-        t3[0] = fmax3(t2[0], t2[1], t2[2]);
-        t3[1] = fmax3(t2[3], t2[4], t2[5]);
-        t3[2] = fmaxf(t2[6], t2[7]);
-        const float m3 = fmax3(t3[0], t3[1], t3[2]);
-        mx = m3 == kNegInf ? kNegInf : SC ? m3 + row_off : m3 * sl2;
+        const float m3 =
+            SC && have_max ? row_max : tree64(sv, [](float p, float q, float r) { return fmax3(p, q, r); });
+        mx = m3 == kNegInf ? kNegInf : SC ? fmaf(m3, sl2, row_off) : m3 * sl2;
       } else {
         mx = kNegInf;
 #pragma unroll

@@ -44,7 +44,8 @@ def histories(gen, B, H, L, D, dtype):
     return (torch.randn((B, H, L, D), generator=gen, device="cuda").to(dtype) for _ in range(2))
 
 
-SCORES = {"cap": (15.0, False), "bias": (0.0, True), "both": (8.0, True), "tiny cap": (1e-3, False), "large cap": (1e5, False)}
+SCORES = {"cap": (15.0, False), "bias": (0.0, True), "both": (8.0, True), "tiny cap": (1e-3, False), "large cap": (1e5, False),
+          "low": (60.0, False), "half": (25.0, False)}
 
 
 @pytest.mark.parametrize("score", sorted(SCORES))
@@ -137,7 +138,7 @@ def test_long_groups_merge_alike():
             assert (np.abs(got[0, g] - ref) <= tol).all(), (workers, g)
 
 
-@pytest.mark.parametrize("score", ["cap", "bias", "both"])
+@pytest.mark.parametrize("score", ["cap", "bias", "both", "low", "half", "tiny cap", "large cap"])
 @pytest.mark.parametrize("D,G,bs,windows,pos,n,max_stages", [
     (128, 4, 16, [64, 200], [0, 150], [130, 7], 0),
     (64, 2, 16, [40, 500, 16], [333, 20], [50, 100], 0),

@@ -137,3 +137,11 @@ def test_tanh_form():
     want = np.tanh(u.astype(np.float64))
     fine = want != 0
     assert (np.abs(got - want)[fine] <= 2.0 ** -20 * np.abs(want)[fine]).all()
+    # the shorter polynomial below half of the cap
+    c = [np.float32(v) for v in (0.999999463558197, -0.33326318860054016, 0.13190296292304993, -0.04440220072865486)]
+    low = (np.abs(u) <= 0.5) & fine
+    p = np.full_like(t, c[3])
+    for v in c[2::-1]:
+        p = (p * t + v).astype(np.float32)
+    got = (u * p).astype(np.float32).astype(np.float64)
+    assert (np.abs(got - want)[low] <= 2.0 ** -20 * np.abs(want)[low]).all()

@@ -285,6 +285,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
   const bool split = sp > 1;
   const int j0 = split ? piece * a.split_stages[hi] : 0;
   const int nloc = split ? min(nst, j0 + a.split_stages[hi]) - j0 : nst;
+  // Biased scores grow towards the newest keys, and a maximum that grows rescales O: such a stream
+  // runs from its newest stage to its oldest (a 1024-token chunk at 40000: 339 -> 288 us).
+  const bool newest_first = SC && a.score.slopes != nullptr;
+  auto stage_of = [&](int jj) { return j0 + (newest_first ? nloc - 1 - jj : jj); };
   if (nloc <= 0) {  // nothing of the stream left for this split: an empty partial
     float2* ml = reinterpret_cast<float2*>(a.part_ml) + (size_t)blockIdx.x * 2 * kPfM;
     for (int r = threadIdx.x; r < 2 * kPfM; r += blockDim.x) ml[r] = make_float2(kNegInf, 0.f);
@@ -344,7 +348,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         {
           const int jj = c0 + lane;
           if (jj < nloc) {
-            const int j = j0 + jj;
+            const int j = stage_of(jj);
             int kind[kPfSub], blk[kPfSub], r0[kPfSub], row[kPfSub];
             bool blk_ok = true;
 #pragma unroll
@@ -518,8 +522,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
     for (int c0 = 0; c0 < nloc && c0 < 32 * kCleanWords; c0 += 32) {
       const int jj = c0 + lane;
       const bool in = jj < nloc;
-      const bool c_0 = in && stage_clean(tl, j0 + jj, C, p0, n, w, pql[0], pqh[0]);
-      const bool c_1 = in && stage_clean(tl, j0 + jj, C, p0, n, w, pql[1], pqh[1]);
+      const bool c_0 = in && stage_clean(tl, stage_of(jj), C, p0, n, w, pql[0], pqh[0]);
+      const bool c_1 = in && stage_clean(tl, stage_of(jj), C, p0, n, w, pql[1], pqh[1]);
       const uint32_t b0 = __ballot_sync(0xffffffffu, c_0), b1 = __ballot_sync(0xffffffffu, c_1);
       if (lane == 0) {
         reinterpret_cast<volatile uint32_t*>(s_clean[0])[c0 >> 5] = b0;
@@ -554,7 +558,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
     // runs), so it is kept off the per-stage path
     uint32_t clean_word = 0u;
     for (int jj = 0; jj < nloc; ++jj) {
-      const int j = j0 + jj;  // stage of the stream; jj counts this CTA's stages (barrier phases)
+      const int j = stage_of(jj);  // stage of the stream; jj counts this CTA's stages (barrier phases)
       const int b = jj & 1;
       ok = __all_sync(0xffffffffu, pf_wait(&s_full[x][b], (uint32_t)(jj >> 1) & 1u, abort, a.pv.err));
       if (!ok) break;
@@ -607,8 +611,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
           const float u_max = fmaxf(hi, -lo) * fabsf(a.score.cap_in);
           // No score of the warp reaches the cap (or half of it): a polynomial in x^2 alone, on packed
           // pairs.  Its terms are what a capped stage costs, 20 us each for a chunk of up to 1024 tokens at
-          // a 40000-token context (cap 50, scores to half the cap: 325 us; cap 25, to the cap:
-          // 335 us; past it, both forms: 515 us; uncapped: 226 us).
+          // a 40000-token context (cap 50, scores to half the cap: 330 us; cap 25, to the cap:
+          // 350 us; past it, both forms: 530 us; uncapped: 226 us).
           auto polynomial = [&](auto degree, const float* coef) {
             constexpr int n = decltype(degree)::value;
             auto capped = [&](float2 v) {
@@ -662,12 +666,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
           // immediate operand, and the row's maximum and exponents the rest.
           auto first_key = [&](const PfKeyTile& k) { return (k.kind == 0 ? tl.p_oldest : p0) + k.a; };
           if ((jj & 31) == 0) {  // 32 stages at a time, one per lane
-            const PfKeyTile k0 = key_tile(tl, (j + lane) * kPfSub, C);
+            const int j_lane = max(stage_of(jj + lane), 0);
+            const PfKeyTile k0 = key_tile(tl, j_lane * kPfSub, C);
             run_first = first_key(k0);
             bool run = true;
 #pragma unroll
             for (int u = 0; u < kPfSub; ++u) {
-              const PfKeyTile k = key_tile(tl, (j + lane) * kPfSub + u, C);
+              const PfKeyTile k = key_tile(tl, j_lane * kPfSub + u, C);
               run = run && first_key(k) == run_first + u * kTile && (k.kind != 0 || k.a + kTile <= C);
             }
             run_word = __ballot_sync(0xffffffffu, run);

@@ -72,7 +72,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   constexpr int V = Vec::V;
   constexpr int K = kLayout == kRopeHalf ? V / 2 : kLayout == kRopeInterleaved ? (V >= 4 ? V / 4 : 1) : 1;
   __shared__ float4 s_cs[kRopeRows][32];
-  griddep_launch_dependents();  // a decode launched with early reads may start its schedule and loads
+  // Launched as a programmatic dependent.  A decode that follows with early reads may start its
+  // schedule and loads once the kernels before this one have completed: its caller vouches for what
+  // they wrote, not for less.
+  griddep_wait();
+  griddep_launch_dependents();
 
   const int tiles = (a.n_max + a.rows - 1) / a.rows;
   const int s = (int)blockIdx.x / tiles;
@@ -236,12 +240,26 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
 }
 
+template <typename T, int kLayout>
+cudaError_t launch_one(const RopeArgs& a, unsigned grid, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kRopeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rope_kernel<T, kLayout>, a);
+}
+
 template <typename T>
-void launch_layout(const RopeArgs& a, int layout, unsigned grid, cudaStream_t st) {
+cudaError_t launch_layout(const RopeArgs& a, int layout, unsigned grid, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T);
-  if (layout == HWKV_ROPE_INTERLEAVED) rope_kernel<T, kRopeInterleaved><<<grid, kRopeThreads, 0, st>>>(a);
-  else if (a.rot % (2 * V) == 0) rope_kernel<T, kRopeHalf><<<grid, kRopeThreads, 0, st>>>(a);
-  else rope_kernel<T, kRopeHalfAny><<<grid, kRopeThreads, 0, st>>>(a);
+  if (layout == HWKV_ROPE_INTERLEAVED) return launch_one<T, kRopeInterleaved>(a, grid, st);
+  if (a.rot % (2 * V) == 0) return launch_one<T, kRopeHalf>(a, grid, st);
+  return launch_one<T, kRopeHalfAny>(a, grid, st);
 }
 
 }  // namespace
@@ -251,10 +269,10 @@ int rope_rows(int64_t tokens) { return tokens >= 1024 ? kRopeRows : 1; }
 
 cudaError_t launch_rope(const RopeArgs& a, int layout, bool f32, cudaStream_t st) {
   const int64_t grid = (int64_t)a.num_seqs * ((a.n_max + a.rows - 1) / a.rows);
-  if (f32) launch_layout<float>(a, layout, (unsigned)grid, st);
-  else launch_layout<__nv_bfloat16>(a, layout, (unsigned)grid, st);
+  const cudaError_t e = f32 ? launch_layout<float>(a, layout, (unsigned)grid, st)
+                            : launch_layout<__nv_bfloat16>(a, layout, (unsigned)grid, st);
   count_launches(1);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace hwkv

@@ -217,11 +217,18 @@ class Pool:
             self._check_rows(q, "q")
             if q_out is None:
                 q_out = new(q.shape, dtype=q.dtype, device=q.device)
+            elif q_out is not q:
+                self._check_rows(q_out, "q_out")
         if k is not None:
             if self._check_rows(k, "k") != self.kv_heads:
                 raise ValueError(f"k must hold {self.kv_heads} heads")
             if k_out is None:
                 k_out = new(k.shape, dtype=k.dtype, device=k.device)
+            elif k_out is not k:
+                self._check_rows(k_out, "k_out")
+        for t in (pos,) if n is None else (pos, n):
+            if t.numel() < self.num_seqs or not t.is_contiguous() or t.device != self.buffer.device:
+                raise ValueError(f"positions and row counts must hold {self.num_seqs} values in a row on {self.buffer.device}")
         hwkv_rope(self.handle, table, q, k, pos, n, q_out, k_out, stream)
         return q_out, k_out
 

@@ -87,7 +87,8 @@ struct Geometry {
   std::vector<int32_t> seq_stride;      // [layers] sum_h nblk
   int64_t total_blocks = 0;
   uint64_t block_area = 0;     // bytes of the blocks; the scales of an 8-bit pool follow them
-  uint64_t pool_bytes = 0;
+  uint64_t used_bytes = 0;     // blocks and scales
+  uint64_t pool_bytes = 0;     // the same, rounded up to 16
 };
 
 constexpr double kInvTwoPi = 0.15915494309189533577;
@@ -140,9 +141,9 @@ int plan_geometry(int layers, int kv_heads, int head_dim, int block_size, const 
   }
   g->total_blocks = blocks;
   g->block_area = (uint64_t)blocks * 2u * (uint64_t)block_size * (uint64_t)head_dim * (uint64_t)g->eb;
-  g->pool_bytes = g->block_area;
-  if (dtype == HWKV_E4M3)  // two fp32 scales per 16 slots after the blocks, read in 16-byte pairs
-    g->pool_bytes += ((uint64_t)blocks * (uint64_t)(block_size / 16) * 8u + 15u) & ~uint64_t(15);
+  // two fp32 scales per 16 slots follow the blocks of an 8-bit pool
+  g->used_bytes = g->block_area + (dtype == HWKV_E4M3 ? (uint64_t)blocks * (uint64_t)(block_size / 16) * 8u : 0u);
+  g->pool_bytes = (g->used_bytes + 15u) & ~uint64_t(15);
   return HWKV_OK;
 }
 
@@ -1274,7 +1275,8 @@ int hwkv_seqcalib(int layers, int kv_heads, int head_dim, int block_size, int nu
                   uint64_t budget_bytes, int32_t* out_windows, int32_t* out_choice, uint64_t* out_bytes) {
   if (num_candidates < 1) return fail(HWKV_ERR_INVALID_ARG, "num_candidates must be >= 1");
   if (!candidates || !distortion || !out_windows) return fail(HWKV_ERR_INVALID_ARG, "NULL argument");
-  // every candidate must be a valid window vector; its cost is the one-layer pool footprint
+  // every candidate must be a valid window vector; its cost is the one-layer pool footprint, of
+  // which the whole pool rounds only the sum up to 16 bytes (so a budget counts in units of 16)
   std::vector<uint64_t> cost((size_t)layers * num_candidates);
   for (int l = 0; l < layers; ++l) {
     for (int c = 0; c < num_candidates; ++c) {
@@ -1282,11 +1284,11 @@ int hwkv_seqcalib(int layers, int kv_heads, int head_dim, int block_size, int nu
       Geometry g;
       const int rc = plan_geometry(1, kv_heads, head_dim, block_size, w, num_seqs, dtype, &g);
       if (rc != HWKV_OK) return rc;
-      cost[(size_t)l * num_candidates + c] = g.pool_bytes;
+      cost[(size_t)l * num_candidates + c] = g.used_bytes;
     }
   }
   std::vector<int32_t> chosen((size_t)layers * kv_heads);
-  uint64_t remaining = budget_bytes, total = 0;
+  uint64_t remaining = budget_bytes & ~uint64_t(15), total = 0;
   for (int l = 0; l < layers; ++l) {
     int best = -1;
     double best_d = std::numeric_limits<double>::infinity();
@@ -1309,7 +1311,7 @@ int hwkv_seqcalib(int layers, int kv_heads, int head_dim, int block_size, int nu
     if (out_choice) out_choice[l] = best;
   }
   std::memcpy(out_windows, chosen.data(), sizeof(int32_t) * chosen.size());
-  if (out_bytes) *out_bytes = total;
+  if (out_bytes) *out_bytes = (total + 15u) & ~uint64_t(15);
   return ok();
 }
 

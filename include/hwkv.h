@@ -246,7 +246,8 @@ int hwkv_decode_attn_ex(hwkv_pool_t pool, int layer, const void* q, int q_heads,
  *     s = s - slope[query head] * (position of the query - position of the key).
  * In a decode step the query's position is len - 1, so the newest token's distance is 0.
  *   softcap: finite, 0 (none) or positive, with scale / softcap and softcap * log2(e) finite in
- *            fp32;  slopes_dev: device float [q_heads], finite, or NULL (none). */
+ *            fp32;  slopes_dev: device float [q_heads] or NULL (none), finite, as must be
+ *            slope * log2(e) * distance in fp32 for every distance within a window or chunk. */
 typedef struct hwkv_score {
   float scale;
   float softcap;
@@ -254,8 +255,8 @@ typedef struct hwkv_score {
 } hwkv_score_t;
 
 /* hwkv_decode_attn_ex with such a score, for every pool type and shape; the same workspace, flags
- * and errors.  The capped or biased scores differ from the formula by at most 2^-20 of their size
- * before the softmax (fp32 pools: a few fp32 roundings).  A score with neither cap nor slopes runs
+ * and errors.  The cap is off by at most 2^-20 of the capped score, the difference with the bias by
+ * a few fp32 roundings of the larger term (fp32 pools: the cap likewise).  A score with neither cap nor slopes runs
  * the plain kernels. */
 int hwkv_decode_attn_score(hwkv_pool_t pool, int layer, const void* q, int q_heads, const hwkv_score_t* score,
                            const void* k_new, const void* v_new, const int32_t* lens_dev, void* out, void* workspace,
@@ -415,7 +416,8 @@ typedef double (*hwkv_distortion_fn)(void* user, int layer, const int32_t* windo
  * for each layer the candidate window vector of smallest distortion whose cost fits the
  * remaining budget is chosen (ties: the first such candidate), and its cost is taken off the
  * budget.  The cost of a vector is its exact pool footprint, the bytes hwkv_pool_bytes predicts:
- * num_seqs * sum_h ceil(w_h / block_size) * block_size * head_dim * 2 * eb.
+ * num_seqs * sum_h ceil(w_h / block_size) * block_size * head_dim * 2 * eb, and an 8-bit pool's
+ * scales (rounded up to 16 bytes once, for all layers together).
  *   candidates: host int32 [layers][num_candidates][kv_heads], every window >= 1.
  *   out_windows: host int32 [layers][kv_heads] (may be the windows argument of pool_create);
  *   out_choice: host int32 [layers] chosen candidate index; out_bytes: total pool bytes.

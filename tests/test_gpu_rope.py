@@ -152,7 +152,10 @@ def test_refusals_and_flags():
     for bad in (lambda: pool.rope(table, q.float(), k, pos), lambda: pool.rope(table, q, k[:, :, :1], pos),
                 lambda: pool.rope(table, q, k[:, :2], pos), lambda: pool.rope(table, q, k, pos.long()),
                 lambda: pool.rope(table, q.transpose(1, 2), None, pos), lambda: pool.rope(table, q[:1], None, pos),
-                lambda: pool.rope(table, q, k, pos, q_out=k)):
+                lambda: pool.rope(table, q, k, pos, q_out=k), lambda: pool.rope(table, q, k, pos.cpu()),
+                lambda: pool.rope(table, q, k, pos[:1]), lambda: pool.rope(table, q, k, pos, pos[:1]),
+                lambda: pool.rope(table, q, k, torch.arange(4, dtype=torch.int32, device="cuda")[::2]),
+                lambda: pool.rope(table, q, None, pos, q_out=torch.empty(q.shape, dtype=q.dtype))):
         with pytest.raises(ValueError):
             bad()
 

@@ -8,6 +8,10 @@ Tolerance, per element, with A = sum_p softmax_p |v_p| and T the largest |score|
 * tensor-core paths round the weights to bf16 (2^-8 A more, 8-bit pools to fp16, 2^-11 A; the sum is
   taken of the unrounded weights); bf16 outputs round by 2^-8 of the value;
 * fp32 pools take tanhf (2 units) instead: e = 2^-21 T + 2^-17 S + 2^-22, outputs 2^-23."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -183,6 +187,65 @@ def test_prefill(D, G, bs, windows, pos, n, max_stages, score):
         dec = np64(pool.decode(0, last, scale, tpos + tn, softcap=cap, slopes=slopes if biased else None))
         for s in range(B):
             np.testing.assert_allclose(dec[s], got[s, n[s] - 1], atol=2.0 ** -5, rtol=2.0 ** -6)
+
+
+@pytest.mark.parametrize("cap", [0.0, 6.0, 40.0])
+@pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
+def test_negative_scales_and_slopes(kind, cap):
+    """A negative scale turns the scores around, a negative slope favours the farthest keys; the decode of
+    every pool type, and the chunked prefill of bf16 pools."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    windows, L = [70, 333], 400
+    pool = hw.Pool(1, 2, 64, 16, [windows], 1, TYPES[kind], q_heads=8)
+    k, v = histories(gen, 1, 2, L, 64, pool.io_dtype)
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    q = (torch.randn((1, 8, 64), generator=gen, device="cuda") * 2).to(pool.io_dtype)
+    slopes = torch.tensor([(-0.5) ** g for g in range(8)], device="cuda")
+    for scale in (-0.125, 0.125):
+        pool.materialize(0, k, v, lens)
+        outs = [pool.decode(0, q, scale, lens, softcap=cap, slopes=slopes)]
+        if kind == "bf16":
+            n = 37
+            pool.materialize(0, k, v, lens - n)
+            kn, vn = (t[:, :, L - n:].transpose(1, 2).contiguous() for t in (k, v))
+            chunk = q[:, None].expand(1, n, 8, 64).contiguous()
+            outs.append(pool.prefill(0, chunk, scale, kn, vn, lens - n, lens * 0 + n, softcap=cap, slopes=slopes)[:, n - 1])
+        for h, w in enumerate(windows):
+            p = np.arange(L - w, L)
+            rk, rv = np64(k)[0, h, p], np64(v)[0, h, p]
+            if kind == "e4m3":
+                ring = Ring8(w, 16, 64)
+                ring.materialize(np64(k)[0, h], np64(v)[0, h], L)
+                p, rk, rv = ring.resident(L)
+            for g in range(4 * h, 4 * h + 4):
+                ref, tol = tolerance(kind, np64(q)[0, g], rk, rv, scale, L - 1 - p, cap, float(slopes[g]))
+                for i, out in enumerate(outs):
+                    got = np64(out)[0, g]
+                    assert (np.abs(got - ref) <= tol).all(), (scale, g, i, float((np.abs(got - ref) / tol).max()))
+    assert pool.check_device_errors() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
+def test_first_call_of_a_process_captured(kind):
+    """A step captured before any of its kernels ran in the process."""
+    code = f"""
+import torch, head_budgeted_kv_gb300 as hw
+from head_budgeted_kv_gb300.graph import DecodeStepGraph
+pool = hw.Pool(2, 2, 64, 16, [[64, 30], [200, 16]], 1, {TYPES[kind]}, q_heads=8)
+pos = torch.tensor([0], dtype=torch.int32, device="cuda")
+kw = dict(softcap=10.0, slopes=torch.ones(8, device="cuda"))
+step = DecodeStepGraph(pool, 0.2, 8, pos, rope=hw.rope_table(64), **kw)
+q, k, v = (torch.randn(s, device="cuda").to(pool.io_dtype) for s in (step.q.shape, step.k_new.shape, step.v_new.shape))
+step.q.copy_(q), step.k_new.copy_(k), step.v_new.copy_(v)
+step.replay()
+for l in range(2):
+    qr, kr = pool.rope(hw.rope_table(64), q[l], k[l], pos)
+    assert torch.equal(pool.append_decode(l, qr, 0.2, kr, v[l], pos, **kw), step.out[l])
+assert pool.check_device_errors() == 0 and step.out.abs().sum() > 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])

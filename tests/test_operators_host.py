@@ -45,6 +45,19 @@ def test_seqcalib_budgets_8_bit_pools(lib):
     assert choice.tolist() == [0]
 
 
+def test_seqcalib_of_8_bit_layers_predicts_the_pool(lib):
+    """Scales of odd block counts: layers chosen together cost what one pool of them takes."""
+    windows = [[16], [33], [1], [80]]
+    cand = np.array([[w] for w in windows], dtype=np.int32)
+    want = _pool_bytes(4, 1, 64, 16, windows, 1, "e4m3")
+    w, _, nbytes = binding.hwkv_seqcalib(cand, np.ones((4, 1)), want, 64, 16, 1, "e4m3")
+    assert nbytes == want and w.tolist() == windows
+    assert binding.hwkv_seqcalib(cand, np.ones((4, 1)), want + 15, 64, 16, 1, "e4m3")[2] == want
+    with pytest.raises(binding.HwkvError) as e:
+        binding.hwkv_seqcalib(cand, np.ones((4, 1)), want - 1, 64, 16, 1, "e4m3")
+    assert e.value.status == binding.HWKV_ERR_BUDGET
+
+
 def test_reference_codes_are_torchs_codes():
     """The reference's rounding to e4m3 is the nearest one with ties to even, as torch's cast has it."""
     gen = torch.Generator().manual_seed(0)

@@ -918,7 +918,6 @@ int hwkv_rope(hwkv_pool_t p, const hwkv_rope_t* rope, const hwkv_rows_t* q, int 
   a.head_dim = g.head_dim;
   a.rot = rope->rot_dim;
   a.copy = copy ? 1 : 0;
-  a.rows = rope_rows((int64_t)g.num_seqs * n_max);
   a.magnitude = (float)rope->magnitude;
   for (int i = 0; i < rope->rot_dim / 2; ++i) {
     // the fraction of a turn per position, in [0, 1), as a 64-bit fraction

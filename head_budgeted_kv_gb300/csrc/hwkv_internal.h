@@ -142,7 +142,7 @@ struct RopeArgs {
   int32_t q_heads, k_heads;  // 0: that tensor is not given
   int32_t head_dim, rot;   // the first rot dims of a row turn
   int32_t copy;            // 1: the other dims are written too (not in place)
-  int32_t rows;            // rows of one CTA
+  int32_t rows;            // rows of one CTA (set by launch_rope)
   float magnitude;
   uint64_t turns[64];      // turns per position of each pair, times 2^64
 };
@@ -183,8 +183,7 @@ int decode_tc_pad_index(int group);  // 0, 1, 2 for 4, 8, 16 columns
 cudaError_t launch_decode_simt(const DecodeArgs& a, int dtype, int items, cudaStream_t st);
 cudaError_t launch_combine(const DecodeArgs& a, int dtype, cudaStream_t st);
 // rotary positions (hwkv_rope.cu)
-int rope_rows(int64_t tokens);  // rows of one CTA when `tokens` rows are turned in all
-cudaError_t launch_rope(const RopeArgs& a, int layout, bool f32, cudaStream_t st);
+cudaError_t launch_rope(RopeArgs a, int layout, bool f32, cudaStream_t st);  // sets a.rows
 // chunked prefill (hwkv_prefill.cu): attention, then the chunk appended to the rings
 int prefill_tokens_per_cta(int group);  // chunk tokens one CTA answers (two query tiles)
 int prefill_tile_tokens(int group);     // chunk tokens of one 128-row query tile

@@ -13,17 +13,32 @@
 // fp32 as half turns in [-1, 1) and sincospif() does the rest: 2^-23 rad at any position.  fp64
 // would give the same at this GPU's far lower fp64 rate.
 //
-// A CTA takes up to T rows (tokens) of one sequence: their cosines and sines are computed once
-// into shared memory, then each thread turns units of 16-byte vectors across all query and key
-// heads, kAhead units' loads in flight.  The work is reading and writing each row once.
+// A CTA takes a few rows (tokens) of one sequence: their cosines and sines are computed once into
+// shared memory, then each thread turns units of 16-byte vectors across all query and key heads,
+// kAhead units' loads in flight.
+//
+// Bound: reading and writing each row once, HBM for long chunks (4 sequences of 2048 rows, 32 + 8
+// heads of 128 in bf16: 126 MB in 21.2 us, 0.88 of the measured copy rate) and the launch for short
+// ones (one row: 3.1 us).
+#include <algorithm>
+
 #include "hwkv_device.cuh"
 
 namespace hwkv {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeAhead = 2;
 constexpr int kRopeRows = 4;  // most rows of a CTA
+
+// How the rows are shared out.  A call that leaves SMs idle wants short work per thread (kWide: 256
+// threads, 2 units ahead); one that fills them wants many small CTAs whose angles and loads overlap
+// (128 threads, 3 ahead).  One row 3.1 us wide, 3.5 narrow; 512 rows of 40 heads 3.9 and 4.0; 1024
+// 6.0 and 4.8; 2048 9.6 and 7.8.
+constexpr int64_t kWideTokens = 512;
+template <bool kWide>
+struct RopeShape {
+  static constexpr int kThreads = kWide ? 256 : 128;
+  static constexpr int kAhead = kWide ? 2 : 3;
+};
 
 template <typename T>
 struct RopeVec {  // a 16-byte vector as fp32
@@ -66,8 +81,11 @@ enum { kRopeHalf = 0, kRopeInterleaved = 1, kRopeHalfAny = 2 };
 // vector past rot); kRopeInterleaved: a unit is one vector; kRopeHalfAny: a unit is one vector
 // whose partners are read one by one, all loads of a pass before its stores (a barrier between,
 // since a row may be turned in place).
-template <typename T, int kLayout>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+template <typename T, int kLayout, bool kWide>
+__global__ void __launch_bounds__(RopeShape<kWide>::kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int kRopeThreads = RopeShape<kWide>::kThreads, kRopeAhead = RopeShape<kWide>::kAhead;
+  // kRopeHalfAny: a pass holds whole heads (of 8, 16 or 32 vectors), so no later one reads what it turned
+  static_assert(kRopeThreads * kRopeAhead % 32 == 0, "a pass holds whole heads");
   using Vec = RopeVec<T>;
   constexpr int V = Vec::V;
   constexpr int K = kLayout == kRopeHalf ? V / 2 : kLayout == kRopeInterleaved ? (V >= 4 ? V / 4 : 1) : 1;
@@ -240,18 +258,24 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
 }
 
-template <typename T, int kLayout>
-cudaError_t launch_one(const RopeArgs& a, unsigned grid, cudaStream_t st) {
+template <typename T, int kLayout, bool kWide>
+cudaError_t launch_shape(const RopeArgs& a, unsigned grid, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kRopeThreads);
+  cfg.blockDim = dim3(RopeShape<kWide>::kThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_kernel<T, kLayout>, a);
+  return cudaLaunchKernelEx(&cfg, rope_kernel<T, kLayout, kWide>, a);
+}
+
+template <typename T, int kLayout>
+cudaError_t launch_one(const RopeArgs& a, unsigned grid, cudaStream_t st) {
+  return (int64_t)a.num_seqs * a.n_max <= kWideTokens ? launch_shape<T, kLayout, true>(a, grid, st)
+                                                      : launch_shape<T, kLayout, false>(a, grid, st);
 }
 
 template <typename T>
@@ -264,10 +288,14 @@ cudaError_t launch_layout(const RopeArgs& a, int layout, unsigned grid, cudaStre
 
 }  // namespace
 
-// rows of a CTA: one while that fills the SMs at most a few times over, else kRopeRows
-int rope_rows(int64_t tokens) { return tokens >= 1024 ? kRopeRows : 1; }
-
-cudaError_t launch_rope(const RopeArgs& a, int layout, bool f32, cudaStream_t st) {
+cudaError_t launch_rope(RopeArgs a, int layout, bool f32, cudaStream_t st) {
+  // Rows of a CTA: enough vectors for its threads (5 heads of 64 in bf16, 20 units to a row, 4096 rows:
+  // 1 row 7.4 us, 4 rows 4.6), and two where CTAs are many (40 heads of 128: 4096 rows 13.6 us with 1,
+  // 13.9 with 2; 8192 rows 22.2 and 21.2).
+  const int64_t tokens = (int64_t)a.num_seqs * a.n_max;
+  const int vectors = (a.q_heads + a.k_heads) * a.head_dim * (f32 ? 4 : 2) / 16;
+  const int units = layout == HWKV_ROPE_INTERLEAVED ? vectors : vectors / 2;
+  a.rows = std::min(kRopeRows, std::max(tokens >= 8192 ? 2 : 1, 512 / units));
   const int64_t grid = (int64_t)a.num_seqs * ((a.n_max + a.rows - 1) / a.rows);
   const cudaError_t e = f32 ? launch_layout<float>(a, layout, (unsigned)grid, st)
                             : launch_layout<__nv_bfloat16>(a, layout, (unsigned)grid, st);

@@ -86,6 +86,28 @@ def test_against_the_formula(B, n, H, G, D, rot, dtype, layout, in_place):
     assert pool.check_device_errors() == 0
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("B,n,H,G,D,rot", [(2, 4200, 2, 4, 64, 64), (1, 700, 3, 1, 128, 20), (3, 171, 8, 4, 128, 128),
+                                           (1, 9001, 1, 1, 64, 34), (2, 1111, 5, 3, 64, 32)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_long_chunks_are_their_rows(B, n, H, G, D, rot, dtype, layout):
+    """However a call shares its rows out, a row's bits are those of a short call."""
+    pool = make_pool(B, H, D, dtype)
+    table = hw.rope_table(D, rot, 10000.0, layout)
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    q = torch.randn((B, n, G * H, D), generator=gen, device="cuda").to(dtype)
+    k = torch.randn((B, n, H, D), generator=gen, device="cuda").to(dtype)
+    pos = torch.arange(B, dtype=torch.int32, device="cuda") * 1000 + 7
+    whole = pool.rope(table, q, k, pos)
+    part = [(pool.rope(table, q[:, i:i + 160], k[:, i:i + 160], pos + i)) for i in range(0, n, 160)]
+    assert torch.equal(whole[0], torch.cat([p[0] for p in part], 1))
+    assert torch.equal(whole[1], torch.cat([p[1] for p in part], 1))
+    qi, ki = q.clone(), k.clone()
+    pool.rope(table, qi, ki, pos, q_out=qi, k_out=ki)
+    assert torch.equal(qi, whole[0]) and torch.equal(ki, whole[1])
+    assert pool.check_device_errors() == 0
+
+
 @pytest.mark.parametrize("pos", [0, 1, 65535, 164864, 2 ** 24 - 2, 2 ** 31 - 9])
 def test_far_positions(pos):
     """The angle keeps its accuracy; beyond 2^24 the frequency's own 64-bit rounding shows (2^-52 of

@@ -1241,8 +1241,7 @@ int hwkv_prefill_attn_score(hwkv_pool_t p, int layer, const void* q, int q_heads
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   HWKV_CUDA_TRY(launch_prefill(a, &p->tmap, &p->stage_map, &kmap, &vmap, &kmap64, &vmap64, &qmap, st),
                 "prefill launch");
-  if (need > 0) HWKV_CUDA_TRY(launch_prefill_combine(a, st), "prefill combine launch");
-  HWKV_CUDA_TRY(launch_chunk_append(a, std::min(n_max, max_c), st), "chunk append launch");
+  HWKV_CUDA_TRY(launch_prefill_finish(a, need > 0, std::min(n_max, max_c), st), "prefill finish launch");
   return ok();
 }
 

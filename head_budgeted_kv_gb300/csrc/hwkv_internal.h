@@ -192,9 +192,9 @@ int prefill_tile_tokens(int group);     // chunk tokens of one 128-row query til
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap* pool_map, const CUtensorMap* stage_map,
                            const CUtensorMap* knew_map, const CUtensorMap* vnew_map, const CUtensorMap* knew64_map,
                            const CUtensorMap* vnew64_map, const CUtensorMap* q_map, cudaStream_t st);
-cudaError_t launch_chunk_append(const PrefillArgs& a, int max_rows, cudaStream_t st);
-// merge of the partials of split key streams (after launch_prefill)
-cudaError_t launch_prefill_combine(const PrefillArgs& a, cudaStream_t st);
+// after launch_prefill: merge of the partials of split key streams, if any, and the append of the
+// chunk, at most max_rows of its rows per (seq, head)
+cudaError_t launch_prefill_finish(const PrefillArgs& a, bool combine, int max_rows, cudaStream_t st);
 // upper bound on the 64-key stages of one prefill CTA's key stream for a head
 int prefill_max_stages(int window, int ring_capacity, int group, int n_max);
 // the 64-key stages the tile pair starting at chunk row qa streams when the context before the

@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
   __shared__ uint32_t s_clean[2][kCleanWords];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_launch_dependents();  // the finish kernel waits for this one's end before it does anything
   if (threadIdx.x == 0) {  // the TMA descriptors, ahead of their first use
     prefetch_tensormap(&q_map);
     prefetch_tensormap(&stage_map);
@@ -843,16 +844,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
 // Appends the chunk to the rings: chunk row i of (seq, head) is position p0 + i and goes to
 // slot (p0 + i) mod C; only the last min(C, n) rows are written (the earlier ones would be
 // overwritten by later rows of the same chunk), so every slot is written at most once.
-// grid.x: groups of 8 rows, grid.y: seq * H + head; one warp per row.
-__global__ void __launch_bounds__(256) chunk_append_kernel(const __grid_constant__ PrefillArgs a, int row_bytes) {
+// A CTA takes 8 rows (group `rows8` of them) of one (seq, head); one warp per row.
+__device__ __forceinline__ void chunk_append(const PrefillArgs& a, int row_bytes, int rows8, int sh) {
   const int H = a.pv.kv_heads;
-  const int s = blockIdx.y / H, h = blockIdx.y - (blockIdx.y / H) * H;
+  const int s = sh / H, h = sh - s * H;
   const int p0 = a.pos0[s], n = a.nlen[s];
   if (p0 < 0 || n < 0 || n > a.n_max) return;  // flagged by the attention kernel
   const int bs = a.pv.block_size;
   const int C = (a.g.nblk_prefix[h + 1] - a.g.nblk_prefix[h]) * bs;
   const int first = n > C ? n - C : 0;
-  const int i = first + blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int i = first + rows8 * 8 + (threadIdx.x >> 5);
   if (i >= n) return;
   const int lane = threadIdx.x & 31;
   const uint32_t slot = (uint32_t)(p0 + i) % (uint32_t)C;
@@ -894,12 +895,12 @@ struct CombineVec<2> {
 };
 
 template <int D>
-__global__ void __launch_bounds__(256) prefill_combine_kernel(const __grid_constant__ PrefillArgs a) {
+__device__ __forceinline__ void combine_splits(const PrefillArgs& a, int block) {
   constexpr int kC = D / 32;  // columns per lane
   constexpr int kSlabs = 2 * kPfM / kCombineRows;
   using Vec = typename CombineVec<kC>::T;
   const int per_head = a.pv.num_seqs * a.q_tiles;
-  const int unit = blockIdx.x / kSlabs, slab = blockIdx.x - unit * kSlabs;
+  const int unit = block / kSlabs, slab = block - unit * kSlabs;
   const int hi = unit / per_head;
   const int item = unit - hi * per_head;
   const int sp = a.splits[hi];
@@ -962,6 +963,22 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const __grid_const
   }
 }
 
+// What follows the attention, in one launch: the merge of split streams (the first
+// `combine_blocks` CTAs) and the chunk's append (the others), which need each other not.
+// Launched as a programmatic dependent: the CTAs are in place when the attention ends.
+template <int D>
+__global__ void __launch_bounds__(256) prefill_finish_kernel(const __grid_constant__ PrefillArgs a, int combine_blocks,
+                                                             int append_groups) {
+  griddep_wait();
+  const int block = (int)blockIdx.x;
+  if (block < combine_blocks) {
+    combine_splits<D>(a, block);
+  } else {
+    const int sh = (block - combine_blocks) / append_groups;
+    chunk_append(a, D * 2, block - combine_blocks - sh * append_groups, sh);
+  }
+}
+
 template <int D, bool SC>
 cudaError_t launch_pf(const PrefillArgs& a, const CUtensorMap* pm, const CUtensorMap* sm, const CUtensorMap* km,
                       const CUtensorMap* vm, const CUtensorMap* km64, const CUtensorMap* vm64, const CUtensorMap* qm,
@@ -1018,26 +1035,27 @@ cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap* pool_map, co
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_prefill_combine(const PrefillArgs& a, cudaStream_t st) {
+cudaError_t launch_prefill_finish(const PrefillArgs& a, bool combine, int max_rows, cudaStream_t st) {
   // CTAs for the work-order positions up to the last split head (the others return at once)
   int split_heads = 0;
-  for (int i = 0; i < a.pv.kv_heads; ++i)
+  for (int i = 0; combine && i < a.pv.kv_heads; ++i)
     if (a.splits[i] > 1) split_heads = i + 1;
-  const int blocks = split_heads * a.pv.num_seqs * a.q_tiles * (2 * kPfM / kCombineRows);
-  if (blocks == 0) return cudaSuccess;
-  if (a.pv.head_dim == 128) prefill_combine_kernel<128><<<blocks, 256, 0, st>>>(a);
-  else if (a.pv.head_dim == 64) prefill_combine_kernel<64><<<blocks, 256, 0, st>>>(a);
-  else return cudaErrorInvalidValue;
+  const int combine_blocks = split_heads * a.pv.num_seqs * a.q_tiles * (2 * kPfM / kCombineRows);
+  const int append_groups = (max_rows + 7) / 8;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(combine_blocks + (int64_t)append_groups * a.pv.num_seqs * a.pv.kv_heads));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto* kernel = a.pv.head_dim == 128 ? prefill_finish_kernel<128> : prefill_finish_kernel<64>;
+  if (a.pv.head_dim != 128 && a.pv.head_dim != 64) return cudaErrorInvalidValue;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, combine_blocks, append_groups);
   count_launches(1);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_chunk_append(const PrefillArgs& a, int max_rows, cudaStream_t st) {
-  const int row_bytes = a.pv.head_dim * 2;
-  const dim3 grid((unsigned)((max_rows + 7) / 8), (unsigned)(a.pv.num_seqs * a.pv.kv_heads));
-  chunk_append_kernel<<<grid, 256, 0, st>>>(a, row_bytes);
-  count_launches(1);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace hwkv

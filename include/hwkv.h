@@ -300,8 +300,8 @@ int hwkv_decode_attn_noalloc(hwkv_pool_t pool, int layer, const void* q, int q_h
  *   a smaller size runs one CTA per stream (same results up to rounding, slower for long windows
  *   at small batch).  Contents need no initialisation and are clobbered.
  * Needs a bf16 pool with block_size % 16 == 0 and q_heads = G * kv_heads with G <= 16
- * (HWKV_ERR_UNSUPPORTED otherwise).  Two or three kernels on `stream` (attention, the merge of
- * split streams, the append). */
+ * (HWKV_ERR_UNSUPPORTED otherwise).  Two kernels on `stream`: the attention, then the merge of
+ * split streams together with the append. */
 int hwkv_prefill_attn(hwkv_pool_t pool, int layer, const void* q, int q_heads, float scale, const void* k_new,
                       const void* v_new, int n_max, const int32_t* pos_dev, const int32_t* n_dev, void* out,
                       void* workspace, uint64_t workspace_bytes, void* stream);

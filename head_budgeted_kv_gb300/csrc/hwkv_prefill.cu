@@ -598,12 +598,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       float row_max = 0.f;  // SC: the row's maximum, when have_max
       bool have_max = false;
       if constexpr (SC) {
-        if (!clean) {  // what is masked does not decide how the others are computed
+        if (!clean) {
           visible();
+          if (a.score.capped) {  // what is masked does not decide how the others are capped
 #pragma unroll
-          for (int u = 0; u < kPfSub; ++u)
+            for (int u = 0; u < kPfSub; ++u)
 #pragma unroll
-            for (int i = 0; i < kTile; ++i) sv[u * kTile + i] = (vis[u] >> i) & 1u ? sv[u * kTile + i] : 0.f;
+              for (int i = 0; i < kTile; ++i) sv[u * kTile + i] = (vis[u] >> i) & 1u ? sv[u * kTile + i] : 0.f;
+          }
         }
         const float2 sl = make_float2(a.scale_log2, a.scale_log2);
         if (a.score.capped) {
@@ -965,18 +967,23 @@ __device__ __forceinline__ void combine_splits(const PrefillArgs& a, int block) 
 
 // What follows the attention, in one launch: the merge of split streams (the first
 // `combine_blocks` CTAs) and the chunk's append (the others), which need each other not.
-// Launched as a programmatic dependent: the CTAs are in place when the attention ends.
-template <int D>
-__global__ void __launch_bounds__(256) prefill_finish_kernel(const __grid_constant__ PrefillArgs a, int combine_blocks,
-                                                             int append_groups) {
+// Launched as a programmatic dependent: the CTAs are in place when the attention ends.  Without a
+// merge the append has an instance of its own, with the registers for eight CTAs per SM.  (Three per
+// SM for the merge: held to the registers of four, a 1024-token chunk at 40000 took 231 us, not 224.)
+template <int D, bool kCombine>
+__global__ void __launch_bounds__(256, kCombine ? 3 : 8)
+    prefill_finish_kernel(const __grid_constant__ PrefillArgs a, int combine_blocks, int append_groups) {
   griddep_wait();
-  const int block = (int)blockIdx.x;
-  if (block < combine_blocks) {
-    combine_splits<D>(a, block);
-  } else {
-    const int sh = (block - combine_blocks) / append_groups;
-    chunk_append(a, D * 2, block - combine_blocks - sh * append_groups, sh);
+  int block = (int)blockIdx.x;
+  if constexpr (kCombine) {
+    if (block < combine_blocks) {
+      combine_splits<D>(a, block);
+      return;
+    }
+    block -= combine_blocks;
   }
+  const int sh = block / append_groups;
+  chunk_append(a, D * 2, block - sh * append_groups, sh);
 }
 
 template <int D, bool SC>
@@ -1051,7 +1058,8 @@ cudaError_t launch_prefill_finish(const PrefillArgs& a, bool combine, int max_ro
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto* kernel = a.pv.head_dim == 128 ? prefill_finish_kernel<128> : prefill_finish_kernel<64>;
+  auto* kernel = a.pv.head_dim == 128 ? (combine_blocks > 0 ? prefill_finish_kernel<128, true> : prefill_finish_kernel<128, false>)
+                                      : (combine_blocks > 0 ? prefill_finish_kernel<64, true> : prefill_finish_kernel<64, false>);
   if (a.pv.head_dim != 128 && a.pv.head_dim != 64) return cudaErrorInvalidValue;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, combine_blocks, append_groups);
   count_launches(1);

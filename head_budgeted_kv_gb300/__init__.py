@@ -74,6 +74,7 @@ class Pool:
         self.nbytes = hwkv_pool_bytes(layers, kv_heads, head_dim, block_size, windows, num_seqs, dtype)
         device = torch.device(device or "cuda")
         self.buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self._device_index = self.buffer.get_device()
         self.handle = hwkv_pool_create(layers, kv_heads, head_dim, block_size, windows, num_seqs, dtype,
                                        self.buffer, stream)
         _, total, block_bytes = hwkv_pool_geometry(self.handle)
@@ -217,28 +218,29 @@ class Pool:
             self._check_rows(q, "q")
             if q_out is None:
                 q_out = new(q.shape, dtype=q.dtype, device=q.device)
-            elif q_out is not q:
-                self._check_rows(q_out, "q_out")
         if k is not None:
             if self._check_rows(k, "k") != self.kv_heads:
                 raise ValueError(f"k must hold {self.kv_heads} heads")
             if k_out is None:
                 k_out = new(k.shape, dtype=k.dtype, device=k.device)
-            elif k_out is not k:
-                self._check_rows(k_out, "k_out")
-        for t in (pos,) if n is None else (pos, n):
-            if t.numel() < self.num_seqs or not t.is_contiguous() or t.device != self.buffer.device:
-                raise ValueError(f"positions and row counts must hold {self.num_seqs} values in a row on {self.buffer.device}")
+        at = self._device_index
+        if (q_out is not None and q_out.get_device() != at) or (k_out is not None and k_out.get_device() != at):
+            raise ValueError(f"outputs must lie on {self.buffer.device}")
+        if not self._is_counts(pos) or not (n is None or self._is_counts(n)):
+            raise ValueError(f"positions and row counts must hold {self.num_seqs} values in a row on {self.buffer.device}")
         hwkv_rope(self.handle, table, q, k, pos, n, q_out, k_out, stream)
         return q_out, k_out
 
     def _check_rows(self, t, name) -> int:
         shape = t.shape
         if (t.dtype != self.io_dtype or len(shape) < 3 or shape[0] != self.num_seqs or shape[-1] != self.head_dim
-                or t.device != self.buffer.device):
+                or t.get_device() != self._device_index):
             raise ValueError(f"{name} must hold {self.io_dtype} rows of head_dim {self.head_dim} for "
                              f"{self.num_seqs} sequences on {self.buffer.device}")
         return shape[-2]
+
+    def _is_counts(self, t) -> bool:
+        return t.get_device() == self._device_index and t.numel() >= self.num_seqs and t.is_contiguous()
 
     def check_device_errors(self, stream=None) -> int:
         return hwkv_check_device_errors(self.handle, stream)

@@ -284,6 +284,59 @@ def test_captured_step(kind):
     assert torch.equal(results[0], results[1])
 
 
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("max_stages", [0, 4])
+def test_captured_prefill(softcap, max_stages):
+    """Chunks captured one after another, turned and attended, replayed on new inputs and positions, give the
+    bits of eager calls and the same rings (max_stages 4: split streams, merged in the finish launch)."""
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    table = hw.rope_table(64)
+
+    def make():
+        pool = hw.Pool(2, 2, 64, 16, [[64, 700], [30, 2000]], 2, torch.bfloat16, q_heads=8)
+        pool.set_prefill_config(max_stages)
+        return pool
+
+    shape_q, shape_k = (2, 90, 8, 64), (2, 90, 2, 64)
+    static = [torch.zeros(s, device="cuda").bfloat16() for s in (shape_q, shape_k, shape_k)]
+    pos = torch.zeros(2, dtype=torch.int32, device="cuda")
+    n = torch.tensor([90, 41], dtype=torch.int32, device="cuda")
+    outs = [torch.zeros(shape_q, device="cuda").bfloat16() for _ in range(2)]
+    captured, eager = make(), make()
+
+    def chunk(pool, q, k, v, p, into=None):
+        res = []
+        for l in range(2):
+            qr, kr = pool.rope(table, q, k, p, n, q_out=turned[0], k_out=turned[1])
+            res.append(pool.prefill(l, qr, 0.2, kr, v, p, n, out=into[l] if into else torch.zeros_like(q),
+                                    softcap=softcap))
+        return res
+
+    turned = [torch.zeros(s, device="cuda").bfloat16() for s in (shape_q, shape_k)]
+    chunk(captured, *static, pos, outs)  # sizes the workspace; position 0 is stored again below
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chunk(captured, *static, pos, outs)
+    at = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for _ in range(12):
+        new = [torch.randn(s.shape, generator=gen, device="cuda").bfloat16() for s in static]
+        for t, x in zip(static, new):
+            t.copy_(x)
+        pos.copy_(at)
+        graph.replay()
+        got = [o.clone() for o in outs]
+        want = chunk(eager, *new, at)
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1, :41], b[1, :41])
+        at = at + n
+    # every slot that holds a position of the sequences
+    assert captured.check_device_errors() == 0 and eager.check_device_errors() == 0
+    last = torch.randn((2, 8, 64), generator=gen, device="cuda").bfloat16()
+    for l in range(2):
+        assert torch.equal(captured.decode(l, last, 0.2, at), eager.decode(l, last, 0.2, at))
+
+
 def test_refusals():
     pool = hw.Pool(1, 2, 64, 16, [[64, 200]], 1, torch.bfloat16, q_heads=4)
     q = torch.zeros((1, 4, 64), device="cuda").bfloat16()

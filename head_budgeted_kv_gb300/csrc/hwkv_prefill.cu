@@ -614,8 +614,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
           const float u_max = fmaxf(hi, -lo) * fabsf(a.score.cap_in);
           // No score of the warp reaches the cap (or half of it): a polynomial in x^2 alone, on packed
           // pairs.  Its terms are what a capped stage costs, 20 us each for a chunk of up to 1024 tokens at
-          // a 40000-token context (cap 50, scores to half the cap: 330 us; cap 25, to the cap:
-          // 350 us; past it, both forms: 530 us; uncapped: 226 us).
+          // a 40000-token context (cap 50, scores to half the cap: 330 us; cap 20, to the cap: 376 us; past
+          // it, both forms: 530 us; uncapped: 224 us).  Scores that straddle the cap cost most (cap 12: 644
+          // us): the warps of an SM then fetch different instructions.
           auto polynomial = [&](auto degree, const float* coef) {
             constexpr int n = decltype(degree)::value;
             auto capped = [&](float2 v) {

@@ -189,8 +189,13 @@ __device__ __forceinline__ float tree64(const float (&v)[kPfKeys], Op op) {
   return op(op(t2[0], t2[1], t2[2]), op(t2[3], t2[4], t2[5]), op(t2[6], t2[7], t2[7]));
 }
 
-// SC: scores are capped or biased by distance, in registers between the two products.
-template <int D, bool SC>
+// What is done to the scores, in registers between the two products: nothing, capped, biased by
+// distance, both.  An instance each, since the softmax warps wait for instructions (with one
+// scored instance for all a 1024-token chunk at 40000 took 330 us capped, 275 biased and 370 both;
+// with these 296, 241 and 342).
+enum { kPlain = 0, kCap = 1, kBias = 2 };
+
+template <int D, int SC>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap pool_map,
                                                                const __grid_constant__ CUtensorMap stage_map,
                                                                const __grid_constant__ CUtensorMap knew_map,
@@ -288,7 +293,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
   const int nloc = split ? min(nst, j0 + a.split_stages[hi]) - j0 : nst;
   // Biased scores grow towards the newest keys, and a maximum that grows rescales O: such a stream
   // runs from its newest stage to its oldest (a 1024-token chunk at 40000: 339 -> 288 us).
-  const bool newest_first = SC && a.score.slopes != nullptr;
+  constexpr bool newest_first = (SC & kBias) != 0;
   auto stage_of = [&](int jj) { return j0 + (newest_first ? nloc - 1 - jj : jj); };
   if (nloc <= 0) {  // nothing of the stream left for this split: an empty partial
     float2* ml = reinterpret_cast<float2*>(a.part_ml) + (size_t)blockIdx.x * 2 * kPfM;
@@ -543,9 +548,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
     const uint32_t colO = Cfg::kColO + x * D;
     // capped scores are in log2 units when they meet the softmax; biased ones alone stay raw, the slope
     // divided by the scale, unless that is too small or negative
-    const bool raw_bias = SC && !a.score.capped && a.scale_log2 > 0x1p-40f;
+    const bool raw_bias = SC == kBias && a.scale_log2 > 0x1p-40f;
     const float sl2 = SC && !raw_bias ? 1.f : a.scale_log2;
-    const float slope = SC ? slope_log2(a.score, h * G + r % G) / sl2 : 0.f;  // in units of sl2
+    const float slope = (SC & kBias) ? slope_log2(a.score, h * G + r % G) / sl2 : 0.f;  // in units of sl2
     uint32_t run_word = 0u;  // SC: bit i: stage i of the next 32 holds 64 consecutive positions ...
     int run_first = 0;       // ... and, in lane i, its first key's position
     // with a positive scale the row maximum is taken on raw scores and scale-and-subtract is
@@ -600,7 +605,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       if constexpr (SC) {
         if (!clean) {
           visible();
-          if (a.score.capped) {  // what is masked does not decide how the others are capped
+          if constexpr ((SC & kCap) != 0) {  // what is masked does not decide how the others are capped
 #pragma unroll
             for (int u = 0; u < kPfSub; ++u)
 #pragma unroll
@@ -608,15 +613,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
           }
         }
         const float2 sl = make_float2(a.scale_log2, a.scale_log2);
-        if (a.score.capped) {
+        if constexpr ((SC & kCap) != 0) {
           const float hi = tree64(sv, [](float p, float q, float r) { return fmax3(p, q, r); });
           const float lo = tree64(sv, [](float p, float q, float r) { return fmin3(p, q, r); });
           const float u_max = fmaxf(hi, -lo) * fabsf(a.score.cap_in);
           // No score of the warp reaches the cap (or half of it): a polynomial in x^2 alone, on packed
           // pairs.  Its terms are what a capped stage costs, 20 us each for a chunk of up to 1024 tokens at
-          // a 40000-token context (cap 50, scores to half the cap: 330 us; cap 20, to the cap: 376 us; past
-          // it, both forms: 530 us; uncapped: 224 us).  Scores that straddle the cap cost most (cap 12: 644
-          // us): the warps of an SM then fetch different instructions.
+          // a 40000-token context (cap 50, scores to half the cap: 296 us; cap 20, to the cap: 327 us; past
+          // it, both forms: 488 us; uncapped: 224 us; without the shorter polynomial 349 and 348).  Scores
+          // that straddle the cap cost most (cap 12: 551 us): the warps of an SM then fetch different
+          // instructions.
           auto polynomial = [&](auto degree, const float* coef) {
             constexpr int n = decltype(degree)::value;
             auto capped = [&](float2 v) {
@@ -633,7 +639,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
               sv[c + 1] = y.y;
             }
             // the cap keeps the order, so a clean stage's maximum is that of its largest raw score
-            if (clean && a.score.slopes == nullptr) {
+            if (clean && SC == kCap) {
               const float top = a.scale_log2 > 0.f ? hi : lo;
               row_max = capped(make_float2(top, top)).x;
               have_max = true;
@@ -665,7 +671,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             sv[c + 1] = y.y;
           }
         }
-        if (a.score.slopes != nullptr) {
+        if constexpr ((SC & kBias) != 0) {
           // less slope * distance.  In a stage of 64 consecutive positions key c gets slope * c alone, an
           // immediate operand, and the row's maximum and exponents the rest.
           auto first_key = [&](const PfKeyTile& k) { return (k.kind == 0 ? tl.p_oldest : p0) + k.a; };
@@ -987,7 +993,7 @@ __global__ void __launch_bounds__(256, kCombine ? 3 : 8)
   chunk_append(a, D * 2, block - sh * append_groups, sh);
 }
 
-template <int D, bool SC>
+template <int D, int SC>
 cudaError_t launch_pf(const PrefillArgs& a, const CUtensorMap* pm, const CUtensorMap* sm, const CUtensorMap* km,
                       const CUtensorMap* vm, const CUtensorMap* km64, const CUtensorMap* vm64, const CUtensorMap* qm,
                       int items, cudaStream_t st) {
@@ -1036,10 +1042,12 @@ cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap* pool_map, co
                            const CUtensorMap* vnew64_map, const CUtensorMap* q_map, cudaStream_t st) {
   const int items = a.head_ctas[a.pv.kv_heads];
   if (a.group < 1 || a.group > kMaxGroup) return cudaErrorInvalidValue;
-  auto* launch = a.pv.head_dim == 128 ? (a.score.on ? launch_pf<128, true> : launch_pf<128, false>)
-                                      : (a.score.on ? launch_pf<64, true> : launch_pf<64, false>);
+  const int sc = (a.score.capped ? kCap : kPlain) | (a.score.slopes != nullptr ? kBias : kPlain);
+  constexpr decltype(&launch_pf<128, kPlain>) launchers[2][4] = {
+      {launch_pf<64, kPlain>, launch_pf<64, kCap>, launch_pf<64, kBias>, launch_pf<64, kCap | kBias>},
+      {launch_pf<128, kPlain>, launch_pf<128, kCap>, launch_pf<128, kBias>, launch_pf<128, kCap | kBias>}};
   if (a.pv.head_dim == 128 || a.pv.head_dim == 64)
-    return launch(a, pool_map, stage_map, knew_map, vnew_map, knew64_map, vnew64_map, q_map, items, st);
+    return launchers[a.pv.head_dim == 128][sc](a, pool_map, stage_map, knew_map, vnew_map, knew64_map, vnew64_map, q_map, items, st);
   return cudaErrorInvalidValue;
 }
 

@@ -192,7 +192,7 @@ __device__ __forceinline__ float tree64(const float (&v)[kPfKeys], Op op) {
 // What is done to the scores, in registers between the two products: nothing, capped, biased by
 // distance, both.  An instance each, since the softmax warps wait for instructions (with one
 // scored instance for all a 1024-token chunk at 40000 took 330 us capped, 275 biased and 370 both;
-// with these 296, 241 and 342).
+// with these 296, 239 and 330).
 enum { kPlain = 0, kCap = 1, kBias = 2 };
 
 template <int D, int SC>
@@ -672,8 +672,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
           }
         }
         if constexpr ((SC & kBias) != 0) {
-          // less slope * distance.  In a stage of 64 consecutive positions key c gets slope * c alone, an
-          // immediate operand, and the row's maximum and exponents the rest.
+          // less slope * distance.  Key c gets slope * c, an immediate operand, and the row's maximum and
+          // exponents the rest, which is all in a stage of 64 consecutive positions.
           auto first_key = [&](const PfKeyTile& k) { return (k.kind == 0 ? tl.p_oldest : p0) + k.a; };
           if ((jj & 31) == 0) {  // 32 stages at a time, one per lane
             const int j_lane = max(stage_of(jj + lane), 0);
@@ -688,20 +688,20 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             run_word = __ballot_sync(0xffffffffu, run);
           }
           const int first = __shfl_sync(0xffffffffu, run_first, jj & 31);
-          if ((run_word >> (jj & 31)) & 1u) {
-            row_off = -slope * sl2 * (float)(pq - first);
+          row_off = -slope * sl2 * (float)(pq - first);
 #pragma unroll
-            for (int c = 0; c < kPfKeys; ++c) sv[c] = fmaf(slope, (float)c, sv[c]);
-          } else {
-            // tile by tile; a ring tile's keys past the ring's end are C positions older
+          for (int c = 0; c < kPfKeys; ++c) sv[c] = fmaf(slope, (float)c, sv[c]);
+          if (!((run_word >> (jj & 31)) & 1u)) {
+            // tile by tile, what its keys are off a run from the first; a ring tile's keys past the ring's end
+            // are C positions older
 #pragma unroll
             for (int u = 0; u < kPfSub; ++u) {
               const PfKeyTile k = key_tile(tl, j * kPfSub + u, C);
-              const int d0 = pq - first_key(k);
-              const float far = -slope * (float)d0, wrapped = -slope * (float)(d0 + C);
+              const int d0 = first_key(k) - first - u * kTile;
+              const float near = slope * (float)d0, wrapped = slope * (float)(d0 - C);
               const int wrap = k.kind == 0 ? C - k.a : kTile;
 #pragma unroll
-              for (int i = 0; i < kTile; ++i) sv[u * kTile + i] += fmaf(slope, (float)i, i < wrap ? far : wrapped);
+              for (int i = 0; i < kTile; ++i) sv[u * kTile + i] += i < wrap ? near : wrapped;
             }
           }
         }

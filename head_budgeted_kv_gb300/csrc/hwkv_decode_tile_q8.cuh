@@ -9,7 +9,7 @@
 // Codes become fp16 exactly, one conversion instruction per two values, and feed
 // mma.sync.m16n8k16 fp16 -> fp32.  fp16's range is kept in three exact ways: each query head is
 // scaled by a power of two so its largest element lies in [2^14, 2^15) (the elements then lose
-// nothing above 2^-39 of that largest one); P carries a factor 2^11 that cancels in O / l (2^15
+// nothing above 2^-39 of that largest one); P carries a factor 2^11 that is taken out of O and l alike (2^15
 // at most, as a maximum may lag by 2^4), so a weight keeps its 11 bits down to 2^-25 of the largest
 // and is off by at most 2^-36 of the largest below; and v_scale enters P relative to the
 // largest v_scale the warp has met, by which its accumulators are finally multiplied.
@@ -108,6 +108,9 @@ struct WarpState<E4m3, D, GP, SC> {
   static constexpr int NT = (GP + 7) / 8;
   static constexpr float kShift = 11.f;  // log2 of the factor P carries over the reference maximum
   static constexpr float kSlack = 4.f;   // log2 of how far a score may pass it (P stays below 2^15)
+  // P's factor and the slack, taken out of sums and accumulators alike where they leave the warp: weights
+  // are then at most 1, and no V that bf16 holds overflows by itself
+  static constexpr float kTake = 0x1p-15f;
   uint32_t qf[NT][D / 16][2];
   float acc[D / 16][NT][4];
   float mx[NT][2];   // reference maximum (log2 units)
@@ -395,15 +398,16 @@ struct WarpState<E4m3, D, GP, SC> {
     if (gq == 0) {
       sc_m[warp * SG + c0] = mx[nt][0];
       sc_m[warp * SG + c0 + 1] = mx[nt][1];
-      sc_l[warp * SG + c0] = ls[nt].x;
-      sc_l[warp * SG + c0 + 1] = ls[nt].y;
+      sc_l[warp * SG + c0] = ls[nt].x * kTake;
+      sc_l[warp * SG + c0 + 1] = ls[nt].y * kTake;
     }
+    const float unit = vs * kTake;
     float* wacc = sc_acc + warp * SG * D;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
       const int d = 16 * j + 2 * gq;
-      *reinterpret_cast<float2*>(wacc + c0 * D + d) = make_float2(acc[j][nt][0] * vs, acc[j][nt][2] * vs);
-      *reinterpret_cast<float2*>(wacc + (c0 + 1) * D + d) = make_float2(acc[j][nt][1] * vs, acc[j][nt][3] * vs);
+      *reinterpret_cast<float2*>(wacc + c0 * D + d) = make_float2(acc[j][nt][0] * unit, acc[j][nt][2] * unit);
+      *reinterpret_cast<float2*>(wacc + (c0 + 1) * D + d) = make_float2(acc[j][nt][1] * unit, acc[j][nt][3] * unit);
     }
   }
 };

@@ -26,7 +26,8 @@
  *   blocks with fp32 scales [total_blocks][bs / 16][2]: one for the K rows and one for the V rows
  *   of each group of 16 consecutive slots; a stored value is code * scale.  The scale is 2^e with
  *   the smallest e >= -120 such that the group's largest finite magnitude is at most 448 * 2^e;
- *   codes are rounded to nearest even; what is not finite is stored as NaN.
+ *   codes are rounded to nearest even (a magnitude of 248 * 2^120, 3.3e38, or more is stored as
+ *   2^128, which a bf16 result shows as infinity); what is not finite is stored as NaN.
  *   Storing a token stores its whole group anew: the slots of the group whose positions are in
  *   the window of the new length keep their values at the new scale (rounded again where a code
  *   becomes subnormal), every other slot becomes zero.  Materialise does so with every group

@@ -1,0 +1,106 @@
+"""The operators around the cache at the ends of what their inputs may be: V scales far apart, the
+largest values, slots outside the window, positions before the first, far angles, steep slopes.
+
+Attention tolerance of 8-bit pools, per element, with A = sum_p w_p |v_p| and w the softmax weights: the
+output's rounding to bf16 (2^-8 |ref|); each weight's rounding to fp16 (2^-11) and the error of its
+score and exponential (2^-12, see test_gpu_q8.py), both counted twice for the sum they are
+normalised by.  A product w_p v_scale_p below fp16's normal range is off by an absolute amount
+instead: the kernel holds it times 2^11 / ref with ref between half of the head's largest such product
+and that product (a lagging reference makes what it holds larger), steps below 2^-14 are 2^-24, so half of
+one is 2^-25 and the output is off by at most 2^-36 max(w_p v_scale_p) sum_p |c_p|."""
+from decimal import Decimal, getcontext
+
+import numpy as np
+import pytest
+import torch
+
+import head_budgeted_kv_gb300 as hw
+from reference_ops import Ring8, attention
+from test_gpu_q8 import Case, np64
+
+pytestmark = pytest.mark.gpu
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32, "e4m3": torch.float8_e4m3fn}
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    hw.binding.load()
+    yield
+    torch.cuda.synchronize()
+
+
+def check_head(got, q, ring, n, scale, slope=0.0, cap=0.0, what=""):
+    """One query head of an 8-bit pool against 64 bits."""
+    p, k, v = ring.resident(n)
+    ref, mass, top = attention(q, k, v, scale, n - 1 - p, cap, slope)
+    s = k @ q * scale
+    if cap > 0:
+        s = cap * np.tanh(s / cap)
+    s = s - slope * (n - 1 - p)
+    w = np.exp(s - s.max())
+    w /= w.sum()
+    floor = 2.0 ** -36 * float((w * np.repeat(ring.scales[1], 16)[p % ring.C]).max())
+    floor = floor * np.abs(ring.codes[1][p % ring.C]).sum(0)
+    e = 2.0 ** -11 + 2.0 ** -12 + (2.0 ** -19 * top if cap > 0 or slope else 0.0)
+    tol = 2.0 ** -8 * np.abs(ref) + 2 * e * mass + floor
+    # what lies half a step or more past bf16's largest number, (2 - 2^-7) 2^127, rounds to infinity
+    over = np.abs(ref) >= 2.0 ** 128 - 2.0 ** 119
+    with np.errstate(invalid="ignore"):
+        off = np.where(over, 0.0, np.abs(got - ref))
+    assert (got[over] == np.sign(ref[over]) * np.inf).all(), f"{what}: {got[over]} past the largest number"
+    worst = off / np.maximum(tol, 1e-300)
+    assert (off <= tol).all(), f"{what}: off by {off.max():.3e} of {np.abs(ref).max():.3e}, {worst.max():.3g} times the tolerance"
+
+
+def keys_for(scores, D):
+    """Rows whose product with a query of 8 in dim 0 is `scores`, as far as e4m3 holds them."""
+    k = torch.zeros((1, 1, len(scores), D), device="cuda")
+    k[0, 0, :, 0] = torch.tensor(scores, device="cuda") / 8.0
+    return k.bfloat16()
+
+
+# ---- 8-bit pools: the largest values ------------------------------------------------------------------
+# 3.3895e38, bf16's largest number, is 255 * 2^120, which e4m3 rounds to 256 * 2^120 = 2^128: such a row
+# on its own gives infinity, the nearest thing bf16 has.  3.2e38 is stored as 240 * 2^120.
+@pytest.mark.parametrize("workers", [0, 4])
+@pytest.mark.parametrize("big", [3.3895e38, 3.2e38])
+@pytest.mark.parametrize("D,group", [(128, 4), (64, 16)])
+def test_the_largest_values_come_out(D, group, big, workers):
+    """V rows at the end of bf16's range: a lone token, and one among many others of less weight, whatever the
+    order in which the maximum meets them."""
+    c = Case([200], 2, group, D, 16, 9, None, workers)
+    v = torch.zeros((2, 1, 200, D), device="cuda")
+    v[0, 0, 0] = big
+    v[1, 0, 30, ::2], v[1, 0, 30, 1::2] = big, -big
+    v[1, 0, 160] = 1.5e38
+    # the maximum rises by less than the reference's slack towards the large rows
+    scores = [0.0 if i < 16 else 1.0 if i < 100 else 2.0 for i in range(200)]
+    scores[30], scores[160] = 2.5, 0.0
+    k = torch.cat((keys_for([0.0] * 200, D), keys_for([x * 0.8 for x in scores], D)))
+    c.materialize([1, 200], k, v.bfloat16())
+    q = torch.zeros((2, group, D), device="cuda").bfloat16()
+    q[..., 0] = 8.0
+    out = np64(c.pool.decode(0, q, 1.0, c.i32([1, 200])))
+    for s, n in enumerate((1, 200)):
+        for g in range(group):
+            check_head(out[s, g], np64(q)[s, g], c.rings[s][0], n, 1.0, what=f"seq {s} head {g}")
+    c.close()
+
+
+@pytest.mark.parametrize("x", [3.3895e38, 3.2e38, 2.0 ** 116, 2.0 ** -110, 2.0 ** -129])
+def test_one_token_gives_its_value(x):
+    """Largest to smallest magnitudes, appended in the launch that attends to them."""
+    c = Case([5], 1, 4, 64, 16, 1)
+    kn, vn = torch.zeros((2, 1, 1, 64), device="cuda").bfloat16().unbind(0)
+    vn = vn + torch.tensor(x, device="cuda").bfloat16()
+    out = c.pool.append_decode(0, c.randn(1, 4, 64), 0.1, kn, vn, c.i32([0]))
+    c.ref_append(kn, vn, [0])
+    want = c.rings[0][0].resident(1)[2][0]
+    if x == 3.3895e38:
+        assert (want == 2.0 ** 128).all() and (np64(out) == np.inf).all()
+        return
+    # below 2^-126 bf16's step is 2^-133: half of one
+    assert (np.abs(np64(out)[0] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -134).all()
+    c.close()

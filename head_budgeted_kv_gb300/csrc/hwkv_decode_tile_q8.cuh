@@ -7,12 +7,21 @@
 //   S = (Kc . Qn^T) * (k_scale * qs)       Qn = Q / qs, qs a power of two per query head
 //   O = sum over tiles of (P * v_scale) . Vc
 // Codes become fp16 exactly, one conversion instruction per two values, and feed
-// mma.sync.m16n8k16 fp16 -> fp32.  fp16's range is kept in three exact ways: each query head is
+// mma.sync.m16n8k16 fp16 -> fp32.  fp16's range is kept in two exact ways.  Each query head is
 // scaled by a power of two so its largest element lies in [2^14, 2^15) (the elements then lose
-// nothing above 2^-39 of that largest one); P carries a factor 2^11 that is taken out of O and l alike (2^15
-// at most, as a maximum may lag by 2^4), so a weight keeps its 11 bits down to 2^-25 of the largest
-// and is off by at most 2^-36 of the largest below; and v_scale enters P relative to the
-// largest v_scale the warp has met, by which its accumulators are finally multiplied.
+// nothing above 2^-39 of that largest one).  And P * v_scale is formed relative to a reference of its own:
+// with m the integer reference maximum of the scores s (log2 units) and e the one of s + log2(v_scale) - m,
+//   p = 2^(s - m)                            fp32, summed to l
+//   p * v_scale = 2^e * 2^(s - m + log2(v_scale) - e)
+// where the last factor, times 2^11, is what fp16 holds: the largest of a head lies in [2^11, 2^12), or up
+// to 2^15.98 while a reference lags.  So a product of weight and scale keeps its 11 bits down to 2^-25 of its
+// head's largest and is off by at most 2^-36 of that below, and a group whose scale is large but whose
+// weight is not has no say in it.  (With the scale relative to the largest one met, whatever its weight, such a
+// group 2^24 above the others put 12% into the result and one 2^37 above them erased it.)  m and e are
+// integers, so no reference is rounded, and 2^e is exact where O leaves the warp.  The second exponential per
+// weight costs up to 2% of a decode whose references seldom move and 6% where steep slopes move them at every
+// stage (policy layer, uncapped 55.0 -> 55.1 us, biased 57.5 -> 61); a product by the power of two instead of it
+// is slower (61 at cap 50 against 57).
 // A dim or token index may be permuted freely inside a contraction: K's bytes are fed in the
 // order ldmatrix delivers them, against queries loaded in the same order, and V's columns come
 // out as dim pairs (2i, 2i + 1) in the accumulator's row halves, which publish() undoes.
@@ -101,24 +110,24 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// 8-bit pools: the GQA group on the N side of mma.sync as for bf16, fp32 accumulators in units
-// of the warp's largest V scale `vs`.
+// 8-bit pools: the GQA group on the N side of mma.sync as for bf16, fp32 accumulators in units of
+// 2^(er - kShift) per head.
 template <int D, int GP, bool SC>
 struct WarpState<E4m3, D, GP, SC> {
   static constexpr int NT = (GP + 7) / 8;
-  static constexpr float kShift = 11.f;  // log2 of the factor P carries over the reference maximum
-  static constexpr float kSlack = 4.f;   // log2 of how far a score may pass it (P stays below 2^15)
-  // P's factor and the slack, taken out of sums and accumulators alike where they leave the warp: weights
-  // are then at most 1, and no V that bf16 holds overflows by itself
-  static constexpr float kTake = 0x1p-15f;
+  static constexpr float kShift = 11.f;   // log2 of the factor P * v_scale carries over its reference
+  static constexpr float kSlack = 4.98f;  // log2 of how far it, or a weight, may pass its reference: below fp16's end
+  static constexpr float kNone = -3e38f;  // the reference before any score: finite, so differences are no NaN
+  // 2^5 for the slack is taken out of sums and accumulators alike where they leave the warp, and the shift out
+  // of the accumulators: weights are then at most 1, and no V that bf16 holds overflows by itself
+  static constexpr float kTakeSum = 0x1p-5f, kTakeAcc = 0x1p-16f;
   uint32_t qf[NT][D / 16][2];
   float acc[D / 16][NT][4];
-  float mx[NT][2];   // reference maximum (log2 units)
-  float2 ls[NT];     // this lane's partial sums
-  float base[NT][2];           // what is subtracted from a score: mx - kShift
+  float mx[NT][2];   // reference maximum of the scores (log2 units, an integer)
+  float er[NT][2];   // reference of score + log2(V scale), less mx: an integer from -120 to 120
+  float2 ls[NT];     // this lane's partial sums of 2^(score - mx)
   float qs[NT][2];  // the power of two taken out of each of the lane's heads (times |scale| log2(e) unless SC)
   float slope[NT][2];  // SC: of the lane's heads, log2 units
-  float vs, vs_inv;  // largest V scale met (0 at first) and its inverse
 
   // Q of the group, normalised: the lane holds q[g][16i + 4*q4 .. + 3], g = 8*nt + lane / 4
   __device__ __forceinline__ void begin(const DecodeArgs& a, const Group& gr, int G, int lane) {
@@ -154,31 +163,26 @@ struct WarpState<E4m3, D, GP, SC> {
       qs[nt][1] = __shfl_sync(0xffffffffu, inv, (2 * q4 + 1) * 4) * (SC ? 1.f : fabsf(a.scale_log2));
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) acc[j][nt][0] = acc[j][nt][1] = acc[j][nt][2] = acc[j][nt][3] = 0.f;
-      mx[nt][0] = mx[nt][1] = kNegInf;
+      mx[nt][0] = mx[nt][1] = kNone;
+      er[nt][0] = er[nt][1] = 0.f;
       ls[nt] = make_float2(0.f, 0.f);
-      base[nt][0] = base[nt][1] = -kShift;
     }
-    vs = vs_inv = 0.f;
     if constexpr (SC) load_slopes<NT>(a, gr, G, lane, slope);
   }
 
-  // The raw scores s (times f) of M tiles capped, biased and in log2 units.  While no score of the warp
+  // The raw scores s of M tiles capped, biased and in log2 units.  While no score of the warp
   // reaches the cap the polynomial alone serves, on packed pairs (a capped policy layer 65 -> 55 us,
   // uncapped 54; past the cap 77).
   template <int M>
   __device__ __forceinline__ void score_tiles(const DecodeArgs& a, const Group& gr, const int (&t0)[M], float (&s)[M][NT][4],
-                                              float2 (&f)[M][NT], int gq) const {
+                                              int gq) const {
     float top = 0.f;
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float2 x = fmul2(make_float2(s[m][nt][0], s[m][nt][1]), f[m][nt]);
-        const float2 y = fmul2(make_float2(s[m][nt][2], s[m][nt][3]), f[m][nt]);
-        s[m][nt][0] = x.x, s[m][nt][1] = x.y, s[m][nt][2] = y.x, s[m][nt][3] = y.y;
-        f[m][nt] = make_float2(1.f, 1.f);
-        top = fmaxf(fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(y.x), fabsf(y.y)));
-      }
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(s[m][nt][e]));
     const float2 sl = make_float2(a.scale_log2, a.scale_log2);
     if (!a.score.capped) {
 #pragma unroll
@@ -232,13 +236,13 @@ struct WarpState<E4m3, D, GP, SC> {
     const uint32_t lane_off = swz_q8<D>((lane & 7) + ((lane >> 3) & 1) * 8, (lane >> 4) * 16);
     bool dirty = false;
 
-    float s[M][NT][4];  // raw scores; times f in log2 units
-    float2 f[M][NT];
-    float vscale[M];
+    float s[M][NT][4];  // scores in log2 units (SC: raw until score_tiles)
+    float ev[M];  // log2 of each tile's V scale
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       const float2 sc = *slot[m];
-      vscale[m] = sc.y;
+      // (a scale of 0, of a group never stored, has codes 0: any exponent serves)
+      ev[m] = (float)max((int)(__float_as_uint(sc.y) >> 23) - 127, kMinScaleExp);
       constexpr bool kTwoChains = M * NT < 4;  // few scores at once: shorter accumulation chains
       float sb[NT][4];
 #pragma unroll
@@ -266,11 +270,15 @@ struct WarpState<E4m3, D, GP, SC> {
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[m][nt][e] += sb[nt][e];
         }
-        // positive (begin() moved a negative scale into Q), and normal so that -inf stays -inf
-        f[m][nt] = make_float2(fmaxf(qs[nt][0] * sc.x, 0x1p-126f), fmaxf(qs[nt][1] * sc.x, 0x1p-126f));
+        // rounded here, not in a multiply-add with the reference: a difference of two scores is then exact
+        // where it counts, however large they are
+        const float2 f = make_float2(qs[nt][0] * sc.x, qs[nt][1] * sc.x);
+        const float2 x = fmul2(make_float2(s[m][nt][0], s[m][nt][1]), f);
+        const float2 y = fmul2(make_float2(s[m][nt][2], s[m][nt][3]), f);
+        s[m][nt][0] = x.x, s[m][nt][1] = x.y, s[m][nt][2] = y.x, s[m][nt][3] = y.y;
       }
     }
-    if constexpr (SC) score_tiles<M>(a, gr, t0, s, f, gq);
+    if constexpr (SC) score_tiles<M>(a, gr, t0, s, gq);
 
 #pragma unroll
     for (int m = 0; m < M; ++m) {
@@ -295,46 +303,48 @@ struct WarpState<E4m3, D, GP, SC> {
       }
     }
 
-    // The reference maximum moves only when a score passes it by more than 2^kSlack (or a V scale
-    // the largest so far): seldom after a group's first tiles, so the common case reduces nothing
-    // over the warp and rescales nothing.
-    float vmax = vscale[0];
+    // The references move only when a weight, or its product with the V scale, passes its own by more than
+    // 2^kSlack: seldom after a group's first tiles, so the common case reduces nothing over the warp and
+    // rescales nothing.  (The products are judged by the tiles' largest scale: at worst a step in vain.)
+    float ev_max = ev[0];
 #pragma unroll
-    for (int m = 1; m < M; ++m) vmax = fmaxf(vmax, vscale[m]);
+    for (int m = 1; m < M; ++m) ev_max = fmaxf(ev_max, ev[m]);
     float top[NT][2];
-    bool grow = vmax > vs;
+    bool grow = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         float x = kNegInf;
 #pragma unroll
-        for (int m = 0; m < M; ++m) x = fmaxf(x, fmaxf(s[m][nt][c], s[m][nt][c + 2]) * (c ? f[m][nt].y : f[m][nt].x));
+        for (int m = 0; m < M; ++m) x = fmaxf(x, fmaxf(s[m][nt][c], s[m][nt][c + 2]));
         top[nt][c] = x;
-        grow = grow || x > mx[nt][c] + kSlack;
+        grow = grow || x - mx[nt][c] + fmaxf(ev_max - er[nt][c], 0.f) > kSlack;
       }
     if (__any_sync(0xffffffffu, grow)) {
-      const float vs_new = fmaxf(vs, vmax);
-      vs_inv = vs_new > 0.f ? pow2_inverse(vs_new) : 0.f;
-      const float keep = vs * vs_inv;
-      vs = vs_new;
+      auto over_lanes = [](float v) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+        return v;
+      };
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float x = top[nt][c];
+          const float n = fmaxf(mx[nt][c], floorf(over_lanes(top[nt][c])));
+          float w = kNegInf;
 #pragma unroll
-          for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-          const float n = fmaxf(mx[nt][c], x);
-          const float b = n == kNegInf ? 0.f : n;
-          const float al = ex2(mx[nt][c] - b);
+          for (int m = 0; m < M; ++m) w = fmaxf(w, fmaxf(s[m][nt][c], s[m][nt][c + 2]) - n + ev[m]);
+          const float fall = mx[nt][c] - n;  // at most 0, as is the accumulators' exponent
+          const float e = fmaxf(er[nt][c] + fall, floorf(over_lanes(w)));
+          const float al = ex2(fall), aa = ex2(er[nt][c] + fall - e);
           mx[nt][c] = n;
-          base[nt][c] = b - kShift;
+          er[nt][c] = e;
           (c ? ls[nt].y : ls[nt].x) *= al;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
-            acc[j][nt][c] *= al * keep;
-            acc[j][nt][c + 2] *= al * keep;
+            acc[j][nt][c] *= aa;
+            acc[j][nt][c + 2] *= aa;
           }
         }
     }
@@ -342,15 +352,16 @@ struct WarpState<E4m3, D, GP, SC> {
     uint32_t pb[M][NT][2];
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      const float2 part = make_float2(vscale[m] * vs_inv, vscale[m] * vs_inv);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float2 nb = make_float2(-base[nt][0], -base[nt][1]);
-        const float2 x = ffma2(make_float2(s[m][nt][0], s[m][nt][1]), f[m][nt], nb);
-        const float2 y = ffma2(make_float2(s[m][nt][2], s[m][nt][3]), f[m][nt], nb);
-        const float2 p = make_float2(ex2(x.x), ex2(x.y)), r = make_float2(ex2(y.x), ex2(y.y));
-        ls[nt] = fadd2(ls[nt], fadd2(p, r));
-        const float2 pv = fmul2(p, part), rv = fmul2(r, part);
+        const float2 nm = make_float2(-mx[nt][0], -mx[nt][1]);
+        const float2 rel = make_float2(ev[m] + kShift - er[nt][0], ev[m] + kShift - er[nt][1]);
+        const float2 x = fadd2(make_float2(s[m][nt][0], s[m][nt][1]), nm);
+        const float2 y = fadd2(make_float2(s[m][nt][2], s[m][nt][3]), nm);
+        ls[nt] = fadd2(ls[nt], fadd2(make_float2(ex2(x.x), ex2(x.y)), make_float2(ex2(y.x), ex2(y.y))));
+        // exponentials of their own: a weight may be below fp32's range where its product with the scale is not
+        const float2 xv = fadd2(x, rel), yv = fadd2(y, rel);
+        const float2 pv = make_float2(ex2(xv.x), ex2(xv.y)), rv = make_float2(ex2(yv.x), ex2(yv.y));
         pb[m][nt][0] = movmatrix_trans(pack_f16(pv.x, pv.y));
         pb[m][nt][1] = movmatrix_trans(pack_f16(rv.x, rv.y));
       }
@@ -398,16 +409,16 @@ struct WarpState<E4m3, D, GP, SC> {
     if (gq == 0) {
       sc_m[warp * SG + c0] = mx[nt][0];
       sc_m[warp * SG + c0 + 1] = mx[nt][1];
-      sc_l[warp * SG + c0] = ls[nt].x * kTake;
-      sc_l[warp * SG + c0 + 1] = ls[nt].y * kTake;
+      sc_l[warp * SG + c0] = ls[nt].x * kTakeSum;
+      sc_l[warp * SG + c0 + 1] = ls[nt].y * kTakeSum;
     }
-    const float unit = vs * kTake;
+    const float u0 = pow2i((int)er[nt][0]) * kTakeAcc, u1 = pow2i((int)er[nt][1]) * kTakeAcc;
     float* wacc = sc_acc + warp * SG * D;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
       const int d = 16 * j + 2 * gq;
-      *reinterpret_cast<float2*>(wacc + c0 * D + d) = make_float2(acc[j][nt][0] * unit, acc[j][nt][2] * unit);
-      *reinterpret_cast<float2*>(wacc + (c0 + 1) * D + d) = make_float2(acc[j][nt][1] * unit, acc[j][nt][3] * unit);
+      *reinterpret_cast<float2*>(wacc + c0 * D + d) = make_float2(acc[j][nt][0] * u0, acc[j][nt][2] * u0);
+      *reinterpret_cast<float2*>(wacc + (c0 + 1) * D + d) = make_float2(acc[j][nt][1] * u1, acc[j][nt][3] * u1);
     }
   }
 };

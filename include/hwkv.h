@@ -209,6 +209,8 @@ int hwkv_decode_workspace_bytes(hwkv_pool_t pool, int q_heads, uint64_t* out);
  * Other shapes (block_size not a multiple of 16, fp32 groups above 4) take the split-K
  * CUDA-core kernel and a merge kernel.  8-bit pools always take the stream-K kernel, on the
  * tensor cores; q, k_new, v_new and out are bf16.
+ *   8-bit pools: a softmax weight times its group's V scale is rounded to 11 bits down to 2^-25 of
+ *   the largest such product of its query head, and is off by at most 2^-36 of that product below.
  * Errors: HWKV_ERR_INVALID_ARG, HWKV_ERR_ALIGNMENT, HWKV_ERR_WORKSPACE_TOO_SMALL,
  *         HWKV_ERR_UNSUPPORTED, HWKV_ERR_CUDA (launch failure). */
 int hwkv_decode_attn(hwkv_pool_t pool, int layer, const void* q, int q_heads, float scale,

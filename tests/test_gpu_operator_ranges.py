@@ -104,3 +104,110 @@ def test_one_token_gives_its_value(x):
     # below 2^-126 bf16's step is 2^-133: half of one
     assert (np.abs(np64(out)[0] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -134).all()
     c.close()
+
+
+# ---- 8-bit pools: V scales far apart ------------------------------------------------------------------
+@pytest.mark.parametrize("where", [0, 2, 5], ids=["first", "middle", "last"])
+@pytest.mark.parametrize("power", [20, 24, 30, 37, 60, 110])
+@pytest.mark.parametrize("D,group", [(128, 2), (64, 16)])
+def test_value_group_without_weight_leaves_the_others_alone(D, group, power, where):
+    """One group of V is 2^power times the others and has no weight; the others' weights are 2^-11.5 of the
+    largest one's, or all alike."""
+    for lead in (8.0, 0.0):
+        c = Case([96], 1, group, D, 16, 3)
+        scores = [0.0] * 96
+        scores[16 * where:16 * where + 16] = [-120.0] * 16
+        scores[16 * ((where + 1) % 6)] = lead
+        v = c.randn(1, 1, 96, D).float()
+        v[0, 0, 16 * where:16 * where + 16] *= 2.0 ** power
+        c.materialize([96], keys_for(scores, D), v.bfloat16())
+        q = torch.zeros((1, group, D), device="cuda").bfloat16()
+        q[..., 0] = 8.0
+        out = np64(c.pool.decode(0, q, 1.0, c.i32([96])))
+        for g in range(group):
+            check_head(out[0, g], np64(q)[0, g], c.rings[0][0], 96, 1.0, what=f"lead {lead} head {g}")
+        c.close()
+
+
+@pytest.mark.parametrize("workers", [0, 1, 5])
+@pytest.mark.parametrize("power", [30, 40, 100])
+@pytest.mark.parametrize("fused", [False, True], ids=["decode", "fused"])
+def test_values_that_slopes_suppress(power, fused, workers):
+    """Steep slopes leave an old group of far larger V no weight in some heads, and all of it in others (negative
+    slopes), also when the merges of many CTAs join them."""
+    c = Case([700, 40], 2, 4, 128, 16, 5, 2, workers)
+    n = 800
+    k, v = c.randn(2, 2, n, 128), c.randn(2, 2, n, 128).float()
+    v[0, :, 200:340] *= 2.0 ** power
+    v[1, :, 100:480] *= 2.0 ** -power
+    c.materialize([n, n - 300], k, v.bfloat16())
+    slopes = torch.tensor([1.0, 0.25, 0.0, -0.5, 4.0, 0.125, 1e-3, -2.0], device="cuda")
+    q = c.randn(2, 8, 128)
+    if fused:
+        kn, vn = c.randn(2, 2, 128), c.randn(2, 2, 128)
+        out = c.pool.append_decode(0, q, c.scale, kn, vn, c.i32([n, n - 300]), slopes=slopes)
+        c.ref_append(kn, vn, [n, n - 300])
+        lens = [n + 1, n - 299]
+    else:
+        lens = [n, n - 300]
+        out = c.pool.decode(0, q, c.scale, c.i32(lens), slopes=slopes)
+    for s in range(2):
+        for g in range(8):
+            check_head(np64(out)[s, g], np64(q)[s, g], c.rings[s][g // 4], lens[s], c.scale, float(slopes[g]), what=f"seq {s} head {g}")
+    c.close()
+
+
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("workers", [0, 3])
+def test_value_scales_over_their_whole_range(seed, workers):
+    """Each group of V at a power of its own between 2^-110 and 2^110, appended rows among them."""
+    rng = np.random.default_rng(seed)
+    D, group = [(128, 4), (64, 1), (128, 16), (64, 8)][seed]
+    c = Case([300, 37], 1, group, D, 16, seed, seed, workers)
+    k, v = c.randn(1, 2, 350, D), c.randn(1, 2, 350, D).float()
+    for g in range(0, 350, 16):
+        v[:, :, g:g + 16] *= 2.0 ** float(rng.integers(-110, 110))
+    c.materialize([350], k, v.bfloat16())
+    pos = 350
+    for i in range(3):
+        q = c.randn(1, 2 * group, D, scale=4.0)
+        kn, vn = c.randn(1, 2, D), (c.randn(1, 2, D).float() * 2.0 ** float(rng.integers(-110, 110))).bfloat16()
+        out = c.pool.append_decode(0, q, c.scale, kn, vn, c.i32([pos]))
+        c.ref_append(kn, vn, [pos])
+        pos += 1
+        for g in range(2 * group):
+            check_head(np64(out)[0, g], np64(q)[0, g], c.rings[0][g // group], pos, c.scale, what=f"step {i} head {g}")
+    c.close()
+
+
+@pytest.mark.parametrize("size", [1e3, 1e6, 1e9, 1e12])
+def test_huge_scores(size):
+    """Scores so large that one key takes all the weight: its V comes out, whatever the scales about it."""
+    c = Case([96], 1, 2, 64, 16, 7)
+    k = keys_for([float(8 * (i % 48)) / 64 for i in range(95)] + [0.0], 64)
+    k[0, 0, 50, 0] = 14.0  # the others stay below 1: a gap of more than 100 sizes
+    v = c.randn(1, 1, 96, 64).float()
+    for g in range(6):
+        v[0, 0, 16 * g:16 * g + 16] *= 2.0 ** (7 * (g - 3))
+    c.materialize([96], k, v.bfloat16())
+    q = torch.zeros((1, 2, 64), device="cuda").bfloat16()
+    q[..., 0] = 8.0
+    for scale in (size, -size):
+        q[0, 1, 0] = 8.0 if scale > 0 else -8.0
+        q[0, 0, 0] = q[0, 1, 0]
+        out = np64(c.pool.decode(0, q, scale, c.i32([96])))
+        want = c.rings[0][0].resident(96)[2][50]
+        assert (np.abs(out[0] - want) <= 2.0 ** -8 * np.abs(want)).all()
+    c.close()
+
+
+def test_far_smaller_rows_than_a_huge_scale():
+    """8-bit pools with a bias: rows and queries so small that a scale of 2^126 still gives no score."""
+    c = Case([48], 1, 2, 64, 16, 21)
+    k = (c.randn(1, 1, 48, 64).float() * 2.0 ** -125).bfloat16()
+    c.materialize([48], k, c.randn(1, 1, 48, 64))
+    q = (c.randn(1, 2, 64).float() * 2.0 ** -110).bfloat16()
+    out = c.pool.decode(0, q, 2.0 ** 126, c.i32([48]), slopes=torch.zeros(2, device="cuda"))
+    for g in range(2):
+        check_head(np64(out)[0, g], np64(q)[0, g], c.rings[0][0], 48, 2.0 ** 126, what=f"head {g}")
+    c.close()

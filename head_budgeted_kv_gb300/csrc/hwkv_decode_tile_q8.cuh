@@ -170,19 +170,35 @@ struct WarpState<E4m3, D, GP, SC> {
     if constexpr (SC) load_slopes<NT>(a, gr, G, lane, slope);
   }
 
+  // whether the tile at slot t0 holds slots outside the window (or the window's two ends)
+  static __device__ __forceinline__ bool partly_resident(const Group& gr, int t0) {
+    int first = t0 - gr.rs.first_slot;
+    if (first < 0) first += gr.rs.C;
+    return first + kTile > gr.rs.n;
+  }
+
   // The raw scores s of M tiles capped, biased and in log2 units.  While no score of the warp
   // reaches the cap the polynomial alone serves, on packed pairs (a capped policy layer 65 -> 55 us,
   // uncapped 54; past the cap 77).
   template <int M>
   __device__ __forceinline__ void score_tiles(const DecodeArgs& a, const Group& gr, const int (&t0)[M], float (&s)[M][NT][4],
                                               int gq) const {
-    float top = 0.f;
+    bool past = false;  // the cap; judged by the slots in the window alone where one outside seems to pass it
+    if (a.score.capped) {
+      auto passes = [&](bool all) {
+        float top = 0.f;
 #pragma unroll
-    for (int m = 0; m < M; ++m)
+        for (int m = 0; m < M; ++m) {
+          const bool v0 = all || slot_valid(gr.rs, t0[m] + gq), v1 = all || slot_valid(gr.rs, t0[m] + gq + 8);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(s[m][nt][e]));
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, (e < 2 ? v0 : v1) ? fabsf(s[m][nt][e]) : 0.f);
+        }
+        return __any_sync(0xffffffffu, top * fabsf(a.score.cap_in) > 1.f) != 0;
+      };
+      past = !a.score.poly_on || (passes(true) && passes(false));
+    }
     const float2 sl = make_float2(a.scale_log2, a.scale_log2);
     if (!a.score.capped) {
 #pragma unroll
@@ -191,7 +207,7 @@ struct WarpState<E4m3, D, GP, SC> {
         const float2 y = fmul2(make_float2(x[0], x[1]), sl);
         x[0] = y.x, x[1] = y.y;
       }
-    } else if (a.score.poly_on && !__any_sync(0xffffffffu, top * fabsf(a.score.cap_in) > 1.f)) {
+    } else if (!past) {
 #pragma unroll
       for (int i = 0; i < M * NT * 2; ++i) {
         float* x = &s[i / (NT * 2)][i / 2 % NT][i % 2 * 2];
@@ -284,9 +300,7 @@ struct WarpState<E4m3, D, GP, SC> {
     for (int m = 0; m < M; ++m) {
       // a tile with slots outside the window: their scores are masked, and their V rows zeroed, as
       // 0 times a NaN is not 0
-      int first = t0[m] - gr.rs.first_slot;
-      if (first < 0) first += gr.rs.C;
-      if (first + kTile > gr.rs.n) {
+      if (partly_resident(gr, t0[m])) {
         const bool v0 = slot_valid(gr.rs, t0[m] + gq), v1 = slot_valid(gr.rs, t0[m] + gq + 8);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

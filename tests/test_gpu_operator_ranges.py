@@ -211,3 +211,30 @@ def test_far_smaller_rows_than_a_huge_scale():
     for g in range(2):
         check_head(np64(out)[0, g], np64(q)[0, g], c.rings[0][0], 48, 2.0 ** 126, what=f"head {g}")
     c.close()
+
+
+# ---- 8-bit pools: what lies outside the window --------------------------------------------------------
+@pytest.mark.parametrize("cap,biased", [(20.0, False), (6.0, False), (6.0, True), (0.0, True), (0.0, False)])
+@pytest.mark.parametrize("D,group", [(128, 4), (64, 16), (64, 1)])
+def test_slots_outside_the_window_do_not_change_a_bit(D, group, cap, biased):
+    """Expired rows as large as codes go and along the query, past the cap where those in the window stay below
+    it, or zeros, in the slots around the window."""
+    outs = []
+    for fill in (0.0, 448.0):
+        c = Case([40, 70, 9], 2, group, D, 16, 15)
+        lens = [100, 230]
+        c.materialize(lens)
+        q = c.randn(2, 3 * group, D)
+        codes = c.pool.blocks().float()
+        for s in range(2):
+            for h in range(3):
+                ring, ids = c.rings[s][h], c.pool.block_table(s, 0, h)
+                inside = {p % ring.C for p in range(max(0, lens[s] - ring.w), lens[s])}
+                for t in set(range(ring.C)) - inside:
+                    codes[int(ids[t // 16]), :, t % 16] = fill * torch.sign(q[s, h * group].float())
+        c.pool.blocks().copy_(codes.to(torch.float8_e4m3fn))
+        slopes = torch.linspace(0.01, 0.3, 3 * group, device="cuda") if biased else None
+        outs.append([c.pool.decode(0, q, c.scale, c.i32(lens), softcap=cap, slopes=slopes),
+                     c.pool.append_decode(0, q, c.scale, c.randn(2, 3, D), c.randn(2, 3, D), c.i32(lens), softcap=cap, slopes=slopes)])
+        c.close()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
 
   if (cta == 0) {
     for (int s = threadIdx.x; s < B; s += kThreads)
-      if (__ldcg(a.lens + s) + a.len_add < 0) atomicOr(a.pv.err, HWKV_DEVERR_NEG_LENGTH);
+      if (__ldcg(a.lens + s) < 0) atomicOr(a.pv.err, HWKV_DEVERR_NEG_LENGTH);
   }
   const int* s_lens = B <= kLensCache ? s_lens_buf : nullptr;
   if (s_lens != nullptr) {

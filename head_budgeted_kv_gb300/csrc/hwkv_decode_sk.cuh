@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
 
   if (cta == 0) {
     for (int s = threadIdx.x; s < B; s += W * 32)
-      if (__ldcg(a.lens + s) + a.len_add < 0) atomicOr(a.pv.err, HWKV_DEVERR_NEG_LENGTH);
+      if (__ldcg(a.lens + s) < 0) atomicOr(a.pv.err, HWKV_DEVERR_NEG_LENGTH);
   }
   // the lengths are staged once, so crossing into the next group never waits on global memory
   const int* s_lens = B <= kLensCache ? s_lens_buf : nullptr;

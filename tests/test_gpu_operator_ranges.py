@@ -238,3 +238,32 @@ def test_slots_outside_the_window_do_not_change_a_bit(D, group, cap, biased):
                      c.pool.append_decode(0, q, c.scale, c.randn(2, 3, D), c.randn(2, 3, D), c.i32(lens), softcap=cap, slopes=slopes)])
         c.close()
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+# ---- positions before the first -----------------------------------------------------------------------
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("kind,bs,group", [("bf16", 16, 4), ("f32", 16, 4), ("e4m3", 16, 4), ("bf16", 5, 2), ("f32", 16, 6)])
+@pytest.mark.parametrize("first", [-1, -3])
+def test_fused_step_flags_negative_positions(kind, bs, group, softcap, first):
+    """As the append on its own: flagged, nothing stored, a zero output; the other sequences go on."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    pool = hw.Pool(1, 2, 64, bs, [[64, 30]], 2, TYPES[kind], q_heads=2 * group)
+    k = torch.randn((2, 2, 80, 64), generator=gen, device="cuda").to(pool.io_dtype)
+    pool.materialize(0, k, k, torch.tensor([80, 80], dtype=torch.int32, device="cuda"))
+    q, kn = torch.randn((2, 2 * group, 64), generator=gen, device="cuda").to(pool.io_dtype), k[:, :, 5].contiguous()
+    separate = pool.buffer.clone()
+    pos = torch.tensor([first, 80], dtype=torch.int32, device="cuda")
+    out = pool.append_decode(0, q, 0.125, kn, kn, pos, softcap=softcap)
+    assert pool.check_device_errors() == hw.binding.HWKV_DEVERR_NEG_LENGTH
+    assert (out[0] == 0).all() and out[1].abs().sum() > 0
+    fused = pool.buffer.clone()
+    pool.buffer.copy_(separate)
+    pool.append(0, kn, kn, pos)
+    assert pool.check_device_errors() == hw.binding.HWKV_DEVERR_NEG_LENGTH
+    assert torch.equal(pool.buffer, fused) and not torch.equal(fused, separate)
+    want = pool.decode(0, q, 0.125, pos + 1, softcap=softcap)
+    assert torch.equal(want, out)
+    pool.check_device_errors()
+    # position 0 is a first token, not an error
+    pool.append_decode(0, q, 0.125, kn, kn, pos * 0, softcap=softcap)
+    assert pool.check_device_errors() == 0

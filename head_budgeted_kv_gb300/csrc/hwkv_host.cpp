@@ -91,7 +91,8 @@ struct Geometry {
   uint64_t pool_bytes = 0;     // the same, rounded up to 16
 };
 
-constexpr double kInvTwoPi = 0.15915494309189533577;
+// 1 / (2 pi) in two parts, good to 2^-110
+constexpr double kInvTwoPi = 0x1.45f306dc9c883p-3, kInvTwoPiLo = -0x1.6b01ec5417056p-57;
 constexpr int64_t kInt32Max = std::numeric_limits<int32_t>::max();
 
 int plan_geometry(int layers, int kv_heads, int head_dim, int block_size, const int32_t* windows, int num_seqs,
@@ -172,6 +173,10 @@ int log2_of(int x) {
     if ((1 << b) == x) return b;
   return -1;
 }
+
+// The fraction of x as a 64-bit fraction (modulo 1, negative x too), off by at most 2^-63.  Not inlined:
+// a compiler that fuses the product x comes from into the difference would count its rounding error here.
+[[gnu::noinline]] uint64_t fraction64(double x) { return (uint64_t)(int64_t)((x - std::trunc(x)) * 0x1p63) << 1; }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -920,12 +925,10 @@ int hwkv_rope(hwkv_pool_t p, const hwkv_rope_t* rope, const hwkv_rows_t* q, int 
   a.copy = copy ? 1 : 0;
   a.magnitude = (float)rope->magnitude;
   for (int i = 0; i < rope->rot_dim / 2; ++i) {
-    // the fraction of a turn per position, in [0, 1), as a 64-bit fraction
-    const double turns = rope->freq[i] * kInvTwoPi;
-    const double frac = turns - std::floor(turns);
-    // 2^32 steps at a time: both parts convert exactly
-    const double hi = std::floor(frac * 0x1p32), lo = (frac * 0x1p32 - hi) * 0x1p32;
-    a.turns[i] = ((uint64_t)hi << 32) + (uint64_t)lo;
+    // The fraction of a turn per position: the product's rounding error and the low part of 1 / (2 pi) count,
+    // as a position multiplies them by up to 2^31.  Off by less than 2^-60 of a turn for |freq| < 2^40.
+    const double f = rope->freq[i], turns = f * kInvTwoPi;
+    a.turns[i] = fraction64(turns) + fraction64(std::fma(f, kInvTwoPi, -turns) + f * kInvTwoPiLo);
   }
   HWKV_CUDA_TRY(launch_rope(a, rope->layout, g.dtype == HWKV_F32, static_cast<cudaStream_t>(stream)), "rope launch");
   return ok();

@@ -8,10 +8,11 @@
 //
 // Angles of far positions: p f_i reaches thousands of turns, of which fp32 would keep none of the
 // fraction's last bits (p = 161K: an error of 0.01 rad).  The host turns f_i into turns as a
-// 64-bit fraction F_i = f_i / (2 pi) * 2^64, so that p * F_i modulo 2^64 -- one integer
-// multiplication -- is the exact fraction of a turn of p f_i, whatever p; its top 32 bits go to
-// fp32 as half turns in [-1, 1) and sincospif() does the rest: 2^-23 rad at any position.  fp64
-// would give the same at this GPU's far lower fp64 rate.
+// 64-bit fraction F_i = f_i / (2 pi) * 2^64, from a product kept in two parts (one rounded fp64 product would be off
+// by up to 2^-21 rad near p = 2^31), so that p * F_i modulo 2^64 -- one integer multiplication -- is the
+// fraction of a turn of p f_i to 2^-29; its top 32 bits go to fp32 as half turns in [-1, 1) and sincospif()
+// does the rest: 2^-23 rad at every int32 position, for |f_i| < 2^40.  fp64 on the device would give the same at this
+// GPU's far lower fp64 rate.
 //
 // A CTA takes a few rows (tokens) of one sequence: their cosines and sines are computed once into
 // shared memory, then each thread turns units of 16-byte vectors across all query and key heads,

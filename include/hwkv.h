@@ -353,7 +353,7 @@ int hwkv_set_decode_config(hwkv_pool_t pool, int split_tokens, int workers, int 
  * with the position.  (The pages store keys after this step and leave it to the caller.)  Pair i
  * of a row at position p, (a, b), becomes
  *     magnitude * (a cos t - b sin t, b cos t + a sin t),   t = p * freq[i],
- * in fp32, with the angle exact to 2^-23 rad at every position below 2^24, rounded once. */
+ * in fp32, with the angle exact to 2^-23 rad at every position (|freq| < 2^40), rounded once. */
 #define HWKV_ROPE_HALF 0         /* pairs (i, i + rot_dim / 2)                                   */
 #define HWKV_ROPE_INTERLEAVED 1  /* pairs (2 i, 2 i + 1)                                         */
 typedef struct hwkv_rope {

@@ -267,3 +267,27 @@ def test_fused_step_flags_negative_positions(kind, bs, group, softcap, first):
     # position 0 is a first token, not an error
     pool.append_decode(0, q, 0.125, kn, kn, pos * 0, softcap=softcap)
     assert pool.check_device_errors() == 0
+
+
+# ---- rotary positions: far angles ---------------------------------------------------------------------
+@pytest.mark.parametrize("pos", [1, 164864, 2 ** 24 - 2, 2 ** 30 + 12345, 2 ** 31 - 9])
+@pytest.mark.parametrize("top", [1.0, 6.0, 1e6, 1e9])
+def test_far_angles_are_exact(pos, top):
+    """The angle of position times frequency is good to 2^-23 rad whatever their sizes: cos and sin of it, two
+    units of fp32 (2^-23) from the function, are within 2^-22 of the exact product's."""
+    getcontext().prec = 80
+    pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534")
+    rng = np.random.default_rng(pos % 1000)
+    pool = hw.Pool(1, 1, 64, 16, [[16]], 1, torch.float32, q_heads=1)
+    table = hw.rope_table(64)
+    freqs = [float(f) for f in top * rng.uniform(-1.0, 1.0, 32)]
+    freqs[0], freqs[1] = top, -top
+    for i, f in enumerate(freqs):
+        table.freq[i] = f
+    x = torch.zeros((1, 8, 1, 64), device="cuda")
+    x[..., :32] = 1.0  # the output is (cos, sin)
+    got = pool.rope(table, None, x, torch.tensor([pos], dtype=torch.int32, device="cuda"))[1].cpu().double().numpy()
+    for i in range(8):
+        t = np.array([float((Decimal(pos + i) * Decimal(f)) % (2 * pi)) for f in freqs])
+        assert np.abs(got[0, i, 0, :32] - np.cos(t)).max() <= 2.0 ** -22
+        assert np.abs(got[0, i, 0, 32:] - np.sin(t)).max() <= 2.0 ** -22

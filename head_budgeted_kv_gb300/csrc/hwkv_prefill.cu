@@ -195,6 +195,14 @@ __device__ __forceinline__ float tree64(const float (&v)[kPfKeys], Op op) {
 // with these 296, 239 and 330).
 enum { kPlain = 0, kCap = 1, kBias = 2 };
 
+// The steepest slope: 2^17 log2 units per position.  A stage's keys share an offset of up to 64 slopes, which
+// their own terms cancel up to a few fp32 roundings of it: with this one a log2 unit or two, which one key's
+// weight and the sum it alone makes share; with 1e33 they would be infinite, and so would a slope divided by a small
+// scale.  No result changes while scores differ by less than this from key to key.  (Each key's distance
+// from the query itself, for warps with a slope above 16, costs every biased chunk 9%: 390 -> 426 us for 1024
+// tokens at 40000.)
+constexpr float kSteepest = 90852.f;
+
 template <int D, int SC>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap pool_map,
                                                                const __grid_constant__ CUtensorMap stage_map,
@@ -550,7 +558,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
     // divided by the scale, unless that is too small or negative
     const bool raw_bias = SC == kBias && a.scale_log2 > 0x1p-40f;
     const float sl2 = SC && !raw_bias ? 1.f : a.scale_log2;
-    const float slope = (SC & kBias) ? slope_log2(a.score, h * G + r % G) / sl2 : 0.f;  // in units of sl2
+    // in units of sl2
+    const float slope =
+        (SC & kBias) ? fminf(fmaxf(__ldg(a.score.slopes + h * G + r % G), -kSteepest), kSteepest) * 1.4426950408889634f / sl2 : 0.f;
     uint32_t run_word = 0u;  // SC: bit i: stage i of the next 32 holds 64 consecutive positions ...
     int run_first = 0;       // ... and, in lane i, its first key's position
     // with a positive scale the row maximum is taken on raw scores and scale-and-subtract is

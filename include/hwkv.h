@@ -310,7 +310,9 @@ int hwkv_prefill_attn(hwkv_pool_t pool, int layer, const void* q, int q_heads, f
                       void* workspace, uint64_t workspace_bytes, void* stream);
 
 /* hwkv_prefill_attn with a capped or distance-biased score (see hwkv_score_t; a query's position
- * is that of its token). */
+ * is that of its token).  The bias adds a few fp32 roundings of 64 slopes to a score's error, and a slope
+ * beyond +-2^17 / log2(e) (9.08e4) counts as that, which no result shows while the scores of neighbouring
+ * keys differ by less. */
 int hwkv_prefill_attn_score(hwkv_pool_t pool, int layer, const void* q, int q_heads, const hwkv_score_t* score,
                             const void* k_new, const void* v_new, int n_max, const int32_t* pos_dev,
                             const int32_t* n_dev, void* out, void* workspace, uint64_t workspace_bytes, void* stream);

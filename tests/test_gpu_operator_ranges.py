@@ -291,3 +291,34 @@ def test_far_angles_are_exact(pos, top):
         t = np.array([float((Decimal(pos + i) * Decimal(f)) % (2 * pi)) for f in freqs])
         assert np.abs(got[0, i, 0, :32] - np.cos(t)).max() <= 2.0 ** -22
         assert np.abs(got[0, i, 0, 32:] - np.sin(t)).max() <= 2.0 ** -22
+
+
+# ---- steep slopes and small scales --------------------------------------------------------------------
+@pytest.mark.parametrize("scale,slope", [(1e-6, 1e32), (1e-6, -1e32), (1e-11, 1e29), (0.125, 1e33), (1e-11, 3.0), (-0.125, 1e30)])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_steep_slopes_leave_one_key(scale, slope, softcap):
+    """A slope whose product with every distance is finite: the newest (or farthest) visible key alone counts,
+    in the chunk and in the decode step."""
+    D, w, n, n0 = 64, 150, 40, 333
+    pool = hw.Pool(1, 1, D, 16, [[w]], 1, torch.bfloat16, q_heads=2)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn((1, 1, n0 + n, D), generator=gen, device="cuda").bfloat16() for _ in range(2))
+    pos = torch.tensor([n0], dtype=torch.int32, device="cuda")
+    pool.materialize(0, k, v, pos)
+    q = torch.randn((1, n, 2, D), generator=gen, device="cuda").bfloat16()
+    kn, vn = (t[:, :, n0:].transpose(1, 2).contiguous() for t in (k, v))
+    slopes = torch.tensor([slope, slope / 4], device="cuda")
+    out = np64(pool.prefill(0, q, scale, kn, vn, pos, pos * 0 + n, softcap=softcap, slopes=slopes))[0]
+    last = np64(pool.decode(0, q[:, -1].contiguous(), scale, pos + n, softcap=softcap, slopes=slopes))[0]
+    for i in range(n):
+        at = n0 + i
+        p = np.arange(at + 1 - w, at + 1)
+        for g in range(2):
+            ref, mass, _ = attention(np64(q)[0, i, g], np64(k)[0, 0, p], np64(v)[0, 0, p], scale, at - p, softcap, float(slopes[g]))
+            # with the steep slopes one weight is 1 and the others 0; with those of 3 and 3/4 the scores stay below
+            # 700 log2 units, 8 roundings of which are 2^-11 of a weight (and of the sum); weights round to bf16
+            tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -10) * mass
+            assert (np.abs(out[i, g] - ref) <= tol).all(), (i, g)
+            if i == n - 1:
+                assert (np.abs(last[g] - ref) <= tol).all(), g
+    assert pool.check_device_errors() == 0

@@ -16,11 +16,12 @@ constexpr int kFlatMerge = 24;  // most contributors one CTA merges directly
 constexpr int kGapTiles = 24;
 
 // The threads that merge: the whole CTA, or its first N threads (those that consumed the tiles)
-// while a producer warp runs on.  Thread indices count from 0 in both.
+// while a producer warp runs on.  Thread indices count from 0 in both.  A whole CTA's number is read at
+// run time: given the constant the compiler unrolls the merges' loops, and the longer kernel costs batch 1 1%.
 struct CtaSync {
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kMergeCols = kThreads;  // most 4-float columns a head pass of a merge sums
-  static constexpr int kFold = 1;              // columns a thread folds together at a segment's end
+  static __device__ __forceinline__ unsigned threads() { return blockDim.x; }
   static __device__ __forceinline__ void sync() { __syncthreads(); }
   static __device__ __forceinline__ bool sync_and(bool p) { return __syncthreads_and(p) != 0; }
   static __device__ __forceinline__ bool sync_or(bool p) { return __syncthreads_or(p) != 0; }
@@ -32,7 +33,7 @@ struct PartSync {
   // a pass may hold more columns than threads: half the heads a pass would double the passes' round
   // trips (96 threads, 16 query heads of 128: 85 -> 80 us for a policy layer of 8-bit pools)
   static constexpr int kMergeCols = (N + 127) / 128 * 128;
-  static constexpr int kFold = 4;  // fewer threads: a head's weights serve four columns
+  static __device__ __forceinline__ unsigned threads() { return N; }
   static __device__ __forceinline__ void sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(N) : "memory"); }
   static __device__ __forceinline__ bool sync_and(bool p) {
     uint32_t r;
@@ -90,7 +91,7 @@ __device__ __forceinline__ void merge_slots_regs(const float* src_acc, const flo
                                                  float* dst_acc, float* dst_ml, long long dst_slot) {
   constexpr int kV = D / 4;  // float4 columns per query head
   constexpr int kBatch = 8;
-  for (int e = threadIdx.x; e < G * kV; e += Sync::kThreads) {
+  for (int e = threadIdx.x; e < G * kV; e += Sync::threads()) {
     const int q = e / kV, d4 = e - (e / kV) * kV;
     float M = kNegInf;
     for (int i0 = 0; i0 < count; i0 += kBatch) {
@@ -176,7 +177,7 @@ __device__ __forceinline__ void merge_slots_one(const float* src_acc, const floa
     for (uint32_t off = 0; off < bytes; off += kBulkChunk)
       bulk_load(smem_addr(ms.buf) + off, src + off, bytes - off < kBulkChunk ? bytes - off : kBulkChunk, ms.bar0);
   }
-  for (int p = threadIdx.x; p < count * G; p += Sync::kThreads) {
+  for (int p = threadIdx.x; p < count * G; p += Sync::threads()) {
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(src_ml) + first * G + p);
     s_ml[p] = ml.x;
     s_ml[count * G + p] = ml.y;
@@ -187,7 +188,7 @@ __device__ __forceinline__ void merge_slots_one(const float* src_acc, const floa
   if (!landed && threadIdx.x == 0) atomicOr(err, HWKV_DEVERR_WAIT_TIMEOUT);
   constexpr int kV = D / 4;  // float4 columns per query head
   const float4* sacc = reinterpret_cast<const float4*>(ms.buf);
-  for (int e = threadIdx.x; e < G * kV; e += Sync::kThreads) {
+  for (int e = threadIdx.x; e < G * kV; e += Sync::threads()) {
     const int q = e / kV, d4 = e - (e / kV) * kV;
     float M = kNegInf;
     for (int i = 0; i < count; ++i) M = fmaxf(M, s_ml[i * G + q]);
@@ -270,7 +271,7 @@ __device__ __forceinline__ void merge_slots_passes(const float* src_acc, const f
     issue(0);
     if (passes > 1) issue(1);
   }
-  for (int p = threadIdx.x; p < count * G; p += Sync::kThreads) {
+  for (int p = threadIdx.x; p < count * G; p += Sync::threads()) {
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(src_ml) + first * G + p);
     s_ml[p] = ml.x;
     s_ml[count * G + p] = ml.y;
@@ -281,7 +282,7 @@ __device__ __forceinline__ void merge_slots_passes(const float* src_acc, const f
   // the weighted sum of heads [p hp, (p + 1) hp) out of the buffer half holding pass p
   auto sum_pass = [&](int p, bool landed) {
     const float4* sacc = reinterpret_cast<const float4*>(ms.buf) + (size_t)(p & 1) * (ms.bytes / 32u);
-    for (int e = threadIdx.x; e < hp * kV; e += Sync::kThreads) {
+    for (int e = threadIdx.x; e < hp * kV; e += Sync::threads()) {
       const int ql = e / kV, d4 = e - (e / kV) * kV;
       const int q = p * hp + ql;
       float M = kNegInf;
@@ -377,121 +378,58 @@ __host__ __device__ constexpr int merge_heads() {
   return GP < 8 ? GP : (D == 128 ? 4 : 8);
 }
 
-// The end of a CTA's segment [seg_begin, seg_end) of group sg (whose boundary sits at spre on the
-// line of T positions): the consuming warps' states are merged in shared memory (sc_m, sc_l,
-// sc_acc) into the group's output, or into this CTA's partial, which the group's last arriver
-// merges with the others.  `more`: the CTA has another segment; `failed`: this thread's warp gave
-// up a wait.  SG: query heads merged per pass.  smem: the stage buffers, free after the last segment.
-template <typename Out, int D, int GP, int SG, typename Sync, int Gap, typename State>
-__device__ __forceinline__ void end_segment(const DecodeArgs& a, State& ws, const Group& sgr, int sg, long long spre,
-                                            long long seg_begin, long long seg_end, long long T, int nctas, int cta,
-                                            bool more, bool failed, uint8_t* smem, float* sc_m, float* sc_l,
-                                            float* sc_acc, int* s_last, MergeStage& ms) {
-  constexpr int W = Sync::kThreads / 32;
-  constexpr int NT = State::NT;                 // 8-column groups of query heads
-  constexpr int kPasses = GP < 8 ? 1 : 8 / SG;  // passes per 8-column group
+// After a CTA's partial of group sg (boundary at spre on the line of T positions) is written: the
+// group's last arriver merges it with the others into the output.  `more`: the CTA has another
+// segment; `failed`: this thread's warp gave up a wait.  SG: query heads the scratch sc_acc holds per
+// warp.  smem: the stage buffers, free after the last segment.
+template <typename Out, int D, int GP, int SG, typename Sync, int Gap>
+__device__ __forceinline__ void join_group(const DecodeArgs& a, const Group& sgr, int sg, long long spre, long long T,
+                                           int nctas, int cta, bool more, bool failed, uint8_t* smem, float* sc_acc,
+                                           int* s_last, MergeStage& ms) {
   // the partial merge's (m, l) scratch reuses the warps' merge area: 2 * slots * G floats
-  constexpr int kMlCap = W * SG * D;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kMlCap = (Sync::kThreads / 32) * SG * D;
   const int G = a.group;
   const int Hq = a.pv.kv_heads * G;
   Out* const out = static_cast<Out*>(a.out);
-  ws.finish();
-  const bool whole = seg_begin == spre + Gap && seg_end == spre + group_span<Gap>(sgr);
-  const long long slot = (long long)sg + cta;  // unique per (group, CTA) along the line
-  // pass (nt, hh): the warps' states of query heads [8*nt + hh*SG, 8*nt + (hh+1)*SG) meet in
-  // shared memory and are folded into the output or this CTA's partial
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-  for (int hh = 0; hh < kPasses; ++hh) {
-    if (nt > 0 || hh > 0) Sync::sync();  // the previous pass has read the scratch
-    ws.template publish<SG>(nt, hh, warp, lane, sc_m, sc_l, sc_acc);
-    Sync::sync();
-    const int g0 = 8 * nt + hh * SG;
-    const int ng = min(SG, G - g0);  // real query heads of this pass
-    constexpr int F = Sync::kFold;
-    for (int e = threadIdx.x * F; e < ng * D; e += Sync::kThreads * F) {
-      const int gl = e / D, d = e - (e / D) * D;
-      const int g = g0 + gl;
-      float M = kNegInf;
-#pragma unroll
-      for (int w = 0; w < W; ++w) M = fmaxf(M, sc_m[w * SG + gl]);
-      float Ls = 0.f, A[F] = {};
-      if (M != kNegInf) {
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const float f = ex2(sc_m[w * SG + gl] - M);
-          Ls += sc_l[w * SG + gl] * f;
-          const float* acc = sc_acc + (w * SG + gl) * D + d;
-          if constexpr (F == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(acc);
-            A[0] += v.x * f;
-            A[1] += v.y * f;
-            A[2] += v.z * f;
-            A[3] += v.w * f;
-          } else {
-            A[0] += acc[0] * f;
-          }
-        }
-      }
-      if (whole) {
-        if constexpr (F == 4)
-          store_merged<Out, D>(M, Ls, make_float4(A[0], A[1], A[2], A[3]), g, d / 4, G,
-                               out + ((int64_t)sgr.s * Hq + sgr.h * G) * D, nullptr, nullptr, 0);
-        else
-          store_out<Out>(out + ((int64_t)sgr.s * Hq + sgr.h * G + g) * D + d, Ls > 0.f ? A[0] / Ls : 0.f);
-      } else {
-        if constexpr (F == 4) *reinterpret_cast<float4*>(a.part_acc + (slot * G + g) * D + d) = make_float4(A[0], A[1], A[2], A[3]);
-        else a.part_acc[(slot * G + g) * D + d] = A[0];
-        if (d == 0) {
-          a.part_ml[(slot * G + g) * 2 + 0] = M;
-          a.part_ml[(slot * G + g) * 2 + 1] = Ls;
-        }
-      }
+  // The partial is published; count arrivals.  Up to kFlatMerge contributors: the last
+  // CTA of the group merges them all.  More (long windows at small batch): blocks of
+  // kMergeBlock consecutive contributors are merged by their last arriver into a second-
+  // level partial, and the last of those merges the blocks (one level of ~100 partials,
+  // streamed through the stage buffers in chunks by one CTA, was slower at batch 1: 877
+  // against 955 tokens/s; it moves ~200 KB through one SM where the tree spreads it).
+  // After the last segment no copy is in flight (unless a wait timed out): merges may
+  // stage partial blocks in the stage buffers.
+  if (!more) ms.buf = Sync::sync_or(failed) ? nullptr : reinterpret_cast<float*>(smem);
+  const int c_lo = cta_of(spre + Gap, T, nctas), c_hi = cta_of(spre + group_span<Gap>(sgr) - 1, T, nctas);
+  const bool all_live = T >= nctas;  // then no CTA range is empty
+  const int k = c_hi - c_lo + 1;
+  Out* const out_grp = out + ((int64_t)sgr.s * Hq + sgr.h * G) * D;
+  if (!all_live || k <= kFlatMerge) {
+    int expected = k;
+    if (!all_live) {
+      expected = 0;
+      for (int c = c_lo; c <= c_hi; ++c) expected += range_start(T, c + 1, nctas) > range_start(T, c, nctas);
     }
-  }
-  if (!whole) {
-    // The partial is published; count arrivals.  Up to kFlatMerge contributors: the last
-    // CTA of the group merges them all.  More (long windows at small batch): blocks of
-    // kMergeBlock consecutive contributors are merged by their last arriver into a second-
-    // level partial, and the last of those merges the blocks (one level of ~100 partials,
-    // streamed through the stage buffers in chunks by one CTA, was slower at batch 1: 877
-    // against 955 tokens/s; it moves ~200 KB through one SM where the tree spreads it).
-    // After the last segment no copy is in flight (unless a wait timed out): merges may
-    // stage partial blocks in the stage buffers.
-    if (!more) ms.buf = Sync::sync_or(failed) ? nullptr : reinterpret_cast<float*>(smem);
-    const int c_lo = cta_of(spre + Gap, T, nctas), c_hi = cta_of(spre + group_span<Gap>(sgr) - 1, T, nctas);
-    const bool all_live = T >= nctas;  // then no CTA range is empty
-    const int k = c_hi - c_lo + 1;
-    Out* const out_grp = out + ((int64_t)sgr.s * Hq + sgr.h * G) * D;
-    if (!all_live || k <= kFlatMerge) {
-      int expected = k;
-      if (!all_live) {
-        expected = 0;
-        for (int c = c_lo; c <= c_hi; ++c) expected += range_start(T, c + 1, nctas) > range_start(T, c, nctas);
-      }
-      if (arrive_last<Sync>(&a.counters[sg], expected, s_last)) {
-        auto live = [&](int i) {
-          return all_live || range_start(T, c_lo + i + 1, nctas) > range_start(T, c_lo + i, nctas);
-        };
-        merge_slots<Out, D, GP, Sync>(a.part_acc, a.part_ml, (long long)sg + c_lo, k, G, live, all_live, out_grp, nullptr,
-                       nullptr, 0, sc_acc, kMlCap, ms, a.pv.err);
-      }
-    } else {
-      auto live = [](int) { return true; };
-      const int nb = (k + kMergeBlock - 1) / kMergeBlock;
-      const int b = (cta - c_lo) / kMergeBlock;
-      const int b_lo = c_lo + b * kMergeBlock;
-      const int b_n = min(kMergeBlock, c_hi - b_lo + 1);
-      const long long slot2 = (long long)sg * a.merge_blocks + b;
-      if (arrive_last<Sync>(&a.counters1[slot2], b_n, s_last)) {
-        merge_slots<Out, D, GP, Sync>(a.part_acc, a.part_ml, (long long)sg + b_lo, b_n, G, live, true, (Out*)nullptr, a.part2_acc,
-                       a.part2_ml, slot2, sc_acc, kMlCap, ms, a.pv.err);
-        if (arrive_last<Sync>(&a.counters[sg], nb, s_last))
-          merge_slots<Out, D, GP, Sync>(a.part2_acc, a.part2_ml, (long long)sg * a.merge_blocks, nb, G, live, true, out_grp,
-                         nullptr, nullptr, 0, sc_acc, kMlCap, ms, a.pv.err);
-      }
+    if (arrive_last<Sync>(&a.counters[sg], expected, s_last)) {
+      auto live = [&](int i) {
+        return all_live || range_start(T, c_lo + i + 1, nctas) > range_start(T, c_lo + i, nctas);
+      };
+      merge_slots<Out, D, GP, Sync>(a.part_acc, a.part_ml, (long long)sg + c_lo, k, G, live, all_live, out_grp, nullptr,
+                     nullptr, 0, sc_acc, kMlCap, ms, a.pv.err);
+    }
+  } else {
+    auto live = [](int) { return true; };
+    const int nb = (k + kMergeBlock - 1) / kMergeBlock;
+    const int b = (cta - c_lo) / kMergeBlock;
+    const int b_lo = c_lo + b * kMergeBlock;
+    const int b_n = min(kMergeBlock, c_hi - b_lo + 1);
+    const long long slot2 = (long long)sg * a.merge_blocks + b;
+    if (arrive_last<Sync>(&a.counters1[slot2], b_n, s_last)) {
+      merge_slots<Out, D, GP, Sync>(a.part_acc, a.part_ml, (long long)sg + b_lo, b_n, G, live, true, (Out*)nullptr, a.part2_acc,
+                     a.part2_ml, slot2, sc_acc, kMlCap, ms, a.pv.err);
+      if (arrive_last<Sync>(&a.counters[sg], nb, s_last))
+        merge_slots<Out, D, GP, Sync>(a.part2_acc, a.part2_ml, (long long)sg * a.merge_blocks, nb, G, live, true, out_grp,
+                       nullptr, nullptr, 0, sc_acc, kMlCap, ms, a.pv.err);
     }
   }
 }

@@ -93,6 +93,63 @@ __device__ __forceinline__ bool q8_wait(uint64_t* bar, uint32_t parity, volatile
   }
 }
 
+// The end of a CTA's segment [seg_begin, seg_end) of group sg (whose boundary sits at spre on the
+// line of T positions): the consuming warps' states are merged in shared memory (sc_m, sc_l,
+// sc_acc) into the group's output, or into this CTA's partial, which join_group takes on.  A thread folds
+// four columns at a time: fewer threads than a whole CTA, so a head's weights serve four.
+template <int D, int GP, typename Sync, typename State>
+__device__ __forceinline__ void end_segment(const DecodeArgs& a, State& ws, const Group& sgr, int sg, long long spre,
+                                            long long seg_begin, long long seg_end, long long T, int nctas, int cta,
+                                            bool more, bool failed, uint8_t* smem, float* sc_m, float* sc_l,
+                                            float* sc_acc, int* s_last, MergeStage& ms) {
+  constexpr int W = Sync::kThreads / 32;
+  constexpr int SG = q8_merge_heads<GP>();      // query heads merged per pass
+  constexpr int NT = State::NT;                 // 8-column groups of query heads
+  constexpr int kPasses = GP < 8 ? 1 : 8 / SG;  // passes per 8-column group
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.group;
+  ws.finish();
+  const bool whole = seg_begin == spre + kGap && seg_end == spre + group_span<kGap>(sgr);
+  const long long slot = (long long)sg + cta;  // unique per (group, CTA) along the line
+  __nv_bfloat16* const out_grp = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)sgr.s * a.pv.kv_heads + sgr.h) * G * D;
+  // pass (nt, hh): the warps' states of query heads [8*nt + hh*SG, 8*nt + (hh+1)*SG) meet in
+  // shared memory and are folded into the output or this CTA's partial
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+  for (int hh = 0; hh < kPasses; ++hh) {
+    if (nt > 0 || hh > 0) Sync::sync();  // the previous pass has read the scratch
+    ws.template publish<SG>(nt, hh, warp, lane, sc_m, sc_l, sc_acc);
+    Sync::sync();
+    const int g0 = 8 * nt + hh * SG;
+    const int ng = min(SG, G - g0);  // real query heads of this pass
+    for (int e = threadIdx.x * 4; e < ng * D; e += Sync::kThreads * 4) {
+      const int gl = e / D, d = e - (e / D) * D;
+      const int g = g0 + gl;
+      float M = kNegInf;
+#pragma unroll
+      for (int w = 0; w < W; ++w) M = fmaxf(M, sc_m[w * SG + gl]);
+      float Ls = 0.f;
+      float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (M != kNegInf) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float f = ex2(sc_m[w * SG + gl] - M);
+          Ls += sc_l[w * SG + gl] * f;
+          const float4 v = *reinterpret_cast<const float4*>(sc_acc + (w * SG + gl) * D + d);
+          A.x += v.x * f;
+          A.y += v.y * f;
+          A.z += v.z * f;
+          A.w += v.w * f;
+        }
+      }
+      store_merged<__nv_bfloat16, D>(M, Ls, A, g, d / 4, G, whole ? out_grp : nullptr, a.part_acc, a.part_ml, slot);
+    }
+  }
+  if (!whole)
+    join_group<__nv_bfloat16, D, GP, SG, Sync, kGap>(a, sgr, sg, spre, T, nctas, cta, more, failed, smem, sc_acc, s_last, ms);
+}
+
 template <int D, int GP, bool SC>
 __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ DecodeArgs a) {
@@ -336,8 +393,8 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
       if (lane == 0) mbar_arrive_one(&empty[st]);
     }
     const long long seg_begin = spre + kGap + first;
-    end_segment<__nv_bfloat16, D, GP, SG, Sync, kGap>(a, ws, sgr, sg, spre, seg_begin, seg_begin + count, T, nctas, cta, more, !ok,
-                                            smem, sc_m, sc_l, sc_acc, &s_last, ms);
+    end_segment<D, GP, Sync>(a, ws, sgr, sg, spre, seg_begin, seg_begin + count, T, nctas, cta, more, !ok, smem, sc_m,
+                             sc_l, sc_acc, &s_last, ms);
     Sync::sync();  // the merge scratch is rewritten by the next segment
     if (!more) break;
     stage0 += nstages;

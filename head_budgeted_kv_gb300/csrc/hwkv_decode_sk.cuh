@@ -72,7 +72,9 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
   constexpr int kEB = (int)sizeof(Elem);
   constexpr int kTileBytes = kTile * D * kEB;  // 16 rows
   constexpr int kStageBytes = 2 * kTileBytes;  // K tile + V tile
+  constexpr int NT = State::NT;                 // 8-column groups of query heads
   constexpr int SG = merge_heads<D, GP>();      // query heads merged per pass in shared memory
+  constexpr int kPasses = GP < 8 ? 1 : 8 / SG;  // passes per 8-column group
 
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -271,8 +273,50 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
       j_cons += W;
     }
 
-    end_segment<Elem, D, GP, SG, CtaSync, kGapTiles>(a, ws, sgr, sg, spre, seg_begin, seg_end, T, nctas, cta, more, drain_from >= 0, smem,
-                                      sc_m, sc_l, sc_acc, &s_last, ms);
+    // ---- end of segment: merge the warps, then store output or partial -----------------
+    // (in place: as a function shared with the 8-bit kernel it cost batch 1 0.5%)
+    ws.finish();
+    const bool whole = seg_begin == spre + kGapTiles && seg_end == spre + group_span(sgr);
+    const long long slot = (long long)sg + cta;  // unique per (group, CTA) along the line
+    // pass (nt, hh): the warps' states of query heads [8*nt + hh*SG, 8*nt + (hh+1)*SG) meet in
+    // shared memory and are folded into the output or this CTA's partial
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int hh = 0; hh < kPasses; ++hh) {
+      if (nt > 0 || hh > 0) __syncthreads();  // the previous pass has read the scratch
+      ws.template publish<SG>(nt, hh, warp, lane, sc_m, sc_l, sc_acc);
+      __syncthreads();
+      const int g0 = 8 * nt + hh * SG;
+      const int ng = min(SG, G - g0);  // real query heads of this pass
+      for (int e = threadIdx.x; e < ng * D; e += W * 32) {
+        const int gl = e / D, d = e - (e / D) * D;
+        const int g = g0 + gl;
+        float M = kNegInf;
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, sc_m[w * SG + gl]);
+        float Ls = 0.f, A = 0.f;
+        if (M != kNegInf) {
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const float f = ex2(sc_m[w * SG + gl] - M);
+            Ls += sc_l[w * SG + gl] * f;
+            A += sc_acc[(w * SG + gl) * D + d] * f;
+          }
+        }
+        if (whole) {
+          store_out<Elem>(out + ((int64_t)sgr.s * Hq + sgr.h * G + g) * D + d, Ls > 0.f ? A / Ls : 0.f);
+        } else {
+          a.part_acc[(slot * G + g) * D + d] = A;
+          if (d == 0) {
+            a.part_ml[(slot * G + g) * 2 + 0] = M;
+            a.part_ml[(slot * G + g) * 2 + 1] = Ls;
+          }
+        }
+      }
+    }
+    if (!whole)
+      join_group<Elem, D, GP, SG, CtaSync, kGapTiles>(a, sgr, sg, spre, T, nctas, cta, more, drain_from >= 0, smem, sc_acc, &s_last, ms);
     __syncthreads();  // the merge scratch is rewritten by the next segment
     if (!more) break;
     do {

@@ -261,16 +261,6 @@ struct E4m3 {
   uint8_t code;
 };
 
-// the element type of the tensors passed with a pool of T: queries, new rows, outputs
-template <typename T_>
-struct IoType {
-  using T = T_;
-};
-template <>
-struct IoType<E4m3> {
-  using T = __nv_bfloat16;
-};
-
 template <typename T>
 __device__ __forceinline__ void store_out(T* p, float x);
 template <>

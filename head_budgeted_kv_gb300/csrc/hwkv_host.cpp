@@ -1274,6 +1274,7 @@ int hwkv_set_decode_config(hwkv_pool_t p, int split_tokens, int workers, int ker
 int hwkv_seqcalib(int layers, int kv_heads, int head_dim, int block_size, int num_seqs, int dtype,
                   int num_candidates, const int32_t* candidates, hwkv_distortion_fn distortion, void* user,
                   uint64_t budget_bytes, int32_t* out_windows, int32_t* out_choice, uint64_t* out_bytes) {
+  if (layers < 0) return fail(HWKV_ERR_INVALID_ARG, "layers must not be negative (got %d)", layers);
   if (num_candidates < 1) return fail(HWKV_ERR_INVALID_ARG, "num_candidates must be >= 1");
   if (!candidates || !distortion || !out_windows) return fail(HWKV_ERR_INVALID_ARG, "NULL argument");
   // every candidate must be a valid window vector; its cost is the one-layer pool footprint, of

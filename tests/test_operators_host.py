@@ -58,6 +58,18 @@ def test_seqcalib_of_8_bit_layers_predicts_the_pool(lib):
     assert e.value.status == binding.HWKV_ERR_BUDGET
 
 
+def test_seqcalib_refuses_a_negative_count_of_layers(lib):
+    """A status, as from every entry point: sizing its tables from the count would throw across the C boundary."""
+    cand = np.ones((1, 1, 1), dtype=np.int32)
+    out = np.zeros(1, dtype=np.int32)
+    fn = binding.DISTORTION_FN(lambda *a: 0.0)
+    p = cand.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
+    for layers in (-1, -(2 ** 31)):
+        rc = lib.hwkv_seqcalib(layers, 1, 64, 16, 1, binding.HWKV_BF16, 1, p, fn, None, 1 << 20,
+                               out.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), None, None)
+        assert rc == binding.HWKV_ERR_INVALID_ARG
+
+
 def test_reference_codes_are_torchs_codes():
     """The reference's rounding to e4m3 is the nearest one with ties to even, as torch's cast has it."""
     gen = torch.Generator().manual_seed(0)

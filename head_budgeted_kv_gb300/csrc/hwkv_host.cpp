@@ -21,6 +21,7 @@
 #include <new>
 #include <string>
 #include <tuple>
+#include <utility>
 #include <vector>
 
 #include "hwkv_internal.h"
@@ -203,6 +204,8 @@ struct hwkv_pool {
   // arrival counters of the tensor-core kernel, all kept at 0 between launches:
   // [layers][groups] final counters, then [layers][groups][merge_blocks] first-level ones
   uint32_t* d_counters = nullptr;
+  // outgrown counters and their numbers, kept: a captured graph may still count in them
+  std::vector<std::pair<uint32_t*, size_t>> old_counters;
   int counter_merge_blocks = 0;
   std::vector<int32_t> h_tbl;
   int device = 0;
@@ -461,6 +464,10 @@ WorkspaceLayout workspace_layout(const hwkv_pool* p, int group) {
 
 uint64_t workspace_bytes(const hwkv_pool* p, int group) { return workspace_layout(p, group).total; }
 
+size_t counter_count(const hwkv_pool* p) {
+  return (size_t)p->g.layers * p->g.num_seqs * p->g.kv_heads * (1 + (size_t)p->counter_merge_blocks);
+}
+
 // (Re)allocates the arrival counters for the current grid size, zeroed.
 int ensure_counters(hwkv_pool* p) {
   const int mb = merge_blocks_for(max_tc_workers(p));
@@ -474,17 +481,10 @@ int ensure_counters(hwkv_pool* p) {
     cudaFree(c);
     return fail(HWKV_ERR_CUDA, "cudaMemset of the arrival counters: %s", cudaGetErrorString(e));
   }
-  if (p->d_counters) {
-    cudaDeviceSynchronize();  // no launch may still use the old counters
-    cudaFree(p->d_counters);
-  }
+  if (p->d_counters) p->old_counters.emplace_back(p->d_counters, counter_count(p));
   p->d_counters = c;
   p->counter_merge_blocks = mb;
   return HWKV_OK;
-}
-
-size_t counter_count(const hwkv_pool* p) {
-  return (size_t)p->g.layers * p->g.num_seqs * p->g.kv_heads * (1 + (size_t)p->counter_merge_blocks);
 }
 
 int check_device(const hwkv_pool* p) {
@@ -699,6 +699,7 @@ int hwkv_pool_create(int layers, int kv_heads, int head_dim, int block_size, con
 int hwkv_pool_destroy(hwkv_pool_t p) {
   if (!p) return ok();
   if (p->d_counters) cudaFree(p->d_counters);
+  for (const auto& c : p->old_counters) cudaFree(c.first);
   cudaError_t e = cudaFree(p->d_meta);
   delete p;
   if (e != cudaSuccess) return fail(HWKV_ERR_CUDA, "cudaFree: %s", cudaGetErrorString(e));
@@ -1337,6 +1338,8 @@ int hwkv_check_device_errors(hwkv_pool_t p, void* stream, int32_t* out_bits) {
     // an aborted launch can leave arrival counters behind: start the next launch from zero
     if (p->d_counters)
       HWKV_CUDA_TRY(cudaMemset(p->d_counters, 0, counter_count(p) * sizeof(uint32_t)), "reset of the arrival counters");
+    for (const auto& c : p->old_counters)
+      HWKV_CUDA_TRY(cudaMemset(c.first, 0, c.second * sizeof(uint32_t)), "reset of the arrival counters");
     return fail(HWKV_ERR_DEVICE_CHECK, "device error bits 0x%x", bits);
   }
   return ok();

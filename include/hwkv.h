@@ -348,7 +348,8 @@ int hwkv_set_prefill_config(hwkv_pool_t pool, int max_stages);
  * the tensor-core kernel's persistent grid (0 = automatic: every SM, as many CTAs as fit; 95% of
  * that when a layer's ring capacity is under 128 16-token tiles per CTA, so the next launch's
  * first CTAs find free slots).
- * Changes the workspace size.  Results differ between configurations only by rounding. */
+ * Changes the workspace size.  Results differ between configurations only by rounding.  Graphs captured
+ * before keep their configuration, their workspace and the library's counters. */
 int hwkv_set_decode_config(hwkv_pool_t pool, int split_tokens, int workers, int kernel);
 
 /* Rotary positions: before a key is appended and a query attends, the pairs of their rows turn

@@ -322,3 +322,34 @@ def test_steep_slopes_leave_one_key(scale, slope, softcap):
             if i == n - 1:
                 assert (np.abs(last[g] - ref) <= tol).all(), g
     assert pool.check_device_errors() == 0
+
+
+# ---- captured graphs beside later calls that need more room ------------------------------------------
+@pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
+def test_captured_decode_outlives_a_larger_configuration(kind):
+    """A graph captured before the grid (and with it the arrival counters) grew counts in what it was captured
+    with, and gives the same bits."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    pool = hw.Pool(1, 2, 64, 16, [[3000, 64]], 2, TYPES[kind], q_heads=8)
+    pool.set_decode_config(workers=20)
+    k = torch.randn((2, 2, 3100, 64), generator=gen, device="cuda").to(pool.io_dtype)
+    lens = torch.tensor([3100, 700], dtype=torch.int32, device="cuda")
+    pool.materialize(0, k, k, lens)
+    q = torch.randn((2, 8, 64), generator=gen, device="cuda").to(pool.io_dtype)
+    out = torch.empty_like(q)
+    want = pool.decode(0, q, 0.125, lens).clone()
+    pool.decode(0, q, 0.125, lens, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pool.decode(0, q, 0.125, lens, out=out)
+    keep = pool.workspace  # the captured launch's
+    pool.set_decode_config(workers=3000)
+    wide = pool.decode(0, q, 0.125, lens)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want)
+        assert torch.equal(pool.decode(0, q, 0.125, lens), wide)
+    assert keep is not None and pool.check_device_errors() == 0
+    pool.close()

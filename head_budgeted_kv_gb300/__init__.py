@@ -86,11 +86,15 @@ class Pool:
             self._scales = area.view(torch.float32).view(total, groups, 2)
         self.workspace = None
         self.prefill_workspace = None
+        self._prefill_captured = False
+        self._outgrown = []  # workspaces that captured graphs may still use
         self._size_workspace()
 
     def _size_workspace(self):
         need = hwkv_decode_workspace_bytes(self.handle, self.q_heads)
         if self.workspace is None or self.workspace.numel() < need:
+            if self.workspace is not None:  # seldom: the group or the configuration grew
+                self._outgrown.append(self.workspace)
             self.workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=self.buffer.device)
 
     def set_decode_config(self, split_tokens: int = 0, kernel: int = HWKV_KERNEL_AUTO, workers: int = 0):
@@ -185,13 +189,19 @@ class Pool:
                 slopes=None):
         """Chunked prefill: q [B][n_max][Hq][D], k_new/v_new [B][n_max][Hkv][D]; pos, n int32 [B];
         softcap, slopes: as ``decode``.
-        Keeps a workspace for the split of long key streams, grown on demand."""
+        Keeps a workspace for the split of long key streams, grown on demand; one that a capture has
+        used stays when it is outgrown."""
         if out is None:
             out = torch.zeros_like(q)
         need = hwkv_prefill_workspace_bytes(self.handle, layer, q.shape[2], q.shape[1])
         if need and (self.prefill_workspace is None or self.prefill_workspace.numel() < need):
+            if self._prefill_captured:
+                self._outgrown.append(self.prefill_workspace)
+                self._prefill_captured = False
             self.prefill_workspace = torch.empty(need, dtype=torch.uint8, device=self.buffer.device)
         workspace = self.prefill_workspace if need else None
+        if need and torch.cuda.is_current_stream_capturing():
+            self._prefill_captured = True
         if softcap == 0 and slopes is None:
             hwkv_prefill_attn(self.handle, layer, q, scale, k_new, v_new, pos, n, out, workspace, stream)
         else:

@@ -8,6 +8,7 @@ normalised by.  A product w_p v_scale_p below fp16's normal range is off by an a
 instead: the kernel holds it times 2^11 / ref with ref between half of the head's largest such product
 and that product (a lagging reference makes what it holds larger), steps below 2^-14 are 2^-24, so half of
 one is 2^-25 and the output is off by at most 2^-36 max(w_p v_scale_p) sum_p |c_p|."""
+import weakref
 from decimal import Decimal, getcontext
 
 import numpy as np
@@ -353,3 +354,53 @@ def test_captured_decode_outlives_a_larger_configuration(kind):
         assert torch.equal(pool.decode(0, q, 0.125, lens), wide)
     assert keep is not None and pool.check_device_errors() == 0
     pool.close()
+
+
+def test_captured_calls_keep_their_workspaces():
+    """A pool's workspaces that captured launches use stay when later calls need larger ones; others go."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    pool = hw.Pool(1, 2, 64, 16, [[3000, 64]], 1, torch.bfloat16, q_heads=4)
+    k = torch.randn((1, 2, 3100, 64), generator=gen, device="cuda").bfloat16()
+    lens = torch.tensor([3100], dtype=torch.int32, device="cuda")
+    pool.materialize(0, k, k, lens)
+    q = torch.randn((1, 4, 64), generator=gen, device="cuda").bfloat16()
+    out = torch.empty_like(q)
+    want = pool.decode(0, q, 0.125, lens).clone()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        pool.decode(0, q, 0.125, lens, out=out)
+    used = weakref.ref(pool.workspace)
+    pool.decode(0, q.repeat(1, 8, 1), 0.125, lens)  # a larger group
+    assert pool.workspace is not used() and used() is not None
+    graph.replay()
+    assert torch.equal(out, want)
+
+    # chunks: the workspace of splits grows with the chunk
+    pool.set_prefill_config(4)
+    chunk = torch.randn((1, 300, 4, 64), generator=gen, device="cuda").bfloat16()
+    kn = torch.randn((1, 300, 2, 64), generator=gen, device="cuda").bfloat16()
+
+    def call(n, into=None):
+        return pool.prefill(0, chunk[:, :n].contiguous(), 0.125, kn[:, :n].contiguous(), kn[:, :n].contiguous(), lens, lens * 0 + n,
+                            out=into)
+
+    call(20)
+    plain = weakref.ref(pool.prefill_workspace)
+    call(60)
+    assert pool.prefill_workspace.numel() > 0 and plain() is None  # no capture used it
+    args = [t[:, :60].contiguous() for t in (chunk, kn, kn)]
+    n60, into = lens * 0 + 60, torch.zeros((1, 60, 4, 64), device="cuda").bfloat16()
+    pool.materialize(0, k, k, lens)  # the ring as it was before the chunks
+    want = pool.prefill(0, args[0], 0.125, args[1], args[2], lens, n60).clone()
+    torch.cuda.synchronize()
+    graph2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph2):
+        pool.prefill(0, args[0], 0.125, args[1], args[2], lens, n60, out=into)
+    used = weakref.ref(pool.prefill_workspace)
+    call(300)
+    assert pool.prefill_workspace is not used() and used() is not None
+    pool.materialize(0, k, k, lens)
+    graph2.replay()
+    assert torch.equal(into, want)
+    assert pool.check_device_errors() == 0

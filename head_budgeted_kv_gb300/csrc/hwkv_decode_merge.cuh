@@ -378,61 +378,5 @@ __host__ __device__ constexpr int merge_heads() {
   return GP < 8 ? GP : (D == 128 ? 4 : 8);
 }
 
-// After a CTA's partial of group sg (boundary at spre on the line of T positions) is written: the
-// group's last arriver merges it with the others into the output.  `more`: the CTA has another
-// segment; `failed`: this thread's warp gave up a wait.  SG: query heads the scratch sc_acc holds per
-// warp.  smem: the stage buffers, free after the last segment.
-template <typename Out, int D, int GP, int SG, typename Sync, int Gap>
-__device__ __forceinline__ void join_group(const DecodeArgs& a, const Group& sgr, int sg, long long spre, long long T,
-                                           int nctas, int cta, bool more, bool failed, uint8_t* smem, float* sc_acc,
-                                           int* s_last, MergeStage& ms) {
-  // the partial merge's (m, l) scratch reuses the warps' merge area: 2 * slots * G floats
-  constexpr int kMlCap = (Sync::kThreads / 32) * SG * D;
-  const int G = a.group;
-  const int Hq = a.pv.kv_heads * G;
-  Out* const out = static_cast<Out*>(a.out);
-  // The partial is published; count arrivals.  Up to kFlatMerge contributors: the last
-  // CTA of the group merges them all.  More (long windows at small batch): blocks of
-  // kMergeBlock consecutive contributors are merged by their last arriver into a second-
-  // level partial, and the last of those merges the blocks (one level of ~100 partials,
-  // streamed through the stage buffers in chunks by one CTA, was slower at batch 1: 877
-  // against 955 tokens/s; it moves ~200 KB through one SM where the tree spreads it).
-  // After the last segment no copy is in flight (unless a wait timed out): merges may
-  // stage partial blocks in the stage buffers.
-  if (!more) ms.buf = Sync::sync_or(failed) ? nullptr : reinterpret_cast<float*>(smem);
-  const int c_lo = cta_of(spre + Gap, T, nctas), c_hi = cta_of(spre + group_span<Gap>(sgr) - 1, T, nctas);
-  const bool all_live = T >= nctas;  // then no CTA range is empty
-  const int k = c_hi - c_lo + 1;
-  Out* const out_grp = out + ((int64_t)sgr.s * Hq + sgr.h * G) * D;
-  if (!all_live || k <= kFlatMerge) {
-    int expected = k;
-    if (!all_live) {
-      expected = 0;
-      for (int c = c_lo; c <= c_hi; ++c) expected += range_start(T, c + 1, nctas) > range_start(T, c, nctas);
-    }
-    if (arrive_last<Sync>(&a.counters[sg], expected, s_last)) {
-      auto live = [&](int i) {
-        return all_live || range_start(T, c_lo + i + 1, nctas) > range_start(T, c_lo + i, nctas);
-      };
-      merge_slots<Out, D, GP, Sync>(a.part_acc, a.part_ml, (long long)sg + c_lo, k, G, live, all_live, out_grp, nullptr,
-                     nullptr, 0, sc_acc, kMlCap, ms, a.pv.err);
-    }
-  } else {
-    auto live = [](int) { return true; };
-    const int nb = (k + kMergeBlock - 1) / kMergeBlock;
-    const int b = (cta - c_lo) / kMergeBlock;
-    const int b_lo = c_lo + b * kMergeBlock;
-    const int b_n = min(kMergeBlock, c_hi - b_lo + 1);
-    const long long slot2 = (long long)sg * a.merge_blocks + b;
-    if (arrive_last<Sync>(&a.counters1[slot2], b_n, s_last)) {
-      merge_slots<Out, D, GP, Sync>(a.part_acc, a.part_ml, (long long)sg + b_lo, b_n, G, live, true, (Out*)nullptr, a.part2_acc,
-                     a.part2_ml, slot2, sc_acc, kMlCap, ms, a.pv.err);
-      if (arrive_last<Sync>(&a.counters[sg], nb, s_last))
-        merge_slots<Out, D, GP, Sync>(a.part2_acc, a.part2_ml, (long long)sg * a.merge_blocks, nb, G, live, true, out_grp,
-                       nullptr, nullptr, 0, sc_acc, kMlCap, ms, a.pv.err);
-    }
-  }
-}
-
 }  // namespace
 }  // namespace hwkv

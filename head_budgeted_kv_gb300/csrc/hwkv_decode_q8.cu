@@ -95,8 +95,10 @@ __device__ __forceinline__ bool q8_wait(uint64_t* bar, uint32_t parity, volatile
 
 // The end of a CTA's segment [seg_begin, seg_end) of group sg (whose boundary sits at spre on the
 // line of T positions): the consuming warps' states are merged in shared memory (sc_m, sc_l,
-// sc_acc) into the group's output, or into this CTA's partial, which join_group takes on.  A thread folds
-// four columns at a time: fewer threads than a whole CTA, so a head's weights serve four.
+// sc_acc) into the group's output, or into this CTA's partial, which the group's last arriver merges with
+// the others.  A thread folds four columns at a time: fewer threads than a whole CTA, so a head's weights
+// serve four.  `more`: the CTA has another segment; `failed`: this thread's warp gave up a wait.  smem: the
+// stage buffers, free after the last segment.
 template <int D, int GP, typename Sync, typename State>
 __device__ __forceinline__ void end_segment(const DecodeArgs& a, State& ws, const Group& sgr, int sg, long long spre,
                                             long long seg_begin, long long seg_end, long long T, int nctas, int cta,
@@ -106,12 +108,15 @@ __device__ __forceinline__ void end_segment(const DecodeArgs& a, State& ws, cons
   constexpr int SG = q8_merge_heads<GP>();      // query heads merged per pass
   constexpr int NT = State::NT;                 // 8-column groups of query heads
   constexpr int kPasses = GP < 8 ? 1 : 8 / SG;  // passes per 8-column group
+  // the partial merge's (m, l) scratch reuses the warps' merge area: 2 * slots * G floats
+  constexpr int kMlCap = W * SG * D;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.group;
   ws.finish();
   const bool whole = seg_begin == spre + kGap && seg_end == spre + group_span<kGap>(sgr);
   const long long slot = (long long)sg + cta;  // unique per (group, CTA) along the line
-  __nv_bfloat16* const out_grp = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)sgr.s * a.pv.kv_heads + sgr.h) * G * D;
+  using Out = __nv_bfloat16;
+  Out* const out_grp = static_cast<Out*>(a.out) + ((int64_t)sgr.s * a.pv.kv_heads + sgr.h) * G * D;
   // pass (nt, hh): the warps' states of query heads [8*nt + hh*SG, 8*nt + (hh+1)*SG) meet in
   // shared memory and are folded into the output or this CTA's partial
 #pragma unroll
@@ -143,11 +148,50 @@ __device__ __forceinline__ void end_segment(const DecodeArgs& a, State& ws, cons
           A.w += v.w * f;
         }
       }
-      store_merged<__nv_bfloat16, D>(M, Ls, A, g, d / 4, G, whole ? out_grp : nullptr, a.part_acc, a.part_ml, slot);
+      store_merged<Out, D>(M, Ls, A, g, d / 4, G, whole ? out_grp : nullptr, a.part_acc, a.part_ml, slot);
     }
   }
-  if (!whole)
-    join_group<__nv_bfloat16, D, GP, SG, Sync, kGap>(a, sgr, sg, spre, T, nctas, cta, more, failed, smem, sc_acc, s_last, ms);
+  if (whole) return;
+  // The partial is published; count arrivals.  Up to kFlatMerge contributors: the last
+  // CTA of the group merges them all.  More (long windows at small batch): blocks of
+  // kMergeBlock consecutive contributors are merged by their last arriver into a second-
+  // level partial, and the last of those merges the blocks (one level of ~100 partials,
+  // streamed through the stage buffers in chunks by one CTA, was slower at batch 1: 877
+  // against 955 tokens/s; it moves ~200 KB through one SM where the tree spreads it).
+  // After the last segment no copy is in flight (unless a wait timed out): merges may
+  // stage partial blocks in the stage buffers.
+  if (!more) ms.buf = Sync::sync_or(failed) ? nullptr : reinterpret_cast<float*>(smem);
+  const int c_lo = cta_of(spre + kGap, T, nctas), c_hi = cta_of(spre + group_span<kGap>(sgr) - 1, T, nctas);
+  const bool all_live = T >= nctas;  // then no CTA range is empty
+  const int k = c_hi - c_lo + 1;
+  if (!all_live || k <= kFlatMerge) {
+    int expected = k;
+    if (!all_live) {
+      expected = 0;
+      for (int c = c_lo; c <= c_hi; ++c) expected += range_start(T, c + 1, nctas) > range_start(T, c, nctas);
+    }
+    if (arrive_last<Sync>(&a.counters[sg], expected, s_last)) {
+      auto live = [&](int i) {
+        return all_live || range_start(T, c_lo + i + 1, nctas) > range_start(T, c_lo + i, nctas);
+      };
+      merge_slots<Out, D, GP, Sync>(a.part_acc, a.part_ml, (long long)sg + c_lo, k, G, live, all_live, out_grp, nullptr,
+                                    nullptr, 0, sc_acc, kMlCap, ms, a.pv.err);
+    }
+  } else {
+    auto live = [](int) { return true; };
+    const int nb = (k + kMergeBlock - 1) / kMergeBlock;
+    const int b = (cta - c_lo) / kMergeBlock;
+    const int b_lo = c_lo + b * kMergeBlock;
+    const int b_n = min(kMergeBlock, c_hi - b_lo + 1);
+    const long long slot2 = (long long)sg * a.merge_blocks + b;
+    if (arrive_last<Sync>(&a.counters1[slot2], b_n, s_last)) {
+      merge_slots<Out, D, GP, Sync>(a.part_acc, a.part_ml, (long long)sg + b_lo, b_n, G, live, true, (Out*)nullptr,
+                                    a.part2_acc, a.part2_ml, slot2, sc_acc, kMlCap, ms, a.pv.err);
+      if (arrive_last<Sync>(&a.counters[sg], nb, s_last))
+        merge_slots<Out, D, GP, Sync>(a.part2_acc, a.part2_ml, (long long)sg * a.merge_blocks, nb, G, live, true, out_grp,
+                                      nullptr, nullptr, 0, sc_acc, kMlCap, ms, a.pv.err);
+    }
+  }
 }
 
 template <int D, int GP, bool SC>

@@ -75,6 +75,8 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
   constexpr int NT = State::NT;                 // 8-column groups of query heads
   constexpr int SG = merge_heads<D, GP>();      // query heads merged per pass in shared memory
   constexpr int kPasses = GP < 8 ? 1 : 8 / SG;  // passes per 8-column group
+  // the partial merge's (m, l) scratch reuses the warps' merge area: 2 * slots * G floats
+  constexpr int kMlCap = W * SG * D;
 
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -274,7 +276,8 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
     }
 
     // ---- end of segment: merge the warps, then store output or partial -----------------
-    // (in place: as a function shared with the 8-bit kernel it cost batch 1 0.5%)
+    // (in place: as functions shared with the 8-bit kernel the fold cost batch 1 0.5% and what follows
+    // it fp32 pools 1%)
     ws.finish();
     const bool whole = seg_begin == spre + kGapTiles && seg_end == spre + group_span(sgr);
     const long long slot = (long long)sg + cta;  // unique per (group, CTA) along the line
@@ -315,8 +318,49 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
         }
       }
     }
-    if (!whole)
-      join_group<Elem, D, GP, SG, CtaSync, kGapTiles>(a, sgr, sg, spre, T, nctas, cta, more, drain_from >= 0, smem, sc_acc, &s_last, ms);
+    if (!whole) {
+      // The partial is published; count arrivals.  Up to kFlatMerge contributors: the last
+      // CTA of the group merges them all.  More (long windows at small batch): blocks of
+      // kMergeBlock consecutive contributors are merged by their last arriver into a second-
+      // level partial, and the last of those merges the blocks (one level of ~100 partials,
+      // streamed through the stage buffers in chunks by one CTA, was slower at batch 1: 877
+      // against 955 tokens/s; it moves ~200 KB through one SM where the tree spreads it).
+      // After the last segment no copy is in flight (unless a wait timed out): merges may
+      // stage partial blocks in the stage buffers.
+      if (!more) ms.buf = __syncthreads_or(drain_from >= 0) ? nullptr : reinterpret_cast<float*>(smem);
+      const int c_lo = cta_of(spre + kGapTiles, T, nctas), c_hi = cta_of(spre + group_span(sgr) - 1, T, nctas);
+      const bool all_live = T >= nctas;  // then no CTA range is empty
+      const int k = c_hi - c_lo + 1;
+      Elem* const out_grp = out + ((int64_t)sgr.s * Hq + sgr.h * G) * D;
+      if (!all_live || k <= kFlatMerge) {
+        int expected = k;
+        if (!all_live) {
+          expected = 0;
+          for (int c = c_lo; c <= c_hi; ++c) expected += range_start(T, c + 1, nctas) > range_start(T, c, nctas);
+        }
+        if (arrive_last<CtaSync>(&a.counters[sg], expected, &s_last)) {
+          auto live = [&](int i) {
+            return all_live || range_start(T, c_lo + i + 1, nctas) > range_start(T, c_lo + i, nctas);
+          };
+          merge_slots<Elem, D, GP, CtaSync>(a.part_acc, a.part_ml, (long long)sg + c_lo, k, G, live, all_live, out_grp, nullptr,
+                         nullptr, 0, sc_acc, kMlCap, ms, a.pv.err);
+        }
+      } else {
+        auto live = [](int) { return true; };
+        const int nb = (k + kMergeBlock - 1) / kMergeBlock;
+        const int b = (cta - c_lo) / kMergeBlock;
+        const int b_lo = c_lo + b * kMergeBlock;
+        const int b_n = min(kMergeBlock, c_hi - b_lo + 1);
+        const long long slot2 = (long long)sg * a.merge_blocks + b;
+        if (arrive_last<CtaSync>(&a.counters1[slot2], b_n, &s_last)) {
+          merge_slots<Elem, D, GP, CtaSync>(a.part_acc, a.part_ml, (long long)sg + b_lo, b_n, G, live, true, (Elem*)nullptr, a.part2_acc,
+                         a.part2_ml, slot2, sc_acc, kMlCap, ms, a.pv.err);
+          if (arrive_last<CtaSync>(&a.counters[sg], nb, &s_last))
+            merge_slots<Elem, D, GP, CtaSync>(a.part2_acc, a.part2_ml, (long long)sg * a.merge_blocks, nb, G, live, true, out_grp,
+                           nullptr, nullptr, 0, sc_acc, kMlCap, ms, a.pv.err);
+        }
+      }
+    }
     __syncthreads();  // the merge scratch is rewritten by the next segment
     if (!more) break;
     do {

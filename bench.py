@@ -35,11 +35,11 @@ METRIC = "decode tokens/s and resident-KV HBM GB/s (fraction of GB300 peak), 1 G
 FALLBACK_HBM_GBS = 6800.0
 
 # dram__bytes_read.sum + dram__bytes_write.sum per decode launch from one ncu capture of the
-# stream-K decode kernel, with the sha256 of its sources (hwkv_decode_tc.cu, then
-# hwkv_decode_tile.cuh) it was taken on.  When the kernel source changes the figure no longer
-# applies and is reported as null.
-DECODE_TRAFFIC = {"source_sha256": "1c00563c90368234af1ad9540ba43971664c11ae329c77154a06aa51d334f0e1",
-                  "bytes_per_launch": (621.369856 + 2.454272 + 489.221632 + 0.178432) / 2 * 1e6,
+# stream-K decode kernel, with the sha256 of its sources (DECODE_SOURCES, in that order) it was
+# taken on.  When the kernel source changes the figure no longer applies and is reported as null.
+DECODE_SOURCES = ("hwkv_decode_tc.cu", "hwkv_decode_sk.cuh", "hwkv_decode_merge.cuh", "hwkv_decode_tile.cuh")
+DECODE_TRAFFIC = {"source_sha256": "8d7d18e6a7abb7cc63f681a84e0b95c219e365762ff9c88eef7164c1359d3f96",
+                  "bytes_per_launch": (621.376256 + 3.041024 + 489.206784 + 0.169472) / 2 * 1e6,
                   "launch": "layers 0 and 1 of the full workload (2-layer run, same per-launch shape)"}
 
 
@@ -156,7 +156,7 @@ def measured_peak():
 
 def decode_source_sha() -> str:
     h = hashlib.sha256()
-    for name in ("hwkv_decode_tc.cu", "hwkv_decode_tile.cuh"):
+    for name in DECODE_SOURCES:
         with open(os.path.join(ROOT, "head_budgeted_kv_gb300", "csrc", name), "rb") as f:
             h.update(f.read())
     return h.hexdigest()

@@ -34,6 +34,22 @@ def test_materialize_and_append_bytes():
     assert bench.materialize_bytes(cfg, 5) == 2 * sum(min(x, 164864) for x in w) * 512
 
 
+
+def test_traffic_is_keyed_to_every_source_of_the_decode_kernel():
+    """The DRAM figure holds for the sources the kernel is compiled from: hwkv_decode_tc.cu and each decode
+    header it includes, itself or through another."""
+    csrc = os.path.join(bench.ROOT, "head_budgeted_kv_gb300", "csrc")
+    found, todo = set(), ["hwkv_decode_tc.cu"]
+    while todo:
+        name = todo.pop()
+        found.add(name)
+        with open(os.path.join(csrc, name)) as f:
+            names = [line.split('"')[1] for line in f if line.startswith('#include "hwkv_decode')]
+        todo += [n for n in names if n not in found]
+    assert found == set(bench.DECODE_SOURCES)
+    assert len(bench.decode_source_sha()) == 64
+
+
 def _free_port():
     s = socket.socket()
     s.bind(("127.0.0.1", 0))

@@ -45,7 +45,9 @@ def rope_table(head_dim: int, rot_dim: Optional[int] = None, base: float = 10000
     """The table ``Pool.rope`` turns heads of ``head_dim`` with: pairs of the first ``rot_dim`` dims
     (all by default), ``layout`` "half" (i, i + rot_dim / 2) or "interleaved" (2i, 2i + 1),
     frequencies base^(-2i / rot_dim) scaled for longer contexts by ``scaling`` "none", "linear",
-    "ntk" or "by_parts" (see hwkv_rope_table in the header)."""
+    "ntk" or "by_parts".  by_parts ramps over a pair's turns in original_len positions and scales by
+    0.1 ln(factor) + 1; a configuration that ramps over the pair's index, or keeps magnitude 1, sets the
+    table's ``freq[i]`` and ``magnitude`` itself (see hwkv_rope_table in the header)."""
     rot_dim = head_dim if rot_dim is None else rot_dim
     if rot_dim > head_dim:
         raise ValueError(f"rot_dim {rot_dim} exceeds head_dim {head_dim}")

@@ -45,7 +45,9 @@
  *     across decode steps; kernels check them and record problems in a device error word
  *     that hwkv_check_device_errors() reads.  Kernels never trap or spin without bound.
  *   - Inputs must be finite: a masked pool row that holds Inf/NaN bits can still poison
- *     a result (0 * Inf), as in any attention kernel (not so in 8-bit pools).
+ *     a result (0 * Inf), as in any attention kernel (not so in 8-bit pools).  Weighted sums are
+ *     held in fp32 relative to the largest weight: the sum of |value| over keys of like weight
+ *     must stay below 2^128.
  */
 #ifndef HWKV_H
 #define HWKV_H
@@ -259,8 +261,9 @@ typedef struct hwkv_score {
 
 /* hwkv_decode_attn_ex with such a score, for every pool type and shape; the same workspace, flags
  * and errors.  The cap is off by at most 2^-20 of the capped score, the difference with the bias by
- * a few fp32 roundings of the larger term (fp32 pools: the cap likewise).  A score with neither cap nor slopes runs
- * the plain kernels. */
+ * a few fp32 roundings of the larger term (fp32 pools: the cap likewise).  8-bit decode and chunked
+ * prefill take longer where scores pass the cap, or where scale * (scale / softcap)^10 is below fp32's normal
+ * range (caps from about 250 at scale 128^-1/2).  A score with neither cap nor slopes runs the plain kernels. */
 int hwkv_decode_attn_score(hwkv_pool_t pool, int layer, const void* q, int q_heads, const hwkv_score_t* score,
                            const void* k_new, const void* v_new, const int32_t* lens_dev, void* out, void* workspace,
                            uint64_t workspace_bytes, int flags, void* stream);
@@ -374,6 +377,11 @@ typedef struct hwkv_rope {
  *   HWKV_ROPE_SCALE_BY_PARTS  a pair that makes r turns over original_len positions keeps the
  *                             share c = clamp((r - beta_slow) / (beta_fast - beta_slow), 0, 1):
  *                             freq = c freq + (1 - c) freq / factor; magnitude 0.1 ln(factor) + 1.
+ *                             (Over turns.  A ramp over the pair's index between two rounded bounds, as many
+ *                             configurations compute it, has other frequencies: up to 1.7 times these at
+ *                             rot_dim 128, base 1e6, 32768 and factor 4, 3.0 times at base 1e4, 4096 and
+ *                             16; and a ramp over turns may go with magnitude 1.  Such a caller sets
+ *                             freq and magnitude.)
  * factor >= 1 and finite; original_len > 0 and beta_fast > beta_slow for BY_PARTS (ignored
  * otherwise); base > 0 and finite.  Host only.  Errors: HWKV_ERR_INVALID_ARG.  A caller may also
  * fill the struct itself. */

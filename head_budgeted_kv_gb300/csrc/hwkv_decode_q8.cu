@@ -17,8 +17,8 @@
 // Stages are handed over by mbarriers: full[] (bytes landed), empty[] (its consumer has read it).
 //
 // Bound: HBM, with ~8 us per launch that no byte covers (a policy layer of four sequences at 112K: 311 MB
-// in 54.1 us, 0.85 of the measured copy rate); at batch 1 the latency of schedule and merges (45 MB in
-// 20.8 us).  Waits are bounded (~2 s); a timeout records HWKV_DEVERR_WAIT_TIMEOUT, all roles stop and
+// in 54.5 us, 0.84 of the measured copy rate); at batch 1 the latency of schedule and merges (45 MB in
+// 20.9 us).  Waits are bounded (~2 s); a timeout records HWKV_DEVERR_WAIT_TIMEOUT, all roles stop and
 // the copies in flight land before the shared memory is released.
 #include <atomic>
 
@@ -42,8 +42,9 @@ constexpr int kMinPositions = 16;
 
 template <int D>
 struct Q8Cfg {
-  // 3 consumers and the producer: with two CTAs per SM a warp may then hold 255 registers and none
-  // spills (4 or 5 consumers: 168, with spills, and slower: policy layer 58.6 -> 62.1 and 59.7 us)
+  // 3 consumers and the producer: with two CTAs per SM a warp may then hold 255 registers, and only 16
+  // columns of 128 spill, 12 bytes (4 or 5 consumers: 168, with spills, and slower: policy layer 58.6 -> 62.1 and
+  // 59.7 us)
   static constexpr int W = 3;
   static constexpr int kThreads = (W + 1) * 32;
   static constexpr int M = D == 128 ? 2 : 4;          // tiles of a stage

@@ -20,7 +20,7 @@
 // group 2^24 above the others put 12% into the result and one 2^37 above them erased it.)  m and e are
 // integers, so no reference is rounded, and 2^e is exact where O leaves the warp.  The second exponential per
 // weight costs up to 2% of a decode whose references seldom move and 6% where steep slopes move them at every
-// stage (policy layer, uncapped 55.0 -> 55.1 us, biased 57.5 -> 61); a product by the power of two instead of it
+// stage (policy layer, uncapped 55.0 -> 55.1 us, biased 57.5 -> 62); a product by the power of two instead of it
 // is slower (61 at cap 50 against 57).
 // A dim or token index may be permuted freely inside a contraction: K's bytes are fed in the
 // order ldmatrix delivers them, against queries loaded in the same order, and V's columns come
@@ -178,8 +178,8 @@ struct WarpState<E4m3, D, GP, SC> {
   }
 
   // The raw scores s of M tiles capped, biased and in log2 units.  While no score of the warp
-  // reaches the cap the polynomial alone serves, on packed pairs (a capped policy layer 65 -> 55 us,
-  // uncapped 54; past the cap 77).
+  // reaches the cap the polynomial alone serves, on packed pairs (a capped policy layer 65 -> 55 us when it
+  // came; now 58, uncapped 55, past the cap 83).
   template <int M>
   __device__ __forceinline__ void score_tiles(const DecodeArgs& a, const Group& gr, const int (&t0)[M], float (&s)[M][NT][4],
                                               int gq) const {

@@ -21,7 +21,7 @@ from .binding import (HWKV_BF16, HWKV_E4M3, HWKV_F32, HWKV_KERNEL_AUTO, HWKV_KER
                       hwkv_check_device_errors, hwkv_kernel_launches,
                       hwkv_decode_attn, hwkv_decode_attn_score, hwkv_decode_workspace_bytes, hwkv_materialize, hwkv_pool_bytes,
                       hwkv_pool_create, hwkv_pool_destroy, hwkv_pool_geometry, hwkv_prefill_attn,
-                      hwkv_prefill_attn_score, hwkv_prefill_plan, hwkv_prefill_workspace_bytes, hwkv_rope, hwkv_rope_table, hwkv_set_block_table, hwkv_set_decode_config,
+                      hwkv_prefill_attn_score, hwkv_prefill_plan, hwkv_prefill_workspace_bytes, hwkv_rope, hwkv_rope_append, hwkv_rope_table, hwkv_set_block_table, hwkv_set_decode_config,
                       hwkv_set_prefill_config, hwkv_wait_selftest)
 
 __all__ = [
@@ -29,7 +29,7 @@ __all__ = [
     "HWKV_KERNEL_SIMT", "hwkv_abi_version", "hwkv_advance_positions", "hwkv_append", "hwkv_append_decode_attn", "hwkv_block_table",
     "hwkv_check_device_errors", "hwkv_kernel_launches",
     "hwkv_decode_attn", "hwkv_decode_attn_score", "hwkv_decode_workspace_bytes", "hwkv_materialize", "hwkv_pool_bytes", "hwkv_pool_create",
-    "hwkv_pool_destroy", "hwkv_pool_geometry", "hwkv_prefill_attn", "hwkv_prefill_attn_score", "hwkv_prefill_plan", "hwkv_prefill_workspace_bytes", "hwkv_rope", "hwkv_rope_table",
+    "hwkv_pool_destroy", "hwkv_pool_geometry", "hwkv_prefill_attn", "hwkv_prefill_attn_score", "hwkv_prefill_plan", "hwkv_prefill_workspace_bytes", "hwkv_rope", "hwkv_rope_append", "hwkv_rope_table",
     "hwkv_set_block_table", "hwkv_set_decode_config", "hwkv_set_prefill_config", "hwkv_wait_selftest",
 ]
 
@@ -241,6 +241,31 @@ class Pool:
         if not self._is_counts(pos) or not (n is None or self._is_counts(n)):
             raise ValueError(f"positions and row counts must hold {self.num_seqs} values in a row on {self.buffer.device}")
         hwkv_rope(self.handle, table, q, k, pos, n, q_out, k_out, stream)
+        return q_out, k_out
+
+    def rope_append(self, layer: int, table: Optional[RopeTable], q, k, v, pos, n=None, q_out=None, k_out=None, turn_pos=None,
+                    stream=None):
+        """Rotary positions on the way into the pool, in one launch: q [B][n_max][Hq][D] and k [B][n_max][Hkv][D]
+        (or single rows [B][heads][D]) turn at positions turn_pos[s] + row (pos[s] + row by default), and the
+        turned k and v are stored at positions pos[s] + row, rows below n[s] (all when n is None).  q may be None;
+        table None turns nothing.  q_out defaults to a new tensor (zeros past n); pass q_out=q to work in place.
+        k_out, when given, receives the turned keys too.  Returns (q_out, k_out)."""
+        if q is None and q_out is not None:
+            raise ValueError("q_out goes with q")
+        if q is not None:
+            heads = self._check_rows(q, "q")
+            if heads % self.kv_heads:
+                raise ValueError(f"q must hold a multiple of {self.kv_heads} heads")
+            if q_out is None:
+                q_out = (torch.empty if n is None else torch.zeros)(q.shape, dtype=q.dtype, device=q.device)
+        if self._check_rows(k, "k") != self.kv_heads or self._check_rows(v, "v") != self.kv_heads:
+            raise ValueError(f"k and v must hold {self.kv_heads} heads")
+        at = self._device_index
+        if (q_out is not None and q_out.get_device() != at) or (k_out is not None and k_out.get_device() != at):
+            raise ValueError(f"outputs must lie on {self.buffer.device}")
+        if not self._is_counts(pos) or not (n is None or self._is_counts(n)) or not (turn_pos is None or self._is_counts(turn_pos)):
+            raise ValueError(f"positions and row counts must hold {self.num_seqs} values in a row on {self.buffer.device}")
+        hwkv_rope_append(self.handle, layer, table, q, k, v, pos, n, turn_pos, q_out, k_out, stream)
         return q_out, k_out
 
     def _check_rows(self, t, name) -> int:

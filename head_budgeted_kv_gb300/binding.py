@@ -83,6 +83,7 @@ SIGNATURES = [
     ("hwkv_rope_table", _i, [_i, _i, ctypes.c_double, _i, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                              ctypes.c_double, _ropep]),
     ("hwkv_rope", _i, [_vp, _ropep, _rowsp, _i, _rowsp, _i, _vp, _vp, _rowsp, _rowsp, _vp]),
+    ("hwkv_rope_append", _i, [_vp, _i, _ropep, _rowsp, _i, _rowsp, _rowsp, _i, _vp, _vp, _vp, _rowsp, _rowsp, _vp]),
     ("hwkv_wait_selftest", _i, [ctypes.c_uint32, _vp, _vp]),
     ("hwkv_decode_workspace_bytes", _i, [_vp, _i, _c_u64p]),
     ("hwkv_decode_attn", _i, [_vp, _i, _vp, _i, ctypes.c_float, _vp, _vp, _vp, _u64, _vp]),
@@ -277,11 +278,11 @@ def hwkv_rope_table(rot_dim: int, layout: int = HWKV_ROPE_HALF, base: float = 10
 
 
 class _RowSlots(threading.local):
-    """The four hwkv_rows_t of a rope call, kept per thread with the references ctypes passes: making
+    """The hwkv_rows_t of a rope call, kept per thread with the references ctypes passes: making
     them anew costs a small call as much as its launch."""
 
     def __init__(self):
-        self.rows = [Rows() for _ in range(4)]
+        self.rows = [Rows() for _ in range(5)]
         self.refs = [ctypes.byref(r) for r in self.rows]
 
 
@@ -338,6 +339,48 @@ def hwkv_rope(pool: int, table: RopeTable, q: Optional[torch.Tensor], k: Optiona
             _fill_rows(rows[3], k_out, shape[-1], "k_out")
             rp = refs[3]
     _check(load().hwkv_rope(pool, table, rq, heads, rk, n_max, pos.data_ptr(), _ptr(n), ro, rp, _stream_ptr(stream)))
+
+
+def _turned_rows(slots, i: int, t: torch.Tensor, out: Optional[torch.Tensor], name: str):
+    """References to the rows of t (slot i) and of its output (slot i + 1, or slot i in place)."""
+    rows, refs = slots.rows, slots.refs
+    _fill_rows(rows[i], t, t.shape[-1], name)
+    if out is None or out is t:
+        return refs[i], None if out is None else refs[i]
+    if out.shape != t.shape or out.dtype != t.dtype:
+        raise ValueError(f"{name}_out must match {name}")
+    _fill_rows(rows[i + 1], out, t.shape[-1], name + "_out")
+    return refs[i], refs[i + 1]
+
+
+def hwkv_rope_append(pool: int, layer: int, table: Optional[RopeTable], q: Optional[torch.Tensor], k: torch.Tensor,
+                     v: torch.Tensor, pos: torch.Tensor, n: Optional[torch.Tensor] = None,
+                     turn_pos: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                     k_out: Optional[torch.Tensor] = None, stream=None):
+    """Turns q [B][n_max][Hq][D] (or None) and k [B][n_max][Hkv][D] (or one row each, [B][heads][D]) at positions
+    turn_pos + row (pos + row when None) and stores the turned k and v at positions pos + row; table None
+    turns nothing."""
+    if pos.dtype != torch.int32 or (n is not None and n.dtype != torch.int32) or (
+            turn_pos is not None and turn_pos.dtype != torch.int32):
+        raise ValueError("positions and row counts must be int32")
+    shape = k.shape
+    if v.shape != shape or v.dtype != k.dtype:
+        raise ValueError("k and v must match")
+    slots = _row_slots
+    rq = ro = rp = None
+    heads = 0
+    if q is not None:
+        qs = q.shape
+        if q_out is None:
+            raise ValueError("q goes with q_out")
+        if len(qs) != len(shape) or qs[:-2] != shape[:-2] or qs[-1] != shape[-1] or q.dtype != k.dtype:
+            raise ValueError("q and k must have the same sequences and rows")
+        heads = qs[-2]
+        rq, ro = _turned_rows(slots, 0, q, q_out, "q")
+    rk, rp = _turned_rows(slots, 2, k, k_out, "k")
+    _fill_rows(slots.rows[4], v, shape[-1], "v")
+    _check(load().hwkv_rope_append(pool, layer, table, rq, heads, rk, slots.refs[4], shape[1] if len(shape) == 4 else 1,
+                                   pos.data_ptr(), _ptr(turn_pos), _ptr(n), ro, rp, _stream_ptr(stream)))
 
 
 def hwkv_decode_workspace_bytes(pool: int, q_heads: int) -> int:

@@ -529,6 +529,73 @@ LayerGeom layer_geom(const hwkv_pool* p, int layer) {
   return lg;
 }
 
+
+int check_rope(const hwkv_rope_t* rope, int head_dim) {
+  if (rope->rot_dim < 2 || rope->rot_dim > head_dim || rope->rot_dim % 2 != 0)
+    return fail(HWKV_ERR_INVALID_ARG, "rot_dim must be even and in [2, head_dim = %d] (got %d)", head_dim, rope->rot_dim);
+  if (rope->layout != HWKV_ROPE_HALF && rope->layout != HWKV_ROPE_INTERLEAVED)
+    return fail(HWKV_ERR_INVALID_ARG, "unknown rope layout %d", rope->layout);
+  if (!std::isfinite(rope->magnitude) || !std::isfinite((float)rope->magnitude))
+    return fail(HWKV_ERR_INVALID_ARG, "magnitude must be finite");
+  for (int i = 0; i < rope->rot_dim / 2; ++i)
+    if (!std::isfinite(rope->freq[i])) return fail(HWKV_ERR_INVALID_ARG, "freq[%d] must be finite", i);
+  return HWKV_OK;
+}
+
+int check_rows(const Geometry& g, const hwkv_rows_t* r) {
+  if (!r->data) return fail(HWKV_ERR_INVALID_ARG, "NULL tensor argument");
+  if (r->seq_stride < 0 || r->row_stride < 0) return fail(HWKV_ERR_INVALID_ARG, "negative stride");
+  if (!aligned(r->data, 16) || (r->seq_stride * g.io_eb) % 16 != 0 || (r->row_stride * g.io_eb) % 16 != 0)
+    return fail(HWKV_ERR_ALIGNMENT, "rows must be 16-byte aligned, strides multiples of 16 bytes");
+  return HWKV_OK;
+}
+
+// Rows and where they go when turned: an output of its own, or in place.
+int check_turned_rows(const Geometry& g, const hwkv_rows_t* in, const hwkv_rows_t* to, int heads, int n_max) {
+  for (const hwkv_rows_t* r : {in, to}) {
+    const int rc = check_rows(g, r);
+    if (rc != HWKV_OK) return rc;
+  }
+  // no two rows of an output may share an element: sequences apart by whole chunks, or rows
+  // apart by whole batches
+  const int64_t row = (int64_t)heads * g.head_dim;
+  const int64_t ss = g.num_seqs > 1 ? to->seq_stride : 0, rs = n_max > 1 ? to->row_stride : 0;
+  const bool by_seq = (n_max == 1 || rs >= row) && (g.num_seqs == 1 || ss >= (n_max - 1) * rs + row);
+  const bool by_row = (g.num_seqs == 1 || ss >= row) && (n_max == 1 || rs >= (g.num_seqs - 1) * ss + row);
+  if (!by_seq && !by_row) return fail(HWKV_ERR_INVALID_ARG, "rows of an output overlap");
+  if (in->data == to->data &&
+      ((g.num_seqs > 1 && in->seq_stride != to->seq_stride) || (n_max > 1 && in->row_stride != to->row_stride)))
+    return fail(HWKV_ERR_INVALID_ARG, "an output in place of its input needs the input's strides");
+  return HWKV_OK;
+}
+
+// What a rope launch takes of its call (rope null: nothing turns).
+void fill_rope(RopeArgs* a, const hwkv_pool* p, const hwkv_rope_t* rope, const hwkv_rows_t* q, int q_heads,
+               const hwkv_rows_t* k, int k_heads, int n_max, const int32_t* pos_dev, const int32_t* n_dev,
+               const hwkv_rows_t* q_out, const hwkv_rows_t* k_out) {
+  RopeTensor* t[4] = {&a->q, &a->k, &a->q_out, &a->k_out};
+  const hwkv_rows_t* r[4] = {q, k, q_out, k_out};
+  for (int i = 0; i < 4; ++i)
+    if (r[i]) *t[i] = RopeTensor{r[i]->data, r[i]->seq_stride, r[i]->row_stride};
+  a->pos = pos_dev;
+  a->n = n_dev;
+  a->err = p->d_err;
+  a->num_seqs = p->g.num_seqs;
+  a->n_max = n_max;
+  a->q_heads = q_heads;
+  a->k_heads = k_heads;
+  a->head_dim = p->g.head_dim;
+  if (!rope) return;
+  a->rot = rope->rot_dim;
+  a->magnitude = (float)rope->magnitude;
+  for (int i = 0; i < rope->rot_dim / 2; ++i) {
+    // The fraction of a turn per position: the product's rounding error and the low part of 1 / (2 pi) count,
+    // as a position multiplies them by up to 2^31.  Off by less than 2^-60 of a turn for |freq| < 2^40.
+    const double f = rope->freq[i], turns = f * kInvTwoPi;
+    a->turns[i] = fraction64(turns) + fraction64(std::fma(f, kInvTwoPi, -turns) + f * kInvTwoPiLo);
+  }
+}
+
 }  // namespace
 
 extern "C" {
@@ -866,14 +933,8 @@ int hwkv_rope(hwkv_pool_t p, const hwkv_rope_t* rope, const hwkv_rows_t* q, int 
   if (!p) return fail(HWKV_ERR_INVALID_ARG, "pool is NULL");
   const Geometry& g = p->g;
   if (!rope || !pos_dev) return fail(HWKV_ERR_INVALID_ARG, "NULL argument");
-  if (rope->rot_dim < 2 || rope->rot_dim > g.head_dim || rope->rot_dim % 2 != 0)
-    return fail(HWKV_ERR_INVALID_ARG, "rot_dim must be even and in [2, head_dim = %d] (got %d)", g.head_dim, rope->rot_dim);
-  if (rope->layout != HWKV_ROPE_HALF && rope->layout != HWKV_ROPE_INTERLEAVED)
-    return fail(HWKV_ERR_INVALID_ARG, "unknown rope layout %d", rope->layout);
-  if (!std::isfinite(rope->magnitude) || !std::isfinite((float)rope->magnitude))
-    return fail(HWKV_ERR_INVALID_ARG, "magnitude must be finite");
-  for (int i = 0; i < rope->rot_dim / 2; ++i)
-    if (!std::isfinite(rope->freq[i])) return fail(HWKV_ERR_INVALID_ARG, "freq[%d] must be finite", i);
+  int rc = check_rope(rope, g.head_dim);
+  if (rc != HWKV_OK) return rc;
   if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr) || (!q && !k))
     return fail(HWKV_ERR_INVALID_ARG, "q goes with q_out and k with k_out, and one of them must be given");
   if (q && (q_heads < 1 || q_heads > 65535)) return fail(HWKV_ERR_UNSUPPORTED, "q_heads must be in [1, 65535] (got %d)", q_heads);
@@ -886,52 +947,69 @@ int hwkv_rope(hwkv_pool_t p, const hwkv_rope_t* rope, const hwkv_rows_t* q, int 
   bool copy = false;
   for (int i = 0; i < 2; ++i) {
     if (!in[i]) continue;
-    for (const hwkv_rows_t* r : {in[i], to[i]}) {
-      if (!r->data) return fail(HWKV_ERR_INVALID_ARG, "NULL tensor argument");
-      if (r->seq_stride < 0 || r->row_stride < 0) return fail(HWKV_ERR_INVALID_ARG, "negative stride");
-      if (!aligned(r->data, 16) || (r->seq_stride * g.io_eb) % 16 != 0 || (r->row_stride * g.io_eb) % 16 != 0)
-        return fail(HWKV_ERR_ALIGNMENT, "rows must be 16-byte aligned, strides multiples of 16 bytes");
-    }
-    // no two rows of an output may share an element: sequences apart by whole chunks, or rows
-    // apart by whole batches
-    const int64_t row = (int64_t)heads[i] * g.head_dim;
-    const int64_t ss = g.num_seqs > 1 ? to[i]->seq_stride : 0, rs = n_max > 1 ? to[i]->row_stride : 0;
-    const bool by_seq = (n_max == 1 || rs >= row) && (g.num_seqs == 1 || ss >= (n_max - 1) * rs + row);
-    const bool by_row = (g.num_seqs == 1 || ss >= row) && (n_max == 1 || rs >= (g.num_seqs - 1) * ss + row);
-    if (!by_seq && !by_row) return fail(HWKV_ERR_INVALID_ARG, "rows of an output overlap");
+    rc = check_turned_rows(g, in[i], to[i], heads[i], n_max);
+    if (rc != HWKV_OK) return rc;
     if (in[i]->data != to[i]->data) copy = true;
-    else if ((g.num_seqs > 1 && in[i]->seq_stride != to[i]->seq_stride) || (n_max > 1 && in[i]->row_stride != to[i]->row_stride))
-      return fail(HWKV_ERR_INVALID_ARG, "an output in place of its input needs the input's strides");
   }
   if (q && k && (q_out->data == k_out->data || q_out->data == k->data || k_out->data == q->data))
     return fail(HWKV_ERR_INVALID_ARG, "an output overlaps the other output or the other input");
-  int rc = check_device(p);
+  rc = check_device(p);
   if (rc != HWKV_OK) return rc;
   NvtxRange range_("hwkv_rope", n_max);
   RopeArgs a;
   std::memset(&a, 0, sizeof a);
-  RopeTensor* t[4] = {&a.q, &a.k, &a.q_out, &a.k_out};
-  const hwkv_rows_t* r[4] = {q, k, q_out, k_out};
-  for (int i = 0; i < 4; ++i)
-    if (r[i]) *t[i] = RopeTensor{r[i]->data, r[i]->seq_stride, r[i]->row_stride};
-  a.pos = pos_dev;
-  a.n = n_dev;
-  a.err = p->d_err;
-  a.num_seqs = g.num_seqs;
-  a.n_max = n_max;
-  a.q_heads = heads[0];
-  a.k_heads = heads[1];
-  a.head_dim = g.head_dim;
-  a.rot = rope->rot_dim;
+  fill_rope(&a, p, rope, q, heads[0], k, heads[1], n_max, pos_dev, n_dev, q_out, k_out);
   a.copy = copy ? 1 : 0;
-  a.magnitude = (float)rope->magnitude;
-  for (int i = 0; i < rope->rot_dim / 2; ++i) {
-    // The fraction of a turn per position: the product's rounding error and the low part of 1 / (2 pi) count,
-    // as a position multiplies them by up to 2^31.  Off by less than 2^-60 of a turn for |freq| < 2^40.
-    const double f = rope->freq[i], turns = f * kInvTwoPi;
-    a.turns[i] = fraction64(turns) + fraction64(std::fma(f, kInvTwoPi, -turns) + f * kInvTwoPiLo);
-  }
   HWKV_CUDA_TRY(launch_rope(a, rope->layout, g.dtype == HWKV_F32, static_cast<cudaStream_t>(stream)), "rope launch");
+  return ok();
+}
+
+int hwkv_rope_append(hwkv_pool_t p, int layer, const hwkv_rope_t* rope, const hwkv_rows_t* q, int q_heads,
+                     const hwkv_rows_t* k, const hwkv_rows_t* v, int n_max, const int32_t* pos_dev,
+                     const int32_t* turn_pos_dev, const int32_t* n_dev, const hwkv_rows_t* q_out,
+                     const hwkv_rows_t* k_out, void* stream) {
+  if (!p) return fail(HWKV_ERR_INVALID_ARG, "pool is NULL");
+  const Geometry& g = p->g;
+  if (layer < 0 || layer >= g.layers) return fail(HWKV_ERR_INVALID_ARG, "layer %d out of range", layer);
+  if (!k || !v || !pos_dev) return fail(HWKV_ERR_INVALID_ARG, "NULL argument");
+  int rc = rope ? check_rope(rope, g.head_dim) : HWKV_OK;
+  if (rc != HWKV_OK) return rc;
+  if ((q == nullptr) != (q_out == nullptr)) return fail(HWKV_ERR_INVALID_ARG, "q goes with q_out");
+  if (q && (q_heads < g.kv_heads || q_heads % g.kv_heads != 0 || q_heads > 65535))
+    return fail(HWKV_ERR_UNSUPPORTED, "q_heads must be a multiple of kv_heads, at most 65535 (got %d)", q_heads);
+  if (n_max < 1) return fail(HWKV_ERR_INVALID_ARG, "n_max must be >= 1");
+  if (((int64_t)n_max + 2 * 16) * g.num_seqs * g.kv_heads > kInt32Max)
+    return fail(HWKV_ERR_UNSUPPORTED, "num_seqs * kv_heads * n_max must be below 2^31");
+  if (!aligned(pos_dev, 4) || !aligned(turn_pos_dev, 4) || !aligned(n_dev, 4))
+    return fail(HWKV_ERR_ALIGNMENT, "positions must be 4-byte aligned");
+  if (q && (rc = check_turned_rows(g, q, q_out, q_heads, n_max)) != HWKV_OK) return rc;
+  if (k_out && (rc = check_turned_rows(g, k, k_out, g.kv_heads, n_max)) != HWKV_OK) return rc;
+  if (!k_out && (rc = check_rows(g, k)) != HWKV_OK) return rc;
+  if ((rc = check_rows(g, v)) != HWKV_OK) return rc;
+  if (k_out && k_out->data == k->data && g.dtype == HWKV_E4M3)
+    return fail(HWKV_ERR_UNSUPPORTED, "an 8-bit pool's keys cannot be turned in place while they are stored");
+  const void* outs[2] = {q ? q_out->data : nullptr, k_out ? k_out->data : nullptr};
+  const void* others[2][3] = {{k->data, v->data, outs[1]}, {q ? q->data : nullptr, v->data, outs[0]}};
+  for (int i = 0; i < 2; ++i)
+    for (const void* o : others[i])
+      if (outs[i] && o == outs[i]) return fail(HWKV_ERR_INVALID_ARG, "an output overlaps the other output or another input");
+  rc = check_device(p);
+  if (rc != HWKV_OK) return rc;
+  NvtxRange range_("hwkv_rope_append", layer);
+  RopeAppendArgs a;
+  std::memset(static_cast<void*>(&a), 0, sizeof a);
+  fill_rope(&a, p, rope, q, q ? q_heads : 0, k, g.kv_heads, n_max, pos_dev, n_dev, q_out, k_out);
+  a.copy = 1;
+  a.pv = pool_view(p);
+  a.g = layer_geom(p, layer);
+  a.v = RopeTensor{v->data, v->seq_stride, v->row_stride};
+  a.turn_pos = turn_pos_dev;
+  a.keys_out = k_out ? 1 : 0;
+  const int layout = rope ? rope->layout : HWKV_ROPE_HALF;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  HWKV_CUDA_TRY(g.dtype == HWKV_E4M3 ? launch_rope_append_q8(a, layout, p->num_sms, st)
+                                     : launch_rope_append(a, layout, g.dtype == HWKV_F32, st),
+                "rope-append launch");
   return ok();
 }
 

@@ -22,8 +22,9 @@
 // heads of 128 in bf16: 126 MB in 19.4-23.3 us by box and run, 0.80-0.95 of the measured copy rate; pairs side by
 // side 26) and the launch for short ones (one row: 3.1 us).
 #include <algorithm>
+#include <type_traits>
 
-#include "hwkv_device.cuh"
+#include "hwkv_rope.cuh"
 
 namespace hwkv {
 namespace {
@@ -41,32 +42,6 @@ struct RopeShape {
   static constexpr int kAhead = kWide ? 2 : 3;
 };
 
-template <typename T>
-struct RopeVec {  // a 16-byte vector as fp32
-  static constexpr int V = 16 / (int)sizeof(T);
-  float v[V];
-  __device__ __forceinline__ void load(uint4 w) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(u[i]);
-      else v[i] = __uint_as_float((i & 1) ? (u[i >> 1] & 0xFFFF0000u) : (u[i >> 1] << 16));
-    }
-  }
-  __device__ __forceinline__ uint4 store() const {
-    if constexpr (sizeof(T) == 4)
-      return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-    else
-      return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-  }
-};
-
-__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
-  const float x = a, y = b;
-  a = fmaf(x, c, -(y * s));
-  b = fmaf(y, c, x * s);
-}
-
 // Cosines and sines of a row, two pairs to a 16-byte vector: (cos 2v, cos 2v + 1, sin 2v, sin 2v + 1).
 // A unit takes K consecutive vectors; vector v is stored at (v % K) * (32 / K) + v / K, so that the
 // units of neighbouring threads read neighbouring vectors (unit after unit they would share banks).
@@ -82,8 +57,13 @@ enum { kRopeHalf = 0, kRopeInterleaved = 1, kRopeHalfAny = 2 };
 // vector past rot); kRopeInterleaved: a unit is one vector; kRopeHalfAny: a unit is one vector
 // whose partners are read one by one, all loads of a pass before its stores (a barrier between,
 // since a row may be turned in place).
-template <typename T, int kLayout, bool kWide>
-__global__ void __launch_bounds__(RopeShape<kWide>::kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+//
+// kAppend: keys and values go to their ring slots instead of an output; a row's heads are the queries,
+// the keys and the values, and a value's vectors pass as they are.  The slots of the CTA's rows are
+// looked up once per head, beside the angles.
+template <typename T, int kLayout, bool kWide, bool kAppend>
+__global__ void __launch_bounds__(RopeShape<kWide>::kThreads)
+    rope_kernel(const __grid_constant__ std::conditional_t<kAppend, RopeAppendArgs, RopeArgs> a) {
   constexpr int kRopeThreads = RopeShape<kWide>::kThreads, kRopeAhead = RopeShape<kWide>::kAhead;
   // kRopeHalfAny: a pass holds whole heads (of 8, 16 or 32 vectors), so no later one reads what it turned
   static_assert(kRopeThreads * kRopeAhead % 32 == 0, "a pass holds whole heads");
@@ -91,6 +71,7 @@ __global__ void __launch_bounds__(RopeShape<kWide>::kThreads) rope_kernel(const 
   constexpr int V = Vec::V;
   constexpr int K = kLayout == kRopeHalf ? V / 2 : kLayout == kRopeInterleaved ? (V >= 4 ? V / 4 : 1) : 1;
   __shared__ float4 s_cs[kRopeRows][32];
+  __shared__ int32_t s_row[kAppend ? kRopeRows * kMaxKvHeads : 1];  // pool row of (row, KV head), -1: not stored
   // Launched as a programmatic dependent.  A decode that follows with early reads may start its
   // schedule and loads once the kernels before this one have completed: its caller vouches for what
   // they wrote, not for less.
@@ -106,13 +87,23 @@ __global__ void __launch_bounds__(RopeShape<kWide>::kThreads) rope_kernel(const 
     if (threadIdx.x == 0 && i0 == 0) atomicOr(a.err, HWKV_DEVERR_NEG_LENGTH);
     return;
   }
+  int turn_pos = pos;
+  if constexpr (kAppend) {
+    if (a.turn_pos != nullptr) turn_pos = a.turn_pos[s];
+    if (turn_pos < 0 || pos > INT32_MAX - n || turn_pos > INT32_MAX - n) {
+      if (threadIdx.x == 0 && i0 == 0) atomicOr(a.err, HWKV_DEVERR_NEG_LENGTH);
+      return;
+    }
+  }
   const int rows = min(a.rows, n - i0);
   if (rows <= 0) return;
 
+  bool keys_out = false;
+  if constexpr (kAppend) keys_out = a.keys_out != 0;
   const int D = a.head_dim, half = a.rot / 2;
-  const int nh = a.q_heads + a.k_heads;
+  const int nh = a.q_heads + (kAppend ? 2 : 1) * a.k_heads;
   const int turned = kLayout == kRopeHalf ? half / V : D / V;         // units of a head that turn
-  const int per_head = kLayout == kRopeHalf ? turned + a.copy * (D - a.rot) / V : turned;
+  const int per_head = kLayout == kRopeHalf ? turned + (kAppend ? 1 : a.copy) * (D - a.rot) / V : turned;
   const int units = rows * nh * per_head;
 
   // cosines and sines; pairs past rot / 2 do not turn
@@ -122,15 +113,30 @@ __global__ void __launch_bounds__(RopeShape<kWide>::kThreads) rope_kernel(const 
       const int r = e / pairs, i = e - r * pairs;
       float sn = 0.f, cn = 1.f;
       if (i < half) {
-        const uint64_t t = a.turns[i] * (uint64_t)((uint32_t)pos + (uint32_t)(i0 + r));
-        const float x = (float)(int32_t)(t >> 32) * 0x1p-31f;  // half turns
-        sincospif(x, &sn, &cn);
-        cn *= a.magnitude;
-        sn *= a.magnitude;
+        turn_angle(a.turns[i], (uint32_t)turn_pos + (uint32_t)(i0 + r), a.magnitude, cn, sn);
       }
       float* at = reinterpret_cast<float*>(&s_cs[r][cs_slot<K>(i >> 1)]) + (i & 1);
       at[0] = cn;
       at[2] = sn;
+    }
+  };
+
+  // kAppend: where the rows go, -1 for those whose slot a later row of the chunk takes
+  auto slots = [&]() {
+    if constexpr (kAppend) {
+      for (int e = threadIdx.x; e < rows * a.k_heads; e += kRopeThreads) {
+        const int r = e / a.k_heads, h = e - r * a.k_heads;
+        const int bs = a.pv.block_size;
+        const int C = (a.g.nblk_prefix[h + 1] - a.g.nblk_prefix[h]) * bs;
+        int32_t at = -1;
+        if (n - (i0 + r) <= C) {
+          const int slot = (pos + i0 + r) % C, jb = slot / bs;
+          const int32_t blk = a.pv.tbl[a.g.tbl_base + (int64_t)s * a.g.tbl_seq_stride + a.g.nblk_prefix[h] + jb];
+          if (blk >= 0 && (int64_t)blk < a.pv.total_blocks) at = blk * 2 * bs + (slot - jb * bs);
+          else atomicOr(a.err, HWKV_DEVERR_BAD_BLOCK);
+        }
+        s_row[e] = at;
+      }
     }
   };
 
@@ -158,9 +164,32 @@ __global__ void __launch_bounds__(RopeShape<kWide>::kThreads) rope_kernel(const 
   };
   auto row_of = [&](const Unit& x, const RopeTensor& q, const RopeTensor& k) {
     const bool key = x.h >= a.q_heads;
-    const RopeTensor& t = key ? k : q;
-    return static_cast<T*>(t.data) + s * t.seq_stride + (i0 + x.r) * t.row_stride + (int64_t)(key ? x.h - a.q_heads : x.h) * D;
+    int h = key ? x.h - a.q_heads : x.h;
+    const RopeTensor* t = key ? &k : &q;
+    if constexpr (kAppend) {
+      if (h >= a.k_heads && key) {
+        t = &a.v;
+        h -= a.k_heads;
+      }
+    }
+    return static_cast<T*>(t->data) + s * t->seq_stride + (i0 + x.r) * t->row_stride + (int64_t)h * D;
   };
+  // Stores a vector of a turned row: to its output and, kAppend, a key's or value's to its slot
+  auto put = [&](const Unit& x, T* dst, int d, uint4 v) {
+    if constexpr (!kAppend) {
+      *reinterpret_cast<uint4*>(dst + d) = v;
+    } else {
+      const int kh = x.h - a.q_heads;
+      if (kh < 0 || (kh < a.k_heads && a.keys_out)) *reinterpret_cast<uint4*>(dst + d) = v;
+      if (kh < 0) return;
+      const bool val = kh >= a.k_heads;
+      const int32_t at = s_row[x.r * a.k_heads + (val ? kh - a.k_heads : kh)];
+      if (at < 0) return;
+      *reinterpret_cast<uint4*>(static_cast<T*>(a.pv.pool) + ((int64_t)at + (val ? a.pv.block_size : 0)) * D + d) = v;
+    }
+  };
+  // whether a unit's row turns (a value's does not)
+  auto turns_at = [&](const Unit& x) { return !kAppend || x.h < a.q_heads + a.k_heads; };
 
   for (int u0 = 0; u0 < units; u0 += kRopeThreads * kRopeAhead) {
     uint4 lo[kRopeAhead], hi[kRopeAhead];
@@ -184,13 +213,14 @@ __global__ void __launch_bounds__(RopeShape<kWide>::kThreads) rope_kernel(const 
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             const int d = j * V + e;
-            if (d < a.rot) mate[k][e] = src[d < half ? d + half : d - half];
+            if (d < a.rot && turns_at(un[k])) mate[k][e] = src[d < half ? d + half : d - half];
           }
         }
       }
     }
     if (u0 == 0) {
       angles();
+      slots();
       __syncthreads();
     } else if (kLayout == kRopeHalfAny) {
       __syncthreads();
@@ -201,9 +231,12 @@ __global__ void __launch_bounds__(RopeShape<kWide>::kThreads) rope_kernel(const 
       if (u >= units) continue;
       const int j = un[k].j;
       const float4* cs = s_cs[un[k].r];
-      T* dst = row_of(un[k], a.q_out, a.k_out);
+      T* dst = kAppend && un[k].h >= a.q_heads && !(keys_out && un[k].h < nh - a.k_heads) ? nullptr : row_of(un[k], a.q_out, a.k_out);
       if constexpr (kLayout == kRopeHalf) {
-        if (j < turned) {
+        if (j < turned && !turns_at(un[k])) {
+          put(un[k], dst, j * V, lo[k]);
+          put(un[k], dst, half + j * V, hi[k]);
+        } else if (j < turned) {
           Vec x, y;
           x.load(lo[k]);
           y.load(hi[k]);
@@ -218,14 +251,14 @@ __global__ void __launch_bounds__(RopeShape<kWide>::kThreads) rope_kernel(const 
             y.v[e] = q.x;
             y.v[e + 1] = q.y;
           }
-          *reinterpret_cast<uint4*>(dst + j * V) = x.store();
-          *reinterpret_cast<uint4*>(dst + half + j * V) = y.store();
+          put(un[k], dst, j * V, x.store());
+          put(un[k], dst, half + j * V, y.store());
         } else {
-          *reinterpret_cast<uint4*>(dst + a.rot + (j - turned) * V) = lo[k];
+          put(un[k], dst, a.rot + (j - turned) * V, lo[k]);
         }
       } else if constexpr (kLayout == kRopeInterleaved) {
-        if (j * V >= a.rot) {  // past the pairs: unchanged, whatever its bits
-          if (a.copy) *reinterpret_cast<uint4*>(dst + j * V) = lo[k];
+        if (j * V >= a.rot || !turns_at(un[k])) {  // past the pairs: unchanged, whatever its bits
+          if (kAppend || a.copy) put(un[k], dst, j * V, lo[k]);
           continue;
         }
         Vec x;
@@ -236,10 +269,10 @@ __global__ void __launch_bounds__(RopeShape<kWide>::kThreads) rope_kernel(const 
           if (j * V + e < a.rot) turn(x.v[e], x.v[e + 1], t.x, t.z);
           if (j * V + e + 2 < a.rot) turn(x.v[e + 2], x.v[e + 3], t.y, t.w);
         }
-        *reinterpret_cast<uint4*>(dst + j * V) = x.store();
+        put(un[k], dst, j * V, x.store());
       } else {
-        if (j * V >= a.rot) {
-          if (a.copy) *reinterpret_cast<uint4*>(dst + j * V) = lo[k];
+        if (j * V >= a.rot || !turns_at(un[k])) {
+          if (kAppend || a.copy) put(un[k], dst, j * V, lo[k]);
           continue;
         }
         Vec x;
@@ -253,14 +286,14 @@ __global__ void __launch_bounds__(RopeShape<kWide>::kThreads) rope_kernel(const 
           const float* t = reinterpret_cast<const float*>(&cs[i >> 1]) + (i & 1);
           x.v[e] = d < half ? fmaf(x.v[e], t[0], -(m * t[2])) : fmaf(x.v[e], t[0], m * t[2]);
         }
-        *reinterpret_cast<uint4*>(dst + j * V) = x.store();
+        put(un[k], dst, j * V, x.store());
       }
     }
   }
 }
 
-template <typename T, int kLayout, bool kWide>
-cudaError_t launch_shape(const RopeArgs& a, unsigned grid, cudaStream_t st) {
+template <typename T, int kLayout, bool kWide, bool kAppend, typename Args>
+cudaError_t launch_shape(const Args& a, unsigned grid, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(RopeShape<kWide>::kThreads);
@@ -270,38 +303,47 @@ cudaError_t launch_shape(const RopeArgs& a, unsigned grid, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_kernel<T, kLayout, kWide>, a);
+  return cudaLaunchKernelEx(&cfg, rope_kernel<T, kLayout, kWide, kAppend>, a);
 }
 
-template <typename T, int kLayout>
-cudaError_t launch_one(const RopeArgs& a, unsigned grid, cudaStream_t st) {
-  return (int64_t)a.num_seqs * a.n_max <= kWideTokens ? launch_shape<T, kLayout, true>(a, grid, st)
-                                                      : launch_shape<T, kLayout, false>(a, grid, st);
+template <typename T, int kLayout, bool kAppend, typename Args>
+cudaError_t launch_one(const Args& a, unsigned grid, cudaStream_t st) {
+  return (int64_t)a.num_seqs * a.n_max <= kWideTokens ? launch_shape<T, kLayout, true, kAppend>(a, grid, st)
+                                                      : launch_shape<T, kLayout, false, kAppend>(a, grid, st);
 }
 
-template <typename T>
-cudaError_t launch_layout(const RopeArgs& a, int layout, unsigned grid, cudaStream_t st) {
+template <typename T, bool kAppend, typename Args>
+cudaError_t launch_layout(const Args& a, int layout, unsigned grid, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T);
-  if (layout == HWKV_ROPE_INTERLEAVED) return launch_one<T, kRopeInterleaved>(a, grid, st);
-  if (a.rot % (2 * V) == 0) return launch_one<T, kRopeHalf>(a, grid, st);
-  return launch_one<T, kRopeHalfAny>(a, grid, st);
+  if (layout == HWKV_ROPE_INTERLEAVED && a.rot > 0) return launch_one<T, kRopeInterleaved, kAppend>(a, grid, st);
+  if (a.rot % (2 * V) == 0) return launch_one<T, kRopeHalf, kAppend>(a, grid, st);
+  return launch_one<T, kRopeHalfAny, kAppend>(a, grid, st);
+}
+
+// Rows of a CTA: enough vectors for its threads (5 heads of 64 in bf16, 20 units to a row, 4096 rows:
+// 1 row 7.4 us, 4 rows 4.6), and two where CTAs are many (40 heads of 128: 4096 rows 13.6 us with 1,
+// 13.9 with 2; 8192 rows 22.2 and 21.2).
+template <bool kAppend, typename Args>
+cudaError_t launch_rows(Args a, int heads, int layout, bool f32, cudaStream_t st) {
+  const int64_t tokens = (int64_t)a.num_seqs * a.n_max;
+  const int vectors = heads * a.head_dim * (f32 ? 4 : 2) / 16;
+  const int units = layout == HWKV_ROPE_INTERLEAVED ? vectors : vectors / 2;
+  a.rows = std::min(kRopeRows, std::max(tokens >= 8192 ? 2 : 1, 512 / units));
+  const int64_t grid = (int64_t)a.num_seqs * ((a.n_max + a.rows - 1) / a.rows);
+  const cudaError_t e = f32 ? launch_layout<float, kAppend>(a, layout, (unsigned)grid, st)
+                            : launch_layout<__nv_bfloat16, kAppend>(a, layout, (unsigned)grid, st);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_rope(RopeArgs a, int layout, bool f32, cudaStream_t st) {
-  // Rows of a CTA: enough vectors for its threads (5 heads of 64 in bf16, 20 units to a row, 4096 rows:
-  // 1 row 7.4 us, 4 rows 4.6), and two where CTAs are many (40 heads of 128: 4096 rows 13.6 us with 1,
-  // 13.9 with 2; 8192 rows 22.2 and 21.2).
-  const int64_t tokens = (int64_t)a.num_seqs * a.n_max;
-  const int vectors = (a.q_heads + a.k_heads) * a.head_dim * (f32 ? 4 : 2) / 16;
-  const int units = layout == HWKV_ROPE_INTERLEAVED ? vectors : vectors / 2;
-  a.rows = std::min(kRopeRows, std::max(tokens >= 8192 ? 2 : 1, 512 / units));
-  const int64_t grid = (int64_t)a.num_seqs * ((a.n_max + a.rows - 1) / a.rows);
-  const cudaError_t e = f32 ? launch_layout<float>(a, layout, (unsigned)grid, st)
-                            : launch_layout<__nv_bfloat16>(a, layout, (unsigned)grid, st);
-  count_launches(1);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_rows<false>(a, a.q_heads + a.k_heads, layout, f32, st);
+}
+
+cudaError_t launch_rope_append(RopeAppendArgs a, int layout, bool f32, cudaStream_t st) {
+  return launch_rows<true>(a, a.q_heads + 2 * a.k_heads, layout, f32, st);
 }
 
 }  // namespace hwkv

@@ -415,6 +415,26 @@ int hwkv_rope(hwkv_pool_t pool, const hwkv_rope_t* rope, const hwkv_rows_t* q, i
               int n_max, const int32_t* pos_dev, const int32_t* n_dev, const hwkv_rows_t* q_out,
               const hwkv_rows_t* k_out, void* stream);
 
+/* Rotary positions on the way into the pool: one call turns the queries and keys of a chunk (or of one token, n_max 1)
+ * and stores the turned keys and the values in one layer.  Row i of sequence s, 0 <= i < n_s, is token pos_s + i of the
+ * sequence: its slot is (pos_s + i) mod C, and its query and key turn by position turn_pos_s + i (turn_pos_dev
+ * NULL: pos_s + i; a prefix kept in a pool of its own puts the two apart).  The last min(C, n_s) rows are written, as
+ * hwkv_prefill_attn does; it is the append of any pool type for a chunk that is attended elsewhere.
+ *   rope: as hwkv_rope, or NULL: nothing turns.  q with q_out, or neither; k_out (the turned keys, rows below
+ *   n_s, beside those stored) or NULL.  q_out may be q; k_out may be k, but not for 8-bit pools; outputs
+ *   must not overlap anything else.  q_heads is a multiple of kv_heads.  Strides as in hwkv_rows_t.
+ *   pos_dev, turn_pos_dev, n_dev: device int32 [num_seqs]; a negative position, one that reaches 2^31, or n_s outside
+ *   [0, n_max] flags HWKV_DEVERR_NEG_LENGTH and skips the sequence.  n_dev NULL: all n_max rows.
+ * bf16 and fp32 pools hold what hwkv_rope and then hwkv_append of each row in turn leave, bit for bit.  8-bit pools store every
+ * group of 16 slots that a row goes to once, anew: the slots whose positions are in the window of the new length take their row,
+ * rounded once from the turned fp32 value, or keep their value at the new scale; every other slot becomes zero.
+ * One kernel on `stream`.
+ * Errors: HWKV_ERR_INVALID_ARG, HWKV_ERR_ALIGNMENT, HWKV_ERR_UNSUPPORTED, HWKV_ERR_CUDA. */
+int hwkv_rope_append(hwkv_pool_t pool, int layer, const hwkv_rope_t* rope, const hwkv_rows_t* q, int q_heads,
+                     const hwkv_rows_t* k, const hwkv_rows_t* v, int n_max, const int32_t* pos_dev,
+                     const int32_t* turn_pos_dev, const int32_t* n_dev, const hwkv_rows_t* q_out,
+                     const hwkv_rows_t* k_out, void* stream);
+
 /* Number of kernels this library has launched in this process (all pools, all devices).
  * Lets a caller count the launches inside a timed region. */
 int hwkv_kernel_launches(uint64_t* out);

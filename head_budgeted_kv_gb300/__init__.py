@@ -19,7 +19,8 @@ from . import binding
 from .binding import (HWKV_BF16, HWKV_E4M3, HWKV_F32, HWKV_KERNEL_AUTO, HWKV_KERNEL_SIMT, HWKV_KERNEL_TENSOR, DecodeLaunch, HwkvError, RopeTable, Score,
                       hwkv_abi_version, hwkv_advance_positions, hwkv_append, hwkv_append_decode_attn, hwkv_block_table,
                       hwkv_check_device_errors, hwkv_kernel_launches,
-                      hwkv_decode_attn, hwkv_decode_attn_score, hwkv_decode_workspace_bytes, hwkv_materialize, hwkv_pool_bytes,
+                      hwkv_decode_attn, hwkv_decode_attn_score, hwkv_decode_attn_shared,
+                      hwkv_decode_shared_workspace_bytes, hwkv_decode_workspace_bytes, hwkv_materialize, hwkv_pool_bytes,
                       hwkv_pool_create, hwkv_pool_destroy, hwkv_pool_geometry, hwkv_prefill_attn,
                       hwkv_prefill_attn_score, hwkv_prefill_plan, hwkv_prefill_workspace_bytes, hwkv_rope, hwkv_rope_append, hwkv_rope_table, hwkv_set_block_table, hwkv_set_decode_config,
                       hwkv_set_prefill_config, hwkv_wait_selftest)
@@ -28,7 +29,8 @@ __all__ = [
     "Pool", "DecodeLaunch", "HwkvError", "RopeTable", "Score", "binding", "rope_table", "HWKV_F32", "HWKV_BF16", "HWKV_E4M3", "HWKV_KERNEL_AUTO", "HWKV_KERNEL_TENSOR",
     "HWKV_KERNEL_SIMT", "hwkv_abi_version", "hwkv_advance_positions", "hwkv_append", "hwkv_append_decode_attn", "hwkv_block_table",
     "hwkv_check_device_errors", "hwkv_kernel_launches",
-    "hwkv_decode_attn", "hwkv_decode_attn_score", "hwkv_decode_workspace_bytes", "hwkv_materialize", "hwkv_pool_bytes", "hwkv_pool_create",
+    "hwkv_decode_attn", "hwkv_decode_attn_score", "hwkv_decode_attn_shared", "hwkv_decode_shared_workspace_bytes",
+    "hwkv_decode_workspace_bytes", "hwkv_materialize", "hwkv_pool_bytes", "hwkv_pool_create",
     "hwkv_pool_destroy", "hwkv_pool_geometry", "hwkv_prefill_attn", "hwkv_prefill_attn_score", "hwkv_prefill_plan", "hwkv_prefill_workspace_bytes", "hwkv_rope", "hwkv_rope_append", "hwkv_rope_table",
     "hwkv_set_block_table", "hwkv_set_decode_config", "hwkv_set_prefill_config", "hwkv_wait_selftest",
 ]
@@ -89,6 +91,8 @@ class Pool:
         self.workspace = None
         self.prefill_workspace = None
         self._prefill_captured = False
+        self.shared_workspace = None
+        self._shared_captured = False
         self._outgrown = []  # workspaces that captured graphs may still use
         self._size_workspace()
 
@@ -174,6 +178,43 @@ class Pool:
         else:
             hwkv_decode_attn_score(self.handle, layer, q, binding.score(scale, softcap, slopes, q), pos, out,
                                    self.workspace, k_new, v_new, stream, early_reads)
+        return out
+
+    def shared_decode(self, layer: int, prefix: "Pool", q, scale: float, lens, prefix_of, prefix_lens, k_new=None, v_new=None,
+                      out=None, stream=None, softcap: float = 0.0, slopes=None):
+        """Attention of q [B][Hq][D] whose sequences continue prefixes kept once in the pool ``prefix``: sequence s has
+        lens[s] tokens of its own in this pool (after the append; with k_new and v_new [B][Hkv][D] the length before it) behind
+        the prefix_lens[f] tokens of prefix f = prefix_of[s] (negative: behind none).  int32 [B], [B] and
+        [prefix.num_seqs].  softcap, slopes: as ``decode``.  Keeps a workspace, grown on demand; one that
+        a capture has used stays when it is outgrown."""
+        if out is None:
+            out = torch.empty_like(q)
+        if (k_new is None) != (v_new is None):
+            raise ValueError("k_new and v_new go together")
+        if out.shape != q.shape:
+            raise ValueError("out must match q")
+        for t, heads in ((q, q.shape[1]), (out, q.shape[1]), (k_new, self.kv_heads), (v_new, self.kv_heads)):
+            if t is not None and (self._check_rows(t, "q, out, k_new and v_new") != heads or t.dim() != 3):
+                raise ValueError("q, out, k_new and v_new must be [B][heads][D]")
+        if not (self._is_counts(lens) and self._is_counts(prefix_of) and prefix._is_counts(prefix_lens)):
+            raise ValueError(f"lens and prefix_of must hold {self.num_seqs} values, prefix_lens {prefix.num_seqs}, in a row on "
+                             f"{self.buffer.device}")
+        if torch.cuda.is_current_stream_capturing():
+            self._shared_captured = True
+        args = (layer, q, binding.score(scale, softcap, slopes, q), lens, prefix_of, prefix_lens, out)
+        if self.shared_workspace is not None:
+            try:
+                hwkv_decode_attn_shared(self.handle, prefix.handle, *args, self.shared_workspace, k_new, v_new, stream)
+                return out
+            except HwkvError as e:
+                if e.status != binding.HWKV_ERR_WORKSPACE_TOO_SMALL:
+                    raise
+                if self._shared_captured:
+                    self._outgrown.append(self.shared_workspace)
+        need = hwkv_decode_shared_workspace_bytes(self.handle, prefix.handle, q.shape[1])
+        self.shared_workspace = torch.empty(need, dtype=torch.uint8, device=self.buffer.device)
+        self._shared_captured = torch.cuda.is_current_stream_capturing()
+        hwkv_decode_attn_shared(self.handle, prefix.handle, *args, self.shared_workspace, k_new, v_new, stream)
         return out
 
     def decode_launch(self, layer: int, q, scale: float, lens, out, k_new=None, v_new=None, stream=None,

@@ -34,6 +34,7 @@ HWKV_BF16 = 1
 HWKV_E4M3 = 2
 HWKV_KERNEL_AUTO, HWKV_KERNEL_TENSOR, HWKV_KERNEL_SIMT = 0, 1, 2
 HWKV_DEVERR_NEG_LENGTH, HWKV_DEVERR_BAD_BLOCK, HWKV_DEVERR_SRC_RANGE, HWKV_DEVERR_WAIT_TIMEOUT = 1, 2, 4, 8
+HWKV_DEVERR_BAD_PREFIX = 16
 HWKV_DECODE_EARLY_READS = 1
 HWKV_ROPE_HALF, HWKV_ROPE_INTERLEAVED = 0, 1
 HWKV_ROPE_SCALE_NONE, HWKV_ROPE_SCALE_LINEAR, HWKV_ROPE_SCALE_NTK, HWKV_ROPE_SCALE_BY_PARTS = 0, 1, 2, 3
@@ -90,6 +91,8 @@ SIGNATURES = [
     ("hwkv_append_decode_attn", _i, [_vp, _i, _vp, _i, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _u64, _vp]),
     ("hwkv_decode_attn_ex", _i, [_vp, _i, _vp, _i, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _u64, _i, _vp]),
     ("hwkv_decode_attn_score", _i, [_vp, _i, _vp, _i, _scorep, _vp, _vp, _vp, _vp, _vp, _u64, _i, _vp]),
+    ("hwkv_decode_attn_shared", _i, [_vp, _vp, _i, _vp, _i, _scorep, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _u64, _vp]),
+    ("hwkv_decode_shared_workspace_bytes", _i, [_vp, _vp, _i, _c_u64p]),
     ("hwkv_decode_attn_noalloc", _i, [_vp, _i, _vp, _i, ctypes.c_float, _vp, _vp, _vp]),
     ("hwkv_prefill_attn", _i, [_vp, _i, _vp, _i, ctypes.c_float, _vp, _vp, _i, _vp, _vp, _vp, _vp, _u64, _vp]),
     ("hwkv_prefill_attn_score", _i, [_vp, _i, _vp, _i, _scorep, _vp, _vp, _i, _vp, _vp, _vp, _vp, _u64, _vp]),
@@ -445,6 +448,27 @@ def hwkv_decode_attn_score(pool: int, layer: int, q: torch.Tensor, score: Score,
     _check(load().hwkv_decode_attn_score(pool, layer, _ptr(q), q.shape[1], score, _ptr(k_new), _ptr(v_new), _ptr(lens),
                                          _ptr(out), _ptr(workspace), ws_bytes,
                                          HWKV_DECODE_EARLY_READS if early_reads else 0, _stream_ptr(stream)))
+
+
+def hwkv_decode_shared_workspace_bytes(pool: int, prefix: int, q_heads: int) -> int:
+    out = ctypes.c_uint64(0)
+    _check(load().hwkv_decode_shared_workspace_bytes(pool, prefix, q_heads, ctypes.byref(out)))
+    return out.value
+
+
+def hwkv_decode_attn_shared(pool: int, prefix: int, layer: int, q: torch.Tensor, score: Score, lens: torch.Tensor,
+                            prefix_of: torch.Tensor, prefix_lens: torch.Tensor, out: torch.Tensor,
+                            workspace: torch.Tensor, k_new: Optional[torch.Tensor] = None,
+                            v_new: Optional[torch.Tensor] = None, stream=None):
+    """Decode of sequences behind the prefixes that pool `prefix` holds: at own lengths `lens` (after the append),
+    or with k_new, v_new at own positions `lens`, appended first."""
+    if not all(t.is_contiguous() for t in (q, out, k_new, v_new) if t is not None):
+        raise ValueError("q, out, k_new and v_new must be contiguous")
+    if not (lens.dtype == prefix_of.dtype == prefix_lens.dtype == torch.int32):
+        raise ValueError("lengths and prefixes must be int32")
+    _check(load().hwkv_decode_attn_shared(pool, prefix, layer, _ptr(q), q.shape[1], score, _ptr(k_new), _ptr(v_new), _ptr(lens),
+                                          _ptr(prefix_of), _ptr(prefix_lens), _ptr(out), _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
 
 
 class DecodeLaunch:

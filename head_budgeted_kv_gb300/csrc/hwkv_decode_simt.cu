@@ -150,7 +150,11 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_simt_kernel(const __gr
         A += sm_acc[(w * GH + gl) * D + d] * f;
       }
     }
-    if (it.nchunks == 1) {
+    if (it.nchunks == 1 && a.open_acc != nullptr) {
+      const int64_t row = ((int64_t)it.s * a.pv.kv_heads + it.h) * G + g;
+      a.open_acc[row * D + d] = A;
+      if (d == 0) reinterpret_cast<float2*>(a.open_ml)[row] = make_float2(M, Ls);
+    } else if (it.nchunks == 1) {
       T* out = static_cast<T*>(a.out) + ((int64_t)it.s * Hq + it.h * G + g) * D + d;
       store_out<T>(out, Ls > 0.f ? A / Ls : 0.f);
     } else {
@@ -185,8 +189,13 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ De
         A += a.part_acc[ig * D + d] * f;
       }
     }
-    T* out = static_cast<T*>(a.out) + ((int64_t)s * H * G + h * G + g) * D + d;
-    store_out<T>(out, Ls > 0.f ? A / Ls : 0.f);
+    const int64_t row = (int64_t)s * H * G + h * G + g;
+    if (a.open_acc != nullptr) {
+      a.open_acc[row * D + d] = A;
+      if (d == 0) reinterpret_cast<float2*>(a.open_ml)[row] = make_float2(M, Ls);
+    } else {
+      store_out<T>(static_cast<T*>(a.out) + row * D + d, Ls > 0.f ? A / Ls : 0.f);
+    }
   }
 }
 

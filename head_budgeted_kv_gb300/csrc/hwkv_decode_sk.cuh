@@ -64,7 +64,10 @@ __host__ __device__ constexpr int sk_min_ctas() {
   return sizeof(T) == 2 ? (D == 64 ? 3 : 2) : (D == 64 ? 2 : 1);
 }
 
-template <typename Elem, int D, int GP, int NS, bool SC>
+// kOpen: the results stay open, each group's (m, l) and accumulators to be joined with those of other keys.
+// Such a grid needs nothing of the grid ahead of it, which starts it only once all before has completed: it
+// waits for that grid at its end alone, so that what follows this grid follows both.
+template <typename Elem, int D, int GP, int NS, bool SC, bool kOpen>
 __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
     decode_sk_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ DecodeArgs a) {
   using State = WarpState<Elem, D, GP, SC>;
@@ -112,7 +115,7 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
   // layer's pool were written before the preceding grid in the stream started, so the schedule
   // and the first tile loads run before the wait; q, k_new / v_new and every write of this
   // grid come after it.
-  if (!a.early) griddep_wait();
+  if (!kOpen && !a.early) griddep_wait();
 
   if (cta == 0) {
     for (int s = threadIdx.x; s < B; s += W * 32)
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
   // the first stages are issued by different lanes so their table lookups overlap
   if (has_range)
     for (int i = 0; i < NS && j_issue < t_hi; ++i) issue_next(i);
-  if (a.early && has_range && lane < l2_prefetch<D>() && t_hi - t_lo >= kL2PrefetchMin) {
+  if (!kOpen && a.early && has_range && lane < l2_prefetch<D>() && t_hi - t_lo >= kL2PrefetchMin) {
     // Until the wait below ends, the preceding grid only merges and completes and the memory
     // system is nearly idle: pull the tiles this warp takes after its staged ones into L2
     // (lane i: the position i steps on; a position inside a gap is skipped).
@@ -220,15 +223,24 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
       }
     }
   }
-  if (a.early) griddep_wait();
+  if (!kOpen && a.early) griddep_wait();
   // groups with nothing resident (length 0) get a zero output, each from one CTA
   for (int g = cta; g < ngroups; g += nctas) {
     const Group gr = load_group(a, s_lens, g);
-    if (gr.tiles == 0)
-      for (int e = threadIdx.x; e < G * D; e += W * 32)
-        store_out<Elem>(out + ((int64_t)gr.s * Hq + gr.h * G + e / D) * D + e % D, 0.f);
+    if (gr.tiles == 0) {
+      if constexpr (kOpen) {
+        for (int e = threadIdx.x; e < G; e += W * 32)
+          reinterpret_cast<float2*>(a.open_ml)[(int64_t)g * G + e] = make_float2(kNegInf, 0.f);
+      } else {
+        for (int e = threadIdx.x; e < G * D; e += W * 32)
+          store_out<Elem>(out + ((int64_t)gr.s * Hq + gr.h * G + e / D) * D + e % D, 0.f);
+      }
+    }
   }
-  if (!has_range) return;
+  if (!has_range) {
+    if constexpr (kOpen) griddep_wait();
+    return;
+  }
 
   int sg = g_start;            // segment cursor (uniform in the CTA)
   long long spre = pre_start;
@@ -307,7 +319,10 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
             A += sc_acc[(w * SG + gl) * D + d] * f;
           }
         }
-        if (whole) {
+        if (kOpen && whole) {
+          a.open_acc[((int64_t)sg * G + g) * D + d] = A;
+          if (d == 0) reinterpret_cast<float2*>(a.open_ml)[(int64_t)sg * G + g] = make_float2(M, Ls);
+        } else if (whole) {
           store_out<Elem>(out + ((int64_t)sgr.s * Hq + sgr.h * G + g) * D + d, Ls > 0.f ? A / Ls : 0.f);
         } else {
           a.part_acc[(slot * G + g) * D + d] = A;
@@ -331,7 +346,10 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
       const int c_lo = cta_of(spre + kGapTiles, T, nctas), c_hi = cta_of(spre + group_span(sgr) - 1, T, nctas);
       const bool all_live = T >= nctas;  // then no CTA range is empty
       const int k = c_hi - c_lo + 1;
-      Elem* const out_grp = out + ((int64_t)sgr.s * Hq + sgr.h * G) * D;
+      Elem* const out_grp = kOpen ? nullptr : out + ((int64_t)sgr.s * Hq + sgr.h * G) * D;
+      float* const open_acc = kOpen ? a.open_acc : nullptr;
+      float* const open_ml = kOpen ? a.open_ml : nullptr;
+      const long long open_slot = kOpen ? sg : 0;
       if (!all_live || k <= kFlatMerge) {
         int expected = k;
         if (!all_live) {
@@ -342,8 +360,8 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
           auto live = [&](int i) {
             return all_live || range_start(T, c_lo + i + 1, nctas) > range_start(T, c_lo + i, nctas);
           };
-          merge_slots<Elem, D, GP, CtaSync>(a.part_acc, a.part_ml, (long long)sg + c_lo, k, G, live, all_live, out_grp, nullptr,
-                         nullptr, 0, sc_acc, kMlCap, ms, a.pv.err);
+          merge_slots<Elem, D, GP, CtaSync>(a.part_acc, a.part_ml, (long long)sg + c_lo, k, G, live, all_live, out_grp, open_acc,
+                         open_ml, open_slot, sc_acc, kMlCap, ms, a.pv.err);
         }
       } else {
         auto live = [](int) { return true; };
@@ -357,7 +375,7 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
                          a.part2_ml, slot2, sc_acc, kMlCap, ms, a.pv.err);
           if (arrive_last<CtaSync>(&a.counters[sg], nb, &s_last))
             merge_slots<Elem, D, GP, CtaSync>(a.part2_acc, a.part2_ml, (long long)sg * a.merge_blocks, nb, G, live, true, out_grp,
-                           nullptr, nullptr, 0, sc_acc, kMlCap, ms, a.pv.err);
+                           open_acc, open_ml, open_slot, sc_acc, kMlCap, ms, a.pv.err);
         }
       }
     }
@@ -376,6 +394,7 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
   }
   if (ms.stuck0 >= 0) mbar_wait_bounded(&merge_bar[0], (uint32_t)ms.stuck0);
   if (ms.stuck1 >= 0) mbar_wait_bounded(&merge_bar[1], (uint32_t)ms.stuck1);
+  if constexpr (kOpen) griddep_wait();
 }
 
 template <typename T, int D, int GP, int NS>
@@ -396,26 +415,26 @@ constexpr int stages() {
 template <typename T, int D, int GP>
 cudaError_t configure_one(int* ctas_per_sm) {
   constexpr int NS = stages<T, D>();
-  cudaError_t e = cudaFuncSetAttribute(decode_sk_kernel<T, D, GP, NS, false>,
+  cudaError_t e = cudaFuncSetAttribute(decode_sk_kernel<T, D, GP, NS, false, false>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, sk_smem_bytes<T, D, GP, NS>());
   if (e != cudaSuccess) return e;
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_sk_kernel<T, D, GP, NS, false>, kWarps * 32,
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_sk_kernel<T, D, GP, NS, false, false>, kWarps * 32,
                                                        sk_smem_bytes<T, D, GP, NS>());
 }
 
-// Scored instances (SC) are prepared at their first launch on a device, not with every pool, and
+// Scored and open instances (SC, kOpen) are prepared at their first launch on a device, not with every pool, and
 // run on the grid of the plain ones.
-template <typename T, int D, int GP, bool SC = false>
+template <typename T, int D, int GP, bool SC = false, bool kOpen = false>
 cudaError_t launch_one(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, cudaStream_t st) {
   constexpr int NS = stages<T, D>();
-  if constexpr (SC) {
+  if constexpr (SC || kOpen) {
     static std::atomic<uint64_t> prepared{0};  // a bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
     if (!(prepared.load(std::memory_order_relaxed) & bit)) {
-      e = cudaFuncSetAttribute(decode_sk_kernel<T, D, GP, NS, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(decode_sk_kernel<T, D, GP, NS, SC, kOpen>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                sk_smem_bytes<T, D, GP, NS>());
       if (e != cudaSuccess) return e;
       prepared.fetch_or(bit, std::memory_order_relaxed);
@@ -433,7 +452,7 @@ cudaError_t launch_one(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, decode_sk_kernel<T, D, GP, NS, SC>, *tmap, a);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, decode_sk_kernel<T, D, GP, NS, SC, kOpen>, *tmap, a);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -121,6 +121,7 @@ struct WarpState<E4m3, D, GP, SC> {
   // 2^5 for the slack is taken out of sums and accumulators alike where they leave the warp, and the shift out
   // of the accumulators: weights are then at most 1, and no V that bf16 holds overflows by itself
   static constexpr float kTakeSum = 0x1p-5f, kTakeAcc = 0x1p-16f;
+  static_assert(kTakeSum == 1.f / (1 << (int)kQ8Shift), "what a join of open results puts back");
   uint32_t qf[NT][D / 16][2];
   float acc[D / 16][NT][4];
   float mx[NT][2];   // reference maximum of the scores (log2 units, an integer)

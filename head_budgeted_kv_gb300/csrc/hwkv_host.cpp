@@ -1066,11 +1066,17 @@ int score_args(const hwkv_score_t& sc, ScoreArgs* out) {
   return HWKV_OK;
 }
 
-// Shared body of hwkv_decode_attn (len_add 0, no new rows) and hwkv_append_decode_attn
-// (len_add 1: lens are the positions before the append, k_new / v_new are appended).
-int decode_common(hwkv_pool_t p, int layer, const void* q, int q_heads, hwkv_score_t score, const int32_t* lens_dev,
-                  int len_add, const void* k_new, const void* v_new, void* out, void* workspace, uint64_t ws_bytes,
-                  int flags, void* stream) {
+// A decode whose arguments are checked: the kernels' arguments, and which kernels.
+struct DecodeCall {
+  DecodeArgs a;
+  bool tc = false;
+  const void* k_new = nullptr;
+  const void* v_new = nullptr;
+};
+
+int prepare_decode(hwkv_pool_t p, int layer, const void* q, int q_heads, hwkv_score_t score, const int32_t* lens_dev,
+                   int len_add, const void* k_new, const void* v_new, void* out, void* workspace, uint64_t ws_bytes,
+                   int flags, DecodeCall* call) {
   if (!p) return fail(HWKV_ERR_INVALID_ARG, "pool is NULL");
   if (flags & ~HWKV_DECODE_EARLY_READS) return fail(HWKV_ERR_INVALID_ARG, "unknown decode flags %#x", flags);
   const Geometry& g = p->g;
@@ -1099,12 +1105,11 @@ int decode_common(hwkv_pool_t p, int layer, const void* q, int q_heads, hwkv_sco
   }
   int rc = check_device(p);
   if (rc != HWKV_OK) return rc;
-  NvtxRange range_(len_add ? "hwkv_append_decode_attn" : "hwkv_decode_attn", layer);
   if (p->kernel_choice == HWKV_KERNEL_TENSOR && !(tc_eligible(p) && tc_group_ok(p, G)))
     return fail(HWKV_ERR_UNSUPPORTED,
                 "the stream-K decode needs block_size % 16 == 0, and up to 4 query heads per KV head for fp32");
 
-  DecodeArgs a;
+  DecodeArgs& a = call->a;
   std::memset(&a, 0, sizeof a);
   a.pv = pool_view(p);
   a.g = layer_geom(p, layer);
@@ -1131,26 +1136,107 @@ int decode_common(hwkv_pool_t p, int layer, const void* q, int q_heads, hwkv_sco
   a.group = G;
   a.split_tokens = lp.split;
   std::memcpy(a.chunk_prefix, lp.chunk_prefix, sizeof a.chunk_prefix);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (tc) {
-    a.k_new = len_add ? k_new : nullptr;  // appended inside the kernel
-    a.v_new = len_add ? v_new : nullptr;
-    HWKV_CUDA_TRY(launch_decode_tc(a, &p->tmap, tc_workers(p, G), st), "decode launch");
-    return ok();
+  call->tc = tc;
+  call->k_new = len_add ? k_new : nullptr;
+  call->v_new = len_add ? v_new : nullptr;
+  return HWKV_OK;
+}
+
+// Launches a prepared decode (open when a.open_acc is set).
+int launch_decode(hwkv_pool_t p, int layer, DecodeCall& call, cudaStream_t st) {
+  DecodeArgs& a = call.a;
+  const Geometry& g = p->g;
+  if (call.tc) {
+    a.k_new = call.k_new;  // appended inside the kernel
+    a.v_new = call.v_new;
+    HWKV_CUDA_TRY(a.open_acc ? launch_decode_open(a, &p->tmap, tc_workers(p, a.group), st)
+                             : launch_decode_tc(a, &p->tmap, tc_workers(p, a.group), st),
+                  "decode launch");
+    return HWKV_OK;
   }
-  if (len_add) {
+  const LayerPlan& lp = p->plans[layer];
+  if (call.k_new) {
     CopyArgs c;
     std::memset(&c, 0, sizeof c);
     c.pv = a.pv;
     c.g = a.g;
-    c.k = k_new;
-    c.v = v_new;
-    c.lens = lens_dev;
+    c.k = call.k_new;
+    c.v = call.v_new;
+    c.lens = a.lens;
     HWKV_CUDA_TRY(launch_append(c, g.dtype, st), "append launch");
   }
   HWKV_CUDA_TRY(launch_decode_simt(a, g.dtype, lp.items, st), "decode launch");
   if (lp.multi_chunk) HWKV_CUDA_TRY(launch_combine(a, g.dtype, st), "combine launch");
-  return ok();
+  return HWKV_OK;
+}
+
+// Shared body of hwkv_decode_attn (len_add 0, no new rows) and hwkv_append_decode_attn
+// (len_add 1: lens are the positions before the append, k_new / v_new are appended).
+int decode_common(hwkv_pool_t p, int layer, const void* q, int q_heads, hwkv_score_t score, const int32_t* lens_dev,
+                  int len_add, const void* k_new, const void* v_new, void* out, void* workspace, uint64_t ws_bytes,
+                  int flags, void* stream) {
+  DecodeCall call;
+  int rc = prepare_decode(p, layer, q, q_heads, score, lens_dev, len_add, k_new, v_new, out, workspace, ws_bytes, flags, &call);
+  if (rc != HWKV_OK) return rc;
+  NvtxRange range_(len_add ? "hwkv_append_decode_attn" : "hwkv_decode_attn", layer);
+  rc = launch_decode(p, layer, call, static_cast<cudaStream_t>(stream));
+  return rc != HWKV_OK ? rc : ok();
+}
+
+// How the keys of the prefixes are split on the CUDA cores: ring slots per CTA for about six CTAs per SM over
+// the sequences' tiles, and the chunks of each head.
+struct SharedPlan {
+  int split = 0;
+  int chunks = 0;
+  int32_t chunk_prefix[kMaxKvHeads + 1] = {};
+};
+
+SharedPlan plan_shared(const hwkv_pool* p, const hwkv_pool* prefix, int layer, int group) {
+  SharedPlan s;
+  const Geometry& g = prefix->g;
+  auto capacity = [&](int h) { return (int64_t)g.nblk[(size_t)layer * g.kv_heads + h] * g.block_size; };
+  int64_t slots = 0;
+  for (int h = 0; h < g.kv_heads; ++h) slots += capacity(h);
+  const int per = shared_simt_seqs(group);
+  const int64_t want = slots * g.num_seqs * ((p->g.num_seqs + per - 1) / per) / (6LL * std::max(1, p->num_sms));
+  s.split = 256;
+  while (s.split < want && s.split < 4096) s.split <<= 1;
+  for (int h = 0; h < g.kv_heads; ++h)
+    s.chunk_prefix[h + 1] = s.chunk_prefix[h] + (int32_t)((capacity(h) + s.split - 1) / s.split);
+  s.chunks = s.chunk_prefix[g.kv_heads];
+  return s;
+}
+
+// Regions of the workspace: the own decode's, its open results, the prefixes' partials.
+struct SharedLayout {
+  uint64_t own_acc = 0, own_ml = 0, part_o = 0, part_ml = 0, total = 0;
+};
+
+SharedLayout shared_layout(const hwkv_pool* p, const hwkv_pool* prefix, int group) {
+  SharedLayout w;
+  const uint64_t rows = (uint64_t)p->g.num_seqs * p->g.kv_heads * group, D = (uint64_t)p->g.head_dim;
+  uint64_t chunks = 0;
+  for (int l = 0; l < p->g.layers; ++l) chunks = std::max<uint64_t>(chunks, plan_shared(p, prefix, l, group).chunks);
+  const uint64_t parts = (uint64_t)p->g.num_seqs * chunks * group;
+  w.own_acc = align256(workspace_bytes(p, group));
+  w.own_ml = align256(w.own_acc + rows * D * 4);
+  w.part_o = align256(w.own_ml + rows * 8);
+  w.part_ml = align256(w.part_o + parts * D * 4);
+  w.total = align256(w.part_ml + parts * 8);
+  return w;
+}
+
+int check_shared(const hwkv_pool* p, const hwkv_pool* prefix, int q_heads) {
+  if (!p || !prefix) return fail(HWKV_ERR_INVALID_ARG, "pool is NULL");
+  if (p == prefix) return fail(HWKV_ERR_INVALID_ARG, "the prefixes need a pool of their own");
+  const Geometry &g = p->g, &f = prefix->g;
+  if (g.layers != f.layers || g.kv_heads != f.kv_heads || g.head_dim != f.head_dim || g.io_eb != f.io_eb)
+    return fail(HWKV_ERR_INVALID_ARG, "the prefix pool must have the pool's layers, kv_heads, head_dim and tensor type");
+  if (p->device != prefix->device) return fail(HWKV_ERR_INVALID_ARG, "the pools live on different devices");
+  if (q_heads < g.kv_heads || q_heads % g.kv_heads != 0 || q_heads / g.kv_heads > kMaxGroup)
+    return fail(HWKV_ERR_UNSUPPORTED, "q_heads must be G * kv_heads with 1 <= G <= %d (got %d)", kMaxGroup, q_heads);
+  if (g.num_seqs > 65535) return fail(HWKV_ERR_UNSUPPORTED, "at most 65535 sequences behind prefixes (got %d)", g.num_seqs);
+  return HWKV_OK;
 }
 
 }  // namespace
@@ -1178,6 +1264,71 @@ int hwkv_decode_attn_score(hwkv_pool_t p, int layer, const void* q, int q_heads,
   const bool fused = k_new != nullptr || v_new != nullptr;
   return decode_common(p, layer, q, q_heads, *score, lens_dev, fused ? 1 : 0, k_new, v_new, out, workspace, ws_bytes,
                        flags, stream);
+}
+
+int hwkv_decode_shared_workspace_bytes(hwkv_pool_t p, hwkv_pool_t prefix, int q_heads, uint64_t* out) {
+  const int rc = check_shared(p, prefix, q_heads);
+  if (rc != HWKV_OK) return rc;
+  if (!out) return fail(HWKV_ERR_INVALID_ARG, "out is NULL");
+  *out = shared_layout(p, prefix, q_heads / p->g.kv_heads).total;
+  return ok();
+}
+
+int hwkv_decode_attn_shared(hwkv_pool_t p, hwkv_pool_t prefix, int layer, const void* q, int q_heads,
+                            const hwkv_score_t* score, const void* k_new, const void* v_new, const int32_t* lens_dev,
+                            const int32_t* prefix_of_dev, const int32_t* prefix_lens_dev, void* out, void* workspace,
+                            uint64_t ws_bytes, void* stream) {
+  int rc = check_shared(p, prefix, q_heads);
+  if (rc != HWKV_OK) return rc;
+  if (!score) return fail(HWKV_ERR_INVALID_ARG, "score is NULL");
+  if (!prefix_of_dev || !prefix_lens_dev) return fail(HWKV_ERR_INVALID_ARG, "NULL tensor argument");
+  if (!aligned(prefix_of_dev, 4) || !aligned(prefix_lens_dev, 4))
+    return fail(HWKV_ERR_ALIGNMENT, "prefixes and their lengths must be 4-byte aligned");
+  const int G = q_heads / p->g.kv_heads;
+  const SharedLayout wl = shared_layout(p, prefix, G);
+  if (!workspace || ws_bytes < wl.total)
+    return fail(HWKV_ERR_WORKSPACE_TOO_SMALL, "workspace holds %llu bytes, this decode needs %llu", (unsigned long long)ws_bytes,
+                (unsigned long long)wl.total);
+  const bool fused = k_new != nullptr || v_new != nullptr;
+  DecodeCall call;
+  rc = prepare_decode(p, layer, q, q_heads, *score, lens_dev, fused ? 1 : 0, k_new, v_new, out, workspace, ws_bytes, 0, &call);
+  if (rc != HWKV_OK) return rc;
+  if (!aligned(workspace, 16)) return fail(HWKV_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  char* ws = static_cast<char*>(workspace);
+  call.a.open_acc = reinterpret_cast<float*>(ws + wl.own_acc);
+  call.a.open_ml = reinterpret_cast<float*>(ws + wl.own_ml);
+  SharedArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.pv = pool_view(prefix);
+  a.pv.err = p->d_err;
+  a.g = layer_geom(prefix, layer);
+  a.q = q;
+  a.out = out;
+  a.lens = lens_dev;
+  a.len_add = fused ? 1 : 0;
+  a.prefix_of = prefix_of_dev;
+  a.prefix_lens = prefix_lens_dev;
+  a.num_seqs = p->g.num_seqs;
+  a.num_prefixes = prefix->g.num_seqs;
+  a.group = G;
+  a.scale_log2 = call.a.scale_log2;
+  a.score = call.a.score;
+  a.own_acc = call.a.open_acc;
+  a.own_ml = call.a.open_ml;
+  a.own_shift = p->g.dtype == HWKV_E4M3 ? kQ8Shift : 0.f;
+  a.part_o = reinterpret_cast<float*>(ws + wl.part_o);
+  a.part_ml = reinterpret_cast<float*>(ws + wl.part_ml);
+  const SharedPlan sp = plan_shared(p, prefix, layer, G);
+  a.split_tokens = sp.split;
+  a.seqs_per_cta = shared_simt_seqs(G);
+  std::memcpy(a.chunk_prefix, sp.chunk_prefix, sizeof a.chunk_prefix);
+  NvtxRange range_("hwkv_decode_attn_shared", layer);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  HWKV_CUDA_TRY(launch_shared_simt(a, prefix->g.dtype, sp.chunks, st), "shared prefix launch");
+  rc = launch_decode(p, layer, call, st);
+  if (rc != HWKV_OK) return rc;
+  HWKV_CUDA_TRY(launch_shared_join(a, p->g.dtype == HWKV_F32, st), "shared join launch");
+  return ok();
 }
 
 int hwkv_append_decode_attn(hwkv_pool_t p, int layer, const void* q, int q_heads, float scale, const void* k_new,

@@ -100,6 +100,39 @@ struct DecodeArgs {
   // last: among the others they cost the plain kernels 0.4% at batch 1
   int32_t bs_log2;         // 8-bit pools: log2(block_size), or -1 when it is not a power of two
   ScoreArgs score;         // capped or distance-biased scores (scored instances only)
+  // open instances: every (seq, kv head) leaves its (m, l) and accumulators here instead of an output
+  float* open_acc;         // [B*H][G][D]
+  float* open_ml;          // [B*H][G][2]
+};
+
+// log2 of the factor that the 8-bit decode takes out of sums and accumulators alike (hwkv_decode_tile_q8.cuh)
+constexpr float kQ8Shift = 5.f;
+
+// Decode behind shared prefixes: the attention to the prefixes' keys, one partial per row and key range,
+// joined with the sequences' own parts (open instances of the decode kernels).
+struct SharedArgs {
+  PoolView pv;             // the prefixes' pool
+  LayerGeom g;
+  const void* q;           // [B][Hq][D]
+  void* out;               // [B][Hq][D]
+  const int32_t* lens;     // [B] own lengths; length after the append = lens[s] + len_add
+  int32_t len_add;
+  const int32_t* prefix_of;    // [B] prefix of each sequence, below 0: none
+  const int32_t* prefix_lens;  // [num_prefixes]
+  int32_t num_seqs;        // B
+  int32_t num_prefixes;
+  int32_t group;           // G = Hq / H
+  float scale_log2;
+  ScoreArgs score;
+  const float* own_acc;    // the open decode's results
+  const float* own_ml;
+  float own_shift;         // log2 of the factor that own sums and accumulators are short of
+  float* part_o;           // prefix partials: unnormalised sums ...
+  float* part_ml;          // ... and (reference maximum in log2 units, sum of weights) of each
+  // CUDA-core kernel: key ranges of split_tokens ring slots; partial [seq][chunk of the head][G]
+  int32_t split_tokens;
+  int32_t seqs_per_cta;
+  int32_t chunk_prefix[kMaxKvHeads + 1];
 };
 
 struct PrefillArgs {
@@ -194,6 +227,14 @@ int decode_tc_group_pad(int group);  // query-head columns the kernel instance h
 int decode_tc_pad_index(int group);  // 0, 1, 2 for 4, 8, 16 columns
 cudaError_t launch_decode_simt(const DecodeArgs& a, int dtype, int items, cudaStream_t st);
 cudaError_t launch_combine(const DecodeArgs& a, int dtype, cudaStream_t st);
+// open instances for a decode behind shared prefixes (hwkv_decode_open.cu; e4m3 pools hwkv_decode_open_q8.cu): results
+// to a.open_acc / open_ml; they may start before the grid ahead of them ends and end after it
+cudaError_t launch_decode_open(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, cudaStream_t st);
+cudaError_t launch_decode_open_q8(const DecodeArgs& a, const CUtensorMap* tmap, int ctas, cudaStream_t st);
+// shared prefixes (hwkv_shared.cu): partials of the prefixes' keys, CUDA cores; and the join
+int shared_simt_seqs(int group);  // sequences of one CTA
+cudaError_t launch_shared_simt(const SharedArgs& a, int dtype, int chunks, cudaStream_t st);
+cudaError_t launch_shared_join(const SharedArgs& a, bool f32, cudaStream_t st);
 // rotary positions (hwkv_rope.cu)
 cudaError_t launch_rope(RopeArgs a, int layout, bool f32, cudaStream_t st);  // sets a.rows
 // the same with keys and values stored (bf16 and fp32 pools here, e4m3 pools in hwkv_rope_q8.cu)

@@ -1,0 +1,309 @@
+// Decode behind shared prefixes: sequences whose contexts begin alike keep the common part once, in a pool of
+// prefixes, and their own tokens in their own pool.  The query of sequence s (own length n, prefix f of N tokens) attends
+// to its own window and to the prefix's positions in [max(0, N + n - w), N):
+//
+//   out = (sum_own p v + sum_prefix p v) / (sum_own p + sum_prefix p),   p = 2^(score - m)
+//
+// Three launches.  The prefixes' keys are read once for all sequences behind them, as a product of
+// (sequences x group) rows with the keys (on tcgen05: hwkv_shared_tc.cu; here: CUDA cores, for fp32 pools and
+// block sizes that no 16-row tile divides); the own parts come from the decode kernels, left open
+// (hwkv_decode_sk.cuh, kOpen); and the join below weighs the partials of both by their reference maxima.
+#include <algorithm>
+#include <type_traits>
+
+#include "hwkv_fp8.cuh"
+#include "hwkv_shared.cuh"
+
+namespace hwkv {
+namespace {
+
+constexpr int kRows = 32;     // query rows of a CTA
+constexpr int kKeys = 32;     // keys of a pass
+constexpr int kThreads = 128;  // four per row
+
+// CTA = (prefix, head, chunk of ring slots; sequences).  A pass brings 32 keys and values into shared memory; the four
+// threads of a row take eight scores each, the row's maximum and sum over them by shuffles, then a quarter
+// of head_dim each of the weighted sum.  fp32 throughout.
+template <typename T>
+struct Io {
+  using type = T;  // of queries and outputs
+};
+template <>
+struct Io<E4m3> {
+  using type = __nv_bfloat16;
+};
+
+__device__ __forceinline__ float code_value(const E4m3* p) {
+  uint32_t lo, hi;
+  e4m3x4_to_f16(p->code, lo, hi);
+  return half2_to_float2(lo).x;
+}
+
+template <typename T, int D, bool SC>
+__global__ void __launch_bounds__(kThreads) shared_simt_kernel(const __grid_constant__ SharedArgs a) {
+  using Q = typename Io<T>::type;
+  constexpr int kLd = D + 4;  // floats per row in shared memory: rows 16 bytes apart in the banks
+  extern __shared__ float4 smem4[];
+  float* s_q = reinterpret_cast<float*>(smem4);  // [kRows][kLd]
+  float* s_k = s_q + kRows * kLd;                // [kKeys][kLd]
+  float* s_v = s_k + kKeys * kLd;                // [kKeys][kLd]
+  float* s_p = s_v + kKeys * kLd;                // [kRows][kKeys + 1]
+  __shared__ int s_seq[kRows];
+  __shared__ int s_count;
+
+  const int H = a.pv.kv_heads, G = a.group, bs = a.pv.block_size;
+  const int chunks = a.chunk_prefix[H];
+  const int f = (int)blockIdx.x / chunks;
+  const int ci = (int)blockIdx.x - f * chunks;
+  int h = 0;
+  while (a.chunk_prefix[h + 1] <= ci) ++h;
+  const int c = ci - a.chunk_prefix[h];
+  const int C = (a.g.nblk_prefix[h + 1] - a.g.nblk_prefix[h]) * bs;
+  const int w = a.g.window[h];
+  const int first = (int)blockIdx.y * a.seqs_per_cta;
+  if (threadIdx.x == 0 && ci == 0 && first == 0 && a.prefix_lens[f] < 0) atomicOr(a.pv.err, HWKV_DEVERR_NEG_LENGTH);
+  if (threadIdx.x < 32) {
+    const int n = shared_members(a, f, first, a.seqs_per_cta, s_seq, threadIdx.x);
+    if (threadIdx.x == 0) s_count = n;
+  }
+  __syncthreads();
+  const int seqs = s_count;
+  if (seqs == 0) return;
+  const int rows = seqs * G;
+  const int N = prefix_len(a, f);
+
+  for (int e = threadIdx.x; e < kRows * D; e += kThreads) {
+    const int r = e / D, d = e - r * D;
+    float x = 0.f;
+    if (r < rows) x = load_in<Q>(static_cast<const Q*>(a.q) + (((int64_t)s_seq[r / G] * H + h) * G + r % G) * D + d);
+    s_q[r * kLd + d] = x;
+  }
+  const int r = threadIdx.x >> 2, part = threadIdx.x & 3;
+  const bool live = r < rows;
+  const int s = live ? s_seq[r / G] : 0;
+  const int n = live ? shared_len(a, s) : 0;
+  // a key's age, counted from the prefix's last token, that the row still sees
+  const int reach = live ? max(0, w - n) : 0;
+  const float slope = SC && live ? slope_log2(a.score, h * G + r % G) : 0.f;
+  float m = kNegInf, l = 0.f;
+  float acc[D / 4];
+#pragma unroll
+  for (int i = 0; i < D / 4; ++i) acc[i] = 0.f;
+
+  const int t_begin = c * a.split_tokens, t_end = min(C, t_begin + a.split_tokens);
+  for (int t0 = t_begin; t0 < t_end; t0 += kKeys) {
+    __syncthreads();  // the pass before has been read
+    for (int e = threadIdx.x; e < kKeys * D; e += kThreads) {
+      const int key = e / D, d = e - key * D;
+      const int t = t0 + key;
+      float kx = 0.f, vx = 0.f;
+      if (t < t_end && ring_age(N, t, C) < min(N, w)) {
+        const int j = t / bs;
+        const int32_t blk = a.pv.tbl[a.g.tbl_base + (int64_t)f * a.g.tbl_seq_stride + a.g.nblk_prefix[h] + j];
+        if (blk < 0 || (int64_t)blk >= a.pv.total_blocks) {
+          if (d == 0) atomicOr(a.pv.err, HWKV_DEVERR_BAD_BLOCK);
+        } else {
+          const T* row = static_cast<const T*>(a.pv.pool) + ((int64_t)blk * 2 * bs + (t - j * bs)) * D;
+          if constexpr (std::is_same_v<T, E4m3>) {
+            const float* scale = a.pv.scales + ((int64_t)blk * (bs / kScaleGroup) + (t - j * bs) / kScaleGroup) * 2;
+            kx = code_value(row + d) * scale[0];
+            vx = code_value(row + (int64_t)bs * D + d) * scale[1];
+          } else {
+            kx = load_in<T>(row + d);
+            vx = load_in<T>(row + (int64_t)bs * D + d);
+          }
+        }
+      }
+      s_k[key * kLd + d] = kx;
+      s_v[key * kLd + d] = vx;
+    }
+    __syncthreads();
+    float sc[kKeys / 4];
+    float top = kNegInf;
+#pragma unroll
+    for (int j = 0; j < kKeys / 4; ++j) sc[j] = 0.f;
+    for (int d = 0; d < D; d += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(s_q + r * kLd + d);
+#pragma unroll
+      for (int j = 0; j < kKeys / 4; ++j) {
+        const float4 k = *reinterpret_cast<const float4*>(s_k + (4 * j + part) * kLd + d);
+        sc[j] = fmaf(q.w, k.w, fmaf(q.z, k.z, fmaf(q.y, k.y, fmaf(q.x, k.x, sc[j]))));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kKeys / 4; ++j) {
+      const int t = t0 + 4 * j + part;
+      const int age = t < t_end ? ring_age(N, t, C) : INT32_MAX;
+      const bool seen = age < N && age < reach;
+      const float x = SC ? scored_log2<sizeof(T) == 4>(a.score, a.scale_log2, sc[j], slope, (float)((uint32_t)age + (uint32_t)n))
+                         : sc[j] * a.scale_log2;
+      sc[j] = seen ? x : kNegInf;
+      top = fmaxf(top, sc[j]);
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const float mn = fmaxf(m, top);
+    const float base = mn == kNegInf ? 0.f : mn;
+    const float al = ex2(m - base);
+    m = mn;
+    l *= al;
+#pragma unroll
+    for (int j = 0; j < kKeys / 4; ++j) {
+      const float p = ex2(sc[j] - base);
+      l += p;
+      s_p[r * (kKeys + 1) + 4 * j + part] = p;
+    }
+    __syncwarp();  // a row's four threads are of one warp
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) acc[i] *= al;
+    for (int key = 0; key < kKeys; ++key) {
+      const float p = s_p[r * (kKeys + 1) + key];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(s_v + key * kLd + 16 * i + 4 * part);
+        acc[4 * i] = fmaf(p, v.x, acc[4 * i]);
+        acc[4 * i + 1] = fmaf(p, v.y, acc[4 * i + 1]);
+        acc[4 * i + 2] = fmaf(p, v.z, acc[4 * i + 2]);
+        acc[4 * i + 3] = fmaf(p, v.w, acc[4 * i + 3]);
+      }
+    }
+  }
+  l += __shfl_xor_sync(0xffffffffu, l, 1);
+  l += __shfl_xor_sync(0xffffffffu, l, 2);
+  if (!live) return;
+  const int64_t slot = ((int64_t)s * chunks + ci) * G + r % G;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+    *reinterpret_cast<float4*>(a.part_o + slot * D + 16 * i + 4 * part) =
+        make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+  if (part == 0) reinterpret_cast<float2*>(a.part_ml)[slot] = make_float2(m, l);
+}
+
+template <int D>
+constexpr int simt_smem() {
+  return ((kRows + 2 * kKeys) * (D + 4) + kRows * (kKeys + 1)) * 4;
+}
+
+// One warp per (sequence, query head): out = sum_i acc_i 2^(m_i - M) / sum_i l_i 2^(m_i - M) over its own
+// partial and its prefix's, M = max_i m_i, in that order; nothing to attend to gives zeros.  kAhead
+// partials' loads in flight.
+constexpr int kJoinWarps = 4;
+constexpr int kAhead = 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const __grid_constant__ SharedArgs a) {
+  constexpr int kC = D / 32;  // columns per lane
+  griddep_wait();
+  const int H = a.pv.kv_heads, G = a.group, Hq = H * G;
+  const int64_t row = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= (int64_t)a.num_seqs * Hq) return;
+  const int s = (int)(row / Hq), qh = (int)(row - (int64_t)s * Hq), h = qh / G, g = qh - h * G;
+  const int f = prefix_of(a, s, lane == 0 && qh == 0);
+  int64_t slot0 = 0, step = 0;
+  int count = 0;
+  if (f >= 0) {
+    const int chunks = a.chunk_prefix[H];
+    slot0 = ((int64_t)s * chunks + a.chunk_prefix[h]) * G + g;
+    step = G;
+    count = a.chunk_prefix[h + 1] - a.chunk_prefix[h];
+  }
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+  float2 own = reinterpret_cast<const float2*>(a.own_ml)[row];
+  own.x += a.own_shift;
+  float M = own.x;
+  for (int i = lane; i < count; i += 32) M = fmaxf(M, ml[slot0 + i * step].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.f, acc[kC];
+#pragma unroll
+  for (int c = 0; c < kC; ++c) acc[c] = 0.f;
+  auto add = [&](float2 e, const float (&v)[kC]) {
+    const float x = ex2(e.x - M);
+    L = fmaf(e.y, x, L);
+#pragma unroll
+    for (int c = 0; c < kC; ++c) acc[c] = fmaf(v[c], x, acc[c]);
+  };
+  auto load = [&](const float* p, float (&v)[kC]) {
+    if constexpr (kC == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p + lane * kC);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(p + lane * kC);
+      v[0] = x.x, v[1] = x.y;
+    }
+  };
+  if (own.x != kNegInf) {
+    float v[kC];
+    load(a.own_acc + row * D, v);
+    add(own, v);
+  }
+  for (int i0 = 0; i0 < count; i0 += kAhead) {
+    float v[kAhead][kC];
+    float2 e[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      e[j] = i0 + j < count ? ml[slot0 + (i0 + j) * step] : make_float2(kNegInf, 0.f);
+      if (e[j].x != kNegInf) load(a.part_o + (slot0 + (i0 + j) * step) * D, v[j]);  // an empty partial's sums are not written
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (e[j].x != kNegInf) add(e[j], v[j]);
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  T* out = static_cast<T*>(a.out) + row * D + lane * kC;
+#pragma unroll
+  for (int c = 0; c < kC; ++c) store_out<T>(out + c, acc[c] * inv);
+}
+
+template <typename T, int D, bool SC>
+cudaError_t launch_simt(const SharedArgs& a, dim3 grid, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(shared_simt_kernel<T, D, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, simt_smem<D>());
+  if (e != cudaSuccess) return e;
+  shared_simt_kernel<T, D, SC><<<grid, kThreads, simt_smem<D>(), st>>>(a);
+  return cudaSuccess;
+}
+
+template <typename T, int D>
+cudaError_t launch_simt(const SharedArgs& a, dim3 grid, cudaStream_t st) {
+  return a.score.on ? launch_simt<T, D, true>(a, grid, st) : launch_simt<T, D, false>(a, grid, st);
+}
+
+template <typename T, int D>
+cudaError_t launch_join(const SharedArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((int64_t)a.num_seqs * a.pv.kv_heads * a.group + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_join_kernel<T, D>, a);
+}
+
+}  // namespace
+
+int shared_simt_seqs(int group) { return std::max(1, kRows / group); }
+
+cudaError_t launch_shared_simt(const SharedArgs& a, int dtype, int chunks, cudaStream_t st) {
+  const dim3 grid((unsigned)(a.num_prefixes * (int64_t)chunks), (unsigned)((a.num_seqs + a.seqs_per_cta - 1) / a.seqs_per_cta));
+  const int D = a.pv.head_dim;
+  cudaError_t e = cudaErrorInvalidValue;
+  if (dtype == HWKV_F32) e = D == 128 ? launch_simt<float, 128>(a, grid, st) : launch_simt<float, 64>(a, grid, st);
+  else if (dtype == HWKV_BF16) e = D == 128 ? launch_simt<__nv_bfloat16, 128>(a, grid, st) : launch_simt<__nv_bfloat16, 64>(a, grid, st);
+  else if (dtype == HWKV_E4M3) e = D == 128 ? launch_simt<E4m3, 128>(a, grid, st) : launch_simt<E4m3, 64>(a, grid, st);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_shared_join(const SharedArgs& a, bool f32, cudaStream_t st) {
+  const bool wide = a.pv.head_dim == 128;
+  const cudaError_t e = f32 ? (wide ? launch_join<float, 128>(a, st) : launch_join<float, 64>(a, st))
+                            : (wide ? launch_join<__nv_bfloat16, 128>(a, st) : launch_join<__nv_bfloat16, 64>(a, st));
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace hwkv

@@ -88,6 +88,7 @@ extern "C" {
 #define HWKV_DEVERR_BAD_BLOCK 2      /* a block-table entry outside the pool            */
 #define HWKV_DEVERR_SRC_RANGE 4      /* materialise length above max_len               */
 #define HWKV_DEVERR_WAIT_TIMEOUT 8   /* a pipeline wait gave up (work was skipped)      */
+#define HWKV_DEVERR_BAD_PREFIX 16    /* a sequence's prefix that the prefix pool does not hold */
 
 typedef struct hwkv_pool* hwkv_pool_t;
 
@@ -267,6 +268,35 @@ typedef struct hwkv_score {
 int hwkv_decode_attn_score(hwkv_pool_t pool, int layer, const void* q, int q_heads, const hwkv_score_t* score,
                            const void* k_new, const void* v_new, const int32_t* lens_dev, void* out, void* workspace,
                            uint64_t workspace_bytes, int flags, void* stream);
+
+/* Decode behind shared prefixes: sequences whose contexts begin with the same tokens keep those once, in a
+ * pool of prefixes (its sequences), and only what follows in their own pool, at positions counted from 0
+ * behind the prefix.  For query head q of sequence s with own length L (after the append), behind prefix f of N tokens,
+ * with w' the own pool's and w the prefix pool's window of the head:
+ *     out[s][q] = softmax over the own positions [max(0, L - w'), L) and the prefix's [max(0, N + L - w), N),
+ * so that own windows w' >= min(w, the longest own part) give the last w tokens of the whole context.  Each
+ * prefix's keys are read once for all the sequences behind it.
+ *   prefix: a pool of the same layers, kv_heads and head_dim, whose tensors have the same type (an 8-bit pool goes with a
+ *   bf16 or an 8-bit one); blocks and windows may differ.  Its sequences hold the prefixes, stored by any call.
+ *   prefix_of_dev: device int32 [num_seqs], the prefix of each sequence, negative for none; one past the
+ *   prefix pool's sequences flags HWKV_DEVERR_BAD_PREFIX and counts as none.  prefix_lens_dev: device int32
+ *   [prefix num_seqs], tokens of each prefix (negative: HWKV_DEVERR_NEG_LENGTH, counts as 0).  What is flagged is
+ *   recorded in `pool`.
+ *   k_new, v_new (both or neither): appended to the own pool first, lens_dev then holding the own lengths before the
+ *   append, as in hwkv_decode_attn_ex.  score: as hwkv_decode_attn_score (a prefix key's distance counts the
+ *   tokens of both pools); nothing to attend to gives zeros.
+ *   workspace: hwkv_decode_shared_workspace_bytes() bytes, otherwise as for hwkv_decode_attn.
+ * Three kernels on `stream` or more: the prefixes' keys, the own parts, their join.  Concurrent launches of the same
+ * layer of `pool` race, decode calls included; `prefix` may be shared by any number of launches that only read it.
+ * A group of up to 16 query heads per KV head, as in every decode.
+ * Errors: as hwkv_decode_attn; HWKV_ERR_INVALID_ARG also for pools that do not go together. */
+int hwkv_decode_attn_shared(hwkv_pool_t pool, hwkv_pool_t prefix, int layer, const void* q, int q_heads,
+                            const hwkv_score_t* score, const void* k_new, const void* v_new, const int32_t* lens_dev,
+                            const int32_t* prefix_of_dev, const int32_t* prefix_lens_dev, void* out, void* workspace,
+                            uint64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace hwkv_decode_attn_shared needs, the most over the layers (host only). */
+int hwkv_decode_shared_workspace_bytes(hwkv_pool_t pool, hwkv_pool_t prefix, int q_heads, uint64_t* out);
 
 /* Bytes of the static scratch array behind hwkv_decode_attn_noalloc. */
 #define HWKV_NOALLOC_SCRATCH_BYTES (4u << 20)

@@ -1183,6 +1183,9 @@ int decode_common(hwkv_pool_t p, int layer, const void* q, int q_heads, hwkv_sco
   return rc != HWKV_OK ? rc : ok();
 }
 
+// Which kernel reads the prefixes' keys: the tensor cores' where its tiles fit.
+bool shared_tc(const hwkv_pool* prefix) { return prefill_eligible(prefix); }
+
 // How the keys of the prefixes are split on the CUDA cores: ring slots per CTA for about six CTAs per SM over
 // the sequences' tiles, and the chunks of each head.
 struct SharedPlan {
@@ -1207,22 +1210,34 @@ SharedPlan plan_shared(const hwkv_pool* p, const hwkv_pool* prefix, int layer, i
   return s;
 }
 
-// Regions of the workspace: the own decode's, its open results, the prefixes' partials.
+// Regions of the workspace: the own decode's, its open results, the prefixes' partials and their records.
 struct SharedLayout {
-  uint64_t own_acc = 0, own_ml = 0, part_o = 0, part_ml = 0, total = 0;
+  int chain_rows = 0;  // tensor cores: rows of a chain's partial
+  uint64_t own_acc = 0, own_ml = 0, part_o = 0, part_ml = 0, rec = 0, total = 0;
 };
 
 SharedLayout shared_layout(const hwkv_pool* p, const hwkv_pool* prefix, int group) {
   SharedLayout w;
-  const uint64_t rows = (uint64_t)p->g.num_seqs * p->g.kv_heads * group, D = (uint64_t)p->g.head_dim;
-  uint64_t chunks = 0;
-  for (int l = 0; l < p->g.layers; ++l) chunks = std::max<uint64_t>(chunks, plan_shared(p, prefix, l, group).chunks);
-  const uint64_t parts = (uint64_t)p->g.num_seqs * chunks * group;
+  const uint64_t B = (uint64_t)p->g.num_seqs, H = (uint64_t)p->g.kv_heads, D = (uint64_t)p->g.head_dim;
+  const uint64_t rows = B * H * group;
+  uint64_t parts = 0;
+  const bool tc = shared_tc(prefix);
+  if (tc) {
+    // a slot per (item, CTA) along the line: at most items + CTAs of them, two chains each
+    const uint64_t QT = (uint64_t)shared_tc_seqs(group);
+    const uint64_t items = H * (std::min<uint64_t>((uint64_t)prefix->g.num_seqs, B) + B / (2 * QT));
+    w.chain_rows = (int)(std::min<uint64_t>(QT, B) * group);
+    parts = (items + (uint64_t)p->num_sms) * 2 * (uint64_t)w.chain_rows;
+  } else {
+    for (int l = 0; l < p->g.layers; ++l) parts = std::max<uint64_t>(parts, plan_shared(p, prefix, l, group).chunks);
+    parts *= B * (uint64_t)group;
+  }
   w.own_acc = align256(workspace_bytes(p, group));
   w.own_ml = align256(w.own_acc + rows * D * 4);
   w.part_o = align256(w.own_ml + rows * 8);
   w.part_ml = align256(w.part_o + parts * D * 4);
-  w.total = align256(w.part_ml + parts * 8);
+  w.rec = align256(w.part_ml + parts * 8);
+  w.total = align256(w.rec + (tc ? B * H * sizeof(int4) : 0));
   return w;
 }
 
@@ -1236,6 +1251,7 @@ int check_shared(const hwkv_pool* p, const hwkv_pool* prefix, int q_heads) {
   if (q_heads < g.kv_heads || q_heads % g.kv_heads != 0 || q_heads / g.kv_heads > kMaxGroup)
     return fail(HWKV_ERR_UNSUPPORTED, "q_heads must be G * kv_heads with 1 <= G <= %d (got %d)", kMaxGroup, q_heads);
   if (g.num_seqs > 65535) return fail(HWKV_ERR_UNSUPPORTED, "at most 65535 sequences behind prefixes (got %d)", g.num_seqs);
+  if (f.num_seqs > kMaxPrefixes) return fail(HWKV_ERR_UNSUPPORTED, "at most %d prefixes (got %d)", kMaxPrefixes, f.num_seqs);
   return HWKV_OK;
 }
 
@@ -1318,13 +1334,22 @@ int hwkv_decode_attn_shared(hwkv_pool_t p, hwkv_pool_t prefix, int layer, const 
   a.own_shift = p->g.dtype == HWKV_E4M3 ? kQ8Shift : 0.f;
   a.part_o = reinterpret_cast<float*>(ws + wl.part_o);
   a.part_ml = reinterpret_cast<float*>(ws + wl.part_ml);
-  const SharedPlan sp = plan_shared(p, prefix, layer, G);
-  a.split_tokens = sp.split;
-  a.seqs_per_cta = shared_simt_seqs(G);
-  std::memcpy(a.chunk_prefix, sp.chunk_prefix, sizeof a.chunk_prefix);
+  a.rec = reinterpret_cast<int4*>(ws + wl.rec);
+  a.chain_rows = wl.chain_rows;
   NvtxRange range_("hwkv_decode_attn_shared", layer);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  HWKV_CUDA_TRY(launch_shared_simt(a, prefix->g.dtype, sp.chunks, st), "shared prefix launch");
+  if (shared_tc(prefix)) {
+    a.tc = 1;
+    a.bs_log2 = log2_of(prefix->g.block_size);
+    a.stage_tb = prefix->stage_tb;
+    HWKV_CUDA_TRY(launch_shared_tc(a, &prefix->tmap, &prefix->stage_map, p->num_sms, st), "shared prefix launch");
+  } else {
+    const SharedPlan sp = plan_shared(p, prefix, layer, G);
+    a.split_tokens = sp.split;
+    a.seqs_per_cta = shared_simt_seqs(G);
+    std::memcpy(a.chunk_prefix, sp.chunk_prefix, sizeof a.chunk_prefix);
+    HWKV_CUDA_TRY(launch_shared_simt(a, prefix->g.dtype, sp.chunks, st), "shared prefix launch");
+  }
   rc = launch_decode(p, layer, call, st);
   if (rc != HWKV_OK) return rc;
   HWKV_CUDA_TRY(launch_shared_join(a, p->g.dtype == HWKV_F32, st), "shared join launch");

@@ -133,6 +133,13 @@ struct SharedArgs {
   int32_t split_tokens;
   int32_t seqs_per_cta;
   int32_t chunk_prefix[kMaxKvHeads + 1];
+  // tensor cores: partials of (item, CTA) slots x two chains x rows, found by a record per (seq, KV head):
+  // (first chain of a slot, step, number, first row)
+  int32_t tc;              // 1: that kernel's partials
+  int32_t bs_log2;         // log2(block_size), or -1 when it is not a power of two
+  int32_t stage_tb;        // rows of one block in a 64-key pool copy (16, 32, 64), 0: per-tile copies only
+  int32_t chain_rows;      // rows of a chain's partial
+  int4* rec;
 };
 
 struct PrefillArgs {
@@ -234,6 +241,10 @@ cudaError_t launch_decode_open_q8(const DecodeArgs& a, const CUtensorMap* tmap, 
 // shared prefixes (hwkv_shared.cu): partials of the prefixes' keys, CUDA cores; and the join
 int shared_simt_seqs(int group);  // sequences of one CTA
 cudaError_t launch_shared_simt(const SharedArgs& a, int dtype, int chunks, cudaStream_t st);
+// the same on the tensor cores (hwkv_shared_tc.cu), bf16 pools
+constexpr int kMaxPrefixes = 2048;
+int shared_tc_seqs(int group);  // sequences of a query tile
+cudaError_t launch_shared_tc(const SharedArgs& a, const CUtensorMap* pool_map, const CUtensorMap* stage_map, int ctas, cudaStream_t st);
 cudaError_t launch_shared_join(const SharedArgs& a, bool f32, cudaStream_t st);
 // rotary positions (hwkv_rope.cu)
 cudaError_t launch_rope(RopeArgs a, int layout, bool f32, cudaStream_t st);  // sets a.rows

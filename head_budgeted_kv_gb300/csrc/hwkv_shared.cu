@@ -200,9 +200,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const __gr
   if (row >= (int64_t)a.num_seqs * Hq) return;
   const int s = (int)(row / Hq), qh = (int)(row - (int64_t)s * Hq), h = qh / G, g = qh - h * G;
   const int f = prefix_of(a, s, lane == 0 && qh == 0);
-  int64_t slot0 = 0, step = 0;
+  int64_t slot0 = 0, step = 0;  // rows of partials
   int count = 0;
-  if (f >= 0) {
+  if (f >= 0 && a.tc) {
+    // a record is there for every row that sees a key of the prefix
+    if (min(prefix_len(a, f), a.g.window[h] - min(a.g.window[h], shared_len(a, s))) > 0) {
+      const int4 rec = a.rec[(int64_t)s * H + h];
+      slot0 = (int64_t)rec.x * a.chain_rows + rec.w + g;
+      step = (int64_t)rec.y * a.chain_rows;
+      count = rec.z;
+    }
+  } else if (f >= 0) {
     const int chunks = a.chunk_prefix[H];
     slot0 = ((int64_t)s * chunks + a.chunk_prefix[h]) * G + g;
     step = G;

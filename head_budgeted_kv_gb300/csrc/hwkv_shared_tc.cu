@@ -1,0 +1,726 @@
+// The prefixes' keys of a decode behind shared prefixes (hwkv_shared.cu) on the sm_100-family tensor cores
+// (tcgen05, accumulators in tensor memory), for bf16 pools whose blocks are whole 16-row tiles.
+//
+// The queries of all sequences behind a prefix are rows of one product with its keys: with r rows a key's
+// 4 D bytes serve 4 r D operations, so up to ~290 rows the keys' bytes bound the call and beyond that the
+// products do.  A query tile holds floor(128 / G) sequences x G heads.
+//
+//   item  = (prefix, KV head, up to two query tiles): a stream of 64-key stages, the ring tiles of the
+//           positions that the sequence with the shortest own part still sees;
+//   line  = all items' stages in a row.  The persistent grid (a CTA per SM) splits it evenly; a CTA walks its range item by
+//           item (segments) and leaves a partial (reference maximum, sum, unnormalised sums) per row and segment.
+//
+// Two query tiles of an item share every stage (each key is staged once for 256 rows).  An item of one tile gives its stages in
+// turn to two chains of the same rows, so the S -> softmax -> P.V latency of one hides behind the other's;
+// they leave two partials.
+//
+// Warp roles: 0 TMA producer; 1 issues S = Q K^T, 2 issues O += P V; 3 plans: segments, their sequences, and the
+// records the join reads; 4-7 softmax of tile (or chain) 0, 8-11 of 1, a thread per row.  Warps without a live row only keep
+// the barriers in step.  Segments are handed out through two descriptors in shared memory, so the
+// producer runs into the next one while the last is finished.
+//
+// Weights are rounded to bf16 for P V (2^-8 of each, half a step); their sum is of the unrounded ones.
+// Waits are bounded (~2 s) and record HWKV_DEVERR_WAIT_TIMEOUT; then all roles stop.
+#include <algorithm>
+
+#include "hwkv_decode_tile.cuh"
+#include "hwkv_shared.cuh"
+#include "hwkv_tcgen05.cuh"
+
+namespace hwkv {
+namespace {
+
+constexpr int kM = 128;                 // query rows per tile (MMA M)
+constexpr int kKeys = 64;               // keys per stage
+constexpr int kSub = kKeys / kTile;     // ring tiles per stage
+constexpr int kThreads = 12 * 32;
+constexpr int kMinStages = 4;           // fewest stages of a CTA
+constexpr int kRoleWarps = 11;          // warps that read a segment's descriptor
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kQBytes = kM * D * 2;
+  static constexpr int kKBytes = kKeys * D * 2;
+  static constexpr int kStageBytes = 2 * kKBytes;
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kStageOff = 2 * kQBytes;
+  static constexpr int kHistOff = kStageOff + kStages * kStageBytes;  // sequences and shortest own part of each prefix
+  static constexpr uint32_t kCols = 512;
+  static constexpr uint32_t kColO = 4 * kKeys;
+  static int smem(int prefixes) { return kHistOff + 8 * prefixes + 1024; }
+};
+
+// A CTA's part of one item.
+struct Segment {
+  int f, h;
+  int N;           // tokens of the prefix
+  int w, C;        // window and ring capacity
+  int first_tile;  // ring tile of the item's first stage
+  int tiles;       // ring tiles of the item
+  int j0, stages;  // this CTA's stages of it, 0: no more segments
+  int seqs;        // sequences
+  int one;         // a single query tile: its stages alternate between two chains
+  int slot;        // where the partials go
+};
+
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// Waits for a phase; gives up when another role has (`abort`) or after ~2 s, which it records and announces.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*abort) return false;
+      if (global_timer_ns() - t0 > 2000000000ull) {
+        *abort = 1;
+        atomicOr(err, HWKV_DEVERR_WAIT_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+// bits lo .. hi (inclusive, clamped to 0 .. 15) of a 16-key tile
+__device__ __forceinline__ uint32_t bits16(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 15);
+  return lo > hi ? 0u : ((0xFFFFu >> (15 - hi)) & (0xFFFFu << lo));
+}
+
+// 64 values folded by a tree of three-input operations, not a dependent chain
+template <typename Op>
+__device__ __forceinline__ float fold64(const float (&v)[kKeys], Op op) {
+  float t1[22], t2[8];
+#pragma unroll
+  for (int i = 0; i < 21; ++i) t1[i] = op(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
+  t1[21] = v[63];
+#pragma unroll
+  for (int i = 0; i < 7; ++i) t2[i] = op(t1[3 * i], t1[3 * i + 1], t1[3 * i + 2]);
+  t2[7] = t1[21];
+  return op(op(t2[0], t2[1], t2[2]), op(t2[3], t2[4], t2[5]), op(t2[6], t2[7], t2[7]));
+}
+
+// The ring tiles of the newest `need` of N tokens: first tile and their number.
+__device__ __forceinline__ void need_tiles(int N, int need, int C, int& first_tile, int& tiles) {
+  first_tile = tiles = 0;
+  if (need <= 0) return;
+  const int first = (N - need) % C;
+  first_tile = first >> 4;
+  tiles = min(C >> 4, (int)(((uint32_t)first + (uint32_t)need - 1u) >> 4) - first_tile + 1);
+}
+
+// age of a ring tile's first slot: its slots' ages fall by one from it, past 0 they go on at C - 1
+__device__ __forceinline__ int tile_age(const Segment& sg, int last, int i) {
+  int t = sg.first_tile + i;
+  if (t >= sg.C >> 4) t -= sg.C >> 4;
+  const int d = last - (t << 4);
+  return d < 0 ? d + sg.C : d;
+}
+
+template <int D, bool SC>
+__global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ CUtensorMap pool_map,
+                                                               const __grid_constant__ CUtensorMap stage_map,
+                                                               const __grid_constant__ SharedArgs a) {
+  using K = Cfg<D>;
+  constexpr int NS = K::kStages;
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  int* s_count = reinterpret_cast<int*>(smem + K::kHistOff);
+  int* s_short = s_count + a.num_prefixes;
+  __shared__ __align__(8) uint64_t kv_full[NS], kv_empty[NS];
+  // per chain x and parity b of its stages (a phase is one stage of that parity, so no waiter falls two behind)
+  __shared__ __align__(8) uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2], drain[2];
+  __shared__ __align__(8) uint64_t seg_full[2], seg_empty[2];
+  __shared__ Segment s_seg[2];
+  __shared__ int s_seq[2][2 * kM];
+  __shared__ int4 s_copy[32];  // copy plan of the producer's next 32 stages: pool rows of the four tiles
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ long long s_scan[kThreads / 32];
+  __shared__ long long s_pre[2];
+  __shared__ int s_entry;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int H = a.pv.kv_heads, G = a.group, bs = a.pv.block_size;
+  const int QT = kM / G;  // sequences per query tile
+  const int cta = blockIdx.x;
+  griddep_wait();
+  griddep_launch_dependents();  // the own parts may start where SMs are free: all before this grid has completed
+
+  // ---- sequences and shortest own part of each prefix ---------------------------------------
+  for (int f = threadIdx.x; f < a.num_prefixes; f += kThreads) {
+    s_count[f] = 0;
+    s_short[f] = INT32_MAX;
+    if (cta == 0 && a.prefix_lens[f] < 0) atomicOr(a.pv.err, HWKV_DEVERR_NEG_LENGTH);
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&s_full[x][b], 1);
+        mbar_init(&p_full[x][b], 4);
+        mbar_init(&o_done[x][b], 1);
+      }
+      mbar_init(&q_full[x], 4);
+      mbar_init(&drain[x], 1);
+      mbar_init(&seg_full[x], 1);
+      mbar_init(&seg_empty[x], kRoleWarps);
+    }
+    s_abort = 0;
+    s_entry = -1;
+    fence_mbar_init();
+    prefetch_tensormap(&pool_map);
+    prefetch_tensormap(&stage_map);
+  }
+  __syncthreads();
+  for (int s = threadIdx.x; s < a.num_seqs; s += kThreads) {
+    const int f = prefix_of(a, s, cta == 0);
+    if (f < 0) continue;
+    atomicAdd(&s_count[f], 1);
+    atomicMin(&s_short[f], shared_len(a, s));
+  }
+  __syncthreads();
+
+  // ---- the line: entries (prefix, head) of tiles x stages -----------------------------------
+  struct Entry {
+    int f, h, N, w, C, first_tile, tiles, stages, items;
+  };
+  auto entry_of = [&](int e) {
+    Entry n;
+    n.f = e / H;
+    n.h = e - n.f * H;
+    n.N = prefix_len(a, n.f);
+    n.w = a.g.window[n.h];
+    n.C = (a.g.nblk_prefix[n.h + 1] - a.g.nblk_prefix[n.h]) * bs;
+    n.items = (s_count[n.f] + 2 * QT - 1) / (2 * QT);
+    const int need = n.items > 0 ? min(n.N, n.w - min(n.w, s_short[n.f])) : 0;
+    need_tiles(n.N, need, n.C, n.first_tile, n.tiles);
+    n.stages = (n.tiles + kSub - 1) / kSub;
+    return n;
+  };
+  const int entries = a.num_prefixes * H;
+  const int per = (entries + kThreads - 1) / kThreads;
+  const int e_lo = min(entries, (int)threadIdx.x * per), e_hi = min(entries, e_lo + per);
+  long long mine = 0, mine_items = 0;
+  for (int e = e_lo; e < e_hi; ++e) {
+    const Entry n = entry_of(e);
+    mine += (long long)n.items * n.stages;
+    mine_items += n.items;
+  }
+  long long T, all_items;
+  const long long excl = block_exclusive_scan<kThreads / 32>(mine, s_scan, T);
+  const long long excl_items = block_exclusive_scan<kThreads / 32>(mine_items, s_scan, all_items);
+  const int ctas = (int)max(1ll, min((long long)gridDim.x, T / kMinStages));
+  if (cta >= ctas || T == 0) return;
+  const long long t_lo = range_start(T, cta, ctas), t_hi = range_start(T, cta + 1, ctas);
+  if (excl <= t_lo && t_lo < excl + mine) {
+    long long pre = excl, items = excl_items;
+    for (int e = e_lo; e < e_hi; ++e) {
+      const Entry n = entry_of(e);
+      const long long span = (long long)n.items * n.stages;
+      if (t_lo < pre + span) {
+        s_entry = e;
+        s_pre[0] = pre;
+        s_pre[1] = items;
+        break;
+      }
+      pre += span;
+      items += n.items;
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(&s_tmem, K::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  const uint32_t sbase = smem_addr(smem);
+  volatile int* abort = &s_abort;
+
+  // Segment i as the roles see it; false: no more, or a wait was given up.
+  auto next_segment = [&](int i, Segment& sg) {
+    if (!__all_sync(0xffffffffu, wait(&seg_full[i & 1], (uint32_t)(i >> 1) & 1u, abort, a.pv.err))) return false;
+    sg = s_seg[i & 1];
+    return sg.stages > 0;
+  };
+  // A role's warp is through with segment i's descriptor and sequences.
+  auto done_segment = [&](int i) {
+    __syncwarp();
+    if (lane == 0) arrive(&seg_empty[i & 1]);
+  };
+
+  if (warp == 3) {
+    // ---- planner ------------------------------------------------------------------------
+    int e = s_entry;
+    long long pre = s_pre[0], items = s_pre[1];
+    Entry n = entry_of(e);
+    long long at = t_lo;
+    for (int i = 0;; ++i) {
+      if (i >= 2 && !__all_sync(0xffffffffu, wait(&seg_empty[i & 1], (uint32_t)((i >> 1) - 1) & 1u, abort, a.pv.err))) break;
+      if (at >= t_hi) {
+        if (lane == 0) {
+          s_seg[i & 1].stages = 0;
+          arrive(&seg_full[i & 1]);
+        }
+        break;
+      }
+      while (at >= pre + (long long)n.items * n.stages) {
+        pre += (long long)n.items * n.stages;
+        items += n.items;
+        n = entry_of(++e);
+      }
+      const int off = (int)((at - pre) / n.stages);  // the entry's item
+      const long long begin = pre + (long long)off * n.stages, end = begin + n.stages;
+      Segment sg;
+      sg.f = n.f, sg.h = n.h, sg.N = n.N, sg.w = n.w, sg.C = n.C, sg.first_tile = n.first_tile, sg.tiles = n.tiles;
+      sg.j0 = (int)(at - begin);
+      sg.stages = (int)(min(end, t_hi) - at);
+      sg.seqs = shared_members(a, n.f, off * 2 * QT, 2 * QT, s_seq[i & 1], lane);
+      sg.one = sg.seqs <= QT;
+      sg.slot = (int)(items + off) + cta;  // unique along the line: each step of it moves on the item or the CTA
+      if (lane == 0) {
+        s_seg[i & 1] = sg;
+        __threadfence_block();
+        arrive(&seg_full[i & 1]);
+      }
+      if (sg.j0 == 0) {  // the item's records: its partials lie one slot per CTA
+        const int parts = cta_of(end - 1, T, ctas) - cta + 1;
+        for (int k = lane; k < sg.seqs; k += 32) {
+          const int x = sg.one ? 0 : k / QT;
+          a.rec[(int64_t)s_seq[i & 1][k] * H + n.h] =
+              make_int4(2 * sg.slot + x, sg.one ? 1 : 2, sg.one ? 2 * parts : parts, (k - x * QT) * G);
+        }
+      }
+      at += sg.stages;
+      __syncwarp();
+    }
+  } else if (warp == 0) {
+    // ---- TMA producer (whole warp) ------------------------------------------------------
+    int issued = 0;
+    bool ok = true;
+    Segment sg;
+    for (int i = 0; ok && next_segment(i, sg); ++i) {
+      const int32_t* tbl = a.pv.tbl + a.g.tbl_base + (int64_t)sg.f * a.g.tbl_seq_stride + a.g.nblk_prefix[sg.h];
+      const int C16 = sg.C >> 4;
+      // 32 stages planned at a time, one per lane (table look-ups in parallel); lane 0 issues the copies
+      for (int c0 = 0; ok && c0 < sg.stages; c0 += 32) {
+        if (c0 + lane < sg.stages) {
+          int row[kSub];
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+            const int k = (sg.j0 + c0 + lane) * kSub + u;
+            row[u] = 0;  // past the item: row 0 of the pool, masked
+            if (k < sg.tiles) {
+              int t = sg.first_tile + k;
+              if (t >= C16) t -= C16;
+              const int t0 = t << 4;
+              const int jb = a.bs_log2 >= 0 ? t0 >> a.bs_log2 : t0 / bs;
+              const int32_t blk = __ldg(tbl + jb);
+              if (blk < 0 || (int64_t)blk >= a.pv.total_blocks) atomicOr(a.pv.err, HWKV_DEVERR_BAD_BLOCK);
+              else row[u] = blk * 2 * bs + (t0 - jb * bs);
+            }
+          }
+          s_copy[lane] = make_int4(row[0], row[1], row[2], row[3]);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          for (int l = 0; l < 32 && c0 + l < sg.stages; ++l, ++issued) {
+            const int st = issued % NS;
+            if (issued >= NS && !wait(&kv_empty[st], (uint32_t)(issued / NS - 1) & 1u, abort, a.pv.err)) {
+              ok = false;
+              break;
+            }
+            const int4 c = s_copy[l];
+            const int row[kSub] = {c.x, c.y, c.z, c.w};
+            const uint32_t kdst = sbase + K::kStageOff + st * K::kStageBytes, vdst = kdst + K::kKBytes;
+            mbar_arrive_expect_tx(&kv_full[st], K::kStageBytes);
+            // 64 keys that one box of the stage map covers: stage_tb rows of each of consecutive blocks
+            const int tb = a.stage_tb;
+            const int blk = row[0] / (2 * bs), r0 = row[0] - blk * 2 * bs;
+            bool box = tb > 0 && r0 + tb <= bs && (sg.j0 + c0 + l) * kSub + kSub <= sg.tiles;
+#pragma unroll
+            for (int u = 1; u < kSub; ++u)
+              box = box && row[u] == row[0] + (kTile * u) / max(tb, 1) * 2 * bs + ((kTile * u) & (tb - 1));
+            if (box) {
+#pragma unroll
+              for (int hf = 0; hf < K::kHalves; ++hf) {
+                tma_3d(kdst + hf * (kKeys * 128), &stage_map, hf * 64, r0, blk, &kv_full[st]);
+                tma_3d(vdst + hf * (kKeys * 128), &stage_map, hf * 64, bs + r0, blk, &kv_full[st]);
+              }
+            } else {
+#pragma unroll
+              for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int hf = 0; hf < K::kHalves; ++hf) {
+                  const uint32_t at = hf * (kKeys * 128) + u * (kTile * 128);
+                  tma_2d(kdst + at, &pool_map, hf * 64, row[u], &kv_full[st]);
+                  tma_2d(vdst + at, &pool_map, hf * 64, row[u] + bs, &kv_full[st]);
+                }
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        __syncwarp();
+      }
+      done_segment(i);
+    }
+    if (lane == 0 && *abort) {  // let the copies in flight land before the shared memory is released
+      for (int j = max(0, issued - NS); j < issued; ++j)
+        if (!mbar_wait_bounded(&kv_full[j % NS], (uint32_t)(j / NS) & 1u)) break;
+    }
+    __syncwarp();
+  } else if (warp == 1 || warp == 2) {
+    // ---- MMA issuers: warp 1 the S of every stage, warp 2 the P . V ---------------------------
+    constexpr uint32_t idS = umma_idesc_bf16(kM, kKeys, false, false);
+    constexpr uint32_t idO = umma_idesc_bf16(kM, D, false, true);
+    const uint64_t dq = umma_desc_sw128(sbase, 16, 1024);
+    const uint64_t dk = umma_desc_sw128(sbase + K::kStageOff, 16, 1024);
+    const uint64_t dv = umma_desc_sw128(sbase + K::kStageOff + K::kKBytes, kKeys * 128, 1024);
+    int stage = 0;          // stages of this CTA so far
+    int done0 = 0, done1 = 0, qs0 = 0, qs1 = 0;  // stages of each chain, segments of each chain
+    bool ok = true;
+    Segment sg;
+    for (int i = 0; ok && next_segment(i, sg); ++i) {
+      if (lane == 0) {
+        for (int jj = 0; ok && jj < sg.stages; ++jj, ++stage) {
+          const int st = stage % NS;
+          if (warp == 1) {
+            ok = wait(&kv_full[st], (uint32_t)(stage / NS) & 1u, abort, a.pv.err);
+            if (!ok) break;
+            tc_fence_after_sync();
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (sg.one && (jj & 1) != x) continue;
+            int& done = x ? done1 : done0;
+            const int b = done & 1;
+            const bool first = sg.one ? jj < 2 : jj == 0;  // the chain's first stage of the segment
+            if (warp == 1) {
+              // S of this stage into buffer b, once the P . V of the chain's stage two before, which read the P there,
+              // has completed
+              if (first) {
+                int& qs = x ? qs1 : qs0;
+                ok = wait(&q_full[x], (uint32_t)qs & 1u, abort, a.pv.err);
+                ++qs;
+                if (!ok) break;
+                tc_fence_after_sync();
+              }
+              if (done >= 2) {
+                ok = wait(&o_done[x][b], (uint32_t)((done - 2) >> 1) & 1u, abort, a.pv.err);
+                if (!ok) break;
+                tc_fence_after_sync();
+              }
+              const uint64_t dks = dk + (uint64_t)((st * K::kStageBytes) >> 4);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                umma_bf16(tmem + (2 * x + b) * kKeys, dq + (uint64_t)((x * K::kQBytes + (k >> 2) * (kM * 128) + (k & 3) * 32) >> 4),
+                          dks + (uint64_t)(((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4), idS, k > 0 ? 1u : 0u);
+              umma_commit(&s_full[x][b]);
+            } else {
+              // O += P . V once the softmax has written P into tensor memory
+              ok = wait(&p_full[x][b], (uint32_t)(done >> 1) & 1u, abort, a.pv.err);
+              if (!ok) break;
+              tc_fence_after_sync();
+              const uint64_t dvs = dv + (uint64_t)((st * K::kStageBytes) >> 4);
+              const uint32_t pcol = tmem + (2 * x + b) * kKeys;
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                umma_bf16_tmem_a(tmem + K::kColO + x * D, pcol + k * 8, dvs + (uint64_t)((k * 16 * 128) >> 4), idO,
+                                 (!first || k > 0) ? 1u : 0u);
+              umma_commit(&o_done[x][b]);
+            }
+            ++done;
+          }
+          if (!ok) break;
+          if (warp == 2) umma_commit(&kv_empty[st]);  // (its S was complete before P was written)
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      done_segment(i);
+    }
+    if (lane == 0) {
+      umma_commit(&drain[warp - 1]);  // all that this lane issued completes before tensor memory is freed
+      mbar_wait_bounded(&drain[warp - 1], 0);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax of chain x: a thread per row ---------------------------------------------
+    const int x = (warp - 4) >> 2;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t colO = K::kColO + x * D;
+    const float sl2 = SC ? 1.f : a.scale_log2;
+    // with a positive scale the maximum is of raw scores; masked ones become -inf before scaling (else +inf)
+    const bool pos_scale = sl2 > 0.f;
+    const float masked = pos_scale ? kNegInf : -kNegInf;
+  int done = 0;
+    bool ok = true;
+    Segment sg;
+    for (int i = 0; ok && next_segment(i, sg); ++i) {
+      const int first_seq = sg.one ? 0 : x * QT;
+      const int seqs = min(QT, sg.seqs - first_seq);
+      const int mine = sg.one ? (sg.stages + 1 - x) >> 1 : sg.stages;  // stages of this chain
+      const bool live = r < seqs * G;
+      const int s = live ? s_seq[i & 1][first_seq + r / G] : 0;
+      {
+        // this warp's rows of Q into shared memory, as a 128-byte-swizzled K-major tile
+        constexpr int kC = D / 8, kR = 32 / kC;  // 16-byte chunks of a row, rows per step
+        const int c = lane % kC;
+        uint4 v[kC];
+#pragma unroll
+        for (int k = 0; k < kC; ++k) {
+          const int rr = quarter * 32 + k * kR + lane / kC;
+          v[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (rr < seqs * G)
+            v[k] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                   (((int64_t)s_seq[i & 1][first_seq + rr / G] * H + sg.h) * G + rr % G) * D + 8 * c);
+        }
+#pragma unroll
+        for (int k = 0; k < kC; ++k) {
+          const int rr = quarter * 32 + k * kR + lane / kC;
+          const uint32_t at = sbase + x * K::kQBytes + (c >> 3) * (kM * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[k].x), "r"(v[k].y), "r"(v[k].z), "r"(v[k].w)
+                       : "memory");
+        }
+        fence_proxy_async_smem();
+      }
+      done_segment(i);
+      if (mine > 0 && lane == 0) arrive(&q_full[x]);
+      const int own = live ? shared_len(a, s) : 0;
+      // a key is seen when its age, counted from the prefix's last token, is below this
+      const int reach = live ? min(sg.N, sg.w - min(sg.w, own)) : 0;
+      const int last = sg.N > 0 ? (sg.N - 1) % sg.C : 0;
+      const bool any_live = __any_sync(0xffffffffu, live);
+      int reach_all = live ? reach : INT32_MAX;  // the least over the warp's rows
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) reach_all = min(reach_all, __shfl_xor_sync(0xffffffffu, reach_all, o));
+      const float slope = SC && live ? slope_log2(a.score, sg.h * G + r % G) : 0.f;
+      float m_ref = kNegInf, l = 0.f;
+      uint32_t clean_word = 0u;
+      for (int jj = 0; jj < mine; ++jj, ++done) {
+        const int b = done & 1;
+        const int j = sg.j0 + (sg.one ? 2 * jj + x : jj);  // stage of the item
+        if ((jj & 31) == 0) {  // stages whose keys all the warp's rows see, 32 at a time
+          const int jl = sg.j0 + (sg.one ? 2 * (jj + lane) + x : jj + lane);
+          bool clean = jl * kSub + kSub <= sg.tiles;
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+            const int age = tile_age(sg, last, min(jl * kSub + u, sg.tiles - 1));
+            clean = clean && (age >= kTile - 1 ? age : sg.C - 1) < reach_all;
+          }
+          clean_word = __ballot_sync(0xffffffffu, clean);
+        }
+        ok = __all_sync(0xffffffffu, wait(&s_full[x][b], (uint32_t)(done >> 1) & 1u, abort, a.pv.err));
+        if (!ok) break;
+        if (!any_live) {  // rows that nothing reads
+          if (lane == 0) arrive(&p_full[x][b]);
+          continue;
+        }
+        tc_fence_after_sync();
+        float sv[kKeys];
+        tmem_ld64(lane_base + (2 * x + b) * kKeys, sv);
+        const bool clean = (clean_word >> (jj & 31)) & 1u;
+        uint32_t vis[kSub];
+        int age[kSub];
+        if (!clean || SC) {
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+            age[u] = tile_age(sg, last, min(j * kSub + u, sg.tiles - 1));
+            // slots up to the newest, then (a tile that holds it) the oldest ones
+            vis[u] = bits16(age[u] - reach + 1, age[u]) | bits16(max(age[u] + 1, age[u] + sg.C - reach + 1), kTile - 1);
+            if (j * kSub + u >= sg.tiles) vis[u] = 0u;
+          }
+        }
+        if constexpr (SC) {
+          if (!clean) {  // what is masked does not decide how the others are capped
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+              for (int k = 0; k < kTile; ++k) sv[u * kTile + k] = (vis[u] >> k) & 1u ? sv[u * kTile + k] : 0.f;
+          }
+          const float2 sl = make_float2(a.scale_log2, a.scale_log2);
+          if (a.score.capped) {
+            const float hi = fold64(sv, [](float p, float q, float z) { return fmax3(p, q, z); });
+            const float lo = fold64(sv, [](float p, float q, float z) { return fmin3(p, q, z); });
+            const bool inside = __all_sync(0xffffffffu, fmaxf(hi, -lo) * fabsf(a.score.cap_in) <= 1.f || !live);
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 2) {
+              const float2 v = make_float2(sv[c], sv[c + 1]);
+              const float2 u = fmul2(v, make_float2(a.score.cap_in, a.score.cap_in));
+              const float2 y = fmul2(fmul2(v, sl), tanh_poly2(fmul2(u, u)));
+              sv[c] = y.x;
+              sv[c + 1] = y.y;
+              if (!inside) {
+                if (fabsf(u.x) > 1.f) sv[c] = a.score.cap_out * tanh_exp(u.x);
+                if (fabsf(u.y) > 1.f) sv[c + 1] = a.score.cap_out * tanh_exp(u.y);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 2) {
+              const float2 y = fmul2(make_float2(sv[c], sv[c + 1]), sl);
+              sv[c] = y.x;
+              sv[c + 1] = y.y;
+            }
+          }
+          if (a.score.slopes != nullptr) {
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+              for (int k = 0; k < kTile; ++k) {
+                int d = age[u] - k;
+                if (d < 0) d += sg.C;
+                sv[u * kTile + k] = fmaf(-slope, (float)((uint32_t)d + (uint32_t)own), sv[u * kTile + k]);
+              }
+          }
+        }
+        if (!clean) {
+#pragma unroll
+          for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) sv[u * kTile + k] = (vis[u] >> k) & 1u ? sv[u * kTile + k] : masked;
+        }
+        // row maximum in log2 units
+        float mx;
+        if (pos_scale) {
+          const float top = fold64(sv, [](float p, float q, float z) { return fmax3(p, q, z); });
+          mx = top == kNegInf ? kNegInf : top * sl2;
+        } else {
+          mx = kNegInf;
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) {
+            sv[c] = sv[c] == -kNegInf ? kNegInf : sv[c] * sl2;
+            mx = fmaxf(mx, sv[c]);
+          }
+        }
+        // the reference moves only when a maximum passes it by 2^8, so O is rarely touched
+        const float m_new = fmaxf(m_ref, mx);
+        const bool grow = m_new > m_ref + 8.f;
+        if (jj > 0 && __any_sync(0xffffffffu, grow)) {
+          const int before = done - 1;  // O may be rescaled once the last P . V into it has completed
+          ok = __all_sync(0xffffffffu, wait(&o_done[x][before & 1], (uint32_t)(before >> 1) & 1u, abort, a.pv.err));
+          if (!ok) break;
+          tc_fence_after_sync();
+          const float f = grow ? ex2(m_ref - m_new) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(lane_base + colO + c, o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] *= f;
+            tmem_st32(lane_base + colO + c, o);
+          }
+        }
+        if (grow) {
+          l *= ex2(m_ref - m_new);
+          m_ref = m_new;
+        }
+        const float bm = m_ref == kNegInf ? 0.f : m_ref;
+        // P (bf16 pairs) over the S columns it came from
+        const float2 sl2v = make_float2(pos_scale ? sl2 : 1.f, pos_scale ? sl2 : 1.f);
+        const float2 nb = make_float2(-bm, -bm);
+        float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float pk[kKeys / 2];
+#pragma unroll
+        for (int c = 0; c < kKeys / 2; ++c) {
+          const float2 t = ffma2(make_float2(sv[2 * c], sv[2 * c + 1]), sl2v, nb);
+          const float2 p = make_float2(ex2(t.x), ex2(t.y));
+          ls[c & 3] = fadd2(ls[c & 3], p);
+          pk[c] = __uint_as_float(pack_bf16(p.x, p.y));
+        }
+        l += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) + ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
+        tmem_st32(lane_base + (2 * x + b) * kKeys, pk);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive(&p_full[x][b]);
+      }
+      // the segment's partial, once the last P . V is in O
+      if (!ok) break;
+      const int64_t row = ((int64_t)2 * sg.slot + x) * a.chain_rows + r;
+      if (mine > 0 && any_live) {
+        const int before = done - 1;
+        ok = __all_sync(0xffffffffu, wait(&o_done[x][before & 1], (uint32_t)(before >> 1) & 1u, abort, a.pv.err));
+        if (!ok) break;
+        tc_fence_after_sync();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(lane_base + colO + c, o);
+          if (live) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<float4*>(a.part_o + row * D + c + 4 * k) = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+        }
+        tc_fence_before_sync();
+      }
+      if (live) reinterpret_cast<float2*>(a.part_ml)[row] = make_float2(m_ref, l);
+    }
+  }
+
+  // teardown: every tensor-memory access has completed (loads waited, the issuers drained)
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, K::kCols);
+  }
+}
+
+template <int D, bool SC>
+cudaError_t launch(const SharedArgs& a, const CUtensorMap* pool_map, const CUtensorMap* stage_map, int ctas, cudaStream_t st) {
+  const int smem = Cfg<D>::smem(a.num_prefixes);
+  const cudaError_t e = cudaFuncSetAttribute(shared_tc_kernel<D, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_tc_kernel<D, SC>, *pool_map, *stage_map, a);
+}
+
+}  // namespace
+
+int shared_tc_seqs(int group) { return kM / group; }
+
+cudaError_t launch_shared_tc(const SharedArgs& a, const CUtensorMap* pool_map, const CUtensorMap* stage_map, int ctas, cudaStream_t st) {
+  cudaError_t e = cudaErrorInvalidValue;
+  if (a.pv.head_dim == 128) e = a.score.on ? launch<128, true>(a, pool_map, stage_map, ctas, st) : launch<128, false>(a, pool_map, stage_map, ctas, st);
+  else if (a.pv.head_dim == 64) e = a.score.on ? launch<64, true>(a, pool_map, stage_map, ctas, st) : launch<64, false>(a, pool_map, stage_map, ctas, st);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace hwkv

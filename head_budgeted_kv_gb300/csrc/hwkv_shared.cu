@@ -184,84 +184,117 @@ constexpr int simt_smem() {
   return ((kRows + 2 * kKeys) * (D + 4) + kRows * (kKeys + 1)) * 4;
 }
 
-// One warp per (sequence, query head): out = sum_i acc_i 2^(m_i - M) / sum_i l_i 2^(m_i - M) over its own
-// partial and its prefix's, M = max_i m_i, in that order; nothing to attend to gives zeros.  kAhead
-// partials' loads in flight.
-constexpr int kJoinWarps = 4;
+// The join, a CTA per (sequence, KV head): out = sum_i acc_i 2^(m_i - M) / sum_i l_i 2^(m_i - M) over the head's own
+// partial and its prefix's, M = max_i m_i; nothing to attend to gives zeros.  A warp takes a head's maxima and
+// sums, a part per lane, and leaves the parts' weights in shared memory; then every thread sums four columns of a head
+// over every kSplit'th part, kAhead loads in flight, and the kSplit sums meet in shared memory.  The order of
+// all sums is fixed.
+constexpr int kJoinThreads = 256;
 constexpr int kAhead = 8;
+constexpr int kJoinParts = 64;  // parts whose weights are held at a time
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const __grid_constant__ SharedArgs a) {
-  constexpr int kC = D / 32;  // columns per lane
+__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_constant__ SharedArgs a) {
+  constexpr int kV = D / 4;  // float4 columns of a head
+  __shared__ float s_w[kJoinParts][kMaxGroup];   // weight of part and head
+  __shared__ float s_m[kMaxGroup], s_l[kMaxGroup];
+  __shared__ float4 s_acc[kJoinThreads];
   griddep_wait();
-  const int H = a.pv.kv_heads, G = a.group, Hq = H * G;
-  const int64_t row = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= (int64_t)a.num_seqs * Hq) return;
-  const int s = (int)(row / Hq), qh = (int)(row - (int64_t)s * Hq), h = qh / G, g = qh - h * G;
-  const int f = prefix_of(a, s, lane == 0 && qh == 0);
-  int64_t slot0 = 0, step = 0;  // rows of partials
-  int count = 0;
+  const int H = a.pv.kv_heads, G = a.group;
+  const int s = (int)blockIdx.x / H, h = (int)blockIdx.x - s * H;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * G;  // the first of the CTA's rows
+  const int f = prefix_of(a, s, threadIdx.x == 0 && h == 0);
+  int64_t part0 = 0, step = 0;  // partial rows of the first head
+  int parts = 0;
   if (f >= 0 && a.tc) {
     // a record is there for every row that sees a key of the prefix
     if (min(prefix_len(a, f), a.g.window[h] - min(a.g.window[h], shared_len(a, s))) > 0) {
-      const int4 rec = a.rec[(int64_t)s * H + h];
-      slot0 = (int64_t)rec.x * a.chain_rows + rec.w + g;
+      const int4 rec = a.rec[blockIdx.x];
+      part0 = (int64_t)rec.x * a.chain_rows + rec.w;
       step = (int64_t)rec.y * a.chain_rows;
-      count = rec.z;
+      parts = rec.z;
     }
   } else if (f >= 0) {
     const int chunks = a.chunk_prefix[H];
-    slot0 = ((int64_t)s * chunks + a.chunk_prefix[h]) * G + g;
+    part0 = ((int64_t)s * chunks + a.chunk_prefix[h]) * G;
     step = G;
-    count = a.chunk_prefix[h + 1] - a.chunk_prefix[h];
+    parts = a.chunk_prefix[h + 1] - a.chunk_prefix[h];
   }
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-  float2 own = reinterpret_cast<const float2*>(a.own_ml)[row];
-  own.x += a.own_shift;
-  float M = own.x;
-  for (int i = lane; i < count; i += 32) M = fmaxf(M, ml[slot0 + i * step].x);
+  const float2* own_ml = reinterpret_cast<const float2*>(a.own_ml) + row;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + part0;
+  // maxima and sums of the heads
+  for (int g = warp; g < G; g += kJoinThreads / 32) {
+    float2 own = own_ml[g];
+    own.x += a.own_shift;
+    float M = own.x;
+    for (int i = lane; i < parts; i += 32) M = fmaxf(M, ml[i * step + g].x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f, acc[kC];
-#pragma unroll
-  for (int c = 0; c < kC; ++c) acc[c] = 0.f;
-  auto add = [&](float2 e, const float (&v)[kC]) {
-    const float x = ex2(e.x - M);
-    L = fmaf(e.y, x, L);
-#pragma unroll
-    for (int c = 0; c < kC; ++c) acc[c] = fmaf(v[c], x, acc[c]);
-  };
-  auto load = [&](const float* p, float (&v)[kC]) {
-    if constexpr (kC == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(p + lane * kC);
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(p + lane * kC);
-      v[0] = x.x, v[1] = x.y;
-    }
-  };
-  if (own.x != kNegInf) {
-    float v[kC];
-    load(a.own_acc + row * D, v);
-    add(own, v);
-  }
-  for (int i0 = 0; i0 < count; i0 += kAhead) {
-    float v[kAhead][kC];
-    float2 e[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      e[j] = i0 + j < count ? ml[slot0 + (i0 + j) * step] : make_float2(kNegInf, 0.f);
-      if (e[j].x != kNegInf) load(a.part_o + (slot0 + (i0 + j) * step) * D, v[j]);  // an empty partial's sums are not written
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f;
+    for (int i = lane; i < parts; i += 32) {
+      const float2 e = ml[i * step + g];
+      const float x = e.x == kNegInf ? 0.f : ex2(e.x - M);
+      L = fmaf(e.y, x, L);
+      if (i < kJoinParts) s_w[i][g] = x;
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (e[j].x != kNegInf) add(e[j], v[j]);
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const float x = own.x == kNegInf ? 0.f : ex2(own.x - M);
+    if (lane == 0) {
+      s_m[g] = M;
+      s_l[g] = fmaf(own.y, x, L);
+    }
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  T* out = static_cast<T*>(a.out) + row * D + lane * kC;
+  __syncthreads();
+  const int cols = G * kV;
+  const int split = max(1, kJoinThreads / cols);  // threads of a column
+  const int e0 = (int)threadIdx.x % cols, k0 = (int)threadIdx.x / cols;
+  for (int c0 = 0; c0 < cols; c0 += kJoinThreads) {  // more than one pass: groups of more heads than threads hold
+    const int e = c0 + e0;
+    const bool on = e < cols && k0 < split;
+    const int g = on ? e / kV : 0, d = on ? e % kV : 0;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float4 v, float x) {
+      acc.x = fmaf(v.x, x, acc.x);
+      acc.y = fmaf(v.y, x, acc.y);
+      acc.z = fmaf(v.z, x, acc.z);
+      acc.w = fmaf(v.w, x, acc.w);
+    };
+    if (on && k0 == 0) {
+      const float m = own_ml[g].x + a.own_shift;
+      const float x = m == kNegInf ? 0.f : ex2(m - s_m[g]);
+      if (x != 0.f) add(reinterpret_cast<const float4*>(a.own_acc + (row + g) * D)[d], x);
+    }
+    for (int i0 = 0; i0 < parts; i0 += kAhead * split) {
+      float4 v[kAhead];
+      float x[kAhead];
 #pragma unroll
-  for (int c = 0; c < kC; ++c) store_out<T>(out + c, acc[c] * inv);
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = i0 + j * split + k0;
+        x[j] = 0.f;
+        if (on && i < parts) {
+          if (i < kJoinParts) x[j] = s_w[i][g];
+          else x[j] = ml[i * step + g].x == kNegInf ? 0.f : ex2(ml[i * step + g].x - s_m[g]);
+          // (a partial of no weight may hold anything)
+          if (x[j] != 0.f) v[j] = reinterpret_cast<const float4*>(a.part_o + (part0 + i * step + g) * D)[d];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (x[j] != 0.f) add(v[j], x[j]);
+    }
+    s_acc[threadIdx.x] = acc;
+    __syncthreads();
+    if (on && k0 == 0) {
+      for (int k = 1; k < split; ++k) add(s_acc[k * cols + e0], 1.f);
+      const float inv = s_l[g] > 0.f ? 1.f / s_l[g] : 0.f;
+      T* out = static_cast<T*>(a.out) + (row + g) * D + 4 * d;
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(out) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      else *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    }
+    __syncthreads();
+  }
 }
 
 template <typename T, int D, bool SC>
@@ -280,8 +313,8 @@ cudaError_t launch_simt(const SharedArgs& a, dim3 grid, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t launch_join(const SharedArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((int64_t)a.num_seqs * a.pv.kv_heads * a.group + kJoinWarps - 1) / kJoinWarps));
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.gridDim = dim3((unsigned)(a.num_seqs * a.pv.kv_heads));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -11,8 +11,8 @@
 //           item (segments) and leaves a partial (reference maximum, sum, unnormalised sums) per row and segment.
 //
 // Two query tiles of an item share every stage (each key is staged once for 256 rows).  An item of one tile gives its stages in
-// turn to two chains of the same rows, so the S -> softmax -> P.V latency of one hides behind the other's;
-// they leave two partials.
+// turn to two chains of the same rows, so the S -> softmax -> P.V latency of one hides behind the other's; at a
+// segment's end their states are joined out of tensor memory.
 //
 // Warp roles: 0 TMA producer; 1 issues S = Q K^T, 2 issues O += P V; 3 plans: segments, their sequences, and the
 // records the join reads; 4-7 softmax of tile (or chain) 0, 8-11 of 1, a thread per row.  Warps without a live row only keep
@@ -23,7 +23,6 @@
 // Waits are bounded (~2 s) and record HWKV_DEVERR_WAIT_TIMEOUT; then all roles stop.
 #include <algorithm>
 
-#include "hwkv_decode_tile.cuh"
 #include "hwkv_shared.cuh"
 #include "hwkv_tcgen05.cuh"
 
@@ -45,10 +44,10 @@ struct Cfg {
   static constexpr int kStageBytes = 2 * kKBytes;
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kStageOff = 2 * kQBytes;
-  static constexpr int kHistOff = kStageOff + kStages * kStageBytes;  // sequences and shortest own part of each prefix
+  static constexpr int kHistOff = kStageOff + kStages * kStageBytes;  // sequences, shortest own part and length of each prefix
   static constexpr uint32_t kCols = 512;
   static constexpr uint32_t kColO = 4 * kKeys;
-  static int smem(int prefixes) { return kHistOff + 8 * prefixes + 1024; }
+  static int smem(int prefixes) { return kHistOff + 12 * prefixes + 1024; }
 };
 
 // A CTA's part of one item.
@@ -119,6 +118,15 @@ __device__ __forceinline__ float fold64(const float (&v)[kKeys], Op op) {
   return op(op(t2[0], t2[1], t2[2]), op(t2[3], t2[4], t2[5]), op(t2[6], t2[7], t2[7]));
 }
 
+// First stage of CTA c's share of a line of T stages over n CTAs, and the CTA whose share holds stage t: 32-bit
+// divisions where the products fit.
+__device__ __forceinline__ long long line_start(long long T, int c, int n) {
+  return T < (1 << 22) ? (long long)((uint32_t)T * (uint32_t)c / (uint32_t)n) : T * c / n;
+}
+__device__ __forceinline__ int line_cta(long long t, long long T, int n) {
+  return T < (1 << 22) ? (int)((((uint32_t)t + 1u) * (uint32_t)n - 1u) / (uint32_t)T) : (int)(((t + 1) * n - 1) / T);
+}
+
 // The ring tiles of the newest `need` of N tokens: first tile and their number.
 __device__ __forceinline__ void need_tiles(int N, int need, int C, int& first_tile, int& tiles) {
   first_tile = tiles = 0;
@@ -136,6 +144,12 @@ __device__ __forceinline__ int tile_age(const Segment& sg, int last, int i) {
   return d < 0 ? d + sg.C : d;
 }
 
+__device__ __forceinline__ void store_part(float* p, const float (&o)[32]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    *reinterpret_cast<float4*>(p + 4 * k) = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+}
+
 template <int D, bool SC>
 __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ CUtensorMap pool_map,
                                                                const __grid_constant__ CUtensorMap stage_map,
@@ -146,18 +160,19 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   int* s_count = reinterpret_cast<int*>(smem + K::kHistOff);
   int* s_short = s_count + a.num_prefixes;
+  int* s_len = s_short + a.num_prefixes;
   __shared__ __align__(8) uint64_t kv_full[NS], kv_empty[NS];
   // per chain x and parity b of its stages (a phase is one stage of that parity, so no waiter falls two behind)
   __shared__ __align__(8) uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2], drain[2];
   __shared__ __align__(8) uint64_t seg_full[2], seg_empty[2];
+  __shared__ __align__(8) uint64_t ml_full, o_read;  // two chains of the same rows: states published, O of both read
+  __shared__ float2 s_ml[2][kM];
   __shared__ Segment s_seg[2];
   __shared__ int s_seq[2][2 * kM];
   __shared__ int4 s_copy[32];  // copy plan of the producer's next 32 stages: pool rows of the four tiles
+  __shared__ int2 s_box[32];   // ... or the one box that holds them: first block (-1: none) and row in it
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ long long s_scan[kThreads / 32];
-  __shared__ long long s_pre[2];
-  __shared__ int s_entry;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int H = a.pv.kv_heads, G = a.group, bs = a.pv.block_size;
@@ -166,12 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   griddep_wait();
   griddep_launch_dependents();  // the own parts may start where SMs are free: all before this grid has completed
 
-  // ---- sequences and shortest own part of each prefix ---------------------------------------
-  for (int f = threadIdx.x; f < a.num_prefixes; f += kThreads) {
-    s_count[f] = 0;
-    s_short[f] = INT32_MAX;
-    if (cta == 0 && a.prefix_lens[f] < 0) atomicOr(a.pv.err, HWKV_DEVERR_NEG_LENGTH);
-  }
+  // ---- sequences, shortest own part and length of each prefix ---------------------------------
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&kv_full[i], 1);
@@ -188,72 +198,39 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       mbar_init(&seg_full[x], 1);
       mbar_init(&seg_empty[x], kRoleWarps);
     }
+    mbar_init(&ml_full, 8);
+    mbar_init(&o_read, 8);
     s_abort = 0;
-    s_entry = -1;
     fence_mbar_init();
     prefetch_tensormap(&pool_map);
     prefetch_tensormap(&stage_map);
-  }
-  __syncthreads();
-  for (int s = threadIdx.x; s < a.num_seqs; s += kThreads) {
-    const int f = prefix_of(a, s, cta == 0);
-    if (f < 0) continue;
-    atomicAdd(&s_count[f], 1);
-    atomicMin(&s_short[f], shared_len(a, s));
-  }
-  __syncthreads();
-
-  // ---- the line: entries (prefix, head) of tiles x stages -----------------------------------
-  struct Entry {
-    int f, h, N, w, C, first_tile, tiles, stages, items;
-  };
-  auto entry_of = [&](int e) {
-    Entry n;
-    n.f = e / H;
-    n.h = e - n.f * H;
-    n.N = prefix_len(a, n.f);
-    n.w = a.g.window[n.h];
-    n.C = (a.g.nblk_prefix[n.h + 1] - a.g.nblk_prefix[n.h]) * bs;
-    n.items = (s_count[n.f] + 2 * QT - 1) / (2 * QT);
-    const int need = n.items > 0 ? min(n.N, n.w - min(n.w, s_short[n.f])) : 0;
-    need_tiles(n.N, need, n.C, n.first_tile, n.tiles);
-    n.stages = (n.tiles + kSub - 1) / kSub;
-    return n;
-  };
-  const int entries = a.num_prefixes * H;
-  const int per = (entries + kThreads - 1) / kThreads;
-  const int e_lo = min(entries, (int)threadIdx.x * per), e_hi = min(entries, e_lo + per);
-  long long mine = 0, mine_items = 0;
-  for (int e = e_lo; e < e_hi; ++e) {
-    const Entry n = entry_of(e);
-    mine += (long long)n.items * n.stages;
-    mine_items += n.items;
-  }
-  long long T, all_items;
-  const long long excl = block_exclusive_scan<kThreads / 32>(mine, s_scan, T);
-  const long long excl_items = block_exclusive_scan<kThreads / 32>(mine_items, s_scan, all_items);
-  const int ctas = (int)max(1ll, min((long long)gridDim.x, T / kMinStages));
-  if (cta >= ctas || T == 0) return;
-  const long long t_lo = range_start(T, cta, ctas), t_hi = range_start(T, cta + 1, ctas);
-  if (excl <= t_lo && t_lo < excl + mine) {
-    long long pre = excl, items = excl_items;
-    for (int e = e_lo; e < e_hi; ++e) {
-      const Entry n = entry_of(e);
-      const long long span = (long long)n.items * n.stages;
-      if (t_lo < pre + span) {
-        s_entry = e;
-        s_pre[0] = pre;
-        s_pre[1] = items;
-        break;
-      }
-      pre += span;
-      items += n.items;
-    }
   }
   if (warp == 1) {
     tmem_alloc(&s_tmem, K::kCols);
     tmem_relinquish();
   }
+  for (int f = threadIdx.x; f < a.num_prefixes; f += kThreads) {
+    s_count[f] = 0;
+    s_short[f] = INT32_MAX;
+  }
+  // the first sequence's and prefix's loads are on their way while the counts are cleared
+  const int s_own = (int)threadIdx.x < a.num_seqs ? (int)threadIdx.x : -1;
+  int f_own = s_own >= 0 ? a.prefix_of[s_own] : -1;
+  const int n_own = s_own >= 0 ? shared_len(a, s_own) : 0;
+  for (int f = threadIdx.x; f < a.num_prefixes; f += kThreads) {
+    const int N = a.prefix_lens[f];
+    if (N < 0 && cta == 0) atomicOr(a.pv.err, HWKV_DEVERR_NEG_LENGTH);
+    s_len[f] = max(N, 0);
+  }
+  __syncthreads();
+  auto count = [&](int f, int n) {
+    if (f >= a.num_prefixes && cta == 0) atomicOr(a.pv.err, HWKV_DEVERR_BAD_PREFIX);
+    if (f < 0 || f >= a.num_prefixes) return;
+    atomicAdd(&s_count[f], 1);
+    atomicMin(&s_short[f], n);
+  };
+  count(f_own, n_own);
+  for (int s = threadIdx.x + kThreads; s < a.num_seqs; s += kThreads) count(a.prefix_of[s], shared_len(a, s));
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -275,10 +252,57 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
 
   if (warp == 3) {
     // ---- planner ------------------------------------------------------------------------
-    int e = s_entry;
-    long long pre = s_pre[0], items = s_pre[1];
-    Entry n = entry_of(e);
-    long long at = t_lo;
+    // The line: entries (prefix, head) of items x stages, some consecutive ones per lane.
+    struct Entry {
+      int f, h, C, first_tile, tiles, stages, items;
+    };
+    auto entry_of = [&](int e) {
+      Entry n;
+      n.f = e / H;
+      n.h = e - n.f * H;
+      n.C = (a.g.nblk_prefix[n.h + 1] - a.g.nblk_prefix[n.h]) * bs;
+      n.items = (s_count[n.f] + 2 * QT - 1) / (2 * QT);
+      const int w = a.g.window[n.h];
+      need_tiles(s_len[n.f], n.items > 0 ? min(s_len[n.f], w - min(w, s_short[n.f])) : 0, n.C, n.first_tile, n.tiles);
+      n.stages = (n.tiles + kSub - 1) / kSub;
+      return n;
+    };
+    const int entries = a.num_prefixes * H;
+    const int per = (entries + 31) / 32;
+    const int e_lo = min(entries, lane * per), e_hi = min(entries, e_lo + per);
+    long long mine = 0, sum = 0;
+    int mine_items = 0, sum_items = 0;
+    for (int e = e_lo; e < e_hi; ++e) {
+      const Entry n = entry_of(e);
+      mine += (long long)n.items * n.stages;
+      mine_items += n.items;
+    }
+    sum = mine;
+    sum_items = mine_items;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+      const int z = __shfl_up_sync(0xffffffffu, sum_items, o);
+      if (lane >= o) {
+        sum += y;
+        sum_items += z;
+      }
+    }
+    const long long T = __shfl_sync(0xffffffffu, sum, 31);
+    const int ctas = T < (long long)kMinStages * gridDim.x ? max(1, (int)T / kMinStages) : (int)gridDim.x;
+    long long at = 0, t_hi = 0, pre = 0;
+    int e = 0, items = 0;
+    Entry n{};
+    if (cta < ctas && T > 0) {
+      at = line_start(T, cta, ctas);
+      t_hi = line_start(T, cta + 1, ctas);
+      // the lane whose entries hold the range's first stage
+      const int who = __ffs(__ballot_sync(0xffffffffu, sum - mine <= at && at < sum)) - 1;
+      pre = __shfl_sync(0xffffffffu, sum - mine, who);
+      items = __shfl_sync(0xffffffffu, sum_items - mine_items, who);
+      e = who * per;
+      n = entry_of(e);
+    }
     for (int i = 0;; ++i) {
       if (i >= 2 && !__all_sync(0xffffffffu, wait(&seg_empty[i & 1], (uint32_t)((i >> 1) - 1) & 1u, abort, a.pv.err))) break;
       if (at >= t_hi) {
@@ -293,10 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         items += n.items;
         n = entry_of(++e);
       }
-      const int off = (int)((at - pre) / n.stages);  // the entry's item
+      const int off = at - pre <= INT32_MAX ? (int)(at - pre) / n.stages : (int)((at - pre) / n.stages);  // the entry's item
       const long long begin = pre + (long long)off * n.stages, end = begin + n.stages;
       Segment sg;
-      sg.f = n.f, sg.h = n.h, sg.N = n.N, sg.w = n.w, sg.C = n.C, sg.first_tile = n.first_tile, sg.tiles = n.tiles;
+      sg.f = n.f, sg.h = n.h, sg.N = s_len[n.f], sg.w = a.g.window[n.h], sg.C = n.C, sg.first_tile = n.first_tile, sg.tiles = n.tiles;
       sg.j0 = (int)(at - begin);
       sg.stages = (int)(min(end, t_hi) - at);
       sg.seqs = shared_members(a, n.f, off * 2 * QT, 2 * QT, s_seq[i & 1], lane);
@@ -308,11 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         arrive(&seg_full[i & 1]);
       }
       if (sg.j0 == 0) {  // the item's records: its partials lie one slot per CTA
-        const int parts = cta_of(end - 1, T, ctas) - cta + 1;
+        const int parts = line_cta(end - 1, T, ctas) - cta + 1;
         for (int k = lane; k < sg.seqs; k += 32) {
           const int x = sg.one ? 0 : k / QT;
           a.rec[(int64_t)s_seq[i & 1][k] * H + n.h] =
-              make_int4(2 * sg.slot + x, sg.one ? 1 : 2, sg.one ? 2 * parts : parts, (k - x * QT) * G);
+              make_int4(2 * sg.slot + x, 2, parts, (k - x * QT) * G);
         }
       }
       at += sg.stages;
@@ -329,22 +353,38 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       // 32 stages planned at a time, one per lane (table look-ups in parallel); lane 0 issues the copies
       for (int c0 = 0; ok && c0 < sg.stages; c0 += 32) {
         if (c0 + lane < sg.stages) {
-          int row[kSub];
+          int row[kSub], blk[kSub], r0[kSub];
+          bool box = a.stage_tb > 0;  // one box of the stage map: stage_tb rows of each of consecutive blocks
 #pragma unroll
           for (int u = 0; u < kSub; ++u) {
             const int k = (sg.j0 + c0 + lane) * kSub + u;
-            row[u] = 0;  // past the item: row 0 of the pool, masked
+            blk[u] = 0;  // past the item: row 0 of the pool, masked
+            r0[u] = 0;
             if (k < sg.tiles) {
               int t = sg.first_tile + k;
               if (t >= C16) t -= C16;
               const int t0 = t << 4;
               const int jb = a.bs_log2 >= 0 ? t0 >> a.bs_log2 : t0 / bs;
-              const int32_t blk = __ldg(tbl + jb);
-              if (blk < 0 || (int64_t)blk >= a.pv.total_blocks) atomicOr(a.pv.err, HWKV_DEVERR_BAD_BLOCK);
-              else row[u] = blk * 2 * bs + (t0 - jb * bs);
+              blk[u] = __ldg(tbl + jb);
+              r0[u] = t0 - jb * bs;
+            } else {
+              box = false;
             }
           }
+          const int step_log2 = a.stage_tb == 64 ? 6 : a.stage_tb == 32 ? 5 : 4;
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+            if (blk[u] < 0 || (int64_t)blk[u] >= a.pv.total_blocks) {
+              atomicOr(a.pv.err, HWKV_DEVERR_BAD_BLOCK);
+              blk[u] = r0[u] = 0;
+              box = false;
+            }
+            row[u] = blk[u] * 2 * bs + r0[u];
+            box = box && blk[u] == blk[0] + ((kTile * u) >> step_log2) && r0[u] == r0[0] + ((kTile * u) & (a.stage_tb - 1));
+          }
+          box = box && r0[0] + a.stage_tb <= bs;
           s_copy[lane] = make_int4(row[0], row[1], row[2], row[3]);
+          s_box[lane] = make_int2(box ? blk[0] : -1, r0[0]);
         }
         __syncwarp();
         if (lane == 0) {
@@ -358,18 +398,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             const int row[kSub] = {c.x, c.y, c.z, c.w};
             const uint32_t kdst = sbase + K::kStageOff + st * K::kStageBytes, vdst = kdst + K::kKBytes;
             mbar_arrive_expect_tx(&kv_full[st], K::kStageBytes);
-            // 64 keys that one box of the stage map covers: stage_tb rows of each of consecutive blocks
-            const int tb = a.stage_tb;
-            const int blk = row[0] / (2 * bs), r0 = row[0] - blk * 2 * bs;
-            bool box = tb > 0 && r0 + tb <= bs && (sg.j0 + c0 + l) * kSub + kSub <= sg.tiles;
-#pragma unroll
-            for (int u = 1; u < kSub; ++u)
-              box = box && row[u] == row[0] + (kTile * u) / max(tb, 1) * 2 * bs + ((kTile * u) & (tb - 1));
-            if (box) {
+            const int2 box = s_box[l];
+            if (box.x >= 0) {
 #pragma unroll
               for (int hf = 0; hf < K::kHalves; ++hf) {
-                tma_3d(kdst + hf * (kKeys * 128), &stage_map, hf * 64, r0, blk, &kv_full[st]);
-                tma_3d(vdst + hf * (kKeys * 128), &stage_map, hf * 64, bs + r0, blk, &kv_full[st]);
+                tma_3d(kdst + hf * (kKeys * 128), &stage_map, hf * 64, box.y, box.x, &kv_full[st]);
+                tma_3d(vdst + hf * (kKeys * 128), &stage_map, hf * 64, bs + box.y, box.x, &kv_full[st]);
               }
             } else {
 #pragma unroll
@@ -472,13 +506,16 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     const int x = (warp - 4) >> 2;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
+    const int seq_r = r / G, head_r = r - seq_r * G;  // the row's sequence of the tile, and query head
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t colO = K::kColO + x * D;
     const float sl2 = SC ? 1.f : a.scale_log2;
     // with a positive scale the maximum is of raw scores; masked ones become -inf before scaling (else +inf)
     const bool pos_scale = sl2 > 0.f;
     const float masked = pos_scale ? kNegInf : -kNegInf;
-  int done = 0;
+    int done = 0;
+    uint32_t joins = 0;   // segments of two chains so far
+    bool joined = false;  // after one: O may still be read by the other chain's warps
     bool ok = true;
     Segment sg;
     for (int i = 0; ok && next_segment(i, sg); ++i) {
@@ -486,19 +523,18 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       const int seqs = min(QT, sg.seqs - first_seq);
       const int mine = sg.one ? (sg.stages + 1 - x) >> 1 : sg.stages;  // stages of this chain
       const bool live = r < seqs * G;
-      const int s = live ? s_seq[i & 1][first_seq + r / G] : 0;
+      const int s = live ? s_seq[i & 1][first_seq + seq_r] : 0;
       {
         // this warp's rows of Q into shared memory, as a 128-byte-swizzled K-major tile
         constexpr int kC = D / 8, kR = 32 / kC;  // 16-byte chunks of a row, rows per step
         const int c = lane % kC;
+        const int row = live ? (s * H + sg.h) * G + head_r : -1;  // the lane's row among the queries
         uint4 v[kC];
 #pragma unroll
         for (int k = 0; k < kC; ++k) {
-          const int rr = quarter * 32 + k * kR + lane / kC;
+          const int from = __shfl_sync(0xffffffffu, row, k * kR + lane / kC);
           v[k] = make_uint4(0u, 0u, 0u, 0u);
-          if (rr < seqs * G)
-            v[k] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                   (((int64_t)s_seq[i & 1][first_seq + rr / G] * H + sg.h) * G + rr % G) * D + 8 * c);
+          if (from >= 0) v[k] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (int64_t)from * D + 8 * c);
         }
 #pragma unroll
         for (int k = 0; k < kC; ++k) {
@@ -519,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       int reach_all = live ? reach : INT32_MAX;  // the least over the warp's rows
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) reach_all = min(reach_all, __shfl_xor_sync(0xffffffffu, reach_all, o));
-      const float slope = SC && live ? slope_log2(a.score, sg.h * G + r % G) : 0.f;
+      const float slope = SC && live ? slope_log2(a.score, sg.h * G + head_r) : 0.f;
       float m_ref = kNegInf, l = 0.f;
       uint32_t clean_word = 0u;
       for (int jj = 0; jj < mine; ++jj, ++done) {
@@ -536,6 +572,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           clean_word = __ballot_sync(0xffffffffu, clean);
         }
         ok = __all_sync(0xffffffffu, wait(&s_full[x][b], (uint32_t)(done >> 1) & 1u, abort, a.pv.err));
+        if (ok && joined) {  // the other chain's warps may still read O: no P . V into it before
+          ok = __all_sync(0xffffffffu, wait(&o_read, (joins - 1u) & 1u, abort, a.pv.err));
+          joined = false;
+        }
         if (!ok) break;
         if (!any_live) {  // rows that nothing reads
           if (lane == 0) arrive(&p_full[x][b]);
@@ -661,25 +701,66 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       }
       // the segment's partial, once the last P . V is in O
       if (!ok) break;
-      const int64_t row = ((int64_t)2 * sg.slot + x) * a.chain_rows + r;
-      if (mine > 0 && any_live) {
+      if (mine > 0) {
         const int before = done - 1;
         ok = __all_sync(0xffffffffu, wait(&o_done[x][before & 1], (uint32_t)(before >> 1) & 1u, abort, a.pv.err));
         if (!ok) break;
         tc_fence_after_sync();
+      }
+      int64_t row = ((int64_t)2 * sg.slot + x) * a.chain_rows + r;
+      if (!sg.one) {
+        if (any_live) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32(lane_base + colO + c, o);
-          if (live) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<float4*>(a.part_o + row * D + c + 4 * k) = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(lane_base + colO + c, o);
+            if (live) store_part(a.part_o + row * D + c, o);
           }
         }
+        if (live) reinterpret_cast<float2*>(a.part_ml)[row] = make_float2(m_ref, l);
+      } else {
+        // Two chains of the same rows: each warp learns the other chain's state and writes half of the columns,
+        // sum_x O_x 2^(m_x - M).  (The o_done that each waited for, with the fences around the barrier, orders the
+        // other chain's products before these loads.)
+        if (joined) {  // (a chain without a stage since the last one)
+          ok = __all_sync(0xffffffffu, wait(&o_read, (joins - 1u) & 1u, abort, a.pv.err));
+          if (!ok) break;
+        }
+        s_ml[x][r] = make_float2(m_ref, l);
         tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive(&ml_full);
+        ok = __all_sync(0xffffffffu, wait(&ml_full, joins & 1u, abort, a.pv.err));
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (any_live) {
+          const float2 e0 = s_ml[0][r], e1 = s_ml[1][r];
+          const float M = fmaxf(e0.x, e1.x);
+          const float f0 = e0.x == kNegInf ? 0.f : ex2(e0.x - M), f1 = e1.x == kNegInf ? 0.f : ex2(e1.x - M);
+          const bool two = sg.stages > 1;  // else chain 1 has no product, and its O is of an earlier segment
+          row = (int64_t)2 * sg.slot * a.chain_rows + r;
+#pragma unroll 1
+          for (int c = x * (D / 2); c < (x + 1) * (D / 2); c += 32) {
+            float o[32];
+            tmem_ld32(lane_base + K::kColO + c, o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] *= f0;
+            if (two) {
+              float p[32];
+              tmem_ld32(lane_base + K::kColO + D + c, p);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = fmaf(p[k], f1, o[k]);
+            }
+            if (live) store_part(a.part_o + row * D + c, o);
+          }
+          if (live && x == 0) reinterpret_cast<float2*>(a.part_ml)[row] = make_float2(M, e0.y * f0 + e1.y * f1);
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive(&o_read);
+        ++joins;
+        joined = true;
       }
-      if (live) reinterpret_cast<float2*>(a.part_ml)[row] = make_float2(m_ref, l);
     }
   }
 

@@ -1184,7 +1184,7 @@ int decode_common(hwkv_pool_t p, int layer, const void* q, int q_heads, hwkv_sco
 }
 
 // Which kernel reads the prefixes' keys: the tensor cores' where its tiles fit.
-bool shared_tc(const hwkv_pool* prefix) { return prefill_eligible(prefix); }
+bool shared_tc(const hwkv_pool* prefix) { return prefix->g.dtype == HWKV_E4M3 ? prefix->has_tmap : prefill_eligible(prefix); }
 
 // How the keys of the prefixes are split on the CUDA cores: ring slots per CTA for about six CTAs per SM over
 // the sequences' tiles, and the chunks of each head.

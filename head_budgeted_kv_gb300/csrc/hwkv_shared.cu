@@ -9,9 +9,7 @@
 // block sizes that no 16-row tile divides); the own parts come from the decode kernels, left open
 // (hwkv_decode_sk.cuh, kOpen); and the join below weighs the partials of both by their reference maxima.
 #include <algorithm>
-#include <type_traits>
 
-#include "hwkv_fp8.cuh"
 #include "hwkv_shared.cuh"
 
 namespace hwkv {
@@ -24,24 +22,8 @@ constexpr int kThreads = 128;  // four per row
 // CTA = (prefix, head, chunk of ring slots; sequences).  A pass brings 32 keys and values into shared memory; the four
 // threads of a row take eight scores each, the row's maximum and sum over them by shuffles, then a quarter
 // of head_dim each of the weighted sum.  fp32 throughout.
-template <typename T>
-struct Io {
-  using type = T;  // of queries and outputs
-};
-template <>
-struct Io<E4m3> {
-  using type = __nv_bfloat16;
-};
-
-__device__ __forceinline__ float code_value(const E4m3* p) {
-  uint32_t lo, hi;
-  e4m3x4_to_f16(p->code, lo, hi);
-  return half2_to_float2(lo).x;
-}
-
 template <typename T, int D, bool SC>
 __global__ void __launch_bounds__(kThreads) shared_simt_kernel(const __grid_constant__ SharedArgs a) {
-  using Q = typename Io<T>::type;
   constexpr int kLd = D + 4;  // floats per row in shared memory: rows 16 bytes apart in the banks
   extern __shared__ float4 smem4[];
   float* s_q = reinterpret_cast<float*>(smem4);  // [kRows][kLd]
@@ -75,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) shared_simt_kernel(const __grid_cons
   for (int e = threadIdx.x; e < kRows * D; e += kThreads) {
     const int r = e / D, d = e - r * D;
     float x = 0.f;
-    if (r < rows) x = load_in<Q>(static_cast<const Q*>(a.q) + (((int64_t)s_seq[r / G] * H + h) * G + r % G) * D + d);
+    if (r < rows) x = load_in<T>(static_cast<const T*>(a.q) + (((int64_t)s_seq[r / G] * H + h) * G + r % G) * D + d);
     s_q[r * kLd + d] = x;
   }
   const int r = threadIdx.x >> 2, part = threadIdx.x & 3;
@@ -104,14 +86,8 @@ __global__ void __launch_bounds__(kThreads) shared_simt_kernel(const __grid_cons
           if (d == 0) atomicOr(a.pv.err, HWKV_DEVERR_BAD_BLOCK);
         } else {
           const T* row = static_cast<const T*>(a.pv.pool) + ((int64_t)blk * 2 * bs + (t - j * bs)) * D;
-          if constexpr (std::is_same_v<T, E4m3>) {
-            const float* scale = a.pv.scales + ((int64_t)blk * (bs / kScaleGroup) + (t - j * bs) / kScaleGroup) * 2;
-            kx = code_value(row + d) * scale[0];
-            vx = code_value(row + (int64_t)bs * D + d) * scale[1];
-          } else {
-            kx = load_in<T>(row + d);
-            vx = load_in<T>(row + (int64_t)bs * D + d);
-          }
+          kx = load_in<T>(row + d);
+          vx = load_in<T>(row + (int64_t)bs * D + d);
         }
       }
       s_k[key * kLd + d] = kx;
@@ -334,7 +310,6 @@ cudaError_t launch_shared_simt(const SharedArgs& a, int dtype, int chunks, cudaS
   cudaError_t e = cudaErrorInvalidValue;
   if (dtype == HWKV_F32) e = D == 128 ? launch_simt<float, 128>(a, grid, st) : launch_simt<float, 64>(a, grid, st);
   else if (dtype == HWKV_BF16) e = D == 128 ? launch_simt<__nv_bfloat16, 128>(a, grid, st) : launch_simt<__nv_bfloat16, 64>(a, grid, st);
-  else if (dtype == HWKV_E4M3) e = D == 128 ? launch_simt<E4m3, 128>(a, grid, st) : launch_simt<E4m3, 64>(a, grid, st);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

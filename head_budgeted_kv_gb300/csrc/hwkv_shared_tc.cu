@@ -1,5 +1,5 @@
 // The prefixes' keys of a decode behind shared prefixes (hwkv_shared.cu) on the sm_100-family tensor cores
-// (tcgen05, accumulators in tensor memory), for bf16 pools whose blocks are whole 16-row tiles.
+// (tcgen05, accumulators in tensor memory), for bf16 pools whose blocks are whole 16-row tiles and for 8-bit pools.
 //
 // The queries of all sequences behind a prefix are rows of one product with its keys: with r rows a key's
 // 4 D bytes serve 4 r D operations, so up to ~290 rows the keys' bytes bound the call and beyond that the
@@ -19,10 +19,15 @@
 // the barriers in step.  Segments are handed out through two descriptors in shared memory, so the
 // producer runs into the next one while the last is finished.
 //
+// 8-bit pools: warps 12-15 turn the codes that the producer brings into a stage of bf16 rows, code x scale, which bf16 holds
+// exactly (3 mantissa bits, a power of two); a warp takes the K and V rows of one 16-slot tile.  The same products follow.
+// V rows of slots outside the prefix's window become zeros, whatever they hold.
+//
 // Weights are rounded to bf16 for P V (2^-8 of each, half a step); their sum is of the unrounded ones.
 // Waits are bounded (~2 s) and record HWKV_DEVERR_WAIT_TIMEOUT; then all roles stop.
 #include <algorithm>
 
+#include "hwkv_fp8.cuh"
 #include "hwkv_shared.cuh"
 #include "hwkv_tcgen05.cuh"
 
@@ -32,19 +37,24 @@ namespace {
 constexpr int kM = 128;                 // query rows per tile (MMA M)
 constexpr int kKeys = 64;               // keys per stage
 constexpr int kSub = kKeys / kTile;     // ring tiles per stage
-constexpr int kThreads = 12 * 32;
 constexpr int kMinStages = 4;           // fewest stages of a CTA
 constexpr int kRoleWarps = 11;          // warps that read a segment's descriptor
 
-template <int D>
+template <int D, bool Q8>
 struct Cfg {
+  static constexpr int kThreads = (Q8 ? 16 : 12) * 32;
   static constexpr int kHalves = D / 64;
   static constexpr int kQBytes = kM * D * 2;
   static constexpr int kKBytes = kKeys * D * 2;
   static constexpr int kStageBytes = 2 * kKBytes;
-  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kStages = (D == 128 ? 4 : 8) - (Q8 ? (D == 128 ? 1 : 2) : 0);
   static constexpr int kStageOff = 2 * kQBytes;
-  static constexpr int kHistOff = kStageOff + kStages * kStageBytes;  // sequences, shortest own part and length of each prefix
+  // 8-bit: stages of codes, four tiles of 16 K and 16 V rows each
+  static constexpr int kTileBytes = 2 * kTile * D;
+  static constexpr int kCodeBytes = kSub * kTileBytes;
+  static constexpr int kCodeStages = Q8 ? (D == 128 ? 3 : 4) : 1;
+  static constexpr int kCodeOff = kStageOff + kStages * kStageBytes;
+  static constexpr int kHistOff = kCodeOff + (Q8 ? kCodeStages * kCodeBytes : 0);  // sequences, shortest own part and length of each prefix
   static constexpr uint32_t kCols = 512;
   static constexpr uint32_t kColO = 4 * kKeys;
   static int smem(int prefixes) { return kHistOff + 12 * prefixes + 1024; }
@@ -150,18 +160,22 @@ __device__ __forceinline__ void store_part(float* p, const float (&o)[32]) {
     *reinterpret_cast<float4*>(p + 4 * k) = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
 }
 
-template <int D, bool SC>
-__global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ CUtensorMap pool_map,
+template <int D, bool SC, bool Q8>
+__global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(const __grid_constant__ CUtensorMap pool_map,
                                                                const __grid_constant__ CUtensorMap stage_map,
                                                                const __grid_constant__ SharedArgs a) {
-  using K = Cfg<D>;
-  constexpr int NS = K::kStages;
+  using K = Cfg<D, Q8>;
+  constexpr int NS = K::kStages, kThreads = K::kThreads;
+  constexpr int NC = K::kCodeStages;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   int* s_count = reinterpret_cast<int*>(smem + K::kHistOff);
   int* s_short = s_count + a.num_prefixes;
   int* s_len = s_short + a.num_prefixes;
   __shared__ __align__(8) uint64_t kv_full[NS], kv_empty[NS];
+  __shared__ __align__(8) uint64_t code_full[NC], code_empty[NC];
+  constexpr int kScaleRing = Q8 ? 64 : 1;  // scales (K, V) of the stages' tiles, planned up to 32 stages ahead
+  __shared__ float2 s_scale[kScaleRing][kSub];
   // per chain x and parity b of its stages (a phase is one stage of that parity, so no waiter falls two behind)
   __shared__ __align__(8) uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2], drain[2];
   __shared__ __align__(8) uint64_t seg_full[2], seg_empty[2];
@@ -170,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   __shared__ Segment s_seg[2];
   __shared__ int s_seq[2][2 * kM];
   __shared__ int4 s_copy[32];  // copy plan of the producer's next 32 stages: pool rows of the four tiles
+  __shared__ int4 s_rows[Q8 ? 32 : 1];  // 8-bit: blocks in s_copy, rows in them here
   __shared__ int2 s_box[32];   // ... or the one box that holds them: first block (-1: none) and row in it
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
@@ -184,8 +199,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   // ---- sequences, shortest own part and length of each prefix ---------------------------------
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_full[i], Q8 ? 4 : 1);
       mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < NC; ++i) {
+      mbar_init(&code_full[i], 1);
+      mbar_init(&code_empty[i], 4);
     }
     for (int x = 0; x < 2; ++x) {
       for (int b = 0; b < 2; ++b) {
@@ -196,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       mbar_init(&q_full[x], 4);
       mbar_init(&drain[x], 1);
       mbar_init(&seg_full[x], 1);
-      mbar_init(&seg_empty[x], kRoleWarps);
+      mbar_init(&seg_empty[x], kRoleWarps + (Q8 ? 4 : 0));
     }
     mbar_init(&ml_full, 8);
     mbar_init(&o_read, 8);
@@ -383,12 +402,34 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             box = box && blk[u] == blk[0] + ((kTile * u) >> step_log2) && r0[u] == r0[0] + ((kTile * u) & (a.stage_tb - 1));
           }
           box = box && r0[0] + a.stage_tb <= bs;
-          s_copy[lane] = make_int4(row[0], row[1], row[2], row[3]);
+          if constexpr (Q8) {
+            const int groups = bs / kScaleGroup;
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+              s_scale[(issued + lane) % kScaleRing][u] =
+                  __ldcg(reinterpret_cast<const float2*>(a.pv.scales) + (int64_t)blk[u] * groups + (r0[u] >> 4));
+          }
+          s_copy[lane] = Q8 ? make_int4(blk[0], blk[1], blk[2], blk[3]) : make_int4(row[0], row[1], row[2], row[3]);
           s_box[lane] = make_int2(box ? blk[0] : -1, r0[0]);
+          if constexpr (Q8) s_rows[lane] = make_int4(r0[0], r0[1], r0[2], r0[3]);
         }
         __syncwarp();
         if (lane == 0) {
           for (int l = 0; l < 32 && c0 + l < sg.stages; ++l, ++issued) {
+            if constexpr (Q8) {
+              const int cs = issued % NC;
+              if (issued >= NC && !wait(&code_empty[cs], (uint32_t)(issued / NC - 1) & 1u, abort, a.pv.err)) {
+                ok = false;
+                break;
+              }
+              const int4 cb = s_copy[l], cr = s_rows[l];
+              const int cblk[kSub] = {cb.x, cb.y, cb.z, cb.w}, crow[kSub] = {cr.x, cr.y, cr.z, cr.w};
+              mbar_arrive_expect_tx(&code_full[cs], K::kCodeBytes);
+#pragma unroll
+              for (int u = 0; u < kSub; ++u)
+                tma_3d(sbase + K::kCodeOff + cs * K::kCodeBytes + u * K::kTileBytes, &pool_map, 0, crow[u], 2 * cblk[u], &code_full[cs]);
+              continue;
+            }
             const int st = issued % NS;
             if (issued >= NS && !wait(&kv_empty[st], (uint32_t)(issued / NS - 1) & 1u, abort, a.pv.err)) {
               ok = false;
@@ -418,13 +459,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           }
         }
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-        __syncwarp();
+        issued = __shfl_sync(0xffffffffu, issued, 0);
       }
       done_segment(i);
     }
     if (lane == 0 && *abort) {  // let the copies in flight land before the shared memory is released
-      for (int j = max(0, issued - NS); j < issued; ++j)
-        if (!mbar_wait_bounded(&kv_full[j % NS], (uint32_t)(j / NS) & 1u)) break;
+      constexpr int n = Q8 ? NC : NS;
+      uint64_t* full = Q8 ? code_full : kv_full;
+      for (int j = max(0, issued - n); j < issued; ++j)
+        if (!mbar_wait_bounded(&full[j % n], (uint32_t)(j / n) & 1u)) break;
     }
     __syncwarp();
   } else if (warp == 1 || warp == 2) {
@@ -501,6 +544,73 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       mbar_wait_bounded(&drain[warp - 1], 0);
     }
     __syncwarp();
+  } else if (Q8 && warp >= 12) {
+    // ---- 8-bit: codes to bf16 rows, a warp per tile of the stage -------------------------------
+    const int u = warp - 12;
+    constexpr int kC = D / 16;        // 16-code chunks of a row
+    constexpr int kR = 32 / kC;       // rows a warp covers at a time
+    const int c = lane % kC, r_lane = lane / kC;
+    int stage = 0;
+    bool ok = true;
+    Segment sg;
+    for (int i = 0; ok && next_segment(i, sg); ++i) {
+      const int last = sg.N > 0 ? (sg.N - 1) % sg.C : 0;
+      const int window = min(sg.N, sg.w);
+      for (int jj = 0; jj < sg.stages; ++jj, ++stage) {
+        const int st = stage % NS, cs = stage % NC;
+        ok = __all_sync(0xffffffffu, wait(&code_full[cs], (uint32_t)(stage / NC) & 1u, abort, a.pv.err));
+        if (ok && stage >= NS) ok = __all_sync(0xffffffffu, wait(&kv_empty[st], (uint32_t)(stage / NS - 1) & 1u, abort, a.pv.err));
+        if (!ok) break;
+        const float2 scale = s_scale[stage % kScaleRing][u];
+        const int k = (sg.j0 + jj) * kSub + u;  // tile of the item
+        const int age0 = k < sg.tiles ? tile_age(sg, last, k) : 0;
+        const uint32_t code = sbase + K::kCodeOff + cs * K::kCodeBytes + u * K::kTileBytes;
+        const uint32_t rows = sbase + K::kStageOff + st * K::kStageBytes + u * (kTile * 128);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const float f = kv ? scale.y : scale.x;
+#pragma unroll
+          for (int g = 0; g < kTile / kR; ++g) {
+            const int r = g * kR + r_lane;
+            // rows of D bytes, their 16-byte chunks swizzled with the row (128: by row % 8, 64: by row / 2 % 4)
+            const uint32_t from = code + kv * (kTile * D) + r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+            uint4 w;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(from));
+            if (kv) {
+              int age = age0 - r;
+              if (age < 0) age += sg.C;
+              if (k >= sg.tiles || age >= window) w = make_uint4(0u, 0u, 0u, 0u);
+            }
+            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+            uint32_t out[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t lo, hi;
+              e4m3x4_to_f16(in[e], lo, hi);
+              const float2 x = fmul2(half2_to_float2(lo), make_float2(f, f)), y = fmul2(half2_to_float2(hi), make_float2(f, f));
+              out[2 * e] = pack_bf16(x.x, x.y);
+              out[2 * e + 1] = pack_bf16(y.x, y.y);
+            }
+            // 16 values are chunks 2 c and 2 c + 1 of the bf16 row: column block c / 4, swizzled by the row
+            const uint32_t to = rows + kv * K::kKBytes + (c >> 2) * (kKeys * 128) + r * 128;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t at = to + (((2 * (c & 3) + e) ^ (r & 7)) << 4);
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(out[4 * e]), "r"(out[4 * e + 1]), "r"(out[4 * e + 2]),
+                           "r"(out[4 * e + 3])
+                           : "memory");
+            }
+          }
+        }
+        fence_proxy_async_smem();  // before the products read the rows
+        __syncwarp();
+        if (lane == 0) {
+          arrive(&kv_full[st]);
+          arrive(&code_empty[cs]);
+        }
+      }
+      done_segment(i);
+    }
   } else {
     // ---- softmax of chain x: a thread per row ---------------------------------------------
     const int x = (warp - 4) >> 2;
@@ -774,14 +884,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   }
 }
 
-template <int D, bool SC>
+template <int D, bool SC, bool Q8>
 cudaError_t launch(const SharedArgs& a, const CUtensorMap* pool_map, const CUtensorMap* stage_map, int ctas, cudaStream_t st) {
-  const int smem = Cfg<D>::smem(a.num_prefixes);
-  const cudaError_t e = cudaFuncSetAttribute(shared_tc_kernel<D, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto* kernel = shared_tc_kernel<D, SC, Q8>;
+  const int smem = Cfg<D, Q8>::smem(a.num_prefixes);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Cfg<D, Q8>::kThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -789,7 +900,12 @@ cudaError_t launch(const SharedArgs& a, const CUtensorMap* pool_map, const CUten
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_tc_kernel<D, SC>, *pool_map, *stage_map, a);
+  return cudaLaunchKernelEx(&cfg, kernel, *pool_map, *stage_map, a);
+}
+
+template <int D, bool Q8>
+cudaError_t launch(const SharedArgs& a, const CUtensorMap* pool_map, const CUtensorMap* stage_map, int ctas, cudaStream_t st) {
+  return a.score.on ? launch<D, true, Q8>(a, pool_map, stage_map, ctas, st) : launch<D, false, Q8>(a, pool_map, stage_map, ctas, st);
 }
 
 }  // namespace
@@ -797,9 +913,10 @@ cudaError_t launch(const SharedArgs& a, const CUtensorMap* pool_map, const CUten
 int shared_tc_seqs(int group) { return kM / group; }
 
 cudaError_t launch_shared_tc(const SharedArgs& a, const CUtensorMap* pool_map, const CUtensorMap* stage_map, int ctas, cudaStream_t st) {
+  const bool q8 = a.pv.elem_bytes == 1;
   cudaError_t e = cudaErrorInvalidValue;
-  if (a.pv.head_dim == 128) e = a.score.on ? launch<128, true>(a, pool_map, stage_map, ctas, st) : launch<128, false>(a, pool_map, stage_map, ctas, st);
-  else if (a.pv.head_dim == 64) e = a.score.on ? launch<64, true>(a, pool_map, stage_map, ctas, st) : launch<64, false>(a, pool_map, stage_map, ctas, st);
+  if (a.pv.head_dim == 128) e = q8 ? launch<128, true>(a, pool_map, stage_map, ctas, st) : launch<128, false>(a, pool_map, stage_map, ctas, st);
+  else if (a.pv.head_dim == 64) e = q8 ? launch<64, true>(a, pool_map, stage_map, ctas, st) : launch<64, false>(a, pool_map, stage_map, ctas, st);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

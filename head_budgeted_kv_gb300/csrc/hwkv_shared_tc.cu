@@ -7,7 +7,7 @@
 //
 //   item  = (prefix, KV head, up to two query tiles): a stream of 64-key stages, the ring tiles of the
 //           positions that the sequence with the shortest own part still sees;
-//   line  = all items' stages in a row.  The persistent grid (a CTA per SM) splits it evenly; a CTA walks its range item by
+//   line  = all items in a row, each kGap positions without work and then its stages.  The persistent grid (a CTA per SM) splits it evenly; a CTA walks its range item by
 //           item (segments) and leaves a partial (reference maximum, sum, unnormalised sums) per row and segment.
 //
 // Two query tiles of an item share every stage (each key is staged once for 256 rows).  An item of one tile gives its stages in
@@ -37,7 +37,10 @@ namespace {
 constexpr int kM = 128;                 // query rows per tile (MMA M)
 constexpr int kKeys = 64;               // keys per stage
 constexpr int kSub = kKeys / kTile;     // ring tiles per stage
-constexpr int kMinStages = 4;           // fewest stages of a CTA
+constexpr int kMinStages = 4;           // fewest line positions of a CTA
+// Line positions charged for an item's start: what another segment costs a CTA (its queries, the first stage's
+// latency, the last's and the partial), in stages.
+constexpr int kGap = 5;
 constexpr int kRoleWarps = 11;          // warps that read a segment's descriptor
 
 template <int D, bool Q8>
@@ -286,6 +289,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
       n.stages = (n.tiles + kSub - 1) / kSub;
       return n;
     };
+    auto span_of = [](const Entry& n) { return n.stages > 0 ? (long long)n.stages + kGap : 0ll; };  // line positions of an item
     const int entries = a.num_prefixes * H;
     const int per = (entries + 31) / 32;
     const int e_lo = min(entries, lane * per), e_hi = min(entries, e_lo + per);
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
     int mine_items = 0, sum_items = 0;
     for (int e = e_lo; e < e_hi; ++e) {
       const Entry n = entry_of(e);
-      mine += (long long)n.items * n.stages;
+      mine += n.items * span_of(n);
       mine_items += n.items;
     }
     sum = mine;
@@ -324,6 +328,23 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
     }
     for (int i = 0;; ++i) {
       if (i >= 2 && !__all_sync(0xffffffffu, wait(&seg_empty[i & 1], (uint32_t)((i >> 1) - 1) & 1u, abort, a.pv.err))) break;
+      // the next item with stages in the range: over its gap, or past it
+      int off = 0;
+      long long begin = 0, end = 0;  // the item's stages on the line
+      while (at < t_hi) {
+        while (at >= pre + n.items * span_of(n)) {
+          pre += n.items * span_of(n);
+          items += n.items;
+          n = entry_of(++e);
+        }
+        const int span = n.stages + kGap;
+        off = at - pre <= INT32_MAX ? (int)(at - pre) / span : (int)((at - pre) / span);
+        begin = pre + (long long)off * span + kGap;
+        end = begin + n.stages;
+        at = max(at, begin);
+        if (at < min(end, t_hi)) break;
+        at = end;
+      }
       if (at >= t_hi) {
         if (lane == 0) {
           s_seg[i & 1].stages = 0;
@@ -331,13 +352,6 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
         }
         break;
       }
-      while (at >= pre + (long long)n.items * n.stages) {
-        pre += (long long)n.items * n.stages;
-        items += n.items;
-        n = entry_of(++e);
-      }
-      const int off = at - pre <= INT32_MAX ? (int)(at - pre) / n.stages : (int)((at - pre) / n.stages);  // the entry's item
-      const long long begin = pre + (long long)off * n.stages, end = begin + n.stages;
       Segment sg;
       sg.f = n.f, sg.h = n.h, sg.N = s_len[n.f], sg.w = a.g.window[n.h], sg.C = n.C, sg.first_tile = n.first_tile, sg.tiles = n.tiles;
       sg.j0 = (int)(at - begin);
@@ -768,15 +782,16 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
             mx = fmaxf(mx, sv[c]);
           }
         }
-        // the reference moves only when a maximum passes it by 2^8, so O is rarely touched
+        // the reference moves only when a maximum passes it by 2^8, so O is rarely touched (a row that has seen no
+        // key yet has nothing in O: rows of other reaches would otherwise touch it stage after stage)
         const float m_new = fmaxf(m_ref, mx);
         const bool grow = m_new > m_ref + 8.f;
-        if (jj > 0 && __any_sync(0xffffffffu, grow)) {
+        if (jj > 0 && __any_sync(0xffffffffu, grow && m_ref != kNegInf)) {
           const int before = done - 1;  // O may be rescaled once the last P . V into it has completed
           ok = __all_sync(0xffffffffu, wait(&o_done[x][before & 1], (uint32_t)(before >> 1) & 1u, abort, a.pv.err));
           if (!ok) break;
           tc_fence_after_sync();
-          const float f = grow ? ex2(m_ref - m_new) : 1.f;
+          const float f = grow && m_ref != kNegInf ? ex2(m_ref - m_new) : 1.f;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];

@@ -111,6 +111,14 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   }
 }
 
+// One lane of the warp.  (A branch on it, unlike one on lane == 0, is known to run a single thread, which leaves
+// descriptors in uniform registers.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // bits lo .. hi (inclusive, clamped to 0 .. 15) of a 16-key tile
 __device__ __forceinline__ uint32_t bits16(int lo, int hi) {
   lo = max(lo, 0);
@@ -496,7 +504,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
     bool ok = true;
     Segment sg;
     for (int i = 0; ok && next_segment(i, sg); ++i) {
-      if (lane == 0) {
+      if (elect_one()) {
         for (int jj = 0; ok && jj < sg.stages; ++jj, ++stage) {
           const int st = stage % NS;
           if (warp == 1) {
@@ -550,10 +558,10 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
           if (warp == 2) umma_commit(&kv_empty[st]);  // (its S was complete before P was written)
         }
       }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      ok = __all_sync(0xffffffffu, ok);
       done_segment(i);
     }
-    if (lane == 0) {
+    if (elect_one()) {
       umma_commit(&drain[warp - 1]);  // all that this lane issued completes before tensor memory is freed
       mbar_wait_bounded(&drain[warp - 1], 0);
     }

@@ -14,8 +14,8 @@
 // turn to two chains of the same rows, so the S -> softmax -> P.V latency of one hides behind the other's; at a
 // segment's end their states are joined out of tensor memory.
 //
-// Warp roles: 0 TMA producer; 1 issues S = Q K^T, 2 issues O += P V; 3 plans: segments, their sequences, and the
-// records the join reads; 4-7 softmax of tile (or chain) 0, 8-11 of 1, a thread per row.  Warps without a live row only keep
+// Warp roles: 0 plans (segments, their sequences, and the records the join reads) and brings the keys by TMA; 1 and 3
+// issue S = Q K^T of chain 0 and 1, 2 issues O += P V of both; 4-7 softmax of tile (or chain) 0, 8-11 of 1, a thread per row.  Warps without a live row only keep
 // the barriers in step.  Segments are handed out through two descriptors in shared memory, so the
 // producer runs into the next one while the last is finished.
 //
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
   constexpr int kScaleRing = Q8 ? 64 : 1;  // scales (K, V) of the stages' tiles, planned up to 32 stages ahead
   __shared__ float2 s_scale[kScaleRing][kSub];
   // per chain x and parity b of its stages (a phase is one stage of that parity, so no waiter falls two behind)
-  __shared__ __align__(8) uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2], drain[2];
+  __shared__ __align__(8) uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2], drain[3];
   __shared__ __align__(8) uint64_t seg_full[2], seg_empty[2];
   __shared__ __align__(8) uint64_t ml_full, o_read;  // two chains of the same rows: states published, O of both read
   __shared__ float2 s_ml[2][kM];
@@ -224,10 +224,10 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
         mbar_init(&o_done[x][b], 1);
       }
       mbar_init(&q_full[x], 4);
-      mbar_init(&drain[x], 1);
       mbar_init(&seg_full[x], 1);
       mbar_init(&seg_empty[x], kRoleWarps + (Q8 ? 4 : 0));
     }
+    for (int i = 0; i < 3; ++i) mbar_init(&drain[i], 1);
     mbar_init(&ml_full, 8);
     mbar_init(&o_read, 8);
     s_abort = 0;
@@ -280,8 +280,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
     if (lane == 0) arrive(&seg_empty[i & 1]);
   };
 
-  if (warp == 3) {
-    // ---- planner ------------------------------------------------------------------------
+  if (warp == 0) {
+    // ---- plan and TMA producer (whole warp) ----------------------------------------------------
     // The line: entries (prefix, head) of items x stages, some consecutive ones per lane.
     struct Entry {
       int f, h, C, first_tile, tiles, stages, items;
@@ -334,7 +334,9 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
       e = who * per;
       n = entry_of(e);
     }
-    for (int i = 0;; ++i) {
+    int issued = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
       if (i >= 2 && !__all_sync(0xffffffffu, wait(&seg_empty[i & 1], (uint32_t)((i >> 1) - 1) & 1u, abort, a.pv.err))) break;
       // the next item with stages in the range: over its gap, or past it
       int off = 0;
@@ -381,14 +383,6 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
         }
       }
       at += sg.stages;
-      __syncwarp();
-    }
-  } else if (warp == 0) {
-    // ---- TMA producer (whole warp) ------------------------------------------------------
-    int issued = 0;
-    bool ok = true;
-    Segment sg;
-    for (int i = 0; ok && next_segment(i, sg); ++i) {
       const int32_t* tbl = a.pv.tbl + a.g.tbl_base + (int64_t)sg.f * a.g.tbl_seq_stride + a.g.nblk_prefix[sg.h];
       const int C16 = sg.C >> 4;
       // 32 stages planned at a time, one per lane (table look-ups in parallel); lane 0 issues the copies
@@ -483,7 +477,6 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         issued = __shfl_sync(0xffffffffu, issued, 0);
       }
-      done_segment(i);
     }
     if (lane == 0 && *abort) {  // let the copies in flight land before the shared memory is released
       constexpr int n = Q8 ? NC : NS;
@@ -492,73 +485,76 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
         if (!mbar_wait_bounded(&full[j % n], (uint32_t)(j / n) & 1u)) break;
     }
     __syncwarp();
-  } else if (warp == 1 || warp == 2) {
-    // ---- MMA issuers: warp 1 the S of every stage, warp 2 the P . V ---------------------------
+  } else if (warp < 4) {
+    // ---- MMA issuers: warps 1 and 3 the S of chain 0 and 1, warp 2 the P . V of both ------------------
     constexpr uint32_t idS = umma_idesc_bf16(kM, kKeys, false, false);
     constexpr uint32_t idO = umma_idesc_bf16(kM, D, false, true);
     const uint64_t dq = umma_desc_sw128(sbase, 16, 1024);
     const uint64_t dk = umma_desc_sw128(sbase + K::kStageOff, 16, 1024);
     const uint64_t dv = umma_desc_sw128(sbase + K::kStageOff + K::kKBytes, kKeys * 128, 1024);
-    int stage = 0;          // stages of this CTA so far
-    int done0 = 0, done1 = 0, qs0 = 0, qs1 = 0;  // stages of each chain, segments of each chain
+    int stage = 0;              // stages of this CTA so far
+    int done[2] = {0, 0};       // stages of each chain (an S issuer: of its own)
+    int queries = 0;            // segments of an S issuer's chain
     bool ok = true;
     Segment sg;
     for (int i = 0; ok && next_segment(i, sg); ++i) {
       if (elect_one()) {
-        for (int jj = 0; ok && jj < sg.stages; ++jj, ++stage) {
-          const int st = stage % NS;
-          if (warp == 1) {
-            ok = wait(&kv_full[st], (uint32_t)(stage / NS) & 1u, abort, a.pv.err);
+        if (warp != 2) {
+          // S of each of the chain's stages into its buffers in turn, once the P . V of the stage two before, which read
+          // the P there, has completed
+          const int x = warp >> 1;
+          int n = done[0];
+          for (int jj = sg.one ? x : 0; ok && jj < sg.stages; jj += sg.one ? 2 : 1, ++n) {
+            const int g = stage + jj, st = g % NS, b = n & 1;
+            if (jj < 1 + sg.one) {  // the segment's first
+              ok = wait(&q_full[x], (uint32_t)queries & 1u, abort, a.pv.err);
+              if (!ok) break;
+              ++queries;
+            }
+            if (n >= 2) {
+              ok = wait(&o_done[x][b], (uint32_t)((n - 2) >> 1) & 1u, abort, a.pv.err);
+              if (!ok) break;
+            }
+            ok = wait(&kv_full[st], (uint32_t)(g / NS) & 1u, abort, a.pv.err);
             if (!ok) break;
             tc_fence_after_sync();
+            const uint64_t dqx = dq + (uint64_t)((x * K::kQBytes) >> 4);
+            const uint64_t dks = dk + (uint64_t)((st * K::kStageBytes) >> 4);
+            const uint32_t to = tmem + (2 * x + b) * kKeys;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              umma_bf16(to, dqx + (uint64_t)(((k >> 2) * (kM * 128) + (k & 3) * 32) >> 4),
+                        dks + (uint64_t)(((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4), idS, k > 0 ? 1u : 0u);
+            umma_commit(&s_full[x][b]);
           }
+          done[0] = n;
+        } else {
+          // O += P . V once the softmax has written P into tensor memory
+          for (int jj = 0; ok && jj < sg.stages; ++jj) {
+            const int st = (stage + jj) % NS;
+            const uint64_t dvs = dv + (uint64_t)((st * K::kStageBytes) >> 4);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (sg.one && (jj & 1) != x) continue;
-            int& done = x ? done1 : done0;
-            const int b = done & 1;
-            const bool first = sg.one ? jj < 2 : jj == 0;  // the chain's first stage of the segment
-            if (warp == 1) {
-              // S of this stage into buffer b, once the P . V of the chain's stage two before, which read the P there,
-              // has completed
-              if (first) {
-                int& qs = x ? qs1 : qs0;
-                ok = wait(&q_full[x], (uint32_t)qs & 1u, abort, a.pv.err);
-                ++qs;
-                if (!ok) break;
-                tc_fence_after_sync();
-              }
-              if (done >= 2) {
-                ok = wait(&o_done[x][b], (uint32_t)((done - 2) >> 1) & 1u, abort, a.pv.err);
-                if (!ok) break;
-                tc_fence_after_sync();
-              }
-              const uint64_t dks = dk + (uint64_t)((st * K::kStageBytes) >> 4);
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k)
-                umma_bf16(tmem + (2 * x + b) * kKeys, dq + (uint64_t)((x * K::kQBytes + (k >> 2) * (kM * 128) + (k & 3) * 32) >> 4),
-                          dks + (uint64_t)(((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4), idS, k > 0 ? 1u : 0u);
-              umma_commit(&s_full[x][b]);
-            } else {
-              // O += P . V once the softmax has written P into tensor memory
-              ok = wait(&p_full[x][b], (uint32_t)(done >> 1) & 1u, abort, a.pv.err);
+            for (int x = 0; x < 2; ++x) {
+              if (sg.one && (jj & 1) != x) continue;
+              const int b = done[x] & 1;
+              ok = wait(&p_full[x][b], (uint32_t)(done[x] >> 1) & 1u, abort, a.pv.err);
               if (!ok) break;
               tc_fence_after_sync();
-              const uint64_t dvs = dv + (uint64_t)((st * K::kStageBytes) >> 4);
               const uint32_t pcol = tmem + (2 * x + b) * kKeys;
+              const uint32_t add = jj < 1 + sg.one ? 0u : 1u;  // 0: the segment's first
 #pragma unroll
               for (int k = 0; k < kKeys / 16; ++k)
-                umma_bf16_tmem_a(tmem + K::kColO + x * D, pcol + k * 8, dvs + (uint64_t)((k * 16 * 128) >> 4), idO,
-                                 (!first || k > 0) ? 1u : 0u);
+                umma_bf16_tmem_a(tmem + K::kColO + x * D, pcol + k * 8, dvs + (uint64_t)((k * 16 * 128) >> 4), idO, k > 0 ? 1u : add);
               umma_commit(&o_done[x][b]);
+              ++done[x];
             }
-            ++done;
+            if (!ok) break;
+            umma_commit(&kv_empty[st]);  // (its S was complete before P was written)
           }
-          if (!ok) break;
-          if (warp == 2) umma_commit(&kv_empty[st]);  // (its S was complete before P was written)
         }
       }
       ok = __all_sync(0xffffffffu, ok);
+      stage += sg.stages;
       done_segment(i);
     }
     if (elect_one()) {

@@ -15,6 +15,11 @@ constexpr int kFlatMerge = 24;  // most contributors one CTA merges directly
 // publishing a partial, the next group's q), so CTAs with boundaries do not end last.
 constexpr int kGapTiles = 24;
 
+// The end of a CTA of an open instance (hwkv_decode_sk.cuh)
+__device__ __forceinline__ void open_end() {
+  if (blockIdx.x == gridDim.x - 1) griddep_wait();
+}
+
 // The threads that merge: the whole CTA, or its first N threads (those that consumed the tiles)
 // while a producer warp runs on.  Thread indices count from 0 in both.  A whole CTA's number is read at
 // run time: given the constant the compiler unrolls the merges' loops, and the longer kernel costs batch 1 1%.

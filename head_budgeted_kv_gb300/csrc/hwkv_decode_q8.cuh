@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
     }
   }
   if (!has_range) {
-    if constexpr (kOpen) griddep_wait();
+    if constexpr (kOpen) open_end();
     return;
   }
 
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kCtas)
   }
   if (ms.stuck0 >= 0) mbar_wait_bounded(&merge_bar[0], (uint32_t)ms.stuck0);
   if (ms.stuck1 >= 0) mbar_wait_bounded(&merge_bar[1], (uint32_t)ms.stuck1);
-  if constexpr (kOpen) griddep_wait();
+  if constexpr (kOpen) open_end();
 }
 
 template <int D, int GP, bool SC, bool kOpen = false>

@@ -65,8 +65,9 @@ __host__ __device__ constexpr int sk_min_ctas() {
 }
 
 // kOpen: the results stay open, each group's (m, l) and accumulators to be joined with those of other keys.
-// Such a grid needs nothing of the grid ahead of it, which starts it only once all before has completed: it
-// waits for that grid at its end alone, so that what follows this grid follows both.
+// Such a grid needs nothing of the grid ahead of it, which starts it only once all before has completed: its last
+// CTA alone waits for that grid, at its end, so that what follows this grid follows both (and the others leave
+// their SMs to those still to come).
 template <typename Elem, int D, int GP, int NS, bool SC, bool kOpen>
 __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
     decode_sk_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ DecodeArgs a) {
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
     }
   }
   if (!has_range) {
-    if constexpr (kOpen) griddep_wait();
+    if constexpr (kOpen) open_end();
     return;
   }
 
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(kWarps * 32, sk_min_ctas<Elem, D>())
   }
   if (ms.stuck0 >= 0) mbar_wait_bounded(&merge_bar[0], (uint32_t)ms.stuck0);
   if (ms.stuck1 >= 0) mbar_wait_bounded(&merge_bar[1], (uint32_t)ms.stuck1);
-  if constexpr (kOpen) griddep_wait();
+  if constexpr (kOpen) open_end();
 }
 
 template <typename T, int D, int GP, int NS>

@@ -1070,6 +1070,7 @@ int score_args(const hwkv_score_t& sc, ScoreArgs* out) {
 struct DecodeCall {
   DecodeArgs a;
   bool tc = false;
+  int ctas = 0;  // the stream-K kernel's grid
   const void* k_new = nullptr;
   const void* v_new = nullptr;
 };
@@ -1137,6 +1138,7 @@ int prepare_decode(hwkv_pool_t p, int layer, const void* q, int q_heads, hwkv_sc
   a.split_tokens = lp.split;
   std::memcpy(a.chunk_prefix, lp.chunk_prefix, sizeof a.chunk_prefix);
   call->tc = tc;
+  call->ctas = tc ? tc_workers(p, G) : 0;
   call->k_new = len_add ? k_new : nullptr;
   call->v_new = len_add ? v_new : nullptr;
   return HWKV_OK;
@@ -1149,8 +1151,7 @@ int launch_decode(hwkv_pool_t p, int layer, DecodeCall& call, cudaStream_t st) {
   if (call.tc) {
     a.k_new = call.k_new;  // appended inside the kernel
     a.v_new = call.v_new;
-    HWKV_CUDA_TRY(a.open_acc ? launch_decode_open(a, &p->tmap, tc_workers(p, a.group), st)
-                             : launch_decode_tc(a, &p->tmap, tc_workers(p, a.group), st),
+    HWKV_CUDA_TRY(a.open_acc ? launch_decode_open(a, &p->tmap, call.ctas, st) : launch_decode_tc(a, &p->tmap, call.ctas, st),
                   "decode launch");
     return HWKV_OK;
   }
@@ -1185,6 +1186,31 @@ int decode_common(hwkv_pool_t p, int layer, const void* q, int q_heads, hwkv_sco
 
 // Which kernel reads the prefixes' keys: the tensor cores' where its tiles fit.
 bool shared_tc(const hwkv_pool* prefix) { return prefix->g.dtype == HWKV_E4M3 ? prefix->has_tmap : prefill_eligible(prefix); }
+
+// Times of the two kernels of a decode behind shared prefixes that run side by side: of a 64-key stage of the prefixes on an SM, and of
+// a CTA of the own parts, one of those that share an SM, with its start and per 16-token tile (measured, see pick_ctas).
+struct SharedTimes {
+  int stage_ns, base_ns, tile_ns, per_sm;
+};
+
+SharedTimes shared_times(const hwkv_pool* p, const hwkv_pool* prefix, int group, bool scored) {
+  SharedTimes t;
+  const bool wide = p->g.head_dim == 128, q8 = p->g.dtype == HWKV_E4M3;
+  t.stage_ns = prefix->g.dtype == HWKV_E4M3 ? (wide ? 1150 : 800) : (wide ? 950 : 700);
+  if (scored) t.stage_ns = t.stage_ns * 2;
+  t.per_sm = std::max(1, p->ctas_per_sm[decode_tc_pad_index(group)]);
+  t.base_ns = q8 ? 18000 : (wide ? 12500 : 16000);
+  t.tile_ns = q8 ? (wide ? 190 : 150) : (wide ? 270 : 220);
+  return t;
+}
+
+// CTAs of the own parts' kernel: as for a decode, but no more than own windows of four tiles each keep busy.
+int open_workers(const hwkv_pool* p, int layer, int group) {
+  const Geometry& g = p->g;
+  int64_t tiles = 0;
+  for (int h = 0; h < g.kv_heads; ++h) tiles += (g.windows[(size_t)layer * g.kv_heads + h] + 15) / 16;
+  return (int)std::min<int64_t>(tc_workers(p, group), std::max<int64_t>(16, tiles * g.num_seqs / 4));
+}
 
 // How the keys of the prefixes are split on the CUDA cores: ring slots per CTA for about six CTAs per SM over
 // the sequences' tiles, and the chunks of each head.
@@ -1342,6 +1368,15 @@ int hwkv_decode_attn_shared(hwkv_pool_t p, hwkv_pool_t prefix, int layer, const 
     a.tc = 1;
     a.bs_log2 = log2_of(prefix->g.block_size);
     a.stage_tb = prefix->stage_tb;
+    const SharedTimes times = shared_times(p, prefix, G, a.score.on);
+    a.stage_ns = times.stage_ns;
+    if (call.tc) {
+      a.own_ctas = call.ctas = open_workers(p, layer, G);
+      a.own_per_sm = times.per_sm;
+      a.own_base_ns = times.base_ns;
+      a.own_tile_ns = times.tile_ns;
+      std::memcpy(a.own_window, call.a.g.window, sizeof a.own_window);
+    }
     HWKV_CUDA_TRY(launch_shared_tc(a, &prefix->tmap, &prefix->stage_map, p->num_sms, st), "shared prefix launch");
   } else {
     const SharedPlan sp = plan_shared(p, prefix, layer, G);

@@ -161,32 +161,31 @@ constexpr int simt_smem() {
 }
 
 // The join, a CTA per (sequence, KV head): out = sum_i acc_i 2^(m_i - M) / sum_i l_i 2^(m_i - M) over the head's own
-// partial and its prefix's, M = max_i m_i; nothing to attend to gives zeros.  A warp takes a head's maxima and
-// sums, a part per lane, and leaves the parts' weights in shared memory; then every thread sums four columns of a head
-// over every kSplit'th part, kAhead loads in flight, and the kSplit sums meet in shared memory.  The order of
-// all sums is fixed.
-constexpr int kJoinThreads = 256;
+// partial and its prefix's, M = max_i m_i; nothing to attend to gives zeros.  A thread sums four columns of a head over every
+// kSplit'th part, the states and sums of kAhead parts on their way at once; where a head has more
+// threads than columns, their sums meet in shared memory.  The order of all sums is fixed.
+constexpr int kJoinThreads = 128;
 constexpr int kAhead = 8;
-constexpr int kJoinParts = 64;  // parts whose weights are held at a time
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_constant__ SharedArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 6) shared_join_kernel(const __grid_constant__ SharedArgs a) {
   constexpr int kV = D / 4;  // float4 columns of a head
-  __shared__ float s_w[kJoinParts][kMaxGroup];   // weight of part and head
-  __shared__ float s_m[kMaxGroup], s_l[kMaxGroup];
   __shared__ float4 s_acc[kJoinThreads];
-  griddep_wait();
+  __shared__ float2 s_ml[kJoinThreads];
   const int H = a.pv.kv_heads, G = a.group;
   const int s = (int)blockIdx.x / H, h = (int)blockIdx.x - s * H;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * G;  // the first of the CTA's rows
+  const int cols = G * kV;
+  const int split = max(1, kJoinThreads / cols);  // threads of a column
+  const int e0 = split > 1 ? (int)threadIdx.x % cols : (int)threadIdx.x, k0 = split > 1 ? (int)threadIdx.x / cols : 0;
+  griddep_wait();
   const int f = prefix_of(a, s, threadIdx.x == 0 && h == 0);
   int64_t part0 = 0, step = 0;  // partial rows of the first head
   int parts = 0;
   if (f >= 0 && a.tc) {
     // a record is there for every row that sees a key of the prefix
+    const int4 rec = a.rec[blockIdx.x];
     if (min(prefix_len(a, f), a.g.window[h] - min(a.g.window[h], shared_len(a, s))) > 0) {
-      const int4 rec = a.rec[blockIdx.x];
       part0 = (int64_t)rec.x * a.chain_rows + rec.w;
       step = (int64_t)rec.y * a.chain_rows;
       parts = rec.z;
@@ -197,79 +196,79 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_
     step = G;
     parts = a.chunk_prefix[h + 1] - a.chunk_prefix[h];
   }
-  const float2* own_ml = reinterpret_cast<const float2*>(a.own_ml) + row;
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + part0;
-  // maxima and sums of the heads
-  for (int g = warp; g < G; g += kJoinThreads / 32) {
-    float2 own = own_ml[g];
-    own.x += a.own_shift;
-    float M = own.x;
-    for (int i = lane; i < parts; i += 32) M = fmaxf(M, ml[i * step + g].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f;
-    for (int i = lane; i < parts; i += 32) {
-      const float2 e = ml[i * step + g];
-      const float x = e.x == kNegInf ? 0.f : ex2(e.x - M);
-      L = fmaf(e.y, x, L);
-      if (i < kJoinParts) s_w[i][g] = x;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const float x = own.x == kNegInf ? 0.f : ex2(own.x - M);
-    if (lane == 0) {
-      s_m[g] = M;
-      s_l[g] = fmaf(own.y, x, L);
-    }
-  }
-  __syncthreads();
-  const int cols = G * kV;
-  const int split = max(1, kJoinThreads / cols);  // threads of a column
-  const int e0 = (int)threadIdx.x % cols, k0 = (int)threadIdx.x / cols;
-  for (int c0 = 0; c0 < cols; c0 += kJoinThreads) {  // more than one pass: groups of more heads than threads hold
+  for (int c0 = 0; c0 < cols; c0 += kJoinThreads) {  // more than one pass: heads of more columns than threads
     const int e = c0 + e0;
     const bool on = e < cols && k0 < split;
     const int g = on ? e / kV : 0, d = on ? e % kV : 0;
+    float M = kNegInf, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float4 v, float x) {
+    // adds a part of state e and sums v, both at a reference of M already
+    auto add = [&](float2 e, float4 v) {
+      if (e.x == kNegInf) return;  // a part without a key: its sums may be anything
+      const float x = ex2(e.x - M);
+      L = fmaf(e.y, x, L);
       acc.x = fmaf(v.x, x, acc.x);
       acc.y = fmaf(v.y, x, acc.y);
       acc.z = fmaf(v.z, x, acc.z);
       acc.w = fmaf(v.w, x, acc.w);
     };
-    if (on && k0 == 0) {
-      const float m = own_ml[g].x + a.own_shift;
-      const float x = m == kNegInf ? 0.f : ex2(m - s_m[g]);
-      if (x != 0.f) add(reinterpret_cast<const float4*>(a.own_acc + (row + g) * D)[d], x);
-    }
-    for (int i0 = 0; i0 < parts; i0 += kAhead * split) {
-      float4 v[kAhead];
-      float x[kAhead];
+    auto raise = [&](float m) {
+      if (m <= M) return;
+      const float x = M == kNegInf ? 0.f : ex2(M - m);
+      L *= x;
+      acc = make_float4(acc.x * x, acc.y * x, acc.z * x, acc.w * x);
+      M = m;
+    };
+    if (on) {
+      const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + part0 + g;
+      const float4* po = reinterpret_cast<const float4*>(a.part_o + (part0 + g) * D) + d;
+      float2 own = make_float2(kNegInf, 0.f);
+      float4 own_v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 == 0) {
+        own = reinterpret_cast<const float2*>(a.own_ml)[row + g];
+        own_v = reinterpret_cast<const float4*>(a.own_acc + (row + g) * D)[d];
+        own.x += a.own_shift;
+      }
+      for (int i0 = k0; i0 < parts || i0 == k0; i0 += kAhead * split) {
+        float2 st[kAhead];
+        float4 v[kAhead];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int i = i0 + j * split + k0;
-        x[j] = 0.f;
-        if (on && i < parts) {
-          if (i < kJoinParts) x[j] = s_w[i][g];
-          else x[j] = ml[i * step + g].x == kNegInf ? 0.f : ex2(ml[i * step + g].x - s_m[g]);
-          // (a partial of no weight may hold anything)
-          if (x[j] != 0.f) v[j] = reinterpret_cast<const float4*>(a.part_o + (part0 + i * step + g) * D)[d];
+        for (int j = 0; j < kAhead; ++j) {
+          const int i = i0 + j * split;
+          st[j] = make_float2(kNegInf, 0.f);
+          if (i < parts) {
+            st[j] = ml[i * step];
+            v[j] = po[i * step * kV];
+          }
+        }
+        float m = kNegInf;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) m = fmaxf(m, st[j].x);
+        if (i0 == k0) m = fmaxf(m, own.x);
+        raise(m);
+        if (i0 == k0) add(own, own_v);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) add(st[j], v[j]);
+      }
+    }
+    if (split > 1) {
+      s_acc[threadIdx.x] = acc;
+      s_ml[threadIdx.x] = make_float2(M, L);
+      __syncthreads();
+      if (on && k0 == 0) {
+        for (int k = 1; k < split; ++k) {
+          const float2 e2 = s_ml[k * cols + e0];
+          raise(e2.x);
+          add(e2, s_acc[k * cols + e0]);
         }
       }
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        if (x[j] != 0.f) add(v[j], x[j]);
     }
-    s_acc[threadIdx.x] = acc;
-    __syncthreads();
     if (on && k0 == 0) {
-      for (int k = 1; k < split; ++k) add(s_acc[k * cols + e0], 1.f);
-      const float inv = s_l[g] > 0.f ? 1.f / s_l[g] : 0.f;
+      const float inv = L > 0.f ? 1.f / L : 0.f;
       T* out = static_cast<T*>(a.out) + (row + g) * D + 4 * d;
       if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(out) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       else *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     }
-    __syncthreads();
   }
 }
 

@@ -10,6 +10,9 @@
 //   line  = all items in a row, each kGap positions without work and then its stages.  The persistent grid (a CTA per SM) splits it evenly; a CTA walks its range item by
 //           item (segments) and leaves a partial (reference maximum, sum, unnormalised sums) per row and segment.
 //
+// The own parts' kernel needs nothing of this one and starts on the SMs that it leaves: how many CTAs are used is chosen from the
+// lengths, so that the two run side by side and end together (pick_ctas).
+//
 // Two query tiles of an item share every stage (each key is staged once for 256 rows).  An item of one tile gives its stages in
 // turn to two chains of the same rows, so the S -> softmax -> P.V latency of one hides behind the other's; at a
 // segment's end their states are joined out of tensor memory.
@@ -148,6 +151,27 @@ __device__ __forceinline__ int line_cta(long long t, long long T, int n) {
   return T < (1 << 22) ? (int)((((uint32_t)t + 1u) * (uint32_t)n - 1u) / (uint32_t)T) : (int)(((t + 1) * n - 1) / T);
 }
 
+// CTAs for T line positions beside the own parts' kernel of `tiles` tiles in `groups` groups: the number that lets the later of the two
+// end first, by a model of both in ns.  Here 8 us and a stage per position; there a CTA takes its tiles, 4.8 us a group and 12 to 18 us
+// (fitted to that kernel alone on 16 to 288 CTAs: within 10% from 20 to 500 us), 5 of them once, and its CTAs go through the SMs left
+// to them in waves (lane w tries w + 1 of them, with two SMs to spare: a straggler is another wave; the last lane tries all SMs here
+// and the own parts after).  In integers: every CTA must choose alike.
+__device__ __forceinline__ int pick_ctas(const SharedArgs& a, long long T, uint32_t tiles, uint32_t groups, int sms, int lane) {
+  const long long each = a.own_base_ns - 5000 + ((long long)tiles * a.own_tile_ns + (long long)groups * 4800) / a.own_ctas;
+  const int waves = lane + 1;
+  const int slots = (a.own_ctas + waves - 1) / waves, theirs = (slots + a.own_per_sm - 1) / a.own_per_sm + 2;
+  const int mine = lane == 31 ? sms : sms - theirs;
+  long long time = (long long)1 << 60;
+  if (mine >= 1) {
+    const long long here = 8000 + T * a.stage_ns / mine;
+    time = lane == 31 ? here + each + 8000 : max(here, waves * each + 5000);
+  }
+  long long best = time;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+  return __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, time == best)) - 1);
+}
+
 // The ring tiles of the newest `need` of N tokens: first tile and their number.
 __device__ __forceinline__ void need_tiles(int N, int need, int C, int& first_tile, int& tiles) {
   first_tile = tiles = 0;
@@ -199,6 +223,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
   __shared__ int2 s_box[32];   // ... or the one box that holds them: first block (-1: none) and row in it
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ uint32_t s_own, s_groups;  // tiles of the own parts, (sequence, head) groups that have some
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int H = a.pv.kv_heads, G = a.group, bs = a.pv.block_size;
@@ -231,6 +256,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
     mbar_init(&ml_full, 8);
     mbar_init(&o_read, 8);
     s_abort = 0;
+    s_own = s_groups = 0u;
     fence_mbar_init();
     prefetch_tensormap(&pool_map);
     prefetch_tensormap(&stage_map);
@@ -244,9 +270,9 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
     s_short[f] = INT32_MAX;
   }
   // the first sequence's and prefix's loads are on their way while the counts are cleared
-  const int s_own = (int)threadIdx.x < a.num_seqs ? (int)threadIdx.x : -1;
-  int f_own = s_own >= 0 ? a.prefix_of[s_own] : -1;
-  const int n_own = s_own >= 0 ? shared_len(a, s_own) : 0;
+  const int s_own_seq = (int)threadIdx.x < a.num_seqs ? (int)threadIdx.x : -1;
+  const int f_own = s_own_seq >= 0 ? a.prefix_of[s_own_seq] : -1;
+  const int n_own = s_own_seq >= 0 ? shared_len(a, s_own_seq) : 0;
   for (int f = threadIdx.x; f < a.num_prefixes; f += kThreads) {
     const int N = a.prefix_lens[f];
     if (N < 0 && cta == 0) atomicOr(a.pv.err, HWKV_DEVERR_NEG_LENGTH);
@@ -259,8 +285,25 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
     atomicAdd(&s_count[f], 1);
     atomicMin(&s_short[f], n);
   };
-  count(f_own, n_own);
-  for (int s = threadIdx.x + kThreads; s < a.num_seqs; s += kThreads) count(a.prefix_of[s], shared_len(a, s));
+  uint32_t own_tiles = 0u, own_groups = 0u;
+  auto own_work = [&](int n) {
+    if (n <= 0 || a.own_ctas == 0) return;
+    for (int h = 0; h < H; ++h) own_tiles += (uint32_t)((min(n, a.own_window[h]) + 15) >> 4);
+    own_groups += (uint32_t)H;
+  };
+  if (s_own_seq >= 0) {
+    count(f_own, n_own);
+    own_work(n_own);
+  }
+  for (int s = threadIdx.x + kThreads; s < a.num_seqs; s += kThreads) {
+    const int n = shared_len(a, s);
+    count(a.prefix_of[s], n);
+    own_work(n);
+  }
+  if (own_tiles > 0u) {
+    atomicAdd(&s_own, own_tiles);
+    atomicAdd(&s_groups, own_groups);
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -320,7 +363,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
       }
     }
     const long long T = __shfl_sync(0xffffffffu, sum, 31);
-    const int ctas = T < (long long)kMinStages * gridDim.x ? max(1, (int)T / kMinStages) : (int)gridDim.x;
+    const int share = T > 0 && s_own > 0u ? pick_ctas(a, T, s_own, s_groups, (int)gridDim.x, lane) : (int)gridDim.x;
+    const int ctas = T < (long long)kMinStages * share ? max(1, (int)T / kMinStages) : share;
     long long at = 0, t_hi = 0, pre = 0;
     int e = 0, items = 0;
     Entry n{};
@@ -757,14 +801,19 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
             }
           }
           if (a.score.slopes != nullptr) {
+            // less slope * distance: a tile's keys are one position apart, so each gets slope * k and its tile's first distance
 #pragma unroll
-            for (int u = 0; u < kSub; ++u)
+            for (int u = 0; u < kSub; ++u) {
+              const float first = -slope * (float)((uint32_t)age[u] + (uint32_t)own);
 #pragma unroll
-              for (int k = 0; k < kTile; ++k) {
-                int d = age[u] - k;
-                if (d < 0) d += sg.C;
-                sv[u * kTile + k] = fmaf(-slope, (float)((uint32_t)d + (uint32_t)own), sv[u * kTile + k]);
+              for (int k = 0; k < kTile; ++k) sv[u * kTile + k] = fmaf(slope, (float)k, sv[u * kTile + k] + first);
+              if (age[u] < kTile - 1) {  // past the newest slot come the oldest, a ring away
+                const float wrap = -slope * (float)sg.C;
+#pragma unroll
+                for (int k = 1; k < kTile; ++k)
+                  if (k > age[u]) sv[u * kTile + k] += wrap;
               }
+            }
           }
         }
         if (!clean) {

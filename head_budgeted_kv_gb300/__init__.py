@@ -59,6 +59,10 @@ def rope_table(head_dim: int, rot_dim: Optional[int] = None, base: float = 10000
                            beta_slow)
 
 
+# The check alone, without the one of torch.cuda that a device is initialised: a pool is on one.
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+
+
 class Pool:
     """A per-head paged KV pool on the current CUDA device.
 
@@ -191,15 +195,18 @@ class Pool:
             out = torch.empty_like(q)
         if (k_new is None) != (v_new is None):
             raise ValueError("k_new and v_new go together")
-        if out.shape != q.shape:
+        shape = q.shape
+        if out is not q and out.shape != shape:
             raise ValueError("out must match q")
-        for t, heads in ((q, q.shape[1]), (out, q.shape[1]), (k_new, self.kv_heads), (v_new, self.kv_heads)):
-            if t is not None and (self._check_rows(t, "q, out, k_new and v_new") != heads or t.dim() != 3):
-                raise ValueError("q, out, k_new and v_new must be [B][heads][D]")
+        self._check_row(q, "q", shape[-2])
+        self._check_row(out, "out", shape[-2])
+        if k_new is not None:
+            self._check_row(k_new, "k_new", self.kv_heads)
+            self._check_row(v_new, "v_new", self.kv_heads)
         if not (self._is_counts(lens) and self._is_counts(prefix_of) and prefix._is_counts(prefix_lens)):
             raise ValueError(f"lens and prefix_of must hold {self.num_seqs} values, prefix_lens {prefix.num_seqs}, in a row on "
                              f"{self.buffer.device}")
-        if torch.cuda.is_current_stream_capturing():
+        if _capturing():
             self._shared_captured = True
         args = (layer, q, binding.score(scale, softcap, slopes, q), lens, prefix_of, prefix_lens, out)
         if self.shared_workspace is not None:
@@ -213,7 +220,7 @@ class Pool:
                     self._outgrown.append(self.shared_workspace)
         need = hwkv_decode_shared_workspace_bytes(self.handle, prefix.handle, q.shape[1])
         self.shared_workspace = torch.empty(need, dtype=torch.uint8, device=self.buffer.device)
-        self._shared_captured = torch.cuda.is_current_stream_capturing()
+        self._shared_captured = _capturing()
         hwkv_decode_attn_shared(self.handle, prefix.handle, *args, self.shared_workspace, k_new, v_new, stream)
         return out
 
@@ -316,6 +323,12 @@ class Pool:
             raise ValueError(f"{name} must hold {self.io_dtype} rows of head_dim {self.head_dim} for "
                              f"{self.num_seqs} sequences on {self.buffer.device}")
         return shape[-2]
+
+    def _check_row(self, t, name, heads):
+        if (t.dtype != self.io_dtype or t.shape != (self.num_seqs, heads, self.head_dim) or not t.is_contiguous()
+                or t.get_device() != self._device_index):
+            raise ValueError(f"{name} must be contiguous {self.io_dtype} [{self.num_seqs}][{heads}][{self.head_dim}] on "
+                             f"{self.buffer.device}")
 
     def _is_counts(self, t) -> bool:
         return t.get_device() == self._device_index and t.numel() >= self.num_seqs and t.is_contiguous()

@@ -9,6 +9,7 @@
 // block sizes that no 16-row tile divides); the own parts come from the decode kernels, left open
 // (hwkv_decode_sk.cuh, kOpen); and the join below weighs the partials of both by their reference maxima.
 #include <algorithm>
+#include <atomic>
 
 #include "hwkv_shared.cuh"
 
@@ -274,8 +275,16 @@ __global__ void __launch_bounds__(kJoinThreads, 6) shared_join_kernel(const __gr
 
 template <typename T, int D, bool SC>
 cudaError_t launch_simt(const SharedArgs& a, dim3 grid, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(shared_simt_kernel<T, D, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, simt_smem<D>());
+  static std::atomic<uint64_t> prepared{0};  // a bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(prepared.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(shared_simt_kernel<T, D, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, simt_smem<D>());
+    if (e != cudaSuccess) return e;
+    prepared.fetch_or(bit, std::memory_order_relaxed);
+  }
   shared_simt_kernel<T, D, SC><<<grid, kThreads, simt_smem<D>(), st>>>(a);
   return cudaSuccess;
 }

@@ -29,6 +29,7 @@
 // Weights are rounded to bf16 for P V (2^-8 of each, half a step); their sum is of the unrounded ones.
 // Waits are bounded (~2 s) and record HWKV_DEVERR_WAIT_TIMEOUT; then all roles stop.
 #include <algorithm>
+#include <atomic>
 
 #include "hwkv_fp8.cuh"
 #include "hwkv_shared.cuh"
@@ -956,8 +957,16 @@ template <int D, bool SC, bool Q8>
 cudaError_t launch(const SharedArgs& a, const CUtensorMap* pool_map, const CUtensorMap* stage_map, int ctas, cudaStream_t st) {
   auto* kernel = shared_tc_kernel<D, SC, Q8>;
   const int smem = Cfg<D, Q8>::smem(a.num_prefixes);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> prepared{0};  // a bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(prepared.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, Q8>::smem(kMaxPrefixes));
+    if (e != cudaSuccess) return e;
+    prepared.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(Cfg<D, Q8>::kThreads);

@@ -288,7 +288,7 @@ int hwkv_decode_attn_score(hwkv_pool_t pool, int layer, const void* q, int q_hea
  *   workspace: hwkv_decode_shared_workspace_bytes() bytes, otherwise as for hwkv_decode_attn.
  * Three kernels on `stream` or more: the prefixes' keys, the own parts, their join.  Concurrent launches of the same
  * layer of `pool` race, decode calls included; `prefix` may be shared by any number of launches that only read it.
- * A group of up to 16 query heads per KV head, as in every decode.
+ * At most 65535 sequences and 768 prefixes; a group of up to 16 query heads per KV head, as in every decode.
  * Errors: as hwkv_decode_attn; HWKV_ERR_INVALID_ARG also for pools that do not go together. */
 int hwkv_decode_attn_shared(hwkv_pool_t pool, hwkv_pool_t prefix, int layer, const void* q, int q_heads,
                             const hwkv_score_t* score, const void* k_new, const void* v_new, const int32_t* lens_dev,

@@ -203,6 +203,15 @@ def test_equals_decode_of_whole_contexts():
     assert np.abs(a - b).max() <= 2.0 ** -6 * np.abs(b).max()  # each within 2^-7 of the definition's largest
 
 
+@pytest.mark.parametrize("types", PAIRS[:2], ids=PAIR_IDS[:2])
+def test_many_prefixes(types):
+    """As many as there may be, most without a sequence."""
+    rng = np.random.default_rng(0)
+    of = [767, 0, 500, 499, 500, 767, 767, -1, 31]
+    c = Case([20], [40], rng.integers(0, 30, 9).tolist(), rng.integers(0, 90, 768).tolist(), of, 2, 128, 16, types, seed=1)
+    c.step()
+
+
 def test_nothing_to_attend_to():
     c = Case([16, 32], [16, 8], [0, 0, 20, 40], [0, 30], [0, -1, 1, 1], 4, 64, seed=2)
     out = c.step(append=False)
@@ -326,6 +335,8 @@ def test_refusals():
     for other in (hw.Pool(1, 2, 64, 16, [[64, 64]], 1, BF16), hw.Pool(1, 1, 128, 16, [[64]], 1, BF16), hw.Pool(1, 1, 64, 16, [[64]], 1, F32),
                   hw.Pool(2, 1, 64, 16, [[64], [64]], 1, BF16)):
         refused(B.HwkvError, B.HWKV_ERR_INVALID_ARG, prefix=other)
+    many = hw.Pool(1, 1, 64, 16, [[16]], 769, BF16)
+    refused(B.HwkvError, B.HWKV_ERR_UNSUPPORTED, prefix=many, pl=i32([1] * 769))
     refused(B.HwkvError, B.HWKV_ERR_UNSUPPORTED, q=torch.zeros(2, 17, 64, dtype=BF16, device="cuda"))
     refused(B.HwkvError, B.HWKV_ERR_INVALID_ARG, softcap=-1.0)
     refused(ValueError, lens=lens.long())

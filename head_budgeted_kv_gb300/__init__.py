@@ -298,18 +298,19 @@ class Pool:
         turned k and v are stored at positions pos[s] + row, rows below n[s] (all when n is None).  q may be None;
         table None turns nothing.  q_out defaults to a new tensor (zeros past n); pass q_out=q to work in place.
         k_out, when given, receives the turned keys too.  Returns (q_out, k_out)."""
-        if q is None and q_out is not None:
-            raise ValueError("q_out goes with q")
+        at = self._device_index
         if q is not None:
-            heads = self._check_rows(q, "q")
-            if heads % self.kv_heads:
+            if self._check_rows(q, "q") % self.kv_heads:
                 raise ValueError(f"q must hold a multiple of {self.kv_heads} heads")
             if q_out is None:
                 q_out = (torch.empty if n is None else torch.zeros)(q.shape, dtype=q.dtype, device=q.device)
+            elif q_out.get_device() != at:
+                raise ValueError(f"outputs must lie on {self.buffer.device}")
+        elif q_out is not None:
+            raise ValueError("q_out goes with q")
         if self._check_rows(k, "k") != self.kv_heads or self._check_rows(v, "v") != self.kv_heads:
             raise ValueError(f"k and v must hold {self.kv_heads} heads")
-        at = self._device_index
-        if (q_out is not None and q_out.get_device() != at) or (k_out is not None and k_out.get_device() != at):
+        if k_out is not None and k_out.get_device() != at:
             raise ValueError(f"outputs must lie on {self.buffer.device}")
         if not self._is_counts(pos) or not (n is None or self._is_counts(n)) or not (turn_pos is None or self._is_counts(turn_pos)):
             raise ValueError(f"positions and row counts must hold {self.num_seqs} values in a row on {self.buffer.device}")

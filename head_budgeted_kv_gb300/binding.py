@@ -344,18 +344,6 @@ def hwkv_rope(pool: int, table: RopeTable, q: Optional[torch.Tensor], k: Optiona
     _check(load().hwkv_rope(pool, table, rq, heads, rk, n_max, pos.data_ptr(), _ptr(n), ro, rp, _stream_ptr(stream)))
 
 
-def _turned_rows(slots, i: int, t: torch.Tensor, out: Optional[torch.Tensor], name: str):
-    """References to the rows of t (slot i) and of its output (slot i + 1, or slot i in place)."""
-    rows, refs = slots.rows, slots.refs
-    _fill_rows(rows[i], t, t.shape[-1], name)
-    if out is None or out is t:
-        return refs[i], None if out is None else refs[i]
-    if out.shape != t.shape or out.dtype != t.dtype:
-        raise ValueError(f"{name}_out must match {name}")
-    _fill_rows(rows[i + 1], out, t.shape[-1], name + "_out")
-    return refs[i], refs[i + 1]
-
-
 def hwkv_rope_append(pool: int, layer: int, table: Optional[RopeTable], q: Optional[torch.Tensor], k: torch.Tensor,
                      v: torch.Tensor, pos: torch.Tensor, n: Optional[torch.Tensor] = None,
                      turn_pos: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
@@ -363,27 +351,42 @@ def hwkv_rope_append(pool: int, layer: int, table: Optional[RopeTable], q: Optio
     """Turns q [B][n_max][Hq][D] (or None) and k [B][n_max][Hkv][D] (or one row each, [B][heads][D]) at positions
     turn_pos + row (pos + row when None) and stores the turned k and v at positions pos + row; table None
     turns nothing."""
-    if pos.dtype != torch.int32 or (n is not None and n.dtype != torch.int32) or (
-            turn_pos is not None and turn_pos.dtype != torch.int32):
+    int32 = torch.int32
+    if pos.dtype != int32 or (n is not None and n.dtype != int32) or (turn_pos is not None and turn_pos.dtype != int32):
         raise ValueError("positions and row counts must be int32")
-    shape = k.shape
-    if v.shape != shape or v.dtype != k.dtype:
+    shape, dtype = k.shape, k.dtype
+    if v.shape != shape or v.dtype != dtype:
         raise ValueError("k and v must match")
     slots = _row_slots
+    rows, refs = slots.rows, slots.refs
+    dims, head_dim = len(shape), shape[-1]
     rq = ro = rp = None
     heads = 0
     if q is not None:
         qs = q.shape
-        if q_out is None:
-            raise ValueError("q goes with q_out")
-        if len(qs) != len(shape) or qs[:-2] != shape[:-2] or qs[-1] != shape[-1] or q.dtype != k.dtype:
+        if q_out is None or (q_out is not q and (q_out.shape != qs or q_out.dtype != dtype)):
+            raise ValueError("q_out must match q")
+        if (len(qs) != dims or qs[0] != shape[0] or (dims == 4 and qs[1] != shape[1]) or qs[-1] != head_dim
+                or q.dtype != dtype):
             raise ValueError("q and k must have the same sequences and rows")
         heads = qs[-2]
-        rq, ro = _turned_rows(slots, 0, q, q_out, "q")
-    rk, rp = _turned_rows(slots, 2, k, k_out, "k")
-    _fill_rows(slots.rows[4], v, shape[-1], "v")
-    _check(load().hwkv_rope_append(pool, layer, table, rq, heads, rk, slots.refs[4], shape[1] if len(shape) == 4 else 1,
-                                   pos.data_ptr(), _ptr(turn_pos), _ptr(n), ro, rp, _stream_ptr(stream)))
+        _fill_rows(rows[0], q, head_dim, "q")
+        rq = ro = refs[0]
+        if q_out is not q:
+            _fill_rows(rows[1], q_out, head_dim, "q_out")
+            ro = refs[1]
+    _fill_rows(rows[2], k, head_dim, "k")
+    if k_out is not None:
+        rp = refs[2]
+        if k_out is not k:
+            if k_out.shape != shape or k_out.dtype != dtype:
+                raise ValueError("k_out must match k")
+            _fill_rows(rows[3], k_out, head_dim, "k_out")
+            rp = refs[3]
+    _fill_rows(rows[4], v, head_dim, "v")
+    _check(load().hwkv_rope_append(pool, layer, table, rq, heads, refs[2], refs[4], shape[1] if dims == 4 else 1, pos.data_ptr(),
+                                   None if turn_pos is None else turn_pos.data_ptr(), None if n is None else n.data_ptr(),
+                                   ro, rp, _stream_ptr(stream)))
 
 
 def hwkv_decode_workspace_bytes(pool: int, q_heads: int) -> int:
@@ -462,13 +465,14 @@ def hwkv_decode_attn_shared(pool: int, prefix: int, layer: int, q: torch.Tensor,
                             v_new: Optional[torch.Tensor] = None, stream=None):
     """Decode of sequences behind the prefixes that pool `prefix` holds: at own lengths `lens` (after the append),
     or with k_new, v_new at own positions `lens`, appended first."""
-    if not all(t.is_contiguous() for t in (q, out, k_new, v_new) if t is not None):
+    if not (q.is_contiguous() and out.is_contiguous() and (k_new is None or k_new.is_contiguous())
+            and (v_new is None or v_new.is_contiguous())):
         raise ValueError("q, out, k_new and v_new must be contiguous")
     if not (lens.dtype == prefix_of.dtype == prefix_lens.dtype == torch.int32):
         raise ValueError("lengths and prefixes must be int32")
-    _check(load().hwkv_decode_attn_shared(pool, prefix, layer, _ptr(q), q.shape[1], score, _ptr(k_new), _ptr(v_new), _ptr(lens),
-                                          _ptr(prefix_of), _ptr(prefix_lens), _ptr(out), _ptr(workspace),
-                                          workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
+    _check(load().hwkv_decode_attn_shared(pool, prefix, layer, q.data_ptr(), q.shape[1], score, _ptr(k_new), _ptr(v_new),
+                                          lens.data_ptr(), prefix_of.data_ptr(), prefix_lens.data_ptr(), out.data_ptr(),
+                                          workspace.data_ptr(), workspace.nbytes, _stream_ptr(stream)))
 
 
 class DecodeLaunch:

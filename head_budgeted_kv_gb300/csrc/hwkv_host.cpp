@@ -978,7 +978,7 @@ int hwkv_rope_append(hwkv_pool_t p, int layer, const hwkv_rope_t* rope, const hw
   if (q && (q_heads < g.kv_heads || q_heads % g.kv_heads != 0 || q_heads > 65535))
     return fail(HWKV_ERR_UNSUPPORTED, "q_heads must be a multiple of kv_heads, at most 65535 (got %d)", q_heads);
   if (n_max < 1) return fail(HWKV_ERR_INVALID_ARG, "n_max must be >= 1");
-  if (((int64_t)n_max + 2 * 16) * g.num_seqs * g.kv_heads > kInt32Max)
+  if (((int64_t)n_max + 2 * 16) * g.num_seqs * std::max(4, g.kv_heads) > kInt32Max)
     return fail(HWKV_ERR_UNSUPPORTED, "num_seqs * kv_heads * n_max must be below 2^31");
   if (!aligned(pos_dev, 4) || !aligned(turn_pos_dev, 4) || !aligned(n_dev, 4))
     return fail(HWKV_ERR_ALIGNMENT, "positions must be 4-byte aligned");
@@ -1007,7 +1007,7 @@ int hwkv_rope_append(hwkv_pool_t p, int layer, const hwkv_rope_t* rope, const hw
   a.keys_out = k_out ? 1 : 0;
   const int layout = rope ? rope->layout : HWKV_ROPE_HALF;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  HWKV_CUDA_TRY(g.dtype == HWKV_E4M3 ? launch_rope_append_q8(a, layout, p->num_sms, st)
+  HWKV_CUDA_TRY(g.dtype == HWKV_E4M3 ? launch_rope_append_q8(a, layout, st)
                                      : launch_rope_append(a, layout, g.dtype == HWKV_F32, st),
                 "rope-append launch");
   return ok();

@@ -202,7 +202,7 @@ struct RopeAppendArgs : RopeArgs {
   RopeTensor v;
   const int32_t* turn_pos;  // [B] position whose angle row 0 turns by, null: pos
   int32_t keys_out;         // 1: k_out receives the turned keys too
-  int32_t part_heads;       // 8-bit pools: KV heads of one CTA (set by launch_rope_append)
+  int32_t q_parts;          // 8-bit pools: CTAs that share the query rows of a tile (set by launch_rope_append_q8)
 };
 
 // Counts every kernel launch the library makes (read by hwkv_kernel_launches).
@@ -256,7 +256,7 @@ cudaError_t launch_shared_join(const SharedArgs& a, bool f32, cudaStream_t st);
 cudaError_t launch_rope(RopeArgs a, int layout, bool f32, cudaStream_t st);  // sets a.rows
 // the same with keys and values stored (bf16 and fp32 pools here, e4m3 pools in hwkv_rope_q8.cu)
 cudaError_t launch_rope_append(RopeAppendArgs a, int layout, bool f32, cudaStream_t st);
-cudaError_t launch_rope_append_q8(RopeAppendArgs a, int layout, int num_sms, cudaStream_t st);
+cudaError_t launch_rope_append_q8(RopeAppendArgs a, int layout, cudaStream_t st);
 // chunked prefill (hwkv_prefill.cu): attention, then the chunk appended to the rings
 int prefill_tokens_per_cta(int group);  // chunk tokens one CTA answers (two query tiles)
 int prefill_tile_tokens(int group);     // chunk tokens of one 128-row query tile

@@ -1070,7 +1070,9 @@ int score_args(const hwkv_score_t& sc, ScoreArgs* out) {
 struct DecodeCall {
   DecodeArgs a;
   bool tc = false;
-  int ctas = 0;  // the stream-K kernel's grid
+  int ctas = 0;   // the stream-K kernel's grid, or
+  int items = 0;  // the split-K kernel's, and whether its partials need a merge
+  bool multi_chunk = false;
   const void* k_new = nullptr;
   const void* v_new = nullptr;
 };
@@ -1139,13 +1141,15 @@ int prepare_decode(hwkv_pool_t p, int layer, const void* q, int q_heads, hwkv_sc
   std::memcpy(a.chunk_prefix, lp.chunk_prefix, sizeof a.chunk_prefix);
   call->tc = tc;
   call->ctas = tc ? tc_workers(p, G) : 0;
+  call->items = lp.items;
+  call->multi_chunk = lp.multi_chunk;
   call->k_new = len_add ? k_new : nullptr;
   call->v_new = len_add ? v_new : nullptr;
   return HWKV_OK;
 }
 
 // Launches a prepared decode (open when a.open_acc is set).
-int launch_decode(hwkv_pool_t p, int layer, DecodeCall& call, cudaStream_t st) {
+int launch_decode(hwkv_pool_t p, DecodeCall& call, cudaStream_t st) {
   DecodeArgs& a = call.a;
   const Geometry& g = p->g;
   if (call.tc) {
@@ -1155,7 +1159,6 @@ int launch_decode(hwkv_pool_t p, int layer, DecodeCall& call, cudaStream_t st) {
                   "decode launch");
     return HWKV_OK;
   }
-  const LayerPlan& lp = p->plans[layer];
   if (call.k_new) {
     CopyArgs c;
     std::memset(&c, 0, sizeof c);
@@ -1166,8 +1169,8 @@ int launch_decode(hwkv_pool_t p, int layer, DecodeCall& call, cudaStream_t st) {
     c.lens = a.lens;
     HWKV_CUDA_TRY(launch_append(c, g.dtype, st), "append launch");
   }
-  HWKV_CUDA_TRY(launch_decode_simt(a, g.dtype, lp.items, st), "decode launch");
-  if (lp.multi_chunk) HWKV_CUDA_TRY(launch_combine(a, g.dtype, st), "combine launch");
+  HWKV_CUDA_TRY(launch_decode_simt(a, g.dtype, call.items, st), "decode launch");
+  if (call.multi_chunk) HWKV_CUDA_TRY(launch_combine(a, g.dtype, st), "combine launch");
   return HWKV_OK;
 }
 
@@ -1180,7 +1183,7 @@ int decode_common(hwkv_pool_t p, int layer, const void* q, int q_heads, hwkv_sco
   int rc = prepare_decode(p, layer, q, q_heads, score, lens_dev, len_add, k_new, v_new, out, workspace, ws_bytes, flags, &call);
   if (rc != HWKV_OK) return rc;
   NvtxRange range_(len_add ? "hwkv_append_decode_attn" : "hwkv_decode_attn", layer);
-  rc = launch_decode(p, layer, call, static_cast<cudaStream_t>(stream));
+  rc = launch_decode(p, call, static_cast<cudaStream_t>(stream));
   return rc != HWKV_OK ? rc : ok();
 }
 
@@ -1212,23 +1215,22 @@ int open_workers(const hwkv_pool* p, int layer, int group) {
   return (int)std::min<int64_t>(tc_workers(p, group), std::max<int64_t>(16, tiles * g.num_seqs / 4));
 }
 
-// How the keys of the prefixes are split on the CUDA cores: ring slots per CTA for about six CTAs per SM over
-// the sequences' tiles, and the chunks of each head.
+// How keys are split on the CUDA cores: ring slots per CTA for about six CTAs per SM, and the chunks of each head.
 struct SharedPlan {
   int split = 0;
   int chunks = 0;
   int32_t chunk_prefix[kMaxKvHeads + 1] = {};
 };
 
-SharedPlan plan_shared(const hwkv_pool* p, const hwkv_pool* prefix, int layer, int group) {
+// Of one layer of `pool`, whose chunks `times` CTAs read.
+SharedPlan plan_chunks(const hwkv_pool* pool, int layer, int times) {
   SharedPlan s;
-  const Geometry& g = prefix->g;
+  const Geometry& g = pool->g;
   auto capacity = [&](int h) { return (int64_t)g.nblk[(size_t)layer * g.kv_heads + h] * g.block_size; };
   int64_t slots = 0;
   for (int h = 0; h < g.kv_heads; ++h) slots += capacity(h);
-  const int per = shared_simt_seqs(group);
-  const int64_t want = slots * g.num_seqs * ((p->g.num_seqs + per - 1) / per) / (6LL * std::max(1, p->num_sms));
-  s.split = 256;
+  const int64_t want = slots * g.num_seqs * times / (6LL * std::max(1, pool->num_sms));
+  s.split = 64;
   while (s.split < want && s.split < 4096) s.split <<= 1;
   for (int h = 0; h < g.kv_heads; ++h)
     s.chunk_prefix[h + 1] = s.chunk_prefix[h] + (int32_t)((capacity(h) + s.split - 1) / s.split);
@@ -1236,9 +1238,16 @@ SharedPlan plan_shared(const hwkv_pool* p, const hwkv_pool* prefix, int layer, i
   return s;
 }
 
+// The prefixes' keys, read by a CTA per tile of sequences.
+SharedPlan plan_shared(const hwkv_pool* p, const hwkv_pool* prefix, int layer, int group) {
+  const int per = shared_simt_seqs(group);
+  return plan_chunks(prefix, layer, (p->g.num_seqs + per - 1) / per);
+}
+
 // Regions of the workspace: the own decode's, its open results, the prefixes' partials and their records.
 struct SharedLayout {
   int chain_rows = 0;  // tensor cores: rows of a chain's partial
+  uint64_t split_acc = 0, split_ml = 0;  // the own parts' partials on the CUDA cores
   uint64_t own_acc = 0, own_ml = 0, part_o = 0, part_ml = 0, rec = 0, total = 0;
 };
 
@@ -1258,7 +1267,16 @@ SharedLayout shared_layout(const hwkv_pool* p, const hwkv_pool* prefix, int grou
     for (int l = 0; l < p->g.layers; ++l) parts = std::max<uint64_t>(parts, plan_shared(p, prefix, l, group).chunks);
     parts *= B * (uint64_t)group;
   }
-  w.own_acc = align256(workspace_bytes(p, group));
+  uint64_t own = workspace_bytes(p, group);
+  if (!use_tc(p, group)) {
+    uint64_t items = 0;
+    for (int l = 0; l < p->g.layers; ++l) items = std::max<uint64_t>(items, plan_chunks(p, l, 1).chunks);
+    items *= B * (uint64_t)group;
+    w.split_acc = align256(own);
+    w.split_ml = align256(w.split_acc + items * D * 4);
+    own = w.split_ml + items * 8;
+  }
+  w.own_acc = align256(own);
   w.own_ml = align256(w.own_acc + rows * D * 4);
   w.part_o = align256(w.own_ml + rows * 8);
   w.part_ml = align256(w.part_o + parts * D * 4);
@@ -1339,6 +1357,15 @@ int hwkv_decode_attn_shared(hwkv_pool_t p, hwkv_pool_t prefix, int layer, const 
   char* ws = static_cast<char*>(workspace);
   call.a.open_acc = reinterpret_cast<float*>(ws + wl.own_acc);
   call.a.open_ml = reinterpret_cast<float*>(ws + wl.own_ml);
+  if (!call.tc) {
+    const SharedPlan own = plan_chunks(p, layer, 1);
+    call.a.split_tokens = own.split;
+    std::memcpy(call.a.chunk_prefix, own.chunk_prefix, sizeof own.chunk_prefix);
+    call.items = own.chunks * p->g.num_seqs;
+    call.multi_chunk = own.chunks > p->g.kv_heads;
+    call.a.part_acc = reinterpret_cast<float*>(ws + wl.split_acc);
+    call.a.part_ml = reinterpret_cast<float*>(ws + wl.split_ml);
+  }
   SharedArgs a;
   std::memset(&a, 0, sizeof a);
   a.pv = pool_view(prefix);
@@ -1385,7 +1412,7 @@ int hwkv_decode_attn_shared(hwkv_pool_t p, hwkv_pool_t prefix, int layer, const 
     std::memcpy(a.chunk_prefix, sp.chunk_prefix, sizeof a.chunk_prefix);
     HWKV_CUDA_TRY(launch_shared_simt(a, prefix->g.dtype, sp.chunks, st), "shared prefix launch");
   }
-  rc = launch_decode(p, layer, call, st);
+  rc = launch_decode(p, call, st);
   if (rc != HWKV_OK) return rc;
   HWKV_CUDA_TRY(launch_shared_join(a, p->g.dtype == HWKV_F32, st), "shared join launch");
   return ok();

@@ -41,5 +41,18 @@ __device__ __forceinline__ void turn_angle(uint64_t turns, uint32_t p, float mag
   sn *= magnitude;
 }
 
+// The same from the nearest quarter turn: what is left is below an eighth of a turn, so that its fp32 value is off by 2^-26 rad,
+// not 2^-23 (codes of 8 bits stand on the exact turned value, where fp32 and bf16 outputs round it away).
+__device__ __forceinline__ void turn_angle_fine(uint64_t turns, uint32_t p, float magnitude, float& cn, float& sn) {
+  const uint64_t t = turns * (uint64_t)p;
+  const uint32_t quarter = (uint32_t)((t + (1ull << 61)) >> 62);      // modulo 4
+  const int32_t rest = (int32_t)(uint32_t)((t << 2) >> 32);       // from there, 2^-33 half turns
+  float s, c;
+  sincospif((float)rest * 0x1p-33f, &s, &c);
+  const float a = quarter & 1u ? -s : c, b = quarter & 1u ? c : s;    // (cos, sin) a quarter further for odd ones
+  cn = (quarter & 2u ? -a : a) * magnitude;
+  sn = (quarter & 2u ? -b : b) * magnitude;
+}
+
 }  // namespace
 }  // namespace hwkv

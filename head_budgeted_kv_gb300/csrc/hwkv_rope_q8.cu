@@ -51,28 +51,33 @@ __device__ __forceinline__ Place place_of(int j, int rot) {
 
 using Vec8 = RopeVec<__nv_bfloat16>;
 
-// Turns the pair of vectors in place; cs(i): cosine and sine of pair i; mate(d): element d of the row
-// (kHalfAny).
-template <int kLayout, typename Cs, typename Mate>
-__device__ __forceinline__ void turn_pair(Vec8& x, Vec8& y, const Place& at, int rot, Cs cs, Mate mate) {
+// Where the cosine and sine of pair i of a row lie, in float2: two pairs to a 16-byte vector, vector v at (v % 4) * (D / 16) + v / 4, so
+// that the lanes of a row, which want pairs 8 j and up, read neighbouring vectors.
+template <int D>
+__device__ __forceinline__ int cs_slot(int i) {
+  const int v = i >> 1;
+  return 2 * ((v & 3) * (D / 16) + (v >> 2)) + (i & 1);
+}
+
+// Turns the pair of vectors in place, place j of a row; cs(i): cosine and sine of pair i (kHalfAny); cs2(k): of pairs 8 j + 2 k
+// and the next; mate(d): element d of the row (kHalfAny).
+template <int kLayout, typename Cs, typename Cs2, typename Mate>
+__device__ __forceinline__ void turn_pair(Vec8& x, Vec8& y, const Place& at, int rot, Cs cs, Cs2 cs2, Mate mate) {
   if constexpr (kLayout == kHalf) {
     if (!at.turned) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float2 c = cs(at.a + e);
+    for (int e = 0; e < 8; e += 2) {
+      const float4 c = cs2(e / 2);
       turn(x.v[e], y.v[e], c.x, c.y);
+      turn(x.v[e + 1], y.v[e + 1], c.z, c.w);
     }
   } else if constexpr (kLayout == kInterleaved) {
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      if (at.a + e < rot) {
-        const float2 c = cs((at.a + e) / 2);
-        turn(x.v[e], x.v[e + 1], c.x, c.y);
-      }
-      if (at.b + e < rot) {
-        const float2 c = cs((at.b + e) / 2);
-        turn(y.v[e], y.v[e + 1], c.x, c.y);
-      }
+    for (int e = 0; e < 16; e += 4) {
+      float* v = (e < 8 ? x.v : y.v) + (e & 7);
+      const float4 c = cs2(e / 4);
+      if (at.a + e < rot) turn(v[0], v[1], c.x, c.y);
+      if (at.a + e + 2 < rot) turn(v[2], v[3], c.z, c.w);
     }
   } else {
     const int half = rot / 2;
@@ -94,7 +99,7 @@ __global__ void __launch_bounds__(kQ8Threads, 4) rope_append_q8_kernel(const __g
   constexpr int kRows = 32 / kPairs;     // rows the lanes of a warp cover
   constexpr int kPer = kScaleGroup / kRows;
   static_assert(kQ8Threads % kPairs == 0, "a thread keeps its place in the rows");
-  __shared__ float2 s_cs[kScaleGroup][D / 2 + 1];
+  __shared__ __align__(16) float2 s_cs[kScaleGroup][D / 2];
   griddep_wait();
   griddep_launch_dependents();
 
@@ -121,12 +126,14 @@ __global__ void __launch_bounds__(kQ8Threads, 4) rope_append_q8_kernel(const __g
   const int rot = a.rot, half = rot / 2;
   const Place at = place_of<kLayout>((int)threadIdx.x % kPairs, rot);
 
+  const int j = (int)threadIdx.x % kPairs;
+  auto cs2 = [&](int r, int k) { return *reinterpret_cast<const float4*>(&s_cs[r][2 * (k * kPairs + j)]); };  // pairs 8 j + 2 k and the next
   auto angles = [&]() {
     for (int e = threadIdx.x; e < (r_hi - r_lo) * half; e += kQ8Threads) {
       const int r = r_lo + e / half, i = e - (r - r_lo) * half;
       float cn, sn;
-      turn_angle(a.turns[i], (uint32_t)turn_pos + (uint32_t)(p0 + r - pos), a.magnitude, cn, sn);
-      s_cs[r][i] = make_float2(cn, sn);
+      turn_angle_fine(a.turns[i], (uint32_t)turn_pos + (uint32_t)(p0 + r - pos), a.magnitude, cn, sn);
+      s_cs[r][cs_slot<D>(i)] = make_float2(cn, sn);
     }
   };
 
@@ -177,7 +184,8 @@ __global__ void __launch_bounds__(kQ8Threads, 4) rope_append_q8_kernel(const __g
           Vec8 x, y;
           x.load(u[k]);
           y.load(v[k]);
-          turn_pair<kLayout>(x, y, at, rot, [&](int c) { return s_cs[rk[k]][c]; }, [&](int d) { return __bfloat162float(src[d]); });
+          turn_pair<kLayout>(x, y, at, rot, [&](int c) { return s_cs[rk[k]][cs_slot<D>(c)]; }, [&](int c) { return cs2(rk[k], c); },
+                             [&](int d) { return __bfloat162float(src[d]); });
           u[k] = x.store();
           v[k] = y.store();
         }
@@ -276,12 +284,19 @@ __global__ void __launch_bounds__(kQ8Threads, 4) rope_append_q8_kernel(const __g
       const int i_row = here ? p0 + r - pos : p0 + r - C - pos;  // chunk row
       const __nv_bfloat16* row = in + (int64_t)i_row * src.row_stride;
       auto mate = [&](int d) { return __bfloat162float(row[d]); };
-      // (a row of the lap before: its angles are not the tile's)
-      turn_pair<kLayout>(x[i], y[i], at, rot, [&](int k) {
-        float2 c = s_cs[r][k];
-        if (!here) turn_angle(a.turns[k], (uint32_t)turn_pos + (uint32_t)i_row, a.magnitude, c.x, c.y);
-        return c;
-      }, mate);
+      if (here) {
+        turn_pair<kLayout>(x[i], y[i], at, rot, [&](int k) { return s_cs[r][cs_slot<D>(k)]; }, [&](int k) { return cs2(r, k); }, mate);
+      } else {  // a row of the lap before: its angles are not the tile's
+        auto far = [&](int k) {
+          float2 c = make_float2(1.f, 0.f);
+          if (k < half) turn_angle_fine(a.turns[k], (uint32_t)turn_pos + (uint32_t)i_row, a.magnitude, c.x, c.y);
+          return c;
+        };
+        turn_pair<kLayout>(x[i], y[i], at, rot, far, [&](int k) {
+          const float2 c = far(8 * j + 2 * k), d = far(8 * j + 2 * k + 1);
+          return make_float4(c.x, c.y, d.x, d.y);
+        }, mate);
+      }
     }
     float mx = 0.f;
 #pragma unroll

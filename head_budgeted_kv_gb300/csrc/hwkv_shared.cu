@@ -76,23 +76,50 @@ __global__ void __launch_bounds__(kThreads) shared_simt_kernel(const __grid_cons
   const int t_begin = c * a.split_tokens, t_end = min(C, t_begin + a.split_tokens);
   for (int t0 = t_begin; t0 < t_end; t0 += kKeys) {
     __syncthreads();  // the pass before has been read
-    for (int e = threadIdx.x; e < kKeys * D; e += kThreads) {
-      const int key = e / D, d = e - key * D;
-      const int t = t0 + key;
-      float kx = 0.f, vx = 0.f;
+    {
+      // four threads bring a key's row and a value's, 16 bytes at a time
+      const int key = (int)threadIdx.x >> 2, t = t0 + key;
+      constexpr int V = 16 / (int)sizeof(T), kVec = D / V;  // elements of a vector, vectors of a row
+      const T* from = nullptr;
       if (t < t_end && ring_age(N, t, C) < min(N, w)) {
         const int j = t / bs;
         const int32_t blk = a.pv.tbl[a.g.tbl_base + (int64_t)f * a.g.tbl_seq_stride + a.g.nblk_prefix[h] + j];
         if (blk < 0 || (int64_t)blk >= a.pv.total_blocks) {
-          if (d == 0) atomicOr(a.pv.err, HWKV_DEVERR_BAD_BLOCK);
+          if (part == 0) atomicOr(a.pv.err, HWKV_DEVERR_BAD_BLOCK);
         } else {
-          const T* row = static_cast<const T*>(a.pv.pool) + ((int64_t)blk * 2 * bs + (t - j * bs)) * D;
-          kx = load_in<T>(row + d);
-          vx = load_in<T>(row + (int64_t)bs * D + d);
+          from = static_cast<const T*>(a.pv.pool) + ((int64_t)blk * 2 * bs + (t - j * bs)) * D;
         }
       }
-      s_k[key * kLd + d] = kx;
-      s_v[key * kLd + d] = vx;
+      uint4 kx[kVec / 4], vx[kVec / 4];
+#pragma unroll
+      for (int i = 0; i < kVec / 4; ++i) {
+        kx[i] = vx[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (from != nullptr) {
+          kx[i] = *reinterpret_cast<const uint4*>(from + (4 * i + part) * V);
+          vx[i] = *reinterpret_cast<const uint4*>(from + (int64_t)bs * D + (4 * i + part) * V);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kVec / 4; ++i) {
+        float k[V], v[V];
+        const uint32_t kw[4] = {kx[i].x, kx[i].y, kx[i].z, kx[i].w}, vw[4] = {vx[i].x, vx[i].y, vx[i].z, vx[i].w};
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          if constexpr (sizeof(T) == 4) {
+            k[e] = __uint_as_float(kw[e]);
+            v[e] = __uint_as_float(vw[e]);
+          } else {
+            k[e] = __uint_as_float((e & 1) ? (kw[e >> 1] & 0xFFFF0000u) : (kw[e >> 1] << 16));
+            v[e] = __uint_as_float((e & 1) ? (vw[e >> 1] & 0xFFFF0000u) : (vw[e >> 1] << 16));
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+          const int d = (4 * i + part) * V + e;
+          *reinterpret_cast<float4*>(s_k + key * kLd + d) = make_float4(k[e], k[e + 1], k[e + 2], k[e + 3]);
+          *reinterpret_cast<float4*>(s_v + key * kLd + d) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+      }
     }
     __syncthreads();
     float sc[kKeys / 4];

@@ -247,10 +247,12 @@ cudaError_t launch_decode_open_q8(const DecodeArgs& a, const CUtensorMap* tmap, 
 // shared prefixes (hwkv_shared.cu): partials of the prefixes' keys, CUDA cores; and the join
 int shared_simt_seqs(int group);  // sequences of one CTA
 cudaError_t launch_shared_simt(const SharedArgs& a, int dtype, int chunks, cudaStream_t st);
-// the same on the tensor cores (hwkv_shared_tc.cu), bf16 pools
+// the same on the tensor cores (hwkv_shared_tc.cu, 8-bit pools hwkv_shared_tc_q8.cu)
 constexpr int kMaxPrefixes = 768;  // what shared memory leaves room for beside 8-bit stages
 int shared_tc_seqs(int group);  // sequences of a query tile
 cudaError_t launch_shared_tc(const SharedArgs& a, const CUtensorMap* pool_map, const CUtensorMap* stage_map, int ctas, cudaStream_t st);
+cudaError_t launch_shared_tc_q8(const SharedArgs& a, const CUtensorMap* pool_map, const CUtensorMap* stage_map, int ctas,
+                                cudaStream_t st);
 cudaError_t launch_shared_join(const SharedArgs& a, bool f32, cudaStream_t st);
 // rotary positions (hwkv_rope.cu)
 cudaError_t launch_rope(RopeArgs a, int layout, bool f32, cudaStream_t st);  // sets a.rows

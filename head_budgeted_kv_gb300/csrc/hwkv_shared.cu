@@ -5,7 +5,7 @@
 //   out = (sum_own p v + sum_prefix p v) / (sum_own p + sum_prefix p),   p = 2^(score - m)
 //
 // Three launches.  The prefixes' keys are read once for all sequences behind them, as a product of
-// (sequences x group) rows with the keys (on tcgen05: hwkv_shared_tc.cu; here: CUDA cores, for fp32 pools and
+// (sequences x group) rows with the keys (on tcgen05: hwkv_shared_tc.cuh; here: CUDA cores, for fp32 pools and
 // block sizes that no 16-row tile divides); the own parts come from the decode kernels, left open
 // (hwkv_decode_sk.cuh, kOpen); and the join below weighs the partials of both by their reference maxima.
 #include <algorithm>

@@ -639,22 +639,35 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
         const int age0 = k < sg.tiles ? tile_age(sg, last, k) : 0;
         const uint32_t code = sbase + K::kCodeOff + cs * K::kCodeBytes + u * K::kTileBytes;
         const uint32_t rows = sbase + K::kStageOff + st * K::kStageBytes + u * (kTile * 128);
+        // all loads ahead of the arithmetic: rows of D bytes, their 16-byte chunks swizzled with the row (head_dim 128: by row % 8,
+        // 64: by row / 2 % 4)
+        constexpr int kG = kTile / kR;
+        uint4 w[2][kG];
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+          for (int g = 0; g < kG; ++g) {
+            const int r = g * kR + r_lane;
+            const uint32_t from = code + kv * (kTile * D) + r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[kv][g].x), "=r"(w[kv][g].y), "=r"(w[kv][g].z), "=r"(w[kv][g].w)
+                         : "r"(from));
+          }
+        if (!(k < sg.tiles && age0 >= kTile - 1 && age0 < window)) {  // a tile with slots outside the window
+#pragma unroll
+          for (int g = 0; g < kG; ++g) {
+            int age = age0 - (g * kR + r_lane);
+            if (age < 0) age += sg.C;
+            if (k >= sg.tiles || age >= window) w[1][g] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const float f = kv ? scale.y : scale.x;
 #pragma unroll
-          for (int g = 0; g < kTile / kR; ++g) {
+          for (int g = 0; g < kG; ++g) {
             const int r = g * kR + r_lane;
-            // rows of D bytes, their 16-byte chunks swizzled with the row (128: by row % 8, 64: by row / 2 % 4)
-            const uint32_t from = code + kv * (kTile * D) + r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
-            uint4 w;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(from));
-            if (kv) {
-              int age = age0 - r;
-              if (age < 0) age += sg.C;
-              if (k >= sg.tiles || age >= window) w = make_uint4(0u, 0u, 0u, 0u);
-            }
-            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+            const uint32_t in[4] = {w[kv][g].x, w[kv][g].y, w[kv][g].z, w[kv][g].w};
             uint32_t out[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {

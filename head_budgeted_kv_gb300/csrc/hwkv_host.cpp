@@ -1196,23 +1196,27 @@ struct SharedTimes {
   int stage_ns, base_ns, tile_ns, per_sm;
 };
 
-SharedTimes shared_times(const hwkv_pool* p, const hwkv_pool* prefix, int group, bool scored) {
+SharedTimes shared_times(const hwkv_pool* p, const hwkv_pool* prefix, int group, const ScoreArgs& score) {
   SharedTimes t;
   const bool wide = p->g.head_dim == 128, q8 = p->g.dtype == HWKV_E4M3;
-  t.stage_ns = prefix->g.dtype == HWKV_E4M3 ? (wide ? 1150 : 800) : (wide ? 950 : 700);
-  if (scored) t.stage_ns = t.stage_ns * 2;
+  t.stage_ns = prefix->g.dtype == HWKV_E4M3 ? (wide ? 1200 : 800) : (wide ? 930 : 650);
+  t.stage_ns = t.stage_ns * (2 + (score.capped ? 1 : 0) + (score.slopes ? 1 : 0)) / 2;  // 1.4, 1.4 and 2.1 us at 256 rows
   t.per_sm = std::max(1, p->ctas_per_sm[decode_tc_pad_index(group)]);
   t.base_ns = q8 ? 18000 : (wide ? 12500 : 16000);
   t.tile_ns = q8 ? (wide ? 190 : 150) : (wide ? 270 : 220);
   return t;
 }
 
-// CTAs of the own parts' kernel: as for a decode, but no more than own windows of four tiles each keep busy.
+// CTAs of the own parts' kernel: half of a decode's, which half of the SMs take at once beside the prefixes, but no more than
+// own windows of four tiles each keep busy.  (All of them, in two or three waves: 32K document 49 us, not 46; several
+// prefixes 42, not 35; a third: 53 and 45.)
 int open_workers(const hwkv_pool* p, int layer, int group) {
+  const int full = tc_workers(p, group);
+  if (p->workers_override > 0) return full;
   const Geometry& g = p->g;
   int64_t tiles = 0;
   for (int h = 0; h < g.kv_heads; ++h) tiles += (g.windows[(size_t)layer * g.kv_heads + h] + 15) / 16;
-  return (int)std::min<int64_t>(tc_workers(p, group), std::max<int64_t>(16, tiles * g.num_seqs / 4));
+  return (int)std::min<int64_t>((full + 1) / 2, std::max<int64_t>(16, tiles * g.num_seqs / 4));
 }
 
 // How keys are split on the CUDA cores: ring slots per CTA for about six CTAs per SM, and the chunks of each head.
@@ -1395,7 +1399,7 @@ int hwkv_decode_attn_shared(hwkv_pool_t p, hwkv_pool_t prefix, int layer, const 
     a.tc = 1;
     a.bs_log2 = log2_of(prefix->g.block_size);
     a.stage_tb = prefix->stage_tb;
-    const SharedTimes times = shared_times(p, prefix, G, a.score.on);
+    const SharedTimes times = shared_times(p, prefix, G, a.score);
     a.stage_ns = times.stage_ns;
     if (call.tc) {
       a.own_ctas = call.ctas = open_workers(p, layer, G);

@@ -157,18 +157,18 @@ __device__ __forceinline__ int line_cta(long long t, long long T, int n) {
 
 // CTAs for T line positions beside the own parts' kernel of `tiles` tiles in `groups` groups: the number that lets the later of the two
 // end first, by a model of both in ns.  Here 8 us and a stage per position; there a CTA takes its tiles, 4.8 us a group and 12 to 18 us
-// (fitted to that kernel alone on 16 to 288 CTAs: within 10% from 20 to 500 us), 5 of them once, and its CTAs go through the SMs left
-// to them in waves (lane w tries w + 1 of them, with two SMs to spare: a straggler is another wave; the last lane tries all SMs here
-// and the own parts after).  In integers: every CTA must choose alike.
+// (fitted to that kernel alone on 16 to 288 CTAs: within 10% from 20 to 500 us), and its CTAs go through the SMs left to them in waves
+// (lane w tries w + 1 of them, with two SMs to spare: a straggler is another wave; the last lane tries all SMs here and the own
+// parts after).  In integers: every CTA must choose alike.
 __device__ __forceinline__ int pick_ctas(const SharedArgs& a, long long T, uint32_t tiles, uint32_t groups, int sms, int lane) {
-  const long long each = a.own_base_ns - 5000 + ((long long)tiles * a.own_tile_ns + (long long)groups * 4800) / a.own_ctas;
+  const long long each = a.own_base_ns + ((long long)tiles * a.own_tile_ns + (long long)groups * 4800) / a.own_ctas;
   const int waves = lane + 1;
   const int slots = (a.own_ctas + waves - 1) / waves, theirs = (slots + a.own_per_sm - 1) / a.own_per_sm + 2;
   const int mine = lane == 31 ? sms : sms - theirs;
   long long time = (long long)1 << 60;
   if (mine >= 1) {
     const long long here = 8000 + T * a.stage_ns / mine;
-    time = lane == 31 ? here + each + 8000 : max(here, waves * each + 5000);
+    time = lane == 31 ? here + each + 3000 : max(here, waves * each);
   }
   long long best = time;
 #pragma unroll

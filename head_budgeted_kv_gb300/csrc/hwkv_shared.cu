@@ -192,19 +192,18 @@ constexpr int simt_smem() {
 // partial and its prefix's, M = max_i m_i; nothing to attend to gives zeros.  A thread sums four columns of a head over every
 // kSplit'th part, the states and sums of kAhead parts on their way at once; where a head has more
 // threads than columns, their sums meet in shared memory.  The order of all sums is fixed.
-constexpr int kJoinThreads = 128;
 constexpr int kAhead = 8;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads, 6) shared_join_kernel(const __grid_constant__ SharedArgs a) {
+template <typename T, int D, int threads>
+__global__ void __launch_bounds__(threads, threads == 512 ? 1 : 768 / threads) shared_join_kernel(const __grid_constant__ SharedArgs a) {
   constexpr int kV = D / 4;  // float4 columns of a head
-  __shared__ float4 s_acc[kJoinThreads];
-  __shared__ float2 s_ml[kJoinThreads];
+  __shared__ float4 s_acc[threads];
+  __shared__ float2 s_ml[threads];
   const int H = a.pv.kv_heads, G = a.group;
   const int s = (int)blockIdx.x / H, h = (int)blockIdx.x - s * H;
   const int64_t row = (int64_t)blockIdx.x * G;  // the first of the CTA's rows
   const int cols = G * kV;
-  const int split = max(1, kJoinThreads / cols);  // threads of a column
+  const int split = max(1, threads / cols);  // threads of a column
   const int e0 = split > 1 ? (int)threadIdx.x % cols : (int)threadIdx.x, k0 = split > 1 ? (int)threadIdx.x / cols : 0;
   griddep_wait();
   const int f = prefix_of(a, s, threadIdx.x == 0 && h == 0);
@@ -224,7 +223,7 @@ __global__ void __launch_bounds__(kJoinThreads, 6) shared_join_kernel(const __gr
     step = G;
     parts = a.chunk_prefix[h + 1] - a.chunk_prefix[h];
   }
-  for (int c0 = 0; c0 < cols; c0 += kJoinThreads) {  // more than one pass: heads of more columns than threads
+  for (int c0 = 0; c0 < cols; c0 += threads) {  // more than one pass: heads of more columns than threads
     const int e = c0 + e0;
     const bool on = e < cols && k0 < split;
     const int g = on ? e / kV : 0, d = on ? e % kV : 0;
@@ -321,18 +320,26 @@ cudaError_t launch_simt(const SharedArgs& a, dim3 grid, cudaStream_t st) {
   return a.score.on ? launch_simt<T, D, true>(a, grid, st) : launch_simt<T, D, false>(a, grid, st);
 }
 
-template <typename T, int D>
+template <typename T, int D, int threads>
 cudaError_t launch_join(const SharedArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.num_seqs * a.pv.kv_heads));
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_join_kernel<T, D>, a);
+  return cudaLaunchKernelEx(&cfg, shared_join_kernel<T, D, threads>, a);
+}
+
+// Few heads: more threads for each, which share its parts (96 heads of 8 queries and 22 parts: 10 us with 128 threads, 4.5 with 512;
+// 1024 heads of 8 and 6 parts: 8.5 with 128, 10.8 with 256 of as many registers as 512 want).
+template <typename T, int D>
+cudaError_t launch_join(const SharedArgs& a, cudaStream_t st) {
+  const int64_t ctas = (int64_t)a.num_seqs * a.pv.kv_heads;
+  return ctas <= 200 ? launch_join<T, D, 512>(a, st) : ctas <= 800 ? launch_join<T, D, 256>(a, st) : launch_join<T, D, 128>(a, st);
 }
 
 }  // namespace

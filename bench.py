@@ -38,8 +38,8 @@ FALLBACK_HBM_GBS = 6800.0
 # stream-K decode kernel, with the sha256 of its sources (DECODE_SOURCES, in that order) it was
 # taken on.  When the kernel source changes the figure no longer applies and is reported as null.
 DECODE_SOURCES = ("hwkv_decode_tc.cu", "hwkv_decode_sk.cuh", "hwkv_decode_merge.cuh", "hwkv_decode_tile.cuh")
-DECODE_TRAFFIC = {"source_sha256": "8d7d18e6a7abb7cc63f681a84e0b95c219e365762ff9c88eef7164c1359d3f96",
-                  "bytes_per_launch": (621.376256 + 3.041024 + 489.206784 + 0.169472) / 2 * 1e6,
+DECODE_TRAFFIC = {"source_sha256": "1330b6b0e5fcde38a39780e721c34313ea4a2e16cec79fe7ce744c8b0a98a7c8",
+                  "bytes_per_launch": (621.369344 + 2.720000 + 489.206016 + 0.175104) / 2 * 1e6,
                   "launch": "layers 0 and 1 of the full workload (2-layer run, same per-launch shape)"}
 
 

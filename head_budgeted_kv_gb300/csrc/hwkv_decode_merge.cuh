@@ -1,5 +1,5 @@
 // The line of tiles the stream-K decode kernels split over their CTAs, and the merges of the
-// partial results (hwkv_decode_sk.cuh for bf16 and fp32 pools, hwkv_decode_q8.cu for 8-bit ones).
+// partial results (hwkv_decode_sk.cuh for bf16 and fp32 pools, hwkv_decode_q8.cuh for 8-bit ones).
 #pragma once
 
 #include "hwkv_decode_tile.cuh"

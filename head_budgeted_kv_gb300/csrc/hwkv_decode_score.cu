@@ -1,5 +1,5 @@
 // The stream-K decode kernel (hwkv_decode_sk.cuh) with capped or distance-biased scores, for bf16
-// and fp32 pools (8-bit pools: hwkv_decode_q8.cu).  A tile's scores change between the two
+// and fp32 pools (8-bit pools: hwkv_decode_q8.cuh).  A tile's scores change between the two
 // products, cap * tanh(s / cap) - slope * distance per score, in registers: no more bytes move.
 //
 // Bound: HBM, as the plain instances (eight sequences at 32K, 445 MB: cap 50 75.5 us, uncapped 75; fp32, 890

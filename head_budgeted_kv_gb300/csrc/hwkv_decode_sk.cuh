@@ -1,7 +1,7 @@
 // Stream-K split-K decode attention over per-head paged rings (block_size % 16 == 0, head_dim
 // 64 or 128), optionally fused with the append of the step's new token: tile work on the
 // tensor cores for bf16 pools (up to 16 query heads per KV head), on the CUDA cores for fp32
-// pools (up to 4).  (8-bit pools: hwkv_decode_q8.cu, the same line of tiles and merges.)
+// pools (up to 4).  (8-bit pools: hwkv_decode_q8.cuh, the same line of tiles and merges.)
 //
 // "HeadWiseKV: Budgeted Per-Head Cache Residency for Hybrid Long-Context Language Models",
 // abstract and section "Grouped-Cache Runtime": attention reads only the materialised window

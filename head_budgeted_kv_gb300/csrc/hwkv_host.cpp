@@ -1250,7 +1250,7 @@ SharedPlan plan_shared(const hwkv_pool* p, const hwkv_pool* prefix, int layer, i
 
 // Regions of the workspace: the own decode's, its open results, the prefixes' partials and their records.
 struct SharedLayout {
-  int chain_rows = 0;  // tensor cores: rows of a chain's partial
+  int chain_rows = 0, slots = 0;  // tensor cores: rows of a chain's partial, and slots of two chains
   uint64_t split_acc = 0, split_ml = 0;  // the own parts' partials on the CUDA cores
   uint64_t own_acc = 0, own_ml = 0, part_o = 0, part_ml = 0, rec = 0, total = 0;
 };
@@ -1266,7 +1266,8 @@ SharedLayout shared_layout(const hwkv_pool* p, const hwkv_pool* prefix, int grou
     const uint64_t QT = (uint64_t)shared_tc_seqs(group);
     const uint64_t items = H * (std::min<uint64_t>((uint64_t)prefix->g.num_seqs, B) + B / (2 * QT));
     w.chain_rows = (int)(std::min<uint64_t>(QT, B) * group);
-    parts = (items + (uint64_t)p->num_sms) * 2 * (uint64_t)w.chain_rows;
+    w.slots = (int)(items + (uint64_t)p->num_sms);
+    parts = (uint64_t)w.slots * 2 * (uint64_t)w.chain_rows;
   } else {
     for (int l = 0; l < p->g.layers; ++l) parts = std::max<uint64_t>(parts, plan_shared(p, prefix, l, group).chunks);
     parts *= B * (uint64_t)group;
@@ -1393,6 +1394,7 @@ int hwkv_decode_attn_shared(hwkv_pool_t p, hwkv_pool_t prefix, int layer, const 
   a.part_ml = reinterpret_cast<float*>(ws + wl.part_ml);
   a.rec = reinterpret_cast<int4*>(ws + wl.rec);
   a.chain_rows = wl.chain_rows;
+  a.slots = wl.slots;
   NvtxRange range_("hwkv_decode_attn_shared", layer);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (shared_tc(prefix)) {

@@ -139,6 +139,7 @@ struct SharedArgs {
   int32_t bs_log2;         // log2(block_size), or -1 when it is not a power of two
   int32_t stage_tb;        // rows of one block in a 64-key pool copy (16, 32, 64), 0: per-tile copies only
   int32_t chain_rows;      // rows of a chain's partial
+  int32_t slots;           // slots of partials
   int32_t stage_ns;        // time of a stage
   int32_t own_ctas;        // CTAs of the own parts' kernel (0: it does not run beside), those an SM holds, a CTA's time and that per tile
   int32_t own_per_sm;

@@ -213,9 +213,12 @@ __global__ void __launch_bounds__(threads, threads == 512 ? 1 : 768 / threads) s
     // a record is there for every row that sees a key of the prefix
     const int4 rec = a.rec[blockIdx.x];
     if (min(prefix_len(a, f), a.g.window[h] - min(a.g.window[h], shared_len(a, s))) > 0) {
-      part0 = (int64_t)rec.x * a.chain_rows + rec.w;
-      step = (int64_t)rec.y * a.chain_rows;
-      parts = rec.z;
+      // (one left by a launch that gave up a wait may say anything: it is read only within the partials)
+      if (rec.x >= 0 && rec.y == 2 && rec.z >= 0 && rec.x + 2ll * rec.z < 2ll * a.slots + 2 && rec.w >= 0 && rec.w + G <= a.chain_rows) {
+        part0 = (int64_t)rec.x * a.chain_rows + rec.w;
+        step = (int64_t)rec.y * a.chain_rows;
+        parts = rec.z;
+      }
     }
   } else if (f >= 0) {
     const int chunks = a.chunk_prefix[H];

@@ -8,7 +8,8 @@ windowed attention (``hwkv_append_decode_attn``, or ``hwkv_append`` + ``hwkv_dec
 followed by the advance of the positions (``hwkv_advance_positions``), and replays that whole
 step with one launch from the host: every kernel of a replayed step is the library's.  With a
 rotary table each layer's queries and new keys are first turned at the step's positions
-(``hwkv_rope``).  Inputs are read from, and outputs written to, the static buffers it owns.
+(``hwkv_rope``).  Behind shared prefixes (``hwkv_decode_attn_shared``) they turn at the positions of the
+whole contexts and go into the pool on the way (``hwkv_rope_append``).  Inputs are read from, and outputs written to, the static buffers it owns.
 """
 from __future__ import annotations
 
@@ -25,10 +26,13 @@ class DecodeStepGraph:
     Output: out [layers][B][q_heads][D].
     rope: a ``rope_table`` when q and k_new come without their rotary positions.
     softcap, slopes: capped or distance-biased scores, as in ``Pool.decode``.
+    prefix, prefix_of, prefix_lens: sequences behind prefixes kept once, as in ``Pool.shared_decode``; pos then
+    counts a sequence's own tokens, and turn_pos [B] int32 (advanced with it) its positions in its whole context.
+    Whoever moves a sequence to another prefix writes prefix_of, pos and turn_pos between steps.
     """
 
     def __init__(self, pool, scale: float, q_heads: int, pos0, fused: bool = True, rope=None, softcap: float = 0.0,
-                 slopes=None):
+                 slopes=None, prefix=None, prefix_of=None, prefix_lens=None):
         dev = pool.buffer.device
         L, B, H, D = pool.layers, pool.num_seqs, pool.kv_heads, pool.head_dim
         dt = pool.io_dtype
@@ -42,6 +46,13 @@ class DecodeStepGraph:
         if q_heads != pool.q_heads:
             pool.q_heads = q_heads
             pool._size_workspace()
+        self.prefix = prefix
+        if prefix is not None:
+            self.prefix_of = torch.as_tensor(prefix_of, dtype=torch.int32, device=dev).clone()
+            self.prefix_lens = torch.as_tensor(prefix_lens, dtype=torch.int32, device=dev).clone()
+            f = self.prefix_of.long()
+            ahead = torch.where((f >= 0) & (f < prefix.num_seqs), self.prefix_lens[f.clamp(0, prefix.num_seqs - 1)], 0)
+            self.turn_pos = (self.pos + ahead).to(torch.int32)
         self.rope = rope
         self._score = {"softcap": softcap, "slopes": slopes}
         self._q, self._k = self.q, self.k_new  # what the attention reads
@@ -59,6 +70,9 @@ class DecodeStepGraph:
 
     def _record(self):
         p = self.pool
+        if self.prefix is not None:
+            self._record_shared()
+            return
         if not self.fused:
             p.advance_positions(self.pos, out=self.lens)  # lengths after the append
         for l in range(p.layers):
@@ -73,6 +87,22 @@ class DecodeStepGraph:
                 p.append(l, self._k[l], self.v_new[l], self.pos)
                 p.decode(l, self._q[l], self.scale, self.lens, out=self.out[l], **self._score)
         p.advance_positions(self.pos)  # the next step's positions
+
+    def _record_shared(self):
+        p = self.pool
+        behind = (self.prefix_of, self.prefix_lens)
+        if self.rope is not None:
+            p.advance_positions(self.pos, out=self.lens)  # lengths after the append
+        for l in range(p.layers):
+            if self.rope is not None:
+                p.rope_append(l, self.rope, self.q[l], self.k_new[l], self.v_new[l], self.pos, q_out=self._q[l],
+                              turn_pos=self.turn_pos)
+                p.shared_decode(l, self.prefix, self._q[l], self.scale, self.lens, *behind, out=self.out[l], **self._score)
+            else:
+                p.shared_decode(l, self.prefix, self.q[l], self.scale, self.pos, *behind, k_new=self.k_new[l],
+                                v_new=self.v_new[l], out=self.out[l], **self._score)
+        p.advance_positions(self.pos)  # the next step's positions
+        p.advance_positions(self.turn_pos)
 
     def replay(self):
         self.graph.replay()

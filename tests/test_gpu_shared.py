@@ -279,6 +279,53 @@ def test_captured_steps_move_on(types):
     assert c.own.pool.check_device_errors() == 0 and d.own.pool.check_device_errors() == 0
 
 
+@pytest.mark.parametrize("rope", [False, True], ids=["plain", "rope"])
+@pytest.mark.parametrize("types", [(BF16, BF16), (E4M3, E4M3), (F32, F32)], ids=["bf16", "e4m3", "f32"])
+def test_step_graph_behind_prefixes(types, rope):
+    """DecodeStepGraph over two layers equals the calls one by one, token after token, past the own windows."""
+    from head_budgeted_kv_gb300.graph import DecodeStepGraph
+    own, pre, lens, pre_lens, of = [[24, 40], [16, 8]], [[200, 90], [64, 300]], [0, 5, 30], [150, 33], [1, -1, 0]
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def pools():
+        a, b = hw.Pool(2, 2, 64, 16, own, 3, types[0], q_heads=8), hw.Pool(2, 2, 64, 16, pre, 2, types[1], q_heads=8)
+        g = torch.Generator(device="cuda").manual_seed(2)
+        for p, n, ls in ((a, 40, lens), (b, 160, pre_lens)):
+            for layer in range(2):
+                k, v = (torch.randn((p.num_seqs, 2, n, 64), generator=g, device="cuda").to(p.io_dtype) for _ in range(2))
+                p.materialize(layer, k, v, i32(ls))
+        return a, b
+
+    (a, pa), (b, pb) = pools(), pools()
+    table = hw.rope_table(64) if rope else None
+    step = DecodeStepGraph(a, 0.125, 8, lens, rope=table, prefix=pa, prefix_of=of, prefix_lens=pre_lens)
+    assert step.turn_pos.tolist() == [33, 5, 180]
+    for i in range(50):
+        q, k, v = (torch.randn(t.shape, generator=gen, device="cuda").to(a.io_dtype) for t in (step.q, step.k_new, step.v_new))
+        step.q.copy_(q), step.k_new.copy_(k), step.v_new.copy_(v)
+        step.replay()
+        pos, turn = i32([n + i for n in lens]), i32([n + i for n in (33, 5, 180)])
+        for layer in range(2):
+            if rope:
+                qq, _ = b.rope_append(layer, table, q[layer], k[layer], v[layer], pos, turn_pos=turn)
+                out = b.shared_decode(layer, pb, qq, 0.125, pos + 1, i32(of), i32(pre_lens))
+            else:
+                out = b.shared_decode(layer, pb, q[layer], 0.125, pos, i32(of), i32(pre_lens), k_new=k[layer].contiguous(),
+                                      v_new=v[layer].contiguous())
+            assert torch.equal(out, step.out[layer]), (i, layer)
+    assert torch.equal(a.blocks().view(torch.uint8), b.blocks().view(torch.uint8))
+    assert a.check_device_errors() == 0
+
+
+def test_output_in_place_of_the_queries():
+    for types in ((BF16, BF16), (F32, F32)):
+        c = Case([64], [900], [3, 60, 17], [800], [0, 0, -1], 4, 128, types=types, seed=4)
+        want = c.call().clone()
+        q = c.q.clone()
+        got = c.own.pool.shared_decode(0, c.pre.pool, q, c.scale, i32(c.own.lens), i32(c.of), i32(c.pre.lens), out=q)
+        assert got is q and torch.equal(q, want)
+
+
 def test_two_pools_share_a_prefix_on_two_streams():
     a = Case([64], [900], [3, 60, 17], [800], [0, 0, 0], 4, 128, seed=4)
     b = Case([64], [900], [3, 60, 17], [800], [0, 0, 0], 4, 128, seed=4)

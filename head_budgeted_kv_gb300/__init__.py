@@ -11,6 +11,7 @@ is a convenience wrapper that owns the device buffers (allocated with torch).
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from typing import Optional
 
 import torch
@@ -59,8 +60,11 @@ def rope_table(head_dim: int, rot_dim: Optional[int] = None, base: float = 10000
                            beta_slow)
 
 
-# The check alone, without the one of torch.cuda that a device is initialised: a pool is on one.
-_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+def _on(stream):
+    """Where tensors that a call on ``stream`` makes are allocated and filled."""
+    if stream is None:
+        return nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 class Pool:
@@ -96,8 +100,7 @@ class Pool:
         self.prefill_workspace = None
         self._prefill_captured = False
         self.shared_workspace = None
-        self._shared_captured = False
-        self._outgrown = []  # workspaces that captured graphs may still use
+        self._outgrown = []  # workspaces that captured graphs (or other streams) may still use
         self._size_workspace()
 
     def _size_workspace(self):
@@ -190,9 +193,10 @@ class Pool:
         lens[s] tokens of its own in this pool (after the append; with k_new and v_new [B][Hkv][D] the length before it) behind
         the prefix_lens[f] tokens of prefix f = prefix_of[s] (negative: behind none).  int32 [B], [B] and
         [prefix.num_seqs].  softcap, slopes: as ``decode``.  Keeps a workspace, grown on demand; one that
-        a capture has used stays when it is outgrown."""
+        is outgrown stays, for a captured graph or another stream may still use it.  What is allocated belongs to ``stream``."""
         if out is None:
-            out = torch.empty_like(q)
+            with _on(stream):
+                out = torch.empty_like(q)
         if (k_new is None) != (v_new is None):
             raise ValueError("k_new and v_new go together")
         shape = q.shape
@@ -206,8 +210,6 @@ class Pool:
         if not (self._is_counts(lens) and self._is_counts(prefix_of) and prefix._is_counts(prefix_lens)):
             raise ValueError(f"lens and prefix_of must hold {self.num_seqs} values, prefix_lens {prefix.num_seqs}, in a row on "
                              f"{self.buffer.device}")
-        if _capturing():
-            self._shared_captured = True
         args = (layer, q, binding.score(scale, softcap, slopes, q), lens, prefix_of, prefix_lens, out)
         if self.shared_workspace is not None:
             try:
@@ -216,11 +218,10 @@ class Pool:
             except HwkvError as e:
                 if e.status != binding.HWKV_ERR_WORKSPACE_TOO_SMALL:
                     raise
-                if self._shared_captured:
-                    self._outgrown.append(self.shared_workspace)
+                self._outgrown.append(self.shared_workspace)
         need = hwkv_decode_shared_workspace_bytes(self.handle, prefix.handle, q.shape[1])
-        self.shared_workspace = torch.empty(need, dtype=torch.uint8, device=self.buffer.device)
-        self._shared_captured = _capturing()
+        with _on(stream):
+            self.shared_workspace = torch.empty(need, dtype=torch.uint8, device=self.buffer.device)
         hwkv_decode_attn_shared(self.handle, prefix.handle, *args, self.shared_workspace, k_new, v_new, stream)
         return out
 
@@ -296,14 +297,15 @@ class Pool:
         """Rotary positions on the way into the pool, in one launch: q [B][n_max][Hq][D] and k [B][n_max][Hkv][D]
         (or single rows [B][heads][D]) turn at positions turn_pos[s] + row (pos[s] + row by default), and the
         turned k and v are stored at positions pos[s] + row, rows below n[s] (all when n is None).  q may be None;
-        table None turns nothing.  q_out defaults to a new tensor (zeros past n); pass q_out=q to work in place.
+        table None turns nothing.  q_out defaults to a new tensor of ``stream`` (zeros past n); pass q_out=q to work in place.
         k_out, when given, receives the turned keys too.  Returns (q_out, k_out)."""
         at = self._device_index
         if q is not None:
             if self._check_rows(q, "q") % self.kv_heads:
                 raise ValueError(f"q must hold a multiple of {self.kv_heads} heads")
             if q_out is None:
-                q_out = (torch.empty if n is None else torch.zeros)(q.shape, dtype=q.dtype, device=q.device)
+                with _on(stream):
+                    q_out = (torch.empty if n is None else torch.zeros)(q.shape, dtype=q.dtype, device=q.device)
             elif q_out.get_device() != at:
                 raise ValueError(f"outputs must lie on {self.buffer.device}")
         elif q_out is not None:

@@ -60,7 +60,9 @@ enum { kRopeHalf = 0, kRopeInterleaved = 1, kRopeHalfAny = 2 };
 //
 // kAppend: keys and values go to their ring slots instead of an output; a row's heads are the queries,
 // the keys and the values, and a value's vectors pass as they are.  The slots of the CTA's rows are
-// looked up once per head, beside the angles.
+// looked up once per head, beside the angles.  4 sequences of 2048 rows, 32 + 8 + 8 heads of 128 in bf16: 151 MB in
+// 26.5-27.6 us, 0.82-0.85 of the measured copy rate (a turn and the appends in separate launches move 42 MB more);
+// one token 3.8 us.
 template <typename T, int kLayout, bool kWide, bool kAppend>
 __global__ void __launch_bounds__(RopeShape<kWide>::kThreads)
     rope_kernel(const __grid_constant__ std::conditional_t<kAppend, RopeAppendArgs, RopeArgs> a) {

@@ -58,6 +58,10 @@ struct Cfg {
   static constexpr int kKBytes = kKeys * D * 2;
   static constexpr int kStageBytes = 2 * kKBytes;
   static constexpr int kStages = (D == 128 ? 4 : 8) - (Q8 ? (D == 128 ? 1 : 2) : 0);
+  // An issuer of S that takes every other stage does not see each phase of a slot.  The parity it waits for tells phases
+  // k - 1 and k + 1 apart only if it knows that the stage kStages before has arrived: that was its own where kStages is
+  // even; codes are converted in order, so there it came before the issuer's last one.  (Copies land in any order.)
+  static_assert(Q8 ? kStages >= 3 : kStages % 2 == 0, "an issuer may take a slot for full before its copy has landed");
   static constexpr int kStageOff = 2 * kQBytes;
   // 8-bit: stages of codes, four tiles of 16 K and 16 V rows each
   static constexpr int kTileBytes = 2 * kTile * D;

@@ -284,7 +284,9 @@ int hwkv_decode_attn_score(hwkv_pool_t pool, int layer, const void* q, int q_hea
  *   recorded in `pool`.
  *   k_new, v_new (both or neither): appended to the own pool first, lens_dev then holding the own lengths before the
  *   append, as in hwkv_decode_attn_ex.  score: as hwkv_decode_attn_score (a prefix key's distance counts the
- *   tokens of both pools); nothing to attend to gives zeros.
+ *   tokens of both pools, and slopes beyond 9.08e4 -- 2^17 log2 units a token -- count as that: no result shows it);
+ *   nothing to attend to gives zeros.  Stored keys and values must be finite, as for every call: the prefix's are operands of
+ *   products over all sequences behind it.
  *   workspace: hwkv_decode_shared_workspace_bytes() bytes, otherwise as for hwkv_decode_attn.
  * Three kernels on `stream` or more: the prefixes' keys, the own parts, their join.  Concurrent launches of the same
  * layer of `pool` race, decode calls included; `prefix` may be shared by any number of launches that only read it.
@@ -458,7 +460,7 @@ int hwkv_rope(hwkv_pool_t pool, const hwkv_rope_t* rope, const hwkv_rows_t* q, i
  * bf16 and fp32 pools hold what hwkv_rope and then hwkv_append of each row in turn leave, bit for bit.  8-bit pools store every
  * group of 16 slots that a row goes to once, anew: the slots whose positions are in the window of the new length take their row,
  * rounded once from the turned fp32 value, or keep their value at the new scale; every other slot becomes zero.
- * One kernel on `stream`.
+ * One kernel on `stream`.  It writes the pool: the call right behind it may not have HWKV_DECODE_EARLY_READS.
  * Errors: HWKV_ERR_INVALID_ARG, HWKV_ERR_ALIGNMENT, HWKV_ERR_UNSUPPORTED, HWKV_ERR_CUDA. */
 int hwkv_rope_append(hwkv_pool_t pool, int layer, const hwkv_rope_t* rope, const hwkv_rows_t* q, int q_heads,
                      const hwkv_rows_t* k, const hwkv_rows_t* v, int n_max, const int32_t* pos_dev,

@@ -287,6 +287,22 @@ def test_values_that_are_not_finite():
         np.testing.assert_array_equal(x, y)
 
 
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_new_outputs_belong_to_the_stream_of_the_call(raw):
+    """Zeros past n are filled on the stream that turns the rows, not on a current stream that is behind."""
+    c = Case([40, 100], 2, 1, 128, 16, torch.bfloat16, seed=2)
+    q, k, v = c.randn(2, 33, 4, 128), c.randn(2, 33, 2, 128), c.randn(2, 33, 2, 128)
+    table, pos, n = hw.rope_table(128), i32([9, 200]), i32([33, 12])
+    want, _ = c.pool.rope_append(0, table, q, k, v, pos, n)
+    want = want.clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(50_000_000)  # tens of milliseconds
+    got, _ = c.pool.rope_append(0, table, q, k, v, pos, n, stream=side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and not got[1, 12:].any()
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 def test_captured_chunks_move_on(dtype):
     """A captured call replays at the positions of the moment, as eager calls do; another stream than the current one."""

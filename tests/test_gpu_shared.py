@@ -341,6 +341,23 @@ def test_two_pools_share_a_prefix_on_two_streams():
         assert torch.equal(x, want_a) and torch.equal(y, want_b)
 
 
+def test_what_a_call_allocates_belongs_to_its_stream():
+    """Memory that the current stream freed and still reads is not the workspace or output of a call on another stream."""
+    c = Case([64], [900], [3, 60, 17], [800], [0, 0, -1], 4, 128, seed=4)
+    need = hw.binding.hwkv_decode_shared_workspace_bytes(c.own.pool.handle, c.pre.pool.handle, c.q.shape[1])
+    lens, of, pre_lens = i32(c.own.lens), i32(c.of), i32(c.pre.lens)
+    held = [torch.ones(need, dtype=torch.uint8, device="cuda"), torch.ones_like(c.q)]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()  # no other free block fits as well
+    torch.cuda._sleep(50_000_000)  # tens of milliseconds
+    read = [t.clone() for t in held]
+    t = held = None
+    got = c.own.pool.shared_decode(0, c.pre.pool, c.q, c.scale, lens, of, pre_lens, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert all(bool((t == 1).all()) for t in read)
+    assert torch.equal(got, c.call())
+
+
 def test_the_workspace_grows_and_other_pools_take_turns():
     """One own pool behind small and large prefix pools, other groups of heads, other decode settings."""
     c = Case([64, 64], [300, 300], [3, 60, 17], [200], [0, 0, 0], 2, 64, seed=4)

@@ -20,8 +20,8 @@
 //
 // Bound: HBM for chunks, the launch for tokens.  4 sequences of 2048 rows, 32 + 8 + 8 heads of 128 with turned keys out:
 // 151 MB in 37 us, 0.61 of the measured copy rate (an angle's sine and cosine, two conversions per element and the scale's
-// reduction share the issue slots with the copies: half of them taken).  From 67: queries at four units a thread, not one
-// (48), a warp's rows all loaded before the angles, which are computed once per tile in shared memory.
+// reduction share the issue slots with the copies: half of them taken).  It was 67 before CTAs took two heads or some
+// query rows with four loads ahead (48), and 48 before the angles' vectors in shared memory avoided each other's banks.
 // 64 tokens: 11 us alone with cold caches.
 #include <algorithm>
 

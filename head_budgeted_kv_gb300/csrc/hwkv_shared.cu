@@ -22,7 +22,9 @@ constexpr int kThreads = 128;  // four per row
 
 // CTA = (prefix, head, chunk of ring slots; sequences).  A pass brings 32 keys and values into shared memory; the four
 // threads of a row take eight scores each, the row's maximum and sum over them by shuffles, then a quarter
-// of head_dim each of the weighted sum.  fp32 throughout.
+// of head_dim each of the weighted sum.  fp32 throughout.  Bound: latency of the passes for few keys, fp32 work and shared memory
+// reads for many.  6 sequences behind two prefixes of up to 3K tokens in fp32, with own parts and join: 45 us
+// (142 with larger chunks and 4-byte loads).
 template <typename T, int D, bool SC>
 __global__ void __launch_bounds__(kThreads) shared_simt_kernel(const __grid_constant__ SharedArgs a) {
   constexpr int kLd = D + 4;  // floats per row in shared memory: rows 16 bytes apart in the banks
@@ -191,7 +193,8 @@ constexpr int simt_smem() {
 // The join, a CTA per (sequence, KV head): out = sum_i acc_i 2^(m_i - M) / sum_i l_i 2^(m_i - M) over the head's own
 // partial and its prefix's, M = max_i m_i; nothing to attend to gives zeros.  A thread sums four columns of a head over every
 // kSplit'th part, the states and sums of kAhead parts on their way at once; where a head has more
-// threads than columns, their sums meet in shared memory.  The order of all sums is fixed.
+// threads than columns, their sums meet in shared memory.  The order of all sums is fixed.  Bound: two dependent loads and L2;
+// 16 sequences of 8 heads, 78 partials: 5 us, 128 sequences of 8: 8.5.
 constexpr int kAhead = 8;
 
 template <typename T, int D, int threads>

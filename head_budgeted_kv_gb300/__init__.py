@@ -193,7 +193,8 @@ class Pool:
         lens[s] tokens of its own in this pool (after the append; with k_new and v_new [B][Hkv][D] the length before it) behind
         the prefix_lens[f] tokens of prefix f = prefix_of[s] (negative: behind none).  int32 [B], [B] and
         [prefix.num_seqs].  softcap, slopes: as ``decode``.  Keeps a workspace, grown on demand; one that
-        is outgrown stays, for a captured graph or another stream may still use it.  What is allocated belongs to ``stream``."""
+        is outgrown stays, for a captured graph or another stream may still use it.  The calls of a pool share it: no two at
+        once, on two streams or in two graphs.  What is allocated belongs to ``stream``."""
         if out is None:
             with _on(stream):
                 out = torch.empty_like(q)

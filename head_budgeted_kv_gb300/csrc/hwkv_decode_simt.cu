@@ -165,6 +165,9 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_simt_kernel(const __gr
       }
     }
   }
+  // Open results (a decode behind shared prefixes): this grid runs beside the prefixes' kernel, of which it needs nothing; its
+  // last CTA waits for that one, so that what follows this grid follows both.
+  if (a.open_acc != nullptr && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) griddep_wait();
 }
 
 // split-K combine: one CTA per (seq, kv head) whose ring spans several chunks
@@ -206,13 +209,20 @@ namespace {
 template <bool SC>
 cudaError_t launch_simt(const DecodeArgs& a, int dtype, int items, cudaStream_t st) {
   const int D = a.pv.head_dim;
-  const dim3 grid((unsigned)items, (unsigned)((a.group + kSimtHeads - 1) / kSimtHeads));
-  if (dtype == HWKV_F32 && D == 64) decode_simt_kernel<float, 64, SC><<<grid, kSimtWarps * 32, 0, st>>>(a);
-  else if (dtype == HWKV_F32 && D == 128) decode_simt_kernel<float, 128, SC><<<grid, kSimtWarps * 32, 0, st>>>(a);
-  else if (dtype == HWKV_BF16 && D == 64) decode_simt_kernel<__nv_bfloat16, 64, SC><<<grid, kSimtWarps * 32, 0, st>>>(a);
-  else if (dtype == HWKV_BF16 && D == 128) decode_simt_kernel<__nv_bfloat16, 128, SC><<<grid, kSimtWarps * 32, 0, st>>>(a);
-  else return cudaErrorInvalidValue;
-  return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)items, (unsigned)((a.group + kSimtHeads - 1) / kSimtHeads));
+  cfg.blockDim = dim3(kSimtWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.open_acc != nullptr ? 1 : 0;  // open: beside the prefixes' kernel
+  if (dtype == HWKV_F32 && D == 64) return cudaLaunchKernelEx(&cfg, decode_simt_kernel<float, 64, SC>, a);
+  if (dtype == HWKV_F32 && D == 128) return cudaLaunchKernelEx(&cfg, decode_simt_kernel<float, 128, SC>, a);
+  if (dtype == HWKV_BF16 && D == 64) return cudaLaunchKernelEx(&cfg, decode_simt_kernel<__nv_bfloat16, 64, SC>, a);
+  if (dtype == HWKV_BF16 && D == 128) return cudaLaunchKernelEx(&cfg, decode_simt_kernel<__nv_bfloat16, 128, SC>, a);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace

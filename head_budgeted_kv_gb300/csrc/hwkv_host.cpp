@@ -1148,7 +1148,21 @@ int prepare_decode(hwkv_pool_t p, int layer, const void* q, int q_heads, hwkv_sc
   return HWKV_OK;
 }
 
-// Launches a prepared decode (open when a.open_acc is set).
+// Appends the new rows of a decode that does not append them itself.
+int launch_append_of(hwkv_pool_t p, const DecodeCall& call, cudaStream_t st) {
+  if (call.tc || !call.k_new) return HWKV_OK;
+  CopyArgs c;
+  std::memset(&c, 0, sizeof c);
+  c.pv = call.a.pv;
+  c.g = call.a.g;
+  c.k = call.k_new;
+  c.v = call.v_new;
+  c.lens = call.a.lens;
+  HWKV_CUDA_TRY(launch_append(c, p->g.dtype, st), "append launch");
+  return HWKV_OK;
+}
+
+// Launches a prepared decode (open when a.open_acc is set: its rows are appended already).
 int launch_decode(hwkv_pool_t p, DecodeCall& call, cudaStream_t st) {
   DecodeArgs& a = call.a;
   const Geometry& g = p->g;
@@ -1159,15 +1173,9 @@ int launch_decode(hwkv_pool_t p, DecodeCall& call, cudaStream_t st) {
                   "decode launch");
     return HWKV_OK;
   }
-  if (call.k_new) {
-    CopyArgs c;
-    std::memset(&c, 0, sizeof c);
-    c.pv = a.pv;
-    c.g = a.g;
-    c.k = call.k_new;
-    c.v = call.v_new;
-    c.lens = a.lens;
-    HWKV_CUDA_TRY(launch_append(c, g.dtype, st), "append launch");
+  if (!a.open_acc) {
+    const int rc = launch_append_of(p, call, st);
+    if (rc != HWKV_OK) return rc;
   }
   HWKV_CUDA_TRY(launch_decode_simt(a, g.dtype, call.items, st), "decode launch");
   if (call.multi_chunk) HWKV_CUDA_TRY(launch_combine(a, g.dtype, st), "combine launch");
@@ -1397,6 +1405,9 @@ int hwkv_decode_attn_shared(hwkv_pool_t p, hwkv_pool_t prefix, int layer, const 
   a.slots = wl.slots;
   NvtxRange range_("hwkv_decode_attn_shared", layer);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // before the prefixes' kernel: what runs beside it needs nothing of it
+  rc = launch_append_of(p, call, st);
+  if (rc != HWKV_OK) return rc;
   if (shared_tc(prefix)) {
     a.tc = 1;
     a.bs_log2 = log2_of(prefix->g.block_size);

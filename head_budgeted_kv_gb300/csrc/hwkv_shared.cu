@@ -36,6 +36,8 @@ __global__ void __launch_bounds__(kThreads) shared_simt_kernel(const __grid_cons
   __shared__ int s_seq[kRows];
   __shared__ int s_count;
 
+  griddep_launch_dependents();  // the own parts may start beside: all before this grid has completed
+
   const int H = a.pv.kv_heads, G = a.group, bs = a.pv.block_size;
   const int chunks = a.chunk_prefix[H];
   const int f = (int)blockIdx.x / chunks;

@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_simt_kernel(const __gr
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = blockIdx.x;
+  if (a.open_acc != nullptr) griddep_launch_dependents();  // they wait for this grid
   const Item it = decode_item(a, item);
   int len = a.lens[it.s] + a.len_add;
   if (len < 0) {
@@ -173,6 +174,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_simt_kernel(const __gr
 // split-K combine: one CTA per (seq, kv head) whose ring spans several chunks
 template <typename T, int D>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ DecodeArgs a) {
+  if (a.open_acc != nullptr) griddep_wait();
   const int H = a.pv.kv_heads;
   const int s = blockIdx.x / H, h = blockIdx.x - (blockIdx.x / H) * H;
   const int nch = a.chunk_prefix[h + 1] - a.chunk_prefix[h];
@@ -206,22 +208,30 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ De
 
 namespace {
 
-template <bool SC>
-cudaError_t launch_simt(const DecodeArgs& a, int dtype, int items, cudaStream_t st) {
-  const int D = a.pv.head_dim;
+// open: beside or right behind the kernel ahead
+template <typename Kernel>
+cudaError_t launch_after(Kernel* kernel, const DecodeArgs& a, dim3 grid, int threads, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)items, (unsigned)((a.group + kSimtHeads - 1) / kSimtHeads));
-  cfg.blockDim = dim3(kSimtWarps * 32);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.open_acc != nullptr ? 1 : 0;  // open: beside the prefixes' kernel
-  if (dtype == HWKV_F32 && D == 64) return cudaLaunchKernelEx(&cfg, decode_simt_kernel<float, 64, SC>, a);
-  if (dtype == HWKV_F32 && D == 128) return cudaLaunchKernelEx(&cfg, decode_simt_kernel<float, 128, SC>, a);
-  if (dtype == HWKV_BF16 && D == 64) return cudaLaunchKernelEx(&cfg, decode_simt_kernel<__nv_bfloat16, 64, SC>, a);
-  if (dtype == HWKV_BF16 && D == 128) return cudaLaunchKernelEx(&cfg, decode_simt_kernel<__nv_bfloat16, 128, SC>, a);
+  cfg.numAttrs = a.open_acc != nullptr ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <bool SC>
+cudaError_t launch_simt(const DecodeArgs& a, int dtype, int items, cudaStream_t st) {
+  const int D = a.pv.head_dim;
+  const dim3 grid((unsigned)items, (unsigned)((a.group + kSimtHeads - 1) / kSimtHeads));
+  constexpr int threads = kSimtWarps * 32;
+  if (dtype == HWKV_F32 && D == 64) return launch_after(decode_simt_kernel<float, 64, SC>, a, grid, threads, st);
+  if (dtype == HWKV_F32 && D == 128) return launch_after(decode_simt_kernel<float, 128, SC>, a, grid, threads, st);
+  if (dtype == HWKV_BF16 && D == 64) return launch_after(decode_simt_kernel<__nv_bfloat16, 64, SC>, a, grid, threads, st);
+  if (dtype == HWKV_BF16 && D == 128) return launch_after(decode_simt_kernel<__nv_bfloat16, 128, SC>, a, grid, threads, st);
   return cudaErrorInvalidValue;
 }
 
@@ -235,13 +245,14 @@ cudaError_t launch_decode_simt(const DecodeArgs& a, int dtype, int items, cudaSt
 }
 
 cudaError_t launch_combine(const DecodeArgs& a, int dtype, cudaStream_t st) {
-  const int blocks = a.pv.num_seqs * a.pv.kv_heads;
+  const dim3 grid((unsigned)(a.pv.num_seqs * a.pv.kv_heads));
   const int D = a.pv.head_dim;
-  if (dtype == HWKV_F32 && D == 64) combine_kernel<float, 64><<<blocks, 256, 0, st>>>(a);
-  else if (dtype == HWKV_F32 && D == 128) combine_kernel<float, 128><<<blocks, 256, 0, st>>>(a);
-  else if (dtype == HWKV_BF16 && D == 64) combine_kernel<__nv_bfloat16, 64><<<blocks, 256, 0, st>>>(a);
-  else if (dtype == HWKV_BF16 && D == 128) combine_kernel<__nv_bfloat16, 128><<<blocks, 256, 0, st>>>(a);
-  else return cudaErrorInvalidValue;
+  cudaError_t e = cudaErrorInvalidValue;
+  if (dtype == HWKV_F32 && D == 64) e = launch_after(combine_kernel<float, 64>, a, grid, 256, st);
+  else if (dtype == HWKV_F32 && D == 128) e = launch_after(combine_kernel<float, 128>, a, grid, 256, st);
+  else if (dtype == HWKV_BF16 && D == 64) e = launch_after(combine_kernel<__nv_bfloat16, 64>, a, grid, 256, st);
+  else if (dtype == HWKV_BF16 && D == 128) e = launch_after(combine_kernel<__nv_bfloat16, 128>, a, grid, 256, st);
+  if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
 }

@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(kThreads) shared_simt_kernel(const __grid_cons
   __shared__ int s_seq[kRows];
   __shared__ int s_count;
 
+  griddep_wait();
   griddep_launch_dependents();  // the own parts may start beside: all before this grid has completed
 
   const int H = a.pv.kv_heads, G = a.group, bs = a.pv.block_size;
@@ -319,8 +320,17 @@ cudaError_t launch_simt(const SharedArgs& a, dim3 grid, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     prepared.fetch_or(bit, std::memory_order_relaxed);
   }
-  shared_simt_kernel<T, D, SC><<<grid, kThreads, simt_smem<D>(), st>>>(a);
-  return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)simt_smem<D>();
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_simt_kernel<T, D, SC>, a);
 }
 
 template <typename T, int D>

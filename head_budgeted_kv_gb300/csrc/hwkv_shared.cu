@@ -23,8 +23,8 @@ constexpr int kThreads = 128;  // four per row
 // CTA = (prefix, head, chunk of ring slots; sequences).  A pass brings 32 keys and values into shared memory; the four
 // threads of a row take eight scores each, the row's maximum and sum over them by shuffles, then a quarter
 // of head_dim each of the weighted sum.  fp32 throughout.  Bound: latency of the passes for few keys, fp32 work and shared memory
-// reads for many.  6 sequences behind two prefixes of up to 3K tokens in fp32, with own parts and join: 45 us
-// (142 with larger chunks and 4-byte loads).
+// reads for many.  6 sequences behind two prefixes of up to 3K tokens in fp32, with own parts and join: 28 us
+// (142 with larger chunks and 4-byte loads; 45 with the own parts behind this kernel, not beside it).
 template <typename T, int D, bool SC>
 __global__ void __launch_bounds__(kThreads) shared_simt_kernel(const __grid_constant__ SharedArgs a) {
   constexpr int kLd = D + 4;  // floats per row in shared memory: rows 16 bytes apart in the banks

@@ -381,6 +381,22 @@ def test_results_do_not_change_from_call_to_call():
         assert torch.equal(c.call(), first)
 
 
+@pytest.mark.parametrize("types,bs", [((F32, F32), 5), ((F32, F32), 16), ((BF16, BF16), 24)])
+def test_cuda_core_results_do_not_change_and_see_the_row_just_appended(types, bs):
+    """The own parts run beside the prefixes' kernel: their new rows are stored before either."""
+    c = Case([300, 40], [3000, 300], [(7 * i) % 290 for i in range(24)], [2500, 100], [i % 2 for i in range(24)], 8, 128, bs, types, seed=9)
+    k, v = c.new_rows()
+    lens, of, pre_lens = i32(c.own.lens), i32(c.of), i32(c.pre.lens)
+    outs = []
+    for i in range(20):
+        if i % 2:  # other rows in their place
+            c.own.pool.append(0, torch.zeros_like(k), torch.zeros_like(v), lens)
+        outs.append(c.own.pool.shared_decode(0, c.pre.pool, c.q, c.scale, lens, of, pre_lens, k_new=k, v_new=v))
+    c.own.append(k, v)
+    c.check(outs[0], seqs=[0, 1, 23])
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
 def test_refusals():
     B = hw.binding
     c = Case([32], [64], [4, 5], [20], [0, 0], 4, 64, seed=2)

@@ -212,9 +212,10 @@ __device__ __forceinline__ void store_part(float* p, const float (&o)[32]) {
 // What is done to the scores between the two products, an instance each.
 enum { kPlain = 0, kCap = 1, kBias = 2 };
 
-// The steepest slope of a bias, 2^17 log2 units per position: a stage's keys share an offset of up to 64 slopes, which their own terms
-// cancel up to a few fp32 roundings of it.
-constexpr float kSteepest = 90852.f;
+// A biased stage's keys share an offset of up to 64 slopes, kept beside the scores, which their own terms cancel up to a few fp32
+// roundings of it.  Beyond this slope (log2 units per position) that would be more than a log2 unit, and a slope over a small
+// scale infinite: warps with a steeper one keep no offset, and each tile's scores take what its distance takes.
+constexpr float kSteepest = 0x1p17f;
 
 template <int D, int SC, bool Q8>
 __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(const __grid_constant__ CUtensorMap pool_map,
@@ -715,12 +716,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
     const int seq_r = r / G, head_r = r - seq_r * G;  // the row's sequence of the tile, and query head
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t colO = K::kColO + x * D;
-    // capped scores are in log2 units when they meet the softmax; biased ones alone stay raw, the slope divided by the scale, unless
-    // that is too small or negative
-    const bool raw_bias = SC == kBias && a.scale_log2 > 0x1p-40f;
-    const float sl2 = SC && !raw_bias ? 1.f : a.scale_log2;
-    // with a positive scale the maximum is of raw scores; masked ones become -inf before scaling (else +inf)
-    const bool pos_scale = sl2 > 0.f;
+    // with a positive scale the maximum is of scores that are still to be multiplied by it; masked ones become -inf before (else +inf)
+    const bool pos_scale = SC || a.scale_log2 > 0.f;
     const float masked = pos_scale ? kNegInf : -kNegInf;
     int done = 0;
     uint32_t joins = 0;   // segments of two chains so far
@@ -764,9 +761,13 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
       int reach_all = live ? reach : INT32_MAX;  // the least over the warp's rows
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) reach_all = min(reach_all, __shfl_xor_sync(0xffffffffu, reach_all, o));
-      const float slope = (SC & kBias) && live
-                              ? fminf(fmaxf(__ldg(a.score.slopes + sg.h * G + head_r), -kSteepest), kSteepest) * 1.4426950408889634f / sl2
-                              : 0.f;
+      const float slope2 = (SC & kBias) && live ? slope_log2(a.score, sg.h * G + head_r) : 0.f;
+      const bool steep = (SC & kBias) && __any_sync(0xffffffffu, fabsf(slope2) > kSteepest);
+      // capped scores are in log2 units when they meet the softmax; biased ones alone stay raw, the slope divided by the scale, unless
+      // that is too small or negative, or a slope too steep
+      const bool raw_bias = SC == kBias && a.scale_log2 > 0x1p-40f && !steep;
+      const float sl2 = SC && !raw_bias ? 1.f : a.scale_log2;
+      const float slope = slope2 / sl2;
       float m_ref = kNegInf, l = 0.f;
       uint32_t clean_word = 0u;
       for (int jj = 0; jj < mine; ++jj, ++done) {
@@ -866,17 +867,19 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
         }
         if constexpr ((SC & kBias) != 0) {
           // less slope * distance: key c of the stage gets slope * c, an immediate operand, and the row its first key's distance
-          row_off = -slope * sl2 * (float)((uint32_t)age[0] + (uint32_t)own);
+          row_off = steep ? 0.f : -slope * sl2 * (float)((uint32_t)age[0] + (uint32_t)own);
 #pragma unroll
           for (int c = 0; c < kKeys; ++c) sv[c] = fmaf(slope, (float)c, sv[c]);
-          bool run = age[kSub - 1] >= kTile - 1;  // 64 consecutive positions
+          bool run = age[kSub - 1] >= kTile - 1 && !steep;  // 64 consecutive positions
 #pragma unroll
           for (int u = 1; u < kSub; ++u) run = run && age[u] == age[0] - u * kTile;
           if (!run) {
-            // tile by tile, what its keys are off a run from the first; past the newest slot come the oldest, a ring away
+            // tile by tile, what its keys are off a run from the first (or from the query); past the newest slot come the oldest, a ring
+            // away
+            const int from = steep ? own : -age[0];
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
-              const float near = -slope * (float)(age[u] - age[0] + u * kTile), wrapped = near - slope * (float)sg.C;
+              const float near = -slope * (float)(int)((uint32_t)age[u] + (uint32_t)from + u * kTile), wrapped = near - slope * (float)sg.C;
 #pragma unroll
               for (int k = 0; k < kTile; ++k) sv[u * kTile + k] += k <= age[u] ? near : wrapped;
             }

@@ -284,7 +284,8 @@ int hwkv_decode_attn_score(hwkv_pool_t pool, int layer, const void* q, int q_hea
  *   recorded in `pool`.
  *   k_new, v_new (both or neither): appended to the own pool first, lens_dev then holding the own lengths before the
  *   append, as in hwkv_decode_attn_ex.  score: as hwkv_decode_attn_score (a prefix key's distance counts the
- *   tokens of both pools, and slopes beyond 9.08e4 -- 2^17 log2 units a token -- count as that: no result shows it);
+ *   tokens of both pools; its bias is off by a few fp32 roundings of slope * (distance + 64), and slope * log2(e) *
+ *   distance must be finite up to 64 tokens past the prefix pool's window);
  *   nothing to attend to gives zeros.  Stored keys and values must be finite, as for every call: the prefix's are operands of
  *   products over all sequences behind it.
  *   workspace: hwkv_decode_shared_workspace_bytes() bytes, otherwise as for hwkv_decode_attn.

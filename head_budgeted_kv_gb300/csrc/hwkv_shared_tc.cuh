@@ -904,10 +904,11 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
             mx = fmaxf(mx, sv[c]);
           }
         }
-        // the reference moves only when a maximum passes it by 2^8, so O is rarely touched (a row that has seen no
-        // key yet has nothing in O: rows of other reaches would otherwise touch it stage after stage)
-        const float m_new = fmaxf(m_ref, mx);
-        const bool grow = m_new > m_ref + 8.f;
+        // The reference lies 2^8 above a maximum and moves only when one passes it, so O is rarely touched (a row that has seen no
+        // key yet has nothing in O: rows of other reaches would otherwise touch it stage after stage).  Weights are at most 1:
+        // no value overflows by itself.
+        const bool grow = mx > m_ref;
+        const float m_new = mx + 8.f;
         if (jj > 0 && __any_sync(0xffffffffu, grow && m_ref != kNegInf)) {
           const int before = done - 1;  // O may be rescaled once the last P . V into it has completed
           ok = __all_sync(0xffffffffu, wait(&o_done[x][before & 1], (uint32_t)(before >> 1) & 1u, abort, a.pv.err));

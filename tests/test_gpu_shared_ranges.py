@@ -83,6 +83,17 @@ def ranged(types, G=4, D=64, seed=7, **kw):
     return Ranged([64, 40, 300], [700, 90, 500], [0, 5, 30, 63, 200], [500, 100, 30], [0, 1, 0, 0, 2], G, D, 16, types, seed=seed, **kw)
 
 
+def refill(side, k, v):
+    """Other keys and values in a side's pool, and in what is known of it."""
+    side.k, side.v = k, v
+    side.pool.materialize(0, k, v, i32(side.lens))
+    side.kk, side.vv = np64(k), np64(v)
+    if side.rings:
+        for s, n in enumerate(side.lens):
+            for h in range(len(side.windows)):
+                side.rings[s][h].materialize(side.kk[s, h], side.vv[s, h], n)
+
+
 def every_other(heads, steep):
     """Slopes of both signs, whole and a quarter, side by side."""
     return torch.tensor([steep * (1.0, -1.0, 0.25, -0.25)[i % 4] for i in range(heads)], device="cuda")
@@ -109,14 +120,26 @@ def test_scores_as_large_as_steep_slopes(types, steep):
     for side in (c.own, c.pre):
         k = torch.zeros_like(side.k)
         k[..., 0] = torch.tensor(gen.integers(0, 8, k.shape[:-1]), device="cuda").to(k.dtype)
-        side.k = k
-        side.pool.materialize(0, k, side.v, i32(side.lens))
-        side.kk = np64(k)
-        if side.rings:
-            for s in range(len(side.lens)):
-                for h in range(2):
-                    side.rings[s][h].materialize(side.kk[s, h], side.vv[s, h], side.lens[s])
+        refill(side, k, side.v)
     c.q.zero_()
     c.q[..., 0] = 8.0
     c.scale, c.slopes = steep / 8, every_other(8, 0.937 * steep)
     assert c.check(c.call()) == 0
+
+
+@pytest.mark.parametrize("types", PAIRS, ids=PAIR_IDS)
+@pytest.mark.parametrize("G,D,N", [(4, 128, 256), (1, 64, 700), (16, 64, 300)])
+def test_the_largest_values_do_not_overflow(types, G, D, N):
+    """Sums are held relative to the largest weight: a value of 2^125 under a weight e^5 times those before it, at places of every
+    stage and chain, gives its share of the result, not infinity."""
+    places = list(range(5, N, 61))
+    c = Ranged([16], [N], [0] * 20, [N] * len(places), [i % len(places) for i in range(20)], G, D, 16, types, seed=1)
+    k, v = torch.zeros_like(c.pre.k), c.pre.v.clone()
+    for f, p in enumerate(places):
+        k[f, :, p, 0] = 5.0
+        v[f, :, p] = 2.0 ** 125 * torch.where(v[f, :, p] < 0, -1.0, 1.0).to(v.dtype)
+    refill(c.pre, k, v)
+    c.q.zero_()
+    c.q[..., 0] = 8.0
+    c.scale = 0.125
+    c.check(c.call())

@@ -26,7 +26,10 @@
 // exactly (3 mantissa bits, a power of two); a warp takes the K and V rows of one 16-slot tile.  The same products follow.
 // V rows of slots outside the prefix's window become zeros, whatever they hold.
 //
-// Weights are rounded to bf16 for P V (2^-8 of each, half a step); their sum is of the unrounded ones.
+// Weights are rounded to bf16 for P V (2^-8 of each, half a step), as in the decode of bf16 pools; their sum is of the unrounded ones.
+// That goes for 8-bit prefixes too, where the decode has fp16 weights (2^-11): a product's operands have one type, and only bf16
+// holds code x scale.  Keys and values of theirs are off by up to 2^-4 already.  (The weight as two bf16 numbers, the second
+// of what the first leaves, gives 2^-15 but takes 17-26% of the call: one 64K prefix, 64 rows 76 -> 91 us, 1024 rows 293 -> 370.)
 //
 // Measured (head_dim 128, one prefix of 64K, all SMs): 0.83-0.90 us a stage of 64 keys up to 256 rows, 0.81-0.90 of the copy rate;
 // 0.95 at 1024 rows, 1420 TFLOP/s or 0.74 of the measured peak, bound by the exponentials between the products.  Scored stages of 256

@@ -286,8 +286,10 @@ int hwkv_decode_attn_score(hwkv_pool_t pool, int layer, const void* q, int q_hea
  *   append, as in hwkv_decode_attn_ex.  score: as hwkv_decode_attn_score (a prefix key's distance counts the
  *   tokens of both pools; its bias is off by a few fp32 roundings of slope * (distance + 64), and slope * log2(e) *
  *   distance must be finite up to 64 tokens past the prefix pool's window);
- *   nothing to attend to gives zeros.  Stored keys and values must be finite, as for every call: the prefix's are operands of
- *   products over all sequences behind it.
+ *   nothing to attend to gives zeros.  Weights of a prefix's keys are rounded to bf16 (2^-8 of each) before they multiply
+ *   its values, in bf16 and 8-bit prefix pools alike (an 8-bit decode rounds its own to fp16, 2^-11); those of fp32 pools, and of
+ *   bf16 pools with block_size % 16 != 0, are not.  Stored keys and values must be finite, as for every call (and below
+ *   2^128 in 8-bit pools): the prefix's are operands of products over all sequences behind it.
  *   workspace: hwkv_decode_shared_workspace_bytes() bytes, otherwise as for hwkv_decode_attn.
  * Three kernels on `stream` or more: the prefixes' keys, the own parts, their join.  Concurrent launches of the same
  * layer of `pool` race, decode calls included; `prefix` may be shared by any number of launches that only read it.

@@ -143,3 +143,134 @@ def test_the_largest_values_do_not_overflow(types, G, D, N):
     c.q[..., 0] = 8.0
     c.scale = 0.125
     c.check(c.call())
+
+
+def alternating(heads):
+    """Slopes of both signs that halve from head to head."""
+    return torch.tensor([(-0.5) ** i for i in range(heads)], device="cuda")
+
+
+@pytest.mark.parametrize("types", PAIRS, ids=PAIR_IDS)
+@pytest.mark.parametrize("scale,cap,biased", [(-0.125, 0.0, False), (0.0, 0.0, False), (-0.125, 20.0, False), (0.0, 20.0, False),
+                                              (4.0, 3.0, False), (2.0, 30.0, True), (0.125, 500.0, False), (-0.125, 0.0, True),
+                                              (0.0, 0.0, True), (1e-14, 0.0, True), (0.125, 0.0, True), (-0.125, 6.0, True),
+                                              (1e-14, 6.0, True)])
+def test_scales_caps_and_slopes(types, scale, cap, biased):
+    """Negative, zero and tiny scales, scores far past the cap and far below it, slopes of both signs."""
+    for G, D in ((4, 64), (7, 128)):
+        c = ranged(types, G, D, cap=cap)
+        c.scale, c.slopes = scale, alternating(3 * G) if biased else None
+        c.step(append=False)
+        c.step()
+
+
+class Counted:
+    """Queries of zero: every visible key has the same weight.  With values of 1 in one place of a row, of zero in the others, a result
+    times the number of visible keys counts the keys whose values lie in that place."""
+
+    def __init__(self, types, own, pre, lens, pre_lens, of, G, D, bs, seed):
+        self.gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.B, self.H, self.G, self.D = len(lens), len(own), G, D
+        self.own_w, self.pre_w, self.lens, self.pre_lens, self.of = own, pre, lens, pre_lens, of
+        self.own = hw.Pool(1, self.H, D, bs, [own], self.B, types[0], q_heads=G * self.H)
+        self.pre = hw.Pool(1, self.H, D, bs, [pre], len(pre_lens), types[1], q_heads=G * self.H)
+        for pool in (self.own, self.pre):
+            pool.set_block_table(np.random.default_rng(seed).permutation(pool.geometry()[1]).astype(np.int32))
+        self.q = torch.zeros((self.B, G * self.H, D), dtype=self.own.io_dtype, device="cuda")
+        self.keys = [torch.randn((p.num_seqs, self.H, max(1, max(ls)), D), generator=self.gen, device="cuda").to(p.io_dtype)
+                     for p, ls in ((self.own, lens), (self.pre, pre_lens))]
+
+    def check(self, own_place, pre_place):
+        """own_place, pre_place: the places of the values of position p of head h (-1: none), from [n] to [n]."""
+        D = self.D
+        places = []
+        for pool, keys, lens, place in ((self.own, self.keys[0], self.lens, own_place), (self.pre, self.keys[1], self.pre_lens, pre_place)):
+            at = np.stack([place(h, np.arange(keys.shape[2])) for h in range(self.H)])
+            t = torch.tensor(at, device="cuda")
+            rows = (torch.arange(D, device="cuda") == t[..., None]).to(keys.dtype)  # [H, n, D]
+            pool.materialize(0, keys, rows.expand(keys.shape).contiguous(), i32(lens))
+            # how many of the first p positions have their values in each place
+            some = at[..., None] == np.arange(D)
+            places.append(np.concatenate((np.zeros((self.H, 1, D), np.int64), np.cumsum(some, 1)), 1))
+        out = self.own.shared_decode(0, self.pre, self.q, 0.125, i32(self.lens), i32(self.of), i32(self.pre_lens))
+        assert self.own.check_device_errors() == 0
+        got = np64(out).reshape(self.B, self.H, self.G, D)
+        half = 2.0 ** -8 if self.own.io_dtype == BF16 else 2.0 ** -22
+        for s, (n, f) in enumerate(zip(self.lens, self.of)):
+            for h in range(self.H):
+                total, count = min(n, self.own_w[h]), places[0][h][n] - places[0][h][max(0, n - self.own_w[h])]
+                if f >= 0:
+                    N = self.pre_lens[f]
+                    first = min(N, max(0, N + n - self.pre_w[h]))
+                    total, count = total + N - first, count + places[1][h][N] - places[1][h][first]
+                want = count / max(total, 1)
+                assert (np.abs(got[s, h] - want) <= half * want + 2.0 ** -22).all(), (s, h, n, f, np.abs(got[s, h] * total - count).max())
+        return out
+
+    def check_all(self, rounds):
+        """Tile by tile, then around the ends of windows, rings, tiles, stages and wherever chance has it."""
+        D = self.D
+        whole = self.check(lambda h, p: (p + h) % D, lambda h, p: (p // 16 + h) % D)
+        rng = np.random.default_rng(len(self.lens))
+        for r in range(rounds):
+            def place(h, p):
+                N, w = max(self.pre_lens), self.pre_w[h]
+                C = -(-w // self.pre.block_size) * self.pre.block_size
+                some = [x + d for n in rng.choice(self.lens, 8) for x in (N + n - w, N - w) for d in (-1, 0)]
+                some += [x + d for x in range(C, N + 1, C) for d in (-1, 0)][:8] + [0, N - 1, N - 2]
+                some += [64 * int(i) + d for i in rng.integers(0, max(1, N // 64) + 1, D) for d in (-1, 0)]
+                at = np.full(len(p), -1)
+                some = [x for x in dict.fromkeys(some) if 0 <= x < len(p)][:D]
+                at[some] = np.arange(len(some))
+                return at
+            self.check(lambda h, p: np.full(len(p), -1), place)
+        return whole
+
+
+@pytest.mark.parametrize("types", [(BF16, BF16), (E4M3, E4M3), (BF16, E4M3)], ids=["bf16", "e4m3", "bf16-e4m3"])
+@pytest.mark.parametrize("G,D,B", [(8, 128, 40), (4, 64, 70)])
+def test_every_key_of_a_long_prefix_counts_once(types, G, D, B):
+    """One prefix, a pair of query tiles and a single one per head (B sequences, 32 or 64 to a pair), 2 x 4256 stages: more than 32 to
+    a CTA, whose stage slots go round many times, and segments that begin and end within a head."""
+    lens = [(37 * i) % 200 for i in range(B)]
+    c = Counted(types, [200] * 8, [40000, 39999, 33333, 20000, 48000, 45001, 64, 47003], lens, [47003], [0] * B, G, D, 16, 5)
+    c.check_all(4)
+
+
+@pytest.mark.parametrize("types", PAIRS, ids=PAIR_IDS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_key_of_many_prefixes_counts_once(types, D):
+    """200 prefixes of 1 to 400 tokens and four heads: several segments to a CTA, of one query tile and of two, of one stage and of
+    more, one prefix with 40 sequences (groups of 16: eight to a tile), some with none."""
+    rng = np.random.default_rng(D)
+    pre_lens = rng.integers(1, 400, 200).tolist()
+    pre_lens[3], pre_lens[7] = 0, 64
+    of = [5] * 40 + [int(f) if f != 11 else -1 for f in rng.integers(0, 190, 220)]
+    of = [of[i] for i in rng.permutation(260)]
+    c = Counted(types, [32, 48, 16, 64], [400, 300, 100, 64], rng.integers(0, 60, 260).tolist(), pre_lens, of, 16, D, 32, 6)
+    first = c.check_all(4)
+    for _ in range(3):
+        assert torch.equal(c.check(lambda h, p: (p + h) % D, lambda h, p: (p // 16 + h) % D), first)
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16)], ids=["f32", "bf16"])
+def test_every_key_counts_once_on_cuda_cores(types):
+    rng = np.random.default_rng(2)
+    lens, of = rng.integers(0, 90, 30).tolist(), rng.integers(-1, 3, 30).tolist()
+    Counted(types, [90, 7, 40], [3000, 5000, 777], lens, [5000, 1203, 77], of, 3, 64, 24, 7).check_all(4)
+
+
+@pytest.mark.parametrize("types", PAIRS[:4], ids=PAIR_IDS[:4])
+@pytest.mark.parametrize("G,D", [(16, 64), (4, 128)])
+def test_many_segments_against_the_definition(types, G, D):
+    """As above with random keys, and the same bits from call to call."""
+    rng = np.random.default_rng(G)
+    of = [2] * (3 * (128 // G) + 1) + rng.integers(-1, 60, 150).tolist()
+    c = Ranged([32, 48, 16, 64], [400, 300, 100, 64], rng.integers(0, 60, len(of)).tolist(), rng.integers(1, 400, 60).tolist(),
+               [int(f) for f in rng.permutation(of)], G, D, 32, types, seed=G)
+    first = c.call().clone()
+    c.check(first, seqs=list(range(0, len(of), 9)))
+    for _ in range(3):
+        assert torch.equal(c.call(), first)
+    c.scale, c.slopes, c.cap = 0.2, alternating(4 * G), 5.0
+    c.check(c.call(), seqs=list(range(1, len(of), 17)))

@@ -51,7 +51,8 @@ class DecodeStepGraph:
             self.prefix_of = torch.as_tensor(prefix_of, dtype=torch.int32, device=dev).clone()
             self.prefix_lens = torch.as_tensor(prefix_lens, dtype=torch.int32, device=dev).clone()
             f = self.prefix_of.long()
-            ahead = torch.where((f >= 0) & (f < prefix.num_seqs), self.prefix_lens[f.clamp(0, prefix.num_seqs - 1)], 0)
+            # as the attention counts them: a negative length is none
+            ahead = torch.where((f >= 0) & (f < prefix.num_seqs), self.prefix_lens[f.clamp(0, prefix.num_seqs - 1)].clamp(min=0), 0)
             self.turn_pos = (self.pos + ahead).to(torch.int32)
         self.rope = rope
         self._score = {"softcap": softcap, "slopes": slopes}

@@ -33,6 +33,8 @@ class DecodeStepGraph:
 
     def __init__(self, pool, scale: float, q_heads: int, pos0, fused: bool = True, rope=None, softcap: float = 0.0,
                  slopes=None, prefix=None, prefix_of=None, prefix_lens=None):
+        if len({x is None for x in (prefix, prefix_of, prefix_lens)}) != 1:
+            raise ValueError("prefix, prefix_of and prefix_lens go together")
         dev = pool.buffer.device
         L, B, H, D = pool.layers, pool.num_seqs, pool.kv_heads, pool.head_dim
         dt = pool.io_dtype
@@ -50,6 +52,8 @@ class DecodeStepGraph:
         if prefix is not None:
             self.prefix_of = torch.as_tensor(prefix_of, dtype=torch.int32, device=dev).clone()
             self.prefix_lens = torch.as_tensor(prefix_lens, dtype=torch.int32, device=dev).clone()
+            if self.prefix_of.shape != (B,) or self.prefix_lens.numel() < prefix.num_seqs:
+                raise ValueError(f"prefix_of must hold {B} values, prefix_lens {prefix.num_seqs}")
             f = self.prefix_of.long()
             # as the attention counts them: a negative length is none
             ahead = torch.where((f >= 0) & (f < prefix.num_seqs), self.prefix_lens[f.clamp(0, prefix.num_seqs - 1)].clamp(min=0), 0)

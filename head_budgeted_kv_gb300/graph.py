@@ -24,6 +24,7 @@ class DecodeStepGraph:
       k_new [layers][B][kv_heads][D]  new keys, v_new likewise
       pos   [B] int32                 lengths before the append; the step adds 1 to them
     Output: out [layers][B][q_heads][D].
+    fused: the attention appends k_new and v_new (else, and behind prefixes with a rope, a launch ahead of it).
     rope: a ``rope_table`` when q and k_new come without their rotary positions.
     softcap, slopes: capped or distance-biased scores, as in ``Pool.decode``.
     prefix, prefix_of, prefix_lens: sequences behind prefixes kept once, as in ``Pool.shared_decode``; pos then
@@ -96,12 +97,16 @@ class DecodeStepGraph:
     def _record_shared(self):
         p = self.pool
         behind = (self.prefix_of, self.prefix_lens)
-        if self.rope is not None:
+        apart = self.rope is not None or not self.fused  # the append in a launch of its own
+        if apart:
             p.advance_positions(self.pos, out=self.lens)  # lengths after the append
         for l in range(p.layers):
             if self.rope is not None:
                 p.rope_append(l, self.rope, self.q[l], self.k_new[l], self.v_new[l], self.pos, q_out=self._q[l],
                               turn_pos=self.turn_pos)
+            elif apart:
+                p.append(l, self.k_new[l], self.v_new[l], self.pos)
+            if apart:
                 p.shared_decode(l, self.prefix, self._q[l], self.scale, self.lens, *behind, out=self.out[l], **self._score)
             else:
                 p.shared_decode(l, self.prefix, self.q[l], self.scale, self.pos, *behind, k_new=self.k_new[l],

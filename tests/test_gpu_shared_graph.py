@@ -51,3 +51,26 @@ def test_a_negative_prefix_length_is_none():
         results.append((step.out.clone(), own.blocks().clone()))
         assert own.check_device_errors() == (hw.binding.HWKV_DEVERR_NEG_LENGTH if lens[1] < 0 else 0)
     assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
+
+
+@pytest.mark.parametrize("rope", [False, True], ids=["plain", "rope"])
+@pytest.mark.parametrize("dtype", [BF16, torch.float8_e4m3fn, torch.float32], ids=["bf16", "e4m3", "f32"])
+def test_an_append_apart_gives_the_same(dtype, rope):
+    """fused=False appends in a launch of its own (with a rope the two are the same step), bit for bit as the fused step."""
+    results, launches = [], []
+    for fused in (True, False):
+        own, pre = pools(dtype)
+        before = hw.hwkv_kernel_launches()
+        step = DecodeStepGraph(own, 0.125, 8, [0, 5, 30], fused=fused, rope=hw.rope_table(64) if rope else None, prefix=pre,
+                               prefix_of=[1, -1, 0], prefix_lens=[150, 33])
+        launches.append(hw.hwkv_kernel_launches() - before)
+        outs = []
+        for i in range(20):  # past the own windows
+            inputs(step, i)
+            step.replay()
+            outs.append(step.out.clone())
+        assert step.pos.tolist() == [20, 25, 50] and own.check_device_errors() == 0
+        results.append((torch.stack(outs), own.buffer.clone()))
+    assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
+    # an append for each layer and the lengths once
+    assert launches[1] - launches[0] == (0 if rope else 3)

@@ -1227,21 +1227,21 @@ int open_workers(const hwkv_pool* p, int layer, int group) {
   return (int)std::min<int64_t>((full + 1) / 2, std::max<int64_t>(16, tiles * g.num_seqs / 4));
 }
 
-// How keys are split on the CUDA cores: ring slots per CTA for about six CTAs per SM, and the chunks of each head.
+// How keys are split on the CUDA cores: ring slots per CTA, and the chunks of each head.
 struct SharedPlan {
   int split = 0;
   int chunks = 0;
   int32_t chunk_prefix[kMaxKvHeads + 1] = {};
 };
 
-// Of one layer of `pool`, whose chunks `times` CTAs read.
-SharedPlan plan_chunks(const hwkv_pool* pool, int layer, int times) {
+// Of one layer of `pool`, of whose sequences `reads` are read in whole, for about `per_sm` CTAs per SM.
+SharedPlan plan_chunks(const hwkv_pool* pool, int layer, int reads, int per_sm) {
   SharedPlan s;
   const Geometry& g = pool->g;
   auto capacity = [&](int h) { return (int64_t)g.nblk[(size_t)layer * g.kv_heads + h] * g.block_size; };
   int64_t slots = 0;
   for (int h = 0; h < g.kv_heads; ++h) slots += capacity(h);
-  const int64_t want = slots * g.num_seqs * times / (6LL * std::max(1, pool->num_sms));
+  const int64_t want = slots * reads / ((int64_t)per_sm * std::max(1, pool->num_sms));
   s.split = 64;
   while (s.split < want && s.split < 4096) s.split <<= 1;
   for (int h = 0; h < g.kv_heads; ++h)
@@ -1250,10 +1250,17 @@ SharedPlan plan_chunks(const hwkv_pool* pool, int layer, int times) {
   return s;
 }
 
-// The prefixes' keys, read by a CTA per tile of sequences.
+// A sequence's own keys.
+SharedPlan plan_own(const hwkv_pool* p, int layer) { return plan_chunks(p, layer, p->g.num_seqs, 6); }
+
+// The prefixes' keys, read by a CTA per tile of a prefix's sequences: at most this many tiles hold any; the CTAs of the others end
+// at once.  (Sized as if each prefix had all sequences: 8 behind 8 of 64 prefixes of 3000 tokens took 118 us in fp32, now 74; 128 behind
+// 16 of 1500 155 and 59.)  Twelve CTAs per SM, since sequences are often behind fewer prefixes than that: with six, 24 of them
+// behind one of 8 prefixes of 4000 tokens took 311 us in bf16, now 168; behind all 8 314 and 301; 24 of groups of 16 behind one, fp32,
+// 323 and 260; 32 behind one of 32K, bf16, 604 and 614.
 SharedPlan plan_shared(const hwkv_pool* p, const hwkv_pool* prefix, int layer, int group) {
-  const int per = shared_simt_seqs(group);
-  return plan_chunks(prefix, layer, (p->g.num_seqs + per - 1) / per);
+  const int B = p->g.num_seqs;
+  return plan_chunks(prefix, layer, std::min(prefix->g.num_seqs, B) + B / shared_simt_seqs(group), 12);
 }
 
 // Regions of the workspace: the own decode's, its open results, the prefixes' partials and their records.
@@ -1283,7 +1290,7 @@ SharedLayout shared_layout(const hwkv_pool* p, const hwkv_pool* prefix, int grou
   uint64_t own = workspace_bytes(p, group);
   if (!use_tc(p, group)) {
     uint64_t items = 0;
-    for (int l = 0; l < p->g.layers; ++l) items = std::max<uint64_t>(items, plan_chunks(p, l, 1).chunks);
+    for (int l = 0; l < p->g.layers; ++l) items = std::max<uint64_t>(items, plan_own(p, l).chunks);
     items *= B * (uint64_t)group;
     w.split_acc = align256(own);
     w.split_ml = align256(w.split_acc + items * D * 4);
@@ -1371,7 +1378,7 @@ int hwkv_decode_attn_shared(hwkv_pool_t p, hwkv_pool_t prefix, int layer, const 
   call.a.open_acc = reinterpret_cast<float*>(ws + wl.own_acc);
   call.a.open_ml = reinterpret_cast<float*>(ws + wl.own_ml);
   if (!call.tc) {
-    const SharedPlan own = plan_chunks(p, layer, 1);
+    const SharedPlan own = plan_own(p, layer);
     call.a.split_tokens = own.split;
     std::memcpy(call.a.chunk_prefix, own.chunk_prefix, sizeof own.chunk_prefix);
     call.items = own.chunks * p->g.num_seqs;

@@ -260,6 +260,15 @@ def test_every_key_counts_once_on_cuda_cores(types):
     Counted(types, [90, 7, 40], [3000, 5000, 777], lens, [5000, 1203, 77], of, 3, 64, 24, 7).check_all(4)
 
 
+@pytest.mark.parametrize("dtype,bs", [(F32, 16), (BF16, 24)], ids=["f32", "bf16"])
+def test_prefixes_that_nobody_is_behind_split_no_coarser(dtype, bs):
+    """What the CUDA cores take at a time goes by the prefixes that sequences can be behind: the partials' room is that of as many."""
+    own = hw.Pool(1, 2, 64, bs, [[64, 64]], 8, dtype, q_heads=8)
+    pres = [hw.Pool(1, 2, 64, bs, [[3000, 900]], n, dtype, q_heads=8) for n in (8, 64, 500)]
+    need = [hw.binding.hwkv_decode_shared_workspace_bytes(own.handle, p.handle, 8) for p in pres]
+    assert need[0] == need[1] == need[2]
+
+
 @pytest.mark.parametrize("types", PAIRS[:4], ids=PAIR_IDS[:4])
 @pytest.mark.parametrize("G,D", [(16, 64), (4, 128)])
 def test_many_segments_against_the_definition(types, G, D):

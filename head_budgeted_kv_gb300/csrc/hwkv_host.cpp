@@ -1217,7 +1217,8 @@ SharedTimes shared_times(const hwkv_pool* p, const hwkv_pool* prefix, int group,
 
 // CTAs of the own parts' kernel: half of a decode's, which half of the SMs take at once beside the prefixes, but no more than
 // own windows of four tiles each keep busy.  (All of them, in two or three waves: 32K document 49 us, not 46; several
-// prefixes 42, not 35; a third: 53 and 45.)
+// prefixes 42, not 35; a third: 53 and 45.  No share is best throughout, as the lengths are on the device: with the best number for
+// each case the document takes 44, 8-bit pools behind two of 32K 75, not 86, several prefixes 34.5.)
 int open_workers(const hwkv_pool* p, int layer, int group) {
   const int full = tc_workers(p, group);
   if (p->workers_override > 0) return full;

@@ -31,10 +31,11 @@
 // holds code x scale.  Keys and values of theirs are off by up to 2^-4 already.  (The weight as two bf16 numbers, the second
 // of what the first leaves, gives 2^-15 but takes 17-26% of the call: one 64K prefix, 64 rows 76 -> 91 us, 1024 rows 293 -> 370.)
 //
-// Measured (head_dim 128, one prefix of 64K, all SMs): 0.83-0.90 us a stage of 64 keys up to 256 rows, 0.81-0.90 of the copy rate;
-// 0.95 at 1024 rows, 1420 TFLOP/s or 0.74 of the measured peak, bound by the exponentials between the products.  Scored stages of 256
-// rows: capped 1.41, biased 1.43, both 2.1 us.  8-bit: 0.89-0.92 us up to 128 rows, bound by the conversion (1180 of 1700 cycles),
-// 1.08-1.17 beyond.  The keys' bytes cross from DRAM once (88.2 of 88.1 MB for 64 rows; 1024 rows share them through L2).
+// Measured (head_dim 128, 8 KV heads, all SMs; a stage of 64 keys on an SM, from calls with prefixes of 16K and 128K): 0.78 us at 64
+// rows, 0.95 of the measured copy rate; 0.88 at 256; 0.98 at 1024, where 1300 TFLOP/s are 0.68 of the measured peak, bound by the
+// exponentials between the products.  Scored stages of 256 rows (32K and 96K): capped 1.26, biased 1.34, both 1.94 us.  8-bit: 0.89 us at
+// 64 rows, bound by the conversion (1180 of 1700 cycles), 1.1 from 256 on.  The keys' bytes cross from DRAM once (88.2 of 88.1 MB for 64
+// rows; 1024 rows share them through L2).
 //
 // Waits are bounded (~2 s) and record HWKV_DEVERR_WAIT_TIMEOUT; then all roles stop.
 #pragma once

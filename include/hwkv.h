@@ -460,6 +460,8 @@ int hwkv_rope(hwkv_pool_t pool, const hwkv_rope_t* rope, const hwkv_rows_t* q, i
  *   must not overlap anything else.  q_heads is a multiple of kv_heads.  Strides as in hwkv_rows_t.
  *   pos_dev, turn_pos_dev, n_dev: device int32 [num_seqs]; a negative position, one that reaches 2^31, or n_s outside
  *   [0, n_max] flags HWKV_DEVERR_NEG_LENGTH and skips the sequence.  n_dev NULL: all n_max rows.
+ * Cosines and sines are fp32 of angles as exact as hwkv_rope's (queries, bf16 and fp32 keys 2^-23; keys of 8-bit pools and
+ * the queries beside them 2^-26).
  * bf16 and fp32 pools hold what hwkv_rope and then hwkv_append of each row in turn leave, bit for bit.  8-bit pools store every
  * group of 16 slots that a row goes to once, anew: the slots whose positions are in the window of the new length take their row,
  * rounded once from the turned fp32 value, or keep their value at the new scale; every other slot becomes zero.

@@ -216,10 +216,11 @@ __device__ __forceinline__ void store_part(float* p, const float (&o)[32]) {
 // What is done to the scores between the two products, an instance each.
 enum { kPlain = 0, kCap = 1, kBias = 2 };
 
-// A biased stage's keys share an offset of up to 64 slopes, kept beside the scores, which their own terms cancel up to a few fp32
-// roundings of it.  Beyond this slope (log2 units per position) that would be more than a log2 unit, and a slope over a small
-// scale infinite: warps with a steeper one keep no offset, and each tile's scores take what its distance takes.
-constexpr float kSteepest = 0x1p17f;
+// A biased stage's keys share an offset, the bias of its first, kept beside the scores; their own terms of up to 64 slopes cancel what is
+// over.  Both leave a few fp32 roundings of the bias.  Where it may pass this (log2 units) within the window, or 64 slopes pass half of it, that
+// would be more than a log2 unit in a weight (past 2^31 the weight overflows), and a slope over a small scale is infinite: warps with
+// such a slope keep no offset, and each tile's scores take what its distance takes.
+constexpr float kFarBias = 0x1p24f;
 
 template <int D, int SC, bool Q8>
 __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(const __grid_constant__ CUtensorMap pool_map,
@@ -766,7 +767,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1) shared_tc_kernel(cons
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) reach_all = min(reach_all, __shfl_xor_sync(0xffffffffu, reach_all, o));
       const float slope2 = (SC & kBias) && live ? slope_log2(a.score, sg.h * G + head_r) : 0.f;
-      const bool steep = (SC & kBias) && __any_sync(0xffffffffu, fabsf(slope2) > kSteepest);
+      const bool steep = (SC & kBias) && __any_sync(0xffffffffu, fabsf(slope2) * (float)max(reach + own, 128) > kFarBias);
       // capped scores are in log2 units when they meet the softmax; biased ones alone stay raw, the slope divided by the scale, unless
       // that is too small or negative, or a slope too steep
       const bool raw_bias = SC == kBias && a.scale_log2 > 0x1p-40f && !steep;

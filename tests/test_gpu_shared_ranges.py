@@ -283,3 +283,13 @@ def test_many_segments_against_the_definition(types, G, D):
         assert torch.equal(c.call(), first)
     c.scale, c.slopes, c.cap = 0.2, alternating(4 * G), 5.0
     c.check(c.call(), seqs=list(range(1, len(of), 17)))
+
+
+@pytest.mark.parametrize("types", PAIRS, ids=PAIR_IDS)
+@pytest.mark.parametrize("slope", [2e4, -2e4, 8e4])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_slopes_over_long_distances(types, cap, slope):
+    """What the distance takes passes 2^31 log2 units within the window: the newest key, or the farthest, takes all the weight."""
+    c = Ranged([40], [160000], [20, 0, 39], [150000, 149000], [0, 0, 1], 4, 64, 16, types, seed=1, cap=cap)
+    c.slopes = torch.tensor([slope, slope / 2, slope, slope / 4], device="cuda")
+    assert c.check(c.call()) == 0

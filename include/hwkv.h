@@ -285,7 +285,8 @@ int hwkv_decode_attn_score(hwkv_pool_t pool, int layer, const void* q, int q_hea
  *   k_new, v_new (both or neither): appended to the own pool first, lens_dev then holding the own lengths before the
  *   append, as in hwkv_decode_attn_ex.  score: as hwkv_decode_attn_score (a prefix key's distance counts the
  *   tokens of both pools; its bias is off by a few fp32 roundings of slope * (distance + 64), and slope * log2(e) *
- *   distance must be finite up to 64 tokens past the prefix pool's window);
+ *   distance must be finite up to 64 tokens past the prefix pool's window; scale * <q, k> must stay below 2^26 in
+ *   magnitude for prefixes in bf16 and 8-bit pools);
  *   nothing to attend to gives zeros.  Weights of a prefix's keys are rounded to bf16 (2^-8 of each) before they multiply
  *   its values, in bf16 and 8-bit prefix pools alike (an 8-bit decode rounds its own to fp16, 2^-11); those of fp32 pools, and of
  *   bf16 pools with block_size % 16 != 0, are not.  Stored keys and values must be finite, as for every call (and below

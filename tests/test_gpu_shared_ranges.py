@@ -286,6 +286,27 @@ def test_many_segments_against_the_definition(types, G, D):
 
 
 @pytest.mark.parametrize("types", PAIRS, ids=PAIR_IDS)
+@pytest.mark.parametrize("size", [1e3, 5e5])
+@pytest.mark.parametrize("biased", [False, True])
+def test_huge_scores(types, size, biased):
+    """Scores (up to 5.6e7) so large that one key takes all the weight, in the prefix or among the own ones: its value comes out."""
+    places = [23, 70, 140, 250, 299]
+    for own_wins in (False, True):
+        c = Ranged([40], [300], [20] * 10, [300] * len(places), [i % len(places) for i in range(10)], 4, 64, 16, types, seed=1)
+        for side in (c.own, c.pre):
+            k = torch.zeros_like(side.k)
+            k[..., 0] = (torch.arange(k.shape[2], device="cuda") * 7 % 48 / 64).to(k.dtype)
+            for i in range(len(side.lens)):
+                k[i, :, 11 if side is c.own else places[i], 0] = 14.0 if (side is c.own) == own_wins else 0.0
+            refill(side, k, side.v)
+        c.q.zero_()
+        c.slopes = torch.tensor([0.5, 0.25, -0.25, 0.0], device="cuda") if biased else None
+        for c.scale in (size, -size):
+            c.q[..., 0] = 8.0 if c.scale > 0 else -8.0
+            assert c.check(c.call()) == 0, c.scale
+
+
+@pytest.mark.parametrize("types", PAIRS, ids=PAIR_IDS)
 @pytest.mark.parametrize("slope", [2e4, -2e4, 8e4])
 @pytest.mark.parametrize("cap", [0.0, 20.0])
 def test_slopes_over_long_distances(types, cap, slope):
